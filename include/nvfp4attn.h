@@ -80,7 +80,8 @@ const char* nvq_last_error_detail(void);
 /*
  * Synchronizes `stream`, then returns and clears the device error word that
  * bounded waits set on the current device: NVQ_OK or NVQ_ERR_TIMEOUT (or
- * NVQ_ERR_CUDA if the synchronization itself failed).
+ * NVQ_ERR_CUDA if the synchronization itself failed).  The paged-cache calls
+ * record NVQ_ERR_INVALID there for a page number or a length out of range.
  */
 nvq_status nvq_device_status(nvq_stream_t stream);
 
@@ -403,19 +404,145 @@ nvq_status nvfp4_linear_bwd(const void* grad_out, const void* x, const void* w, 
                             int64_t N, int64_t K, void* grad_x, void* grad_w, void* grad_b,
                             void* ws, size_t ws_bytes, nvq_stream_t stream);
 
+/*
+ * The NVFP4 linear on a weight packed once (serving): the product of
+ * nvfp4_linear_fwd without quantizing w at every call.
+ *   x        bf16 [M, K], row stride ld_x (elements, >= K, % 8 == 0); quantized
+ *            under x_global_sf (device fp32 scalar, or NULL for 448*6/amax(x))
+ *   w_codes  uint8 [N, K/2], w_scales nvfp4_tiled_scale_bytes(N, K) bytes, as
+ *            nvfp4_quantize_tiled wrote them (16-byte aligned); w_global_sf the
+ *            device fp32 scalar it was given (NULL: 1.0)
+ *   bias     bf16 [N] or NULL; out bf16 [M, N] contiguous; 16-byte aligned
+ * M >= 1, K % 64 == 0 and N % 16 == 0 (else NVQ_ERR_UNSUPPORTED).  On the same
+ * operands and scales the result is nvfp4_linear_fwd's up to the order of the
+ * fp32 sums over K.  ws: nvfp4_linear_packed_workspace(M, N, K) bytes, 256-byte
+ * aligned.  The backward of a packed weight is not defined: train with
+ * nvfp4_linear_fwd / nvfp4_linear_bwd, then pack.
+ */
+size_t nvfp4_linear_packed_workspace(int64_t M, int64_t N, int64_t K);
+nvq_status nvfp4_linear_packed_fwd(const void* x, int64_t ld_x, const uint8_t* w_codes,
+                                   const uint8_t* w_scales, const float* w_global_sf,
+                                   const void* bias, int64_t M, int64_t N, int64_t K,
+                                   const float* x_global_sf, void* out, void* ws, size_t ws_bytes,
+                                   nvq_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rotary positions                                                         */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Rotary position embedding of Q and K in one launch (no counterpart in the
+ * pages: it stands before attn_qat_fwd in the models that train with it).
+ *   q, q_out  bf16 [T, Hq, D], token strides ld_q, ld_qo (elements, % 8 == 0,
+ *             >= Hq*D); heads contiguous.  q_out may be q itself (with ld_qo ==
+ *             ld_q); other overlaps are not allowed
+ *   k, k_out  the same with Hk heads; Hk == 0: only q (k, k_out ignored)
+ *   D         a multiple of 16, at most 256; rot_dim a multiple of 16 in 16..D
+ *             (else NVQ_ERR_UNSUPPORTED): the first rot_dim elements of a head
+ *             are rotated, the others copied
+ *   interleaved  1: pair p is elements (2p, 2p + 1); 0: (p, p + rot_dim/2)
+ *   positions int32 [T, axes], 4-byte aligned; any int32 value
+ *   axes      1..3 position axes; axis_pairs: HOST array of `axes` counts >= 0
+ *             that add up to rot_dim/2: the first axis_pairs[0] pairs turn by
+ *             axis 0's position, the next by axis 1's, and so on
+ *   inv_freq  device f64 [rot_dim/2], 8-byte aligned, finite: pair p turns by
+ *             a = position * inv_freq[p] radians.  Scaled contexts change
+ *             inv_freq (and mscale) only
+ *   mscale    > 0 and finite; multiplies the rotated elements
+ *   inverse   0: (x1, x2) -> mscale (x1 cos a - x2 sin a, x1 sin a + x2 cos a);
+ *             1: by -a, which is the gradient with respect to the input
+ * The angle is reduced to a fraction of a turn in 64-bit fixed point, so far
+ * positions lose nothing; the rotation is fp32, rounded once to bf16.  T == 0
+ * is a valid call that does nothing.
+ */
+nvq_status rope_apply(const void* q, int64_t ld_q, void* q_out, int64_t ld_qo, int Hq,
+                      const void* k, int64_t ld_k, void* k_out, int64_t ld_ko, int Hk, int64_t T,
+                      int D, int rot_dim, int interleaved, const int32_t* positions, int axes,
+                      const int* axis_pairs, const double* inv_freq, float mscale, int inverse,
+                      nvq_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Paged NVFP4 key-value cache                                              */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A cache is a pool of pages of NVQ_KV_PAGE tokens, uint8 [num_pages, Hkv, R],
+ * R = nvfp4_kv_page_bytes(1, D).  The record of one page and KV head is
+ *   K codes [128][D/2] | V codes [128][D/2] | K scales [128][D/16] | V scales [128][D/16]
+ * with the codes and E4M3 scale bytes of nvfp4_quantize_codes under the unit
+ * global scale, blocks along D: the K~ and V~ of attn_qat_fwd.  A sequence's
+ * page i (its tokens [128 i, 128 i + 128)) is pool page page_table[b][i]; only
+ * the entries of pages that hold tokens are read.  The pool is 16-byte aligned.
+ *
+ * Device-side tables (page_table int32 [B, max_pages], row stride ld_table >=
+ * max_pages; seq_lens int32 [B]) are read by the kernels, so captured graphs
+ * follow their changes.  A page number outside [0, num_pages), or a length over
+ * 128 * max_pages, is never followed: the write is left out, the key treated as
+ * not visible, and NVQ_ERR_INVALID recorded for nvq_device_status().
+ */
+#define NVQ_KV_PAGE 128
+
+/* Bytes of one page: Hkv * 144 * D; 0 for invalid sizes (D must be 64 or 128). */
+size_t nvfp4_kv_page_bytes(int Hkv, int D);
+
+/*
+ * Quantizes new tokens' K and V into the cache.
+ *   k, v       bf16 [T, Hkv, D], token strides ld_k, ld_v (elements, % 8 == 0,
+ *              >= Hkv*D)
+ *   cu_tokens  int32 [B + 1]: sequence b's new tokens are rows [cu_tokens[b],
+ *              cu_tokens[b + 1]), not decreasing; rows outside all of them are
+ *              ignored.  NULL: one token per sequence (T == B)
+ *   seq_lens   lengths AFTER the append: the last new token of sequence b is
+ *              written at position seq_lens[b] - 1, those before it in order.
+ *              Tokens that would fall before position 0 are ignored (a padded
+ *              batch gives its empty places length 0)
+ * Two sequences must not be given the same page for new tokens.  T == 0 is a
+ * valid call that does nothing.
+ */
+nvq_status nvfp4_kv_append(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int64_t T,
+                           int B, int Hkv, int D, const int32_t* cu_tokens,
+                           const int32_t* seq_lens, const int32_t* page_table, int64_t ld_table,
+                           int max_pages, void* pool, int64_t num_pages, nvq_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over the cache (the serving form of
+ * attn_qat_fwd: the last row of a causal forward).
+ *   q     bf16 [B, H, D], row stride ld_q (elements, % 8 == 0, >= H*D);
+ *         H % Hkv == 0, query head h reads KV head h / (H / Hkv)
+ *   o     bf16 [B, H, D] contiguous; lse f32 [B, H] or NULL (written)
+ *   S_j = scale * q~ . K~_j over the visible keys j of the sequence,
+ *   lse = ln sum exp S_j,  o = sum exp(S_j - lse) V~_j
+ * with q~ the NVFP4 fake quantization of q and the probabilities left
+ * unquantized (attn_qat_fwd_hp's O_hp; f16 inputs of the tensor-core product).
+ * Visible keys: all j < seq_lens[b] when window == 0; with window > 0 the last
+ * `window` of them and the first `sinks`.  The new token's own K and V are in
+ * the cache (append first).  A sequence without visible keys gets o = 0 and
+ * lse = -inf.  D in {64, 128}; window, sinks >= 0.  Long sequences are split
+ * over the GPU and joined in a fixed order: results do not vary from run to run.
+ * ws: attn_qat_decode_workspace(B, H, Hkv, D, max_pages) bytes, 256-byte
+ * aligned; its size follows from the current device's multiprocessor count.
+ */
+size_t attn_qat_decode_workspace(int B, int H, int Hkv, int D, int max_pages);
+nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_t num_pages,
+                           const int32_t* page_table, int64_t ld_table, int max_pages,
+                           const int32_t* seq_lens, int B, int H, int Hkv, int D, float scale,
+                           int window, int sinks, void* o, float* lse, void* ws, size_t ws_bytes,
+                           nvq_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Per-kernel device timing (a profiling aid; no counterpart in the pages)  */
 /* ------------------------------------------------------------------------ */
 
 /* Kernel kinds the library launches. */
 enum {
-  NVQ_KERNEL_QUANTIZE = 0,   /* NVFP4 fake-quant / codes pass (also inside the attention calls) */
-  NVQ_KERNEL_ATTN_FWD = 1,   /* attention forward */
+  NVQ_KERNEL_QUANTIZE = 0,   /* NVFP4 fake-quant / codes pass (also inside the attention calls); cache append */
+  NVQ_KERNEL_ATTN_FWD = 1,   /* attention forward; single tokens over the cache (with the join) */
   NVQ_KERNEL_BWD_DELTA = 2,  /* backward pre-pass delta = rowsum(dO * o) */
   NVQ_KERNEL_BWD_DKDV = 3,   /* backward, key-outer dK and dV kernel */
   NVQ_KERNEL_BWD_DQ = 4,     /* backward, query-outer dQ kernel */
   NVQ_KERNEL_GLOBAL_SF = 5,  /* static global scale (amax reduction and finalize) */
-  NVQ_KERNEL_VSA = 6,        /* block-sparse support: token reorder, block selection, list transpose */
+  NVQ_KERNEL_VSA = 6,        /* block-sparse support: token reorder, block selection, list
+                                transpose; rotary positions */
   NVQ_KERNEL_LINEAR = 7,     /* NVFP4 linear: the FP4 and BF16 GEMMs and the bias gradient */
   NVQ_KERNEL_KINDS = 8
 };

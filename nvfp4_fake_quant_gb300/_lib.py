@@ -57,6 +57,21 @@ SIGNATURES = {
     "nvfp4_linear_bwd_workspace": (c_size_t, [c_int64, c_int64, c_int64]),
     "nvfp4_linear_bwd": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64,
                                  c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "nvfp4_linear_packed_workspace": (c_size_t, [c_int64, c_int64, c_int64]),
+    "nvfp4_linear_packed_fwd": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p,
+                                        c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                                        c_size_t, c_void_p]),
+    "rope_apply": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int, c_void_p, c_int64, c_void_p,
+                           c_int64, c_int, c_int64, c_int, c_int, c_int, c_void_p, c_int, c_void_p,
+                           c_void_p, c_float, c_int, c_void_p]),
+    "nvfp4_kv_page_bytes": (c_size_t, [c_int, c_int]),
+    "nvfp4_kv_append": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int, c_int, c_int,
+                                c_void_p, c_void_p, c_void_p, c_int64, c_int, c_void_p, c_int64,
+                                c_void_p]),
+    "attn_qat_decode_workspace": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "attn_qat_decode": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int,
+                                c_void_p, c_int, c_int, c_int, c_int, c_float, c_int, c_int,
+                                c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "vsa_reorder": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                             c_int, c_void_p, c_void_p]),
     "vsa_select_workspace": (c_size_t, [c_int, c_int, c_int, c_int]),

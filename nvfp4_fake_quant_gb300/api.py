@@ -338,6 +338,315 @@ class NVFP4Linear(torch.nn.Module):
     def forward(self, x):
         return NVFP4LinearFunction.apply(x, self.weight, self.bias, self.input_global_sf)
 
+    def pack(self) -> "NVFP4PackedLinear":
+        """The layer for serving: its weight quantized once, under the same scale."""
+        return NVFP4PackedLinear(self.weight, self.bias, self.input_global_sf)
+
+
+# ------------------------------------------------- single tokens: shared helpers
+
+def _same_device(*tensors):
+    """The common device of the tensors (None entries left out)."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is not None and t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device}: one device expected")
+            dev = t.device
+    return dev
+
+
+def _call_on(device, name, *args):
+    """The entry point, with the stream of ``device`` as its last argument and that
+    device current (the library works on the current device)."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        _lib.call(name, *args, stream)
+    else:
+        with torch.cuda.device(device):
+            _lib.call(name, *args, stream)
+
+
+def _rows_nd(x: torch.Tensor, name: str):
+    """(rows, heads, D, row stride) of a bf16 [rows, heads, D] tensor whose rows are
+    contiguous inside."""
+    _check(x, name)
+    if x.dim() != 3 or (x.numel() > 0 and ((x.shape[2] > 1 and x.stride(2) != 1) or
+                                           (x.shape[1] > 1 and x.stride(1) != x.shape[2]))):
+        raise ValueError(f"{name} must be [tokens, heads, D] with contiguous heads")
+    t, h, d = x.shape
+    return t, h, d, (x.stride(0) if t > 1 else max(h * d, x.stride(0)))
+
+
+def _check_i32(t, name, dim):
+    _check(t, name, torch.int32)
+    if t.dim() != dim or (t.numel() > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a {dim}-dimensional int32 tensor with unit last stride")
+
+
+def _check_out(t, name, shape, dtype, like):
+    """An output to write: the caller's, checked, or a new contiguous one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _check(t, name, dtype)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)}")
+    return t
+
+
+# ------------------------------------------------------- NVFP4 linear, packed weight
+
+def nvfp4_linear_packed_workspace(m: int, n: int, k: int) -> int:
+    return int(_lib.load().nvfp4_linear_packed_workspace(m, n, k))
+
+
+def nvfp4_linear_packed_fwd(x, w_codes, w_scales, w_global_sf=None, bias=None, x_global_sf=None,
+                            out=None, workspace=None):
+    """out [M, N] bf16 = x~ w~^T (+ bias) for a weight packed by nvfp4_quantize_tiled
+    (codes uint8 [N, K/2], tiled scales) under ``w_global_sf`` (None: 1).  x bf16
+    [M, K], rows may be strided; ``x_global_sf`` None: 448*6/amax(x)."""
+    _check(x, "x")
+    m, k, ld = _rows_ld(x)
+    _check(w_codes, "w_codes", torch.uint8)
+    _check(w_scales, "w_scales", torch.uint8)
+    n = w_codes.shape[0]
+    if w_codes.dim() != 2 or w_codes.shape[1] * 2 != k or not w_codes.is_contiguous():
+        raise ValueError(f"w_codes must be contiguous [N, {k // 2}], got {tuple(w_codes.shape)}")
+    if not w_scales.is_contiguous() or w_scales.numel() != nvfp4_tiled_scale_bytes(n, k):
+        raise ValueError("w_scales must be the tiled scales of w_codes")
+    if bias is not None:
+        _check(bias, "bias")
+        if tuple(bias.shape) != (n,) or not bias.is_contiguous():
+            raise ValueError(f"bias must be contiguous [{n}]")
+    dev = _same_device(x, w_codes, w_scales, w_global_sf, bias, x_global_sf, out, workspace)
+    out = _check_out(out, "out", (m, n), BF16, x)
+    ws = _workspace(nvfp4_linear_packed_workspace(m, n, k), dev, workspace)
+    _call_on(dev, "nvfp4_linear_packed_fwd", _ptr(x), ld if m > 1 else max(ld, k), _ptr(w_codes),
+             _ptr(w_scales), _opt_ptr(w_global_sf), _ptr(bias), m, n, k, _opt_ptr(x_global_sf),
+             _ptr(out), _ptr(ws), ws.numel() * ws.element_size())
+    return out
+
+
+class NVFP4PackedLinear(torch.nn.Module):
+    """The serving form of NVFP4Linear: the weight's codes, tiled scales and global
+    scale, packed once; the forward of the layer it was packed from."""
+
+    def __init__(self, weight, bias=None, input_global_sf=None):
+        super().__init__()
+        w = weight.detach().contiguous()
+        self.register_buffer("weight_global_sf", nvfp4_global_sf(w))
+        codes, scales = nvfp4_quantize_tiled(w, self.weight_global_sf)
+        self.register_buffer("codes", codes)
+        self.register_buffer("scales", scales)
+        self.register_buffer("bias", None if bias is None else bias.detach().clone())
+        self.register_buffer("input_global_sf", input_global_sf)
+
+    @torch.no_grad()
+    def forward(self, x):
+        out = nvfp4_linear_packed_fwd(x.reshape(-1, x.shape[-1]), self.codes, self.scales,
+                                      self.weight_global_sf, self.bias, self.input_global_sf)
+        return out.view(*x.shape[:-1], self.codes.shape[0])
+
+
+# ----------------------------------------------------------------- rotary positions
+
+def rope_inv_freq(rot_dim: int, theta: float = 10000.0, scaling: str | None = None,
+                  factor: float = 1.0, original_len: int = 8192, beta_fast: float = 32.0,
+                  beta_slow: float = 1.0, device=None):
+    """(inv_freq f64 [rot_dim/2], mscale) for rope_apply.
+
+    inv_freq[p] = theta^(-2p/rot_dim).  For contexts ``factor`` times longer than the
+    ``original_len`` trained on, ``scaling`` is
+      "linear"    every frequency divided by factor (positions interpolated);
+      "theta"     theta raised to theta * factor^(rot_dim/(rot_dim - 2)), which divides
+                  the lowest frequency by factor and leaves the highest;
+      "by_parts"  pairs that turn fewer than beta_slow times in original_len positions
+                  divided by factor, those over beta_fast kept, a linear blend between;
+                  rotated elements multiplied by mscale = 0.1 ln(factor) + 1.
+    """
+    if rot_dim < 2 or rot_dim % 2 or not theta > 0 or not factor >= 1:
+        raise ValueError("rot_dim must be even and >= 2, theta > 0, factor >= 1")
+    if scaling not in (None, "linear", "theta", "by_parts"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    mscale = 1.0
+    if scaling == "theta" and rot_dim > 2:
+        theta = theta * factor ** (rot_dim / (rot_dim - 2))
+    f = float(theta) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts" and factor > 1:
+        if not beta_fast > beta_slow:
+            raise ValueError("beta_fast must be over beta_slow")
+        turns = original_len * f / (2 * math.pi)
+        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0, 1)
+        f = f / factor * (1 - keep) + f * keep
+        mscale = 0.1 * math.log(factor) + 1
+    return f.to(device), mscale
+
+
+def rope_apply(q, k, positions, inv_freq, interleaved=False, axis_pairs=None, mscale=1.0,
+               inverse=False, q_out=None, k_out=None):
+    """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (bf16, token rows may be
+    strided; k may be None): returns (q_out, k_out).  ``positions`` int32 [T] or
+    [T, axes]; ``axis_pairs`` the number of pairs that turn by each axis (default:
+    all by the first); ``inv_freq`` f64 [rot_dim/2].  q_out / k_out may be q / k."""
+    t, hq, d, ld_q = _rows_nd(q, "q")
+    _check(inv_freq, "inv_freq", torch.float64)
+    if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous vector")
+    rot = 2 * inv_freq.numel()
+    pos = positions.unsqueeze(1) if positions.dim() == 1 else positions
+    _check(pos, "positions", torch.int32)
+    axes = pos.shape[1] if pos.dim() == 2 else 0
+    if pos.dim() != 2 or pos.shape[0] != t or not pos.is_contiguous():
+        raise ValueError(f"positions must be contiguous [{t}] or [{t}, axes]")
+    pairs = (rot // 2,) + (0,) * (axes - 1) if axis_pairs is None else tuple(axis_pairs)
+    if len(pairs) != axes or not 1 <= axes <= 3:
+        raise ValueError(f"axis_pairs must give one count for each of 1..3 axes, got {pairs}")
+    outs = [torch.empty((t, hq, d), dtype=BF16, device=q.device) if q_out is None else q_out, None]
+    t2, h2, d2, ld_qo = _rows_nd(outs[0], "q_out")
+    hk, ld_k, ld_ko = 0, 0, 0
+    if k is not None:
+        tk, hk, dk, ld_k = _rows_nd(k, "k")
+        outs[1] = torch.empty((t, hk, d), dtype=BF16, device=q.device) if k_out is None else k_out
+        t3, h3, d3, ld_ko = _rows_nd(outs[1], "k_out")
+        if (tk, dk) != (t, d) or (t3, h3, d3) != (t, hk, d):
+            raise ValueError(f"k and k_out must be [{t}, heads, {d}]")
+    if (t2, h2, d2) != (t, hq, d):
+        raise ValueError(f"q_out must be {(t, hq, d)}, got {(t2, h2, d2)}")
+    dev = _same_device(q, k, pos, inv_freq, *outs)
+    _call_on(dev, "rope_apply", _ptr(q), ld_q, _ptr(outs[0]), ld_qo, hq, _ptr(k), ld_k,
+             _ptr(outs[1]), ld_ko, hk, t, d, rot, int(bool(interleaved)), _ptr(pos), axes,
+             (_lib.c_int * axes)(*pairs), _ptr(inv_freq), float(mscale), int(bool(inverse)))
+    return outs[0], outs[1]
+
+
+class RotaryFunction(torch.autograd.Function):
+    """rope_apply with its gradient (the rotation back, scaled alike)."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, interleaved, axis_pairs, mscale):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.args = (interleaved, axis_pairs, mscale)
+        return rope_apply(q, k, positions, inv_freq, *ctx.args)
+
+    @staticmethod
+    def backward(ctx, gq, gk):
+        positions, inv_freq = ctx.saved_tensors
+        gq, gk = rope_apply(gq.contiguous(), gk.contiguous(), positions, inv_freq, *ctx.args,
+                            inverse=True)
+        return gq, gk, None, None, None, None, None
+
+
+class Rotary(torch.nn.Module):
+    """Rotary positions of q and k before AttnQAT: forward(q, k, positions) with q, k
+    bf16 [B, N, H, D] (or [T, H, D]) and positions int32 of N (shared by the batch) or
+    B*N rows, [rows] or [rows, axes].  ``scaling`` and the rest as in rope_inv_freq."""
+
+    def __init__(self, rot_dim: int, interleaved: bool = False, axis_pairs=None, device=None,
+                 inv_freq: torch.Tensor | None = None, **frequencies):
+        super().__init__()
+        self.mscale = 1.0
+        if inv_freq is None:
+            inv_freq, self.mscale = rope_inv_freq(rot_dim, device=device, **frequencies)
+        if inv_freq.numel() * 2 != rot_dim:
+            raise ValueError(f"inv_freq must have {rot_dim // 2} entries")
+        self.register_buffer("inv_freq", inv_freq, persistent=False)
+        self.interleaved, self.axis_pairs = interleaved, axis_pairs
+
+    def forward(self, q, k, positions):
+        t = q.shape[:-2].numel()
+        if positions.shape[0] != t and q.dim() == 4 and positions.shape[0] == q.shape[1]:
+            positions = positions.repeat(q.shape[0], *(1,) * (positions.dim() - 1))
+        q3, k3 = (x.reshape(t, *x.shape[-2:]) for x in (q, k))
+        qo, ko = RotaryFunction.apply(q3, k3, positions, self.inv_freq, self.interleaved,
+                                      self.axis_pairs, self.mscale)
+        return qo.view(q.shape), ko.view(k.shape)
+
+
+# ------------------------------------------------------------- paged NVFP4 KV cache
+
+KV_PAGE = 128  # tokens per page (NVQ_KV_PAGE)
+
+
+def nvfp4_kv_page_bytes(hkv: int, d: int) -> int:
+    return int(_lib.load().nvfp4_kv_page_bytes(hkv, d))
+
+
+def nvfp4_kv_pool(num_pages: int, hkv: int, d: int, device="cuda") -> torch.Tensor:
+    """A zeroed pool of pages: uint8 [num_pages, Hkv, record bytes]."""
+    record = nvfp4_kv_page_bytes(1, d)
+    if num_pages < 1 or hkv < 1 or record == 0:
+        raise ValueError(f"bad pool sizes: {num_pages} pages, {hkv} heads of {d}")
+    return torch.zeros((num_pages, hkv, record), dtype=torch.uint8, device=device)
+
+
+def _check_cache(pool, page_table, seq_lens, d):
+    _check(pool, "pool", torch.uint8)
+    if pool.dim() != 3 or not pool.is_contiguous() or pool.shape[2] != 144 * d:
+        raise ValueError(f"pool must be contiguous uint8 [pages, Hkv, {144 * d}], "
+                         f"got {tuple(pool.shape)}")
+    _check_i32(page_table, "page_table", 2)
+    _check_i32(seq_lens, "seq_lens", 1)
+    if page_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError(f"page_table has {page_table.shape[0]} rows, seq_lens "
+                         f"{seq_lens.shape[0]}")
+    b, max_pages = page_table.shape
+    return b, max_pages, (page_table.stride(0) if b > 1 else max_pages)
+
+
+def nvfp4_kv_append(k, v, seq_lens, page_table, pool, cu_tokens=None) -> None:
+    """Quantizes new tokens' k, v (bf16 [T, Hkv, D], token rows may be strided) into the
+    pages of ``pool``.  seq_lens int32 [B]: lengths after the append; page_table int32
+    [B, max_pages]; cu_tokens int32 [B + 1] (None: one token per sequence)."""
+    t, hkv, d, ld_k = _rows_nd(k, "k")
+    tv, hv, dv, ld_v = _rows_nd(v, "v")
+    if (tv, hv, dv) != (t, hkv, d):
+        raise ValueError(f"v must be {(t, hkv, d)}, got {(tv, hv, dv)}")
+    b, max_pages, ld_t = _check_cache(pool, page_table, seq_lens, d)
+    if pool.shape[1] != hkv:
+        raise ValueError(f"pool has {pool.shape[1]} heads, k {hkv}")
+    if cu_tokens is not None:
+        _check_i32(cu_tokens, "cu_tokens", 1)
+        if cu_tokens.shape[0] != b + 1:
+            raise ValueError(f"cu_tokens must have {b + 1} entries")
+    elif t != b:
+        raise ValueError(f"without cu_tokens one token per sequence is expected: {t} tokens, "
+                         f"{b} sequences")
+    dev = _same_device(k, v, seq_lens, page_table, pool, cu_tokens)
+    _call_on(dev, "nvfp4_kv_append", _ptr(k), ld_k, _ptr(v), ld_v, t, b, hkv, d, _ptr(cu_tokens),
+             _ptr(seq_lens), _ptr(page_table), ld_t, max_pages, _ptr(pool), pool.shape[0])
+
+
+def attn_qat_decode_workspace(b, h, hkv, d, max_pages) -> int:
+    return int(_lib.load().attn_qat_decode_workspace(b, h, hkv, d, max_pages))
+
+
+def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0, o=None, lse=None,
+                    workspace=None):
+    """Attention of one new token per sequence over the paged cache: q bf16 [B, H, D]
+    (rows may be strided), returns (o bf16 [B, H, D], lse f32 [B, H]).  ``window`` > 0:
+    only the last ``window`` keys and the first ``sinks`` are visible."""
+    b, h, d, ld_q = _rows_nd(q, "q")
+    bt, max_pages, ld_t = _check_cache(pool, page_table, seq_lens, d)
+    if bt != b:
+        raise ValueError(f"q has {b} rows, page_table {bt}")
+    hkv = pool.shape[1]
+    scale = _scale(scale, d)
+    o = _check_out(o, "o", (b, h, d), BF16, q)
+    lse = _check_out(lse, "lse", (b, h), torch.float32, q)
+    dev = _same_device(q, pool, page_table, seq_lens, o, lse, workspace)
+    if dev.index == torch.cuda.current_device():
+        need = attn_qat_decode_workspace(b, h, hkv, d, max_pages)
+    else:
+        with torch.cuda.device(dev):  # the size follows from the device's SM count
+            need = attn_qat_decode_workspace(b, h, hkv, d, max_pages)
+    ws = _workspace(need, dev, workspace)
+    _call_on(dev, "attn_qat_decode", _ptr(q), ld_q, _ptr(pool), pool.shape[0], _ptr(page_table),
+             ld_t, max_pages, _ptr(seq_lens), b, h, hkv, d, scale, int(window), int(sinks),
+             _ptr(o), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size())
+    return o, lse
+
 
 # Kernel kinds of nvq_timing_read (include/nvfp4attn.h, NVQ_KERNEL_*)
 KERNEL_KINDS = {"quantize": 0, "attn_fwd": 1, "bwd_delta": 2, "bwd_dkdv": 3, "bwd_dq": 4,

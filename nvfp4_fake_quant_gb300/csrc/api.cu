@@ -532,7 +532,7 @@ nvq_status nvq_device_status(nvq_stream_t stream) {
     const int zero = 0;
     e = cudaMemcpyToSymbol(g_error_word, &zero, sizeof(int));
     if (e != cudaSuccess) return fail_cuda("clear error word", e);
-    return NVQ_ERR_TIMEOUT;
+    return v == kErrTable ? NVQ_ERR_INVALID : NVQ_ERR_TIMEOUT;
   }
   return NVQ_OK;
 }

@@ -45,6 +45,21 @@ LinWs lin_ws(int64_t M, int64_t N, int64_t K) {
   return w;
 }
 
+// Workspace of the packed form: codes, tiled scales and global scale of x, alpha.
+struct PackedWs {
+  size_t cx, sx, gx, ab, total;
+};
+
+PackedWs packed_ws(int64_t M, int64_t K) {
+  PackedWs w{};
+  w.cx = 0;
+  w.sx = rup(static_cast<size_t>(M) * static_cast<size_t>(K / 2), 256);
+  w.gx = w.sx + rup(tiled_scale_bytes(M, K), 256);
+  w.ab = w.gx + 256;
+  w.total = w.ab + 256;
+  return w;
+}
+
 // alpha = 1 / (gsf_w * gsf_x) (a NULL scale counts as 1).
 __global__ void alpha_kernel(const float* gx, const float* gw, float* ab) {
   const float a = (gx != nullptr ? *gx : 1.0f) * (gw != nullptr ? *gw : 1.0f);
@@ -125,6 +140,35 @@ nvq_status cuda_st(const char* where, cudaError_t e) {
   return e == cudaSuccess ? NVQ_OK : nvq::fail_cuda(where, e);
 }
 
+// The FP4 GEMM on quantized operands: out = alpha x~ w~^T (+ bias).
+nvq_status gemm_fp4(const uint8_t* cx, const uint8_t* sx, const uint8_t* cw, const uint8_t* sw,
+                    const float* ab, const void* bias, int64_t M, int64_t N, int64_t K, void* out,
+                    cudaStream_t stream) {
+  int* err = nvq::device_error_word();
+  if (err == nullptr) return NVQ_ERR_CUDA;
+  CUtensorMap tx, tw;
+  int r;
+  if ((r = nvq::make_codes_map(&tx, cx, M, K / 2)) != 0)
+    return nvq::fail_driver("cuTensorMapEncodeTiled", r);
+  if (K <= nvq::kGemmFp4XresMaxK) {
+    // x resident per CTA, W shared across a cluster by multicast, TMA stores
+    CUtensorMap tout;
+    if ((r = nvq::make_codes_map(&tw, cw, N, K / 2, 32)) != 0 ||
+        (r = nvq::make_2d_map(&tout, out, M, N, 32)) != 0)
+      return nvq::fail_driver("cuTensorMapEncodeTiled", r);
+    return cuda_st("fp4 gemm", nvq::timed(NVQ_KERNEL_LINEAR, stream, [&] {
+                     return nvq::launch_gemm_fp4_xres(tx, tw, tout, sx, sw, ab, bias,
+                                                      M, N, K, out, err, stream);
+                   }));
+  }
+  if ((r = nvq::make_codes_map(&tw, cw, N, K / 2)) != 0)
+    return nvq::fail_driver("cuTensorMapEncodeTiled", r);
+  return cuda_st("fp4 gemm", nvq::timed(NVQ_KERNEL_LINEAR, stream, [&] {
+                   return nvq::launch_gemm_fp4(tx, tw, sx, sw, ab, bias, M, N, K, out,
+                                               err, stream);
+                 }));
+}
+
 // bias gradient scratch: fp32 sums [N] and one counter per block of 2048 columns
 size_t bwd_scratch(int64_t N) {
   return nvq::rup(static_cast<size_t>(N) * 4, 256) +
@@ -193,29 +237,49 @@ nvq_status nvfp4_linear_fwd(const void* x, const void* w, const void* bias, int6
   if (e != cudaSuccess) return nvq::fail_cuda("quantize x, w", e);
   nvq::alpha_kernel<<<1, 1, 0, stream>>>(use_gx, use_gw, ab);
   if ((e = cudaGetLastError()) != cudaSuccess) return nvq::fail_cuda("alpha", e);
-  int* err = nvq::device_error_word();
-  if (err == nullptr) return NVQ_ERR_CUDA;
-  CUtensorMap tx, tw;
-  int r;
-  if ((r = nvq::make_codes_map(&tx, wb + L.cx, M, K / 2)) != 0)
-    return nvq::fail_driver("cuTensorMapEncodeTiled", r);
-  if (K <= nvq::kGemmFp4XresMaxK) {
-    // x resident per CTA, W shared across a cluster by multicast, TMA stores
-    CUtensorMap tout;
-    if ((r = nvq::make_codes_map(&tw, wb + L.cw, N, K / 2, 32)) != 0 ||
-        (r = nvq::make_2d_map(&tout, out, M, N, 32)) != 0)
-      return nvq::fail_driver("cuTensorMapEncodeTiled", r);
-    return cuda_st("fp4 gemm", nvq::timed(NVQ_KERNEL_LINEAR, stream, [&] {
-                     return nvq::launch_gemm_fp4_xres(tx, tw, tout, wb + L.sx, wb + L.sw, ab, bias,
-                                                      M, N, K, out, err, stream);
-                   }));
+  return gemm_fp4(wb + L.cx, wb + L.sx, wb + L.cw, wb + L.sw, ab, bias, M, N, K, out, stream);
+}
+
+size_t nvfp4_linear_packed_workspace(int64_t M, int64_t N, int64_t K) {
+  if (check_lin(M, N, K) != NVQ_OK) return 0;
+  return nvq::packed_ws(M, K).total;
+}
+
+nvq_status nvfp4_linear_packed_fwd(const void* x, int64_t ld_x, const uint8_t* w_codes,
+                                   const uint8_t* w_scales, const float* w_global_sf,
+                                   const void* bias, int64_t M, int64_t N, int64_t K,
+                                   const float* x_global_sf, void* out, void* ws, size_t ws_bytes,
+                                   nvq_stream_t stream) {
+  nvq_status st = check_lin(M, N, K);
+  if (st != NVQ_OK) return st;
+  if (ld_x < K || ld_x % 8 != 0) return NVQ_ERR_INVALID;
+  const void* ptrs[] = {x, w_codes, w_scales, out};
+  for (const void* p : ptrs)
+    if (p == nullptr || !al16(p)) return NVQ_ERR_INVALID;
+  if (bias != nullptr && !al16(bias)) return NVQ_ERR_INVALID;
+  const float* gsfs[] = {x_global_sf, w_global_sf};
+  for (const float* g : gsfs)
+    if (g != nullptr && (reinterpret_cast<uintptr_t>(g) & 3u) != 0) return NVQ_ERR_INVALID;
+  const nvq::PackedWs L = nvq::packed_ws(M, K);
+  if (ws == nullptr || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return NVQ_ERR_WORKSPACE;
+  uint8_t* wb = static_cast<uint8_t*>(ws);
+  float* ab = reinterpret_cast<float*>(wb + L.ab);
+  const float* gx = x_global_sf;
+  cudaError_t e = cudaSuccess;
+  if (gx == nullptr) {
+    float* g = reinterpret_cast<float*>(wb + L.gx);
+    e = nvq::timed(NVQ_KERNEL_GLOBAL_SF, stream, [&] { return nvq::launch_global_sf(x, M, K, ld_x, g, stream); });
+    if (e != cudaSuccess) return nvq::fail_cuda("global scale", e);
+    gx = g;
   }
-  if ((r = nvq::make_codes_map(&tw, wb + L.cw, N, K / 2)) != 0)
-    return nvq::fail_driver("cuTensorMapEncodeTiled", r);
-  return cuda_st("fp4 gemm", nvq::timed(NVQ_KERNEL_LINEAR, stream, [&] {
-                   return nvq::launch_gemm_fp4(tx, tw, wb + L.sx, wb + L.sw, ab, bias, M, N, K, out,
-                                               err, stream);
-                 }));
+  e = nvq::timed(NVQ_KERNEL_QUANTIZE, stream, [&] {
+    return nvq::launch_quant_tiled(x, M, K, ld_x, gx, wb + L.cx, wb + L.sx, stream);
+  });
+  if (e != cudaSuccess) return nvq::fail_cuda("quantize x", e);
+  nvq::alpha_kernel<<<1, 1, 0, stream>>>(gx, w_global_sf, ab);
+  if ((e = cudaGetLastError()) != cudaSuccess) return nvq::fail_cuda("alpha", e);
+  return gemm_fp4(wb + L.cx, wb + L.sx, w_codes, w_scales, ab, bias, M, N, K, out, stream);
 }
 
 size_t nvfp4_linear_bwd_workspace(int64_t M, int64_t N, int64_t K) {

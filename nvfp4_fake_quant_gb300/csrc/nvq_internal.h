@@ -13,6 +13,10 @@ namespace nvq {
 
 constexpr int kTile = 128;  // query / key rows per attention tile
 
+// Device error word: a page number or sequence length of the paged cache out of
+// range (recorded with atomicMax, so that a timeout, a larger code, stays).
+constexpr int kErrTable = 1;
+
 // Quantizer output modes.
 enum QuantMode : int { kUnitBf16 = 0, kUnitF16 = 1, kStaticBf16 = 2 };
 

@@ -17,6 +17,8 @@ Modules
                the cube-mean score selection of key tiles.
 ``linear``     the NVFP4 linear: quantized forward with the FP4 GEMM's global-scale
                alpha, straight-through backward, the 128 x 4 tiled scale layout.
+``serving``    rotary positions, the paged NVFP4 cache's records, single-token
+               attention over it.
 
 Sources (web pages on the subject; cited by title and section):
   * "nvfp4_qad.py" (FastVideo ``fastvideo/layers/quantization/nvfp4_qad.py``):

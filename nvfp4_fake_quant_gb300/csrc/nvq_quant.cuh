@@ -49,6 +49,14 @@ __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t b) {
   return h;
 }
 
+// Two E4M3FN bit patterns (bytes 0 and 1 of `b`) to their values as an f16x2.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) {
+  uint32_t h;
+  const uint16_t in = static_cast<uint16_t>(b);
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(in));
+  return h;
+}
+
 __device__ __forceinline__ float f16lo_to_f32(uint32_t h2) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(h2 & 0xFFFFu)));
 }

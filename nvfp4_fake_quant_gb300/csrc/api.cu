@@ -182,6 +182,22 @@ int make_bnhd_u8_map(CUtensorMap* map, const void* base, int B, int N, int H, in
   return static_cast<int>(r);
 }
 
+int make_kv_codes_map(CUtensorMap* map, const void* pool, int64_t records, int D) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return CUDA_ERROR_NOT_FOUND;
+  // a record is 288 rows of D/2 bytes; its first 128 are the K codes
+  const cuuint64_t rb = static_cast<cuuint64_t>(D) / 2;
+  const cuuint64_t dims[4] = {rb, 288, static_cast<cuuint64_t>(records), 1};
+  const cuuint64_t strides[3] = {rb, 288 * rb, 288 * rb * static_cast<cuuint64_t>(records)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(rb), 32, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pool), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return static_cast<int>(r);
+}
+
 int* device_error_word() { return error_word(); }
 
 int make_codes_map(CUtensorMap* map, const void* base, int64_t rows, int64_t row_bytes,

@@ -15,21 +15,27 @@
 // leaves (m, l, sum p V~) per run in the workspace, and a second small kernel
 // joins them in run order, so results do not vary from run to run.
 //
-// One CTA: a producer warp fetches records by bulk copies into a ring of stages
-// (only the rows that hold tokens) and writes each tile's description beside it;
-// eight consumer warps take 16 of a tile's keys each.  The products run on the
-// tensor cores with the query heads as the 8-column side (mma.sync, not tcgen05:
-// the operands are decoded in registers, where the fragments are wanted, and
-// tcgen05 would need them written back to shared memory as f16; at 8 columns the
-// products are 1/4 of the time that the bytes allow):
-//   S^T [16 keys x 8 heads] = K~ [16 x D] q~^T      K~ decoded as the A operand
-//   O^T [D x 8 heads] += V~^T [D x 16 keys] P^T     V~ decoded as the A operand
-// The contraction of the first runs over D in an order of its own: lane t of four
-// owns D/4 consecutive elements (one 16-byte load for D = 128), its q~ fragment
-// likewise.  S's accumulator becomes the second product's B operand by an 8x8
-// transpose across lanes.  Codes become f16 by the hardware conversion times
-// their scale, which is exact; p is rounded to f16 (as in the training forward),
-// its sum is taken before the rounding, all sums are fp32.
+// One CTA, six warps (three CTAs per SM at up to 8 query heads):
+//   producer  fetches records into a ring of stages (K codes by tensor-map loads
+//             with the swizzle the MMA reads, the rest by bulk copies; only the
+//             rows that hold tokens) and describes each tile beside it
+//   MMA       quantizes q of a new segment, brings K's scales into the order of
+//             the scale operand and issues S [128 keys x 16 heads] = K~ q~^T as
+//             block-scaled FP4 tcgen05 MMAs on the stored codes: K is never
+//             decoded.  (Decoding K in registers for mma.sync made the issue
+//             slots the bound: 159 us for 8 x 131072 tokens, 8 KV heads of 128.)
+//   4 x 32    keys: read S from tensor memory in the fragment layout of an
+//             m16n8 product, exponentiate, and accumulate
+//               O^T [D x 8 heads] += V~^T [D x 16 keys] P^T
+//             with V decoded as the A operand of mma.sync.  (V's scales run along
+//             D, so its codes cannot be the FP4 operand of a product over keys;
+//             decoded values are wanted in registers, where mma.sync takes them.)
+// The accumulator fragment of S becomes the B operand by an 8x8 transpose across
+// lanes.  Codes become f16 by the hardware conversion times their scale, exactly;
+// p is rounded to f16 (as in the training forward), its sum is taken before the
+// rounding; all sums are fp32.  The maximum that p refers to is raised only when
+// a score exceeds it by 8 (log2): p then stays below 2^8, far inside f16, and the
+// cross-lane maximum and the rescaling of O leave the common path.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -46,23 +52,34 @@ namespace nvq {
 
 namespace {
 
-constexpr int kWarps = 8;                        // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;      // and the producer
+constexpr int kWarps = 4;  // consumer warps, 32 keys of a tile each
+constexpr int kProducer = kWarps, kMma = kWarps + 1;
+constexpr int kThreads = (kWarps + 2) * 32;
+constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Per shape: query heads per CTA (8 NT), CTAs per SM and ring stages.
+// Per shape: query heads per CTA (8 NT), CTAs per SM, ring stages; shared memory.
 template <int D, int NT>
 struct Cfg {
   static constexpr int kHeads = 8 * NT;
-  static constexpr int kPerSm = NT == 1 ? 2 : 1;
-  static constexpr int kStages = D == 128 ? (NT == 1 ? 4 : 6) : 6;
+  static constexpr int kPerSm = NT == 1 ? 3 : 2;
+  static constexpr int kStages = D == 64 ? 6 : (NT == 1 ? 2 : 3);
   static constexpr int kRow = D + 4;  // floats of a head's row in the join area
   static constexpr uint32_t kRec = record_bytes(D);
-  static constexpr uint32_t kJoin = kStages * kRec;                            // float [8][heads][kRow]
-  static constexpr uint32_t kMl = kJoin + kWarps * kHeads * kRow * 4;          // float2 [8][heads]
-  static constexpr uint32_t kDesc = kMl + kWarps * kHeads * 8;                 // TileDesc [stages]
+  static constexpr uint32_t kQ = kHeads * D * 2;         // q of a segment that starts with the tile
+  static constexpr uint32_t kStage = kRec + kQ;
+  static constexpr uint32_t kQCodes = kStages * kStage;  // [2] q~ codes, 16 rows of D/2 bytes
+  static constexpr uint32_t kQScales = kQCodes + 2 * 1024;               // [2][D/64] blocks of 512
+  static constexpr uint32_t kJoin = kQScales + 2 * 1024;                 // float [4][heads][kRow]
+  static constexpr uint32_t kMl = kJoin + kWarps * kHeads * kRow * 4;    // float2 [4][heads]
+  static constexpr uint32_t kDesc = kMl + kWarps * kHeads * 8;           // TileDesc [stages]
   static constexpr uint32_t kBars = kDesc + kStages * 32;
-  static constexpr uint32_t kSmem = kBars + (2 * kStages + 2) * 8 + 16;
+  static constexpr uint32_t kSmem = kBars + (3 * kStages + 4) * 8 + 16 + 1024;  // + alignment
+  // tensor memory columns: S of stage s, scales of K of stage s, of q~ of buffer b
+  static constexpr uint32_t kSfa = 16 * kStages, kSfb = kSfa + kStages * (D / 16);
+  static constexpr uint32_t kCols = 128;
+  static_assert(kSfb + 2 * (D / 16) <= kCols, "tensor memory");
+  static_assert(kStage % 1024 == 0, "swizzle atoms");
 };
 
 enum : int { kStart = 1, kEnd = 2, kMasked = 4, kAbsent = 8 };
@@ -136,157 +153,125 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// tcgen05.ld of 16 lanes (keys) x 8 NT columns (heads): register 4 nt + e holds, as
+// the accumulator of an m16n8 product, key g (e < 2) or g + 8, head 8 nt + 2t + e % 2.
+template <int NT>
+__device__ __forceinline__ void load_scores(uint32_t taddr, float (&v)[NT][4]) {
+  uint32_t r[4 * NT];
+  if constexpr (NT == 1)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 4 * NT; ++i) v[i / 4][i % 4] = __uint_as_float(r[i]);
+}
+
 // State of a consumer warp for the current segment.  Lane = 4 g + t.
 template <int D, int NT>
 struct State {
-  uint32_t q[NT][D / 8];      // q~ of head g (of each group of 8), elements [t D/4, (t + 1) D/4)
-  float o[NT][D / 16][4];     // O^T: elements d = D/8 g + 2 i (+1: [2], [3]), heads 2t, 2t + 1
-  float m[NT][2], l[NT][2];   // running maximum (log2 units; all lanes) and this lane's sum
+  float o[NT][D / 16][4];    // O^T: elements d = D/8 g + 2 i (+1: [2], [3]), heads 2t, 2t + 1
+  float m[NT][2], l[NT][2];  // reference maximum (log2 units; all lanes) and this lane's sum
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+  }
 };
 
-template <int D, int NT>
-__device__ __forceinline__ void start_segment(const DecodeArgs& a, const TileDesc& td,
-                                              State<D, NT>& st, int g, int t) {
-  const int hk = td.hg / a.chunks, g0 = (td.hg % a.chunks) * 8 * NT;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int gi = g0 + nt * 8 + g;
-    if (gi < a.G) {
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + td.b * a.ld_q + static_cast<int64_t>(hk * a.G + gi) * D + t * (D / 4));
-#pragma unroll
-      for (int blk = 0; blk < D / 64; ++blk) {
-        const uint4 lo = __ldg(src + 2 * blk), hi = __ldg(src + 2 * blk + 1);
-        const uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        const Q16 r = quant16_unit<true>(x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) st.q[nt][8 * blk + j] = r.out[j];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) st.q[nt][j] = 0;
-    }
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) st.o[nt][i][e] = 0.f;
-    st.m[nt][0] = st.m[nt][1] = -INFINITY;
-    st.l[nt][0] = st.l[nt][1] = 0.f;
-  }
+__device__ __forceinline__ bool sees(const TileDesc& td, int sinks, int key) {
+  return key < td.len && (key >= td.wstart || key < sinks);
 }
 
-// Sixteen keys, rows r0..r0 + 15 of the record at `rec`.  Row index rho of the
-// first product's A operand is key r0 + key_of(rho): neighbouring lane groups and
-// the second product's lanes then hit different banks.
-__device__ __forceinline__ int key_of(int rho) { return rho ^ ((rho >> 1) & 1); }
-
+// Keys r0..r0 + 31 of the record at `rec`, scores at tensor memory address `tm`.
 template <int D, int NT>
-__device__ __forceinline__ void sixteen_keys(const DecodeArgs& a, const uint8_t* rec, int r0,
-                                             const TileDesc& td, bool masked, State<D, NT>& st,
-                                             int g, int t) {
-  constexpr int kSteps = D / 16;  // products over D; also tiles of 16 elements of O^T
+__device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* rec, int r0,
+                                          uint32_t tm, const TileDesc& td, State<D, NT>& st, int g,
+                                          int t) {
   constexpr int kRowCodes = D / 2, kRowScales = D / 16;
-  float s[NT][4];
-  {
-    // ---- S^T: codes and scales of keys rho = g and g + 8
-    uint32_t kc[2][D / 32], ks[2][D / 64];
+  float s[2][NT][4];
+  load_scores<NT>(tm, s[0]);
+  load_scores<NT>(tm + (16u << 16), s[1]);
+  // ---- codes and scales of V~: of each 16 keys 2t, 2t + 1, 2t + 8, 2t + 9, elements
+  // [D/8 g, D/8 (g + 1)).  Lanes of odd t fetch the odd key first: keys of both
+  // parities in one load, whose rows lie in different banks; their halves of p are
+  // swapped to match
+  uint32_t vc[2][4][D / 64], vs[2][2];
+  const int odd = t & 1;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = r0 + key_of(g) + 8 * h;
-      const uint8_t* c = rec + row * kRowCodes + t * (D / 8);
-      const uint8_t* sc = rec + k_scales_at(D) + row * kRowScales + t * (D / 64);
-      if constexpr (D == 128) {
-        const uint4 v = *reinterpret_cast<const uint4*>(c);
-        kc[h][0] = v.x; kc[h][1] = v.y; kc[h][2] = v.z; kc[h][3] = v.w;
-        const uint32_t two = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sc));
-        ks[h][0] = prmt(two, two, 0x1010u);
-        ks[h][1] = prmt(two, two, 0x3232u);
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(c);
-        kc[h][0] = v.x; kc[h][1] = v.y;
-        const uint32_t one = e4m3x2_to_f16x2(*sc);
-        ks[h][0] = prmt(one, one, 0x1010u);
-      }
-    }
-    float acc[NT][2][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[nt][p][e] = 0.f;
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {  // 8 codes of each key: two steps
-      uint32_t h0[4], h1[4];
-      e2m1x8_to_f16x2(kc[0][w], h0);
-      e2m1x8_to_f16x2(kc[1][w], h1);
-      const uint32_t s0 = ks[0][w / 2], s1 = ks[1][w / 2];
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const uint32_t af[4] = {hmul2(h0[2 * p], s0), hmul2(h1[2 * p], s1),
-                                hmul2(h0[2 * p + 1], s0), hmul2(h1[2 * p + 1], s1)};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma16816(acc[nt][p], af, st.q[nt][4 * w + 2 * p], st.q[nt][4 * w + 2 * p + 1]);
-      }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = (acc[nt][0][e] + acc[nt][1][e]) * a.scale_log2;
-  }
-  // ---- codes and scales of V~ (keys rho = 2t, 2t + 1, 2t + 8, 2t + 9), elements [D/8 g, D/8 (g + 1))
-  uint32_t vc[4][D / 64], vs[2];
-  {
+  for (int i = 0; i < 2; ++i) {
     uint32_t sb[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = r0 + key_of(2 * t + (j & 1)) + 8 * (j >> 1);
+      const int row = r0 + 16 * i + 2 * t + ((j & 1) ^ odd) + 8 * (j >> 1);
       const uint8_t* c = rec + v_codes_at(D) + row * kRowCodes + g * (D / 16);
       if constexpr (D == 128) {
         const uint2 v = *reinterpret_cast<const uint2*>(c);
-        vc[j][0] = v.x; vc[j][1] = v.y;
+        vc[i][j][0] = v.x;
+        vc[i][j][1] = v.y;
       } else {
-        vc[j][0] = *reinterpret_cast<const uint32_t*>(c);
+        vc[i][j][0] = *reinterpret_cast<const uint32_t*>(c);
       }
       sb[j] = rec[v_scales_at(D) + row * kRowScales + g * (D / 8) / 16];
     }
-    if (masked) {
-      // rows that no visible key owns may hold anything, NaN scales among it:
-      // their p is 0, their V~ made 0 too
+    if (td.flags & kMasked) {
+      // rows that no visible key owns may hold anything, NaN scales among it: their p
+      // becomes 0 below, their V~ here
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int key = td.key0 + r0 + key_of(2 * t + (j & 1)) + 8 * (j >> 1);
-        if (!(key < td.len && (key >= td.wstart || key < a.sinks))) sb[j] = 0;
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int key = td.key0 + r0 + key_of(g) + 8 * h;
-        if (!(key < td.len && (key >= td.wstart || key < a.sinks))) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) s[nt][2 * h] = s[nt][2 * h + 1] = -INFINITY;
-        }
-      }
+      for (int j = 0; j < 4; ++j)
+        if (!sees(td, a.sinks, td.key0 + r0 + 16 * i + 2 * t + ((j & 1) ^ odd) + 8 * (j >> 1)))
+          sb[j] = 0;
     }
-    vs[0] = e4m3x2_to_f16x2(sb[0] | (sb[1] << 8));
-    vs[1] = e4m3x2_to_f16x2(sb[2] | (sb[3] << 8));
+    vs[i][0] = e4m3x2_to_f16x2(sb[0] | (sb[1] << 8));
+    vs[i][1] = e4m3x2_to_f16x2(sb[2] | (sb[3] << 8));
   }
-  // ---- running maximum and sum; p as the B operand of the second product
-  uint32_t p0[NT], p1[NT];
+  tmem_wait_ld();
+  // ---- p = 2^(S log2e - m)
+  float mx[NT][2];
+  bool grows = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float mx[2] = {fmaxf(s[nt][0], s[nt][2]), fmaxf(s[nt][1], s[nt][3])};
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xFFFFFFFFu, mx[0], off));
-      mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xFFFFFFFFu, mx[1], off));
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][nt][e] *= a.scale_log2;
+    if (td.flags & kMasked) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (!sees(td, a.sinks, td.key0 + r0 + 16 * i + g + 8 * h))
+            s[i][nt][2 * h] = s[i][nt][2 * h + 1] = -INFINITY;
     }
-    const bool grows = mx[0] > st.m[nt][0] || mx[1] > st.m[nt][1];
-    if (__any_sync(0xFFFFFFFFu, grows)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mx[nt][h] = fmaxf(fmaxf(s[0][nt][h], s[0][nt][2 + h]), fmaxf(s[1][nt][h], s[1][nt][2 + h]));
+      grows |= mx[nt][h] > st.m[nt][h] + kSlack;
+    }
+  }
+  if (__any_sync(0xFFFFFFFFu, grows)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float mn = fmaxf(st.m[nt][h], mx[h]);
-        // both -inf: nothing seen yet, the factor of 0 does not matter
+        float mn = mx[nt][h];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+          mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, off));
+        mn = fmaxf(mn, st.m[nt][h]);
+        // -inf: nothing seen yet, the sums are 0
         const float c = mn > -INFINITY ? ex2_f32(st.m[nt][h] - mn) : 1.f;
         st.m[nt][h] = mn;
         st.l[nt][h] *= c;
@@ -296,35 +281,94 @@ __device__ __forceinline__ void sixteen_keys(const DecodeArgs& a, const uint8_t*
           st.o[nt][i][2 + h] *= c;
         }
       }
-    }
-    float p[4];
+  }
+  uint32_t pb[2][NT][2];
+  const uint32_t swap = odd ? 0x1032u : 0x3210u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = ex2_f32(s[nt][e] - fmaxf(st.m[nt][e & 1], -3.4e38f));
-    st.l[nt][0] += p[0] + p[2];
-    st.l[nt][1] += p[1] + p[3];
-    p0[nt] = movmatrix_trans(pack_f16x2_rn(p[0], p[1]));
-    p1[nt] = movmatrix_trans(pack_f16x2_rn(p[2], p[3]));
+  for (int nt = 0; nt < NT; ++nt) {
+    const float m0 = fmaxf(st.m[nt][0], -3.4e38f), m1 = fmaxf(st.m[nt][1], -3.4e38f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float p0 = ex2_f32(s[i][nt][0] - m0), p1 = ex2_f32(s[i][nt][1] - m1);
+      const float p2 = ex2_f32(s[i][nt][2] - m0), p3 = ex2_f32(s[i][nt][3] - m1);
+      st.l[nt][0] += p0 + p2;
+      st.l[nt][1] += p1 + p3;
+      pb[i][nt][0] = movmatrix_trans(pack_f16x2_rn(p0, p1));
+      pb[i][nt][1] = movmatrix_trans(pack_f16x2_rn(p2, p3));
+      pb[i][nt][0] = prmt(pb[i][nt][0], 0u, swap);
+      pb[i][nt][1] = prmt(pb[i][nt][1], 0u, swap);
+    }
   }
   // ---- O^T += V~^T P^T: codes of two keys interleaved, so that one conversion
-  // gives the pair (key 2t, key 2t + 1) of an element
+  // gives a pair of keys of one element
 #pragma unroll
-  for (int w = 0; w < D / 64; ++w) {
-    uint32_t ev[2][4], od[2][4];  // even and odd elements of the 4 bytes, keys (0, 1) and (2, 3)
+  for (int i = 0; i < 2; ++i) {
 #pragma unroll
-    for (int pr = 0; pr < 2; ++pr) {
-      const uint32_t x = vc[2 * pr][w], y = vc[2 * pr + 1][w];
-      e2m1x8_to_f16x2((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[pr]);
-      e2m1x8_to_f16x2(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[pr]);
-    }
+    for (int w = 0; w < D / 64; ++w) {
+      uint32_t ev[2][4], od[2][4];  // even and odd elements of the 4 bytes, the two pairs of keys
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t af[4] = {hmul2(ev[0][i], vs[0]), hmul2(od[0][i], vs[0]),
-                              hmul2(ev[1][i], vs[1]), hmul2(od[1][i], vs[1])};
+      for (int pr = 0; pr < 2; ++pr) {
+        const uint32_t x = vc[i][2 * pr][w], y = vc[i][2 * pr + 1][w];
+        e2m1x8_to_f16x2((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[pr]);
+        e2m1x8_to_f16x2(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[pr]);
+      }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma16816(st.o[nt][4 * w + i], af, p0[nt], p1[nt]);
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t af[4] = {hmul2(ev[0][e], vs[i][0]), hmul2(od[0][e], vs[i][0]),
+                                hmul2(ev[1][e], vs[i][1]), hmul2(od[1][e], vs[i][1])};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma16816(st.o[nt][4 * w + e], af, pb[i][nt][0], pb[i][nt][1]);
+      }
     }
   }
-  static_assert(kSteps == 4 * (D / 64), "tiles of O^T");
+}
+
+// The MMA warp: q~ of the segment whose first tile holds q at `qraw` -- codes in the
+// swizzled rows of the B operand, scales in the 512-byte blocks of the scale operand.
+template <int D, int NT>
+__device__ __forceinline__ void quantize_q(const uint8_t* qraw, int heads, uint8_t* codes,
+                                           uint8_t* scales, int lane) {
+  constexpr int kBlocks = D / 16;
+#pragma unroll
+  for (int x = lane; x < 8 * NT * kBlocks; x += 32) {
+    const int n = x / kBlocks, j = x % kBlocks;
+    uint2 c = make_uint2(0u, 0u);
+    uint32_t sb = 0;
+    if (n < heads) {
+      const uint4* src = reinterpret_cast<const uint4*>(qraw + n * (D * 2) + j * 32);
+      const uint4 lo = src[0], hi = src[1];
+      const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      const Q16 r = quant16_unit<true>(v);
+      c = make_uint2(r.codes[0], r.codes[1]);
+      sb = r.sbyte;
+    }
+    const int swz = D == 128 ? (n >> 1) & 3 : (n >> 2) & 1;  // 64- and 32-byte swizzles
+    *reinterpret_cast<uint2*>(codes + n * (D / 2) + (((j >> 1) ^ swz) << 4) + (j & 1) * 8) = c;
+    scales[(j >> 2) * 512 + n * 16 + (j & 3)] = static_cast<uint8_t>(sb);
+  }
+}
+
+// K's scales [128][D/16] to D/64 blocks of 512 bytes, in place: row r of a block holds
+// the words (4 scales) of keys r, r + 32, r + 64, r + 96.
+template <int D>
+__device__ __forceinline__ void arrange_scales(uint8_t* sc, int lane) {
+  uint32_t w[D / 64][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (D == 128) {
+      const uint2 v = *reinterpret_cast<const uint2*>(sc + (lane + 32 * i) * 8);
+      w[0][i] = v.x;
+      w[1][i] = v.y;
+    } else {
+      w[0][i] = *reinterpret_cast<const uint32_t*>(sc + (lane + 32 * i) * 4);
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k)
+    *reinterpret_cast<uint4*>(sc + k * 512 + lane * 16) =
+        make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
 }
 
 // Element of O at position `pos` of a stored row: the rows keep the order in which
@@ -335,19 +379,25 @@ __device__ __forceinline__ int element_of(int pos) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) 
+decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
   using C = Cfg<D, NT>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) &
+                                             ~static_cast<uintptr_t>(1023u));
   float* join = reinterpret_cast<float*>(smem + C::kJoin);
   float2* ml = reinterpret_cast<float2*>(smem + C::kMl);
   TileDesc* desc = reinterpret_cast<TileDesc*>(smem + C::kDesc);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);
   uint64_t* empty = full + C::kStages;
-  uint64_t* meet = empty + C::kStages;  // [2]: parts written, parts read
+  uint64_t* scored = empty + C::kStages;  // S of the stage is in tensor memory
+  uint64_t* q_free = scored + C::kStages;  // [2]: the MMAs that read q~ buffer b are done
+  uint64_t* meet = q_free + 2;             // [2]: parts written, parts read
   volatile int* abort = reinterpret_cast<volatile int*>(meet + 2);
-  __shared__ int64_t warp_sum[kWarps + 1];
+  __shared__ int64_t warp_sum[kThreads / 32];
   __shared__ int64_t start_before;
   __shared__ int start_b;
+  __shared__ uint32_t tmem_slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -356,11 +406,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) decode_kernel(co
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kWarps);
+      mbar_init(&scored[s], 1);
     }
+    mbar_init(&q_free[0], 1);
+    mbar_init(&q_free[1], 1);
     mbar_init(&meet[0], kWarps);
     mbar_init(&meet[1], kWarps);
     fence_mbar_init();
   }
+  for (uint32_t i = threadIdx.x; i < 4096 / 16; i += kThreads)  // unused rows of q~ stay 0
+    *reinterpret_cast<uint4*>(smem + C::kQCodes + 16 * i) = make_uint4(0, 0, 0, 0);
   // ---- this CTA's run of the line of tiles: a scan over the sequences
   const int hgs = a.Hkv * a.chunks;
   const int per = (a.B + kThreads - 1) / kThreads;
@@ -380,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) decode_kernel(co
   if (lane == 31) warp_sum[warp] = scan;
   __syncthreads();
   int64_t total = 0;
-  for (int w = 0; w <= kWarps; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) scan += warp_sum[w];
     total += warp_sum[w];
   }
@@ -409,11 +464,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) decode_kernel(co
     start_b = b;
     start_before = before;
   }
+  if (u0 < u1 && warp == kMma) {
+    tmem_alloc(&tmem_slot, C::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
   if (u0 >= u1) return;
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
   const int n_tiles = static_cast<int>(u1 - u0);
 
-  if (warp == kWarps) {
+  if (warp == kProducer) {
     // ------------------------------------------------------------ producer
     int b = start_b;
     bool over;
@@ -458,22 +520,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) decode_kernel(co
       }
       if (lane == 0) desc[s] = td;
       __syncwarp();
-      uint8_t* dst = smem + s * C::kRec;
-      const uint8_t* src =
-          a.pool + (static_cast<int64_t>(page) * a.Hkv + hg / a.chunks) * record_bytes(D);
-      if (!there) {
-        mbar_arrive_expect_tx_w(&full[s], 0);
-      } else if (td.rows == kPage) {
-        mbar_arrive_expect_tx_w(&full[s], C::kRec);
-        bulk_load_w(dst, src, C::kRec, &full[s]);
-      } else {
-        const uint32_t rows = (td.rows + 3) & ~3;  // whole 16-byte units of scales
-        const uint32_t cb = rows * (D / 2), sb = rows * (D / 16);
-        mbar_arrive_expect_tx_w(&full[s], 2 * (cb + sb));
-        bulk_load_w(dst, src, cb, &full[s]);
-        bulk_load_w(dst + v_codes_at(D), src + v_codes_at(D), cb, &full[s]);
-        bulk_load_w(dst + k_scales_at(D), src + k_scales_at(D), sb, &full[s]);
-        bulk_load_w(dst + v_scales_at(D), src + v_scales_at(D), sb, &full[s]);
+      uint8_t* dst = smem + s * C::kStage;
+      const int hk = hg / a.chunks, g0 = hg % a.chunks * C::kHeads;
+      const uint32_t q_bytes =
+          td.flags & kStart ? min(C::kHeads, a.G - g0) * (D * 2) : 0;  // q of the segment
+      const int64_t rec = static_cast<int64_t>(page) * a.Hkv + hk;
+      const uint8_t* src = a.pool + rec * record_bytes(D);
+      const uint32_t boxes = (td.rows + 31) / 32;  // K codes in boxes of 32 keys
+      const uint32_t rows = (td.rows + 3) & ~3;    // whole 16-byte units of scales
+      const uint32_t cb = rows * (D / 2), sb = rows * (D / 16);
+      mbar_arrive_expect_tx_w(&full[s],
+                              q_bytes + (there ? boxes * (16 * D) + cb + 2 * sb : 0));
+      if (q_bytes > 0)
+        bulk_load_w(dst + C::kRec,
+                    a.q + b * a.ld_q + static_cast<int64_t>(hk * a.G + g0) * D, q_bytes, &full[s]);
+      if (there) {
+        for (uint32_t x = 0; x < boxes; ++x)
+          tma_load_4d_w(dst + x * (16 * D), &tk, 0, x * 32, static_cast<int>(rec), 0, &full[s]);
+        if (td.rows == kPage) {
+          bulk_load_w(dst + v_codes_at(D), src + v_codes_at(D), C::kRec - v_codes_at(D), &full[s]);
+        } else {
+          bulk_load_w(dst + v_codes_at(D), src + v_codes_at(D), cb, &full[s]);
+          bulk_load_w(dst + k_scales_at(D), src + k_scales_at(D), sb, &full[s]);
+          bulk_load_w(dst + v_scales_at(D), src + v_scales_at(D), sb, &full[s]);
+        }
       }
       issued = n + 1;
       if (++i == e.tiles && n + 1 < n_tiles) {
@@ -492,6 +562,57 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) decode_kernel(co
       for (int n = max(0, issued - C::kStages); n < issued; ++n)
         mbar_wait_warp(&full[n % C::kStages], (n / C::kStages) & 1, nullptr, 10000000ull);
     }
+  } else if (warp == kMma) {
+    // ----------------------------------------------------------------- MMA
+    constexpr uint32_t idesc = idesc_mxf4nvf4(128, 16);
+    constexpr uint32_t lay = D == 128 ? 4u : 6u, sbo = 4 * D;  // swizzle, bytes of 8 rows
+    int seg = 0;  // segments begun
+    bool ok = true;
+    int n = 0;
+    for (; n < n_tiles; ++n) {
+      const int s = n % C::kStages;
+      if (!(ok = mbar_wait_warp(&full[s], (n / C::kStages) & 1, abort))) break;
+      tc_fence_after();  // the scores that were in this stage's columns have been read
+      const TileDesc td = desc[s];
+      uint8_t* stage = smem + s * C::kStage;
+      if (td.flags & kStart) {
+        const int qb = seg & 1;
+        if (!(ok = mbar_wait_warp(&q_free[qb], ((seg >> 1) & 1) ^ 1, abort))) break;
+        const int g0 = td.hg % a.chunks * C::kHeads;
+        quantize_q<D, NT>(stage + C::kRec, min(C::kHeads, a.G - g0), smem + C::kQCodes + qb * 1024,
+                          smem + C::kQScales + qb * 1024, lane);
+        ++seg;
+      }
+      const int qb = (seg - 1) & 1;
+      if (!(td.flags & kAbsent)) {
+        arrange_scales<D>(stage + k_scales_at(D), lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        const uint32_t sfa = tmem + C::kSfa + s * (D / 16), sfb = tmem + C::kSfb + qb * (D / 16);
+        const uint32_t ka = smem_u32(stage), qa = smem_u32(smem + C::kQCodes + qb * 1024);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {
+          tmem_cp_32x128_x4_w(sfa + 4 * k, smem_u32(stage + k_scales_at(D)) + 512 * k);
+          if (td.flags & kStart)
+            tmem_cp_32x128_x4_w(sfb + 4 * k, smem_u32(smem + C::kQScales + qb * 1024) + 512 * k);
+        }
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+          umma_fp4_ss_w(tmem + 16 * s, sdesc(ka + 32 * k, 16, sbo, lay),
+                        sdesc(qa + 32 * k, 16, sbo, lay), idesc, sfa + 4 * k, sfb + 4 * k, k > 0);
+      } else if (td.flags & kStart) {
+        fence_proxy_async_smem();
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+          tmem_cp_32x128_x4_w(tmem + C::kSfb + qb * (D / 16) + 4 * k,
+                              smem_u32(smem + C::kQScales + qb * 1024) + 512 * k);
+      }
+      umma_commit_w(&scored[s]);
+      if (td.flags & kEnd) umma_commit_w(&q_free[qb]);
+    }
+    for (int m = max(0, n - C::kStages); m < n; ++m)  // the MMAs in flight end before the block
+      mbar_wait_warp(&scored[m % C::kStages], (m / C::kStages) & 1, nullptr, 10000000ull);
   } else {
     // ----------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3;
@@ -500,10 +621,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) decode_kernel(co
     for (int n = 0; n < n_tiles; ++n) {
       const int s = n % C::kStages;
       if (!mbar_wait_warp(&full[s], (n / C::kStages) & 1, abort)) break;
+      if (!mbar_wait_warp(&scored[s], (n / C::kStages) & 1, abort)) break;
+      tc_fence_after();
       const TileDesc td = desc[s];
-      if (td.flags & kStart) start_segment<D, NT>(a, td, st, g, t);
-      if (!(td.flags & kAbsent) && warp * 16 < td.rows)
-        sixteen_keys<D, NT>(a, smem + s * C::kRec, warp * 16, td, td.flags & kMasked, st, g, t);
+      if (td.flags & kStart) st.clear();
+      if (!(td.flags & kAbsent) && warp * 32 < td.rows) {
+        tile_keys<D, NT>(a, smem + s * C::kStage, warp * 32,
+                         tmem + 16 * s + (static_cast<uint32_t>(warp * 32) << 16), td, st, g, t);
+        tc_fence_before();
+      }
       mbar_arrive_warp(&empty[s]);
       if (!(td.flags & kEnd)) continue;
       // ---- the warps' parts meet in shared memory
@@ -564,8 +690,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) decode_kernel(co
       ++meets;
     }
   }
+  tc_fence_before();
   __syncthreads();
   report_abort(abort, a.err);
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols);
+  }
 }
 
 // Joins the parts of one sequence and query head, in run order; writes the empty
@@ -658,19 +789,20 @@ Plan plan(int B, int H, int Hkv, int D, int max_pages) {
   p.nt = G > 8 ? 2 : 1;  // 8 or 16 columns: K~ and V~ are decoded once for both
   p.chunks = (G + 8 * p.nt - 1) / (8 * p.nt);
   const int64_t most = static_cast<int64_t>(B) * Hkv * p.chunks * max_pages;
-  p.runs = static_cast<int>(std::min<int64_t>(most, sm_count() * (p.nt == 1 ? 2 : 1)));
+  p.runs = static_cast<int>(std::min<int64_t>(most, sm_count() * (p.nt == 1 ? 3 : 2)));
   p.parts = (static_cast<size_t>(B + 1) * 8 + 255) / 256 * 256;
   p.total = p.parts + static_cast<size_t>(2 * p.runs) * part_floats(D, 8 * p.nt) * 4;
   return p;
 }
 
 template <int D, int NT>
-cudaError_t launch_decode(const DecodeArgs& a, int runs, cudaStream_t stream) {
+cudaError_t launch_decode(const CUtensorMap& tk, const DecodeArgs& a, int runs,
+                          cudaStream_t stream) {
   using C = Cfg<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  decode_kernel<D, NT><<<runs, kThreads, C::kSmem, stream>>>(a);
+  decode_kernel<D, NT><<<runs, kThreads, C::kSmem, stream>>>(tk, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // the join's blocks come up while the last runs finish
   cudaLaunchAttribute attr[1];
@@ -712,10 +844,14 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
   st = check_kv(pool, num_pages, page_table, ld_table, max_pages, seq_lens);
   if (st != NVQ_OK) return st;
   const Plan p = plan(B, H, Hkv, D, max_pages);
+  if (num_pages > 0x7FFFFFFF / Hkv) return NVQ_ERR_UNSUPPORTED;  // tensor-map coordinates
   if (ws == nullptr || ws_bytes < p.total || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return NVQ_ERR_WORKSPACE;
   int* err = device_error_word();
   if (err == nullptr) return NVQ_ERR_CUDA;
+  CUtensorMap tk;
+  if (const int r = make_kv_codes_map(&tk, pool, num_pages * Hkv, D); r != 0)
+    return fail_driver("cuTensorMapEncodeTiled", r);
   uint8_t* wb = static_cast<uint8_t*>(ws);
   const DecodeArgs a{static_cast<const uint16_t*>(q), ld_q, static_cast<const uint8_t*>(pool),
                      num_pages, page_table, ld_table, max_pages, seq_lens, B, H, Hkv, H / Hkv,
@@ -723,10 +859,10 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
                      reinterpret_cast<int64_t*>(wb), reinterpret_cast<float*>(wb + p.parts), err};
   const cudaError_t e = timed(NVQ_KERNEL_ATTN_FWD, stream, [&] {
     if (D == 128)
-      return p.nt == 1 ? launch_decode<128, 1>(a, p.runs, stream)
-                       : launch_decode<128, 2>(a, p.runs, stream);
-    return p.nt == 1 ? launch_decode<64, 1>(a, p.runs, stream)
-                     : launch_decode<64, 2>(a, p.runs, stream);
+      return p.nt == 1 ? launch_decode<128, 1>(tk, a, p.runs, stream)
+                       : launch_decode<128, 2>(tk, a, p.runs, stream);
+    return p.nt == 1 ? launch_decode<64, 1>(tk, a, p.runs, stream)
+                     : launch_decode<64, 2>(tk, a, p.runs, stream);
   });
   return e == cudaSuccess ? NVQ_OK : fail_cuda("attn decode", e);
 }

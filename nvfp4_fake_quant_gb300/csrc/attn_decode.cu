@@ -63,15 +63,16 @@ template <int D, int NT>
 struct Cfg {
   static constexpr int kHeads = 8 * NT;
   static constexpr int kPerSm = NT == 1 ? 3 : 2;
-  static constexpr int kStages = D == 64 ? 6 : (NT == 1 ? 2 : 3);
+  static constexpr int kStages = D == 64 ? 6 : (NT == 1 ? 3 : 4);
+  static constexpr int kHalf = kHeads / 2;  // heads that the warps join at a time
   static constexpr int kRow = D + 4;  // floats of a head's row in the join area
   static constexpr uint32_t kRec = record_bytes(D);
   static constexpr uint32_t kQ = kHeads * D * 2;         // q of a segment that starts with the tile
   static constexpr uint32_t kStage = kRec + kQ;
   static constexpr uint32_t kQCodes = kStages * kStage;  // [2] q~ codes, 16 rows of D/2 bytes
   static constexpr uint32_t kQScales = kQCodes + 2 * 1024;               // [2][D/64] blocks of 512
-  static constexpr uint32_t kJoin = kQScales + 2 * 1024;                 // float [4][heads][kRow]
-  static constexpr uint32_t kMl = kJoin + kWarps * kHeads * kRow * 4;    // float2 [4][heads]
+  static constexpr uint32_t kJoin = kQScales + 2 * 1024;                 // float [4][kHalf][kRow]
+  static constexpr uint32_t kMl = kJoin + kWarps * kHalf * kRow * 4;     // float2 [4][heads]
   static constexpr uint32_t kDesc = kMl + kWarps * kHeads * 8;           // TileDesc [stages]
   static constexpr uint32_t kBars = kDesc + kStages * 32;
   static constexpr uint32_t kSmem = kBars + (3 * kStages + 4) * 8 + 16 + 1024;  // + alignment
@@ -487,8 +488,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
     bool ok = true;
     int issued = 0;
     for (int n = 0; n < n_tiles; ++n) {
+      // everything about the tile first, then the wait for its stage: the loads go out
+      // as soon as the stage is free
       const int s = n % C::kStages;
-      if (!(ok = mbar_wait_warp(&empty[s], ((n / C::kStages) & 1) ^ 1, abort))) break;
       if (pages_at < 0 || i >= pages_at + 32 || i < pages_at) {
         const int j = i + lane;
         const int p = j < e.sink_pages ? j : e.first + j - e.sink_pages;
@@ -518,8 +520,6 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
         td.flags |= kAbsent;
         if (lane == 0) atomicMax(a.err, kErrTable);
       }
-      if (lane == 0) desc[s] = td;
-      __syncwarp();
       uint8_t* dst = smem + s * C::kStage;
       const int hk = hg / a.chunks, g0 = hg % a.chunks * C::kHeads;
       const uint32_t q_bytes =
@@ -529,6 +529,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
       const uint32_t boxes = (td.rows + 31) / 32;  // K codes in boxes of 32 keys
       const uint32_t rows = (td.rows + 3) & ~3;    // whole 16-byte units of scales
       const uint32_t cb = rows * (D / 2), sb = rows * (D / 16);
+      if (!(ok = mbar_wait_warp(&empty[s], ((n / C::kStages) & 1) ^ 1, abort))) break;
+      if (lane == 0) desc[s] = td;
+      __syncwarp();
       mbar_arrive_expect_tx_w(&full[s],
                               q_bytes + (there ? boxes * (16 * D) + cb + 2 * sb : 0));
       if (q_bytes > 0)
@@ -617,7 +620,6 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
     // ----------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3;
     State<D, NT> st;
-    uint32_t meets = 0;
     for (int n = 0; n < n_tiles; ++n) {
       const int s = n % C::kStages;
       if (!mbar_wait_warp(&full[s], (n / C::kStages) & 1, abort)) break;
@@ -632,62 +634,70 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
       }
       mbar_arrive_warp(&empty[s]);
       if (!(td.flags & kEnd)) continue;
-      // ---- the warps' parts meet in shared memory
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float l = st.l[nt][h];
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
-          const int head = nt * 8 + 2 * t + h;
-          if (g == 0) ml[warp * C::kHeads + head] = make_float2(st.m[nt][h], l);
-          float* row = join + (warp * C::kHeads + head) * C::kRow + 2 * g;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i)
-            *reinterpret_cast<float2*>(row + 16 * i) =
-                make_float2(st.o[nt][i][h], st.o[nt][i][2 + h]);
-        }
-      }
-      mbar_arrive_warp(&meet[0]);
-      if (!mbar_wait_warp(&meet[0], meets & 1, abort)) break;
+      // ---- the warps' parts meet in shared memory, half of the heads at a time
       const int hk = td.hg / a.chunks, g0 = (td.hg % a.chunks) * C::kHeads;
       const int heads = min(C::kHeads, a.G - g0);
-      for (int x = threadIdx.x; x < heads * (D / 2); x += kWarps * 32) {
-        const int head = x / (D / 2), pos = 2 * (x % (D / 2));
-        float mx = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
+      bool met = true;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ml[w * C::kHeads + head].x);
-        const float ref = fmaxf(mx, -3.4e38f);
+      for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 v = ml[w * C::kHeads + head];
-          const float c = ex2_f32(v.x - ref);
-          const float2 ov = *reinterpret_cast<const float2*>(
-              join + (w * C::kHeads + head) * C::kRow + pos);
-          l = fmaf(v.y, c, l);
-          o0 = fmaf(ov.x, c, o0);
-          o1 = fmaf(ov.y, c, o1);
-        }
-        if (td.slot < 0) {
-          const int64_t row = static_cast<int64_t>(td.b) * a.H + hk * a.G + g0 + head;
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          *reinterpret_cast<__nv_bfloat162*>(a.o + row * D + element_of<D>(pos)) =
-              __floats2bfloat162_rn(o0 * inv, o1 * inv);
-          if (pos == 0 && a.lse != nullptr)
-            a.lse[row] = l > 0.f ? (mx + log2f(l)) * kLn2 : -INFINITY;
-        } else {
-          float* part = a.parts + static_cast<int64_t>(td.slot) * part_floats(D, C::kHeads);
-          if (pos == 0) {
-            part[2 * head] = mx;
-            part[2 * head + 1] = l;
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int head = nt * 8 + 2 * t + h;
+            if (half == 0) {
+              float l = st.l[nt][h];
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
+              if (g == 0) ml[warp * C::kHeads + head] = make_float2(st.m[nt][h], l);
+            }
+            if (head / C::kHalf != half) continue;
+            float* row = join + (warp * C::kHalf + head % C::kHalf) * C::kRow + 2 * g;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+              *reinterpret_cast<float2*>(row + 16 * i) =
+                  make_float2(st.o[nt][i][h], st.o[nt][i][2 + h]);
           }
-          *reinterpret_cast<float2*>(part + 2 * C::kHeads + head * D + pos) = make_float2(o0, o1);
         }
+        mbar_arrive_warp(&meet[0]);
+        if (!(met = mbar_wait_warp(&meet[0], half, abort))) break;
+        for (int x = threadIdx.x; x < C::kHalf * (D / 2); x += kWarps * 32) {
+          const int hrow = x / (D / 2), head = half * C::kHalf + hrow, pos = 2 * (x % (D / 2));
+          if (head >= heads) break;
+          float mx = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ml[w * C::kHeads + head].x);
+          const float ref = fmaxf(mx, -3.4e38f);
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float2 v = ml[w * C::kHeads + head];
+            const float c = ex2_f32(v.x - ref);
+            const float2 ov = *reinterpret_cast<const float2*>(
+                join + (w * C::kHalf + hrow) * C::kRow + pos);
+            l = fmaf(v.y, c, l);
+            o0 = fmaf(ov.x, c, o0);
+            o1 = fmaf(ov.y, c, o1);
+          }
+          if (td.slot < 0) {
+            const int64_t row = static_cast<int64_t>(td.b) * a.H + hk * a.G + g0 + head;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            *reinterpret_cast<__nv_bfloat162*>(a.o + row * D + element_of<D>(pos)) =
+                __floats2bfloat162_rn(o0 * inv, o1 * inv);
+            if (pos == 0 && a.lse != nullptr)
+              a.lse[row] = l > 0.f ? (mx + log2f(l)) * kLn2 : -INFINITY;
+          } else {
+            float* part = a.parts + static_cast<int64_t>(td.slot) * part_floats(D, C::kHeads);
+            if (pos == 0) {
+              part[2 * head] = mx;
+              part[2 * head + 1] = l;
+            }
+            *reinterpret_cast<float2*>(part + 2 * C::kHeads + head * D + pos) = make_float2(o0, o1);
+          }
+        }
+        mbar_arrive_warp(&meet[1]);
+        if (!(met = mbar_wait_warp(&meet[1], half, abort))) break;
       }
-      mbar_arrive_warp(&meet[1]);
-      if (!mbar_wait_warp(&meet[1], meets & 1, abort)) break;
-      ++meets;
+      if (!met) break;
     }
   }
   tc_fence_before();

@@ -104,9 +104,14 @@ struct DecodeArgs {
   int window, sinks;
   __nv_bfloat16* o;
   float* lse;
-  int64_t* prefix;  // [B + 1] tiles before each sequence (workspace)
-  float* parts;     // [2 gridDim.x] parts (workspace)
+  struct RunInfo* runs;  // [gridDim.x] (workspace)
+  float* parts;          // [2 gridDim.x] parts (workspace)
   int* err;
+};
+
+// The segment that begins in a run and goes on in later ones; last < 0: none.
+struct RunInfo {
+  int b, hg, slot, last;  // slot of the run's own part, last run of the segment
 };
 
 // Floats of one part: m (log2 units) and l per head, then the sums [heads][D].
@@ -173,6 +178,22 @@ __device__ __forceinline__ void load_scores(uint32_t taddr, float (&v)[NT][4]) {
   for (int i = 0; i < 4 * NT; ++i) v[i / 4][i % 4] = __uint_as_float(r[i]);
 }
 
+// Offsets in a record of what a lane (4 g + t) reads of V: of each 16 keys 2t, 2t + 1,
+// 2t + 8, 2t + 9, elements [D/8 g, D/8 (g + 1)).  Lanes of odd t take the odd key
+// first: keys of both parities in one load, whose rows lie in different banks.
+template <int D>
+struct VOffsets {
+  int codes[2], scales[2];
+  __device__ __forceinline__ VOffsets(int r0, int g, int t) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = r0 + 2 * t + (j ^ (t & 1));
+      codes[j] = v_codes_at(D) + row * (D / 2) + g * (D / 16);
+      scales[j] = v_scales_at(D) + row * (D / 16) + g * (D / 8) / 16;
+    }
+  }
+};
+
 // State of a consumer warp for the current segment.  Lane = 4 g + t.
 template <int D, int NT>
 struct State {
@@ -199,16 +220,12 @@ __device__ __forceinline__ bool sees(const TileDesc& td, int sinks, int key) {
 // Keys r0..r0 + 31 of the record at `rec`, scores at tensor memory address `tm`.
 template <int D, int NT>
 __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* rec, int r0,
-                                          uint32_t tm, const TileDesc& td, State<D, NT>& st, int g,
-                                          int t) {
-  constexpr int kRowCodes = D / 2, kRowScales = D / 16;
+                                          uint32_t tm, const TileDesc& td, const VOffsets<D>& vo,
+                                          State<D, NT>& st, int g, int t) {
   float s[2][NT][4];
   load_scores<NT>(tm, s[0]);
   load_scores<NT>(tm + (16u << 16), s[1]);
-  // ---- codes and scales of V~: of each 16 keys 2t, 2t + 1, 2t + 8, 2t + 9, elements
-  // [D/8 g, D/8 (g + 1)).  Lanes of odd t fetch the odd key first: keys of both
-  // parities in one load, whose rows lie in different banks; their halves of p are
-  // swapped to match
+  // ---- codes and scales of V~
   uint32_t vc[2][4][D / 64], vs[2][2];
   const int odd = t & 1;
 #pragma unroll
@@ -216,8 +233,8 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
     uint32_t sb[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int row = r0 + 16 * i + 2 * t + ((j & 1) ^ odd) + 8 * (j >> 1);
-      const uint8_t* c = rec + v_codes_at(D) + row * kRowCodes + g * (D / 16);
+      const int row = 16 * i + 8 * (j >> 1);  // behind the lane's first
+      const uint8_t* c = rec + vo.codes[j & 1] + row * (D / 2);
       if constexpr (D == 128) {
         const uint2 v = *reinterpret_cast<const uint2*>(c);
         vc[i][j][0] = v.x;
@@ -225,7 +242,7 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
       } else {
         vc[i][j][0] = *reinterpret_cast<const uint32_t*>(c);
       }
-      sb[j] = rec[v_scales_at(D) + row * kRowScales + g * (D / 8) / 16];
+      sb[j] = rec[vo.scales[j & 1] + row * (D / 16)];
     }
     if (td.flags & kMasked) {
       // rows that no visible key owns may hold anything, NaN scales among it: their p
@@ -244,10 +261,6 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
   bool grows = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[i][nt][e] *= a.scale_log2;
     if (td.flags & kMasked) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -259,6 +272,7 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       mx[nt][h] = fmaxf(fmaxf(s[0][nt][h], s[0][nt][2 + h]), fmaxf(s[1][nt][h], s[1][nt][2 + h]));
+      mx[nt][h] *= a.scale_log2;
       grows |= mx[nt][h] > st.m[nt][h] + kSlack;
     }
   }
@@ -290,8 +304,10 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
     const float m0 = fmaxf(st.m[nt][0], -3.4e38f), m1 = fmaxf(st.m[nt][1], -3.4e38f);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float p0 = ex2_f32(s[i][nt][0] - m0), p1 = ex2_f32(s[i][nt][1] - m1);
-      const float p2 = ex2_f32(s[i][nt][2] - m0), p3 = ex2_f32(s[i][nt][3] - m1);
+      const float p0 = ex2_f32(fmaf(s[i][nt][0], a.scale_log2, -m0));
+      const float p1 = ex2_f32(fmaf(s[i][nt][1], a.scale_log2, -m1));
+      const float p2 = ex2_f32(fmaf(s[i][nt][2], a.scale_log2, -m0));
+      const float p3 = ex2_f32(fmaf(s[i][nt][3], a.scale_log2, -m1));
       st.l[nt][0] += p0 + p2;
       st.l[nt][1] += p1 + p3;
       pb[i][nt][0] = movmatrix_trans(pack_f16x2_rn(p0, p1));
@@ -445,14 +461,15 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
   const int runs = runs_of(all, static_cast<int>(gridDim.x)), run = static_cast<int>(blockIdx.x);
   const int64_t u0 = run < runs ? all * run / runs : all;
   const int64_t u1 = run < runs ? all * (run + 1) / runs : all;
-  if (blockIdx.x == 0) {
-    int64_t at = before;
-    for (int b = b_lo; b < b_hi; ++b) {
-      bool over;
-      a.prefix[b] = at;
-      at += extent(a, b, &over).tiles;
-    }
-    if (threadIdx.x == 0) a.prefix[a.B] = total;
+  if (threadIdx.x == 0) a.runs[blockIdx.x].last = -1;
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {  // sequences without visible keys
+    bool over;
+    if (extent(a, b, &over).tiles > 0) continue;
+    const int64_t row0 = static_cast<int64_t>(b) * a.H;
+    for (int x = threadIdx.x; x < a.H * (D / 8); x += kThreads)
+      reinterpret_cast<uint4*>(a.o + row0 * D)[x] = make_uint4(0, 0, 0, 0);
+    if (a.lse != nullptr)
+      for (int x = threadIdx.x; x < a.H; x += kThreads) a.lse[row0 + x] = -INFINITY;
   }
   if (u0 < u1 && before * hgs <= u0 && u0 < (before + mine) * hgs) {
     int b = b_lo;
@@ -515,6 +532,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
       // to the run's slot 0, one that begins inside it to slot 1
       const bool whole = first >= u0 && first + e.tiles <= u1;
       td.slot = whole ? -1 : 2 * run + (first > u0 ? 1 : 0);
+      if (n == n_tiles - 1 && first >= u0 && first + e.tiles > u1 && lane == 0) {
+        // the run that holds tile u: the last c with all c / runs <= u
+        const int64_t u = first + e.tiles - 1;
+        a.runs[run] = {b, hg, td.slot, static_cast<int>(((u + 1) * runs + all - 1) / all - 1)};
+      }
       const bool there = page >= 0 && page < a.num_pages;
       if (!there) {
         td.flags |= kAbsent;
@@ -619,6 +641,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
   } else {
     // ----------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3;
+    const VOffsets<D> vo(warp * 32, g, t);
     State<D, NT> st;
     for (int n = 0; n < n_tiles; ++n) {
       const int s = n % C::kStages;
@@ -629,7 +652,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
       if (td.flags & kStart) st.clear();
       if (!(td.flags & kAbsent) && warp * 32 < td.rows) {
         tile_keys<D, NT>(a, smem + s * C::kStage, warp * 32,
-                         tmem + 16 * s + (static_cast<uint32_t>(warp * 32) << 16), td, st, g, t);
+                         tmem + 16 * s + (static_cast<uint32_t>(warp * 32) << 16), td, vo, st, g, t);
         tc_fence_before();
       }
       mbar_arrive_warp(&empty[s]);
@@ -709,64 +732,68 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
   }
 }
 
-// Joins the parts of one sequence and query head, in run order; writes the empty
-// rows.  Thread x of the first D takes the stored position x; groups of D threads
-// take every kGroups-th part.
+// Joins the parts of the segments that cross runs, in run order.  Block (c, y): the
+// segment that begins in run c and goes on, heads [y, y + 1) kHeads / gridDim.y.
+// Sixteen or 32 lanes of four stored positions take one head; where fewer heads than
+// lane groups are left, the groups share the parts and meet in shared memory.
 template <int D, int NT>
-__global__ void __launch_bounds__(256) join_kernel(const DecodeArgs a, int ctas) {
-  constexpr int kHeads = 8 * NT, kGroups = 256 / D, kFloats = part_floats(D, kHeads);
-  __shared__ float red[kGroups][D + 2];
-  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
-  const int hk = h / a.G, gi = h % a.G, head = gi % kHeads;
-  const int hgs = a.Hkv * a.chunks, hg = hk * a.chunks + gi / kHeads;
+__global__ void __launch_bounds__(256) join_kernel(const DecodeArgs a) {
+  constexpr int kHeads = 8 * NT, kLanes = D / 4, kGroups = 256 / kLanes;
+  constexpr int kFloats = part_floats(D, kHeads);
+  __shared__ float4 red[kGroups][kLanes];
+  __shared__ float2 red_ml[kGroups];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t p0 = a.prefix[b], tiles = a.prefix[b + 1] - p0, all = a.prefix[a.B] * hgs;
-  const int64_t row = static_cast<int64_t>(b) * a.H + h;
-  if (tiles == 0) {
-    if (threadIdx.x < D) a.o[row * D + threadIdx.x] = __float2bfloat16_rn(0.f);
-    if (threadIdx.x == 0 && a.lse != nullptr) a.lse[row] = -INFINITY;
-    return;
+  const RunInfo r = a.runs[blockIdx.x];
+  if (r.last < 0) return;
+  const int per = kHeads / gridDim.y;  // heads of this block
+  const int share = max(1, kGroups / per);
+  const int x = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+  const int g0 = r.hg % a.chunks * kHeads;
+  for (int h0 = 0; h0 < per; h0 += kGroups / share) {
+    const int head = blockIdx.y * per + h0 + grp / share, sub = grp % share;
+    float mx = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = static_cast<int>(blockIdx.x) + sub; c <= r.last; c += share) {
+      const int slot = c == static_cast<int>(blockIdx.x) ? r.slot : 2 * c;
+      const float* part = a.parts + static_cast<int64_t>(slot) * kFloats;
+      const float2 pml = *reinterpret_cast<const float2*>(part + 2 * head);
+      const float4 po = *reinterpret_cast<const float4*>(part + 2 * kHeads + head * D + 4 * x);
+      const float mn = fmaxf(mx, pml.x), ref = fmaxf(mn, -3.4e38f);
+      const float co = ex2_f32(mx - ref), cn = ex2_f32(pml.x - ref);
+      mx = mn;
+      l = l * co + pml.y * cn;
+      o = make_float4(o.x * co + po.x * cn, o.y * co + po.y * cn, o.z * co + po.z * cn,
+                      o.w * co + po.w * cn);
+    }
+    if (share > 1) {
+      red[grp][x] = o;
+      if (x == 0) red_ml[grp] = make_float2(mx, l);
+      __syncthreads();
+      if (sub == 0) {
+        for (int i = 1; i < share; ++i) mx = fmaxf(mx, red_ml[grp + i].x);
+        const float ref = fmaxf(mx, -3.4e38f);
+        l = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < share; ++i) {
+          const float c = ex2_f32(red_ml[grp + i].x - ref);
+          const float4 po = red[grp + i][x];
+          l += red_ml[grp + i].y * c;
+          o = make_float4(o.x + po.x * c, o.y + po.y * c, o.z + po.z * c, o.w + po.w * c);
+        }
+      }
+      __syncthreads();
+    }
+    if (sub == 0 && g0 + head < a.G) {
+      const int64_t row = static_cast<int64_t>(r.b) * a.H + r.hg / a.chunks * a.G + g0 + head;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      __nv_bfloat16* dst = a.o + row * D;
+      *reinterpret_cast<__nv_bfloat162*>(dst + element_of<D>(4 * x)) =
+          __floats2bfloat162_rn(o.x * inv, o.y * inv);
+      *reinterpret_cast<__nv_bfloat162*>(dst + element_of<D>(4 * x + 2)) =
+          __floats2bfloat162_rn(o.z * inv, o.w * inv);
+      if (x == 0 && a.lse != nullptr) a.lse[row] = l > 0.f ? (mx + log2f(l)) * kLn2 : -INFINITY;
+    }
   }
-  const int runs = runs_of(all, ctas);
-  const int64_t s0 = p0 * hgs + hg * tiles, s1 = s0 + tiles;
-  // the run that holds tile u
-  auto run_of = [&](int64_t u) { return static_cast<int>(((u + 1) * runs + all - 1) / all - 1); };
-  const int c0 = run_of(s0), c1 = run_of(s1 - 1);
-  if (c0 == c1) return;  // written by its run
-  const int x = threadIdx.x % D, grp = threadIdx.x / D;
-  float mx = -INFINITY, l = 0.f, o = 0.f;
-  for (int c = c0 + grp; c <= c1; c += kGroups) {
-    const int slot = 2 * c + (c == c0 && all * c / runs < s0 ? 1 : 0);
-    const float* part = a.parts + static_cast<int64_t>(slot) * kFloats;
-    const float pm = part[2 * head], pl = part[2 * head + 1];
-    const float po = part[2 * kHeads + head * D + x];
-    const float mn = fmaxf(mx, pm), ref = fmaxf(mn, -3.4e38f);
-    const float c_old = ex2_f32(mx - ref), c_new = ex2_f32(pm - ref);
-    mx = mn;
-    l = l * c_old + pl * c_new;
-    o = o * c_old + po * c_new;
-  }
-  red[grp][x] = o;
-  if (x == 0) {
-    red[grp][D] = mx;
-    red[grp][D + 1] = l;
-  }
-  __syncthreads();
-  if (grp != 0) return;
-  mx = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kGroups; ++i) mx = fmaxf(mx, red[i][D]);
-  const float ref = fmaxf(mx, -3.4e38f);
-  l = 0.f;
-  o = 0.f;
-#pragma unroll
-  for (int i = 0; i < kGroups; ++i) {
-    const float c = ex2_f32(red[i][D] - ref);
-    l += red[i][D + 1] * c;
-    o += red[i][x] * c;
-  }
-  a.o[row * D + element_of<D>(x)] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
-  if (x == 0 && a.lse != nullptr) a.lse[row] = l > 0.f ? (mx + log2f(l)) * kLn2 : -INFINITY;
 }
 
 int sm_count() {
@@ -786,10 +813,10 @@ nvq_status check_decode(int B, int H, int Hkv, int D, int max_pages) {
   return NVQ_OK;
 }
 
-// Runs (CTAs), query heads per CTA and the workspace: the prefix, then two parts
-// per run.
+// Runs (CTAs), query heads per CTA and the workspace: what goes on from each run,
+// then two parts per run.
 struct Plan {
-  int nt, chunks, runs;
+  int nt, chunks, runs, join_y;
   size_t parts, total;
 };
 
@@ -800,31 +827,33 @@ Plan plan(int B, int H, int Hkv, int D, int max_pages) {
   p.chunks = (G + 8 * p.nt - 1) / (8 * p.nt);
   const int64_t most = static_cast<int64_t>(B) * Hkv * p.chunks * max_pages;
   p.runs = static_cast<int>(std::min<int64_t>(most, sm_count() * (p.nt == 1 ? 3 : 2)));
-  p.parts = (static_cast<size_t>(B + 1) * 8 + 255) / 256 * 256;
+  // few segments: each has many parts, whose heads then get blocks of their own
+  p.join_y = static_cast<int64_t>(B) * Hkv * p.chunks * 8 >= p.runs ? 1 : 8 * p.nt;
+  p.parts = (static_cast<size_t>(p.runs) * sizeof(RunInfo) + 255) / 256 * 256;
   p.total = p.parts + static_cast<size_t>(2 * p.runs) * part_floats(D, 8 * p.nt) * 4;
   return p;
 }
 
 template <int D, int NT>
-cudaError_t launch_decode(const CUtensorMap& tk, const DecodeArgs& a, int runs,
+cudaError_t launch_decode(const CUtensorMap& tk, const DecodeArgs& a, const Plan& p,
                           cudaStream_t stream) {
   using C = Cfg<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  decode_kernel<D, NT><<<runs, kThreads, C::kSmem, stream>>>(tk, a);
+  decode_kernel<D, NT><<<p.runs, kThreads, C::kSmem, stream>>>(tk, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // the join's blocks come up while the last runs finish
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.B * a.H));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.runs), static_cast<unsigned>(p.join_y));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, a, runs);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, a);
 }
 
 }  // namespace
@@ -866,13 +895,13 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
   const DecodeArgs a{static_cast<const uint16_t*>(q), ld_q, static_cast<const uint8_t*>(pool),
                      num_pages, page_table, ld_table, max_pages, seq_lens, B, H, Hkv, H / Hkv,
                      p.chunks, scale * kLog2e, window, sinks, static_cast<__nv_bfloat16*>(o), lse,
-                     reinterpret_cast<int64_t*>(wb), reinterpret_cast<float*>(wb + p.parts), err};
+                     reinterpret_cast<RunInfo*>(wb), reinterpret_cast<float*>(wb + p.parts), err};
   const cudaError_t e = timed(NVQ_KERNEL_ATTN_FWD, stream, [&] {
     if (D == 128)
-      return p.nt == 1 ? launch_decode<128, 1>(tk, a, p.runs, stream)
-                       : launch_decode<128, 2>(tk, a, p.runs, stream);
-    return p.nt == 1 ? launch_decode<64, 1>(tk, a, p.runs, stream)
-                     : launch_decode<64, 2>(tk, a, p.runs, stream);
+      return p.nt == 1 ? launch_decode<128, 1>(tk, a, p, stream)
+                       : launch_decode<128, 2>(tk, a, p, stream);
+    return p.nt == 1 ? launch_decode<64, 1>(tk, a, p, stream)
+                     : launch_decode<64, 2>(tk, a, p, stream);
   });
   return e == cudaSuccess ? NVQ_OK : fail_cuda("attn decode", e);
 }

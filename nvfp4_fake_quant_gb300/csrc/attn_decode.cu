@@ -9,13 +9,14 @@
 //
 // Work split.  The visible pages of every (sequence, KV head, group of query
 // heads) lie one after another on one line of tiles (a tile: one page record, 128
-// keys), and every CTA takes an equal run of that line, whatever the lengths: no
-// CTA waits for the longest sequence.  A run that covers all tiles of a segment
+// keys), which is cut into equal runs, whatever the lengths: nothing waits for the
+// longest sequence.  A run that covers all tiles of a segment
 // (one sequence, KV head and group) writes o itself; a segment that crosses runs
 // leaves (m, l, sum p V~) per run in the workspace, and a second small kernel
 // joins them in run order, so results do not vary from run to run.
 //
-// One CTA, six warps (three CTAs per SM at up to 8 query heads):
+// One run, six warps; three runs (two above 8 query heads) make a CTA, one CTA an SM
+// (as CTAs of their own the second and third of an SM started 2 us and more late):
 //   producer  fetches records into a ring of stages (K codes by tensor-map loads
 //             with the swizzle the MMA reads, the rest by bulk copies; only the
 //             rows that hold tokens) and describes each tile beside it
@@ -52,17 +53,19 @@ namespace nvq {
 
 namespace {
 
-constexpr int kWarps = 4;  // consumer warps, 32 keys of a tile each
+constexpr int kWarps = 4;  // consumer warps of a run, 32 keys of a tile each
 constexpr int kProducer = kWarps, kMma = kWarps + 1;
-constexpr int kThreads = (kWarps + 2) * 32;
+constexpr int kRunWarps = kWarps + 2;
 constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Per shape: query heads per CTA (8 NT), CTAs per SM, ring stages; shared memory.
+// Per shape: query heads per run (8 NT), runs per CTA, ring stages; shared memory and
+// tensor memory of a run.
 template <int D, int NT>
 struct Cfg {
   static constexpr int kHeads = 8 * NT;
-  static constexpr int kPerSm = NT == 1 ? 3 : 2;
+  static constexpr int kRuns = NT == 1 ? 3 : 2;  // per CTA, one CTA per SM
+  static constexpr int kThreads = kRuns * kRunWarps * 32;
   static constexpr int kStages = D == 64 ? 6 : (NT == 1 ? 3 : 4);
   static constexpr int kHalf = kHeads / 2;  // heads that the warps join at a time
   static constexpr int kRow = D + 4;  // floats of a head's row in the join area
@@ -75,10 +78,11 @@ struct Cfg {
   static constexpr uint32_t kMl = kJoin + kWarps * kHalf * kRow * 4;     // float2 [4][heads]
   static constexpr uint32_t kDesc = kMl + kWarps * kHeads * 8;           // TileDesc [stages]
   static constexpr uint32_t kBars = kDesc + kStages * 32;
-  static constexpr uint32_t kSmem = kBars + (3 * kStages + 4) * 8 + 16 + 1024;  // + alignment
+  static constexpr uint32_t kRun = (kBars + (3 * kStages + 4) * 8 + 1023) / 1024 * 1024;
+  static constexpr uint32_t kSmem = kRuns * kRun + 1024;  // + alignment
   // tensor memory columns: S of stage s, scales of K of stage s, of q~ of buffer b
   static constexpr uint32_t kSfa = 16 * kStages, kSfb = kSfa + kStages * (D / 16);
-  static constexpr uint32_t kCols = 128;
+  static constexpr uint32_t kCols = 128, kAlloc = kRuns > 2 ? 512 : 256;
   static_assert(kSfb + 2 * (D / 16) <= kCols, "tensor memory");
   static_assert(kStage % 1024 == 0, "swizzle atoms");
 };
@@ -396,30 +400,35 @@ __device__ __forceinline__ int element_of(int pos) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) 
-decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
   using C = Cfg<D, NT>;
+  constexpr int kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ int64_t warp_sum[kThreads / 32];
+  __shared__ int64_t start_before[C::kRuns];
+  __shared__ int start_b[C::kRuns];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  const int sub = threadIdx.x / (kRunWarps * 32);     // run of the CTA
+  const int tid = threadIdx.x % (kRunWarps * 32);     // thread and warp of the run
+  const int warp = tid >> 5, lane = threadIdx.x & 31;
+  const int quarter = threadIdx.x >> 5 & 3;           // of tensor memory that this warp may read
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) &
-                                             ~static_cast<uintptr_t>(1023u));
+                                             ~static_cast<uintptr_t>(1023u)) + sub * C::kRun;
   float* join = reinterpret_cast<float*>(smem + C::kJoin);
   float2* ml = reinterpret_cast<float2*>(smem + C::kMl);
   TileDesc* desc = reinterpret_cast<TileDesc*>(smem + C::kDesc);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);
   uint64_t* empty = full + C::kStages;
-  uint64_t* scored = empty + C::kStages;  // S of the stage is in tensor memory
+  uint64_t* scored = empty + C::kStages;   // S of the stage is in tensor memory
   uint64_t* q_free = scored + C::kStages;  // [2]: the MMAs that read q~ buffer b are done
   uint64_t* meet = q_free + 2;             // [2]: parts written, parts read
-  volatile int* abort = reinterpret_cast<volatile int*>(meet + 2);
-  __shared__ int64_t warp_sum[kThreads / 32];
-  __shared__ int64_t start_before;
-  __shared__ int start_b;
-  __shared__ uint32_t tmem_slot;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  volatile int* abort = &abort_word;
+  pdl_trigger();
 
-  if (threadIdx.x == 0) {
-    *abort = 0;
+  if (threadIdx.x == 0) *abort = 0;
+  if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kWarps);
@@ -431,9 +440,15 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
     mbar_init(&meet[1], kWarps);
     fence_mbar_init();
   }
-  for (uint32_t i = threadIdx.x; i < 4096 / 16; i += kThreads)  // unused rows of q~ stay 0
+  for (uint32_t i = tid; i < 4096 / 16; i += kRunWarps * 32)  // unused rows of q~ stay 0
     *reinterpret_cast<uint4*>(smem + C::kQCodes + 16 * i) = make_uint4(0, 0, 0, 0);
-  // ---- this CTA's run of the line of tiles: a scan over the sequences
+  if (threadIdx.x < 32) {
+    tmem_alloc(&tmem_slot, C::kAlloc);
+    tmem_relinquish();
+    tma_prefetch_desc(&tk);
+  }
+  pdl_wait();  // before this nothing that another kernel may have written is read
+  // ---- the runs of this CTA: a scan over the sequences
   const int hgs = a.Hkv * a.chunks;
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b_lo = min(a.B, static_cast<int>(threadIdx.x) * per), b_hi = min(a.B, b_lo + per);
@@ -449,56 +464,48 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
     const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, off);
     if (lane >= off) scan += v;
   }
-  if (lane == 31) warp_sum[warp] = scan;
+  if (lane == 31) warp_sum[threadIdx.x >> 5] = scan;
   __syncthreads();
   int64_t total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) scan += warp_sum[w];
+    if (w < static_cast<int>(threadIdx.x >> 5)) scan += warp_sum[w];
     total += warp_sum[w];
   }
-  int64_t before = scan - mine;  // tiles (of one head group) before this thread's sequences
+  const int64_t before = scan - mine;  // tiles (of one head group) before this thread's sequences
   const int64_t all = total * hgs;
-  const int runs = runs_of(all, static_cast<int>(gridDim.x)), run = static_cast<int>(blockIdx.x);
-  const int64_t u0 = run < runs ? all * run / runs : all;
-  const int64_t u1 = run < runs ? all * (run + 1) / runs : all;
-  if (threadIdx.x == 0) a.runs[blockIdx.x].last = -1;
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {  // sequences without visible keys
-    bool over;
-    if (extent(a, b, &over).tiles > 0) continue;
-    const int64_t row0 = static_cast<int64_t>(b) * a.H;
-    for (int x = threadIdx.x; x < a.H * (D / 8); x += kThreads)
-      reinterpret_cast<uint4*>(a.o + row0 * D)[x] = make_uint4(0, 0, 0, 0);
-    if (a.lse != nullptr)
-      for (int x = threadIdx.x; x < a.H; x += kThreads) a.lse[row0 + x] = -INFINITY;
-  }
-  if (u0 < u1 && before * hgs <= u0 && u0 < (before + mine) * hgs) {
-    int b = b_lo;
-    for (;; ++b) {
-      bool over;
-      const int n = extent(a, b, &over).tiles;
-      if (u0 < (before + n) * hgs) break;
-      before += n;
+  const int ctas = static_cast<int>(gridDim.x), runs = runs_of(all, C::kRuns * ctas);
+  // consecutive runs lie on different SMs: a few tiles spread over all of them
+  auto begin_of = [&](int r) { return r < runs ? all * r / runs : all; };
+  for (int i = 0; i < C::kRuns; ++i) {
+    const int64_t u = begin_of(i * ctas + static_cast<int>(blockIdx.x));
+    if (u < all && before * hgs <= u && u < (before + mine) * hgs) {
+      int64_t at = before;
+      int b = b_lo;
+      for (;; ++b) {
+        bool over;
+        const int n = extent(a, b, &over).tiles;
+        if (u < (at + n) * hgs) break;
+        at += n;
+      }
+      start_b[i] = b;
+      start_before[i] = at;
     }
-    start_b = b;
-    start_before = before;
-  }
-  if (u0 < u1 && warp == kMma) {
-    tmem_alloc(&tmem_slot, C::kCols);
-    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
-  if (u0 >= u1) return;
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = tmem_slot + sub * C::kCols;
+  const int run = sub * ctas + static_cast<int>(blockIdx.x);
+  const int64_t u0 = begin_of(run), u1 = begin_of(run + 1);
   const int n_tiles = static_cast<int>(u1 - u0);
+  if (warp == kProducer && lane == 0) a.runs[run].last = -1;
 
-  if (warp == kProducer) {
+  if (warp == kProducer && n_tiles > 0) {
     // ------------------------------------------------------------ producer
-    int b = start_b;
+    int b = start_b[sub];
     bool over;
     Extent e = extent(a, b, &over);
-    int64_t seg0 = start_before * hgs;  // line position of the sequence's first tile
+    int64_t seg0 = start_before[sub] * hgs;  // line position of the sequence's first tile
     int hg = static_cast<int>((u0 - seg0) / e.tiles);
     int i = static_cast<int>((u0 - seg0) - static_cast<int64_t>(hg) * e.tiles);
     int pages = 0, pages_at = -1;  // this lane's page number of the 32 tiles from pages_at
@@ -594,6 +601,17 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
     int seg = 0;  // segments begun
     bool ok = true;
     int n = 0;
+    if (sub == 0) {  // sequences without visible keys, while the first tile is on its way
+      for (int b = blockIdx.x; b < a.B; b += ctas) {
+        bool over;
+        if (extent(a, b, &over).tiles > 0) continue;
+        const int64_t row0 = static_cast<int64_t>(b) * a.H;
+        for (int x = lane; x < a.H * (D / 8); x += 32)
+          reinterpret_cast<uint4*>(a.o + row0 * D)[x] = make_uint4(0, 0, 0, 0);
+        if (a.lse != nullptr)
+          for (int x = lane; x < a.H; x += 32) a.lse[row0 + x] = -INFINITY;
+      }
+    }
     for (; n < n_tiles; ++n) {
       const int s = n % C::kStages;
       if (!(ok = mbar_wait_warp(&full[s], (n / C::kStages) & 1, abort))) break;
@@ -638,10 +656,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
     }
     for (int m = max(0, n - C::kStages); m < n; ++m)  // the MMAs in flight end before the block
       mbar_wait_warp(&scored[m % C::kStages], (m / C::kStages) & 1, nullptr, 10000000ull);
-  } else {
+  } else if (warp < kWarps) {
     // ----------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3;
-    const VOffsets<D> vo(warp * 32, g, t);
+    const int r0 = quarter * 32;  // its keys of a tile
+    const VOffsets<D> vo(r0, g, t);
     State<D, NT> st;
     for (int n = 0; n < n_tiles; ++n) {
       const int s = n % C::kStages;
@@ -650,9 +669,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
       tc_fence_after();
       const TileDesc td = desc[s];
       if (td.flags & kStart) st.clear();
-      if (!(td.flags & kAbsent) && warp * 32 < td.rows) {
-        tile_keys<D, NT>(a, smem + s * C::kStage, warp * 32,
-                         tmem + 16 * s + (static_cast<uint32_t>(warp * 32) << 16), td, vo, st, g, t);
+      if (!(td.flags & kAbsent) && r0 < td.rows) {
+        tile_keys<D, NT>(a, smem + s * C::kStage, r0,
+                         tmem + 16 * s + (static_cast<uint32_t>(r0) << 16), td, vo, st, g, t);
         tc_fence_before();
       }
       mbar_arrive_warp(&empty[s]);
@@ -684,7 +703,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
         }
         mbar_arrive_warp(&meet[0]);
         if (!(met = mbar_wait_warp(&meet[0], half, abort))) break;
-        for (int x = threadIdx.x; x < C::kHalf * (D / 2); x += kWarps * 32) {
+        for (int x = tid; x < C::kHalf * (D / 2); x += kWarps * 32) {
           const int hrow = x / (D / 2), head = half * C::kHalf + hrow, pos = 2 * (x % (D / 2));
           if (head >= heads) break;
           float mx = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
@@ -726,9 +745,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
   tc_fence_before();
   __syncthreads();
   report_abort(abort, a.err);
-  if (warp == kMma) {
+  if (threadIdx.x < 32) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kCols);
+    tmem_dealloc(tmem_slot, C::kAlloc);
   }
 }
 
@@ -742,7 +761,8 @@ __global__ void __launch_bounds__(256) join_kernel(const DecodeArgs a) {
   constexpr int kFloats = part_floats(D, kHeads);
   __shared__ float4 red[kGroups][kLanes];
   __shared__ float2 red_ml[kGroups];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_trigger();
+  pdl_wait();
   const RunInfo r = a.runs[blockIdx.x];
   if (r.last < 0) return;
   const int per = kHeads / gridDim.y;  // heads of this block
@@ -753,17 +773,28 @@ __global__ void __launch_bounds__(256) join_kernel(const DecodeArgs a) {
     const int head = blockIdx.y * per + h0 + grp / share, sub = grp % share;
     float mx = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = static_cast<int>(blockIdx.x) + sub; c <= r.last; c += share) {
-      const int slot = c == static_cast<int>(blockIdx.x) ? r.slot : 2 * c;
-      const float* part = a.parts + static_cast<int64_t>(slot) * kFloats;
-      const float2 pml = *reinterpret_cast<const float2*>(part + 2 * head);
-      const float4 po = *reinterpret_cast<const float4*>(part + 2 * kHeads + head * D + 4 * x);
-      const float mn = fmaxf(mx, pml.x), ref = fmaxf(mn, -3.4e38f);
-      const float co = ex2_f32(mx - ref), cn = ex2_f32(pml.x - ref);
-      mx = mn;
-      l = l * co + pml.y * cn;
-      o = make_float4(o.x * co + po.x * cn, o.y * co + po.y * cn, o.z * co + po.z * cn,
-                      o.w * co + po.w * cn);
+    // eight parts' loads in flight: one after another they cost a memory latency each
+    for (int c0 = static_cast<int>(blockIdx.x) + sub; c0 <= r.last; c0 += 8 * share) {
+      float2 pml[8];
+      float4 po[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = min(c0 + i * share, r.last);
+        const int slot = c == static_cast<int>(blockIdx.x) ? r.slot : 2 * c;
+        const float* part = a.parts + static_cast<int64_t>(slot) * kFloats;
+        pml[i] = *reinterpret_cast<const float2*>(part + 2 * head);
+        po[i] = *reinterpret_cast<const float4*>(part + 2 * kHeads + head * D + 4 * x);
+        if (c0 + i * share > r.last) pml[i] = make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float mn = fmaxf(mx, pml[i].x), ref = fmaxf(mn, -3.4e38f);
+        const float co = ex2_f32(mx - ref), cn = ex2_f32(pml[i].x - ref);
+        mx = mn;
+        l = l * co + pml[i].y * cn;
+        o = make_float4(o.x * co + po[i].x * cn, o.y * co + po[i].y * cn, o.z * co + po[i].z * cn,
+                        o.w * co + po[i].w * cn);
+      }
     }
     if (share > 1) {
       red[grp][x] = o;
@@ -813,10 +844,10 @@ nvq_status check_decode(int B, int H, int Hkv, int D, int max_pages) {
   return NVQ_OK;
 }
 
-// Runs (CTAs), query heads per CTA and the workspace: what goes on from each run,
+// CTAs and runs, query heads per run and the workspace: what goes on from each run,
 // then two parts per run.
 struct Plan {
-  int nt, chunks, runs, join_y;
+  int nt, chunks, ctas, runs, join_y;
   size_t parts, total;
 };
 
@@ -826,7 +857,8 @@ Plan plan(int B, int H, int Hkv, int D, int max_pages) {
   p.nt = G > 8 ? 2 : 1;  // 8 or 16 columns: K~ and V~ are decoded once for both
   p.chunks = (G + 8 * p.nt - 1) / (8 * p.nt);
   const int64_t most = static_cast<int64_t>(B) * Hkv * p.chunks * max_pages;
-  p.runs = static_cast<int>(std::min<int64_t>(most, sm_count() * (p.nt == 1 ? 3 : 2)));
+  p.ctas = static_cast<int>(std::min<int64_t>(most, sm_count()));
+  p.runs = p.ctas * (p.nt == 1 ? 3 : 2);
   // few segments: each has many parts, whose heads then get blocks of their own
   p.join_y = static_cast<int64_t>(B) * Hkv * p.chunks * 8 >= p.runs ? 1 : 8 * p.nt;
   p.parts = (static_cast<size_t>(p.runs) * sizeof(RunInfo) + 255) / 256 * 256;
@@ -841,19 +873,10 @@ cudaError_t launch_decode(const CUtensorMap& tk, const DecodeArgs& a, const Plan
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  decode_kernel<D, NT><<<p.runs, kThreads, C::kSmem, stream>>>(tk, a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // the join's blocks come up while the last runs finish
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.runs), static_cast<unsigned>(p.join_y));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, a);
+  if ((e = launch_pdl(decode_kernel<D, NT>, dim3(p.ctas), dim3(C::kThreads), C::kSmem, stream, tk,
+                      a)) != cudaSuccess)
+    return e;
+  return launch_pdl(join_kernel<D, NT>, dim3(p.runs, p.join_y), dim3(256), 0, stream, a);
 }
 
 }  // namespace

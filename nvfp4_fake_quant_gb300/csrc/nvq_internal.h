@@ -113,6 +113,25 @@ cudaError_t timed(int kind, cudaStream_t stream, F&& launch) {
   return launch();
 }
 
+// Launches `kernel` so that it may come up (set up its shared memory and so on)
+// while the kernel before it on the stream still runs; its pdl_wait() then orders
+// it behind that kernel's completion.
+template <class... P, class... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                       cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Tensor map over packed E2M1 codes [B, N, H, D/2] (bytes), box {D/2, 128, 1, 1},
 // with the (D/2)-byte swizzle; D in {64, 128}.
 int make_bnhd_u8_map(CUtensorMap* map, const void* base, int B, int N, int H, int D);

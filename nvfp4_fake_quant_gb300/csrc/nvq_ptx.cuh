@@ -139,6 +139,18 @@ __device__ __forceinline__ void bulk_load_w(void* smem_dst, const void* src, uin
       : "memory");
 }
 
+// ------------------------------------- programmatic dependent launch (launch_pdl)
+// Lets the kernel launched behind this one on the stream come up as SMs get free.
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// Waits until the kernels before this one on the stream have completed and their
+// writes are visible.  Every kernel started by launch_pdl calls it before it reads
+// or writes anything that they might.
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;

@@ -221,11 +221,12 @@ __device__ __forceinline__ bool sees(const TileDesc& td, int sinks, int key) {
   return key < td.len && (key >= td.wstart || key < sinks);
 }
 
-// Keys r0..r0 + 31 of the record at `rec`, scores at tensor memory address `tm`.
+// Keys r0..r0 + 31 of the record at `rec`, scores at tensor memory address `tm`;
+// arrives on `release` once the stage is read.
 template <int D, int NT>
 __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* rec, int r0,
-                                          uint32_t tm, const TileDesc& td, const VOffsets<D>& vo,
-                                          State<D, NT>& st, int g, int t) {
+                                          uint32_t tm, uint64_t* release, const TileDesc& td,
+                                          const VOffsets<D>& vo, State<D, NT>& st, int g, int t) {
   float s[2][NT][4];
   load_scores<NT>(tm, s[0]);
   load_scores<NT>(tm + (16u << 16), s[1]);
@@ -260,6 +261,11 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
     vs[i][1] = e4m3x2_to_f16x2(sb[2] | (sb[3] << 8));
   }
   tmem_wait_ld();
+  // everything of the stage is in registers: it is refilled under the arithmetic
+  // (held until its end, the loads in flight fell short: 128 against 117 us at 8 x
+  // 131072 tokens)
+  tc_fence_before();
+  mbar_arrive_warp(release);
   // ---- p = 2^(S log2e - m)
   float mx[NT][2];
   bool grows = false;
@@ -671,10 +677,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       if (td.flags & kStart) st.clear();
       if (!(td.flags & kAbsent) && r0 < td.rows) {
         tile_keys<D, NT>(a, smem + s * C::kStage, r0,
-                         tmem + 16 * s + (static_cast<uint32_t>(r0) << 16), td, vo, st, g, t);
-        tc_fence_before();
+                         tmem + 16 * s + (static_cast<uint32_t>(r0) << 16), &empty[s], td, vo, st,
+                         g, t);
+      } else {
+        mbar_arrive_warp(&empty[s]);
       }
-      mbar_arrive_warp(&empty[s]);
       if (!(td.flags & kEnd)) continue;
       // ---- the warps' parts meet in shared memory, half of the heads at a time
       const int hk = td.hg / a.chunks, g0 = (td.hg % a.chunks) * C::kHeads;

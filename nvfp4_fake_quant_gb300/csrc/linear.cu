@@ -45,18 +45,24 @@ LinWs lin_ws(int64_t M, int64_t N, int64_t K) {
   return w;
 }
 
-// Workspace of the packed form: codes, tiled scales and global scale of x, alpha.
+// Workspace of the packed form: few rows (linear_small.cu's at 0) or codes and tiled
+// scales of x and alpha; the global scale of x.
 struct PackedWs {
-  size_t cx, sx, gx, ab, total;
+  size_t cx, sx, ab, gx, total;
+  bool small;
 };
 
-PackedWs packed_ws(int64_t M, int64_t K) {
+PackedWs packed_ws(int64_t M, int64_t N, int64_t K) {
   PackedWs w{};
-  w.cx = 0;
-  w.sx = rup(static_cast<size_t>(M) * static_cast<size_t>(K / 2), 256);
-  w.gx = w.sx + rup(tiled_scale_bytes(M, K), 256);
-  w.ab = w.gx + 256;
-  w.total = w.ab + 256;
+  w.small = linear_small_takes(M, N, K);
+  if (w.small) {
+    w.gx = rup(linear_small_workspace(M, N, K), 256);
+  } else {
+    w.sx = rup(static_cast<size_t>(M) * static_cast<size_t>(K / 2), 256);
+    w.ab = w.sx + rup(tiled_scale_bytes(M, K), 256);
+    w.gx = w.ab + 256;
+  }
+  w.total = w.gx + 256;
   return w;
 }
 
@@ -242,7 +248,7 @@ nvq_status nvfp4_linear_fwd(const void* x, const void* w, const void* bias, int6
 
 size_t nvfp4_linear_packed_workspace(int64_t M, int64_t N, int64_t K) {
   if (check_lin(M, N, K) != NVQ_OK) return 0;
-  return nvq::packed_ws(M, K).total;
+  return nvq::packed_ws(M, N, K).total;
 }
 
 nvq_status nvfp4_linear_packed_fwd(const void* x, int64_t ld_x, const uint8_t* w_codes,
@@ -260,7 +266,7 @@ nvq_status nvfp4_linear_packed_fwd(const void* x, int64_t ld_x, const uint8_t* w
   const float* gsfs[] = {x_global_sf, w_global_sf};
   for (const float* g : gsfs)
     if (g != nullptr && (reinterpret_cast<uintptr_t>(g) & 3u) != 0) return NVQ_ERR_INVALID;
-  const nvq::PackedWs L = nvq::packed_ws(M, K);
+  const nvq::PackedWs L = nvq::packed_ws(M, N, K);
   if (ws == nullptr || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return NVQ_ERR_WORKSPACE;
   uint8_t* wb = static_cast<uint8_t*>(ws);
@@ -272,6 +278,19 @@ nvq_status nvfp4_linear_packed_fwd(const void* x, int64_t ld_x, const uint8_t* w
     e = nvq::timed(NVQ_KERNEL_GLOBAL_SF, stream, [&] { return nvq::launch_global_sf(x, M, K, ld_x, g, stream); });
     if (e != cudaSuccess) return nvq::fail_cuda("global scale", e);
     gx = g;
+  }
+  if (L.small) {
+    int* err = nvq::device_error_word();
+    if (err == nullptr) return NVQ_ERR_CUDA;
+    CUtensorMap tx, tw;
+    int r;
+    if ((r = nvq::make_codes_map(&tx, wb, M, K / 2, static_cast<int>((M + 15) / 16 * 16))) != 0 ||
+        (r = nvq::make_codes_map(&tw, w_codes, N, K / 2)) != 0)
+      return nvq::fail_driver("cuTensorMapEncodeTiled", r);
+    return cuda_st("linear of few rows", nvq::timed(NVQ_KERNEL_LINEAR, stream, [&] {
+                     return nvq::launch_linear_small(x, ld_x, gx, tx, tw, w_scales, w_global_sf, bias,
+                                                     M, N, K, out, wb, err, stream);
+                   }));
   }
   e = nvq::timed(NVQ_KERNEL_QUANTIZE, stream, [&] {
     return nvq::launch_quant_tiled(x, M, K, ld_x, gx, wb + L.cx, wb + L.sx, stream);

@@ -1,0 +1,336 @@
+// The packed NVFP4 linear of a few rows (a decode step's tokens):
+//   out[m, n] = alpha sum_k x~[m, k] w~[n, k] + bias[n],  M <= 64.
+//
+// Bound.  Every weight is read once, 9/16 byte each (codes and scales): the call is
+// a stream of w through the chip.  The weights are the 128-row side of the
+// block-scaled FP4 MMAs (tcgen05 kind::mxf4nvf4) and are never decoded; the rows of
+// x are the narrow side (M rounded up to 16 columns).
+//
+// Work split.  The line of (128-row tile of w, 256-element stage of K) units is cut
+// into equal runs, one CTA each, so that every SM streams the same bytes whatever N
+// and K are.  A tile that lies in one run is written by it.  A tile that crosses
+// runs leaves fp32 parts in the workspace; whichever warp arrives last at the tile's
+// ticket adds the parts in run order (the sum does not depend on who that is).
+//
+// Two launches: x is quantized (and the tickets cleared) by a small kernel, while the
+// main kernel, launched behind it programmatically, already fills its ring with
+// weights, which do not depend on x.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "nvq_internal.h"
+#include "nvq_ptx.cuh"
+#include "nvq_quant.cuh"
+
+namespace nvq {
+
+namespace {
+
+constexpr int kThreads = 192;  // producer, MMA, 4 epilogue warps
+constexpr int kSteps = 4;      // MMA steps (64 elements) per stage
+constexpr int kMaxStages = 9;
+constexpr uint32_t kW = 128 * 128, kSc = kSteps * 512;  // bytes of a stage's w codes; of scales
+constexpr uint32_t kScCol = 128;  // tensor memory: two accumulators of 64 columns, then scales
+static_assert(kScCol + 32 * kMaxStages <= 512, "tensor memory");
+
+struct SmallArgs {
+  int M, N, cols, stages;   // cols: M rounded up to 16; stages of the ring
+  int tiles, k_stages, k_steps, runs;
+  const uint8_t* sx;        // x scales (tiled layout), w scales
+  const uint8_t* sw;
+  const float* gx;          // device scalars; gw nullptr: 1
+  const float* gw;
+  const __nv_bfloat16* bias;
+  __nv_bfloat16* out;
+  unsigned int* tickets;    // [4 tiles], zero at the start
+  float* parts;             // [2 runs][cols][128]
+  int* err;
+};
+
+// x [M, K] to codes and scales in the tiled layout (one row tile; the scales of rows
+// M and up are not written: the products of those rows are never stored), one
+// 16-element block per thread; clears the tickets.
+__global__ void __launch_bounds__(128) quant_rows_kernel(const uint16_t* __restrict__ x, int64_t ld,
+                                                         int M, int nbc,
+                                                         const float* __restrict__ gsf,
+                                                         uint8_t* __restrict__ codes,
+                                                         uint8_t* __restrict__ scales,
+                                                         unsigned int* __restrict__ tickets,
+                                                         int n_tickets) {
+  // the kernels before this one are done when the next one starts: it may read w early
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.x * 128 + threadIdx.x;
+  if (i < n_tickets) tickets[i] = 0;
+  if (i >= M * nbc) return;
+  const int r = i / nbc, cb = i - r * nbc;
+  const float g = *gsf;
+  const uint4* src = reinterpret_cast<const uint4*>(x + r * ld + static_cast<int64_t>(cb) * 16);
+  const uint4 lo = __ldg(src), hi = __ldg(src + 1);
+  const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  Q16 q = quant16_static_fast<false>(v, g, __frcp_rn(g));
+  code_signs(v, q.codes);
+  *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(i) * 8) = make_uint2(q.codes[0], q.codes[1]);
+  scales[(cb >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (cb & 3)] = static_cast<uint8_t>(q.sbyte);
+}
+
+// Run c covers units [units c / runs, units (c + 1) / runs) of the line.
+__device__ __forceinline__ int run_begin(int64_t units, int runs, int c) {
+  return static_cast<int>(units * c / runs);
+}
+// The run that holds unit u: the last c with units c / runs <= u.
+__device__ __forceinline__ int run_of(int64_t units, int runs, int u) {
+  return static_cast<int>((static_cast<int64_t>(u + 1) * runs + units - 1) / units - 1);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_small_kernel(const __grid_constant__ CUtensorMap tx,
+                        const __grid_constant__ CUtensorMap tw, const SmallArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) &
+                                             ~static_cast<uintptr_t>(1023u));
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  volatile int* abort = &abort_word;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t x_bytes = static_cast<uint32_t>(p.cols) * 128;
+  const uint32_t stage_bytes = kW + x_bytes + 2 * kSc;
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    *abort = 0;
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int64_t units = static_cast<int64_t>(p.tiles) * p.k_stages;
+  const int u0 = run_begin(units, p.runs, blockIdx.x), u1 = run_begin(units, p.runs, blockIdx.x + 1);
+  const int count = u1 - u0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    tma_prefetch_desc(&tx);
+    tma_prefetch_desc(&tw);
+    bool ok = true;
+    int issued = 0;
+    auto load_w = [&](int i) {
+      const int u = u0 + i, s = i % p.stages, tile = u / p.k_stages, ks = u - tile * p.k_stages;
+      const int ns = min(kSteps, p.k_steps - ks * kSteps);
+      uint8_t* st = smem + s * stage_bytes;
+      mbar_arrive_expect_tx_w(&full[s], kW + x_bytes + 2 * static_cast<uint32_t>(ns) * 512u);
+      tma_load_4d_w(st, &tw, ks * 128, tile * 128, 0, 0, &full[s]);
+      bulk_load_w(st + kW + x_bytes,
+                  p.sw + (static_cast<int64_t>(tile) * p.k_steps + ks * kSteps) * 512, ns * 512,
+                  &full[s]);
+      issued = i + 1;
+    };
+    auto load_x = [&](int i) {
+      const int u = u0 + i, s = i % p.stages, ks = u % p.k_stages;
+      const int ns = min(kSteps, p.k_steps - ks * kSteps);
+      uint8_t* st = smem + s * stage_bytes;
+      tma_load_4d_w(st + kW, &tx, ks * 128, 0, 0, 0, &full[s]);
+      bulk_load_w(st + kW + x_bytes + kSc, p.sx + static_cast<int64_t>(ks) * kSc, ns * 512, &full[s]);
+    };
+    const int head = min(count, p.stages);
+    for (int i = 0; i < head; ++i) load_w(i);
+    pdl_wait();  // x~
+    for (int i = 0; i < head; ++i) load_x(i);
+    for (int i = head; i < count; ++i) {
+      if (!(ok = mbar_wait_warp(&empty[i % p.stages], ((i / p.stages) & 1) ^ 1, abort))) break;
+      load_w(i);
+      load_x(i);
+    }
+    if (!ok) {  // let the copies already issued land before the block leaves
+      for (int i = max(0, issued - p.stages); i < issued; ++i)
+        mbar_wait_warp(&full[i % p.stages], (i / p.stages) & 1, nullptr, 10000000ull);
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------------- MMA
+    const uint32_t idesc = idesc_mxf4nvf4(128, 0) | (static_cast<uint32_t>(p.cols >> 3) << 17);
+    int part = 0, i = 0;
+    for (; i < count; ++i) {
+      const int u = u0 + i, s = i % p.stages, ks = u % p.k_stages;
+      const int ns = min(kSteps, p.k_steps - ks * kSteps);
+      const bool first = i == 0 || ks == 0;
+      const uint32_t d = tmem + 64 * (part & 1);
+      if (first && !mbar_wait_warp(&acc_empty[part & 1], ((part >> 1) & 1) ^ 1, abort)) break;
+      if (!mbar_wait_warp(&full[s], (i / p.stages) & 1, abort)) break;
+      tc_fence_after();
+      const uint32_t a = smem_u32(smem + s * stage_bytes), b = a + kW, sa = b + x_bytes, sb = sa + kSc;
+      const uint32_t col = tmem + kScCol + 32 * s;
+      for (int j = 0; j < ns; ++j) {
+        tmem_cp_32x128_x4_w(col + 4 * j, sa + 512 * j);
+        tmem_cp_32x128_x4_w(col + 16 + 4 * j, sb + 512 * j);
+        umma_fp4_ss_w(d, sdesc_sw128(a + 32 * j, 16, 1024), sdesc_sw128(b + 32 * j, 16, 1024), idesc,
+                      col + 4 * j, col + 16 + 4 * j, (!first || j > 0) ? 1u : 0u);
+      }
+      umma_commit_w(&empty[s]);
+      if (ks == p.k_stages - 1 || i == count - 1) {
+        umma_commit_w(&acc_full[part & 1]);
+        ++part;
+      }
+    }
+    // the MMAs in flight end before the block does
+    for (int k = max(0, i - p.stages); k < i; ++k)
+      mbar_wait_warp(&empty[k % p.stages], (k / p.stages) & 1, nullptr, 10000000ull);
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    pdl_wait();
+    const float alpha = 1.0f / (*p.gx * (p.gw != nullptr ? *p.gw : 1.0f));
+    int part = 0;
+    for (int u = u0; u < u1; ++part) {
+      const int tile = u / p.k_stages, t0 = tile * p.k_stages;
+      const int from = u;
+      u = min(u1, t0 + p.k_stages);
+      const int n = tile * 128 + row;
+      const bool whole = from == t0 && u == t0 + p.k_stages;
+      const float bias = p.bias != nullptr && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
+      if (!mbar_wait_warp(&acc_full[part & 1], (part >> 1) & 1, abort)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + 64 * (part & 1) + (static_cast<uint32_t>(quarter * 32) << 16);
+      // slot 0 of a run: the part that begins with it; slot 1: one that begins inside
+      float* mine = p.parts +
+                    (static_cast<int64_t>(2 * blockIdx.x + (from > u0 ? 1 : 0)) * p.cols) * 128 + row;
+      for (int c = 0; c < p.M; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(acc + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if (c + j >= p.M) break;
+          const float f = __uint_as_float(v[j]);
+          if (!whole)
+            mine[(c + j) * 128] = f;
+          else if (n < p.N)
+            p.out[static_cast<int64_t>(c + j) * p.N + n] = __float2bfloat16_rn(fmaf(alpha, f, bias));
+        }
+      }
+      tc_fence_before();
+      mbar_arrive_warp(&acc_empty[part & 1]);
+      if (whole) continue;
+      // ---- the last of the tile's parts to arrive adds them up, in run order
+      const int c0 = run_of(units, p.runs, t0), c1 = run_of(units, p.runs, t0 + p.k_stages - 1);
+      __threadfence();
+      __syncwarp();
+      unsigned int before = 0;
+      if (lane == 0) before = atomicAdd(&p.tickets[4 * tile + quarter], 1u);
+      before = __shfl_sync(0xFFFFFFFFu, before, 0);
+      if (before != static_cast<unsigned int>(c1 - c0)) continue;
+      __threadfence();
+      const float* first = p.parts + row +
+          (static_cast<int64_t>(2 * c0 + (run_begin(units, p.runs, c0) < t0 ? 1 : 0)) * p.cols) * 128;
+      for (int m = 0; m < p.M && n < p.N; ++m) {
+        float f = __ldcg(first + m * 128);
+        for (int c = c0 + 1; c <= c1; ++c)
+          f += __ldcg(p.parts + (static_cast<int64_t>(2 * c) * p.cols + m) * 128 + row);
+        p.out[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(fmaf(alpha, f, bias));
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  report_abort(abort, p.err);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+size_t rup(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return 152;
+  return sms;
+}
+
+// Workspace, each region 256-byte aligned.
+struct SmallPlan {
+  int cols, tiles, k_stages, runs;
+  size_t cx, sx, tickets, parts, total;
+};
+
+SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
+  SmallPlan p{};
+  p.cols = static_cast<int>((M + 15) / 16 * 16);
+  p.tiles = static_cast<int>((N + 127) / 128);
+  p.k_stages = static_cast<int>((K + 255) / 256);
+  p.runs = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.tiles) * p.k_stages, sm_count()));
+  p.cx = 0;
+  p.sx = rup(static_cast<size_t>(M) * (K / 2), 256);
+  p.tickets = p.sx + rup(tiled_scale_bytes(M, K), 256);
+  p.parts = p.tickets + rup(static_cast<size_t>(p.tiles) * 16, 256);
+  p.total = p.parts + static_cast<size_t>(2 * p.runs) * p.cols * 128 * 4;
+  return p;
+}
+
+}  // namespace
+
+// N K / 256 units have to fit 31 bits (weights of up to 2^39 elements do).
+bool linear_small_takes(int64_t M, int64_t N, int64_t K) {
+  return M <= kLinearSmallRows && N <= (int64_t{1} << 30) && K <= (int64_t{1} << 30) &&
+         (N + 127) / 128 * ((K + 255) / 256) < (int64_t{1} << 31) / 4 - 1;
+}
+
+size_t linear_small_workspace(int64_t M, int64_t N, int64_t K) { return small_plan(M, N, K).total; }
+
+cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
+                                const CUtensorMap& tx, const CUtensorMap& tw, const uint8_t* sw,
+                                const float* gw, const void* bias, int64_t M, int64_t N, int64_t K,
+                                void* out, uint8_t* ws, int* err, cudaStream_t stream) {
+  const SmallPlan q = small_plan(M, N, K);
+  unsigned int* tickets = reinterpret_cast<unsigned int*>(ws + q.tickets);
+  const int nbc = static_cast<int>(K / 16), blocks = static_cast<int>(M) * nbc;
+  cudaError_t e = launch_pdl(quant_rows_kernel, dim3((std::max(blocks, 4 * q.tiles) + 127) / 128),
+                             dim3(128), 0, stream, static_cast<const uint16_t*>(x), ld_x,
+                             static_cast<int>(M), nbc, gx, ws + q.cx, ws + q.sx, tickets,
+                             4 * q.tiles);
+  if (e != cudaSuccess) return e;
+  const uint32_t stage = kW + q.cols * 128u + 2 * kSc;
+  SmallArgs a{};
+  a.M = static_cast<int>(M);
+  a.N = static_cast<int>(N);
+  a.cols = q.cols;
+  a.stages = std::min<int>(kMaxStages, (220 * 1024) / stage);
+  a.tiles = q.tiles;
+  a.k_stages = q.k_stages;
+  a.k_steps = static_cast<int>(K / 64);
+  a.runs = q.runs;
+  a.sx = ws + q.sx;
+  a.sw = sw;
+  a.gx = gx;
+  a.gw = gw;
+  a.bias = static_cast<const __nv_bfloat16*>(bias);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.tickets = tickets;
+  a.parts = reinterpret_cast<float*>(ws + q.parts);
+  a.err = err;
+  const size_t smem = a.stages * stage + 1024;
+  e = cudaFuncSetAttribute(linear_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           227 * 1024 - 1024);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(linear_small_kernel, dim3(q.runs), dim3(kThreads), smem, stream, tx, tw, a);
+}
+
+}  // namespace nvq

@@ -32,14 +32,16 @@ namespace {
 constexpr int kThreads = 192;  // producer, MMA, 4 epilogue warps
 constexpr int kSteps = 4;      // MMA steps (64 elements) per stage
 constexpr int kMaxStages = 9;
-constexpr uint32_t kW = 128 * 128, kSc = kSteps * 512;  // bytes of a stage's w codes; of scales
+// bytes of a stage: w codes, w scales, x scales
+constexpr uint32_t kW = 128 * 128, kSc = kSteps * 512, kXs = 1024;
 constexpr uint32_t kScCol = 128;  // tensor memory: two accumulators of 64 columns, then scales
 static_assert(kScCol + 32 * kMaxStages <= 512, "tensor memory");
 
 struct SmallArgs {
   int M, N, cols, stages;   // cols: M rounded up to 16; stages of the ring
   int tiles, k_stages, k_steps, runs;
-  const uint8_t* sx;        // x scales (tiled layout), w scales
+  int per_run, rest;        // units / runs, units % runs
+  const uint8_t* sx;        // x scales (stage blocks), w scales (tiled layout)
   const uint8_t* sw;
   const float* gx;          // device scalars; gw nullptr: 1
   const float* gw;
@@ -50,9 +52,13 @@ struct SmallArgs {
   int* err;
 };
 
-// x [M, K] to codes and scales in the tiled layout (one row tile; the scales of rows
-// M and up are not written: the products of those rows are never stored), one
-// 16-element block per thread; clears the tickets.
+// x [M, K] to codes and scales, one 16-element block per thread; clears the tickets.
+// The scales of a stage (4 MMA steps) are two blocks of 512 bytes: row r % 32 of block
+// i holds 4 words (of 4 scales), those of (step 2 i, r / 32 = 0), (2 i, 1), (2 i + 1,
+// 0), (2 i + 1, 1).  One copy of a block then brings the scales of two steps to 4
+// columns of tensor memory, where the tiled layout, made for 128 rows, takes a copy
+// per step.  The scales of rows M and up are not written: the products of those rows
+// are never stored.
 __global__ void __launch_bounds__(128) quant_rows_kernel(const uint16_t* __restrict__ x, int64_t ld,
                                                          int M, int nbc,
                                                          const float* __restrict__ gsf,
@@ -74,16 +80,51 @@ __global__ void __launch_bounds__(128) quant_rows_kernel(const uint16_t* __restr
   Q16 q = quant16_static_fast<false>(v, g, __frcp_rn(g));
   code_signs(v, q.codes);
   *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(i) * 8) = make_uint2(q.codes[0], q.codes[1]);
-  scales[(cb >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (cb & 3)] = static_cast<uint8_t>(q.sbyte);
+  const int step = cb >> 2, w = (step & 1) * 2 + (r >> 5);
+  scales[(step >> 1) * 512 + (r & 31) * 16 + w * 4 + (cb & 3)] = static_cast<uint8_t>(q.sbyte);
 }
 
 // Run c covers units [units c / runs, units (c + 1) / runs) of the line.
-__device__ __forceinline__ int run_begin(int64_t units, int runs, int c) {
-  return static_cast<int>(units * c / runs);
+__device__ __forceinline__ int run_begin(const SmallArgs& p, int c) {
+  return p.per_run * c + p.rest * c / p.runs;
 }
 // The run that holds unit u: the last c with units c / runs <= u.
-__device__ __forceinline__ int run_of(int64_t units, int runs, int u) {
-  return static_cast<int>((static_cast<int64_t>(u + 1) * runs + units - 1) / units - 1);
+__device__ __forceinline__ int run_of(const SmallArgs& p, int u) {
+  const int64_t units = static_cast<int64_t>(p.tiles) * p.k_stages;
+  return static_cast<int>((static_cast<int64_t>(u + 1) * p.runs + units - 1) / units - 1);
+}
+
+// One whole stage from one elected lane: the copies of its scales, four MMAs, the
+// commit.  wd, xd: descriptors of the scale blocks; a, b: of the codes; w_col, x_col:
+// tensor memory columns of the scales (4 a step; 2 a step).
+__device__ __forceinline__ void issue_stage(uint32_t d, uint32_t idesc, uint32_t acc, uint64_t a,
+                                            uint64_t b, uint64_t wd, uint64_t xd, uint32_t w_col,
+                                            uint32_t x_col, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p, e, t;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "setp.eq.u32 t, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%11], %3;\n\t"
+      "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%15], %7;\n\t"
+      "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%17], %8;\n\t"
+      "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%12], %4;\n\t"
+      "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%13], %5;\n\t"
+      "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%14], %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %9, %10, %1, "
+      "[%11], [%15], p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %19, %20, %1, "
+      "[%12], [%16], t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %21, %22, %1, "
+      "[%13], [%17], t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %24, %25, %1, "
+      "[%14], [%18], t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%23];\n\t}" ::"r"(d),
+      "r"(idesc), "r"(acc), "l"(wd), "l"(wd + 32), "l"(wd + 64), "l"(wd + 96), "l"(xd),
+      "l"(xd + 32), "l"(a), "l"(b), "r"(w_col), "r"(w_col + 4), "r"(w_col + 8), "r"(w_col + 12),
+      "r"(x_col), "r"(x_col + 2), "r"(x_col + 4), "r"(x_col + 6), "l"(a + 2), "l"(b + 2), "l"(a + 4), "l"(b + 4), "r"(smem_u32(bar)),
+      "l"(a + 6), "l"(b + 6)
+      : "memory");
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -98,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t x_bytes = static_cast<uint32_t>(p.cols) * 128;
-  const uint32_t stage_bytes = kW + x_bytes + 2 * kSc;
+  const uint32_t stage_bytes = (kW + x_bytes + kSc + kXs + 1023) & ~1023u;
   pdl_trigger();
   if (threadIdx.x == 0) {
     *abort = 0;
@@ -120,8 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const int64_t units = static_cast<int64_t>(p.tiles) * p.k_stages;
-  const int u0 = run_begin(units, p.runs, blockIdx.x), u1 = run_begin(units, p.runs, blockIdx.x + 1);
+  const int u0 = run_begin(p, blockIdx.x), u1 = run_begin(p, blockIdx.x + 1);
   const int count = u1 - u0;
 
   if (warp == 0) {
@@ -134,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int u = u0 + i, s = i % p.stages, tile = u / p.k_stages, ks = u - tile * p.k_stages;
       const int ns = min(kSteps, p.k_steps - ks * kSteps);
       uint8_t* st = smem + s * stage_bytes;
-      mbar_arrive_expect_tx_w(&full[s], kW + x_bytes + 2 * static_cast<uint32_t>(ns) * 512u);
+      mbar_arrive_expect_tx_w(&full[s], kW + x_bytes + kXs + static_cast<uint32_t>(ns) * 512u);
       tma_load_4d_w(st, &tw, ks * 128, tile * 128, 0, 0, &full[s]);
       bulk_load_w(st + kW + x_bytes,
                   p.sw + (static_cast<int64_t>(tile) * p.k_steps + ks * kSteps) * 512, ns * 512,
@@ -142,11 +182,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       issued = i + 1;
     };
     auto load_x = [&](int i) {
-      const int u = u0 + i, s = i % p.stages, ks = u % p.k_stages;
-      const int ns = min(kSteps, p.k_steps - ks * kSteps);
+      const int s = i % p.stages, ks = (u0 + i) % p.k_stages;
       uint8_t* st = smem + s * stage_bytes;
       tma_load_4d_w(st + kW, &tx, ks * 128, 0, 0, 0, &full[s]);
-      bulk_load_w(st + kW + x_bytes + kSc, p.sx + static_cast<int64_t>(ks) * kSc, ns * 512, &full[s]);
+      bulk_load_w(st + kW + x_bytes + kSc, p.sx + static_cast<int64_t>(ks) * kXs, kXs, &full[s]);
     };
     const int head = min(count, p.stages);
     for (int i = 0; i < head; ++i) load_w(i);
@@ -175,13 +214,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t a = smem_u32(smem + s * stage_bytes), b = a + kW, sa = b + x_bytes, sb = sa + kSc;
       const uint32_t col = tmem + kScCol + 32 * s;
-      for (int j = 0; j < ns; ++j) {
-        tmem_cp_32x128_x4_w(col + 4 * j, sa + 512 * j);
-        tmem_cp_32x128_x4_w(col + 16 + 4 * j, sb + 512 * j);
-        umma_fp4_ss_w(d, sdesc_sw128(a + 32 * j, 16, 1024), sdesc_sw128(b + 32 * j, 16, 1024), idesc,
-                      col + 4 * j, col + 16 + 4 * j, (!first || j > 0) ? 1u : 0u);
+      const uint64_t ad = sdesc_sw128(a, 16, 1024), bd = sdesc_sw128(b, 16, 1024);
+      const uint64_t wd = sdesc(sa, 128, 128, 0), xd = sdesc(sb, 128, 128, 0);
+      if (ns == kSteps) {
+        issue_stage(d, idesc, first ? 0u : 1u, ad, bd, wd, xd, col, col + 16, &empty[s]);
+      } else {  // the last stage of a K that is no multiple of 256
+        for (int w = 0; w < 2; ++w) tmem_cp_32x128_x4_w(col + 16 + 4 * w, sb + 512 * w);
+        for (int j = 0; j < ns; ++j) {
+          tmem_cp_32x128_x4_w(col + 4 * j, sa + 512 * j);
+          umma_fp4_ss_w(d, ad + 2 * j, bd + 2 * j, idesc, col + 4 * j, col + 16 + 2 * j,
+                        (!first || j > 0) ? 1u : 0u);
+        }
+        umma_commit_w(&empty[s]);
       }
-      umma_commit_w(&empty[s]);
       if (ks == p.k_stages - 1 || i == count - 1) {
         umma_commit_w(&acc_full[part & 1]);
         ++part;
@@ -227,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_warp(&acc_empty[part & 1]);
       if (whole) continue;
       // ---- the last of the tile's parts to arrive adds them up, in run order
-      const int c0 = run_of(units, p.runs, t0), c1 = run_of(units, p.runs, t0 + p.k_stages - 1);
+      const int c0 = run_of(p, t0), c1 = run_of(p, t0 + p.k_stages - 1);
       __threadfence();
       __syncwarp();
       unsigned int before = 0;
@@ -236,12 +281,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (before != static_cast<unsigned int>(c1 - c0)) continue;
       __threadfence();
       const float* first = p.parts + row +
-          (static_cast<int64_t>(2 * c0 + (run_begin(units, p.runs, c0) < t0 ? 1 : 0)) * p.cols) * 128;
-      for (int m = 0; m < p.M && n < p.N; ++m) {
-        float f = __ldcg(first + m * 128);
-        for (int c = c0 + 1; c <= c1; ++c)
-          f += __ldcg(p.parts + (static_cast<int64_t>(2 * c) * p.cols + m) * 128 + row);
-        p.out[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(fmaf(alpha, f, bias));
+          (static_cast<int64_t>(2 * c0 + (run_begin(p, c0) < t0 ? 1 : 0)) * p.cols) * 128;
+      // 16 rows' loads in flight at a time
+      for (int m0 = 0; m0 < p.M; m0 += 16) {
+        float f[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[j] = __ldcg(first + (m0 + j) * 128);
+        for (int c = c0 + 1; c <= c1; ++c) {
+          const float* more = p.parts + (static_cast<int64_t>(2 * c) * p.cols + m0) * 128 + row;
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __ldcg(more + j * 128);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] += v[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (m0 + j < p.M && n < p.N)
+            p.out[static_cast<int64_t>(m0 + j) * p.N + n] =
+                __float2bfloat16_rn(fmaf(alpha, f[j], bias));
       }
       __syncwarp();
     }
@@ -279,7 +337,7 @@ SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
   p.runs = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.tiles) * p.k_stages, sm_count()));
   p.cx = 0;
   p.sx = rup(static_cast<size_t>(M) * (K / 2), 256);
-  p.tickets = p.sx + rup(tiled_scale_bytes(M, K), 256);
+  p.tickets = p.sx + static_cast<size_t>(p.k_stages) * kXs;
   p.parts = p.tickets + rup(static_cast<size_t>(p.tiles) * 16, 256);
   p.total = p.parts + static_cast<size_t>(2 * p.runs) * p.cols * 128 * 4;
   return p;
@@ -307,7 +365,7 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
                              static_cast<int>(M), nbc, gx, ws + q.cx, ws + q.sx, tickets,
                              4 * q.tiles);
   if (e != cudaSuccess) return e;
-  const uint32_t stage = kW + q.cols * 128u + 2 * kSc;
+  const uint32_t stage = (kW + q.cols * 128u + kSc + kXs + 1023) / 1024 * 1024;
   SmallArgs a{};
   a.M = static_cast<int>(M);
   a.N = static_cast<int>(N);
@@ -317,6 +375,8 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
   a.k_stages = q.k_stages;
   a.k_steps = static_cast<int>(K / 64);
   a.runs = q.runs;
+  a.per_run = static_cast<int>(static_cast<int64_t>(q.tiles) * q.k_stages / q.runs);
+  a.rest = static_cast<int>(static_cast<int64_t>(q.tiles) * q.k_stages % q.runs);
   a.sx = ws + q.sx;
   a.sw = sw;
   a.gx = gx;
@@ -327,8 +387,7 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
   a.parts = reinterpret_cast<float*>(ws + q.parts);
   a.err = err;
   const size_t smem = a.stages * stage + 1024;
-  e = cudaFuncSetAttribute(linear_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           227 * 1024 - 1024);
+  e = cudaFuncSetAttribute(linear_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
   if (e != cudaSuccess) return e;
   return launch_pdl(linear_small_kernel, dim3(q.runs), dim3(kThreads), smem, stream, tx, tw, a);
 }

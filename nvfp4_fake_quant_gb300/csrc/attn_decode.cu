@@ -880,10 +880,10 @@ cudaError_t launch_decode(const CUtensorMap& tk, const DecodeArgs& a, const Plan
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(decode_kernel<D, NT>, dim3(p.ctas), dim3(C::kThreads), C::kSmem, stream, tk,
+  if ((e = launch_pdl(decode_kernel<D, NT>, dim3(p.ctas), dim3(C::kThreads), C::kSmem, stream, 1, tk,
                       a)) != cudaSuccess)
     return e;
-  return launch_pdl(join_kernel<D, NT>, dim3(p.runs, p.join_y), dim3(256), 0, stream, a);
+  return launch_pdl(join_kernel<D, NT>, dim3(p.runs, p.join_y), dim3(256), 0, stream, 1, a);
 }
 
 }  // namespace

@@ -6,11 +6,15 @@
 // block-scaled FP4 MMAs (tcgen05 kind::mxf4nvf4) and are never decoded; the rows of
 // x are the narrow side (M rounded up to 16 columns).
 //
-// Work split.  The line of (128-row tile of w, 256-element stage of K) units is cut
-// into equal runs, one CTA each, so that every SM streams the same bytes whatever N
-// and K are.  A tile that lies in one run is written by it.  A tile that crosses
-// runs leaves fp32 parts in the workspace; whichever warp arrives last at the tile's
-// ticket adds the parts in run order (the sum does not depend on who that is).
+// Work split.  Units are (128-row tile of w, 256-element stage of K).
+//   Up to one tile per SM: 1, 2, 4 or 8 CTAs share a tile, each a range of K, as one
+//   cluster; they leave their sums in the first one's shared memory, which adds them
+//   in order.  (Through the workspace, as below, the same sum costs 3 us more: 7.8
+//   against 4.7 us for 1 x 4608 x 1536.)
+//   More tiles: the line of units is cut into equal runs, one CTA each, so that every
+//   SM streams the same bytes.  A tile that crosses runs leaves fp32 parts in the
+//   workspace; whichever warp arrives last at the tile's ticket adds the parts in run
+//   order (the sum does not depend on who that is).
 //
 // Two launches: x is quantized (and the tickets cleared) by a small kernel, while the
 // main kernel, launched behind it programmatically, already fills its ring with
@@ -35,12 +39,13 @@ constexpr int kMaxStages = 9;
 // bytes of a stage: w codes, w scales, x scales
 constexpr uint32_t kW = 128 * 128, kSc = kSteps * 512, kXs = 1024;
 constexpr uint32_t kScCol = 128;  // tensor memory: two accumulators of 64 columns, then scales
-static_assert(kScCol + 32 * kMaxStages <= 512, "tensor memory");
+static_assert(kScCol + 32 * kMaxStages <= 512 && kScCol + 32 * 4 <= 256, "tensor memory");
 
 struct SmallArgs {
   int M, N, cols, stages;   // cols: M rounded up to 16; stages of the ring
-  int tiles, k_stages, k_steps, runs;
-  int per_run, rest;        // units / runs, units % runs
+  int tiles, k_stages, k_steps;
+  int runs, per_run, rest;  // runs, units / runs, units % runs
+  int split;                // CTAs per tile (clusters)
   const uint8_t* sx;        // x scales (stage blocks), w scales (tiled layout)
   const uint8_t* sw;
   const float* gx;          // device scalars; gw nullptr: 1
@@ -127,19 +132,50 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t idesc, uint32_t
       : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// Wait on a barrier that other CTAs of the cluster arrive on, whose writes into this
+// CTA's shared memory are then visible.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, volatile int* abort) {
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], 0;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar))
+        : "memory");
+    if (__all_sync(0xFFFFFFFFu, ok != 0)) return true;
+    const bool late = globaltimer_ns() - t0 > NVQ_WAIT_LIMIT_NS;
+    if (late) *abort = 1;
+    if (__any_sync(0xFFFFFFFFu, late || *abort)) return false;
+  }
+}
+
+// Address in shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+
+// kClusters: one tile per cluster of p.split CTAs; else runs.
+template <bool kClusters>
+__global__ void __launch_bounds__(kThreads)
     linear_small_kernel(const __grid_constant__ CUtensorMap tx,
                         const __grid_constant__ CUtensorMap tw, const SmallArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) &
                                              ~static_cast<uintptr_t>(1023u));
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+  __shared__ uint64_t sums_full;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   volatile int* abort = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t x_bytes = static_cast<uint32_t>(p.cols) * 128;
   const uint32_t stage_bytes = (kW + x_bytes + kSc + kXs + 1023) & ~1023u;
+  constexpr uint32_t kAlloc = kClusters ? 256 : 512;
   pdl_trigger();
   if (threadIdx.x == 0) {
     *abort = 0;
@@ -151,17 +187,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 4);
     }
+    if (kClusters) mbar_init(&sums_full, 4 * (p.split - 1));
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&tmem_slot, 512);
+    tmem_alloc(&tmem_slot, kAlloc);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
+  if (kClusters && p.split > 1) cluster_arrive();  // waited for before the first remote write
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const int u0 = run_begin(p, blockIdx.x), u1 = run_begin(p, blockIdx.x + 1);
+  int u0, u1;
+  if constexpr (kClusters) {
+    const int tile = blockIdx.x / p.split, rank = blockIdx.x - tile * p.split;
+    u0 = tile * p.k_stages + p.k_stages * rank / p.split;
+    u1 = tile * p.k_stages + p.k_stages * (rank + 1) / p.split;
+  } else {
+    u0 = run_begin(p, blockIdx.x);
+    u1 = run_begin(p, blockIdx.x + 1);
+  }
   const int count = u1 - u0;
 
   if (warp == 0) {
@@ -240,76 +286,126 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, row = quarter * 32 + lane;
     pdl_wait();
     const float alpha = 1.0f / (*p.gx * (p.gw != nullptr ? *p.gw : 1.0f));
-    int part = 0;
-    for (int u = u0; u < u1; ++part) {
-      const int tile = u / p.k_stages, t0 = tile * p.k_stages;
-      const int from = u;
-      u = min(u1, t0 + p.k_stages);
+    if constexpr (kClusters) {
+      const int tile = blockIdx.x / p.split, rank = blockIdx.x - tile * p.split;
       const int n = tile * 128 + row;
-      const bool whole = from == t0 && u == t0 + p.k_stages;
       const float bias = p.bias != nullptr && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
-      if (!mbar_wait_warp(&acc_full[part & 1], (part >> 1) & 1, abort)) break;
+      float* sums = reinterpret_cast<float*>(smem + p.stages * stage_bytes);  // [split - 1][cols][128]
+      if (p.split > 1) cluster_wait();
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+      bool ok = mbar_wait_warp(&acc_full[0], 0, abort);
       tc_fence_after();
-      const uint32_t acc = tmem + 64 * (part & 1) + (static_cast<uint32_t>(quarter * 32) << 16);
-      // slot 0 of a run: the part that begins with it; slot 1: one that begins inside
-      float* mine = p.parts +
-                    (static_cast<int64_t>(2 * blockIdx.x + (from > u0 ? 1 : 0)) * p.cols) * 128 + row;
-      for (int c = 0; c < p.M; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(acc + c, v);
-        tmem_wait_ld();
+      if (rank > 0) {
+        const uint32_t to = map_rank(sums + (rank - 1) * p.cols * 128 + row, 0);
+        for (int c = 0; c < p.M && ok; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(acc + c, v);
+          tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          if (c + j >= p.M) break;
-          const float f = __uint_as_float(v[j]);
-          if (!whole)
-            mine[(c + j) * 128] = f;
-          else if (n < p.N)
-            p.out[static_cast<int64_t>(c + j) * p.N + n] = __float2bfloat16_rn(fmaf(alpha, f, bias));
+          for (int j = 0; j < 16; ++j)
+            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + (c + j) * 512), "r"(v[j])
+                         : "memory");
+        }
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                           map_rank(&sums_full, 0))
+                       : "memory");
+      } else {
+        if (ok && p.split > 1) ok = mbar_wait_cluster(&sums_full, abort);
+        for (int c = 0; c < p.M && ok; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(acc + c, v);
+          tmem_wait_ld();
+          float f[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+          for (int r = 0; r < p.split - 1; ++r)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] += sums[(r * p.cols + c + j) * 128 + row];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < p.M && n < p.N)
+              p.out[static_cast<int64_t>(c + j) * p.N + n] =
+                  __float2bfloat16_rn(fmaf(alpha, f[j], bias));
         }
       }
-      tc_fence_before();
-      mbar_arrive_warp(&acc_empty[part & 1]);
-      if (whole) continue;
-      // ---- the last of the tile's parts to arrive adds them up, in run order
-      const int c0 = run_of(p, t0), c1 = run_of(p, t0 + p.k_stages - 1);
-      __threadfence();
-      __syncwarp();
-      unsigned int before = 0;
-      if (lane == 0) before = atomicAdd(&p.tickets[4 * tile + quarter], 1u);
-      before = __shfl_sync(0xFFFFFFFFu, before, 0);
-      if (before != static_cast<unsigned int>(c1 - c0)) continue;
-      __threadfence();
-      const float* first = p.parts + row +
-          (static_cast<int64_t>(2 * c0 + (run_begin(p, c0) < t0 ? 1 : 0)) * p.cols) * 128;
-      // 16 rows' loads in flight at a time
-      for (int m0 = 0; m0 < p.M; m0 += 16) {
-        float f[16];
+    } else {
+      int part = 0;
+      for (int u = u0; u < u1; ++part) {
+        const int tile = u / p.k_stages, t0 = tile * p.k_stages;
+        const int from = u;
+        u = min(u1, t0 + p.k_stages);
+        const int n = tile * 128 + row;
+        const bool whole = from == t0 && u == t0 + p.k_stages;
+        const float bias = p.bias != nullptr && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
+        if (!mbar_wait_warp(&acc_full[part & 1], (part >> 1) & 1, abort)) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + 64 * (part & 1) + (static_cast<uint32_t>(quarter * 32) << 16);
+        // slot 0 of a run: the part that begins with it; slot 1: one that begins inside
+        float* mine = p.parts +
+                      (static_cast<int64_t>(2 * blockIdx.x + (from > u0 ? 1 : 0)) * p.cols) * 128 + row;
+        for (int c = 0; c < p.M; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(acc + c, v);
+          tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = __ldcg(first + (m0 + j) * 128);
-        for (int c = c0 + 1; c <= c1; ++c) {
-          const float* more = p.parts + (static_cast<int64_t>(2 * c) * p.cols + m0) * 128 + row;
-          float v[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = __ldcg(more + j * 128);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) f[j] += v[j];
+          for (int j = 0; j < 16; ++j) {
+            if (c + j >= p.M) break;
+            const float f = __uint_as_float(v[j]);
+            if (!whole)
+              mine[(c + j) * 128] = f;
+            else if (n < p.N)
+              p.out[static_cast<int64_t>(c + j) * p.N + n] = __float2bfloat16_rn(fmaf(alpha, f, bias));
+          }
         }
+        tc_fence_before();
+        mbar_arrive_warp(&acc_empty[part & 1]);
+        if (whole) continue;
+        // ---- the last of the tile's parts to arrive adds them up, in run order
+        const int c0 = run_of(p, t0), c1 = run_of(p, t0 + p.k_stages - 1);
+        __threadfence();
+        __syncwarp();
+        unsigned int before = 0;
+        if (lane == 0) before = atomicAdd(&p.tickets[4 * tile + quarter], 1u);
+        before = __shfl_sync(0xFFFFFFFFu, before, 0);
+        if (before != static_cast<unsigned int>(c1 - c0)) continue;
+        __threadfence();
+        const float* first = p.parts + row +
+            (static_cast<int64_t>(2 * c0 + (run_begin(p, c0) < t0 ? 1 : 0)) * p.cols) * 128;
+        // 16 rows' loads in flight at a time
+        for (int m0 = 0; m0 < p.M; m0 += 16) {
+          float f[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (m0 + j < p.M && n < p.N)
-            p.out[static_cast<int64_t>(m0 + j) * p.N + n] =
-                __float2bfloat16_rn(fmaf(alpha, f[j], bias));
+          for (int j = 0; j < 16; ++j) f[j] = __ldcg(first + (m0 + j) * 128);
+#pragma unroll 2
+          for (int c = c0 + 1; c <= c1; ++c) {
+            const float* more = p.parts + (static_cast<int64_t>(2 * c) * p.cols + m0) * 128 + row;
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __ldcg(more + j * 128);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] += v[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (m0 + j < p.M && n < p.N)
+              p.out[static_cast<int64_t>(m0 + j) * p.N + n] =
+                  __float2bfloat16_rn(fmaf(alpha, f[j], bias));
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
   }
+  if (kClusters && p.split > 1 && !(warp >= 2)) cluster_wait();
   tc_fence_before();
   __syncthreads();
+  if (kClusters && p.split > 1) cluster_sync_all();  // no CTA leaves while a peer may write into it
   report_abort(abort, p.err);
   if (warp == 1) {
+    __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, kAlloc);
   }
 }
 
@@ -325,7 +421,7 @@ int sm_count() {
 
 // Workspace, each region 256-byte aligned.
 struct SmallPlan {
-  int cols, tiles, k_stages, runs;
+  int cols, tiles, k_stages, split, runs;  // split 0: runs
   size_t cx, sx, tickets, parts, total;
 };
 
@@ -334,12 +430,23 @@ SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
   p.cols = static_cast<int>((M + 15) / 16 * 16);
   p.tiles = static_cast<int>((N + 127) / 128);
   p.k_stages = static_cast<int>((K + 255) / 256);
-  p.runs = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.tiles) * p.k_stages, sm_count()));
+  const int sms = sm_count();
+  if (p.tiles <= sms) {
+    // as many CTAs a tile as there are SMs and stages of K for, at most 24 KB of sums
+    // (56 KB at 8, where few clusters run); 8 only where two per 16 SMs are enough
+    p.split = 1;
+    while (p.split < 8 && 2 * p.split * p.tiles <= sms && 2 * p.split <= p.k_stages &&
+           (2 * p.split - 1) * p.cols <= 16 * 7 && (p.split < 4 || p.tiles <= 16))
+      p.split *= 2;
+    p.runs = p.split * p.tiles;
+  } else {
+    p.runs = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.tiles) * p.k_stages, sms));
+  }
   p.cx = 0;
   p.sx = rup(static_cast<size_t>(M) * (K / 2), 256);
   p.tickets = p.sx + static_cast<size_t>(p.k_stages) * kXs;
-  p.parts = p.tickets + rup(static_cast<size_t>(p.tiles) * 16, 256);
-  p.total = p.parts + static_cast<size_t>(2 * p.runs) * p.cols * 128 * 4;
+  p.parts = p.tickets + (p.split > 0 ? 0 : rup(static_cast<size_t>(p.tiles) * 16, 256));
+  p.total = p.parts + (p.split > 0 ? 0 : static_cast<size_t>(2 * p.runs) * p.cols * 128 * 4);
   return p;
 }
 
@@ -360,10 +467,11 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
   const SmallPlan q = small_plan(M, N, K);
   unsigned int* tickets = reinterpret_cast<unsigned int*>(ws + q.tickets);
   const int nbc = static_cast<int>(K / 16), blocks = static_cast<int>(M) * nbc;
-  cudaError_t e = launch_pdl(quant_rows_kernel, dim3((std::max(blocks, 4 * q.tiles) + 127) / 128),
-                             dim3(128), 0, stream, static_cast<const uint16_t*>(x), ld_x,
+  const int n_tickets = q.split == 0 ? 4 * q.tiles : 0;
+  cudaError_t e = launch_pdl(quant_rows_kernel, dim3((std::max(blocks, n_tickets) + 127) / 128),
+                             dim3(128), 0, stream, 1, static_cast<const uint16_t*>(x), ld_x,
                              static_cast<int>(M), nbc, gx, ws + q.cx, ws + q.sx, tickets,
-                             4 * q.tiles);
+                             n_tickets);
   if (e != cudaSuccess) return e;
   const uint32_t stage = (kW + q.cols * 128u + kSc + kXs + 1023) / 1024 * 1024;
   SmallArgs a{};
@@ -371,6 +479,7 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
   a.N = static_cast<int>(N);
   a.cols = q.cols;
   a.stages = std::min<int>(kMaxStages, (220 * 1024) / stage);
+  a.split = q.split;
   a.tiles = q.tiles;
   a.k_stages = q.k_stages;
   a.k_steps = static_cast<int>(K / 64);
@@ -386,10 +495,22 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
   a.tickets = tickets;
   a.parts = reinterpret_cast<float*>(ws + q.parts);
   a.err = err;
-  const size_t smem = a.stages * stage + 1024;
-  e = cudaFuncSetAttribute(linear_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+  size_t smem = a.stages * stage + 1024;
+  if (q.split == 0) {
+    e = cudaFuncSetAttribute(linear_small_kernel<false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(linear_small_kernel<false>, dim3(q.runs), dim3(kThreads), smem, stream, 1, tx, tw, a);
+  }
+  // at most four stages: two CTAs fit an SM, so that clusters of four find room in
+  // every group of SMs
+  a.stages = std::min(4, (q.k_stages + q.split - 1) / q.split);
+  smem = a.stages * stage + (q.split - 1) * q.cols * 512 + 1024;
+  e = cudaFuncSetAttribute(linear_small_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           226 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_pdl(linear_small_kernel, dim3(q.runs), dim3(kThreads), smem, stream, tx, tw, a);
+  return launch_pdl(linear_small_kernel<true>, dim3(q.runs), dim3(kThreads), smem, stream, q.split,
+                    tx, tw, a);
 }
 
 }  // namespace nvq

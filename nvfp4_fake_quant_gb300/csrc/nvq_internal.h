@@ -115,11 +115,15 @@ cudaError_t timed(int kind, cudaStream_t stream, F&& launch) {
 
 // Launches `kernel` so that it may come up (set up its shared memory and so on)
 // while the kernel before it on the stream still runs; its pdl_wait() then orders
-// it behind that kernel's completion.
+// it behind that kernel's completion.  cluster > 1: CTAs per cluster (along x).
 template <class... P, class... A>
 cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t stream, const A&... args) {
-  cudaLaunchAttribute attr[1];
+                       cudaStream_t stream, int cluster, const A&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
@@ -128,7 +132,7 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

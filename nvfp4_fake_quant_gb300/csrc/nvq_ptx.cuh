@@ -175,6 +175,14 @@ __device__ __forceinline__ void cluster_sync_all() {
                    : "memory");
 }
 
+// The two halves of cluster_sync_all.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // 4-D tiled load written to the same shared-memory offset in every CTA of
 // `mask` (cluster ranks), each completing `bytes` of tx on the mbarrier at
 // bar's offset in that CTA.  Warp-collective (one elected lane issues).

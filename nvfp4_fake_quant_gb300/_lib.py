@@ -150,7 +150,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 
 def call(name: str, *args) -> int:
     """Call an entry point returning nvq_status; raise NvqError unless NVQ_OK."""
-    lib = load()
+    lib = _lib or load()
     st = getattr(lib, name)(*args)
     if st != 0:
         detail = lib.nvq_last_error_detail().decode() if st == 4 else ""

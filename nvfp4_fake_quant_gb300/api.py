@@ -12,6 +12,7 @@ softmax_scale None meaning 1/sqrt(D).
 """
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
@@ -344,42 +345,60 @@ class NVFP4Linear(torch.nn.Module):
 
 
 # ------------------------------------------------- single tokens: shared helpers
+#
+# These calls take microseconds on the device, so their checks are written for the
+# valid call: one pass over plain attributes, with the explanation left to the path
+# that raises.
 
-def _same_device(*tensors):
-    """The common device of the tensors (None entries left out)."""
-    dev = None
-    for t in tensors:
-        if t is not None:
-            if dev is not None and t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device}: one device expected")
-            dev = t.device
-    return dev
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _call_on(device, name, *args):
-    """The entry point, with the stream of ``device`` as its last argument and that
-    device current (the library works on the current device)."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        _lib.call(name, *args, stream)
+def _launch(index: int, name: str, *args) -> None:
+    """The entry point on the current stream of device ``index``, with that device
+    current (the library works on the current device)."""
+    if index == torch.cuda.current_device():
+        _lib.call(name, *args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            _lib.call(name, *args, stream)
+        with torch.cuda.device(index):
+            _lib.call(name, *args, _raw_stream(index))
+
+
+def _on(index: int, name: str, *args) -> int:
+    """A size query with device ``index`` current (sizes follow its SM count)."""
+    f = getattr(_lib.load(), name)
+    if index == torch.cuda.current_device():
+        return int(f(*args))
+    with torch.cuda.device(index):
+        return int(f(*args))
+
+
+def _device_of(first, *others) -> int:
+    """The device index that all tensors (None entries left out) share."""
+    index = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device expected")
+    return index
 
 
 def _rows_nd(x: torch.Tensor, name: str):
     """(rows, heads, D, row stride) of a bf16 [rows, heads, D] tensor whose rows are
     contiguous inside."""
-    _check(x, name)
-    if x.dim() != 3 or (x.numel() > 0 and ((x.shape[2] > 1 and x.stride(2) != 1) or
-                                           (x.shape[1] > 1 and x.stride(1) != x.shape[2]))):
-        raise ValueError(f"{name} must be [tokens, heads, D] with contiguous heads")
-    t, h, d = x.shape
-    return t, h, d, (x.stride(0) if t > 1 else max(h * d, x.stride(0)))
+    if not (isinstance(x, torch.Tensor) and x.dtype is BF16 and x.is_cuda):
+        _check(x, name)
+    if x.dim() == 3:
+        t, h, d = x.shape
+        row, s1, s2 = x.stride()
+        if (s2 == 1 or d == 1) and (s1 == d or h == 1) or t * h * d == 0:
+            return t, h, d, row if t > 1 else max(h * d, row)
+    raise ValueError(f"{name} must be [tokens, heads, D] with contiguous heads")
 
 
 def _check_i32(t, name, dim):
-    _check(t, name, torch.int32)
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cuda):
+        _check(t, name, torch.int32)
     if t.dim() != dim or (t.numel() > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name} must be a {dim}-dimensional int32 tensor with unit last stride")
 
@@ -387,10 +406,10 @@ def _check_i32(t, name, dim):
 def _check_out(t, name, shape, dtype, like):
     """An output to write: the caller's, checked, or a new contiguous one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     _check(t, name, dtype)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {shape}")
     return t
 
 
@@ -407,23 +426,38 @@ def nvfp4_linear_packed_fwd(x, w_codes, w_scales, w_global_sf=None, bias=None, x
     [M, K], rows may be strided; ``x_global_sf`` None: 448*6/amax(x)."""
     _check(x, "x")
     m, k, ld = _rows_ld(x)
-    _check(w_codes, "w_codes", torch.uint8)
-    _check(w_scales, "w_scales", torch.uint8)
+    for t, name in ((w_codes, "w_codes"), (w_scales, "w_scales")):
+        if not (isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and t.is_cuda
+                and t.is_contiguous()):
+            _check(t, name, torch.uint8)
+            raise ValueError(f"{name} must be contiguous")
+    if w_codes.dim() != 2 or w_codes.shape[1] * 2 != k:
+        raise ValueError(f"w_codes must be [N, {k // 2}], got {tuple(w_codes.shape)}")
     n = w_codes.shape[0]
-    if w_codes.dim() != 2 or w_codes.shape[1] * 2 != k or not w_codes.is_contiguous():
-        raise ValueError(f"w_codes must be contiguous [N, {k // 2}], got {tuple(w_codes.shape)}")
-    if not w_scales.is_contiguous() or w_scales.numel() != nvfp4_tiled_scale_bytes(n, k):
+    # the 128x4 tiles of nvfp4_tiled_scale_bytes (k % 16 != 0 is refused below)
+    if w_scales.numel() != -(-n // 128) * -(-(k // 16) // 4) * 512:
         raise ValueError("w_scales must be the tiled scales of w_codes")
     if bias is not None:
         _check(bias, "bias")
-        if tuple(bias.shape) != (n,) or not bias.is_contiguous():
+        if bias.dim() != 1 or bias.shape[0] != n or not bias.is_contiguous():
             raise ValueError(f"bias must be contiguous [{n}]")
-    dev = _same_device(x, w_codes, w_scales, w_global_sf, bias, x_global_sf, out, workspace)
+    index = _device_of(x, w_codes, w_scales, w_global_sf, bias, x_global_sf, out, workspace)
     out = _check_out(out, "out", (m, n), BF16, x)
-    ws = _workspace(nvfp4_linear_packed_workspace(m, n, k), dev, workspace)
-    _call_on(dev, "nvfp4_linear_packed_fwd", _ptr(x), ld if m > 1 else max(ld, k), _ptr(w_codes),
-             _ptr(w_scales), _opt_ptr(w_global_sf), _ptr(bias), m, n, k, _opt_ptr(x_global_sf),
-             _ptr(out), _ptr(ws), ws.numel() * ws.element_size())
+    ws = workspace
+    if ws is None:
+        ws = _workspace(_on(index, "nvfp4_linear_packed_workspace", m, n, k), x.device, None)
+    args = (x.data_ptr(), ld if m > 1 else max(ld, k), w_codes.data_ptr(), w_scales.data_ptr(),
+            _opt_ptr(w_global_sf), None if bias is None else bias.data_ptr(), m, n, k,
+            _opt_ptr(x_global_sf), out.data_ptr())
+    try:
+        _launch(index, "nvfp4_linear_packed_fwd", *args, ws.data_ptr(),
+                ws.numel() * ws.element_size())
+    except _lib.NvqError as e:
+        if e.status != 3 or workspace is None:
+            raise
+        # the caller's workspace is too small (or misaligned): one of our own, as elsewhere
+        ws = _workspace(_on(index, "nvfp4_linear_packed_workspace", m, n, k), x.device, None)
+        _launch(index, "nvfp4_linear_packed_fwd", *args, ws.data_ptr(), ws.numel())
     return out
 
 
@@ -484,6 +518,12 @@ def rope_inv_freq(rot_dim: int, theta: float = 10000.0, scaling: str | None = No
     return f.to(device), mscale
 
 
+@functools.lru_cache(maxsize=256)
+def _host_ints(values: tuple):
+    """A C array of the ints (read by the entry point before it returns)."""
+    return (_lib.c_int * len(values))(*values)
+
+
 def rope_apply(q, k, positions, inv_freq, interleaved=False, axis_pairs=None, mscale=1.0,
                inverse=False, q_out=None, k_out=None):
     """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (bf16, token rows may be
@@ -491,34 +531,44 @@ def rope_apply(q, k, positions, inv_freq, interleaved=False, axis_pairs=None, ms
     [T, axes]; ``axis_pairs`` the number of pairs that turn by each axis (default:
     all by the first); ``inv_freq`` f64 [rot_dim/2].  q_out / k_out may be q / k."""
     t, hq, d, ld_q = _rows_nd(q, "q")
-    _check(inv_freq, "inv_freq", torch.float64)
-    if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dtype is torch.float64
+            and inv_freq.is_cuda and inv_freq.dim() == 1 and inv_freq.is_contiguous()):
+        _check(inv_freq, "inv_freq", torch.float64)
         raise ValueError("inv_freq must be a contiguous vector")
-    rot = 2 * inv_freq.numel()
-    pos = positions.unsqueeze(1) if positions.dim() == 1 else positions
-    _check(pos, "positions", torch.int32)
-    axes = pos.shape[1] if pos.dim() == 2 else 0
-    if pos.dim() != 2 or pos.shape[0] != t or not pos.is_contiguous():
+    rot = 2 * inv_freq.shape[0]
+    if not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32
+            and positions.is_cuda):
+        _check(positions, "positions", torch.int32)
+    axes = 1 if positions.dim() == 1 else positions.shape[1] if positions.dim() == 2 else 0
+    if axes == 0 or positions.shape[0] != t or not positions.is_contiguous():
         raise ValueError(f"positions must be contiguous [{t}] or [{t}, axes]")
     pairs = (rot // 2,) + (0,) * (axes - 1) if axis_pairs is None else tuple(axis_pairs)
-    if len(pairs) != axes or not 1 <= axes <= 3:
+    if len(pairs) != axes or axes > 3:
         raise ValueError(f"axis_pairs must give one count for each of 1..3 axes, got {pairs}")
-    outs = [torch.empty((t, hq, d), dtype=BF16, device=q.device) if q_out is None else q_out, None]
-    t2, h2, d2, ld_qo = _rows_nd(outs[0], "q_out")
-    hk, ld_k, ld_ko = 0, 0, 0
-    if k is not None:
+    if q_out is None:
+        q_out, ld_qo = q.new_empty((t, hq, d)), hq * d
+    else:
+        *shape, ld_qo = _rows_nd(q_out, "q_out")
+        if shape != [t, hq, d]:
+            raise ValueError(f"q_out must be {(t, hq, d)}, got {tuple(shape)}")
+    hk = ld_k = ld_ko = 0
+    if k is None:
+        k_out = None
+    else:
         tk, hk, dk, ld_k = _rows_nd(k, "k")
-        outs[1] = torch.empty((t, hk, d), dtype=BF16, device=q.device) if k_out is None else k_out
-        t3, h3, d3, ld_ko = _rows_nd(outs[1], "k_out")
-        if (tk, dk) != (t, d) or (t3, h3, d3) != (t, hk, d):
-            raise ValueError(f"k and k_out must be [{t}, heads, {d}]")
-    if (t2, h2, d2) != (t, hq, d):
-        raise ValueError(f"q_out must be {(t, hq, d)}, got {(t2, h2, d2)}")
-    dev = _same_device(q, k, pos, inv_freq, *outs)
-    _call_on(dev, "rope_apply", _ptr(q), ld_q, _ptr(outs[0]), ld_qo, hq, _ptr(k), ld_k,
-             _ptr(outs[1]), ld_ko, hk, t, d, rot, int(bool(interleaved)), _ptr(pos), axes,
-             (_lib.c_int * axes)(*pairs), _ptr(inv_freq), float(mscale), int(bool(inverse)))
-    return outs[0], outs[1]
+        if tk != t or dk != d:
+            raise ValueError(f"k must be [{t}, heads, {d}], got {tuple(k.shape)}")
+        if k_out is None:
+            k_out, ld_ko = k.new_empty((t, hk, d)), hk * d
+        else:
+            *shape, ld_ko = _rows_nd(k_out, "k_out")
+            if shape != [t, hk, d]:
+                raise ValueError(f"k_out must be {(t, hk, d)}, got {tuple(shape)}")
+    index = _device_of(q, k, positions, inv_freq, q_out, k_out)
+    _launch(index, "rope_apply", q.data_ptr(), ld_q, q_out.data_ptr(), ld_qo, hq, _ptr(k), ld_k,
+            _ptr(k_out), ld_ko, hk, t, d, rot, int(bool(interleaved)), positions.data_ptr(), axes,
+            _host_ints(pairs), inv_freq.data_ptr(), float(mscale), int(bool(inverse)))
+    return q_out, k_out
 
 
 class RotaryFunction(torch.autograd.Function):
@@ -582,16 +632,16 @@ def nvfp4_kv_pool(num_pages: int, hkv: int, d: int, device="cuda") -> torch.Tens
 
 
 def _check_cache(pool, page_table, seq_lens, d):
-    _check(pool, "pool", torch.uint8)
-    if pool.dim() != 3 or not pool.is_contiguous() or pool.shape[2] != 144 * d:
+    if not (isinstance(pool, torch.Tensor) and pool.dtype is torch.uint8 and pool.is_cuda
+            and pool.dim() == 3 and pool.shape[2] == 144 * d and pool.is_contiguous()):
+        _check(pool, "pool", torch.uint8)
         raise ValueError(f"pool must be contiguous uint8 [pages, Hkv, {144 * d}], "
                          f"got {tuple(pool.shape)}")
     _check_i32(page_table, "page_table", 2)
     _check_i32(seq_lens, "seq_lens", 1)
-    if page_table.shape[0] != seq_lens.shape[0]:
-        raise ValueError(f"page_table has {page_table.shape[0]} rows, seq_lens "
-                         f"{seq_lens.shape[0]}")
     b, max_pages = page_table.shape
+    if seq_lens.shape[0] != b:
+        raise ValueError(f"page_table has {b} rows, seq_lens {seq_lens.shape[0]}")
     return b, max_pages, (page_table.stride(0) if b > 1 else max_pages)
 
 
@@ -613,9 +663,10 @@ def nvfp4_kv_append(k, v, seq_lens, page_table, pool, cu_tokens=None) -> None:
     elif t != b:
         raise ValueError(f"without cu_tokens one token per sequence is expected: {t} tokens, "
                          f"{b} sequences")
-    dev = _same_device(k, v, seq_lens, page_table, pool, cu_tokens)
-    _call_on(dev, "nvfp4_kv_append", _ptr(k), ld_k, _ptr(v), ld_v, t, b, hkv, d, _ptr(cu_tokens),
-             _ptr(seq_lens), _ptr(page_table), ld_t, max_pages, _ptr(pool), pool.shape[0])
+    index = _device_of(k, v, seq_lens, page_table, pool, cu_tokens)
+    _launch(index, "nvfp4_kv_append", k.data_ptr(), ld_k, v.data_ptr(), ld_v, t, b, hkv, d,
+            _ptr(cu_tokens), seq_lens.data_ptr(), page_table.data_ptr(), ld_t, max_pages,
+            pool.data_ptr(), pool.shape[0])
 
 
 def attn_qat_decode_workspace(b, h, hkv, d, max_pages) -> int:
@@ -635,16 +686,23 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
     scale = _scale(scale, d)
     o = _check_out(o, "o", (b, h, d), BF16, q)
     lse = _check_out(lse, "lse", (b, h), torch.float32, q)
-    dev = _same_device(q, pool, page_table, seq_lens, o, lse, workspace)
-    if dev.index == torch.cuda.current_device():
-        need = attn_qat_decode_workspace(b, h, hkv, d, max_pages)
-    else:
-        with torch.cuda.device(dev):  # the size follows from the device's SM count
-            need = attn_qat_decode_workspace(b, h, hkv, d, max_pages)
-    ws = _workspace(need, dev, workspace)
-    _call_on(dev, "attn_qat_decode", _ptr(q), ld_q, _ptr(pool), pool.shape[0], _ptr(page_table),
-             ld_t, max_pages, _ptr(seq_lens), b, h, hkv, d, scale, int(window), int(sinks),
-             _ptr(o), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size())
+    index = _device_of(q, pool, page_table, seq_lens, o, lse, workspace)
+    ws = workspace
+    if ws is None:
+        ws = _workspace(_on(index, "attn_qat_decode_workspace", b, h, hkv, d, max_pages),
+                        q.device, None)
+    args = (q.data_ptr(), ld_q, pool.data_ptr(), pool.shape[0], page_table.data_ptr(), ld_t,
+            max_pages, seq_lens.data_ptr(), b, h, hkv, d, scale, int(window), int(sinks),
+            o.data_ptr(), lse.data_ptr())
+    try:
+        _launch(index, "attn_qat_decode", *args, ws.data_ptr(), ws.numel() * ws.element_size())
+    except _lib.NvqError as e:
+        if e.status != 3 or workspace is None:
+            raise
+        # the caller's workspace is too small (or misaligned): one of our own, as elsewhere
+        ws = _workspace(_on(index, "attn_qat_decode_workspace", b, h, hkv, d, max_pages),
+                        q.device, None)
+        _launch(index, "attn_qat_decode", *args, ws.data_ptr(), ws.numel())
     return o, lse
 
 

@@ -406,7 +406,7 @@ def _check_i32(t, name, dim):
 def _check_out(t, name, shape, dtype, like):
     """An output to write: the caller's, checked, or a new contiguous one."""
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     _check(t, name, dtype)
     if tuple(t.shape) != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, of shape {shape}")
@@ -546,7 +546,7 @@ def rope_apply(q, k, positions, inv_freq, interleaved=False, axis_pairs=None, ms
     if len(pairs) != axes or axes > 3:
         raise ValueError(f"axis_pairs must give one count for each of 1..3 axes, got {pairs}")
     if q_out is None:
-        q_out, ld_qo = q.new_empty((t, hq, d)), hq * d
+        q_out, ld_qo = torch.empty((t, hq, d), dtype=BF16, device=q.device), hq * d
     else:
         *shape, ld_qo = _rows_nd(q_out, "q_out")
         if shape != [t, hq, d]:
@@ -559,7 +559,7 @@ def rope_apply(q, k, positions, inv_freq, interleaved=False, axis_pairs=None, ms
         if tk != t or dk != d:
             raise ValueError(f"k must be [{t}, heads, {d}], got {tuple(k.shape)}")
         if k_out is None:
-            k_out, ld_ko = k.new_empty((t, hk, d)), hk * d
+            k_out, ld_ko = torch.empty((t, hk, d), dtype=BF16, device=q.device), hk * d
         else:
             *shape, ld_ko = _rows_nd(k_out, "k_out")
             if shape != [t, hk, d]:

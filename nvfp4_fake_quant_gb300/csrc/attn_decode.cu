@@ -366,7 +366,7 @@ __device__ __forceinline__ void quantize_q(const uint8_t* qraw, int heads, uint8
       const uint4* src = reinterpret_cast<const uint4*>(qraw + n * (D * 2) + j * 32);
       const uint4 lo = src[0], hi = src[1];
       const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-      const Q16 r = quant16_unit<true>(v);
+      const Codes16 r = codes16_unit(v);
       c = make_uint2(r.codes[0], r.codes[1]);
       sb = r.sbyte;
     }
@@ -834,14 +834,6 @@ __global__ void __launch_bounds__(256) join_kernel(const DecodeArgs a) {
   }
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return 152;
-  return sms;
-}
-
 nvq_status check_decode(int B, int H, int Hkv, int D, int max_pages) {
   if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || max_pages < 1 ||
       max_pages > 0x7FFFFFFF / kPage)
@@ -864,7 +856,7 @@ Plan plan(int B, int H, int Hkv, int D, int max_pages) {
   p.nt = G > 8 ? 2 : 1;  // 8 or 16 columns: K~ and V~ are decoded once for both
   p.chunks = (G + 8 * p.nt - 1) / (8 * p.nt);
   const int64_t most = static_cast<int64_t>(B) * Hkv * p.chunks * max_pages;
-  p.ctas = static_cast<int>(std::min<int64_t>(most, sm_count()));
+  p.ctas = static_cast<int>(std::min<int64_t>(most, device_sms()));
   p.runs = p.ctas * (p.nt == 1 ? 3 : 2);
   // few segments: each has many parts, whose heads then get blocks of their own
   p.join_y = static_cast<int64_t>(B) * Hkv * p.chunks * 8 >= p.runs ? 1 : 8 * p.nt;

@@ -18,6 +18,7 @@
 
 #include "nvq_internal.h"
 #include "nvq_kv.cuh"
+#include "nvq_ptx.cuh"
 #include "nvq_quant.cuh"
 
 namespace nvq {
@@ -82,6 +83,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
   __shared__ uint8_t* page[kTokens];
   __shared__ int row[kTokens];
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
+  pdl_trigger();
+  pdl_wait();
   if (threadIdx.x < kTokens) {
     const int64_t t = t0 + threadIdx.x;
     page[threadIdx.x] = t < a.T ? find_row(a, t, D, &row[threadIdx.x]) : nullptr;
@@ -100,8 +103,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
     const uint4* s4 = reinterpret_cast<const uint4*>(src + h * D + cb * 16);
     const uint4 lo = __ldg(s4), hi = __ldg(s4 + 1);
     const uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    Q16 q = quant16_unit<true>(x);
-    code_signs(x, q.codes);
+    const Codes16 q = codes16_unit(x);
     uint8_t* rec = base + static_cast<int64_t>(h) * record_bytes(D);
     *reinterpret_cast<uint2*>(rec + (is_v ? v_codes_at(D) : 0) + r * (D / 2) + cb * 8) =
         make_uint2(q.codes[0], q.codes[1]);
@@ -147,15 +149,12 @@ nvq_status nvfp4_kv_append(const void* k, int64_t ld_k, const void* v, int64_t l
                      static_cast<uint8_t*>(pool), num_pages, err};
   // a few tokens: spread their heads over the SMs
   const int rows = kThreads / (D / 16 * kTokens);
-  const int64_t want = std::max<int64_t>(1, (2 * 152 + groups - 1) / groups);
+  const int64_t want = std::max<int64_t>(1, (2 * device_sms() + groups - 1) / groups);
   const int y = static_cast<int>(std::min<int64_t>(want, (2 * Hkv + rows - 1) / rows));
   const cudaError_t e = timed(NVQ_KERNEL_QUANTIZE, stream, [&] {
     const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(y));
-    if (D == 128)
-      kv_append_kernel<128><<<grid, kThreads, 0, stream>>>(a);
-    else
-      kv_append_kernel<64><<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(D == 128 ? kv_append_kernel<128> : kv_append_kernel<64>, grid, dim3(kThreads),
+                      0, stream, 1, a);
   });
   return e == cudaSuccess ? NVQ_OK : fail_cuda("kv append", e);
 }

@@ -411,14 +411,6 @@ __global__ void __launch_bounds__(kThreads)
 
 size_t rup(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
-    return 152;
-  return sms;
-}
-
 // Workspace, each region 256-byte aligned.
 struct SmallPlan {
   int cols, tiles, k_stages, split, runs;  // split 0: runs
@@ -430,7 +422,7 @@ SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
   p.cols = static_cast<int>((M + 15) / 16 * 16);
   p.tiles = static_cast<int>((N + 127) / 128);
   p.k_stages = static_cast<int>((K + 255) / 256);
-  const int sms = sm_count();
+  const int sms = device_sms();
   if (p.tiles <= sms) {
     // as many CTAs a tile as there are SMs and stages of K for, at most 24 KB of sums
     // (56 KB at 8, where few clusters run); 8 only where two per 16 SMs are enough

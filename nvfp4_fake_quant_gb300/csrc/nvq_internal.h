@@ -113,6 +113,15 @@ cudaError_t timed(int kind, cudaStream_t stream, F&& launch) {
   return launch();
 }
 
+// Multiprocessors of the current device (152 where there is none to ask).
+inline int device_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+    return 152;
+  return sms;
+}
+
 // Launches `kernel` so that it may come up (set up its shared memory and so on)
 // while the kernel before it on the stream still runs; its pdl_wait() then orders
 // it behind that kernel's completion.  cluster > 1: CTAs per cluster (along x).

@@ -19,6 +19,7 @@
 #include <cuda_runtime.h>
 
 #include "nvq_internal.h"
+#include "nvq_ptx.cuh"
 
 namespace nvq {
 
@@ -26,7 +27,7 @@ namespace {
 
 constexpr int kMaxD = 256;
 constexpr int kMaxTokens = 16;  // tokens per block
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kPerSm = 4;  // blocks per SM
 
 struct RopeTensor {
   const __nv_bfloat16* in;
@@ -57,82 +58,114 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// A block takes a.tokens consecutive tokens, all heads.  The work item of a
-// thread is 16 bytes of a head (interleaved: 4 whole pairs) or, in the half
-// layout, the two 16-byte vectors that hold 8 pairs; the unrotated tail of a
-// head is copied in 16-byte items.
+// Plain load that leaves no line in L1 (q_out may be q: not a read-only load).
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// Blocks take groups of a.tokens consecutive tokens, all heads, in turn (one wave of
+// blocks: F is formed once each).  The work item of a thread is 16 bytes of a head
+// (interleaved: 4 whole pairs) or, in the half layout, the two 16-byte vectors that
+// hold 8 pairs; the unrotated tail of a head is copied in 16-byte items.  A thread
+// keeps its item of the head and walks over the group's (token, head) rows, four rows'
+// loads in flight.
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSm) rope_kernel(const RopeArgs a) {
   constexpr int kPairs = kInterleaved ? 4 : 8;  // pairs per item
+  constexpr int kUnroll = 4;
   __shared__ uint64_t turns[kMaxD / 2];
   // cos and sin of (token, pair p = kPairs u + e) at float4 (e / 2) * units + u of
   // the token's part: the float4 loads of a warp, whose lanes take consecutive
   // items u, touch consecutive addresses
   __shared__ float4 cs4[kMaxTokens * kMaxD / 4];
+  pdl_trigger();
   const int pairs = a.rot / 2, units = pairs / kPairs;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
-  const int tokens = static_cast<int>(a.T - t0 < a.tokens ? a.T - t0 : a.tokens);
+  const int per_head = units + (a.D - a.rot) / 8;      // items of a head
+  const int rows_at_once = kThreads / per_head;        // rows of a pass
+  const int row0 = threadIdx.x / per_head, u = threadIdx.x - row0 * per_head;
+  const int first = u < units ? 8 * u : a.rot + (u - units) * 8;  // element of the head
+  pdl_wait();
   for (int p = threadIdx.x; p < pairs; p += kThreads) {
     double f = a.inv_freq[p] * 0.15915494309189533577;  // 1 / (2 pi)
     f -= rint(f);
     turns[p] = static_cast<uint64_t>(__double2ll_rn(f * 18446744073709551616.0));  // 2^64
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
-    const int tok = i / pairs, p = i - tok * pairs;
-    const int axis = p < a.end0 ? 0 : (p < a.end1 ? 1 : 2);
-    const int64_t pos = a.positions[(t0 + tok) * a.axes + axis];
-    const uint64_t u = static_cast<uint64_t>(pos) * turns[p] + 0x80000000u;
-    const float half_turns = static_cast<float>(static_cast<int32_t>(u >> 32)) * 0x1p-31f;
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    float2* at = reinterpret_cast<float2*>(cs4 + tok * (pairs / 2));
-    at[((p % kPairs) / 2 * units + p / kPairs) * 2 + (p & 1)] =
-        make_float2(c * a.mscale, s * (a.mscale * a.sign));
-  }
-  __syncthreads();
-  const int tail = (a.D - a.rot) / 8;  // 16-byte items copied behind the rotated ones
-  const int per_head = units + tail, per_token = per_head * a.heads;
-  for (int i = threadIdx.x; i < tokens * per_token; i += kThreads) {
-    const int tok = i / per_token, r = i - tok * per_token;
-    const int h = r / per_head, u = r - h * per_head;
-    const bool is_q = h < a.Hq;
-    const RopeTensor& x = is_q ? a.q : a.k;
-    const int hh = is_q ? h : h - a.Hq;
-    const __nv_bfloat16* src = x.in + (t0 + tok) * x.ld_in + hh * a.D;
-    __nv_bfloat16* dst = x.out + (t0 + tok) * x.ld_out + hh * a.D;
-    if (u >= units) {
-      const int d = a.rot + (u - units) * 8;
-      *reinterpret_cast<uint4*>(dst + d) = *reinterpret_cast<const uint4*>(src + d);
-      continue;
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens; t0 < a.T;
+       t0 += static_cast<int64_t>(gridDim.x) * a.tokens) {
+    const int tokens = static_cast<int>(a.T - t0 < a.tokens ? a.T - t0 : a.tokens);
+    __syncthreads();  // turns are there; the last group's cs4 has been read
+    for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+      const int tok = i / pairs, p = i - tok * pairs;
+      const int axis = p < a.end0 ? 0 : (p < a.end1 ? 1 : 2);
+      const int64_t pos = a.positions[(t0 + tok) * a.axes + axis];
+      const uint64_t turn = static_cast<uint64_t>(pos) * turns[p] + 0x80000000u;
+      const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+      float s, c;
+      sincospif(half_turns, &s, &c);
+      float2* at = reinterpret_cast<float2*>(cs4 + tok * (pairs / 2));
+      at[((p % kPairs) / 2 * units + p / kPairs) * 2 + (p & 1)] =
+          make_float2(c * a.mscale, s * (a.mscale * a.sign));
     }
-    const float4* cs = cs4 + tok * (pairs / 2) + u;
-    if constexpr (kInterleaved) {
-      const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * u);
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    __syncthreads();
+    if (row0 >= rows_at_once) continue;  // threads left over
+    const int rows = tokens * a.heads;
+    int tok = row0 / a.heads, h = row0 - tok * a.heads;
+    for (int r = row0; r < rows; r += kUnroll * rows_at_once) {
+      uint4 v1[kUnroll], v2[kUnroll];
+      __nv_bfloat16* dst[kUnroll];
+      const float4* cs[kUnroll];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float4 c = cs[e * units];
-        const float2 y0 = turn(lo_f32(w[2 * e]), hi_f32(w[2 * e]), c.x, c.y);
-        const float2 y1 = turn(lo_f32(w[2 * e + 1]), hi_f32(w[2 * e + 1]), c.z, c.w);
-        w[2 * e] = pack(y0.x, y0.y);
-        w[2 * e + 1] = pack(y1.x, y1.y);
+      for (int i = 0; i < kUnroll; ++i) {
+        if (r + i * rows_at_once < rows) {
+          const bool is_q = h < a.Hq;
+          const RopeTensor& x = is_q ? a.q : a.k;
+          const int at = (is_q ? h : h - a.Hq) * a.D + first;
+          const __nv_bfloat16* src = x.in + (t0 + tok) * x.ld_in + at;
+          dst[i] = x.out + (t0 + tok) * x.ld_out + at;
+          cs[i] = cs4 + tok * (pairs / 2) + u;
+          v1[i] = ld16(src);
+          if (!kInterleaved && u < units) v2[i] = ld16(src + pairs);
+        }
+        h += rows_at_once;
+        while (h >= a.heads) {
+          h -= a.heads;
+          ++tok;
+        }
       }
-      *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      const uint4 v1 = *reinterpret_cast<const uint4*>(src + 8 * u);
-      const uint4 v2 = *reinterpret_cast<const uint4*>(src + pairs + 8 * u);
-      uint32_t w1[4] = {v1.x, v1.y, v1.z, v1.w}, w2[4] = {v2.x, v2.y, v2.z, v2.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 c = cs[e * units];
-        const float2 y0 = turn(lo_f32(w1[e]), lo_f32(w2[e]), c.x, c.y);
-        const float2 y1 = turn(hi_f32(w1[e]), hi_f32(w2[e]), c.z, c.w);
-        w1[e] = pack(y0.x, y1.x);
-        w2[e] = pack(y0.y, y1.y);
+      for (int i = 0; i < kUnroll; ++i) {
+        if (r + i * rows_at_once >= rows) break;
+        if (u < units) {
+          uint32_t w1[4] = {v1[i].x, v1[i].y, v1[i].z, v1[i].w};
+          if constexpr (kInterleaved) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float4 c = cs[i][e * units];
+              const float2 y0 = turn(lo_f32(w1[2 * e]), hi_f32(w1[2 * e]), c.x, c.y);
+              const float2 y1 = turn(lo_f32(w1[2 * e + 1]), hi_f32(w1[2 * e + 1]), c.z, c.w);
+              w1[2 * e] = pack(y0.x, y0.y);
+              w1[2 * e + 1] = pack(y1.x, y1.y);
+            }
+          } else {
+            uint32_t w2[4] = {v2[i].x, v2[i].y, v2[i].z, v2[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 c = cs[i][e * units];
+              const float2 y0 = turn(lo_f32(w1[e]), lo_f32(w2[e]), c.x, c.y);
+              const float2 y1 = turn(hi_f32(w1[e]), hi_f32(w2[e]), c.z, c.w);
+              w1[e] = pack(y0.x, y1.x);
+              w2[e] = pack(y0.y, y1.y);
+            }
+            *reinterpret_cast<uint4*>(dst[i] + pairs) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+          }
+          v1[i] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+        }
+        *reinterpret_cast<uint4*>(dst[i]) = v1[i];
       }
-      *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-      *reinterpret_cast<uint4*>(dst + pairs + 8 * u) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
     }
   }
 }
@@ -190,17 +223,15 @@ extern "C" nvq_status rope_apply(const void* q, int64_t ld_q, void* q_out, int64
   a.inv_freq = inv_freq;
   a.mscale = mscale;
   a.sign = inverse ? -1.0f : 1.0f;
-  // enough blocks for eight on every SM first, then more tokens per block
-  a.tokens = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxTokens, T / (152 * 8))));
-  const int64_t blocks = (T + a.tokens - 1) / a.tokens;
-  if (blocks > 0x7FFFFFFF) return NVQ_ERR_UNSUPPORTED;
+  // one wave of blocks; as few rounds of groups as kMaxTokens allows, all full
+  const int64_t wave = static_cast<int64_t>(kPerSm) * device_sms();
+  const int64_t rounds = (T + kMaxTokens * wave - 1) / (kMaxTokens * wave);
+  a.tokens = static_cast<int>((T + rounds * wave - 1) / (rounds * wave));
+  const int64_t groups = (T + a.tokens - 1) / a.tokens;
   const cudaError_t e = timed(NVQ_KERNEL_VSA, stream, [&] {
-    const dim3 grid(static_cast<unsigned>(blocks));
-    if (interleaved)
-      rope_kernel<true><<<grid, kThreads, 0, stream>>>(a);
-    else
-      rope_kernel<false><<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(groups, wave)));
+    return launch_pdl(interleaved ? rope_kernel<true> : rope_kernel<false>, grid, dim3(kThreads), 0,
+                      stream, 1, a);
   });
   return e == cudaSuccess ? NVQ_OK : fail_cuda("rope", e);
 }

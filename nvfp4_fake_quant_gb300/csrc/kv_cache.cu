@@ -25,8 +25,8 @@ namespace nvq {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTokens = 16;  // tokens per block
+constexpr int kThreads = 128;
+constexpr int kTokens = 8;  // tokens per block
 
 struct AppendArgs {
   const uint16_t* k;

@@ -257,8 +257,8 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
         if (!sees(td, a.sinks, td.key0 + r0 + 16 * i + 2 * t + ((j & 1) ^ odd) + 8 * (j >> 1)))
           sb[j] = 0;
     }
-    vs[i][0] = e4m3x2_to_f16x2(sb[0] | (sb[1] << 8));
-    vs[i][1] = e4m3x2_to_f16x2(sb[2] | (sb[3] << 8));
+    vs[i][0] = e4m3x2_to_f16x2(prmt(sb[0], sb[1], 0x0040u));
+    vs[i][1] = e4m3x2_to_f16x2(prmt(sb[2], sb[3], 0x0040u));
   }
   tmem_wait_ld();
   // everything of the stage is in registers: it is refilled under the arithmetic
@@ -281,7 +281,7 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      mx[nt][h] = fmaxf(fmaxf(s[0][nt][h], s[0][nt][2 + h]), fmaxf(s[1][nt][h], s[1][nt][2 + h]));
+      mx[nt][h] = max3f(s[0][nt][h], s[0][nt][2 + h], fmaxf(s[1][nt][h], s[1][nt][2 + h]));
       mx[nt][h] *= a.scale_log2;
       grows |= mx[nt][h] > st.m[nt][h] + kSlack;
     }
@@ -311,20 +311,25 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
   const uint32_t swap = odd ? 0x1032u : 0x3210u;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const float m0 = fmaxf(st.m[nt][0], -3.4e38f), m1 = fmaxf(st.m[nt][1], -3.4e38f);
+    const uint64_t neg_m = pk2(-fmaxf(st.m[nt][0], -3.4e38f), -fmaxf(st.m[nt][1], -3.4e38f));
+    const uint64_t scale2 = pk2(a.scale_log2, a.scale_log2);
+    uint64_t l2 = pk2(st.l[nt][0], st.l[nt][1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float p0 = ex2_f32(fmaf(s[i][nt][0], a.scale_log2, -m0));
-      const float p1 = ex2_f32(fmaf(s[i][nt][1], a.scale_log2, -m1));
-      const float p2 = ex2_f32(fmaf(s[i][nt][2], a.scale_log2, -m0));
-      const float p3 = ex2_f32(fmaf(s[i][nt][3], a.scale_log2, -m1));
-      st.l[nt][0] += p0 + p2;
-      st.l[nt][1] += p1 + p3;
+      float p0, p1, p2, p3;
+      up2(fma2(pk2(s[i][nt][0], s[i][nt][1]), scale2, neg_m), p0, p1);
+      up2(fma2(pk2(s[i][nt][2], s[i][nt][3]), scale2, neg_m), p2, p3);
+      p0 = ex2_f32(p0);
+      p1 = ex2_f32(p1);
+      p2 = ex2_f32(p2);
+      p3 = ex2_f32(p3);
+      l2 = add2(l2, add2(pk2(p0, p1), pk2(p2, p3)));
       pb[i][nt][0] = movmatrix_trans(pack_f16x2_rn(p0, p1));
       pb[i][nt][1] = movmatrix_trans(pack_f16x2_rn(p2, p3));
       pb[i][nt][0] = prmt(pb[i][nt][0], 0u, swap);
       pb[i][nt][1] = prmt(pb[i][nt][1], 0u, swap);
     }
+    up2(l2, st.l[nt][0], st.l[nt][1]);
   }
   // ---- O^T += V~^T P^T: codes of two keys interleaved, so that one conversion
   // gives a pair of keys of one element
@@ -404,6 +409,18 @@ template <int D>
 __device__ __forceinline__ int element_of(int pos) {
   return (pos >> 1 & 7) * (D / 8) + (pos >> 4) * 2 + (pos & 1);
 }
+
+// Place in a ring of `stages`: stage and the parity of its use.
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
@@ -517,10 +534,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     int pages = 0, pages_at = -1;  // this lane's page number of the 32 tiles from pages_at
     bool ok = true;
     int issued = 0;
-    for (int n = 0; n < n_tiles; ++n) {
+    Ring ring;
+    for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
       // everything about the tile first, then the wait for its stage: the loads go out
       // as soon as the stage is free
-      const int s = n % C::kStages;
+      const int s = ring.s;
       if (pages_at < 0 || i >= pages_at + 32 || i < pages_at) {
         const int j = i + lane;
         const int p = j < e.sink_pages ? j : e.first + j - e.sink_pages;
@@ -564,7 +582,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const uint32_t boxes = (td.rows + 31) / 32;  // K codes in boxes of 32 keys
       const uint32_t rows = (td.rows + 3) & ~3;    // whole 16-byte units of scales
       const uint32_t cb = rows * (D / 2), sb = rows * (D / 16);
-      if (!(ok = mbar_wait_warp(&empty[s], ((n / C::kStages) & 1) ^ 1, abort))) break;
+      if (!(ok = mbar_wait_warp(&empty[s], ring.phase ^ 1, abort))) break;
       if (lane == 0) desc[s] = td;
       __syncwarp();
       mbar_arrive_expect_tx_w(&full[s],
@@ -618,9 +636,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           for (int x = lane; x < a.H; x += 32) a.lse[row0 + x] = -INFINITY;
       }
     }
-    for (; n < n_tiles; ++n) {
-      const int s = n % C::kStages;
-      if (!(ok = mbar_wait_warp(&full[s], (n / C::kStages) & 1, abort))) break;
+    Ring ring;
+    for (; n < n_tiles; ++n, ring.next(C::kStages)) {
+      const int s = ring.s;
+      if (!(ok = mbar_wait_warp(&full[s], ring.phase, abort))) break;
       tc_fence_after();  // the scores that were in this stage's columns have been read
       const TileDesc td = desc[s];
       uint8_t* stage = smem + s * C::kStage;
@@ -668,10 +687,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     const int r0 = quarter * 32;  // its keys of a tile
     const VOffsets<D> vo(r0, g, t);
     State<D, NT> st;
-    for (int n = 0; n < n_tiles; ++n) {
-      const int s = n % C::kStages;
-      if (!mbar_wait_warp(&full[s], (n / C::kStages) & 1, abort)) break;
-      if (!mbar_wait_warp(&scored[s], (n / C::kStages) & 1, abort)) break;
+    Ring ring;
+    for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
+      const int s = ring.s;
+      if (!mbar_wait_warp(&full[s], ring.phase, abort)) break;
+      if (!mbar_wait_warp(&scored[s], ring.phase, abort)) break;
       tc_fence_after();
       const TileDesc td = desc[s];
       if (td.flags & kStart) st.clear();

@@ -182,14 +182,14 @@ int make_bnhd_u8_map(CUtensorMap* map, const void* base, int B, int N, int H, in
   return static_cast<int>(r);
 }
 
-int make_kv_codes_map(CUtensorMap* map, const void* pool, int64_t records, int D) {
+int make_kv_codes_map(CUtensorMap* map, const void* pool, int64_t records, int D, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return CUDA_ERROR_NOT_FOUND;
   // a record is 288 rows of D/2 bytes; its first 128 are the K codes
   const cuuint64_t rb = static_cast<cuuint64_t>(D) / 2;
   const cuuint64_t dims[4] = {rb, 288, static_cast<cuuint64_t>(records), 1};
   const cuuint64_t strides[3] = {rb, 288 * rb, 288 * rb * static_cast<cuuint64_t>(records)};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(rb), 32, 1, 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(rb), static_cast<cuuint32_t>(box_rows), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pool), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -424,7 +424,8 @@ struct Ring {
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
-    decode_kernel(const __grid_constant__ CUtensorMap tk, const DecodeArgs a) {
+    decode_kernel(const __grid_constant__ CUtensorMap tk,
+                  const __grid_constant__ CUtensorMap tk32, const DecodeArgs a) {
   using C = Cfg<D, NT>;
   constexpr int kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
@@ -469,6 +470,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     tmem_alloc(&tmem_slot, C::kAlloc);
     tmem_relinquish();
     tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tk32);
   }
   pdl_wait();  // before this nothing that another kernel may have written is read
   // ---- the runs of this CTA: a scan over the sequences
@@ -498,7 +500,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   const int64_t all = total * hgs;
   const int ctas = static_cast<int>(gridDim.x), runs = runs_of(all, C::kRuns * ctas);
   // consecutive runs lie on different SMs: a few tiles spread over all of them
-  auto begin_of = [&](int r) { return r < runs ? all * r / runs : all; };
+  // (all r / runs = (all / runs) r + (all % runs) r / runs, the second part in 32 bits)
+  const int64_t per_run = runs > 0 ? (all <= 0x7FFFFFFF ? static_cast<int>(all) / runs : all / runs) : 0;
+  const int rest = static_cast<int>(all - per_run * runs);
+  auto begin_of = [&](int r) { return r < runs ? per_run * r + rest * r / runs : all; };
   for (int i = 0; i < C::kRuns; ++i) {
     const int64_t u = begin_of(i * ctas + static_cast<int>(blockIdx.x));
     if (u < all && before * hgs <= u && u < (before + mine) * hgs) {
@@ -526,97 +531,98 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   if (warp == kProducer && n_tiles > 0) {
     // ------------------------------------------------------------ producer
     int b = start_b[sub];
-    bool over;
+    bool over, ok = true;
     Extent e = extent(a, b, &over);
     int64_t seg0 = start_before[sub] * hgs;  // line position of the sequence's first tile
-    int hg = static_cast<int>((u0 - seg0) / e.tiles);
-    int i = static_cast<int>((u0 - seg0) - static_cast<int64_t>(hg) * e.tiles);
-    int pages = 0, pages_at = -1;  // this lane's page number of the 32 tiles from pages_at
-    bool ok = true;
-    int issued = 0;
+    const int64_t into = u0 - seg0;
+    int hg = into <= 0x7FFFFFFF ? static_cast<int>(into) / e.tiles
+                                : static_cast<int>(into / e.tiles);
+    int i = static_cast<int>(into - static_cast<int64_t>(hg) * e.tiles);
+    int n = 0;
     Ring ring;
-    for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
-      // everything about the tile first, then the wait for its stage: the loads go out
-      // as soon as the stage is free
-      const int s = ring.s;
-      if (pages_at < 0 || i >= pages_at + 32 || i < pages_at) {
-        const int j = i + lane;
-        const int p = j < e.sink_pages ? j : e.first + j - e.sink_pages;
-        pages = j < e.tiles ? a.table[b * a.ld_table + p] : -1;
-        pages_at = i;
-      }
-      const int page = __shfl_sync(0xFFFFFFFFu, pages, i - pages_at);
-      const int p = i < e.sink_pages ? i : e.first + i - e.sink_pages;
+    while (n < n_tiles && ok) {
+      // ---- one segment (the part of it that lies in the run: tiles i .. i_end - 1)
       const int64_t first = seg0 + static_cast<int64_t>(hg) * e.tiles;
+      const int i_end = min(e.tiles, i + n_tiles - n);
+      // whole segments are written directly; a part that begins with the run goes
+      // to the run's slot 0, one that begins inside it to slot 1
+      const bool whole = first >= u0 && first + e.tiles <= u1;
       TileDesc td;
-      td.key0 = p * kPage;
       td.len = e.len;
       td.wstart = e.wstart;
       td.b = b;
       td.hg = hg;
-      td.rows = min(kPage, e.len - td.key0);
-      td.flags = 0;
-      if (n == 0 || i == 0) td.flags |= kStart;
-      if (n == n_tiles - 1 || i == e.tiles - 1) td.flags |= kEnd;
-      if (td.rows < kPage || (td.key0 < e.wstart && td.key0 + kPage > a.sinks)) td.flags |= kMasked;
-      // whole segments are written directly; a part that begins with the run goes
-      // to the run's slot 0, one that begins inside it to slot 1
-      const bool whole = first >= u0 && first + e.tiles <= u1;
       td.slot = whole ? -1 : 2 * run + (first > u0 ? 1 : 0);
-      if (n == n_tiles - 1 && first >= u0 && first + e.tiles > u1 && lane == 0) {
+      if (first >= u0 && first + e.tiles > u1 && lane == 0) {
         // the run that holds tile u: the last c with all c / runs <= u
         const int64_t u = first + e.tiles - 1;
         a.runs[run] = {b, hg, td.slot, static_cast<int>(((u + 1) * runs + all - 1) / all - 1)};
       }
-      const bool there = page >= 0 && page < a.num_pages;
-      if (!there) {
-        td.flags |= kAbsent;
-        if (lane == 0) atomicMax(a.err, kErrTable);
-      }
-      uint8_t* dst = smem + s * C::kStage;
-      const int hk = hg / a.chunks, g0 = hg % a.chunks * C::kHeads;
-      const uint32_t q_bytes =
-          td.flags & kStart ? min(C::kHeads, a.G - g0) * (D * 2) : 0;  // q of the segment
-      const int64_t rec = static_cast<int64_t>(page) * a.Hkv + hk;
-      const uint8_t* src = a.pool + rec * record_bytes(D);
-      const uint32_t boxes = (td.rows + 31) / 32;  // K codes in boxes of 32 keys
-      const uint32_t rows = (td.rows + 3) & ~3;    // whole 16-byte units of scales
-      const uint32_t cb = rows * (D / 2), sb = rows * (D / 16);
-      if (!(ok = mbar_wait_warp(&empty[s], ring.phase ^ 1, abort))) break;
-      if (lane == 0) desc[s] = td;
-      __syncwarp();
-      mbar_arrive_expect_tx_w(&full[s],
-                              q_bytes + (there ? boxes * (16 * D) + cb + 2 * sb : 0));
-      if (q_bytes > 0)
-        bulk_load_w(dst + C::kRec,
-                    a.q + b * a.ld_q + static_cast<int64_t>(hk * a.G + g0) * D, q_bytes, &full[s]);
-      if (there) {
-        for (uint32_t x = 0; x < boxes; ++x)
-          tma_load_4d_w(dst + x * (16 * D), &tk, 0, x * 32, static_cast<int>(rec), 0, &full[s]);
-        if (td.rows == kPage) {
+      const int hk = hg / a.chunks, g0 = (hg - hk * a.chunks) * C::kHeads;
+      const uint8_t* q = reinterpret_cast<const uint8_t*>(
+          a.q + b * a.ld_q + static_cast<int64_t>(hk * a.G + g0) * D);
+      uint32_t q_bytes = min(C::kHeads, a.G - g0) * (D * 2);  // with the first tile
+      const int32_t* table = a.table + b * a.ld_table;
+      const int i0 = i;
+      int pages = 0;  // this lane's page number: of tile i0 + 32 k + lane
+      for (; i < i_end; ++i, ++n, ring.next(C::kStages)) {
+        // everything about the tile first, then the wait for its stage: the loads go
+        // out as soon as the stage is free
+        if (((i - i0) & 31) == 0) {
+          const int j = i + lane;
+          pages = j < e.tiles ? table[j < e.sink_pages ? j : e.first + j - e.sink_pages] : -1;
+        }
+        const int page = __shfl_sync(0xFFFFFFFFu, pages, i - i0);
+        td.key0 = (i < e.sink_pages ? i : e.first + i - e.sink_pages) * kPage;
+        td.rows = min(kPage, e.len - td.key0);
+        td.flags = (i == i0 ? kStart : 0) | (i == i_end - 1 ? kEnd : 0);
+        const bool there = page >= 0 && page < a.num_pages;
+        if (!there) {
+          td.flags |= kAbsent;
+          if (lane == 0) atomicMax(a.err, kErrTable);
+        }
+        if (td.rows < kPage || (td.key0 < e.wstart && td.key0 + kPage > a.sinks))
+          td.flags |= kMasked;
+        const int s = ring.s;
+        uint8_t* dst = smem + s * C::kStage;
+        const int rec = page * a.Hkv + hk;
+        const uint8_t* src = a.pool + static_cast<int64_t>(rec) * record_bytes(D);
+        if (!(ok = mbar_wait_warp(&empty[s], ring.phase ^ 1, abort))) break;
+        if (lane == 0) desc[s] = td;
+        __syncwarp();
+        if (there && td.rows == kPage) {
+          mbar_arrive_expect_tx_w(&full[s], q_bytes + C::kRec);
+          tma_load_4d_w(dst, &tk, 0, 0, rec, 0, &full[s]);
           bulk_load_w(dst + v_codes_at(D), src + v_codes_at(D), C::kRec - v_codes_at(D), &full[s]);
-        } else {
+        } else if (there) {
+          const uint32_t boxes = (td.rows + 31) / 32;  // K codes in boxes of 32 keys
+          const uint32_t rows = (td.rows + 3) & ~3;    // whole 16-byte units of scales
+          const uint32_t cb = rows * (D / 2), sb = rows * (D / 16);
+          mbar_arrive_expect_tx_w(&full[s], q_bytes + boxes * (16 * D) + cb + 2 * sb);
+          for (uint32_t x = 0; x < boxes; ++x)
+            tma_load_4d_w(dst + x * (16 * D), &tk32, 0, x * 32, rec, 0, &full[s]);
           bulk_load_w(dst + v_codes_at(D), src + v_codes_at(D), cb, &full[s]);
           bulk_load_w(dst + k_scales_at(D), src + k_scales_at(D), sb, &full[s]);
           bulk_load_w(dst + v_scales_at(D), src + v_scales_at(D), sb, &full[s]);
+        } else {
+          mbar_arrive_expect_tx_w(&full[s], q_bytes);
         }
+        if (q_bytes > 0) bulk_load_w(dst + C::kRec, q, q_bytes, &full[s]);
+        q_bytes = 0;
       }
-      issued = n + 1;
-      if (++i == e.tiles && n + 1 < n_tiles) {
-        i = 0;
-        pages_at = -1;
-        if (++hg == hgs) {
-          hg = 0;
-          seg0 += static_cast<int64_t>(e.tiles) * hgs;
-          do {
-            e = extent(a, ++b, &over);
-          } while (e.tiles == 0);
-        }
+      if (n == n_tiles || !ok) break;
+      i = 0;
+      if (++hg == hgs) {
+        hg = 0;
+        seg0 += static_cast<int64_t>(e.tiles) * hgs;
+        do {
+          e = extent(a, ++b, &over);
+        } while (e.tiles == 0);
       }
     }
     if (!ok) {  // let the copies already issued land before the block leaves
-      for (int n = max(0, issued - C::kStages); n < issued; ++n)
-        mbar_wait_warp(&full[n % C::kStages], (n / C::kStages) & 1, nullptr, 10000000ull);
+      for (int m = max(0, n - C::kStages); m < n; ++m)
+        mbar_wait_warp(&full[m % C::kStages], (m / C::kStages) & 1, nullptr, 10000000ull);
     }
   } else if (warp == kMma) {
     // ----------------------------------------------------------------- MMA
@@ -886,14 +892,14 @@ Plan plan(int B, int H, int Hkv, int D, int max_pages) {
 }
 
 template <int D, int NT>
-cudaError_t launch_decode(const CUtensorMap& tk, const DecodeArgs& a, const Plan& p,
-                          cudaStream_t stream) {
+cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tk32, const DecodeArgs& a,
+                          const Plan& p, cudaStream_t stream) {
   using C = Cfg<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   if ((e = launch_pdl(decode_kernel<D, NT>, dim3(p.ctas), dim3(C::kThreads), C::kSmem, stream, 1, tk,
-                      a)) != cudaSuccess)
+                      tk32, a)) != cudaSuccess)
     return e;
   return launch_pdl(join_kernel<D, NT>, dim3(p.runs, p.join_y), dim3(256), 0, stream, 1, a);
 }
@@ -930,8 +936,10 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
     return NVQ_ERR_WORKSPACE;
   int* err = device_error_word();
   if (err == nullptr) return NVQ_ERR_CUDA;
-  CUtensorMap tk;
-  if (const int r = make_kv_codes_map(&tk, pool, num_pages * Hkv, D); r != 0)
+  CUtensorMap tk, tk32;
+  int r;
+  if ((r = make_kv_codes_map(&tk, pool, num_pages * Hkv, D, kPage)) != 0 ||
+      (r = make_kv_codes_map(&tk32, pool, num_pages * Hkv, D, 32)) != 0)
     return fail_driver("cuTensorMapEncodeTiled", r);
   uint8_t* wb = static_cast<uint8_t*>(ws);
   const DecodeArgs a{static_cast<const uint16_t*>(q), ld_q, static_cast<const uint8_t*>(pool),
@@ -940,10 +948,10 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
                      reinterpret_cast<RunInfo*>(wb), reinterpret_cast<float*>(wb + p.parts), err};
   const cudaError_t e = timed(NVQ_KERNEL_ATTN_FWD, stream, [&] {
     if (D == 128)
-      return p.nt == 1 ? launch_decode<128, 1>(tk, a, p, stream)
-                       : launch_decode<128, 2>(tk, a, p, stream);
-    return p.nt == 1 ? launch_decode<64, 1>(tk, a, p, stream)
-                     : launch_decode<64, 2>(tk, a, p, stream);
+      return p.nt == 1 ? launch_decode<128, 1>(tk, tk32, a, p, stream)
+                       : launch_decode<128, 2>(tk, tk32, a, p, stream);
+    return p.nt == 1 ? launch_decode<64, 1>(tk, tk32, a, p, stream)
+                     : launch_decode<64, 2>(tk, tk32, a, p, stream);
   });
   return e == cudaSuccess ? NVQ_OK : fail_cuda("attn decode", e);
 }

@@ -212,8 +212,8 @@ int make_codes_map(CUtensorMap* map, const void* base, int64_t rows, int64_t row
                    int box_rows = 128);
 
 // Maps the records of a paged cache (uint8 [records, 144 D]) as rows of D/2 bytes,
-// box of 32 rows, (D/2)-byte swizzle; coordinates (0, row, record, 0).
-int make_kv_codes_map(CUtensorMap* map, const void* pool, int64_t records, int D);
+// box of box_rows rows, (D/2)-byte swizzle; coordinates (0, row, record, 0).
+int make_kv_codes_map(CUtensorMap* map, const void* pool, int64_t records, int D, int box_rows);
 
 // The NVFP4 linear's GEMMs (gemm.cu).
 // out [M, N] bf16 = alpha * (x codes . x scales)(w codes . w scales)^T + bias:

@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       const int s = ring.s;
       if (!(ok = mbar_wait_warp(&full[s], ring.phase, abort))) break;
       tc_fence_after();  // the scores that were in this stage's columns have been read
-      const TileDesc td = desc[s];
+      struct { int flags, hg; } td = {desc[s].flags, desc[s].hg};
       uint8_t* stage = smem + s * C::kStage;
       if (td.flags & kStart) {
         const int qb = seg & 1;
@@ -670,20 +670,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
           if (td.flags & kStart)
             tmem_cp_32x128_x4_w(sfb + 4 * k, smem_u32(smem + C::kQScales + qb * 1024) + 512 * k);
         }
+        const uint64_t kd[2] = {sdesc(ka, 16, sbo, lay), sdesc(ka, 16, sbo, lay) + 2};
+        const uint64_t qd[2] = {sdesc(qa, 16, sbo, lay), sdesc(qa, 16, sbo, lay) + 2};
+        umma_fp4_group_w<D / 64>(tmem + 16 * s, kd, qd, idesc, sfa, sfb, bar_u32(&scored[s]),
+                                 td.flags & kEnd ? bar_u32(&q_free[qb]) : 0u);
+      } else {
+        if (td.flags & kStart) {  // later tiles of the segment read q~ all the same
+          fence_proxy_async_smem();
+          __syncwarp();
 #pragma unroll
-        for (int k = 0; k < D / 64; ++k)
-          umma_fp4_ss_w(tmem + 16 * s, sdesc(ka + 32 * k, 16, sbo, lay),
-                        sdesc(qa + 32 * k, 16, sbo, lay), idesc, sfa + 4 * k, sfb + 4 * k, k > 0);
-      } else if (td.flags & kStart) {
-        fence_proxy_async_smem();
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k)
-          tmem_cp_32x128_x4_w(tmem + C::kSfb + qb * (D / 16) + 4 * k,
-                              smem_u32(smem + C::kQScales + qb * 1024) + 512 * k);
+          for (int k = 0; k < D / 64; ++k)
+            tmem_cp_32x128_x4_w(tmem + C::kSfb + qb * (D / 16) + 4 * k,
+                                smem_u32(smem + C::kQScales + qb * 1024) + 512 * k);
+        }
+        umma_commit_w(&scored[s]);
+        if (td.flags & kEnd) umma_commit_w(&q_free[qb]);
       }
-      umma_commit_w(&scored[s]);
-      if (td.flags & kEnd) umma_commit_w(&q_free[qb]);
     }
     for (int m = max(0, n - C::kStages); m < n; ++m)  // the MMAs in flight end before the block
       mbar_wait_warp(&scored[m % C::kStages], (m / C::kStages) & 1, nullptr, 10000000ull);

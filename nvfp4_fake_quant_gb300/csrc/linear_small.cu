@@ -494,10 +494,14 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
     if (e != cudaSuccess) return e;
     return launch_pdl(linear_small_kernel<false>, dim3(q.runs), dim3(kThreads), smem, stream, 1, tx, tw, a);
   }
-  // at most four stages: two CTAs fit an SM, so that clusters of four find room in
-  // every group of SMs
+  // At most four stages and 112 KB: two CTAs fit an SM, so that clusters find room in
+  // every group of SMs.  At least 78 KB: no three do, whose 256 tensor-memory columns
+  // each would not fit, so that no CTA waits for columns that a cluster holds which in
+  // its turn waits for that CTA's cluster.
+  const size_t sums = static_cast<size_t>(q.split - 1) * q.cols * 512;
   a.stages = std::min(4, (q.k_stages + q.split - 1) / q.split);
-  smem = a.stages * stage + (q.split - 1) * q.cols * 512 + 1024;
+  if (q.split < 8) a.stages = std::min<int>(a.stages, (112 * 1024 - 1024 - sums) / stage);
+  smem = std::max<size_t>(a.stages * stage + sums + 1024, 78 * 1024);
   e = cudaFuncSetAttribute(linear_small_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            226 * 1024);
   if (e != cudaSuccess) return e;

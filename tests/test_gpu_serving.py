@@ -167,3 +167,52 @@ def test_prompt_then_single_tokens():
     got_l = torch.stack(ls).cpu().double()
     assert bool(((got_l - lse_ref[0, :, n:].T).abs() <= ref[3] * 2.0 ** -16 + 2.0 ** -18).all())
     assert bool(((got_l - stats[0, :, 0, n:].T.cpu().double()).abs() <= 2e-3).all())
+
+
+def test_captured_step_between_other_kernels():
+    """A decode step captured between ordinary torch kernels (the calls' launches may come up
+    early, behind whatever precedes them): the replay equals the eager step, and weights
+    repacked just before the linear are the ones it uses."""
+    h, d, hidden = 4, 64, 256
+    torch.manual_seed(8)
+    w = (torch.randn(3 * h * d, hidden, device="cuda") * 0.06).to(BF16)
+    x = torch.zeros(2, hidden, dtype=BF16, device="cuda")
+    src = torch.randn(2, hidden, device="cuda").to(BF16)
+    gain = torch.ones((), dtype=BF16, device="cuda")
+    xg = torch.tensor([500.0], device="cuda")
+    f = api.rope_inv_freq(d, device="cuda")[0]
+    pool = api.nvfp4_kv_pool(4, h, d)
+    table = torch.tensor([[0, 2], [3, 1]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([0, 126], dtype=torch.int32, device="cuda")
+    out = torch.zeros(2, h * d, device="cuda")
+
+    def step():
+        lens.add_(1)
+        x.copy_(src * 0.5)
+        codes, scales = api.nvfp4_quantize_tiled(w * gain)
+        qkv = api.nvfp4_linear_packed_fwd(x, codes, scales, x_global_sf=xg).view(2, 3, h, d)
+        q, k = api.rope_apply(qkv[:, 0], qkv[:, 1], lens - 1, f)
+        api.nvfp4_kv_append(k, qkv[:, 2], lens, table, pool)
+        o, lse = api.attn_qat_decode(q, pool, table, lens)
+        out.copy_(o.view(2, -1).float() + lse.mean())
+
+    step()
+    eager = []
+    state = (pool.clone(), lens.clone())
+    for i in range(3):
+        gain.fill_(1.0 + i)
+        step()
+        eager.append(out.clone())
+    pool.copy_(state[0])
+    lens.copy_(state[1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for i in range(3):
+        gain.fill_(1.0 + i)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager[i])
+    assert api.device_status() == 0

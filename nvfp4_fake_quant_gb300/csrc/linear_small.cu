@@ -35,11 +35,11 @@ namespace {
 
 constexpr int kThreads = 192;  // producer, MMA, 4 epilogue warps
 constexpr int kSteps = 4;      // MMA steps (64 elements) per stage
-constexpr int kMaxStages = 9;
+constexpr int kStages = 6;      // of the ring (9: 1 us slower at 32 x 28672 x 8192)
 // bytes of a stage: w codes, w scales, x scales
 constexpr uint32_t kW = 128 * 128, kSc = kSteps * 512, kXs = 1024;
 constexpr uint32_t kScCol = 128;  // tensor memory: two accumulators of 64 columns, then scales
-static_assert(kScCol + 32 * kMaxStages <= 512 && kScCol + 32 * 4 <= 256, "tensor memory");
+static_assert(kScCol + 32 * kStages <= 512 && kScCol + 32 * 4 <= 256, "tensor memory");
 
 struct SmallArgs {
   int M, N, cols, stages;   // cols: M rounded up to 16; stages of the ring
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) &
                                              ~static_cast<uintptr_t>(1023u));
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+  __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
   __shared__ uint64_t sums_full;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -342,57 +342,68 @@ __global__ void __launch_bounds__(kThreads)
         if (!mbar_wait_warp(&acc_full[part & 1], (part >> 1) & 1, abort)) break;
         tc_fence_after();
         const uint32_t acc = tmem + 64 * (part & 1) + (static_cast<uint32_t>(quarter * 32) << 16);
-        // slot 0 of a run: the part that begins with it; slot 1: one that begins inside
-        float* mine = p.parts +
-                      (static_cast<int64_t>(2 * blockIdx.x + (from > u0 ? 1 : 0)) * p.cols) * 128 + row;
-        for (int c = 0; c < p.M; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(acc + c, v);
-          tmem_wait_ld();
+        // the tile's parts are those of runs c0 .. c1; slot 0 of a run: the part that
+        // begins with it; slot 1: one that begins inside
+        const int c0 = whole ? 0 : run_of(p, t0), c1 = whole ? 0 : run_of(p, t0 + p.k_stages - 1);
+        const int me = whole ? 0 : static_cast<int>(blockIdx.x);
+        auto part_of = [&](int c) {
+          const int slot = 2 * c + (c == c0 && run_begin(p, c) < t0 ? 1 : 0);
+          return p.parts + static_cast<int64_t>(slot) * p.cols * 128 + row;
+        };
+        unsigned int* ticket = &p.tickets[4 * tile + quarter];
+        const unsigned int others = static_cast<unsigned int>(c1 - c0);
+        // Usually a run's last part finds all others there (they began their runs): it
+        // adds from its accumulator, without writing it out first.
+        bool last = whole;
+        if (!whole) {
+          unsigned int seen = 0;
+          if (lane == 0) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(ticket) : "memory");
+          last = __shfl_sync(0xFFFFFFFFu, seen, 0) == others;
+        }
+        if (!last) {
+          float* mine = part_of(me);
+          for (int c = 0; c < p.M; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(acc + c, v);
+            tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (c + j >= p.M) break;
-            const float f = __uint_as_float(v[j]);
-            if (!whole)
-              mine[(c + j) * 128] = f;
-            else if (n < p.N)
-              p.out[static_cast<int64_t>(c + j) * p.N + n] = __float2bfloat16_rn(fmaf(alpha, f, bias));
+            for (int j = 0; j < 16; ++j) mine[(c + j) * 128] = __uint_as_float(v[j]);
+          }
+          __threadfence();
+          __syncwarp();
+          unsigned int before = 0;
+          if (lane == 0) before = atomicAdd(ticket, 1u);
+          last = __shfl_sync(0xFFFFFFFFu, before, 0) == others;
+        }
+        if (last) {
+          if (!whole) __threadfence();
+          // in run order, 16 rows at a time
+          for (int m0 = 0; m0 < p.M; m0 += 16) {
+            uint32_t own[16];
+            tmem_ld16(acc + m0, own);
+            tmem_wait_ld();
+            float f[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] = 0.f;
+#pragma unroll 2
+            for (int c = c0; c <= c1; ++c) {
+              const float* from_c = part_of(c) + m0 * 128;
+              float v[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                v[j] = whole || c == me ? __uint_as_float(own[j]) : __ldcg(from_c + j * 128);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) f[j] += v[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (m0 + j < p.M && n < p.N)
+                p.out[static_cast<int64_t>(m0 + j) * p.N + n] =
+                    __float2bfloat16_rn(fmaf(alpha, f[j], bias));
           }
         }
         tc_fence_before();
         mbar_arrive_warp(&acc_empty[part & 1]);
-        if (whole) continue;
-        // ---- the last of the tile's parts to arrive adds them up, in run order
-        const int c0 = run_of(p, t0), c1 = run_of(p, t0 + p.k_stages - 1);
-        __threadfence();
-        __syncwarp();
-        unsigned int before = 0;
-        if (lane == 0) before = atomicAdd(&p.tickets[4 * tile + quarter], 1u);
-        before = __shfl_sync(0xFFFFFFFFu, before, 0);
-        if (before != static_cast<unsigned int>(c1 - c0)) continue;
-        __threadfence();
-        const float* first = p.parts + row +
-            (static_cast<int64_t>(2 * c0 + (run_begin(p, c0) < t0 ? 1 : 0)) * p.cols) * 128;
-        // 16 rows' loads in flight at a time
-        for (int m0 = 0; m0 < p.M; m0 += 16) {
-          float f[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) f[j] = __ldcg(first + (m0 + j) * 128);
-#pragma unroll 2
-          for (int c = c0 + 1; c <= c1; ++c) {
-            const float* more = p.parts + (static_cast<int64_t>(2 * c) * p.cols + m0) * 128 + row;
-            float v[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __ldcg(more + j * 128);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] += v[j];
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (m0 + j < p.M && n < p.N)
-              p.out[static_cast<int64_t>(m0 + j) * p.N + n] =
-                  __float2bfloat16_rn(fmaf(alpha, f[j], bias));
-        }
         __syncwarp();
       }
     }
@@ -470,7 +481,7 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
   a.M = static_cast<int>(M);
   a.N = static_cast<int>(N);
   a.cols = q.cols;
-  a.stages = std::min<int>(kMaxStages, (220 * 1024) / stage);
+  a.stages = std::min<int>(kStages, (220 * 1024) / stage);
   a.split = q.split;
   a.tiles = q.tiles;
   a.k_stages = q.k_stages;

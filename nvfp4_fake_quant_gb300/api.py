@@ -350,15 +350,15 @@ class NVFP4Linear(torch.nn.Module):
 # valid call: one pass over plain attributes, with the explanation left to the path
 # that raises.
 
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
-    torch._C, "_cuda_getCurrentRawStream") else \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch(index: int, name: str, *args) -> None:
     """The entry point on the current stream of device ``index``, with that device
     current (the library works on the current device)."""
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         _lib.call(name, *args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -368,7 +368,7 @@ def _launch(index: int, name: str, *args) -> None:
 def _on(index: int, name: str, *args) -> int:
     """A size query with device ``index`` current (sizes follow its SM count)."""
     f = getattr(_lib.load(), name)
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         return int(f(*args))
     with torch.cuda.device(index):
         return int(f(*args))
@@ -640,7 +640,7 @@ def _check_cache(pool, page_table, seq_lens, d):
     _check_i32(page_table, "page_table", 2)
     _check_i32(seq_lens, "seq_lens", 1)
     b, max_pages = page_table.shape
-    if seq_lens.shape[0] != b:
+    if len(seq_lens) != b:
         raise ValueError(f"page_table has {b} rows, seq_lens {seq_lens.shape[0]}")
     return b, max_pages, (page_table.stride(0) if b > 1 else max_pages)
 

@@ -339,9 +339,6 @@ __global__ void __launch_bounds__(kThreads)
         const int n = tile * 128 + row;
         const bool whole = from == t0 && u == t0 + p.k_stages;
         const float bias = p.bias != nullptr && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
-        if (!mbar_wait_warp(&acc_full[part & 1], (part >> 1) & 1, abort)) break;
-        tc_fence_after();
-        const uint32_t acc = tmem + 64 * (part & 1) + (static_cast<uint32_t>(quarter * 32) << 16);
         // the tile's parts are those of runs c0 .. c1; slot 0 of a run: the part that
         // begins with it; slot 1: one that begins inside
         const int c0 = whole ? 0 : run_of(p, t0), c1 = whole ? 0 : run_of(p, t0 + p.k_stages - 1);
@@ -352,33 +349,62 @@ __global__ void __launch_bounds__(kThreads)
         };
         unsigned int* ticket = &p.tickets[4 * tile + quarter];
         const unsigned int others = static_cast<unsigned int>(c1 - c0);
-        // Usually a run's last part finds all others there (they began their runs): it
-        // adds from its accumulator, without writing it out first.
-        bool last = whole;
-        if (!whole) {
-          unsigned int seen = 0;
-          if (lane == 0) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(ticket) : "memory");
-          last = __shfl_sync(0xFFFFFFFFu, seen, 0) == others;
+        auto all_there = [&] {  // acquired by every lane: the parts may be read
+          unsigned int seen;
+          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(ticket) : "memory");
+          return __all_sync(0xFFFFFFFFu, seen == others) != 0;
+        };
+        // Usually a run's last part finds its one other there (that run began with it):
+        // its values are fetched while the MMAs still run, and added to the accumulator,
+        // which is never written out.
+        float other[32];
+        const bool early = others == 1 && all_there();
+        const float* theirs = part_of(me == c0 ? c1 : c0);
+        if (early) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            other[j] = j < p.cols ? __ldcg(theirs + j * 128) : 0.f;
         }
-        if (!last) {
-          float* mine = part_of(me);
-          for (int c = 0; c < p.M; c += 16) {
-            uint32_t v[16];
-            tmem_ld16(acc + c, v);
+        if (!mbar_wait_warp(&acc_full[part & 1], (part >> 1) & 1, abort)) break;
+        tc_fence_after();
+        const uint32_t acc = tmem + 64 * (part & 1) + (static_cast<uint32_t>(quarter * 32) << 16);
+        auto store = [&](int m, float f) {
+          if (m < p.M && n < p.N)
+            p.out[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(fmaf(alpha, f, bias));
+        };
+        if (whole || early) {
+          for (int m0 = 0; m0 < p.M; m0 += 32) {
+            uint32_t own[32];
+            tmem_ld32(acc + m0, own);
+            if (early && m0 > 0) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                other[j] = m0 + j < p.cols ? __ldcg(theirs + (m0 + j) * 128) : 0.f;
+            }
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) mine[(c + j) * 128] = __uint_as_float(v[j]);
+            for (int j = 0; j < 32; ++j)
+              store(m0 + j, early ? __uint_as_float(own[j]) + other[j] : __uint_as_float(own[j]));
           }
-          __threadfence();
-          __syncwarp();
-          unsigned int before = 0;
-          if (lane == 0) before = atomicAdd(ticket, 1u);
-          last = __shfl_sync(0xFFFFFFFFu, before, 0) == others;
-        }
-        if (last) {
-          if (!whole) __threadfence();
-          // in run order, 16 rows at a time
-          for (int m0 = 0; m0 < p.M; m0 += 16) {
+        } else {
+          bool last = all_there();
+          if (!last) {
+            float* mine = part_of(me);
+            for (int c = 0; c < p.M; c += 16) {
+              uint32_t v[16];
+              tmem_ld16(acc + c, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) mine[(c + j) * 128] = __uint_as_float(v[j]);
+            }
+            __threadfence();
+            __syncwarp();
+            unsigned int before = 0;
+            if (lane == 0) before = atomicAdd(ticket, 1u);
+            last = __shfl_sync(0xFFFFFFFFu, before, 0) == others;
+            if (last) __threadfence();
+          }
+          for (int m0 = 0; m0 < p.M && last; m0 += 16) {  // in run order
             uint32_t own[16];
             tmem_ld16(acc + m0, own);
             tmem_wait_ld();
@@ -391,15 +417,12 @@ __global__ void __launch_bounds__(kThreads)
               float v[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                v[j] = whole || c == me ? __uint_as_float(own[j]) : __ldcg(from_c + j * 128);
+                v[j] = c == me ? __uint_as_float(own[j]) : __ldcg(from_c + j * 128);
 #pragma unroll
               for (int j = 0; j < 16; ++j) f[j] += v[j];
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (m0 + j < p.M && n < p.N)
-                p.out[static_cast<int64_t>(m0 + j) * p.N + n] =
-                    __float2bfloat16_rn(fmaf(alpha, f[j], bias));
+            for (int j = 0; j < 16; ++j) store(m0 + j, f[j]);
           }
         }
         tc_fence_before();

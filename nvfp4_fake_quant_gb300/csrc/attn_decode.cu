@@ -37,6 +37,12 @@
 // rounding; all sums are fp32.  The maximum that p refers to is raised only when
 // a score exceeds it by 8 (log2): p then stays below 2^8, far inside f16, and the
 // cross-lane maximum and the rescaling of O leave the common path.
+//
+// Measured (calls in a CUDA graph): 8 x up to 131072 tokens, 64 heads on 8 of 128:
+// 118 us, 86% of the copy rate in bytes of the cache; 64 sequences of up to 8192, 32
+// heads on 8: 64 us, 68%; one sequence of 777 tokens: 10 us, the latency of two
+// launches, the scan and a tile.  Short segments cost most: each begins with a
+// quantization of q and ends with two barriers of its four warps.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -66,16 +72,15 @@ struct Cfg {
   static constexpr int kHeads = 8 * NT;
   static constexpr int kRuns = NT == 1 ? 3 : 2;  // per CTA, one CTA per SM
   static constexpr int kThreads = kRuns * kRunWarps * 32;
-  static constexpr int kStages = D == 64 ? 6 : (NT == 1 ? 3 : 4);
-  static constexpr int kHalf = kHeads / 2;  // heads that the warps join at a time
+  static constexpr int kStages = D == 64 ? 5 : (NT == 1 ? 2 : 3);
   static constexpr int kRow = D + 4;  // floats of a head's row in the join area
   static constexpr uint32_t kRec = record_bytes(D);
   static constexpr uint32_t kQ = kHeads * D * 2;         // q of a segment that starts with the tile
   static constexpr uint32_t kStage = kRec + kQ;
   static constexpr uint32_t kQCodes = kStages * kStage;  // [2] q~ codes, 16 rows of D/2 bytes
   static constexpr uint32_t kQScales = kQCodes + 2 * 1024;               // [2][D/64] blocks of 512
-  static constexpr uint32_t kJoin = kQScales + 2 * 1024;                 // float [4][kHalf][kRow]
-  static constexpr uint32_t kMl = kJoin + kWarps * kHalf * kRow * 4;     // float2 [4][heads]
+  static constexpr uint32_t kJoin = kQScales + 2 * 1024;                 // float [4][kHeads][kRow]
+  static constexpr uint32_t kMl = kJoin + kWarps * kHeads * kRow * 4;     // float2 [4][heads]
   static constexpr uint32_t kDesc = kMl + kWarps * kHeads * 8;           // TileDesc [stages]
   static constexpr uint32_t kBars = kDesc + kStages * 32;
   static constexpr uint32_t kRun = (kBars + (3 * kStages + 4) * 8 + 1023) / 1024 * 1024;
@@ -108,14 +113,16 @@ struct DecodeArgs {
   int window, sinks;
   __nv_bfloat16* o;
   float* lse;
-  struct RunInfo* runs;  // [gridDim.x] (workspace)
-  float* parts;          // [2 gridDim.x] parts (workspace)
+  struct RunInfo* split;  // what crosses runs, by run or by segment (workspace)
+  int by_segment;         // 1: entries by segment (there are fewer than runs)
+  float* parts;           // [2 runs] parts (workspace)
+  int runs;               // of the grid
   int* err;
 };
 
-// The segment that begins in a run and goes on in later ones; last < 0: none.
+// A segment that begins in a run and goes on in later ones; last < 0: none.
 struct RunInfo {
-  int b, hg, slot, last;  // slot of the run's own part, last run of the segment
+  int b, hg, run, slot, last;  // its first run, that run's part, its last run
 };
 
 // Floats of one part: m (log2 units) and l per head, then the sums [heads][D].
@@ -262,8 +269,7 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
   }
   tmem_wait_ld();
   // everything of the stage is in registers: it is refilled under the arithmetic
-  // (held until its end, the loads in flight fell short: 128 against 117 us at 8 x
-  // 131072 tokens)
+  // (held until its end: 1 us more at 8 x 131072 tokens, 8 KV heads of 128)
   tc_fence_before();
   mbar_arrive_warp(release);
   // ---- p = 2^(S log2e - m)
@@ -526,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   const int run = sub * ctas + static_cast<int>(blockIdx.x);
   const int64_t u0 = begin_of(run), u1 = begin_of(run + 1);
   const int n_tiles = static_cast<int>(u1 - u0);
-  if (warp == kProducer && lane == 0) a.runs[run].last = -1;
+  if (!a.by_segment && warp == kProducer && lane == 0) a.split[run].last = -1;
 
   if (warp == kProducer && n_tiles > 0) {
     // ------------------------------------------------------------ producer
@@ -553,10 +559,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       td.b = b;
       td.hg = hg;
       td.slot = whole ? -1 : 2 * run + (first > u0 ? 1 : 0);
-      if (first >= u0 && first + e.tiles > u1 && lane == 0) {
-        // the run that holds tile u: the last c with all c / runs <= u
-        const int64_t u = first + e.tiles - 1;
-        a.runs[run] = {b, hg, td.slot, static_cast<int>(((u + 1) * runs + all - 1) / all - 1)};
+      if (lane == 0 && first >= u0) {
+        RunInfo* info = a.split + (a.by_segment ? b * hgs + hg : run);
+        if (first + e.tiles > u1) {
+          // the run that holds tile u: the last c with all c / runs <= u
+          const int64_t u = first + e.tiles - 1;
+          *info = {b, hg, run, td.slot, static_cast<int>(((u + 1) * runs + all - 1) / all - 1)};
+        } else if (a.by_segment) {
+          info->last = -1;
+        }
       }
       const int hk = hg / a.chunks, g0 = (hg - hk * a.chunks) * C::kHeads;
       const uint8_t* q = reinterpret_cast<const uint8_t*>(
@@ -635,6 +646,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       for (int b = blockIdx.x; b < a.B; b += ctas) {
         bool over;
         if (extent(a, b, &over).tiles > 0) continue;
+        for (int x = lane; a.by_segment && x < hgs; x += 32) a.split[b * hgs + x].last = -1;
         const int64_t row0 = static_cast<int64_t>(b) * a.H;
         for (int x = lane; x < a.H * (D / 8); x += 32)
           reinterpret_cast<uint4*>(a.o + row0 * D)[x] = make_uint4(0, 0, 0, 0);
@@ -695,6 +707,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     const int r0 = quarter * 32;  // its keys of a tile
     const VOffsets<D> vo(r0, g, t);
     State<D, NT> st;
+    uint32_t ends = 0;
     Ring ring;
     for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
       const int s = ring.s;
@@ -711,72 +724,74 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         mbar_arrive_warp(&empty[s]);
       }
       if (!(td.flags & kEnd)) continue;
-      // ---- the warps' parts meet in shared memory, half of the heads at a time
-      const int hk = td.hg / a.chunks, g0 = (td.hg % a.chunks) * C::kHeads;
+      // ---- the warps' parts meet in shared memory, a head per warp at a time.  (An area
+      // for all heads costs a stage of the ring: 2 us more at 8 x 131072 tokens, but half
+      // of the barriers at a segment's end: 46 -> 39 us at 256 x 512.  A seventh warp that
+      // joins while the others go on leaves 80 registers a thread: 140 us.)
+      if (ends > 0 && !mbar_wait_warp(&meet[1], (ends - 1) & 1, abort)) break;
+      const int hk = td.hg / a.chunks, g0 = (td.hg - hk * a.chunks) * C::kHeads;
       const int heads = min(C::kHeads, a.G - g0);
-      bool met = true;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int h = 0; h < 2; ++h) {
+          const int head = nt * 8 + 2 * t + h;
+          float l = st.l[nt][h];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int head = nt * 8 + 2 * t + h;
-            if (half == 0) {
-              float l = st.l[nt][h];
+          for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
+          if (g == 0) ml[warp * C::kHeads + head] = make_float2(st.m[nt][h], l);
+          float* row = join + (warp * C::kHeads + head) * C::kRow + 2 * g;
 #pragma unroll
-              for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, off);
-              if (g == 0) ml[warp * C::kHeads + head] = make_float2(st.m[nt][h], l);
-            }
-            if (head / C::kHalf != half) continue;
-            float* row = join + (warp * C::kHalf + head % C::kHalf) * C::kRow + 2 * g;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-              *reinterpret_cast<float2*>(row + 16 * i) =
-                  make_float2(st.o[nt][i][h], st.o[nt][i][2 + h]);
-          }
+          for (int i = 0; i < D / 16; ++i)
+            *reinterpret_cast<float2*>(row + 16 * i) =
+                make_float2(st.o[nt][i][h], st.o[nt][i][2 + h]);
         }
-        mbar_arrive_warp(&meet[0]);
-        if (!(met = mbar_wait_warp(&meet[0], half, abort))) break;
-        for (int x = tid; x < C::kHalf * (D / 2); x += kWarps * 32) {
-          const int hrow = x / (D / 2), head = half * C::kHalf + hrow, pos = 2 * (x % (D / 2));
-          if (head >= heads) break;
-          float mx = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
+      }
+      mbar_arrive_warp(&meet[0]);
+      if (!mbar_wait_warp(&meet[0], ends & 1, abort)) break;
+      ++ends;
+      for (int head = warp; head < heads; head += kWarps) {
+        float c[kWarps], mx = -INFINITY, l = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ml[w * C::kHeads + head].x);
-          const float ref = fmaxf(mx, -3.4e38f);
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ml[w * C::kHeads + head].x);
+        const float ref = fmaxf(mx, -3.4e38f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 v = ml[w * C::kHeads + head];
+          c[w] = ex2_f32(v.x - ref);
+          l = fmaf(v.y, c[w], l);
+        }
+        const int64_t row = static_cast<int64_t>(td.b) * a.H + hk * a.G + g0 + head;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        float* part = a.parts + static_cast<int64_t>(max(td.slot, 0)) * part_floats(D, C::kHeads);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) {
+          const int pos = 2 * lane + 64 * x;
+          float o0 = 0.f, o1 = 0.f;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float2 v = ml[w * C::kHeads + head];
-            const float c = ex2_f32(v.x - ref);
             const float2 ov = *reinterpret_cast<const float2*>(
-                join + (w * C::kHalf + hrow) * C::kRow + pos);
-            l = fmaf(v.y, c, l);
-            o0 = fmaf(ov.x, c, o0);
-            o1 = fmaf(ov.y, c, o1);
+                join + (w * C::kHeads + head) * C::kRow + pos);
+            o0 = fmaf(ov.x, c[w], o0);
+            o1 = fmaf(ov.y, c[w], o1);
           }
-          if (td.slot < 0) {
-            const int64_t row = static_cast<int64_t>(td.b) * a.H + hk * a.G + g0 + head;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+          if (td.slot < 0)
             *reinterpret_cast<__nv_bfloat162*>(a.o + row * D + element_of<D>(pos)) =
                 __floats2bfloat162_rn(o0 * inv, o1 * inv);
-            if (pos == 0 && a.lse != nullptr)
-              a.lse[row] = l > 0.f ? (mx + log2f(l)) * kLn2 : -INFINITY;
-          } else {
-            float* part = a.parts + static_cast<int64_t>(td.slot) * part_floats(D, C::kHeads);
-            if (pos == 0) {
-              part[2 * head] = mx;
-              part[2 * head + 1] = l;
-            }
+          else
             *reinterpret_cast<float2*>(part + 2 * C::kHeads + head * D + pos) = make_float2(o0, o1);
-          }
         }
-        mbar_arrive_warp(&meet[1]);
-        if (!(met = mbar_wait_warp(&meet[1], half, abort))) break;
+        if (lane == 0) {
+          if (td.slot >= 0)
+            *reinterpret_cast<float2*>(part + 2 * head) = make_float2(mx, l);
+          else if (a.lse != nullptr)
+            a.lse[row] = l > 0.f ? (mx + log2f(l)) * kLn2 : -INFINITY;
+        }
       }
-      if (!met) break;
+      mbar_arrive_warp(&meet[1]);
     }
   }
+
   tc_fence_before();
   __syncthreads();
   report_abort(abort, a.err);
@@ -786,20 +801,24 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   }
 }
 
-// Joins the parts of the segments that cross runs, in run order.  Block (c, y): the
-// segment that begins in run c and goes on, heads [y, y + 1) kHeads / gridDim.y.
-// Sixteen or 32 lanes of four stored positions take one head; where fewer heads than
-// lane groups are left, the groups share the parts and meet in shared memory.
-template <int D, int NT>
-__global__ void __launch_bounds__(256) join_kernel(const DecodeArgs a) {
-  constexpr int kHeads = 8 * NT, kLanes = D / 4, kGroups = 256 / kLanes;
+// Joins the parts of the segments that cross runs, in run order.  Block (c, y): entry c
+// of what crosses runs, heads [y, y + 1) kHeads / gridDim.y.  Sixteen or 32 lanes of
+// four stored positions take one head; where fewer heads than lane groups are left,
+// the groups share the parts and meet in shared memory.
+template <int D, int NT, int kThreads>
+__global__ void __launch_bounds__(kThreads) join_kernel(const DecodeArgs a) {
+  constexpr int kHeads = 8 * NT, kLanes = D / 4, kGroups = kThreads / kLanes;
   constexpr int kFloats = part_floats(D, kHeads);
   __shared__ float4 red[kGroups][kLanes];
   __shared__ float2 red_ml[kGroups];
   pdl_trigger();
   pdl_wait();
-  const RunInfo r = a.runs[blockIdx.x];
-  if (r.last < 0) return;
+  const RunInfo r = a.split[blockIdx.x];
+  // last < 0: nothing to join; what else is out of range was never written, by a
+  // kernel that gave up a wait and has reported it
+  if (r.run < 0 || r.last < r.run || r.last >= a.runs || r.slot < 0 || r.slot >= 2 * a.runs ||
+      r.b < 0 || r.b >= a.B || r.hg < 0 || r.hg >= a.Hkv * a.chunks)
+    return;
   const int per = kHeads / gridDim.y;  // heads of this block
   const int share = max(1, kGroups / per);
   const int x = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
@@ -809,13 +828,13 @@ __global__ void __launch_bounds__(256) join_kernel(const DecodeArgs a) {
     float mx = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     // eight parts' loads in flight: one after another they cost a memory latency each
-    for (int c0 = static_cast<int>(blockIdx.x) + sub; c0 <= r.last; c0 += 8 * share) {
+    for (int c0 = r.run + sub; c0 <= r.last; c0 += 8 * share) {
       float2 pml[8];
       float4 po[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int c = min(c0 + i * share, r.last);
-        const int slot = c == static_cast<int>(blockIdx.x) ? r.slot : 2 * c;
+        const int slot = c == r.run ? r.slot : 2 * c;
         const float* part = a.parts + static_cast<int64_t>(slot) * kFloats;
         pml[i] = *reinterpret_cast<const float2*>(part + 2 * head);
         po[i] = *reinterpret_cast<const float4*>(part + 2 * kHeads + head * D + 4 * x);
@@ -874,20 +893,27 @@ nvq_status check_decode(int B, int H, int Hkv, int D, int max_pages) {
 // CTAs and runs, query heads per run and the workspace: what goes on from each run,
 // then two parts per run.
 struct Plan {
-  int nt, chunks, ctas, runs, join_y;
+  int nt, chunks, ctas, runs, by_segment, join_x, join_y, join_threads;
   size_t parts, total;
 };
 
 Plan plan(int B, int H, int Hkv, int D, int max_pages) {
   Plan p;
   const int G = H / Hkv;
-  p.nt = G > 8 ? 2 : 1;  // 8 or 16 columns: K~ and V~ are decoded once for both
+  p.nt = G > 8 ? 2 : 1;  // 8 or 16 columns: V~ is decoded once for both
   p.chunks = (G + 8 * p.nt - 1) / (8 * p.nt);
-  const int64_t most = static_cast<int64_t>(B) * Hkv * p.chunks * max_pages;
-  p.ctas = static_cast<int>(std::min<int64_t>(most, device_sms()));
+  const int64_t segments = static_cast<int64_t>(B) * Hkv * p.chunks;
+  p.ctas = static_cast<int>(std::min<int64_t>(segments * max_pages, device_sms()));
   p.runs = p.ctas * (p.nt == 1 ? 3 : 2);
-  // few segments: each has many parts, whose heads then get blocks of their own
-  p.join_y = static_cast<int64_t>(B) * Hkv * p.chunks * 8 >= p.runs ? 1 : 8 * p.nt;
+  // Fewer segments than runs: entries by segment, so the join has no idle blocks.
+  p.by_segment = segments <= p.runs;
+  p.join_x = p.by_segment ? static_cast<int>(segments) : p.runs;
+  // Segments of more than two parts, as they fall on average, get a block per query
+  // head, whose thread groups share the parts (64 sequences of up to 32768 tokens, 16
+  // heads on one KV head: 49 us in all, 54 with one block per segment), and one of 1024
+  // threads above 64 parts (one sequence of 131072 tokens: 23 us, 28 with 256).
+  p.join_y = p.runs > 2 * segments ? 8 * p.nt : 1;
+  p.join_threads = p.runs > 64 * segments ? 1024 : 256;
   p.parts = (static_cast<size_t>(p.runs) * sizeof(RunInfo) + 255) / 256 * 256;
   p.total = p.parts + static_cast<size_t>(2 * p.runs) * part_floats(D, 8 * p.nt) * 4;
   return p;
@@ -903,7 +929,10 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tk32, const 
   if ((e = launch_pdl(decode_kernel<D, NT>, dim3(p.ctas), dim3(C::kThreads), C::kSmem, stream, 1, tk,
                       tk32, a)) != cudaSuccess)
     return e;
-  return launch_pdl(join_kernel<D, NT>, dim3(p.runs, p.join_y), dim3(256), 0, stream, 1, a);
+  const dim3 grid(p.join_x, p.join_y);
+  if (p.join_threads == 1024)
+    return launch_pdl(join_kernel<D, NT, 1024>, grid, dim3(1024), 0, stream, 1, a);
+  return launch_pdl(join_kernel<D, NT, 256>, grid, dim3(256), 0, stream, 1, a);
 }
 
 }  // namespace
@@ -947,7 +976,8 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
   const DecodeArgs a{static_cast<const uint16_t*>(q), ld_q, static_cast<const uint8_t*>(pool),
                      num_pages, page_table, ld_table, max_pages, seq_lens, B, H, Hkv, H / Hkv,
                      p.chunks, scale * kLog2e, window, sinks, static_cast<__nv_bfloat16*>(o), lse,
-                     reinterpret_cast<RunInfo*>(wb), reinterpret_cast<float*>(wb + p.parts), err};
+                     reinterpret_cast<RunInfo*>(wb), p.by_segment,
+                     reinterpret_cast<float*>(wb + p.parts), p.runs, err};
   const cudaError_t e = timed(NVQ_KERNEL_ATTN_FWD, stream, [&] {
     if (D == 128)
       return p.nt == 1 ? launch_decode<128, 1>(tk, tk32, a, p, stream)

@@ -7,14 +7,18 @@
 // x are the narrow side (M rounded up to 16 columns).
 //
 // Work split.  Units are (128-row tile of w, 256-element stage of K).
-//   Up to one tile per SM: 1, 2, 4 or 8 CTAs share a tile, each a range of K, as one
-//   cluster; they leave their sums in the first one's shared memory, which adds them
-//   in order.  (Through the workspace, as below, the same sum costs 3 us more: 7.8
-//   against 4.7 us for 1 x 4608 x 1536.)
+//   Up to one tile per SM: 1 to 8 CTAs share a tile, each a range of K, as one cluster;
+//   they leave their sums in the first one's shared memory, which adds them in order.
+//   (Through the workspace, as below, the same sum costs 2 us more: 7.8 against 5.9 us
+//   for 1 x 4608 x 1536.)
 //   More tiles: the line of units is cut into equal runs, one CTA each, so that every
 //   SM streams the same bytes.  A tile that crosses runs leaves fp32 parts in the
 //   workspace; whichever warp arrives last at the tile's ticket adds the parts in run
 //   order (the sum does not depend on who that is).
+//
+// Measured (calls in a CUDA graph): 32 x 28672 x 8192 31 us, 65% of the copy rate; 1 x
+// 1536 x 8960 8 us and 1 x 4608 x 1536 6 us, the latency of two dependent launches and of
+// the first loads.
 //
 // Two launches: x is quantized (and the tickets cleared) by a small kernel, while the
 // main kernel, launched behind it programmatically, already fills its ring with
@@ -35,7 +39,7 @@ namespace {
 
 constexpr int kThreads = 192;  // producer, MMA, 4 epilogue warps
 constexpr int kSteps = 4;      // MMA steps (64 elements) per stage
-constexpr int kStages = 6;      // of the ring (9: 1 us slower at 32 x 28672 x 8192)
+constexpr int kStages = 6;     // of the ring (8: 1 us slower at 32 x 28672 x 8192)
 // bytes of a stage: w codes, w scales, x scales
 constexpr uint32_t kW = 128 * 128, kSc = kSteps * 512, kXs = 1024;
 constexpr uint32_t kScCol = 128;  // tensor memory: two accumulators of 64 columns, then scales
@@ -127,8 +131,8 @@ __device__ __forceinline__ void issue_stage(uint32_t d, uint32_t idesc, uint32_t
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%23];\n\t}" ::"r"(d),
       "r"(idesc), "r"(acc), "l"(wd), "l"(wd + 32), "l"(wd + 64), "l"(wd + 96), "l"(xd),
       "l"(xd + 32), "l"(a), "l"(b), "r"(w_col), "r"(w_col + 4), "r"(w_col + 8), "r"(w_col + 12),
-      "r"(x_col), "r"(x_col + 2), "r"(x_col + 4), "r"(x_col + 6), "l"(a + 2), "l"(b + 2), "l"(a + 4), "l"(b + 4), "r"(smem_u32(bar)),
-      "l"(a + 6), "l"(b + 6)
+      "r"(x_col), "r"(x_col + 2), "r"(x_col + 4), "r"(x_col + 6), "l"(a + 2), "l"(b + 2),
+      "l"(a + 4), "l"(b + 4), "r"(smem_u32(bar)), "l"(a + 6), "l"(b + 6)
       : "memory");
 }
 
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kThreads)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 4);
     }
-    if (kClusters) mbar_init(&sums_full, 4 * (p.split - 1));
+    if (kClusters) mbar_init(&sums_full, max(4 * (p.split - 1), 1));
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -458,12 +462,19 @@ SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
   p.k_stages = static_cast<int>((K + 255) / 256);
   const int sms = device_sms();
   if (p.tiles <= sms) {
-    // as many CTAs a tile as there are SMs and stages of K for, at most 24 KB of sums
-    // (56 KB at 8, where few clusters run); 8 only where two per 16 SMs are enough
+    // As many CTAs a tile as there are SMs and stages of K for (not only powers of two:
+    // three at 1 x 5120 x 13824 take 14 us, two 19).  The sums are at most 112 KB, and 56
+    // KB where the clusters need two CTAs per SM: those of more than 128 SMs' worth, of
+    // which the chip's groups of SMs do not hold all at once with one CTA per SM (64 x
+    // 4864 x 8192 in four, one per SM: 21 us, in two: 13).  Of 7 and 8 a group holds two,
+    // 16 in all (32 x 2304 x 4096, 18 tiles: 15 us in seven, 8.3 in four).
     p.split = 1;
-    while (p.split < 8 && 2 * p.split * p.tiles <= sms && 2 * p.split <= p.k_stages &&
-           (2 * p.split - 1) * p.cols <= 16 * 7 && (p.split < 4 || p.tiles <= 16))
-      p.split *= 2;
+    for (int x = 2; x <= 8 && x <= p.k_stages; ++x) {
+      const int ctas = x * p.tiles, sum_rows = (x - 1) * p.cols;
+      if (ctas <= 128 ? sum_rows <= 224 && (x < 7 || p.tiles <= 16)
+                      : ctas <= sms && sum_rows <= 112 && x <= 4)
+        p.split = x;
+    }
     p.runs = p.split * p.tiles;
   } else {
     p.runs = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.tiles) * p.k_stages, sms));
@@ -528,13 +539,14 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
     if (e != cudaSuccess) return e;
     return launch_pdl(linear_small_kernel<false>, dim3(q.runs), dim3(kThreads), smem, stream, 1, tx, tw, a);
   }
-  // At most four stages and 112 KB: two CTAs fit an SM, so that clusters find room in
-  // every group of SMs.  At least 78 KB: no three do, whose 256 tensor-memory columns
+  // At most four stages and, with small sums, 112 KB: two CTAs fit an SM, so that
+  // clusters find room in every group of SMs.  At least 78 KB: no three do, whose 256 tensor-memory columns
   // each would not fit, so that no CTA waits for columns that a cluster holds which in
   // its turn waits for that CTA's cluster.
   const size_t sums = static_cast<size_t>(q.split - 1) * q.cols * 512;
   a.stages = std::min(4, (q.k_stages + q.split - 1) / q.split);
-  if (q.split < 8) a.stages = std::min<int>(a.stages, (112 * 1024 - 1024 - sums) / stage);
+  const size_t room = (sums <= 56 * 1024 ? 112 : 222) * 1024;
+  a.stages = std::min<int>(a.stages, (room - 1024 - sums) / stage);
   smem = std::max<size_t>(a.stages * stage + sums + 1024, 78 * 1024);
   e = cudaFuncSetAttribute(linear_small_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            226 * 1024);

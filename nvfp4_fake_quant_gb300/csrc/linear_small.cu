@@ -16,7 +16,7 @@
 //   workspace; whichever warp arrives last at the tile's ticket adds the parts in run
 //   order (the sum does not depend on who that is).
 //
-// Measured (calls in a CUDA graph): 32 x 28672 x 8192 31 us, 65% of the copy rate; 1 x
+// Measured (calls in a CUDA graph): 32 x 28672 x 8192 29 us, 70% of the copy rate; 1 x
 // 1536 x 8960 8 us and 1 x 4608 x 1536 6 us, the latency of two dependent launches and of
 // the first loads.
 //
@@ -102,6 +102,24 @@ __device__ __forceinline__ int run_of(const SmallArgs& p, int u) {
   const int64_t units = static_cast<int64_t>(p.tiles) * p.k_stages;
   return static_cast<int>((static_cast<int64_t>(u + 1) * p.runs + units - 1) / units - 1);
 }
+
+// Place of a unit in the line (tile, stage of K) and in the ring (stage, parity).
+struct Place {
+  int tile, ks, s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ Place(const SmallArgs& p, int u)
+      : tile(u / p.k_stages), ks(u - tile * p.k_stages) {}
+  __device__ __forceinline__ void next(const SmallArgs& p) {
+    if (++ks == p.k_stages) {
+      ks = 0;
+      ++tile;
+    }
+    if (++s == p.stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
 
 // One whole stage from one elected lane: the copies of its scales, four MMAs, the
 // commit.  wd, xd: descriptors of the scale blocks; a, b: of the codes; w_col, x_col:
@@ -218,49 +236,52 @@ __global__ void __launch_bounds__(kThreads)
     // ------------------------------------------------------------ producer
     tma_prefetch_desc(&tx);
     tma_prefetch_desc(&tw);
-    bool ok = true;
-    int issued = 0;
-    auto load_w = [&](int i) {
-      const int u = u0 + i, s = i % p.stages, tile = u / p.k_stages, ks = u - tile * p.k_stages;
-      const int ns = min(kSteps, p.k_steps - ks * kSteps);
-      uint8_t* st = smem + s * stage_bytes;
-      mbar_arrive_expect_tx_w(&full[s], kW + x_bytes + kXs + static_cast<uint32_t>(ns) * 512u);
-      tma_load_4d_w(st, &tw, ks * 128, tile * 128, 0, 0, &full[s]);
+    // Places are counted on, not divided out: a warp alone waits 0.2 us for a division
+    // on its own, and five in a stage held the loads back (1 x 14336 x 16384: 37 us, 29
+    // without them).
+    auto load_w = [&](const Place& at) {
+      const int ns = min(kSteps, p.k_steps - at.ks * kSteps);
+      uint8_t* st = smem + at.s * stage_bytes;
+      mbar_arrive_expect_tx_w(&full[at.s], kW + x_bytes + kXs + static_cast<uint32_t>(ns) * 512u);
+      tma_load_4d_w(st, &tw, at.ks * 128, at.tile * 128, 0, 0, &full[at.s]);
       bulk_load_w(st + kW + x_bytes,
-                  p.sw + (static_cast<int64_t>(tile) * p.k_steps + ks * kSteps) * 512, ns * 512,
-                  &full[s]);
-      issued = i + 1;
+                  p.sw + (static_cast<int64_t>(at.tile) * p.k_steps + at.ks * kSteps) * 512,
+                  ns * 512, &full[at.s]);
     };
-    auto load_x = [&](int i) {
-      const int s = i % p.stages, ks = (u0 + i) % p.k_stages;
-      uint8_t* st = smem + s * stage_bytes;
-      tma_load_4d_w(st + kW, &tx, ks * 128, 0, 0, 0, &full[s]);
-      bulk_load_w(st + kW + x_bytes + kSc, p.sx + static_cast<int64_t>(ks) * kXs, kXs, &full[s]);
+    auto load_x = [&](const Place& at) {
+      uint8_t* st = smem + at.s * stage_bytes;
+      tma_load_4d_w(st + kW, &tx, at.ks * 128, 0, 0, 0, &full[at.s]);
+      bulk_load_w(st + kW + x_bytes + kSc, p.sx + static_cast<int64_t>(at.ks) * kXs, kXs,
+                  &full[at.s]);
     };
     const int head = min(count, p.stages);
-    for (int i = 0; i < head; ++i) load_w(i);
+    Place at(p, u0), at_x(p, u0);
+    for (int i = 0; i < head; ++i, at.next(p)) load_w(at);
     pdl_wait();  // x~
-    for (int i = 0; i < head; ++i) load_x(i);
-    for (int i = head; i < count; ++i) {
-      if (!(ok = mbar_wait_warp(&empty[i % p.stages], ((i / p.stages) & 1) ^ 1, abort))) break;
-      load_w(i);
-      load_x(i);
+    for (int i = 0; i < head; ++i, at_x.next(p)) load_x(at_x);
+    int i = head;
+    bool ok = true;
+    for (; i < count; ++i, at.next(p)) {
+      if (!(ok = mbar_wait_warp(&empty[at.s], at.phase ^ 1, abort))) break;
+      load_w(at);
+      load_x(at);
     }
     if (!ok) {  // let the copies already issued land before the block leaves
-      for (int i = max(0, issued - p.stages); i < issued; ++i)
-        mbar_wait_warp(&full[i % p.stages], (i / p.stages) & 1, nullptr, 10000000ull);
+      for (int k = max(0, i - p.stages); k < i; ++k)
+        mbar_wait_warp(&full[k % p.stages], (k / p.stages) & 1, nullptr, 10000000ull);
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------------- MMA
     const uint32_t idesc = idesc_mxf4nvf4(128, 0) | (static_cast<uint32_t>(p.cols >> 3) << 17);
     int part = 0, i = 0;
-    for (; i < count; ++i) {
-      const int u = u0 + i, s = i % p.stages, ks = u % p.k_stages;
+    Place at(p, u0);
+    for (; i < count; ++i, at.next(p)) {
+      const int s = at.s, ks = at.ks;
       const int ns = min(kSteps, p.k_steps - ks * kSteps);
       const bool first = i == 0 || ks == 0;
       const uint32_t d = tmem + 64 * (part & 1);
       if (first && !mbar_wait_warp(&acc_empty[part & 1], ((part >> 1) & 1) ^ 1, abort)) break;
-      if (!mbar_wait_warp(&full[s], (i / p.stages) & 1, abort)) break;
+      if (!mbar_wait_warp(&full[s], at.phase, abort)) break;
       tc_fence_after();
       const uint32_t a = smem_u32(smem + s * stage_bytes), b = a + kW, sa = b + x_bytes, sb = sa + kSc;
       const uint32_t col = tmem + kScCol + 32 * s;

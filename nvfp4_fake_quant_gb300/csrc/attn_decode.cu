@@ -39,8 +39,8 @@
 // cross-lane maximum and the rescaling of O leave the common path.
 //
 // Measured (calls in a CUDA graph): 8 x up to 131072 tokens, 64 heads on 8 of 128:
-// 118 us, 86% of the copy rate in bytes of the cache; 64 sequences of up to 8192, 32
-// heads on 8: 64 us, 68%; one sequence of 777 tokens: 10 us, the latency of two
+// 117 us, 87% of the copy rate in bytes of the cache; 64 sequences of up to 8192, 32
+// heads on 8: 63 us, 69%; one sequence of 777 tokens: 10 us, the latency of two
 // launches, the scan and a tile.  Short segments cost most: each begins with a
 // quantization of q and ends with two barriers of its four warps.
 #include <algorithm>
@@ -117,6 +117,7 @@ struct DecodeArgs {
   int by_segment;         // 1: entries by segment (there are fewer than runs)
   float* parts;           // [2 runs] parts (workspace)
   int runs;               // of the grid
+  uint64_t runs_magic;    // 2^64 / runs, rounded up
   int* err;
 };
 
@@ -128,11 +129,31 @@ struct RunInfo {
 // Floats of one part: m (log2 units) and l per head, then the sums [heads][D].
 __host__ __device__ constexpr int part_floats(int D, int heads) { return heads * (D + 2); }
 
-// The line of `all` tiles is cut into this many runs; run c is [all c / runs,
-// all (c + 1) / runs).  No run is empty.
-__device__ __forceinline__ int runs_of(int64_t all, int ctas) {
-  return static_cast<int>(all < ctas ? all : ctas);
-}
+// The line of `all` tiles is cut into n = min(all, runs) runs: run c is [all c / n,
+// all (c + 1) / n), never empty; of the grid's runs those from n on have nothing.
+// all c / n = (all / n) c + (all % n) c / n.  n is the grid's or all itself, so there is
+// nothing to divide: the host gives 2^64 / runs, rounded up (all < 2^55 and runs <= 2^9
+// keep the product's error below 1 / runs).
+struct Runs {
+  int64_t all, per;
+  int n, rest;
+  uint32_t magic;
+  __device__ __forceinline__ Runs(int64_t all_, int runs, uint64_t magic_) : all(all_) {
+    if (all < runs) {
+      n = static_cast<int>(all);
+      per = 1;
+      rest = 0;
+    } else {
+      n = runs;
+      per = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(all), magic_));
+      rest = static_cast<int>(all - per * runs);
+    }
+    magic = static_cast<uint32_t>(magic_ >> 32) + 1;  // rest c < 2^24: exact as well
+  }
+  __device__ __forceinline__ int64_t begin(int c) const {
+    return c < n ? per * c + __umulhi(static_cast<uint32_t>(rest * c), magic) : all;
+  }
+};
 
 // The tiles of a sequence: pages [0, sink_pages) and [first, pages).
 struct Extent {
@@ -151,6 +172,11 @@ __device__ __forceinline__ Extent extent(const DecodeArgs& a, int b, bool* over)
   e.sink_pages = e.wstart > 0 ? min((min(a.sinks, e.len) + kPage - 1) / kPage, e.first) : 0;
   e.tiles = pages - e.first + e.sink_pages;
   return e;
+}
+
+// The KV head of a head group (a division only where there are several per KV head).
+__device__ __forceinline__ int kv_head(const DecodeArgs& a, int hg) {
+  return a.chunks == 1 ? hg : hg / a.chunks;
 }
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -503,16 +529,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     total += warp_sum[w];
   }
   const int64_t before = scan - mine;  // tiles (of one head group) before this thread's sequences
-  const int64_t all = total * hgs;
-  const int ctas = static_cast<int>(gridDim.x), runs = runs_of(all, C::kRuns * ctas);
   // consecutive runs lie on different SMs: a few tiles spread over all of them
-  // (all r / runs = (all / runs) r + (all % runs) r / runs, the second part in 32 bits)
-  const int64_t per_run = runs > 0 ? (all <= 0x7FFFFFFF ? static_cast<int>(all) / runs : all / runs) : 0;
-  const int rest = static_cast<int>(all - per_run * runs);
-  auto begin_of = [&](int r) { return r < runs ? per_run * r + rest * r / runs : all; };
-  for (int i = 0; i < C::kRuns; ++i) {
-    const int64_t u = begin_of(i * ctas + static_cast<int>(blockIdx.x));
-    if (u < all && before * hgs <= u && u < (before + mine) * hgs) {
+  const int ctas = static_cast<int>(gridDim.x);
+  const Runs line(total * hgs, a.runs, a.runs_magic);
+  for (int i = 0; i < C::kRuns && mine > 0; ++i) {
+    const int64_t u = line.begin(i * ctas + static_cast<int>(blockIdx.x));
+    if (u < line.all && before * hgs <= u && u < (before + mine) * hgs) {
       int64_t at = before;
       int b = b_lo;
       for (;; ++b) {
@@ -530,7 +552,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot + sub * C::kCols;
   const int run = sub * ctas + static_cast<int>(blockIdx.x);
-  const int64_t u0 = begin_of(run), u1 = begin_of(run + 1);
+  const int64_t u0 = line.begin(run), u1 = line.begin(run + 1);
   const int n_tiles = static_cast<int>(u1 - u0);
   if (!a.by_segment && warp == kProducer && lane == 0) a.split[run].last = -1;
 
@@ -541,8 +563,15 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
     Extent e = extent(a, b, &over);
     int64_t seg0 = start_before[sub] * hgs;  // line position of the sequence's first tile
     const int64_t into = u0 - seg0;
-    int hg = into <= 0x7FFFFFFF ? static_cast<int>(into) / e.tiles
-                                : static_cast<int>(into / e.tiles);
+    int hg;  // into / tiles, below 2^16
+    if (into < (int64_t{1} << 23)) {  // the float quotient is off by less than 1
+      const int n = static_cast<int>(into);
+      hg = static_cast<int>(__fdividef(static_cast<float>(n), static_cast<float>(e.tiles)));
+      if (static_cast<int64_t>(hg) * e.tiles > n) --hg;
+      if (static_cast<int64_t>(hg + 1) * e.tiles <= n) ++hg;
+    } else {
+      hg = static_cast<int>(into / e.tiles);
+    }
     int i = static_cast<int>(into - static_cast<int64_t>(hg) * e.tiles);
     int n = 0;
     Ring ring;
@@ -559,17 +588,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       td.b = b;
       td.hg = hg;
       td.slot = whole ? -1 : 2 * run + (first > u0 ? 1 : 0);
-      if (lane == 0 && first >= u0) {
-        RunInfo* info = a.split + (a.by_segment ? b * hgs + hg : run);
-        if (first + e.tiles > u1) {
-          // the run that holds tile u: the last c with all c / runs <= u
-          const int64_t u = first + e.tiles - 1;
-          *info = {b, hg, run, td.slot, static_cast<int>(((u + 1) * runs + all - 1) / all - 1)};
-        } else if (a.by_segment) {
-          info->last = -1;
-        }
-      }
-      const int hk = hg / a.chunks, g0 = (hg - hk * a.chunks) * C::kHeads;
+      const int hk = kv_head(a, hg), g0 = (hg - hk * a.chunks) * C::kHeads;
       const uint8_t* q = reinterpret_cast<const uint8_t*>(
           a.q + b * a.ld_q + static_cast<int64_t>(hk * a.G + g0) * D);
       uint32_t q_bytes = min(C::kHeads, a.G - g0) * (D * 2);  // with the first tile
@@ -621,6 +640,17 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
         if (q_bytes > 0) bulk_load_w(dst + C::kRec, q, q_bytes, &full[s]);
         q_bytes = 0;
       }
+      if (lane == 0 && first >= u0) {  // with the loads on their way
+        RunInfo* info = a.split + (a.by_segment ? b * hgs + hg : run);
+        if (first + e.tiles > u1) {
+          // the run that holds tile u: the last c with all c / n <= u
+          const int64_t u = first + e.tiles - 1;
+          *info = {b, hg, run, td.slot,
+                   static_cast<int>(((u + 1) * line.n + line.all - 1) / line.all - 1)};
+        } else if (a.by_segment) {
+          info->last = -1;
+        }
+      }
       if (n == n_tiles || !ok) break;
       i = 0;
       if (++hg == hgs) {
@@ -664,7 +694,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       if (td.flags & kStart) {
         const int qb = seg & 1;
         if (!(ok = mbar_wait_warp(&q_free[qb], ((seg >> 1) & 1) ^ 1, abort))) break;
-        const int g0 = td.hg % a.chunks * C::kHeads;
+        const int g0 = (td.hg - kv_head(a, td.hg) * a.chunks) * C::kHeads;
         quantize_q<D, NT>(stage + C::kRec, min(C::kHeads, a.G - g0), smem + C::kQCodes + qb * 1024,
                           smem + C::kQScales + qb * 1024, lane);
         ++seg;
@@ -729,7 +759,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
       // of the barriers at a segment's end: 46 -> 39 us at 256 x 512.  A seventh warp that
       // joins while the others go on leaves 80 registers a thread: 140 us.)
       if (ends > 0 && !mbar_wait_warp(&meet[1], (ends - 1) & 1, abort)) break;
-      const int hk = td.hg / a.chunks, g0 = (td.hg - hk * a.chunks) * C::kHeads;
+      const int hk = kv_head(a, td.hg), g0 = (td.hg - hk * a.chunks) * C::kHeads;
       const int heads = min(C::kHeads, a.G - g0);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -977,7 +1007,8 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
                      num_pages, page_table, ld_table, max_pages, seq_lens, B, H, Hkv, H / Hkv,
                      p.chunks, scale * kLog2e, window, sinks, static_cast<__nv_bfloat16*>(o), lse,
                      reinterpret_cast<RunInfo*>(wb), p.by_segment,
-                     reinterpret_cast<float*>(wb + p.parts), p.runs, err};
+                     reinterpret_cast<float*>(wb + p.parts), p.runs,
+                     ~uint64_t{0} / p.runs + 1, err};
   const cudaError_t e = timed(NVQ_KERNEL_ATTN_FWD, stream, [&] {
     if (D == 128)
       return p.nt == 1 ? launch_decode<128, 1>(tk, tk32, a, p, stream)

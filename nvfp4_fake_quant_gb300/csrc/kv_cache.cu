@@ -6,11 +6,16 @@
 // are one contiguous run for whoever copies pages.
 //
 // Append: per token and head, D/16 blocks of K and of V are read (32 bytes each)
-// and written as 8 code bytes and one scale byte.  A block of threads takes 16
-// tokens; consecutive lanes take the blocks of one token's row, then the next
-// token, so that a prompt's writes of one head are contiguous runs of 1 KB
-// (codes) and its reads whole head rows.  Bound by HBM: reads 4 D, writes 9 D / 8
-// bytes per token and head.
+// and written as 8 code bytes and one scale byte.  A block of threads takes 8 tokens
+// and walks over the heads; consecutive lanes take the blocks of one token's row, then
+// the next token, so that a prompt's reads are whole head rows and its writes of one
+// head contiguous runs of 8 D / 2 bytes.  (16 tokens in 256 threads: 1 us more; the
+// smaller block leaves more of them to hide the loads.)  Where tokens are few their
+// heads are spread over more blocks instead, so that a decode step fills the chip.
+//
+// Bound by HBM: reads 4 D, writes 9 D / 8 bytes per token and head.  Measured (calls in
+// a CUDA graph): 25088 tokens of 12 heads of 128 37 us, 79% of the copy rate; 64 single
+// tokens 2.4 us, the latency of a launch and three dependent loads (length, page, row).
 #include <algorithm>
 #include <cstdint>
 

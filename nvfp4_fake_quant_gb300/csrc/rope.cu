@@ -11,6 +11,12 @@
 // a few operations per clock and SM).  F is formed once per block and pair, the
 // sine and cosine once per (token, pair) and shared by all heads through shared
 // memory; what is left is a copy of Q and K, bound by HBM.
+//
+// Measured (calls in a CUDA graph): 25088 tokens of 12 + 12 heads of 128, half layout,
+// 54 to 56 us, 82 to 85% of the copy rate (one axis, three axes); 32760 tokens of 24 +
+// 12 heads of 64, interleaved, 52 us, 86%; 64 tokens 3 us, the latency of a launch and
+// of the loads behind one another.  With few heads the sines are no longer shared by
+// enough of them: 25088 tokens of 1 + 1 heads take 16 us, 4 of them for the copy.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

@@ -6,17 +6,18 @@
 // The angle.  Only its fraction of a turn matters: with f = inv_freq / 2 pi
 // (turns per position, whole turns dropped) held as a 64-bit fixed-point
 // fraction F = rint(f 2^64), position * F modulo 2^64 IS the fraction of the
-// turn, exact but for F's own rounding.  fp32 products would be off by whole
+// turn, exact but for the roundings of f (fp64) and F.  fp32 products would be off by whole
 // radians at far positions, fp64 sines cost more than the copy (the FP64 rate is
 // a few operations per clock and SM).  F is formed once per block and pair, the
 // sine and cosine once per (token, pair) and shared by all heads through shared
 // memory; what is left is a copy of Q and K, bound by HBM.
 //
-// Measured (calls in a CUDA graph): 25088 tokens of 12 + 12 heads of 128, half layout,
-// 54 to 56 us, 82 to 85% of the copy rate (one axis, three axes); 32760 tokens of 24 +
-// 12 heads of 64, interleaved, 52 us, 86%; 64 tokens 3 us, the latency of a launch and
-// of the loads behind one another.  With few heads the sines are no longer shared by
-// enough of them: 25088 tokens of 1 + 1 heads take 16 us, 4 of them for the copy.
+// Measured (calls in a CUDA graph): 25088 tokens of 12 + 12 heads of 128 54 us (half
+// layout, one axis) and 56 us (interleaved, three axes), 85 and 81% of the copy rate;
+// 32760 tokens of 12 + 12 heads, half of each head rotated, 72 us, 82%; 64 tokens of 32 +
+// 8 heads 3 us, the latency of a launch and of the loads behind one another.  With few
+// heads the sines are no longer shared by enough of them: 25088 tokens of 1 + 1 heads
+// take 16 us, 4 of them for the copy.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

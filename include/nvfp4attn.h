@@ -509,7 +509,8 @@ nvq_status nvfp4_kv_append(const void* k, int64_t ld_k, const void* v, int64_t l
  * attn_qat_fwd: the last row of a causal forward).
  *   q     bf16 [B, H, D], row stride ld_q (elements, % 8 == 0, >= H*D);
  *         H % Hkv == 0, query head h reads KV head h / (H / Hkv)
- *   o     bf16 [B, H, D] contiguous; lse f32 [B, H] or NULL (written)
+ *   o     bf16 [B, H, D] contiguous, not overlapping q; lse f32 [B, H] or NULL
+ *         (written)
  *   S_j = scale * q~ . K~_j over the visible keys j of the sequence,
  *   lse = ln sum exp S_j,  o = sum exp(S_j - lse) V~_j
  * with q~ the NVFP4 fake quantization of q and the probabilities left

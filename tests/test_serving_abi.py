@@ -73,6 +73,16 @@ def test_decode_refusals(lib):
     assert lib.attn_qat_decode_workspace(2, 8, 2, 80, 4) == 0
 
 
+def test_decode_refuses_an_output_over_its_queries(lib):
+    def dec(q, o, ld_q=1024):
+        return lib.attn_qat_decode(q, ld_q, A, 8, A, 4, 4, A, 2, 8, 2, 128, 0.1, 0, 0, o, None, A,
+                                   BIG, None)
+    rows = 2 * 8 * 128 * 2  # bytes of q and of o
+    assert dec(A, A) == INVALID
+    assert dec(A, A + rows - 16) == INVALID and dec(A + rows - 16, A) == INVALID
+    assert dec(A, A + rows, ld_q=2048) == INVALID  # inside a strided q
+
+
 def test_packed_linear_refusals(lib):
     def lin(x=A, ld=128, c=A, s=A, wg=None, bias=None, m=2, n=32, k=128, xg=None, out=A, ws=A,
             ws_bytes=BIG):

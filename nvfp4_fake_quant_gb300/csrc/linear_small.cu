@@ -510,9 +510,11 @@ SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
 
 }  // namespace
 
-// N K / 256 units have to fit 31 bits (weights of up to 2^39 elements do).
+// The M K / 16 blocks of x and N K / 256 units have to fit 31 bits (weights of up to 2^39
+// elements do).
 bool linear_small_takes(int64_t M, int64_t N, int64_t K) {
   return M <= kLinearSmallRows && N <= (int64_t{1} << 30) && K <= (int64_t{1} << 30) &&
+         M * (K / 16) < (int64_t{1} << 31) - 128 &&
          (N + 127) / 128 * ((K + 255) / 256) < (int64_t{1} << 31) / 4 - 1;
 }
 

@@ -99,6 +99,15 @@ def test_packed_linear_refusals(lib):
     assert lib.nvfp4_linear_packed_workspace(2, 24, 128) == 0
 
 
+def test_packed_linear_leaves_x_past_31_bits_of_blocks_to_the_gemm(lib):
+    # 64 x 2^30 elements: 2^32 blocks, over the few-rows kernel's 32-bit index.  The GEMM's
+    # workspace holds x's codes and the scales of whole tiles of 128 rows
+    k = 1 << 30
+    assert lib.nvfp4_linear_packed_workspace(64, 16, k) >= 64 * k // 2 + 128 * k // 16
+    # 31 rows stay below: scales of 1 KB per 256 elements
+    assert lib.nvfp4_linear_packed_workspace(31, 16, k) == 31 * k // 2 + k // 256 * 1024 + 256
+
+
 def test_python_layer_refuses_host_tensors_and_bad_shapes():
     q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
     pos, f = torch.zeros(2, dtype=torch.int32), api.rope_inv_freq(64)[0]

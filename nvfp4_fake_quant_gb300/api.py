@@ -413,6 +413,17 @@ def _check_out(t, name, shape, dtype, like):
     return t
 
 
+def _moved_only(module, apply, fn, recurse):
+    """Module._apply for buffers whose types are part of their meaning: they follow the
+    module to a device, not to another type (model.to(bfloat16), model.half())."""
+    kept = dict(module._buffers)
+    apply(fn, recurse)
+    for name, t in kept.items():
+        if t is not None and module._buffers[name].dtype != t.dtype:
+            module._buffers[name] = t.to(module._buffers[name].device)
+    return module
+
+
 # ------------------------------------------------------- NVFP4 linear, packed weight
 
 def nvfp4_linear_packed_workspace(m: int, n: int, k: int) -> int:
@@ -474,6 +485,9 @@ class NVFP4PackedLinear(torch.nn.Module):
         self.register_buffer("scales", scales)
         self.register_buffer("bias", None if bias is None else bias.detach().clone())
         self.register_buffer("input_global_sf", input_global_sf)
+
+    def _apply(self, fn, recurse=True):
+        return _moved_only(self, super()._apply, fn, recurse)
 
     @torch.no_grad()
     def forward(self, x):
@@ -603,6 +617,9 @@ class Rotary(torch.nn.Module):
             raise ValueError(f"inv_freq must have {rot_dim // 2} entries")
         self.register_buffer("inv_freq", inv_freq, persistent=False)
         self.interleaved, self.axis_pairs = interleaved, axis_pairs
+
+    def _apply(self, fn, recurse=True):
+        return _moved_only(self, super()._apply, fn, recurse)
 
     def forward(self, q, k, positions):
         t = q.shape[:-2].numel()

@@ -71,6 +71,16 @@ def test_packed_module_is_the_training_layer_s_forward():
     assert bool(((a - b).abs().double() <= a.abs().double() * 2.0 ** -7 + 1e-6).all())
 
 
+def test_packed_module_keeps_its_types_when_the_model_changes_them():
+    torch.manual_seed(4)
+    packed = api.NVFP4Linear(128, 64, device="cuda").pack()
+    packed.input_global_sf = torch.tensor([200.0], device="cuda")
+    x = torch.randn(3, 128, device="cuda").to(BF16)
+    before = packed(x)
+    for change in (lambda m: m.to(BF16), lambda m: m.half(), lambda m: m.float()):
+        assert torch.equal(change(packed)(x), before)
+
+
 def test_packed_linear_unit_weight_scale_and_zero_input():
     w = workloads.random_matrix(64, 128, seed=4, scale=2.0)
     codes, scales = api.nvfp4_quantize_tiled(w.cuda())

@@ -128,3 +128,13 @@ def test_python_layer_refuses_host_tensors_and_bad_shapes():
     with pytest.raises(ValueError):
         api.nvfp4_kv_pool(2, 2, 96, device="cpu")
     assert api.nvfp4_kv_pool(2, 3, 64, device="cpu").shape == (2, 3, 9216)
+
+
+def test_rotary_keeps_its_frequencies_when_the_model_changes_type():
+    rot = api.Rotary(64)
+    f = rot.inv_freq.clone()
+    holder = torch.nn.Sequential(torch.nn.Linear(2, 2), rot)
+    for change in (lambda m: m.to(torch.bfloat16), lambda m: m.half(), lambda m: m.float()):
+        change(holder)
+        assert rot.inv_freq.dtype == torch.float64 and torch.equal(rot.inv_freq, f)
+    assert holder[0].weight.dtype == torch.float32

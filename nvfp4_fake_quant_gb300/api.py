@@ -392,7 +392,7 @@ def _rows_nd(x: torch.Tensor, name: str):
         t, h, d = x.shape
         row, s1, s2 = x.stride()
         if (s2 == 1 or d == 1) and (s1 == d or h == 1) or t * h * d == 0:
-            return t, h, d, row if t > 1 else max(h * d, row)
+            return t, h, d, row if t > 1 else h * d
     raise ValueError(f"{name} must be [tokens, heads, D] with contiguous heads")
 
 
@@ -411,6 +411,20 @@ def _check_out(t, name, shape, dtype, like):
     if tuple(t.shape) != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, of shape {shape}")
     return t
+
+
+def _loadable(x: torch.Tensor):
+    """x [rows, ...] itself where the kernels read its layout (contiguous rows with a
+    stride of whole 16-byte units), else a contiguous copy: heads or features of another
+    order, rows that are broadcast, a start between the units."""
+    inner = 1
+    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        if size > 1 and stride != inner:
+            return x.contiguous()
+        inner *= size
+    if x.shape[0] > 1 and (x.stride(0) < inner or x.stride(0) % 8) or x.data_ptr() % 16:
+        return x.clone(memory_format=torch.contiguous_format)
+    return x
 
 
 def _moved_only(module, apply, fn, recurse):
@@ -457,7 +471,7 @@ def nvfp4_linear_packed_fwd(x, w_codes, w_scales, w_global_sf=None, bias=None, x
     ws = workspace
     if ws is None:
         ws = _workspace(_on(index, "nvfp4_linear_packed_workspace", m, n, k), x.device, None)
-    args = (x.data_ptr(), ld if m > 1 else max(ld, k), w_codes.data_ptr(), w_scales.data_ptr(),
+    args = (x.data_ptr(), ld if m > 1 else k, w_codes.data_ptr(), w_scales.data_ptr(),
             _opt_ptr(w_global_sf), None if bias is None else bias.data_ptr(), m, n, k,
             _opt_ptr(x_global_sf), out.data_ptr())
     try:
@@ -491,8 +505,8 @@ class NVFP4PackedLinear(torch.nn.Module):
 
     @torch.no_grad()
     def forward(self, x):
-        out = nvfp4_linear_packed_fwd(x.reshape(-1, x.shape[-1]), self.codes, self.scales,
-                                      self.weight_global_sf, self.bias, self.input_global_sf)
+        out = nvfp4_linear_packed_fwd(_loadable(x.reshape(-1, x.shape[-1])), self.codes,
+                                      self.scales, self.weight_global_sf, self.bias, self.input_global_sf)
         return out.view(*x.shape[:-1], self.codes.shape[0])
 
 
@@ -597,14 +611,15 @@ class RotaryFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, gq, gk):
         positions, inv_freq = ctx.saved_tensors
-        gq, gk = rope_apply(gq.contiguous(), gk.contiguous(), positions, inv_freq, *ctx.args,
+        gq, gk = rope_apply(_loadable(gq), _loadable(gk), positions, inv_freq, *ctx.args,
                             inverse=True)
         return gq, gk, None, None, None, None, None
 
 
 class Rotary(torch.nn.Module):
     """Rotary positions of q and k before AttnQAT: forward(q, k, positions) with q, k
-    bf16 [B, N, H, D] (or [T, H, D]) and positions int32 of N (shared by the batch) or
+    bf16 [B, N, H, D] (or [T, H, D]; a layout the kernel does not read is copied) and
+    positions int32 of N (shared by the batch) or
     B*N rows, [rows] or [rows, axes].  ``scaling`` and the rest as in rope_inv_freq."""
 
     def __init__(self, rot_dim: int, interleaved: bool = False, axis_pairs=None, device=None,
@@ -625,7 +640,7 @@ class Rotary(torch.nn.Module):
         t = q.shape[:-2].numel()
         if positions.shape[0] != t and q.dim() == 4 and positions.shape[0] == q.shape[1]:
             positions = positions.repeat(q.shape[0], *(1,) * (positions.dim() - 1))
-        q3, k3 = (x.reshape(t, *x.shape[-2:]) for x in (q, k))
+        q3, k3 = (_loadable(x.reshape(t, *x.shape[-2:])) for x in (q, k))
         qo, ko = RotaryFunction.apply(q3, k3, positions, self.inv_freq, self.interleaved,
                                       self.axis_pairs, self.mscale)
         return qo.view(q.shape), ko.view(k.shape)

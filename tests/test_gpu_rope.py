@@ -106,6 +106,39 @@ def test_module_shares_positions_over_the_batch():
         assert torch.equal(qo[b], q1) and torch.equal(ko[b], k1)
 
 
+def test_module_takes_heads_first_broadcast_and_shifted_inputs():
+    g = torch.Generator().manual_seed(12)
+    n, h, d = 20, 4, 64
+    rot = api.Rotary(d, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    base = torch.randn(1, h, n, d, generator=g).to(BF16).cuda()
+    shared = torch.randn(1, n, 1, d, generator=g).to(BF16).cuda()  # one head for all
+    flat = torch.randn(n * h * d + 3, generator=g).to(BF16).cuda()
+    gy = torch.randn(1, n, h, d, generator=g).to(BF16).cuda()
+
+    def run(leaf, view):
+        leaf = leaf.clone().requires_grad_()
+        x = view(leaf)
+        y, _ = rot(x, x, pos)
+        ref = rot(x.detach().clone().contiguous(), x.detach().clone().contiguous(), pos)[0]
+        assert torch.equal(y, ref)
+        y.backward(gy)
+        return leaf.grad
+
+    back = api.rope_apply(gy[0], None, pos, rot.inv_freq, inverse=True)[0]
+    assert torch.equal(run(base, lambda x: x.transpose(1, 2))[0].transpose(0, 1), back)
+    assert torch.equal(run(flat, lambda x: x[3:].view(1, n, h, d))[3:].view(n, h, d), back)
+    # the shared head's gradient: the four heads' gradients (bf16 values) summed in bf16
+    # steps: at most 3 additions, each off by half a step of a partial sum
+    got = run(shared, lambda x: x.expand(1, n, h, d))[0, :, 0].double()
+    mag = back.double().abs().sum(1)
+    assert bool(((got - back.double().sum(1)).abs() <= 3 * 2.0 ** -8 * mag).all())
+    # a single row of a wider, unaligned stride
+    odd = torch.randn(2, 2 * d + 4, generator=g).to(BF16).cuda()[:1, :2 * d].view(1, 2, d)
+    assert torch.equal(api.rope_apply(odd, None, pos[:1], rot.inv_freq)[0],
+                       api.rope_apply(odd.clone(), None, pos[:1], rot.inv_freq)[0])
+
+
 def test_replayed_graph_follows_its_positions_on_another_stream():
     q = torch.randn(9, 4, 128, generator=torch.Generator().manual_seed(11)).to(BF16).cuda()
     pos = torch.zeros(9, dtype=torch.int32, device="cuda")

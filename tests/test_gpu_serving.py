@@ -81,6 +81,16 @@ def test_packed_module_keeps_its_types_when_the_model_changes_them():
         assert torch.equal(change(packed)(x), before)
 
 
+def test_packed_module_takes_any_layout():
+    torch.manual_seed(5)
+    packed = api.NVFP4Linear(128, 64, device="cuda").pack()
+    x = torch.randn(6, 128, device="cuda").to(BF16)
+    for view in (x.t().contiguous().t(), x[:1].expand(6, 128), x[::2],
+                 torch.cat([x.new_zeros(1), x.flatten()])[1:].view(6, 128),
+                 torch.cat([x, x[:, :3]], 1)[:, :128], torch.cat([x, x[:, :3]], 1)[:1, :128]):
+        assert torch.equal(packed(view), packed(view.clone(memory_format=torch.contiguous_format)))
+
+
 def test_packed_linear_unit_weight_scale_and_zero_input():
     w = workloads.random_matrix(64, 128, seed=4, scale=2.0)
     codes, scales = api.nvfp4_quantize_tiled(w.cuda())

@@ -157,6 +157,34 @@ def test_replayed_graph_follows_its_positions_on_another_stream():
         assert torch.equal(out, api.rope_apply(q, None, pos, f)[0])
 
 
+def test_captured_forward_and_backward_follow_their_inputs():
+    g = torch.Generator().manual_seed(13)
+    rot = api.Rotary(64, interleaved=True, device="cuda")
+    pos = torch.arange(15, dtype=torch.int32, device="cuda")
+    q, k, gq, gk = (torch.randn(15, 2, 64, generator=g).to(BF16).cuda() for _ in range(4))
+    q.requires_grad_(), k.requires_grad_()
+
+    def step():
+        out = rot(q, k, pos)
+        return (*out, *torch.autograd.grad(out, (q, k), (gq, gk)))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = step()
+    for shift in (0, 1000):
+        pos.add_(shift)
+        with torch.no_grad():
+            q.mul_(-1)
+        gk.mul_(2)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
 def test_refusals_on_device_tensors():
     q = torch.zeros(4, 2, 64, dtype=BF16, device="cuda")
     pos = torch.zeros(4, dtype=torch.int32, device="cuda")

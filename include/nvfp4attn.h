@@ -476,7 +476,8 @@ nvq_status rope_apply(const void* q, int64_t ld_q, void* q_out, int64_t ld_qo, i
  *
  * Device-side tables (page_table int32 [B, max_pages], row stride ld_table >=
  * max_pages; seq_lens int32 [B]) are read by the kernels, so captured graphs
- * follow their changes.  A page number outside [0, num_pages), or a length over
+ * follow their changes.  A length below 1 is an empty sequence.  A page number
+ * outside [0, num_pages), or a length over
  * 128 * max_pages, is never followed: the write is left out, the key treated as
  * not visible, and NVQ_ERR_INVALID recorded for nvq_device_status().
  */

@@ -113,6 +113,40 @@ def test_decode_parity(case):
     assert api.device_status() == 0
 
 
+@pytest.mark.parametrize("h,hkv,d,b,longest,window,sinks", [
+    (2, 1, 64, 700, 400, 0, 0), (32, 2, 128, 200, 600, 0, 0), (4, 4, 128, 150, 900, 200, 3),
+    (18, 2, 64, 180, 300, 0, 0)])
+def test_decode_of_many_sequences(h, hkv, d, b, longest, window, sinks):
+    """More segments than the chip has runs, some sequences empty, pages shared between
+    sequences, the table a slice of a wider one."""
+    g = torch.Generator().manual_seed(b + h)
+    lens = torch.randint(0, longest + 1, (b,), generator=g, dtype=torch.int32)
+    lens[torch.rand(b, generator=g) < 0.1] = 0
+    lens[b // 2] = longest
+    pages, width = 40, -(-longest // PAGE)
+    pool = make_pool(pages, hkv, d, g)
+    vmax = float(os_.unpack(*os_.record_parts(pool, d)[1::2]).abs().max())
+    wide = torch.randint(0, pages, (b, width + 3), generator=g, dtype=torch.int32)
+    q = torch.randn(b, h, d, generator=g).to(BF16)
+    ref = os_.decode(q, pool, wide[:, :width], lens.tolist(), d ** -0.5, window, sinks)
+    args = (q.cuda(), pool.cuda(), wide.cuda()[:, :width], lens.cuda(), d ** -0.5, window, sinks)
+    o, lse = api.attn_qat_decode(*args)
+    check_decode(o, lse, ref, longest, vmax)
+    o2, lse2 = api.attn_qat_decode(*args)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert api.device_status() == 0
+
+
+def test_decode_of_empty_sequences_only():
+    pool = torch.full((2, 2, 144 * 64), 0xFF, dtype=torch.uint8, device="cuda")
+    table = torch.full((5, 3), -1, dtype=torch.int32, device="cuda")
+    lens = torch.tensor([0, 0, -4, 0, 0], dtype=torch.int32, device="cuda")
+    q = torch.randn(5, 4, 64, device="cuda").to(BF16)
+    o, lse = api.attn_qat_decode(q, pool, table, lens)
+    assert not bool(o.any()) and bool((lse == -float("inf")).all())
+    assert api.device_status() == 0
+
+
 def test_sharp_scores_and_negative_sums():
     """Scores hundreds apart (all weight on one key, anywhere in the sequence) and all far
     below zero: the running maximum and the join must not lose either."""

@@ -416,8 +416,9 @@ nvq_status nvfp4_linear_bwd(const void* grad_out, const void* x, const void* w, 
  * M >= 1, K % 64 == 0 and N % 16 == 0 (else NVQ_ERR_UNSUPPORTED).  On the same
  * operands and scales the result is nvfp4_linear_fwd's up to the order of the
  * fp32 sums over K.  ws: nvfp4_linear_packed_workspace(M, N, K) bytes, 256-byte
- * aligned; its size follows from the current device's multiprocessor count.  The backward of a packed weight is not defined: train with
- * nvfp4_linear_fwd / nvfp4_linear_bwd, then pack.
+ * aligned; its size follows from the current device's multiprocessor count.
+ * The backward of a packed weight is not defined: train with nvfp4_linear_fwd /
+ * nvfp4_linear_bwd, then pack.
  */
 size_t nvfp4_linear_packed_workspace(int64_t M, int64_t N, int64_t K);
 nvq_status nvfp4_linear_packed_fwd(const void* x, int64_t ld_x, const uint8_t* w_codes,
@@ -477,9 +478,9 @@ nvq_status rope_apply(const void* q, int64_t ld_q, void* q_out, int64_t ld_qo, i
  * Device-side tables (page_table int32 [B, max_pages], row stride ld_table >=
  * max_pages; seq_lens int32 [B]) are read by the kernels, so captured graphs
  * follow their changes.  A length below 1 is an empty sequence.  A page number
- * outside [0, num_pages), or a length over
- * 128 * max_pages, is never followed: the write is left out, the key treated as
- * not visible, and NVQ_ERR_INVALID recorded for nvq_device_status().
+ * outside [0, num_pages), or a length over 128 * max_pages, is never followed:
+ * the write is left out, the key treated as not visible, and NVQ_ERR_INVALID
+ * recorded for nvq_device_status().
  */
 #define NVQ_KV_PAGE 128
 

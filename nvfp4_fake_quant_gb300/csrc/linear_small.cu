@@ -565,7 +565,9 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
   // At most four stages and, with small sums, 112 KB: two CTAs fit an SM, so that
   // clusters find room in every group of SMs.  At least 78 KB: no three do, whose 256 tensor-memory columns
   // each would not fit, so that no CTA waits for columns that a cluster holds which in
-  // its turn waits for that CTA's cluster.
+  // its turn waits for that CTA's cluster.  (The library's other kernels whose CTAs wait
+  // for one another or hold tensor memory long take over 149 KB: they share no SM with
+  // these.)
   const size_t sums = static_cast<size_t>(q.split - 1) * q.cols * 512;
   a.stages = std::min(4, (q.k_stages + q.split - 1) / q.split);
   const size_t room = (sums <= 56 * 1024 ? 112 : 222) * 1024;

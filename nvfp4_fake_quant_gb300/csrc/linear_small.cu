@@ -16,13 +16,16 @@
 //   workspace; whichever warp arrives last at the tile's ticket adds the parts in run
 //   order (the sum does not depend on who that is).
 //
-// Measured (calls in a CUDA graph): 32 x 28672 x 8192 29 us, 70% of the copy rate; 1 x
-// 1536 x 8960 8 us and 1 x 4608 x 1536 6 us, the latency of two dependent launches and of
-// the first loads.
+// Measured (calls in a CUDA graph): 53248 x 16384 82 us for one row, 88% of the copy
+// rate, 87 for 64; 28672 x 8192 27 us for 1 to 32 rows, 73%; one row of 1536 x 8960 6.8
+// us and of 4608 x 1536 5.2, the latency of a launch, of the first loads and of the
+// cluster's sum.  Addresses count here: 64-bit products for the outputs' rows cost 28672
+// x 8192 2 us at 64 rows, 65536 x 1024 4.
 //
-// Two launches: x is quantized (and the tickets cleared) by a small kernel, while the
-// main kernel, launched behind it programmatically, already fills its ring with
-// weights, which do not depend on x.
+// Launches.  With few blocks of x per CTA the clusters quantize x themselves, each CTA
+// its range of K, while the first weights arrive.  Else there are two: x is quantized
+// (and the tickets cleared) by a small kernel, while the main kernel, launched behind
+// it programmatically, already fills its ring with weights, which do not depend on x.
 #include <algorithm>
 #include <cstdint>
 
@@ -39,6 +42,7 @@ namespace {
 
 constexpr int kThreads = 192;  // producer, MMA, 4 epilogue warps
 constexpr int kSteps = 4;      // MMA steps (64 elements) per stage
+constexpr int kFusedBlocks = 4;  // of x per thread, at most, where the kernel quantizes x itself
 constexpr int kStages = 6;     // of the ring (8: 1 us slower at 32 x 28672 x 8192)
 // bytes of a stage: w codes, w scales, x scales
 constexpr uint32_t kW = 128 * 128, kSc = kSteps * 512, kXs = 1024;
@@ -50,6 +54,9 @@ struct SmallArgs {
   int tiles, k_stages, k_steps;
   int runs, per_run, rest;  // runs, units / runs, units % runs
   int split;                // CTAs per tile (clusters)
+  uint32_t sums_at;         // of their sums in the first one's shared memory
+  const uint16_t* x;        // x itself (kFused)
+  int64_t ld_x;
   const uint8_t* sx;        // x scales (stage blocks), w scales (tiled layout)
   const uint8_t* sw;
   const float* gx;          // device scalars; gw nullptr: 1
@@ -61,13 +68,26 @@ struct SmallArgs {
   int* err;
 };
 
+// One 16-element block of x, quantized.
+__device__ __forceinline__ Q16 quant_block(const uint4& lo, const uint4& hi, float g) {
+  const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  Q16 q = quant16_static_fast<false>(v, g, __frcp_rn(g));
+  code_signs(v, q.codes);
+  return q;
+}
+
+// Where the scale of x's block (row r, K block cb) lies.  The scales of a stage (4 MMA
+// steps) are two blocks of 512 bytes: row r % 32 of block i holds 4 words (of 4 scales),
+// those of (step 2 i, r / 32 = 0), (2 i, 1), (2 i + 1, 0), (2 i + 1, 1).  One copy of a
+// block then brings the scales of two steps to 4 columns of tensor memory, where the
+// tiled layout, made for 128 rows, takes a copy per step.  The scales of rows M and up
+// are not written: the products of those rows are never stored.
+__device__ __forceinline__ int x_scale_at(int r, int cb) {
+  const int step = cb >> 2, w = (step & 1) * 2 + (r >> 5);
+  return (step >> 1) * 512 + (r & 31) * 16 + w * 4 + (cb & 3);
+}
+
 // x [M, K] to codes and scales, one 16-element block per thread; clears the tickets.
-// The scales of a stage (4 MMA steps) are two blocks of 512 bytes: row r % 32 of block
-// i holds 4 words (of 4 scales), those of (step 2 i, r / 32 = 0), (2 i, 1), (2 i + 1,
-// 0), (2 i + 1, 1).  One copy of a block then brings the scales of two steps to 4
-// columns of tensor memory, where the tiled layout, made for 128 rows, takes a copy
-// per step.  The scales of rows M and up are not written: the products of those rows
-// are never stored.
 __global__ void __launch_bounds__(128) quant_rows_kernel(const uint16_t* __restrict__ x, int64_t ld,
                                                          int M, int nbc,
                                                          const float* __restrict__ gsf,
@@ -85,12 +105,10 @@ __global__ void __launch_bounds__(128) quant_rows_kernel(const uint16_t* __restr
   const float g = *gsf;
   const uint4* src = reinterpret_cast<const uint4*>(x + r * ld + static_cast<int64_t>(cb) * 16);
   const uint4 lo = __ldg(src), hi = __ldg(src + 1);
-  const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  Q16 q = quant16_static_fast<false>(v, g, __frcp_rn(g));
-  code_signs(v, q.codes);
-  *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(i) * 8) = make_uint2(q.codes[0], q.codes[1]);
-  const int step = cb >> 2, w = (step & 1) * 2 + (r >> 5);
-  scales[(step >> 1) * 512 + (r & 31) * 16 + w * 4 + (cb & 3)] = static_cast<uint8_t>(q.sbyte);
+  const Q16 q = quant_block(lo, hi, g);
+  *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(i) * 8) =
+      make_uint2(q.codes[0], q.codes[1]);
+  scales[x_scale_at(r, cb)] = static_cast<uint8_t>(q.sbyte);
 }
 
 // Run c covers units [units c / runs, units (c + 1) / runs) of the line.
@@ -181,8 +199,9 @@ __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
   return r;
 }
 
-// kClusters: one tile per cluster of p.split CTAs; else runs.
-template <bool kClusters>
+// kClusters: one tile per cluster of p.split CTAs; else runs.  kFused (clusters only): the
+// epilogue's warps quantize the CTA's part of x into shared memory first.
+template <bool kClusters, bool kFused>
 __global__ void __launch_bounds__(kThreads)
     linear_small_kernel(const __grid_constant__ CUtensorMap tx,
                         const __grid_constant__ CUtensorMap tw, const SmallArgs p) {
@@ -190,13 +209,16 @@ __global__ void __launch_bounds__(kThreads)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) &
                                              ~static_cast<uintptr_t>(1023u));
   __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
-  __shared__ uint64_t sums_full;
+  __shared__ uint64_t sums_full, x_full;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   volatile int* abort = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t x_bytes = static_cast<uint32_t>(p.cols) * 128;
-  const uint32_t stage_bytes = (kW + x_bytes + kSc + kXs + 1023) & ~1023u;
+  // a stage: w codes, x codes, w scales, x scales; fused: without x, whose stages follow
+  // the ring (all codes, then all scales)
+  const uint32_t sx_at = kW + (kFused ? 0u : x_bytes);
+  const uint32_t stage_bytes = (sx_at + kSc + (kFused ? 0u : kXs) + 1023) & ~1023u;
   constexpr uint32_t kAlloc = kClusters ? 256 : 512;
   pdl_trigger();
   if (threadIdx.x == 0) {
@@ -210,6 +232,7 @@ __global__ void __launch_bounds__(kThreads)
       mbar_init(&acc_empty[i], 4);
     }
     if (kClusters) mbar_init(&sums_full, max(4 * (p.split - 1), 1));
+    if (kFused) mbar_init(&x_full, 4);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -231,6 +254,8 @@ __global__ void __launch_bounds__(kThreads)
     u1 = run_begin(p, blockIdx.x + 1);
   }
   const int count = u1 - u0;
+  uint8_t* xc = smem + p.stages * stage_bytes;  // fused: x codes and scales of the CTA's part
+  uint8_t* xs = xc + count * x_bytes;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -242,29 +267,33 @@ __global__ void __launch_bounds__(kThreads)
     auto load_w = [&](const Place& at) {
       const int ns = min(kSteps, p.k_steps - at.ks * kSteps);
       uint8_t* st = smem + at.s * stage_bytes;
-      mbar_arrive_expect_tx_w(&full[at.s], kW + x_bytes + kXs + static_cast<uint32_t>(ns) * 512u);
+      mbar_arrive_expect_tx_w(&full[at.s],
+                              sx_at + (kFused ? 0u : kXs) + static_cast<uint32_t>(ns) * 512u);
       tma_load_4d_w(st, &tw, at.ks * 128, at.tile * 128, 0, 0, &full[at.s]);
-      bulk_load_w(st + kW + x_bytes,
+      bulk_load_w(st + sx_at,
                   p.sw + (static_cast<int64_t>(at.tile) * p.k_steps + at.ks * kSteps) * 512,
                   ns * 512, &full[at.s]);
     };
     auto load_x = [&](const Place& at) {
       uint8_t* st = smem + at.s * stage_bytes;
       tma_load_4d_w(st + kW, &tx, at.ks * 128, 0, 0, 0, &full[at.s]);
-      bulk_load_w(st + kW + x_bytes + kSc, p.sx + static_cast<int64_t>(at.ks) * kXs, kXs,
+      bulk_load_w(st + sx_at + kSc, p.sx + static_cast<int64_t>(at.ks) * kXs, kXs,
                   &full[at.s]);
     };
     const int head = min(count, p.stages);
     Place at(p, u0), at_x(p, u0);
+    if (kFused) pdl_wait();  // no kernel of this call stands between w's writer and this one
     for (int i = 0; i < head; ++i, at.next(p)) load_w(at);
-    pdl_wait();  // x~
-    for (int i = 0; i < head; ++i, at_x.next(p)) load_x(at_x);
+    if (!kFused) {
+      pdl_wait();  // x~
+      for (int i = 0; i < head; ++i, at_x.next(p)) load_x(at_x);
+    }
     int i = head;
     bool ok = true;
     for (; i < count; ++i, at.next(p)) {
       if (!(ok = mbar_wait_warp(&empty[at.s], at.phase ^ 1, abort))) break;
       load_w(at);
-      load_x(at);
+      if (!kFused) load_x(at);
     }
     if (!ok) {  // let the copies already issued land before the block leaves
       for (int k = max(0, i - p.stages); k < i; ++k)
@@ -275,7 +304,8 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t idesc = idesc_mxf4nvf4(128, 0) | (static_cast<uint32_t>(p.cols >> 3) << 17);
     int part = 0, i = 0;
     Place at(p, u0);
-    for (; i < count; ++i, at.next(p)) {
+    const bool x_there = !kFused || mbar_wait_warp(&x_full, 0, abort);
+    for (; i < count && x_there; ++i, at.next(p)) {
       const int s = at.s, ks = at.ks;
       const int ns = min(kSteps, p.k_steps - ks * kSteps);
       const bool first = i == 0 || ks == 0;
@@ -283,7 +313,9 @@ __global__ void __launch_bounds__(kThreads)
       if (first && !mbar_wait_warp(&acc_empty[part & 1], ((part >> 1) & 1) ^ 1, abort)) break;
       if (!mbar_wait_warp(&full[s], at.phase, abort)) break;
       tc_fence_after();
-      const uint32_t a = smem_u32(smem + s * stage_bytes), b = a + kW, sa = b + x_bytes, sb = sa + kSc;
+      const uint32_t a = smem_u32(smem + s * stage_bytes), sa = a + sx_at;
+      const uint32_t b = kFused ? smem_u32(xc + i * x_bytes) : a + kW;
+      const uint32_t sb = kFused ? smem_u32(xs + i * kXs) : sa + kSc;
       const uint32_t col = tmem + kScCol + 32 * s;
       const uint64_t ad = sdesc_sw128(a, 16, 1024), bd = sdesc_sw128(b, 16, 1024);
       const uint64_t wd = sdesc(sa, 128, 128, 0), xd = sdesc(sb, 128, 128, 0);
@@ -310,12 +342,47 @@ __global__ void __launch_bounds__(kThreads)
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, row = quarter * 32 + lane;
     pdl_wait();
+    if constexpr (kFused) {
+      // the CTA's part of x: codes in the swizzled rows of the B operand
+      const int tile = blockIdx.x / p.split, ks0 = u0 - tile * p.k_stages;
+      const int nb = min(16 * count, 4 * p.k_steps - 16 * ks0), all = p.M * nb;
+      const uint16_t* x = p.x + 256 * static_cast<int64_t>(ks0);
+      const float g = *p.gx;
+      auto source = [&](int i, int& r, int& cb) {
+        r = i / nb;
+        cb = i - r * nb;
+        return reinterpret_cast<const uint4*>(x + r * p.ld_x + cb * 16);
+      };
+      for (int i0 = threadIdx.x - 64; i0 < all; i0 += 128 * kFusedBlocks) {
+        uint4 lo[kFusedBlocks], hi[kFusedBlocks];
+        int r[kFusedBlocks], cb[kFusedBlocks];
+#pragma unroll
+        for (int j = 0; j < kFusedBlocks; ++j) {
+          if (i0 + 128 * j >= all) break;
+          const uint4* src = source(i0 + 128 * j, r[j], cb[j]);
+          lo[j] = __ldg(src);
+          hi[j] = __ldg(src + 1);
+        }
+#pragma unroll
+        for (int j = 0; j < kFusedBlocks; ++j) {
+          if (i0 + 128 * j >= all) break;
+          const Q16 q = quant_block(lo[j], hi[j], g);
+          const int c = cb[j] & 15;  // of its stage: 16-byte units c / 2, swizzled by the row
+          uint8_t* row = xc + (cb[j] >> 4) * x_bytes + r[j] * 128;
+          *reinterpret_cast<uint2*>(row + (((c >> 1) ^ (r[j] & 7)) << 4) + (c & 1) * 8) =
+              make_uint2(q.codes[0], q.codes[1]);
+          xs[x_scale_at(r[j], cb[j])] = static_cast<uint8_t>(q.sbyte);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive_warp(&x_full);
+    }
     const float alpha = 1.0f / (*p.gx * (p.gw != nullptr ? *p.gw : 1.0f));
     if constexpr (kClusters) {
       const int tile = blockIdx.x / p.split, rank = blockIdx.x - tile * p.split;
       const int n = tile * 128 + row;
       const float bias = p.bias != nullptr && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
-      float* sums = reinterpret_cast<float*>(smem + p.stages * stage_bytes);  // [split - 1][cols][128]
+      float* sums = reinterpret_cast<float*>(smem + p.sums_at);  // [split - 1][cols][128]
       if (p.split > 1) cluster_wait();
       const uint32_t acc = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
       bool ok = mbar_wait_warp(&acc_full[0], 0, abort);
@@ -345,14 +412,14 @@ __global__ void __launch_bounds__(kThreads)
           float f[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
-          for (int r = 0; r < p.split - 1; ++r)
+          const float* theirs = sums + c * 128 + row;
+          for (int r = 0; r < p.split - 1; ++r, theirs += p.cols * 128)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] += sums[(r * p.cols + c + j) * 128 + row];
+            for (int j = 0; j < 16; ++j) f[j] += theirs[j * 128];
+          __nv_bfloat16* o = p.out + static_cast<int64_t>(c) * p.N + n;
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < p.M && n < p.N)
-              p.out[static_cast<int64_t>(c + j) * p.N + n] =
-                  __float2bfloat16_rn(fmaf(alpha, f[j], bias));
+          for (int j = 0; j < 16; ++j, o += p.N)
+            if (c + j < p.M && n < p.N) *o = __float2bfloat16_rn(fmaf(alpha, f[j], bias));
         }
       }
     } else {
@@ -393,10 +460,6 @@ __global__ void __launch_bounds__(kThreads)
         if (!mbar_wait_warp(&acc_full[part & 1], (part >> 1) & 1, abort)) break;
         tc_fence_after();
         const uint32_t acc = tmem + 64 * (part & 1) + (static_cast<uint32_t>(quarter * 32) << 16);
-        auto store = [&](int m, float f) {
-          if (m < p.M && n < p.N)
-            p.out[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(fmaf(alpha, f, bias));
-        };
         if (whole || early) {
           for (int m0 = 0; m0 < p.M; m0 += 32) {
             uint32_t own[32];
@@ -407,9 +470,12 @@ __global__ void __launch_bounds__(kThreads)
                 other[j] = m0 + j < p.cols ? __ldcg(theirs + (m0 + j) * 128) : 0.f;
             }
             tmem_wait_ld();
+            __nv_bfloat16* o = p.out + static_cast<int64_t>(m0) * p.N + n;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              store(m0 + j, early ? __uint_as_float(own[j]) + other[j] : __uint_as_float(own[j]));
+            for (int j = 0; j < 32; ++j, o += p.N) {
+              const float f = __uint_as_float(own[j]) + (early ? other[j] : 0.f);
+              if (m0 + j < p.M && n < p.N) *o = __float2bfloat16_rn(fmaf(alpha, f, bias));
+            }
           }
         } else {
           bool last = all_there();
@@ -446,8 +512,10 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
               for (int j = 0; j < 16; ++j) f[j] += v[j];
             }
+            __nv_bfloat16* o = p.out + static_cast<int64_t>(m0) * p.N + n;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) store(m0 + j, f[j]);
+            for (int j = 0; j < 16; ++j, o += p.N)
+              if (m0 + j < p.M && n < p.N) *o = __float2bfloat16_rn(fmaf(alpha, f[j], bias));
           }
         }
         tc_fence_before();
@@ -473,6 +541,7 @@ size_t rup(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // Workspace, each region 256-byte aligned.
 struct SmallPlan {
   int cols, tiles, k_stages, split, runs;  // split 0: runs
+  bool fused;
   size_t cx, sx, tickets, parts, total;
 };
 
@@ -492,11 +561,17 @@ SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
     p.split = 1;
     for (int x = 2; x <= 8 && x <= p.k_stages; ++x) {
       const int ctas = x * p.tiles, sum_rows = (x - 1) * p.cols;
-      if (ctas <= 128 ? sum_rows <= 224 && (x < 7 || p.tiles <= 16)
+      if (ctas <= 128 ? sum_rows <= 224 && (x < 7 || p.tiles <= (sum_rows <= 112 ? 16 : 12))
                       : ctas <= sms && sum_rows <= 112 && x <= 4)
         p.split = x;
     }
     p.runs = p.split * p.tiles;
+    // x quantized in place, by every CTA its part, saves the other launch (2 us of the
+    // host's time), and time on the device up to 3.5 blocks a thread: 1 x 4608 x 1536 5.2
+    // us (5.9 in two launches), 5 x 1536 x 8960 (3.1 blocks) 7.4 (7.7); 8 x 4096 x 4096 (4
+    // blocks) 7.3 (7.1).  Eight stages of x, at most, lie beside the ring.
+    const int64_t part = (p.k_stages + p.split - 1) / p.split;
+    p.fused = part <= 8 && 16 * M * part <= 448;  // of 128 kFusedBlocks
   } else {
     p.runs = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.tiles) * p.k_stages, sms));
   }
@@ -526,14 +601,17 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
                                 void* out, uint8_t* ws, int* err, cudaStream_t stream) {
   const SmallPlan q = small_plan(M, N, K);
   unsigned int* tickets = reinterpret_cast<unsigned int*>(ws + q.tickets);
-  const int nbc = static_cast<int>(K / 16), blocks = static_cast<int>(M) * nbc;
-  const int n_tickets = q.split == 0 ? 4 * q.tiles : 0;
-  cudaError_t e = launch_pdl(quant_rows_kernel, dim3((std::max(blocks, n_tickets) + 127) / 128),
-                             dim3(128), 0, stream, 1, static_cast<const uint16_t*>(x), ld_x,
-                             static_cast<int>(M), nbc, gx, ws + q.cx, ws + q.sx, tickets,
-                             n_tickets);
-  if (e != cudaSuccess) return e;
-  const uint32_t stage = (kW + q.cols * 128u + kSc + kXs + 1023) / 1024 * 1024;
+  cudaError_t e = cudaSuccess;
+  if (!q.fused) {
+    const int nbc = static_cast<int>(K / 16), blocks = static_cast<int>(M) * nbc;
+    const int n_tickets = q.split == 0 ? 4 * q.tiles : 0;
+    e = launch_pdl(quant_rows_kernel, dim3((std::max(blocks, n_tickets) + 127) / 128), dim3(128), 0,
+                   stream, 1, static_cast<const uint16_t*>(x), ld_x, static_cast<int>(M), nbc, gx,
+                   ws + q.cx, ws + q.sx, tickets, n_tickets);
+    if (e != cudaSuccess) return e;
+  }
+  const uint32_t x_stage = q.cols * 128u + kXs;
+  const uint32_t stage = (kW + kSc + (q.fused ? 0 : x_stage) + 1023) / 1024 * 1024;
   SmallArgs a{};
   a.M = static_cast<int>(M);
   a.N = static_cast<int>(N);
@@ -546,6 +624,8 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
   a.runs = q.runs;
   a.per_run = static_cast<int>(static_cast<int64_t>(q.tiles) * q.k_stages / q.runs);
   a.rest = static_cast<int>(static_cast<int64_t>(q.tiles) * q.k_stages % q.runs);
+  a.x = static_cast<const uint16_t*>(x);
+  a.ld_x = ld_x;
   a.sx = ws + q.sx;
   a.sw = sw;
   a.gx = gx;
@@ -557,27 +637,29 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
   a.err = err;
   size_t smem = a.stages * stage + 1024;
   if (q.split == 0) {
-    e = cudaFuncSetAttribute(linear_small_kernel<false>,
+    e = cudaFuncSetAttribute(linear_small_kernel<false, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
     if (e != cudaSuccess) return e;
-    return launch_pdl(linear_small_kernel<false>, dim3(q.runs), dim3(kThreads), smem, stream, 1, tx, tw, a);
+    return launch_pdl(linear_small_kernel<false, false>, dim3(q.runs), dim3(kThreads), smem, stream,
+                      1, tx, tw, a);
   }
-  // At most four stages and, with small sums, 112 KB: two CTAs fit an SM, so that
-  // clusters find room in every group of SMs.  At least 78 KB: no three do, whose 256 tensor-memory columns
-  // each would not fit, so that no CTA waits for columns that a cluster holds which in
-  // its turn waits for that CTA's cluster.  (The library's other kernels whose CTAs wait
-  // for one another or hold tensor memory long take over 149 KB: they share no SM with
-  // these.)
+  // At most four stages, and 112 KB where there are more CTAs than one per SM leaves room
+  // for: two fit an SM then.  At least 78 KB: no three do, whose 256 tensor-memory
+  // columns each would not fit, so that no CTA waits for columns that a cluster holds
+  // which in its turn waits for that CTA's cluster.  (The library's other kernels whose
+  // CTAs wait for one another or hold tensor memory long take over 149 KB: they share no
+  // SM with these.)
+  const int part = (q.k_stages + q.split - 1) / q.split;  // stages of a CTA, at most
   const size_t sums = static_cast<size_t>(q.split - 1) * q.cols * 512;
-  a.stages = std::min(4, (q.k_stages + q.split - 1) / q.split);
-  const size_t room = (sums <= 56 * 1024 ? 112 : 222) * 1024;
-  a.stages = std::min<int>(a.stages, (room - 1024 - sums) / stage);
-  smem = std::max<size_t>(a.stages * stage + sums + 1024, 78 * 1024);
-  e = cudaFuncSetAttribute(linear_small_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           226 * 1024);
+  const size_t xs = q.fused ? static_cast<size_t>(part) * x_stage : 0;
+  const size_t room = (q.runs > 128 ? 112 : 222) * 1024;
+  a.stages = std::min<int>({4, part, static_cast<int>((room - 1024 - sums - xs) / stage)});
+  a.sums_at = static_cast<uint32_t>(a.stages * stage + xs);
+  smem = std::max<size_t>(a.sums_at + sums + 1024, 78 * 1024);
+  auto* kernel = q.fused ? linear_small_kernel<true, true> : linear_small_kernel<true, false>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_pdl(linear_small_kernel<true>, dim3(q.runs), dim3(kThreads), smem, stream, q.split,
-                    tx, tw, a);
+  return launch_pdl(kernel, dim3(q.runs), dim3(kThreads), smem, stream, q.split, tx, tw, a);
 }
 
 }  // namespace nvq

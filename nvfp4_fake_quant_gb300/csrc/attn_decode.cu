@@ -15,8 +15,9 @@
 // leaves (m, l, sum p V~) per run in the workspace, and a second small kernel
 // joins them in run order, so results do not vary from run to run.
 //
-// One run, six warps; three runs (two above 8 query heads) make a CTA, one CTA an SM
-// (as CTAs of their own the second and third of an SM started 2 us and more late):
+// One run, six warps; three runs (two above 8 query heads, four of long work on heads of
+// 64) make a CTA, one CTA an SM (as CTAs of their own the second and third of an SM
+// started 2 us and more late):
 //   producer  fetches records into a ring of stages (K codes by tensor-map loads
 //             with the swizzle the MMA reads, the rest by bulk copies; only the
 //             rows that hold tokens) and describes each tile beside it
@@ -67,12 +68,12 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Per shape: query heads per run (8 NT), runs per CTA, ring stages; shared memory and
 // tensor memory of a run.
-template <int D, int NT>
+template <int D, int NT, int kRunsPerCta>
 struct Cfg {
   static constexpr int kHeads = 8 * NT;
-  static constexpr int kRuns = NT == 1 ? 3 : 2;  // per CTA, one CTA per SM
+  static constexpr int kRuns = kRunsPerCta;  // one CTA per SM
   static constexpr int kThreads = kRuns * kRunWarps * 32;
-  static constexpr int kStages = D == 64 ? 5 : (NT == 1 ? 2 : 3);
+  static constexpr int kStages = D == 64 ? (kRuns == 4 ? 4 : 5) : (NT == 1 ? 2 : 3);
   static constexpr int kRow = D + 4;  // floats of a head's row in the join area
   static constexpr uint32_t kRec = record_bytes(D);
   static constexpr uint32_t kQ = kHeads * D * 2;         // q of a segment that starts with the tile
@@ -132,7 +133,7 @@ __host__ __device__ constexpr int part_floats(int D, int heads) { return heads *
 // The line of `all` tiles is cut into n = min(all, runs) runs: run c is [all c / n,
 // all (c + 1) / n), never empty; of the grid's runs those from n on have nothing.
 // all c / n = (all / n) c + (all % n) c / n.  n is the grid's or all itself, so there is
-// nothing to divide: the host gives 2^64 / runs, rounded up (all < 2^55 and runs <= 2^9
+// nothing to divide: the host gives 2^64 / runs, rounded up (all <= 2^53 and runs < 2^10
 // keep the product's error below 1 / runs).
 struct Runs {
   int64_t all, per;
@@ -454,11 +455,11 @@ struct Ring {
   }
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1)
+template <int D, int NT, int kRunsPerCta>
+__global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tk32, const DecodeArgs a) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D, NT, kRunsPerCta>;
   constexpr int kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int64_t warp_sum[kThreads / 32];
@@ -916,25 +917,36 @@ nvq_status check_decode(int B, int H, int Hkv, int D, int max_pages) {
       max_pages > 0x7FFFFFFF / kPage)
     return NVQ_ERR_INVALID;
   if (D != 64 && D != 128) return NVQ_ERR_UNSUPPORTED;
-  if (B > 65535 || H > 65535 || static_cast<int64_t>(B) * H > 0x7FFFFFFF) return NVQ_ERR_UNSUPPORTED;
+  if (B > 65535 || H > 65535 || static_cast<int64_t>(B) * H > 0x7FFFFFFF ||
+      static_cast<int64_t>(B) * H * max_pages > int64_t{1} << 53)
+    return NVQ_ERR_UNSUPPORTED;
   return NVQ_OK;
 }
 
 // CTAs and runs, query heads per run and the workspace: what goes on from each run,
 // then two parts per run.
 struct Plan {
-  int nt, chunks, ctas, runs, by_segment, join_x, join_y, join_threads;
+  int nt, chunks, ctas, per_cta, runs, by_segment, join_x, join_y, join_threads;
   size_t parts, total;
 };
 
-Plan plan(int B, int H, int Hkv, int D, int max_pages) {
+Plan plan(int B, int H, int Hkv, int D, int max_pages, int window, int sinks) {
   Plan p;
   const int G = H / Hkv;
   p.nt = G > 8 ? 2 : 1;  // 8 or 16 columns: V~ is decoded once for both
   p.chunks = (G + 8 * p.nt - 1) / (8 * p.nt);
   const int64_t segments = static_cast<int64_t>(B) * Hkv * p.chunks;
   p.ctas = static_cast<int>(std::min<int64_t>(segments * max_pages, device_sms()));
-  p.runs = p.ctas * (p.nt == 1 ? 3 : 2);
+  int64_t pages = max_pages;  // that a sequence may show
+  if (window > 0)
+    pages = std::min(pages, (int64_t{window} + kPage - 2) / kPage + 1 +
+                                (int64_t{sinks} + kPage - 1) / kPage);
+  // Heads of 64: four runs a CTA from six tiles a run on (64 sequences of up to 8192, 32
+  // heads on 8: 46 us, 48 with three; 8 of up to 131072: 76, 85); with fewer tiles the
+  // fourth only adds a part to join and a larger block to start (32 of a window of 4100, 16
+  // heads on 2: 16.6, 15.7).  Heads of 128 have no registers for it.
+  p.per_cta = p.nt == 2 ? 2 : D == 64 && segments * pages >= 24 * p.ctas ? 4 : 3;
+  p.runs = p.ctas * p.per_cta;
   // Fewer segments than runs: entries by segment, so the join has no idle blocks.
   p.by_segment = segments <= p.runs;
   p.join_x = p.by_segment ? static_cast<int>(segments) : p.runs;
@@ -949,15 +961,16 @@ Plan plan(int B, int H, int Hkv, int D, int max_pages) {
   return p;
 }
 
-template <int D, int NT>
+template <int D, int NT, int kRunsPerCta>
 cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tk32, const DecodeArgs& a,
                           const Plan& p, cudaStream_t stream) {
-  using C = Cfg<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  using C = Cfg<D, NT, kRunsPerCta>;
+  const auto kernel = decode_kernel<D, NT, kRunsPerCta>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(decode_kernel<D, NT>, dim3(p.ctas), dim3(C::kThreads), C::kSmem, stream, 1, tk,
-                      tk32, a)) != cudaSuccess)
+  if ((e = launch_pdl(kernel, dim3(p.ctas), dim3(C::kThreads), C::kSmem, stream, 1, tk, tk32, a)) !=
+      cudaSuccess)
     return e;
   const dim3 grid(p.join_x, p.join_y);
   if (p.join_threads == 1024)
@@ -973,7 +986,7 @@ extern "C" {
 
 size_t attn_qat_decode_workspace(int B, int H, int Hkv, int D, int max_pages) {
   if (nvq::check_decode(B, H, Hkv, D, max_pages) != NVQ_OK) return 0;
-  return nvq::plan(B, H, Hkv, D, max_pages).total;
+  return nvq::plan(B, H, Hkv, D, max_pages, 0, 0).total;  // a window needs no more
 }
 
 nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_t num_pages,
@@ -991,7 +1004,7 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
     return NVQ_ERR_INVALID;
   st = check_kv(pool, num_pages, page_table, ld_table, max_pages, seq_lens);
   if (st != NVQ_OK) return st;
-  const Plan p = plan(B, H, Hkv, D, max_pages);
+  const Plan p = plan(B, H, Hkv, D, max_pages, window, sinks);
   if (num_pages > 0x7FFFFFFF / Hkv) return NVQ_ERR_UNSUPPORTED;  // tensor-map coordinates
   if (ws == nullptr || ws_bytes < p.total || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return NVQ_ERR_WORKSPACE;
@@ -1017,10 +1030,11 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
                      ~uint64_t{0} / p.runs + 1, err};
   const cudaError_t e = timed(NVQ_KERNEL_ATTN_FWD, stream, [&] {
     if (D == 128)
-      return p.nt == 1 ? launch_decode<128, 1>(tk, tk32, a, p, stream)
-                       : launch_decode<128, 2>(tk, tk32, a, p, stream);
-    return p.nt == 1 ? launch_decode<64, 1>(tk, tk32, a, p, stream)
-                     : launch_decode<64, 2>(tk, tk32, a, p, stream);
+      return p.nt == 1 ? launch_decode<128, 1, 3>(tk, tk32, a, p, stream)
+                       : launch_decode<128, 2, 2>(tk, tk32, a, p, stream);
+    if (p.nt == 2) return launch_decode<64, 2, 2>(tk, tk32, a, p, stream);
+    return p.per_cta == 4 ? launch_decode<64, 1, 4>(tk, tk32, a, p, stream)
+                          : launch_decode<64, 1, 3>(tk, tk32, a, p, stream);
   });
   return e == cudaSuccess ? NVQ_OK : fail_cuda("attn decode", e);
 }

@@ -115,7 +115,7 @@ def test_decode_parity(case):
 
 @pytest.mark.parametrize("h,hkv,d,b,longest,window,sinks", [
     (2, 1, 64, 700, 400, 0, 0), (32, 2, 128, 200, 600, 0, 0), (4, 4, 128, 150, 900, 200, 3),
-    (18, 2, 64, 180, 300, 0, 0)])
+    (18, 2, 64, 180, 300, 0, 0), (4, 2, 64, 400, 700, 0, 0), (5, 1, 64, 70, 7000, 0, 0)])
 def test_decode_of_many_sequences(h, hkv, d, b, longest, window, sinks):
     """More segments than the chip has runs, some sequences empty, pages shared between
     sequences, the table a slice of a wider one."""

@@ -83,6 +83,11 @@ def test_decode_refuses_an_output_over_its_queries(lib):
     assert dec(A, A + rows, ld_q=2048) == INVALID  # inside a strided q
 
 
+def test_decode_refuses_more_tiles_than_its_cut_takes(lib):
+    assert lib.attn_qat_decode_workspace(65535, 32767, 32767, 64, (1 << 22) + 300) == 0
+    assert lib.attn_qat_decode_workspace(65535, 32767, 32767, 64, 1 << 20) > 0
+
+
 def test_packed_linear_refusals(lib):
     def lin(x=A, ld=128, c=A, s=A, wg=None, bias=None, m=2, n=32, k=128, xg=None, out=A, ws=A,
             ws_bytes=BIG):

@@ -14,8 +14,9 @@
 // heads are spread over more blocks instead, so that a decode step fills the chip.
 //
 // Bound by HBM: reads 4 D, writes 9 D / 8 bytes per token and head.  Measured (calls in
-// a CUDA graph): 25088 tokens of 12 heads of 128 37 us, 79% of the copy rate; 64 single
-// tokens 2.4 us, the latency of a launch and three dependent loads (length, page, row).
+// a CUDA graph): 25088 tokens of 12 heads of 128 36.6 us, 80% of the copy rate; 64 single
+// tokens 2.1 us, the latency of a launch and of two dependent loads (length, page), under
+// which the first head's values arrive (2.4 us when they were asked for behind them).
 #include <algorithm>
 #include <cstdint>
 
@@ -90,26 +91,34 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
   pdl_trigger();
   pdl_wait();
+  const int cb = threadIdx.x % kBlocks, tok = threadIdx.x / kBlocks % kTokens;
+  constexpr int kRows = kThreads / (kBlocks * kTokens);  // heads per pass
+  const int step = gridDim.y * kRows;
+  int hv = blockIdx.y * kRows + threadIdx.x / (kBlocks * kTokens);
+  const uint16_t* const k = a.k + (t0 + tok) * a.ld_k + cb * 16;
+  const uint16_t* const v = a.v + (t0 + tok) * a.ld_v + cb * 16 - static_cast<int64_t>(a.Hkv) * D;
+  uint4 lo, hi;
+  auto load = [&](int i) {
+    const uint4* s4 = reinterpret_cast<const uint4*>((i >= a.Hkv ? v : k) + i * D);
+    lo = __ldg(s4);
+    hi = __ldg(s4 + 1);
+  };
+  // the first head's loads do not wait for the tokens' places
+  if (t0 + tok < a.T && hv < 2 * a.Hkv) load(hv);
   if (threadIdx.x < kTokens) {
     const int64_t t = t0 + threadIdx.x;
     page[threadIdx.x] = t < a.T ? find_row(a, t, D, &row[threadIdx.x]) : nullptr;
   }
   __syncthreads();
-  const int cb = threadIdx.x % kBlocks, tok = threadIdx.x / kBlocks % kTokens;
-  constexpr int kRows = kThreads / (kBlocks * kTokens);  // heads per pass
   uint8_t* const base = page[tok];
   if (base == nullptr) return;
   const int r = row[tok];
-  for (int hv = blockIdx.y * kRows + threadIdx.x / (kBlocks * kTokens); hv < 2 * a.Hkv;
-       hv += gridDim.y * kRows) {
-    const bool is_v = hv >= a.Hkv;
-    const int h = is_v ? hv - a.Hkv : hv;
-    const uint16_t* src = is_v ? a.v + (t0 + tok) * a.ld_v : a.k + (t0 + tok) * a.ld_k;
-    const uint4* s4 = reinterpret_cast<const uint4*>(src + h * D + cb * 16);
-    const uint4 lo = __ldg(s4), hi = __ldg(s4 + 1);
+  for (; hv < 2 * a.Hkv; hv += step) {
     const uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (hv + step < 2 * a.Hkv) load(hv + step);
+    const bool is_v = hv >= a.Hkv;
     const Codes16 q = codes16_unit(x);
-    uint8_t* rec = base + static_cast<int64_t>(h) * record_bytes(D);
+    uint8_t* rec = base + static_cast<int64_t>(is_v ? hv - a.Hkv : hv) * record_bytes(D);
     *reinterpret_cast<uint2*>(rec + (is_v ? v_codes_at(D) : 0) + r * (D / 2) + cb * 8) =
         make_uint2(q.codes[0], q.codes[1]);
     rec[(is_v ? v_scales_at(D) : k_scales_at(D)) + r * kBlocks + cb] =

@@ -552,17 +552,22 @@ SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
   p.k_stages = static_cast<int>((K + 255) / 256);
   const int sms = device_sms();
   if (p.tiles <= sms) {
-    // As many CTAs a tile as there are SMs and stages of K for (not only powers of two:
-    // three at 1 x 5120 x 13824 take 14 us, two 19).  The sums are at most 112 KB, and 56
-    // KB where the clusters need two CTAs per SM: those of more than 128 SMs' worth, of
-    // which the chip's groups of SMs do not hold all at once with one CTA per SM (64 x
-    // 4864 x 8192 in four, one per SM: 21 us, in two: 13).  Of 7 and 8 a group holds two,
-    // 16 in all (32 x 2304 x 4096, 18 tiles: 15 us in seven, 8.3 in four).
+    // As many CTAs a tile as there are SMs and stages of K for, and half as many again, two
+    // to an SM, for few rows: up to 16 (1 x 10240 x 8192 12 us, 15 without; 1 x 12800 x 4096
+    // 7.3, 9.9), and up to 32 where each CTA has 16 stages and more (32 x 10240 x 8192 13.0,
+    // 15.6).  With more rows or shorter parts the second sum costs more (32 x 10240 x 2048
+    // 7.9, 7.2; 64 x 14336 x 16384 33, 30).
+    // The sums are at most 112 KB, and 56 KB where the clusters need two CTAs per SM: those
+    // of more than 128 SMs' worth, of which the chip's groups of SMs do not hold all at once
+    // with one CTA per SM (64 x 4864 x 8192 in four, one per SM: 21 us, in two: 13).  Of 7
+    // and 8, few fit a group (32 x 2304 x 4096, 18 tiles: 15 us in seven, 8.3 in four; 32 x
+    // 2048 x 4096, 16 tiles: 15 us in eight, 7.9 in seven).
     p.split = 1;
     for (int x = 2; x <= 8 && x <= p.k_stages; ++x) {
       const int ctas = x * p.tiles, sum_rows = (x - 1) * p.cols;
+      const bool pairs = p.cols == 16 || (p.cols == 32 && p.k_stages >= 16 * x);
       if (ctas <= 128 ? sum_rows <= 224 && (x < 7 || p.tiles <= (sum_rows <= 112 ? 16 : 12))
-                      : ctas <= sms && sum_rows <= 112 && x <= 4)
+                      : ctas <= (pairs ? 3 * sms / 2 : sms) && sum_rows <= 112 && x <= 4)
         p.split = x;
     }
     p.runs = p.split * p.tiles;

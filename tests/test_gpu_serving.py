@@ -22,7 +22,7 @@ SIZES = [(1, 16, 64), (1, 4608, 1536), (2, 144, 320), (5, 1536, 8960), (7, 128, 
          (64, 512, 1536), (65, 208, 640), (300, 256, 2048),
          # three, five, six and seven parts of K a tile; many rows with few tiles
          (1, 5120, 1024), (4, 3200, 1600), (18, 2560, 1600), (6, 2000, 1792), (64, 1536, 1024),
-         (48, 640, 1600),
+         (48, 640, 1600), (3, 10256, 576),
          # more tiles of 128 weights than SMs
          (1, 19536, 64), (3, 20000, 704), (33, 39056, 576)]
 

@@ -100,8 +100,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
   uint4 lo, hi;
   auto load = [&](int i) {
     const uint4* s4 = reinterpret_cast<const uint4*>((i >= a.Hkv ? v : k) + i * D);
-    lo = __ldg(s4);
-    hi = __ldg(s4 + 1);
+    lo = ld16(s4);
+    hi = ld16(s4 + 1);
   };
   // the first head's loads do not wait for the tokens' places
   if (t0 + tok < a.T && hv < 2 * a.Hkv) load(hv);

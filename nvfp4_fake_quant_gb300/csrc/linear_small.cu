@@ -85,11 +85,9 @@ __device__ __forceinline__ int x_scale_at(int r, int cb) {
 }
 
 // x [M, K] to codes and scales, one 16-element block per thread.
-__global__ void __launch_bounds__(128) quant_rows_kernel(const uint16_t* __restrict__ x, int64_t ld,
-                                                         int M, int nbc,
-                                                         const float* __restrict__ gsf,
-                                                         uint8_t* __restrict__ codes,
-                                                         uint8_t* __restrict__ scales) {
+__global__ void __launch_bounds__(128)
+    quant_rows_kernel(const uint16_t* x, int64_t ld, int M, int nbc, const float* gsf,
+                      uint8_t* codes, uint8_t* scales) {
   // the kernels before this one are done when the next one starts: it may read w early
   pdl_wait();
   pdl_trigger();
@@ -98,7 +96,7 @@ __global__ void __launch_bounds__(128) quant_rows_kernel(const uint16_t* __restr
   const int r = i / nbc, cb = i - r * nbc;
   const float g = *gsf;
   const uint4* src = reinterpret_cast<const uint4*>(x + r * ld + static_cast<int64_t>(cb) * 16);
-  const uint4 lo = __ldg(src), hi = __ldg(src + 1);
+  const uint4 lo = ld16(src), hi = ld16(src + 1);
   const Q16 q = quant_block(lo, hi, g);
   *reinterpret_cast<uint2*>(codes + static_cast<int64_t>(i) * 8) =
       make_uint2(q.codes[0], q.codes[1]);
@@ -316,8 +314,8 @@ __global__ void __launch_bounds__(kThreads)
         for (int j = 0; j < kFusedBlocks; ++j) {
           if (i0 + 128 * j >= all) break;
           const uint4* src = source(i0 + 128 * j, r[j], cb[j]);
-          lo[j] = __ldg(src);
-          hi[j] = __ldg(src + 1);
+          lo[j] = ld16(src);
+          hi[j] = ld16(src + 1);
         }
 #pragma unroll
         for (int j = 0; j < kFusedBlocks; ++j) {

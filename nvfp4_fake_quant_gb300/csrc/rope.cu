@@ -65,15 +65,6 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Plain load that leaves no line in L1 (q_out may be q: not a read-only load).
-__device__ __forceinline__ uint4 ld16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
 // Blocks take groups of a.tokens consecutive tokens, all heads, in turn (one wave of
 // blocks: F is formed once each).  The work item of a thread is 16 bytes of a head
 // (interleaved: 4 whole pairs) or, in the half layout, the two 16-byte vectors that

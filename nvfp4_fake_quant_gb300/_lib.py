@@ -153,6 +153,10 @@ def call(name: str, *args) -> int:
     lib = _lib or load()
     st = getattr(lib, name)(*args)
     if st != 0:
-        detail = lib.nvq_last_error_detail().decode() if st == 4 else ""
-        raise NvqError(name, st, detail)
+        fail(name, st)
     return st
+
+
+def fail(name: str, st: int):
+    """Raise the NvqError of entry point ``name``'s status ``st``."""
+    raise NvqError(name, st, load().nvq_last_error_detail().decode() if st == 4 else "")

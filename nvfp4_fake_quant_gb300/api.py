@@ -359,7 +359,9 @@ def _launch(index: int, name: str, *args) -> None:
     """The entry point on the current stream of device ``index``, with that device
     current (the library works on the current device)."""
     if index == _current_device():
-        _lib.call(name, *args, _raw_stream(index))
+        st = getattr(_lib._lib or _lib.load(), name)(*args, _raw_stream(index))
+        if st:
+            _lib.fail(name, st)
     else:
         with torch.cuda.device(index):
             _lib.call(name, *args, _raw_stream(index))
@@ -388,19 +390,24 @@ def _rows_nd(x: torch.Tensor, name: str):
     contiguous inside."""
     if not (isinstance(x, torch.Tensor) and x.dtype is BF16 and x.is_cuda):
         _check(x, name)
-    if x.dim() == 3:
-        t, h, d = x.shape
+    shape = x.shape
+    if len(shape) == 3:
+        t, h, d = shape
         row, s1, s2 = x.stride()
         if (s2 == 1 or d == 1) and (s1 == d or h == 1) or t * h * d == 0:
             return t, h, d, row if t > 1 else h * d
     raise ValueError(f"{name} must be [tokens, heads, D] with contiguous heads")
 
 
-def _check_i32(t, name, dim):
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.is_cuda):
+def _int32(t, name, dim):
+    """(shape, strides) of an int32 tensor of ``dim`` dimensions with unit last stride
+    (its device is looked at with the others', by _device_of)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32):
         _check(t, name, torch.int32)
-    if t.dim() != dim or (t.numel() > 1 and t.stride(-1) != 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != dim or (strides[-1] != 1 and t.numel() > 1):
         raise ValueError(f"{name} must be a {dim}-dimensional int32 tensor with unit last stride")
+    return shape, strides
 
 
 def _check_out(t, name, shape, dtype, like):
@@ -449,16 +456,18 @@ def nvfp4_linear_packed_fwd(x, w_codes, w_scales, w_global_sf=None, bias=None, x
     """out [M, N] bf16 = x~ w~^T (+ bias) for a weight packed by nvfp4_quantize_tiled
     (codes uint8 [N, K/2], tiled scales) under ``w_global_sf`` (None: 1).  x bf16
     [M, K], rows may be strided; ``x_global_sf`` None: 448*6/amax(x)."""
-    _check(x, "x")
+    if not (isinstance(x, torch.Tensor) and x.dtype is BF16 and x.is_cuda):
+        _check(x, "x")
     m, k, ld = _rows_ld(x)
     for t, name in ((w_codes, "w_codes"), (w_scales, "w_scales")):
-        if not (isinstance(t, torch.Tensor) and t.dtype is torch.uint8 and t.is_cuda
-                and t.is_contiguous()):
+        if not (isinstance(t, torch.Tensor) and t.dtype is torch.uint8):
             _check(t, name, torch.uint8)
+        if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-    if w_codes.dim() != 2 or w_codes.shape[1] * 2 != k:
-        raise ValueError(f"w_codes must be [N, {k // 2}], got {tuple(w_codes.shape)}")
-    n = w_codes.shape[0]
+    shape = w_codes.shape
+    if len(shape) != 2 or shape[1] * 2 != k:
+        raise ValueError(f"w_codes must be [N, {k // 2}], got {tuple(shape)}")
+    n = shape[0]
     # the 128x4 tiles of nvfp4_tiled_scale_bytes (k % 16 != 0 is refused below)
     if w_scales.numel() != -(-n // 128) * -(-(k // 16) // 4) * 512:
         raise ValueError("w_scales must be the tiled scales of w_codes")
@@ -559,16 +568,17 @@ def rope_apply(q, k, positions, inv_freq, interleaved=False, axis_pairs=None, ms
     [T, axes]; ``axis_pairs`` the number of pairs that turn by each axis (default:
     all by the first); ``inv_freq`` f64 [rot_dim/2].  q_out / k_out may be q / k."""
     t, hq, d, ld_q = _rows_nd(q, "q")
-    if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dtype is torch.float64
-            and inv_freq.is_cuda and inv_freq.dim() == 1 and inv_freq.is_contiguous()):
+    if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dtype is torch.float64):
         _check(inv_freq, "inv_freq", torch.float64)
+    shape = inv_freq.shape
+    if len(shape) != 1 or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be a contiguous vector")
-    rot = 2 * inv_freq.shape[0]
-    if not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32
-            and positions.is_cuda):
+    rot = 2 * shape[0]
+    if not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32):
         _check(positions, "positions", torch.int32)
-    axes = 1 if positions.dim() == 1 else positions.shape[1] if positions.dim() == 2 else 0
-    if axes == 0 or positions.shape[0] != t or not positions.is_contiguous():
+    shape = positions.shape
+    axes = 1 if len(shape) == 1 else shape[1] if len(shape) == 2 else 0
+    if axes == 0 or shape[0] != t or not positions.is_contiguous():
         raise ValueError(f"positions must be contiguous [{t}] or [{t}, axes]")
     pairs = (rot // 2,) + (0,) * (axes - 1) if axis_pairs is None else tuple(axis_pairs)
     if len(pairs) != axes or axes > 3:
@@ -666,17 +676,18 @@ def nvfp4_kv_pool(num_pages: int, hkv: int, d: int, device="cuda") -> torch.Tens
 
 
 def _check_cache(pool, page_table, seq_lens, d):
-    if not (isinstance(pool, torch.Tensor) and pool.dtype is torch.uint8 and pool.is_cuda
-            and pool.dim() == 3 and pool.shape[2] == 144 * d and pool.is_contiguous()):
+    """(pages, Hkv, B, max_pages, row stride of the table)."""
+    if not (isinstance(pool, torch.Tensor) and pool.dtype is torch.uint8):
         _check(pool, "pool", torch.uint8)
+    shape = pool.shape
+    if len(shape) != 3 or shape[2] != 144 * d or not pool.is_contiguous():
         raise ValueError(f"pool must be contiguous uint8 [pages, Hkv, {144 * d}], "
-                         f"got {tuple(pool.shape)}")
-    _check_i32(page_table, "page_table", 2)
-    _check_i32(seq_lens, "seq_lens", 1)
-    b, max_pages = page_table.shape
-    if len(seq_lens) != b:
-        raise ValueError(f"page_table has {b} rows, seq_lens {seq_lens.shape[0]}")
-    return b, max_pages, (page_table.stride(0) if b > 1 else max_pages)
+                         f"got {tuple(shape)}")
+    (b, max_pages), (ld, _) = _int32(page_table, "page_table", 2)
+    (n,), _ = _int32(seq_lens, "seq_lens", 1)
+    if n != b:
+        raise ValueError(f"page_table has {b} rows, seq_lens {n}")
+    return shape[0], shape[1], b, max_pages, ld if b > 1 else max_pages
 
 
 def nvfp4_kv_append(k, v, seq_lens, page_table, pool, cu_tokens=None) -> None:
@@ -687,12 +698,11 @@ def nvfp4_kv_append(k, v, seq_lens, page_table, pool, cu_tokens=None) -> None:
     tv, hv, dv, ld_v = _rows_nd(v, "v")
     if (tv, hv, dv) != (t, hkv, d):
         raise ValueError(f"v must be {(t, hkv, d)}, got {(tv, hv, dv)}")
-    b, max_pages, ld_t = _check_cache(pool, page_table, seq_lens, d)
-    if pool.shape[1] != hkv:
-        raise ValueError(f"pool has {pool.shape[1]} heads, k {hkv}")
+    pages, heads, b, max_pages, ld_t = _check_cache(pool, page_table, seq_lens, d)
+    if heads != hkv:
+        raise ValueError(f"pool has {heads} heads, k {hkv}")
     if cu_tokens is not None:
-        _check_i32(cu_tokens, "cu_tokens", 1)
-        if cu_tokens.shape[0] != b + 1:
+        if _int32(cu_tokens, "cu_tokens", 1)[0][0] != b + 1:
             raise ValueError(f"cu_tokens must have {b + 1} entries")
     elif t != b:
         raise ValueError(f"without cu_tokens one token per sequence is expected: {t} tokens, "
@@ -700,7 +710,7 @@ def nvfp4_kv_append(k, v, seq_lens, page_table, pool, cu_tokens=None) -> None:
     index = _device_of(k, v, seq_lens, page_table, pool, cu_tokens)
     _launch(index, "nvfp4_kv_append", k.data_ptr(), ld_k, v.data_ptr(), ld_v, t, b, hkv, d,
             _ptr(cu_tokens), seq_lens.data_ptr(), page_table.data_ptr(), ld_t, max_pages,
-            pool.data_ptr(), pool.shape[0])
+            pool.data_ptr(), pages)
 
 
 def attn_qat_decode_workspace(b, h, hkv, d, max_pages) -> int:
@@ -713,10 +723,9 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
     (rows may be strided), returns (o bf16 [B, H, D], lse f32 [B, H]).  ``window`` > 0:
     only the last ``window`` keys and the first ``sinks`` are visible."""
     b, h, d, ld_q = _rows_nd(q, "q")
-    bt, max_pages, ld_t = _check_cache(pool, page_table, seq_lens, d)
+    pages, hkv, bt, max_pages, ld_t = _check_cache(pool, page_table, seq_lens, d)
     if bt != b:
         raise ValueError(f"q has {b} rows, page_table {bt}")
-    hkv = pool.shape[1]
     scale = _scale(scale, d)
     o = _check_out(o, "o", (b, h, d), BF16, q)
     lse = _check_out(lse, "lse", (b, h), torch.float32, q)
@@ -725,7 +734,7 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
     if ws is None:
         ws = _workspace(_on(index, "attn_qat_decode_workspace", b, h, hkv, d, max_pages),
                         q.device, None)
-    args = (q.data_ptr(), ld_q, pool.data_ptr(), pool.shape[0], page_table.data_ptr(), ld_t,
+    args = (q.data_ptr(), ld_q, pool.data_ptr(), pages, page_table.data_ptr(), ld_t,
             max_pages, seq_lens.data_ptr(), b, h, hkv, d, scale, int(window), int(sinks),
             o.data_ptr(), lse.data_ptr())
     try:

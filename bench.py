@@ -609,6 +609,12 @@ def linear_bench(peaks, stream, steps):
                             for name, (c, t) in kt_b.items() if c}}
 
 
+def with_linear(args, ws):
+    """Whether this run times the NVFP4 linear: on one GPU only.  Its FP4 GEMM multicasts weight
+    tiles within a cluster (this GPU's own memory), and no run of several GPUs has such loads."""
+    return ws == 1 and not args.skip_linear
+
+
 def gpu_local_cpus(dev):
     """The CPUs sysfs lists as local to the GPU's PCI device (its NUMA node), or None."""
     import torch
@@ -787,8 +793,7 @@ def run_ours(args):
               if rank == 0 and not args.skip_sparse and (n, h) == (25088, 12) else None)
     hp = (hp_bench(peaks, stream, max(3, args.steps), inp, q, k, v, do, wsf, wsb)
           if rank == 0 and not args.skip_hp else None)
-    lin = linear_bench(peaks, stream, max(3, args.steps)) \
-        if rank == 0 and not args.skip_linear else None
+    lin = linear_bench(peaks, stream, max(3, args.steps)) if with_linear(args, ws) else None
 
     peak_t = peaks["bf16_tflops"]
     k_total = sum(ms for _, ms in ktimes.values())
@@ -928,6 +933,8 @@ def main(argv=None):
                                                        iters=args.steps)}), flush=True)
         return 0
     if args.linear_only:
+        if max(args.gpus, int(os.environ.get("WORLD_SIZE", "1"))) > 1:
+            ap.error("--linear-only runs on one GPU")
         import torch
         from nvfp4_fake_quant_gb300 import _lib
         _lib.load()

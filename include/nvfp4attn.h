@@ -613,6 +613,16 @@ nvq_status nvq_selftest_fp4(const void* a, const void* b, const uint32_t* sf_img
 nvq_status nvq_selftest_ex2_monotone(unsigned long long* out, nvq_stream_t stream);
 
 /*
+ * How nvfp4_linear_packed_fwd works on M <= 64 rows on the current device (152
+ * multiprocessors where there is none), without any launch: plan[0] CTAs per tile
+ * of 128 weights, [1] CTAs in all, [2] 1 if they quantize x themselves, [3] stages
+ * of 256 elements of K that a CTA takes at most, [4] stages of its ring, [5] its
+ * shared memory, [6] bytes of the scales of x in the workspace, [7] the end of the
+ * furthest of them.  NVQ_ERR_UNSUPPORTED where the call takes the GEMM instead.
+ */
+nvq_status nvq_selftest_linear_plan(int64_t M, int64_t N, int64_t K, int64_t* plan);
+
+/*
  * Launches one block that waits on a barrier nothing arrives on, with a wait
  * limit of `limit_ns` nanoseconds (1..1e9).  The wait must run out and record
  * NVQ_ERR_TIMEOUT for nvq_device_status(); nothing hangs.

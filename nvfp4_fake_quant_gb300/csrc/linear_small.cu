@@ -28,6 +28,7 @@
 // fills its ring with weights, which do not depend on x.
 #include <algorithm>
 #include <cstdint>
+#include <iterator>
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -78,10 +79,11 @@ __device__ __forceinline__ Q16 quant_block(const uint4& lo, const uint4& hi, flo
 // those of (step 2 i, r / 32 = 0), (2 i, 1), (2 i + 1, 0), (2 i + 1, 1).  One copy of a
 // block then brings the scales of two steps to 4 columns of tensor memory, where the
 // tiled layout, made for 128 rows, takes a copy per step.  The scales of rows M and up
-// are not written: the products of those rows are never stored.
-__device__ __forceinline__ int x_scale_at(int r, int cb) {
+// are not written: the products of those rows are never stored.  (Four bytes an element of
+// K, which the host admits up to 2^30: the offset needs more than 32 bits.)
+__host__ __device__ __forceinline__ int64_t x_scale_at(int r, int cb) {
   const int step = cb >> 2, w = (step & 1) * 2 + (r >> 5);
-  return (step >> 1) * 512 + (r & 31) * 16 + w * 4 + (cb & 3);
+  return static_cast<int64_t>(step >> 1) * 512 + ((r & 31) * 16 + w * 4 + (cb & 3));
 }
 
 // x [M, K] to codes and scales, one 16-element block per thread.
@@ -389,10 +391,13 @@ __global__ void __launch_bounds__(kThreads)
 
 size_t rup(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-// CTAs, and the workspace: codes and scales of x, 256-byte aligned.
+// CTAs and their shared memory, and the workspace: codes and scales of x, 256-byte aligned.
 struct SmallPlan {
   int cols, tiles, k_stages, split, ctas;
   bool fused;
+  int part, stages;   // stages of K of a CTA, at most; of its ring
+  uint32_t sums_at;   // in shared memory: the other CTAs' sums
+  size_t smem;
   size_t sx, total;
 };
 
@@ -426,8 +431,22 @@ SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
   // host's time), and time on the device up to 3.5 blocks a thread: 1 x 4608 x 1536 5.2
   // us (5.9 in two launches), 5 x 1536 x 8960 (3.1 blocks) 7.4 (7.7); 8 x 4096 x 4096 (4
   // blocks) 7.3 (7.1).  Eight stages of x, at most, lie beside the ring.
-  const int64_t part = (p.k_stages + p.split - 1) / p.split;
-  p.fused = part <= 8 && 16 * M * part <= 448;  // of 128 kFusedBlocks
+  p.part = (p.k_stages + p.split - 1) / p.split;
+  p.fused = p.part <= 8 && 16 * M * p.part <= 448;  // of 128 kFusedBlocks
+  // At most four stages, and 112 KB where there are more CTAs than one per SM leaves room
+  // for: two fit an SM then.  At least 78 KB: no three do, whose 256 tensor-memory
+  // columns each would not fit, so that no CTA waits for columns that a cluster holds
+  // which in its turn waits for that CTA's cluster.  (The library's other kernels whose
+  // CTAs wait for one another or hold tensor memory long take over 149 KB: they share no
+  // SM with these.)
+  const uint32_t x_stage = p.cols * 128u + kXs;
+  const uint32_t stage = (kW + kSc + (p.fused ? 0 : x_stage) + 1023) / 1024 * 1024;
+  const int sums = (p.split - 1) * p.cols * 512;
+  const int xs = p.fused ? p.part * static_cast<int>(x_stage) : 0;
+  const int room = (p.ctas > 128 ? 112 : 222) * 1024 - 1024 - sums - xs;
+  p.stages = std::min({kStages, p.part, room / static_cast<int>(stage)});
+  p.sums_at = p.stages * stage + xs;
+  p.smem = std::max<size_t>(p.sums_at + sums + 1024, 78 * 1024);
   p.sx = rup(static_cast<size_t>(M) * (K / 2), 256);
   p.total = p.sx + static_cast<size_t>(p.k_stages) * kXs;
   return p;
@@ -456,27 +475,16 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
                    ws + q.sx);
     if (e != cudaSuccess) return e;
   }
-  // At most four stages, and 112 KB where there are more CTAs than one per SM leaves room
-  // for: two fit an SM then.  At least 78 KB: no three do, whose 256 tensor-memory
-  // columns each would not fit, so that no CTA waits for columns that a cluster holds
-  // which in its turn waits for that CTA's cluster.  (The library's other kernels whose
-  // CTAs wait for one another or hold tensor memory long take over 149 KB: they share no
-  // SM with these.)
-  const uint32_t x_stage = q.cols * 128u + kXs;
-  const uint32_t stage = (kW + kSc + (q.fused ? 0 : x_stage) + 1023) / 1024 * 1024;
-  const int part = (q.k_stages + q.split - 1) / q.split;  // stages of a CTA, at most
-  const int sums = (q.split - 1) * q.cols * 512, xs = q.fused ? part * static_cast<int>(x_stage) : 0;
-  const int room = (q.ctas > 128 ? 112 : 222) * 1024 - 1024 - sums - xs;
+  if (q.stages < 1) return cudaErrorInvalidConfiguration;  // the plan leaves room for one and more
   SmallArgs a{};
   a.M = static_cast<int>(M);
   a.N = static_cast<int>(N);
   a.cols = q.cols;
-  a.stages = std::min({kStages, part, room / static_cast<int>(stage)});
-  if (a.stages < 1) return cudaErrorInvalidConfiguration;  // the plan leaves room for one and more
+  a.stages = q.stages;
   a.k_stages = q.k_stages;
   a.k_steps = static_cast<int>(K / 64);
   a.split = q.split;
-  a.sums_at = a.stages * stage + xs;
+  a.sums_at = q.sums_at;
   a.x = static_cast<const uint16_t*>(x);
   a.ld_x = ld_x;
   a.sx = ws + q.sx;
@@ -486,11 +494,25 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
   a.bias = static_cast<const __nv_bfloat16*>(bias);
   a.out = static_cast<__nv_bfloat16*>(out);
   a.err = err;
-  const size_t smem = std::max<size_t>(a.sums_at + sums + 1024, 78 * 1024);
   const auto kernel = q.fused ? linear_small_kernel<true> : linear_small_kernel<false>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(q.ctas), dim3(kThreads), smem, stream, q.split, tx, tw, a);
+  return launch_pdl(kernel, dim3(q.ctas), dim3(kThreads), q.smem, stream, q.split, tx, tw, a);
 }
 
 }  // namespace nvq
+
+extern "C" nvq_status nvq_selftest_linear_plan(int64_t M, int64_t N, int64_t K, int64_t* plan) {
+  using namespace nvq;
+  if (plan == nullptr || M < 1 || N < 1 || N % 16 != 0 || K < 1 || K % 64 != 0)
+    return NVQ_ERR_INVALID;
+  if (!linear_small_takes(M, N, K)) return NVQ_ERR_UNSUPPORTED;
+  const SmallPlan p = small_plan(M, N, K);
+  int64_t end = 0;  // the last block's scales lie furthest
+  for (int r = 0; r < M; ++r)
+    end = std::max(end, x_scale_at(r, static_cast<int>(K / 16) - 1) + 1);
+  const int64_t got[] = {p.split, p.ctas, p.fused, p.part, p.stages,
+                         static_cast<int64_t>(p.smem), static_cast<int64_t>(p.total - p.sx), end};
+  std::copy(std::begin(got), std::end(got), plan);
+  return NVQ_OK;
+}

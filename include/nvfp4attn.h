@@ -412,7 +412,8 @@ nvq_status nvfp4_linear_bwd(const void* grad_out, const void* x, const void* w, 
  *   w_codes  uint8 [N, K/2], w_scales nvfp4_tiled_scale_bytes(N, K) bytes, as
  *            nvfp4_quantize_tiled wrote them (16-byte aligned); w_global_sf the
  *            device fp32 scalar it was given (NULL: 1.0)
- *   bias     bf16 [N] or NULL; out bf16 [M, N] contiguous; 16-byte aligned
+ *   bias     bf16 [N] or NULL; out bf16 [M, N] contiguous, outside the range of
+ *            memory that x's rows span; 16-byte aligned
  * M >= 1, K % 64 == 0 and N % 16 == 0 (else NVQ_ERR_UNSUPPORTED).  On the same
  * operands and scales the result is nvfp4_linear_fwd's up to the order of the
  * fp32 sums over K.  ws: nvfp4_linear_packed_workspace(M, N, K) bytes, 256-byte

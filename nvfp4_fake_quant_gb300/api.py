@@ -455,7 +455,7 @@ def nvfp4_linear_packed_fwd(x, w_codes, w_scales, w_global_sf=None, bias=None, x
                             out=None, workspace=None):
     """out [M, N] bf16 = x~ w~^T (+ bias) for a weight packed by nvfp4_quantize_tiled
     (codes uint8 [N, K/2], tiled scales) under ``w_global_sf`` (None: 1).  x bf16
-    [M, K], rows may be strided; ``x_global_sf`` None: 448*6/amax(x)."""
+    [M, K], rows may be strided, not under ``out``; ``x_global_sf`` None: 448*6/amax(x)."""
     if not (isinstance(x, torch.Tensor) and x.dtype is BF16 and x.is_cuda):
         _check(x, "x")
     m, k, ld = _rows_ld(x)

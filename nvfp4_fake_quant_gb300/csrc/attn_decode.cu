@@ -1009,10 +1009,9 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
   if (ws == nullptr || ws_bytes < p.total || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return NVQ_ERR_WORKSPACE;
   // q is read by every run of its sequence, at whatever time: o elsewhere
-  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
   const int64_t row = static_cast<int64_t>(H) * D;
-  if (q0 < o0 + static_cast<uint64_t>(2 * row * B) &&
-      o0 < q0 + static_cast<uint64_t>(2 * ((B - 1) * ld_q + row)))
+  if (ranges_meet(q, 2 * static_cast<uint64_t>((B - 1) * ld_q + row), o,
+                  2 * static_cast<uint64_t>(row * B)))
     return NVQ_ERR_INVALID;
   int* err = device_error_word();
   if (err == nullptr) return NVQ_ERR_CUDA;

@@ -269,6 +269,11 @@ nvq_status nvfp4_linear_packed_fwd(const void* x, int64_t ld_x, const uint8_t* w
   const nvq::PackedWs L = nvq::packed_ws(M, N, K);
   if (ws == nullptr || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return NVQ_ERR_WORKSPACE;
+  // x may be read until the last output is written (the few-rows kernel's CTAs quantize it
+  // themselves, one after another): out elsewhere
+  if (nvq::ranges_meet(x, 2 * static_cast<uint64_t>((M - 1) * ld_x + K), out,
+                  2 * static_cast<uint64_t>(M) * static_cast<uint64_t>(N)))
+    return NVQ_ERR_INVALID;
   uint8_t* wb = static_cast<uint8_t*>(ws);
   float* ab = reinterpret_cast<float*>(wb + L.ab);
   const float* gx = x_global_sf;

@@ -113,6 +113,12 @@ cudaError_t timed(int kind, cudaStream_t stream, F&& launch) {
   return launch();
 }
 
+// Whether the bytes [a, a + a_bytes) and [b, b + b_bytes) meet.
+inline bool ranges_meet(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + b_bytes && b0 < a0 + a_bytes;
+}
+
 // Multiprocessors of the current device (152 where there is none to ask).
 inline int device_sms() {
   int dev = 0, sms = 0;

@@ -417,9 +417,8 @@ nvq_status nvfp4_linear_bwd(const void* grad_out, const void* x, const void* w, 
  * M >= 1, K % 64 == 0 and N % 16 == 0 (else NVQ_ERR_UNSUPPORTED).  On the same
  * operands and scales the result is nvfp4_linear_fwd's up to the order of the
  * fp32 sums over K.  ws: nvfp4_linear_packed_workspace(M, N, K) bytes, 256-byte
- * aligned; its size follows from the current device's multiprocessor count.
- * The backward of a packed weight is not defined: train with nvfp4_linear_fwd /
- * nvfp4_linear_bwd, then pack.
+ * aligned, on every device the same.  The backward of a packed weight is not
+ * defined: train with nvfp4_linear_fwd / nvfp4_linear_bwd, then pack.
  */
 size_t nvfp4_linear_packed_workspace(int64_t M, int64_t N, int64_t K);
 nvq_status nvfp4_linear_packed_fwd(const void* x, int64_t ld_x, const uint8_t* w_codes,

@@ -479,7 +479,7 @@ def nvfp4_linear_packed_fwd(x, w_codes, w_scales, w_global_sf=None, bias=None, x
     out = _check_out(out, "out", (m, n), BF16, x)
     ws = workspace
     if ws is None:
-        ws = _workspace(_on(index, "nvfp4_linear_packed_workspace", m, n, k), x.device, None)
+        ws = _workspace(nvfp4_linear_packed_workspace(m, n, k), x.device, None)
     args = (x.data_ptr(), ld if m > 1 else k, w_codes.data_ptr(), w_scales.data_ptr(),
             _opt_ptr(w_global_sf), None if bias is None else bias.data_ptr(), m, n, k,
             _opt_ptr(x_global_sf), out.data_ptr())
@@ -490,7 +490,7 @@ def nvfp4_linear_packed_fwd(x, w_codes, w_scales, w_global_sf=None, bias=None, x
         if e.status != 3 or workspace is None:
             raise
         # the caller's workspace is too small (or misaligned): one of our own, as elsewhere
-        ws = _workspace(_on(index, "nvfp4_linear_packed_workspace", m, n, k), x.device, None)
+        ws = _workspace(nvfp4_linear_packed_workspace(m, n, k), x.device, None)
         _launch(index, "nvfp4_linear_packed_fwd", *args, ws.data_ptr(), ws.numel())
     return out
 

@@ -56,7 +56,7 @@ PackedWs packed_ws(int64_t M, int64_t N, int64_t K) {
   PackedWs w{};
   w.small = linear_small_takes(M, N, K);
   if (w.small) {
-    w.gx = rup(linear_small_workspace(M, N, K), 256);
+    w.gx = rup(linear_small_workspace(M, K), 256);
   } else {
     w.sx = rup(static_cast<size_t>(M) * static_cast<size_t>(K / 2), 256);
     w.ab = w.sx + rup(tiled_scale_bytes(M, K), 256);

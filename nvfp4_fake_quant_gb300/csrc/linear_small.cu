@@ -391,14 +391,17 @@ __global__ void __launch_bounds__(kThreads)
 
 size_t rup(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-// CTAs and their shared memory, and the workspace: codes and scales of x, 256-byte aligned.
+// The workspace: codes of x, its scales at a 256-byte boundary.
+size_t scales_at(int64_t M, int64_t K) { return rup(static_cast<size_t>(M) * (K / 2), 256); }
+size_t scale_bytes(int64_t K) { return static_cast<size_t>((K + 255) / 256) * kXs; }
+
+// CTAs and their shared memory.
 struct SmallPlan {
   int cols, tiles, k_stages, split, ctas;
   bool fused;
   int part, stages;   // stages of K of a CTA, at most; of its ring
   uint32_t sums_at;   // in shared memory: the other CTAs' sums
   size_t smem;
-  size_t sx, total;
 };
 
 SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
@@ -447,8 +450,6 @@ SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
   p.stages = std::min({kStages, p.part, room / static_cast<int>(stage)});
   p.sums_at = p.stages * stage + xs;
   p.smem = std::max<size_t>(p.sums_at + sums + 1024, 78 * 1024);
-  p.sx = rup(static_cast<size_t>(M) * (K / 2), 256);
-  p.total = p.sx + static_cast<size_t>(p.k_stages) * kXs;
   return p;
 }
 
@@ -460,19 +461,19 @@ bool linear_small_takes(int64_t M, int64_t N, int64_t K) {
          M * (K / 16) < (int64_t{1} << 31) - 128;
 }
 
-size_t linear_small_workspace(int64_t M, int64_t N, int64_t K) { return small_plan(M, N, K).total; }
+size_t linear_small_workspace(int64_t M, int64_t K) { return scales_at(M, K) + scale_bytes(K); }
 
 cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
                                 const CUtensorMap& tx, const CUtensorMap& tw, const uint8_t* sw,
                                 const float* gw, const void* bias, int64_t M, int64_t N, int64_t K,
                                 void* out, uint8_t* ws, int* err, cudaStream_t stream) {
   const SmallPlan q = small_plan(M, N, K);
+  uint8_t* const sx = ws + scales_at(M, K);
   cudaError_t e = cudaSuccess;
   if (!q.fused) {
     const int nbc = static_cast<int>(K / 16), blocks = static_cast<int>(M) * nbc;
     e = launch_pdl(quant_rows_kernel, dim3((blocks + 127) / 128), dim3(128), 0, stream, 1,
-                   static_cast<const uint16_t*>(x), ld_x, static_cast<int>(M), nbc, gx, ws,
-                   ws + q.sx);
+                   static_cast<const uint16_t*>(x), ld_x, static_cast<int>(M), nbc, gx, ws, sx);
     if (e != cudaSuccess) return e;
   }
   if (q.stages < 1) return cudaErrorInvalidConfiguration;  // the plan leaves room for one and more
@@ -487,7 +488,7 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
   a.sums_at = q.sums_at;
   a.x = static_cast<const uint16_t*>(x);
   a.ld_x = ld_x;
-  a.sx = ws + q.sx;
+  a.sx = sx;
   a.sw = sw;
   a.gx = gx;
   a.gw = gw;
@@ -512,7 +513,7 @@ extern "C" nvq_status nvq_selftest_linear_plan(int64_t M, int64_t N, int64_t K, 
   for (int r = 0; r < M; ++r)
     end = std::max(end, x_scale_at(r, static_cast<int>(K / 16) - 1) + 1);
   const int64_t got[] = {p.split, p.ctas, p.fused, p.part, p.stages,
-                         static_cast<int64_t>(p.smem), static_cast<int64_t>(p.total - p.sx), end};
+                         static_cast<int64_t>(p.smem), static_cast<int64_t>(scale_bytes(K)), end};
   std::copy(std::begin(got), std::end(got), plan);
   return NVQ_OK;
 }

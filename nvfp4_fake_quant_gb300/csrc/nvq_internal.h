@@ -250,10 +250,10 @@ cudaError_t launch_gemm_bf16_pair(const CUtensorMap& ta0, const CUtensorMap& tb0
 
 // The packed linear of few rows (linear_small.cu).  ws holds the codes of x at its
 // base (tx: make_codes_map over them, box of M rounded up to 16 rows), then the rest
-// of linear_small_workspace(M, N, K) bytes; tw: make_codes_map over w's codes.
+// of linear_small_workspace(M, K) bytes; tw: make_codes_map over w's codes.
 constexpr int64_t kLinearSmallRows = 64;
 bool linear_small_takes(int64_t M, int64_t N, int64_t K);
-size_t linear_small_workspace(int64_t M, int64_t N, int64_t K);
+size_t linear_small_workspace(int64_t M, int64_t K);
 cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
                                 const CUtensorMap& tx, const CUtensorMap& tw, const uint8_t* sw,
                                 const float* gw, const void* bias, int64_t M, int64_t N, int64_t K,

@@ -33,3 +33,13 @@ def test_plan_refusals():
     for m, n, k, out in ((0, 16, 64, at), (1, 24, 64, at), (1, 16, 32, at), (1, 16, 64, None)):
         assert lib.nvq_selftest_linear_plan(m, n, k, out) == 1
     assert lib.nvq_selftest_linear_plan(65, 16, 64, at) == 2
+
+
+@pytest.mark.parametrize("m,k", [(1, 64), (5, 8960), (33, 2112), (64, 16384)])
+def test_workspace_follows_from_x_alone(m, k):
+    """Codes of x, its scales at a 256-byte boundary, one scalar: whatever the weights' rows
+    and the device are."""
+    lib = _lib.load(nvbuild.build())
+    want = -(-m * k // 2 // 256) * 256 + -(-k // 256) * 1024 + 256
+    for n in (16, 4608, 53248):
+        assert lib.nvfp4_linear_packed_workspace(m, n, k) == want

@@ -9,15 +9,16 @@ import torch
 from nvfp4_fake_quant_gb300 import api, workloads
 from oracle import linear as ol
 from oracle import nvfp4 as onv
+from test_linear_plan import LAYOUTS, plan
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
 
 
-def bound(x, w, gx, gw, ref):
-    """x, w: the columns that are not zero in either."""
+def sum_bound(x, w, gx, gw):
+    """The bound without the result's rounding; x, w: the columns that are not zero in either."""
     mag = onv.fq(x, gx).abs() @ onv.fq(w, gw).abs().T
-    return ref.abs() * 2.0 ** -8 + mag * (x.shape[1] * 2.0 ** -23 + 2.0 ** -21)
+    return mag * (x.shape[1] * 2.0 ** -23 + 2.0 ** -21)
 
 
 def guarded_workspace(m, n, k, guard=4096):
@@ -51,4 +52,43 @@ def test_scales_of_x_past_31_bits_of_offset():
     ref = ol.linear_fwd(inp.x, inp.w, None, gx, gw)
     err = (out.cpu().double() - ref).abs()
     # the other columns' products are zero and add nothing to the sum's error
-    assert bool((err <= bound(inp.x, inp.w, gx, gw, ref)).all())
+    tol = ref.abs() * 2.0 ** -8 + sum_bound(inp.x, inp.w, gx, gw)
+    assert bool((err <= tol).all())
+
+
+@pytest.mark.parametrize("case", LAYOUTS, ids=lambda c: "x".join(map(str, c[:3])))
+@pytest.mark.parametrize("given_scale", [True, False])
+def test_parity_in_every_layout(case, given_scale):
+    """The layout is the one that the size is there for, on this device too.  The weight's rows
+    are 144 different ones in an order that no two tiles share."""
+    m, n, k, split, fused, stages, rounds, crowded = case
+    p = plan(m, n, k)
+    assert (p["split"], p["fused"], p["stages"], -(-p["part"] // p["stages"])) == \
+        (split, fused, stages, rounds)
+    inp = workloads.linear_inputs(m, 144, k, seed=m + n + k)
+    rows = torch.randint(0, 144, (n,), generator=torch.Generator().manual_seed(n))
+    rows[:min(n, 144)] = torch.arange(min(n, 144))
+    gw = onv.global_sf(inp.w[rows])
+    gx = 300.0 if given_scale else onv.global_sf(inp.x)
+    wg, xg = (torch.tensor([g], dtype=torch.float32, device="cuda") for g in (gw, gx))
+    codes, scales = api.nvfp4_quantize_tiled(inp.w[rows].cuda(), wg)
+    bias = inp.bias[rows].cuda() if given_scale else None
+    ws, buf = guarded_workspace(m, n, k)
+    ws.fill_(0xFF)
+    obuf = torch.full((m * n + 64,), float("nan"), dtype=BF16, device="cuda")
+    out = obuf[32:-32].view(m, n)
+    args = (inp.x.cuda(), codes, scales, wg, bias, xg if given_scale else None)
+    api.nvfp4_linear_packed_fwd(*args, out=out, workspace=ws)
+    assert api.device_status() == 0
+    assert bool((buf[:4096] == 0xA5).all()) and bool((buf[-4096:] == 0xA5).all())
+    assert bool(obuf[:32].isnan().all()) and bool(obuf[-32:].isnan().all())
+    ref = ol.linear_fwd(inp.x, inp.w, None, gx, gw)[:, rows]
+    tol = sum_bound(inp.x, inp.w, gx, gw)[:, rows]
+    if given_scale:
+        b = inp.bias.double()[rows]
+        ref = ref + b
+        tol = tol + b.abs() * 2.0 ** -21
+    tol = tol + ref.abs() * 2.0 ** -8
+    err = (out.cpu().double() - ref).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
+    assert torch.equal(api.nvfp4_linear_packed_fwd(*args, workspace=ws), out)  # run to run

@@ -43,3 +43,39 @@ def test_workspace_follows_from_x_alone(m, k):
     want = -(-m * k // 2 // 256) * 256 + -(-k // 256) * 1024 + 256
     for n in (16, 4608, 53248):
         assert lib.nvfp4_linear_packed_workspace(m, n, k) == want
+
+
+# m, n, k and the layout each is there for: CTAs a tile, x quantized by them, stages of the
+# ring, times that a CTA goes around it (rounded up), more CTAs than multiprocessors
+LAYOUTS = [
+    (64, 128, 32768, 4, 0, 4, 8, 0), (33, 272, 24640, 5, 0, 4, 5, 0), (1, 128, 32768, 8, 0, 4, 4, 0),
+    (1, 8192, 1024, 3, 1, 2, 1, 1), (32, 10240, 8192, 2, 0, 4, 4, 1), (16, 8320, 4096, 3, 0, 4, 2, 1),
+    (64, 8320, 2240, 2, 0, 2, 3, 0), (1, 7680, 5632, 3, 1, 3, 3, 1), (8, 4992, 4160, 4, 0, 4, 2, 1),
+    (4, 39056, 2112, 1, 0, 4, 3, 1), (1, 19584, 1280, 1, 1, 4, 2, 1), (17, 1664, 6464, 6, 0, 4, 2, 0),
+    (31, 128, 1792, 7, 0, 1, 1, 0), (31, 144, 2048, 8, 0, 1, 1, 0), (1, 128, 1600, 7, 1, 1, 1, 0),
+    (1, 4992, 6464, 4, 1, 3, 3, 1), (64, 1920, 8192, 4, 0, 4, 2, 0),
+]
+
+
+@pytest.mark.parametrize("case", LAYOUTS, ids=lambda c: "x".join(map(str, c[:3])))
+def test_layouts(case):
+    m, n, k, split, fused, stages, rounds, crowded = case
+    p = plan(m, n, k)
+    got = (p["split"], p["fused"], p["stages"], -(-p["part"] // p["stages"]), int(p["ctas"] > 152))
+    assert got == (split, fused, stages, rounds, crowded)
+
+
+def test_every_plan_keeps_its_promises():
+    """Over many sizes: a stage for the ring, the shared memory a block may have, two blocks an
+    SM where there are more of them than fit one each, and never three (each holds half of the
+    tensor memory)."""
+    sms, smem = 152, 228 * 1024
+    for m in (1, 3, 16, 17, 28, 32, 33, 48, 49, 64):
+        for tiles in [*range(1, 50), 65, 76, 100, 152, 153, 304, 400]:
+            for k in [64, *range(256, 9000, 448), 16384, 65536]:
+                p = plan(m, 128 * tiles, k // 64 * 64)
+                assert 1 <= p["stages"] <= p["part"] and p["split"] <= 8
+                assert p["ctas"] == p["split"] * tiles
+                assert p["smem"] <= 227 * 1024 and 3 * (p["smem"] + 1024) > smem
+                if p["ctas"] > sms:
+                    assert 2 * (p["smem"] + 1024) <= smem

@@ -610,20 +610,22 @@ def rope_apply(q, k, positions, inv_freq, interleaved=False, axis_pairs=None, ms
 
 
 class RotaryFunction(torch.autograd.Function):
-    """rope_apply with its gradient (the rotation back, scaled alike)."""
+    """rope_apply with its gradient (the rotation back, scaled alike), of any order: the
+    backward is this function with the direction turned."""
 
     @staticmethod
-    def forward(ctx, q, k, positions, inv_freq, interleaved, axis_pairs, mscale):
+    def forward(ctx, q, k, positions, inv_freq, interleaved, axis_pairs, mscale, inverse=False):
         ctx.save_for_backward(positions, inv_freq)
-        ctx.args = (interleaved, axis_pairs, mscale)
+        ctx.args = (interleaved, axis_pairs, mscale, inverse)
         return rope_apply(q, k, positions, inv_freq, *ctx.args)
 
     @staticmethod
     def backward(ctx, gq, gk):
         positions, inv_freq = ctx.saved_tensors
-        gq, gk = rope_apply(_loadable(gq), _loadable(gk), positions, inv_freq, *ctx.args,
-                            inverse=True)
-        return gq, gk, None, None, None, None, None
+        *args, inverse = ctx.args
+        gq, gk = RotaryFunction.apply(_loadable(gq), _loadable(gk), positions, inv_freq, *args,
+                                      not inverse)
+        return gq, gk, None, None, None, None, None, None
 
 
 class Rotary(torch.nn.Module):

@@ -420,6 +420,14 @@ def _check_out(t, name, shape, dtype, like):
     return t
 
 
+def _overwritten(*outs):
+    """Tells autograd that the caller's tensors have been written, as torch's own in-place
+    operations do: a graph that saved one of them refuses its backward."""
+    for t in outs:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _loadable(x: torch.Tensor):
     """x [rows, ...] itself where the kernels read its layout (contiguous rows with a
     stride of whole 16-byte units), else a contiguous copy: heads or features of another
@@ -476,7 +484,7 @@ def nvfp4_linear_packed_fwd(x, w_codes, w_scales, w_global_sf=None, bias=None, x
         if bias.dim() != 1 or bias.shape[0] != n or not bias.is_contiguous():
             raise ValueError(f"bias must be contiguous [{n}]")
     index = _device_of(x, w_codes, w_scales, w_global_sf, bias, x_global_sf, out, workspace)
-    out = _check_out(out, "out", (m, n), BF16, x)
+    given, out = out, _check_out(out, "out", (m, n), BF16, x)
     ws = workspace
     if ws is None:
         ws = _workspace(nvfp4_linear_packed_workspace(m, n, k), x.device, None)
@@ -492,6 +500,7 @@ def nvfp4_linear_packed_fwd(x, w_codes, w_scales, w_global_sf=None, bias=None, x
         # the caller's workspace is too small (or misaligned): one of our own, as elsewhere
         ws = _workspace(nvfp4_linear_packed_workspace(m, n, k), x.device, None)
         _launch(index, "nvfp4_linear_packed_fwd", *args, ws.data_ptr(), ws.numel())
+    _overwritten(given)
     return out
 
 
@@ -566,7 +575,9 @@ def rope_apply(q, k, positions, inv_freq, interleaved=False, axis_pairs=None, ms
     """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (bf16, token rows may be
     strided; k may be None): returns (q_out, k_out).  ``positions`` int32 [T] or
     [T, axes]; ``axis_pairs`` the number of pairs that turn by each axis (default:
-    all by the first); ``inv_freq`` f64 [rot_dim/2].  q_out / k_out may be q / k."""
+    all by the first); ``inv_freq`` f64 [rot_dim/2].  q_out / k_out may be q / k: the raw
+    call is outside autograd (Rotary is inside), whose graphs that saved them then refuse
+    their backward."""
     t, hq, d, ld_q = _rows_nd(q, "q")
     if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dtype is torch.float64):
         _check(inv_freq, "inv_freq", torch.float64)
@@ -580,6 +591,7 @@ def rope_apply(q, k, positions, inv_freq, interleaved=False, axis_pairs=None, ms
     axes = 1 if len(shape) == 1 else shape[1] if len(shape) == 2 else 0
     if axes == 0 or shape[0] != t or not positions.is_contiguous():
         raise ValueError(f"positions must be contiguous [{t}] or [{t}, axes]")
+    given = (q_out, k_out)
     pairs = (rot // 2,) + (0,) * (axes - 1) if axis_pairs is None else tuple(axis_pairs)
     if len(pairs) != axes or axes > 3:
         raise ValueError(f"axis_pairs must give one count for each of 1..3 axes, got {pairs}")
@@ -606,6 +618,7 @@ def rope_apply(q, k, positions, inv_freq, interleaved=False, axis_pairs=None, ms
     _launch(index, "rope_apply", q.data_ptr(), ld_q, q_out.data_ptr(), ld_qo, hq, _ptr(k), ld_k,
             _ptr(k_out), ld_ko, hk, t, d, rot, int(bool(interleaved)), positions.data_ptr(), axes,
             _host_ints(pairs), inv_freq.data_ptr(), float(mscale), int(bool(inverse)))
+    _overwritten(*given)
     return q_out, k_out
 
 
@@ -713,6 +726,7 @@ def nvfp4_kv_append(k, v, seq_lens, page_table, pool, cu_tokens=None) -> None:
     _launch(index, "nvfp4_kv_append", k.data_ptr(), ld_k, v.data_ptr(), ld_v, t, b, hkv, d,
             _ptr(cu_tokens), seq_lens.data_ptr(), page_table.data_ptr(), ld_t, max_pages,
             pool.data_ptr(), pages)
+    _overwritten(pool)
 
 
 def attn_qat_decode_workspace(b, h, hkv, d, max_pages) -> int:
@@ -729,6 +743,7 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
     if bt != b:
         raise ValueError(f"q has {b} rows, page_table {bt}")
     scale = _scale(scale, d)
+    given = (o, lse)
     o = _check_out(o, "o", (b, h, d), BF16, q)
     lse = _check_out(lse, "lse", (b, h), torch.float32, q)
     index = _device_of(q, pool, page_table, seq_lens, o, lse, workspace)
@@ -748,6 +763,7 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
         ws = _workspace(_on(index, "attn_qat_decode_workspace", b, h, hkv, d, max_pages),
                         q.device, None)
         _launch(index, "attn_qat_decode", *args, ws.data_ptr(), ws.numel())
+    _overwritten(*given)
     return o, lse
 
 

@@ -499,7 +499,7 @@ size_t nvfp4_kv_page_bytes(int Hkv, int D);
  *              Tokens that would fall before position 0 are ignored (a padded
  *              batch gives its empty places length 0)
  * Two sequences must not be given the same page for new tokens.  T == 0 is a
- * valid call that does nothing.
+ * valid call that does nothing; B >= 1.
  */
 nvq_status nvfp4_kv_append(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int64_t T,
                            int B, int Hkv, int D, const int32_t* cu_tokens,
@@ -520,7 +520,7 @@ nvq_status nvfp4_kv_append(const void* k, int64_t ld_k, const void* v, int64_t l
  * Visible keys: all j < seq_lens[b] when window == 0; with window > 0 the last
  * `window` of them and the first `sinks`.  The new token's own K and V are in
  * the cache (append first).  A sequence without visible keys gets o = 0 and
- * lse = -inf.  D in {64, 128}; window, sinks >= 0; B, H <= 65535, B*H < 2^31,
+ * lse = -inf.  D in {64, 128}; window, sinks >= 0; 1 <= B, H <= 65535, B*H < 2^31,
  * B*H*max_pages <= 2^53 (else NVQ_ERR_UNSUPPORTED).  Long sequences are split
  * over the GPU and joined in a fixed order: results do not vary from run to run.
  * ws: attn_qat_decode_workspace(B, H, Hkv, D, max_pages) bytes, 256-byte

@@ -463,7 +463,8 @@ def nvfp4_linear_packed_fwd(x, w_codes, w_scales, w_global_sf=None, bias=None, x
                             out=None, workspace=None):
     """out [M, N] bf16 = x~ w~^T (+ bias) for a weight packed by nvfp4_quantize_tiled
     (codes uint8 [N, K/2], tiled scales) under ``w_global_sf`` (None: 1).  x bf16
-    [M, K], rows may be strided, not under ``out``; ``x_global_sf`` None: 448*6/amax(x)."""
+    [M, K], rows may be strided, not under ``out``; ``x_global_sf`` None: 448*6/amax(x).
+    No rows (M = 0) is a valid call that launches nothing."""
     if not (isinstance(x, torch.Tensor) and x.dtype is BF16 and x.is_cuda):
         _check(x, "x")
     m, k, ld = _rows_ld(x)
@@ -485,6 +486,8 @@ def nvfp4_linear_packed_fwd(x, w_codes, w_scales, w_global_sf=None, bias=None, x
             raise ValueError(f"bias must be contiguous [{n}]")
     index = _device_of(x, w_codes, w_scales, w_global_sf, bias, x_global_sf, out, workspace)
     given, out = out, _check_out(out, "out", (m, n), BF16, x)
+    if m == 0 and nvfp4_linear_packed_workspace(1, n, k):  # no rows of a layer that is served
+        return out
     ws = workspace
     if ws is None:
         ws = _workspace(nvfp4_linear_packed_workspace(m, n, k), x.device, None)
@@ -708,7 +711,8 @@ def _check_cache(pool, page_table, seq_lens, d):
 def nvfp4_kv_append(k, v, seq_lens, page_table, pool, cu_tokens=None) -> None:
     """Quantizes new tokens' k, v (bf16 [T, Hkv, D], token rows may be strided) into the
     pages of ``pool``.  seq_lens int32 [B]: lengths after the append; page_table int32
-    [B, max_pages]; cu_tokens int32 [B + 1] (None: one token per sequence)."""
+    [B, max_pages]; cu_tokens int32 [B + 1] (None: one token per sequence).  No tokens, or
+    no sequences, is a valid call that does nothing."""
     t, hkv, d, ld_k = _rows_nd(k, "k")
     tv, hv, dv, ld_v = _rows_nd(v, "v")
     if (tv, hv, dv) != (t, hkv, d):
@@ -723,6 +727,8 @@ def nvfp4_kv_append(k, v, seq_lens, page_table, pool, cu_tokens=None) -> None:
         raise ValueError(f"without cu_tokens one token per sequence is expected: {t} tokens, "
                          f"{b} sequences")
     index = _device_of(k, v, seq_lens, page_table, pool, cu_tokens)
+    if b == 0 and t == 0 and nvfp4_kv_page_bytes(hkv, d):  # no sequences
+        return
     _launch(index, "nvfp4_kv_append", k.data_ptr(), ld_k, v.data_ptr(), ld_v, t, b, hkv, d,
             _ptr(cu_tokens), seq_lens.data_ptr(), page_table.data_ptr(), ld_t, max_pages,
             pool.data_ptr(), pages)
@@ -737,7 +743,8 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
                     workspace=None):
     """Attention of one new token per sequence over the paged cache: q bf16 [B, H, D]
     (rows may be strided), returns (o bf16 [B, H, D], lse f32 [B, H]).  ``window`` > 0:
-    only the last ``window`` keys and the first ``sinks`` are visible."""
+    only the last ``window`` keys and the first ``sinks`` are visible.  No sequences (B = 0)
+    is a valid call that launches nothing."""
     b, h, d, ld_q = _rows_nd(q, "q")
     pages, hkv, bt, max_pages, ld_t = _check_cache(pool, page_table, seq_lens, d)
     if bt != b:
@@ -747,6 +754,8 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
     o = _check_out(o, "o", (b, h, d), BF16, q)
     lse = _check_out(lse, "lse", (b, h), torch.float32, q)
     index = _device_of(q, pool, page_table, seq_lens, o, lse, workspace)
+    if b == 0 and attn_qat_decode_workspace(1, h, hkv, d, max(max_pages, 1)):  # no sequences
+        return o, lse
     ws = workspace
     if ws is None:
         ws = _workspace(_on(index, "attn_qat_decode_workspace", b, h, hkv, d, max_pages),

@@ -539,16 +539,22 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
 
 /* Kernel kinds the library launches. */
 enum {
-  NVQ_KERNEL_QUANTIZE = 0,   /* NVFP4 fake-quant / codes pass (also inside the attention calls); cache append */
-  NVQ_KERNEL_ATTN_FWD = 1,   /* attention forward; single tokens over the cache (with the join) */
+  NVQ_KERNEL_QUANTIZE = 0,   /* NVFP4 fake-quant / codes pass (also inside the attention calls) */
+  NVQ_KERNEL_ATTN_FWD = 1,   /* attention forward */
   NVQ_KERNEL_BWD_DELTA = 2,  /* backward pre-pass delta = rowsum(dO * o) */
   NVQ_KERNEL_BWD_DKDV = 3,   /* backward, key-outer dK and dV kernel */
   NVQ_KERNEL_BWD_DQ = 4,     /* backward, query-outer dQ kernel */
   NVQ_KERNEL_GLOBAL_SF = 5,  /* static global scale (amax reduction and finalize) */
-  NVQ_KERNEL_VSA = 6,        /* block-sparse support: token reorder, block selection, list
-                                transpose; rotary positions */
-  NVQ_KERNEL_LINEAR = 7,     /* NVFP4 linear: the FP4 and BF16 GEMMs and the bias gradient */
-  NVQ_KERNEL_KINDS = 8
+  NVQ_KERNEL_VSA = 6,        /* block-sparse support: token reorder, block selection, list transpose */
+  NVQ_KERNEL_LINEAR = 7,     /* NVFP4 linear: the FP4 and BF16 GEMMs and the bias gradient; the
+                                packed linear (of few rows with x's quantization) */
+  NVQ_KERNEL_KINDS = 8,
+  /* what serves a trained model, numbered apart so that the kinds above stay what they were */
+  NVQ_KERNEL_SERVING = 16,
+  NVQ_KERNEL_ROPE = 16,      /* rotary positions */
+  NVQ_KERNEL_KV_APPEND = 17, /* new tokens into the paged cache */
+  NVQ_KERNEL_DECODE = 18,    /* single tokens over the cache (with the join) */
+  NVQ_KERNEL_SERVING_END = 19
 };
 
 /*

@@ -779,6 +779,7 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
 # Kernel kinds of nvq_timing_read (include/nvfp4attn.h, NVQ_KERNEL_*)
 KERNEL_KINDS = {"quantize": 0, "attn_fwd": 1, "bwd_delta": 2, "bwd_dkdv": 3, "bwd_dq": 4,
                 "global_sf": 5, "vsa": 6, "linear": 7}
+SERVING_KINDS = {"rope": 16, "kv_append": 17, "decode": 18}
 
 
 def timing_enable(on: bool = True) -> None:
@@ -787,13 +788,15 @@ def timing_enable(on: bool = True) -> None:
 
 
 def timing_read() -> dict:
-    """{kind: (launches, total_ms)} for the launches recorded since timing_enable(True)."""
+    """{kind: (launches, total_ms)} for the launches recorded since timing_enable(True):
+    every kind of KERNEL_KINDS, and those of SERVING_KINDS that were launched."""
     import ctypes
     out = {}
-    for name, kind in KERNEL_KINDS.items():
+    for name, kind in (KERNEL_KINDS | SERVING_KINDS).items():
         n, ms = ctypes.c_int64(0), ctypes.c_double(0.0)
         _lib.call("nvq_timing_read", kind, ctypes.addressof(n), ctypes.addressof(ms))
-        out[name] = (int(n.value), float(ms.value))
+        if n.value or name in KERNEL_KINDS:
+            out[name] = (int(n.value), float(ms.value))
     return out
 
 

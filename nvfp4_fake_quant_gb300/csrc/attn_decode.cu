@@ -1027,7 +1027,7 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
                      reinterpret_cast<RunInfo*>(wb), p.by_segment,
                      reinterpret_cast<float*>(wb + p.parts), p.runs,
                      ~uint64_t{0} / p.runs + 1, err};
-  const cudaError_t e = timed(NVQ_KERNEL_ATTN_FWD, stream, [&] {
+  const cudaError_t e = timed(NVQ_KERNEL_DECODE, stream, [&] {
     if (D == 128)
       return p.nt == 1 ? launch_decode<128, 1, 3>(tk, tk32, a, p, stream)
                        : launch_decode<128, 2, 2>(tk, tk32, a, p, stream);

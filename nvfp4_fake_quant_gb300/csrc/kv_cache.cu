@@ -165,7 +165,7 @@ nvq_status nvfp4_kv_append(const void* k, int64_t ld_k, const void* v, int64_t l
   const int rows = kThreads / (D / 16 * kTokens);
   const int64_t want = std::max<int64_t>(1, (2 * device_sms() + groups - 1) / groups);
   const int y = static_cast<int>(std::min<int64_t>(want, (2 * Hkv + rows - 1) / rows));
-  const cudaError_t e = timed(NVQ_KERNEL_QUANTIZE, stream, [&] {
+  const cudaError_t e = timed(NVQ_KERNEL_KV_APPEND, stream, [&] {
     const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(y));
     return launch_pdl(D == 128 ? kv_append_kernel<128> : kv_append_kernel<64>, grid, dim3(kThreads),
                       0, stream, 1, a);

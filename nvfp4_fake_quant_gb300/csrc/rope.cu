@@ -226,7 +226,7 @@ extern "C" nvq_status rope_apply(const void* q, int64_t ld_q, void* q_out, int64
   const int64_t rounds = (T + kMaxTokens * wave - 1) / (kMaxTokens * wave);
   a.tokens = static_cast<int>((T + rounds * wave - 1) / (rounds * wave));
   const int64_t groups = (T + a.tokens - 1) / a.tokens;
-  const cudaError_t e = timed(NVQ_KERNEL_VSA, stream, [&] {
+  const cudaError_t e = timed(NVQ_KERNEL_ROPE, stream, [&] {
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(groups, wave)));
     return launch_pdl(interleaved ? rope_kernel<true> : rope_kernel<false>, grid, dim3(kThreads), 0,
                       stream, 1, a);

@@ -25,7 +25,12 @@ struct Interval {
 
 std::mutex g_timing_mu;
 bool g_timing_on = false;
-std::vector<Interval> g_records[NVQ_KERNEL_KINDS];
+std::vector<Interval> g_records[NVQ_KERNEL_SERVING_END];
+
+bool is_kind(int kind) {
+  return (kind >= 0 && kind < NVQ_KERNEL_KINDS) ||
+         (kind >= NVQ_KERNEL_SERVING && kind < NVQ_KERNEL_SERVING_END);
+}
 
 void discard_all_locked() {
   for (auto& v : g_records) {
@@ -41,7 +46,7 @@ void discard_all_locked() {
 
 TimedLaunch::TimedLaunch(int kind, cudaStream_t stream) : kind_(kind), stream_(stream) {
   std::lock_guard<std::mutex> lock(g_timing_mu);
-  if (!g_timing_on || kind < 0 || kind >= NVQ_KERNEL_KINDS) return;
+  if (!g_timing_on || !is_kind(kind)) return;
   if (cudaEventCreate(&start_) != cudaSuccess) return;
   if (cudaEventCreate(&stop_) != cudaSuccess) {
     cudaEventDestroy(start_);
@@ -80,8 +85,7 @@ extern "C" nvq_status nvq_timing_enable(int on) {
 }
 
 extern "C" nvq_status nvq_timing_read(int kind, int64_t* launches, double* total_ms) {
-  if (kind < 0 || kind >= NVQ_KERNEL_KINDS || launches == nullptr || total_ms == nullptr)
-    return NVQ_ERR_INVALID;
+  if (!is_kind(kind) || launches == nullptr || total_ms == nullptr) return NVQ_ERR_INVALID;
   std::lock_guard<std::mutex> lock(g_timing_mu);
   double sum = 0.0;
   for (const Interval& r : g_records[kind]) {

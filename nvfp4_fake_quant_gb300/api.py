@@ -420,6 +420,13 @@ def _check_out(t, name, shape, dtype, like):
     return t
 
 
+def _check_workspace(ws):
+    """A caller's workspace: the kernels take all of its bytes as lying one after another (a
+    broadcast view has fewer)."""
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def _overwritten(*outs):
     """Tells autograd that the caller's tensors have been written, as torch's own in-place
     operations do: a graph that saved one of them refuses its backward."""
@@ -485,6 +492,7 @@ def nvfp4_linear_packed_fwd(x, w_codes, w_scales, w_global_sf=None, bias=None, x
         if bias.dim() != 1 or bias.shape[0] != n or not bias.is_contiguous():
             raise ValueError(f"bias must be contiguous [{n}]")
     index = _device_of(x, w_codes, w_scales, w_global_sf, bias, x_global_sf, out, workspace)
+    _check_workspace(workspace)
     given, out = out, _check_out(out, "out", (m, n), BF16, x)
     if m == 0 and nvfp4_linear_packed_workspace(1, n, k):  # no rows of a layer that is served
         return out
@@ -750,6 +758,7 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
     if bt != b:
         raise ValueError(f"q has {b} rows, page_table {bt}")
     scale = _scale(scale, d)
+    _check_workspace(workspace)
     given = (o, lse)
     o = _check_out(o, "o", (b, h, d), BF16, q)
     lse = _check_out(lse, "lse", (b, h), torch.float32, q)

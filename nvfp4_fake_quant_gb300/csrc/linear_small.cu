@@ -417,15 +417,19 @@ SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
   // 7.9, 7.2; 64 x 14336 x 16384 33, 30).
   // The sums are at most 112 KB, and 56 KB where the clusters need two CTAs per SM: those
   // of more than 128 SMs' worth, of which the chip's groups of SMs do not hold all at once
-  // with one CTA per SM (64 x 4864 x 8192 in four, one per SM: 21 us, in two: 13).  Of 7
-  // and 8, few fit a group (32 x 2304 x 4096, 18 tiles: 15 us in seven, 8.3 in four; 32 x
-  // 2048 x 4096, 16 tiles: 15 us in eight, 7.9 in seven).
+  // with one CTA per SM (64 x 4864 x 8192 in four, one per SM: 21 us, in two: 13).  Of
+  // clusters of 7 and 8, 15 run at once with one CTA per SM, 16 do not: 16 x 1920 x 8192, 15
+  // tiles, 7.0 us in eight (6.8 in six), 16 x 2048 x 8192, 16 tiles, 12.0 (6.8); x 28672 9.9
+  // (10.8) and 18.1 (10.9).  With sums over 56 KB they pay from K of 16384 on, up to 12 tiles
+  // by 0 to 9% (32 x 1536 x 28672 11.5 us, 12.1 in six; x 8192 8.5, 7.9; x 2048 7.3, 6.6); at
+  // 13 to 15 tiles, in six, they would win as little and lose as much (32 x 1664 x 28672 12.3
+  // us, 11.6 in eight; x 8192 7.9, 8.5; x 2048 6.6, 7.4).
   p.split = 1;
   for (int x = 2; x <= 8 && x <= p.k_stages; ++x) {
     const int64_t ctas = static_cast<int64_t>(x) * p.tiles;
     const int sum_rows = (x - 1) * p.cols;
     const bool pairs = p.cols == 16 || (p.cols == 32 && p.k_stages >= 16 * x);
-    if (ctas <= 128 ? sum_rows <= 224 && (x < 7 || p.tiles <= (sum_rows <= 112 ? 16 : 12))
+    if (ctas <= 128 ? sum_rows <= 224 && (x < 7 || p.tiles <= (sum_rows <= 112 ? 15 : 12))
                     : ctas <= (pairs ? 3 * sms / 2 : sms) && sum_rows <= 112 && x <= 4)
       p.split = x;
   }

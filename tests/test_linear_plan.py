@@ -79,3 +79,11 @@ def test_every_plan_keeps_its_promises():
                 assert p["smem"] <= 227 * 1024 and 3 * (p["smem"] + 1024) > smem
                 if p["ctas"] > sms:
                     assert 2 * (p["smem"] + 1024) <= smem
+
+
+@pytest.mark.parametrize("m", [1, 5, 8, 16])
+@pytest.mark.parametrize("k", [2048, 8192, 28672])
+def test_sixteen_clusters_of_seven_or_eight_are_not_asked_for(m, k):
+    """With one CTA per SM the chip's groups of SMs hold 15 of them at once."""
+    assert plan(m, 15 * 128, k)["split"] == 8
+    assert plan(m, 16 * 128, k)["split"] == 6

@@ -656,9 +656,12 @@ class Rotary(torch.nn.Module):
     """Rotary positions of q and k before AttnQAT: forward(q, k, positions) with q, k
     bf16 [B, N, H, D] (or [T, H, D]; a layout the kernel does not read is copied) and
     positions int32 of N (shared by the batch) or B*N rows, [rows] or [rows, axes].
-    ``scaling`` and the rest as in rope_inv_freq.  Forward and backward may be captured
-    into one CUDA graph; as for every autograd function, no graph of the same leaves that
-    was recorded outside the capture may be alive then."""
+    ``scaling`` and the rest as in rope_inv_freq: ONE ladder of frequencies through the pairs
+    of all axes, in order.  A model whose ladder restarts with each axis gives
+    inv_freq=torch.cat([rope_inv_freq(2 * n)[0] for n in axis_pairs]).
+    Differentiable any number of times.  Forward and backward may be captured into one CUDA
+    graph; as for every autograd function, no graph of the same leaves that was recorded
+    outside the capture may be alive then."""
 
     def __init__(self, rot_dim: int, interleaved: bool = False, axis_pairs=None, device=None,
                  inv_freq: torch.Tensor | None = None, **frequencies):

@@ -669,9 +669,11 @@ class Rotary(torch.nn.Module):
         self.mscale = 1.0
         if inv_freq is None:
             inv_freq, self.mscale = rope_inv_freq(rot_dim, device=device, **frequencies)
+        elif frequencies:
+            raise ValueError(f"inv_freq is given: {', '.join(frequencies)} would not be looked at")
         if inv_freq.numel() * 2 != rot_dim:
             raise ValueError(f"inv_freq must have {rot_dim // 2} entries")
-        self.register_buffer("inv_freq", inv_freq, persistent=False)
+        self.register_buffer("inv_freq", inv_freq.to(device), persistent=False)
         self.interleaved, self.axis_pairs = interleaved, axis_pairs
 
     def _apply(self, fn, recurse=True):

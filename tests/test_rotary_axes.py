@@ -1,5 +1,6 @@
 """Frequencies of several position axes: one ladder by default, one per axis where inv_freq
 gives it, as the docstring of api.Rotary says (the kernel replaced by the oracle, on the CPU)."""
+import pytest
 import torch
 
 from nvfp4_fake_quant_gb300 import api
@@ -26,3 +27,12 @@ def test_one_ladder_or_one_per_axis(monkeypatch):
         assert torch.equal(one[..., part],
                            os_.rope(x[..., part], pos[:, axis], ladder[at:at + n], True))
         at += n
+
+
+def test_given_frequencies_go_to_the_device_and_stand_alone():
+    f = api.rope_inv_freq(32)[0]
+    assert api.Rotary(32, inv_freq=f, device="meta").inv_freq.device.type == "meta"
+    assert api.Rotary(32, inv_freq=f).inv_freq is f
+    # what would have shaped them is not dropped without a word
+    with pytest.raises(ValueError, match="theta"):
+        api.Rotary(32, inv_freq=f, theta=500000.0)

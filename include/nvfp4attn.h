@@ -521,7 +521,9 @@ nvq_status nvfp4_kv_append(const void* k, int64_t ld_k, const void* v, int64_t l
  * `window` of them and the first `sinks`.  The new token's own K and V are in
  * the cache (append first).  A sequence without visible keys gets o = 0 and
  * lse = -inf.  D in {64, 128}; window, sinks >= 0; 1 <= B, H <= 65535, B*H < 2^31,
- * B*H*max_pages <= 2^53 (else NVQ_ERR_UNSUPPORTED).  Long sequences are split
+ * B*H*max_pages <= 2^53, and a call takes less than 2^31 records for each of its
+ * runs, of which there are 304 to 608 on 152 multiprocessors (else
+ * NVQ_ERR_UNSUPPORTED).  Long sequences are split
  * over the GPU and joined in a fixed order: results do not vary from run to run.
  * ws: attn_qat_decode_workspace(B, H, Hkv, D, max_pages) bytes, 256-byte
  * aligned; its size follows from the current device's multiprocessor count.

@@ -1006,6 +1006,9 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
   if (st != NVQ_OK) return st;
   const Plan p = plan(B, H, Hkv, D, max_pages, window, sinks);
   if (num_pages > 0x7FFFFFFF / Hkv) return NVQ_ERR_UNSUPPORTED;  // tensor-map coordinates
+  // a run counts its tiles in 31 bits
+  if (static_cast<int64_t>(B) * Hkv * p.chunks * max_pages / p.runs >= 0x7FFFFFFF)
+    return NVQ_ERR_UNSUPPORTED;
   if (ws == nullptr || ws_bytes < p.total || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return NVQ_ERR_WORKSPACE;
   // q is read by every run of its sequence, at whatever time: o elsewhere

@@ -107,6 +107,8 @@ struct BwdLayout {
   static constexpr uint32_t kUsed = kAbort + 4u;
   static constexpr uint32_t kAlloc = kUsed + 1024u;
   static_assert(kAlloc <= 232448u, "shared memory of one CTA");
+  // heads of 64 leave room for one CTA of the few-rows linear (they wait for nobody)
+  static_assert(apart_from_linear_small(kAlloc, D == 64 ? 2 : 1), "tensor memory");
 };
 
 // One CTA per (128-key tile, head, batch).  tq4, tk4: packed codes of Q~, K~

@@ -417,6 +417,7 @@ cudaError_t launch_dq4_t(const AttnShape& s, const CUtensorMap& tq4, const CUten
                          cudaStream_t stream) {
   using L = DqLayout<D>;
   static_assert(L::kAlloc <= 227u * 1024u, "shared memory");
+  static_assert(apart_from_linear_small(L::kAlloc), "tensor memory");
   const dim3 grid((s.Nq + kTile - 1) / kTile, s.H, s.B);
   cudaError_t e = cudaFuncSetAttribute(attn_bwd_dq_fp4_kernel<D, kSparse>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);

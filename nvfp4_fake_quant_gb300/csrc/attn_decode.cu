@@ -90,6 +90,7 @@ struct Cfg {
   static constexpr uint32_t kSfa = 16 * kStages, kSfb = kSfa + kStages * (D / 16);
   static constexpr uint32_t kCols = 128, kAlloc = kRuns > 2 ? 512 : 256;
   static_assert(kSfb + 2 * (D / 16) <= kCols, "tensor memory");
+  static_assert(apart_from_linear_small(kSmem), "tensor memory");
   static_assert(kStage % 1024 == 0, "swizzle atoms");
 };
 

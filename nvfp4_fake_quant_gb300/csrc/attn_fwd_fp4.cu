@@ -631,6 +631,8 @@ cudaError_t launch_fp4_d(const AttnShape& s, const CUtensorMap& tq, const CUtens
                          cudaStream_t stream) {
   using L = Fp4Layout<D>;
   static_assert(L::kAlloc <= 227u * 1024u, "shared memory");
+  // heads of 64 leave room for one CTA of the few-rows linear (they wait for nobody)
+  static_assert(apart_from_linear_small(L::kAlloc, D == 64 ? 2 : 1), "tensor memory");
   const dim3 grid((s.Nq + kTile - 1) / kTile, s.H, s.B);
   cudaError_t e = cudaFuncSetAttribute(attn_fwd_fp4_kernel<D, kMode>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);

@@ -70,6 +70,7 @@ constexpr uint32_t kBf16NumBars = 2 * kBf16Stages + 4 + 1;
 constexpr uint32_t kBf16Slot = kBf16Bars + kBf16NumBars * 8;
 constexpr uint32_t kBf16Abort = kBf16Slot + 4;
 constexpr uint32_t kBf16Smem = kBf16Abort + 4 + 1024;  // + alignment slack
+static_assert(apart_from_linear_small(kBf16Smem), "tensor memory");
 
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_bf16_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUtensorMap tb0,
@@ -265,6 +266,7 @@ constexpr uint32_t kF4NumBars = 2 * kF4Stages + 4 + 1;
 constexpr uint32_t kF4Slot = kF4Bars + kF4NumBars * 8;
 constexpr uint32_t kF4Abort = kF4Slot + 4;
 constexpr uint32_t kF4Smem = kF4Abort + 4 + 1024;
+static_assert(apart_from_linear_small(kF4Smem), "tensor memory");
 // TMEM: accumulators [0, 256); scale operands of stage s, step j at
 // kF4ScCol + 8 (s * kF4Steps + j) (x) and + 4 (w).
 constexpr uint32_t kF4ScCol = 256;
@@ -461,6 +463,7 @@ constexpr uint32_t kXresNumBars = 2 * kXresStages + 2 * kXresBoxes + 4 + 1;
 constexpr uint32_t kXresSlot = kXresBars + kXresNumBars * 8;
 constexpr uint32_t kXresAbort = kXresSlot + 4;
 constexpr uint32_t kXresSmem = kXresAbort + 4 + 1024;
+static_assert(apart_from_linear_small(kXresSmem), "tensor memory");
 // TMEM: accumulators [0, 256), x scales of step j at 256 + 4 j, W scales of
 // stage s, step j at kXresBCol + 4 (4 s + j).
 constexpr uint32_t kXresBCol = 256 + 4 * 4 * kXresBoxes;

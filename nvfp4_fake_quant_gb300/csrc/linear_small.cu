@@ -441,11 +441,11 @@ SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
   p.part = (p.k_stages + p.split - 1) / p.split;
   p.fused = p.part <= 8 && 16 * M * p.part <= 448;  // of 128 kFusedBlocks
   // At most four stages, and 112 KB where there are more CTAs than one per SM leaves room
-  // for: two fit an SM then.  At least 78 KB: no three do, whose 256 tensor-memory
+  // for: two fit an SM then.  At least kLinearSmallSmem: no three do, whose 256 tensor-memory
   // columns each would not fit, so that no CTA waits for columns that a cluster holds
-  // which in its turn waits for that CTA's cluster.  (The library's other kernels whose
-  // CTAs wait for one another or hold tensor memory long take over 149 KB: they share no
-  // SM with these.)
+  // which in its turn waits for that CTA's cluster.  (The library's other kernels that hold
+  // tensor memory assert that they share no SM with these, or that their CTAs wait for
+  // nobody.)
   const uint32_t x_stage = p.cols * 128u + kXs;
   const uint32_t stage = (kW + kSc + (p.fused ? 0 : x_stage) + 1023) / 1024 * 1024;
   const int sums = (p.split - 1) * p.cols * 512;
@@ -453,7 +453,7 @@ SmallPlan small_plan(int64_t M, int64_t N, int64_t K) {
   const int room = (p.ctas > 128 ? 112 : 222) * 1024 - 1024 - sums - xs;
   p.stages = std::min({kStages, p.part, room / static_cast<int>(stage)});
   p.sums_at = p.stages * stage + xs;
-  p.smem = std::max<size_t>(p.sums_at + sums + 1024, 78 * 1024);
+  p.smem = std::max<size_t>(p.sums_at + sums + 1024, kLinearSmallSmem);
   return p;
 }
 

@@ -251,6 +251,16 @@ cudaError_t launch_gemm_bf16_pair(const CUtensorMap& ta0, const CUtensorMap& tb0
 // The packed linear of few rows (linear_small.cu).  ws holds the codes of x at its
 // base (tx: make_codes_map over them, box of M rounded up to 16 rows), then the rest
 // of linear_small_workspace(M, K) bytes; tw: make_codes_map over w's codes.
+// Shared memory of one of its CTAs, at least: no three of them lie on an SM, whose 256
+// columns of tensor memory each would not fit.
+constexpr uint32_t kLinearSmallSmem = 78 * 1024;
+// Whether `n` of them never lie on an SM beside a CTA with `smem` bytes (228 KB an SM, of
+// which each CTA takes 1 KB more).  n = 1 has to hold for every kernel whose CTAs hold tensor
+// memory and wait for one another: CTAs of two clusters that wait for each other's columns
+// never end.  One that waits for none gives its columns back, and the cluster goes on.
+constexpr bool apart_from_linear_small(uint32_t smem, uint32_t n = 1) {
+  return smem + 1024 + n * (kLinearSmallSmem + 1024) > 228 * 1024;
+}
 // Up to 64 rows (the columns of sums that tensor memory is laid out for): 64 x 4608 x 1536
 // 7.4 us, x 1536 x 8960 10.5, x 28672 x 8192 26.1; the GEMM, which takes whole tiles of 128
 // rows, from 65 rows on 12.5, 23.2 and 39.8 (512 rows 11.9, 24.9 and 97.1).

@@ -452,8 +452,10 @@ nvq_status nvfp4_linear_packed_fwd(const void* x, int64_t ld_x, const uint8_t* w
  *   mscale    > 0 and finite; multiplies the rotated elements
  *   inverse   0: (x1, x2) -> mscale (x1 cos a - x2 sin a, x1 sin a + x2 cos a);
  *             1: by -a, which is the gradient with respect to the input
- * The angle is reduced to a fraction of a turn in 64-bit fixed point, so far
- * positions lose nothing; the rotation is fp32, rounded once to bf16.  T == 0
+ * The angle is reduced to a fraction of a turn in 64-bit fixed point: by itself off
+ * by less than 2^-36 of a turn at position 2^17, 2^-22 at 2^31.  The fraction is
+ * then rounded to fp32 (up to 2^-26 of a turn at any position), the rotation is
+ * fp32, and its result is rounded once to bf16.  T == 0
  * is a valid call that does nothing.
  */
 nvq_status rope_apply(const void* q, int64_t ld_q, void* q_out, int64_t ld_qo, int Hq,

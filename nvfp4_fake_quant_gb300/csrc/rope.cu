@@ -6,9 +6,10 @@
 // The angle.  Only its fraction of a turn matters: with f = inv_freq / 2 pi
 // (turns per position, whole turns dropped) held as a 64-bit fixed-point
 // fraction F = rint(f 2^64), position * F modulo 2^64 IS the fraction of the
-// turn, exact but for the roundings of f (fp64) and F.  fp32 products would be off by whole
-// radians at far positions, fp64 sines cost more than the copy (the FP64 rate is
-// a few operations per clock and SM).  F is formed once per block and pair, the
+// turn, exact but for the roundings of f (fp64) and F; its upper 32 bits, rounded to fp32
+// (2^-26 of a turn at most, at any position), go to the sine.  fp32 products would be off by
+// whole radians at far positions, fp64 sines cost more than the copy (the FP64 rate is a few
+// operations per clock and SM).  F is formed once per block and pair, the
 // sine and cosine once per (token, pair) and shared by all heads through shared
 // memory; what is left is a copy of Q and K, bound by HBM.
 //
@@ -17,7 +18,9 @@
 // 32760 tokens of 12 + 12 heads, half of each head rotated, 72 us, 82%; 64 tokens of 32 +
 // 8 heads 3 us, the latency of a launch and of the loads behind one another.  With few
 // heads the sines are no longer shared by enough of them: 25088 tokens of 1 + 1 heads
-// take 16 us, 4 of them for the copy.
+// take 16 us (half layout) and 14 us (interleaved), 4 of them for the copy; of 8 + 1 heads
+// 21 and 23, 17 of them.  The half layout spills 12 bytes at the cap of 64 registers that
+// four blocks an SM leave.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

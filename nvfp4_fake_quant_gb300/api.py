@@ -647,8 +647,8 @@ class RotaryFunction(torch.autograd.Function):
     def backward(ctx, gq, gk):
         positions, inv_freq = ctx.saved_tensors
         *args, inverse = ctx.args
-        gq, gk = RotaryFunction.apply(_loadable(gq), _loadable(gk), positions, inv_freq, *args,
-                                      not inverse)
+        turn = RotaryFunction.apply if torch.is_grad_enabled() else rope_apply
+        gq, gk = turn(_loadable(gq), _loadable(gk), positions, inv_freq, *args, not inverse)
         return gq, gk, None, None, None, None, None, None
 
 

@@ -420,6 +420,12 @@ def _check_out(t, name, shape, dtype, like):
     return t
 
 
+def _count(n) -> int:
+    """A number of tokens as a C int, which ctypes would cut to its low 32 bits: those past
+    any length are as good as the largest, those below 0 are refused by the call."""
+    return max(-1, min(int(n), 0x7FFFFFFF))
+
+
 def _check_workspace(ws):
     """A caller's workspace: the kernels take all of its bytes as lying one after another (a
     broadcast view has fewer)."""
@@ -756,8 +762,8 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
                     workspace=None):
     """Attention of one new token per sequence over the paged cache: q bf16 [B, H, D]
     (rows may be strided), returns (o bf16 [B, H, D], lse f32 [B, H]).  ``window`` > 0:
-    only the last ``window`` keys and the first ``sinks`` are visible.  No sequences (B = 0)
-    is a valid call that launches nothing."""
+    only the last ``window`` keys and the first ``sinks`` are visible (numbers past any
+    length: all of them).  No sequences (B = 0) is a valid call that launches nothing."""
     b, h, d, ld_q = _rows_nd(q, "q")
     pages, hkv, bt, max_pages, ld_t = _check_cache(pool, page_table, seq_lens, d)
     if bt != b:
@@ -775,7 +781,7 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
         ws = _workspace(_on(index, "attn_qat_decode_workspace", b, h, hkv, d, max_pages),
                         q.device, None)
     args = (q.data_ptr(), ld_q, pool.data_ptr(), pages, page_table.data_ptr(), ld_t,
-            max_pages, seq_lens.data_ptr(), b, h, hkv, d, scale, int(window), int(sinks),
+            max_pages, seq_lens.data_ptr(), b, h, hkv, d, scale, _count(window), _count(sinks),
             o.data_ptr(), lse.data_ptr())
     try:
         _launch(index, "attn_qat_decode", *args, ws.data_ptr(), ws.numel() * ws.element_size())

@@ -509,6 +509,66 @@ nvq_status nvfp4_kv_append(const void* k, int64_t ld_k, const void* v, int64_t l
                            int max_pages, void* pool, int64_t num_pages, nvq_stream_t stream);
 
 /*
+ * nvfp4_kv_append with every token's place given: row t's K and V go to pool page
+ * slots[t] / 128, token row slots[t] % 128 (int64 [T], 8-byte aligned; as
+ * nvfp4_kv_extend writes them).  A negative slot: the row is not written; one of a
+ * page outside the pool is left out and NVQ_ERR_INVALID recorded for
+ * nvq_device_status().  Two rows must not have the same slot.
+ */
+nvq_status nvfp4_kv_append_slots(const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                                 int64_t T, int Hkv, int D, const int64_t* slots, void* pool,
+                                 int64_t num_pages, nvq_stream_t stream);
+
+/*
+ * Pages and places for new tokens, from the lengths alone and without the host: the
+ * step that stands before rope_apply (positions), nvfp4_kv_append (tables and
+ * lengths, or slots) and the attention calls, and that a captured graph repeats.
+ *   new_tokens, seq_lens  int32 [B]: tokens to add, and held before (a number
+ *                    below 0 counts as 0)
+ *   page_table       int32 [B, max_pages], row stride ld_table: the entries of pages
+ *                    that a sequence grows into are written, the others left
+ *   free_pages       int32 [num_pages], free_count int32 [1]: the pages that nobody
+ *                    holds are free_pages[0 .. *free_count).  The new pages of the
+ *                    call, in the order of (sequence, page), are taken from the end:
+ *                    the first is free_pages[*free_count - 1]
+ *   start            int32 [B] or NULL (0): added to the positions (the length of a
+ *                    prefix that is cached apart)
+ *   seq_lens_out, free_count_out  lengths and count after the call; may be seq_lens
+ *                    and free_count
+ *   cu_tokens        int32 [B + 1] (written): offsets of the sequences' new tokens
+ *   positions, slots int32 [T], int64 [T] (written): of new token i of sequence b, in
+ *                    row cu_tokens[b] + i, p = seq_lens[b] + i: position start[b] + p
+ *                    and slot 128 * page_table[b][p / 128] + p % 128.  Rows behind
+ *                    the last token: -1 in both
+ * No call is served in part: where the new tokens are more than T, their pages more
+ * than the free ones, a length would pass 128 * max_pages or *free_count is outside
+ * [0, num_pages], NVQ_ERR_INVALID is recorded for nvq_device_status(), lengths, count
+ * and table stay, cu_tokens are all 0 and positions and slots -1 (so the calls behind
+ * it write nothing).  The slot of a token in a page outside the pool is -1, recorded
+ * alike.  A sequence's pages are its own: two rows of the table that hold the same
+ * page must not both grow into it or be released.  1 <= B <= 65535, T < 2^31.
+ */
+nvq_status nvfp4_kv_extend(const int32_t* new_tokens, const int32_t* seq_lens,
+                           const int32_t* start, int B, int32_t* page_table, int64_t ld_table,
+                           int max_pages, const int32_t* free_pages, const int32_t* free_count,
+                           int64_t num_pages, int64_t T, int32_t* seq_lens_out,
+                           int32_t* free_count_out, int32_t* cu_tokens, int32_t* positions,
+                           int64_t* slots, nvq_stream_t stream);
+
+/*
+ * The pages of sequences b with done[b] != 0 (uint8 [B]) back to the free ones: pushed
+ * to free_pages[*free_count ..] in the order of (sequence, page), the sequences'
+ * lengths 0.  The table is not changed (entries of an empty sequence are not read).
+ * The other arguments as in nvfp4_kv_extend.  Where a page is outside [0, num_pages), a
+ * length over 128 * max_pages, or the free ones would become more than num_pages,
+ * NVQ_ERR_INVALID is recorded for nvq_device_status() and nothing is given back.
+ */
+nvq_status nvfp4_kv_release(const uint8_t* done, const int32_t* seq_lens, int B,
+                            const int32_t* page_table, int64_t ld_table, int max_pages,
+                            int32_t* free_pages, const int32_t* free_count, int64_t num_pages,
+                            int32_t* seq_lens_out, int32_t* free_count_out, nvq_stream_t stream);
+
+/*
  * Attention of one new token per sequence over the cache (the serving form of
  * attn_qat_fwd: the last row of a causal forward).
  *   q     bf16 [B, H, D], row stride ld_q (elements, % 8 == 0, >= H*D);
@@ -558,7 +618,9 @@ enum {
   NVQ_KERNEL_ROPE = 16,      /* rotary positions */
   NVQ_KERNEL_KV_APPEND = 17, /* new tokens into the paged cache */
   NVQ_KERNEL_DECODE = 18,    /* single tokens over the cache (with the join) */
-  NVQ_KERNEL_SERVING_END = 19
+  NVQ_KERNEL_KV_TABLES = 19, /* pages for new tokens, pages given back */
+  NVQ_KERNEL_CROSS = 20,     /* many rows over the cache (with the join) */
+  NVQ_KERNEL_SERVING_END = 21
 };
 
 /*

@@ -68,6 +68,13 @@ SIGNATURES = {
     "nvfp4_kv_append": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int, c_int, c_int,
                                 c_void_p, c_void_p, c_void_p, c_int64, c_int, c_void_p, c_int64,
                                 c_void_p]),
+    "nvfp4_kv_append_slots": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int, c_int,
+                                      c_void_p, c_void_p, c_int64, c_void_p]),
+    "nvfp4_kv_extend": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int64, c_int,
+                                c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                                c_void_p, c_void_p, c_void_p]),
+    "nvfp4_kv_release": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_int64, c_int, c_void_p,
+                                 c_void_p, c_int64, c_void_p, c_void_p, c_void_p]),
     "attn_qat_decode_workspace": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
     "attn_qat_decode": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int,
                                 c_void_p, c_int, c_int, c_int, c_int, c_float, c_int, c_int,

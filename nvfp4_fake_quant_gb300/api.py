@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import functools
 import math
+import typing
 
 import torch
 
@@ -712,19 +713,25 @@ def nvfp4_kv_pool(num_pages: int, hkv: int, d: int, device="cuda") -> torch.Tens
     return torch.zeros((num_pages, hkv, record), dtype=torch.uint8, device=device)
 
 
-def _check_cache(pool, page_table, seq_lens, d):
-    """(pages, Hkv, B, max_pages, row stride of the table)."""
+def _check_pool(pool, d):
+    """(pages, Hkv)."""
     if not (isinstance(pool, torch.Tensor) and pool.dtype is torch.uint8):
         _check(pool, "pool", torch.uint8)
     shape = pool.shape
     if len(shape) != 3 or shape[2] != 144 * d or not pool.is_contiguous():
         raise ValueError(f"pool must be contiguous uint8 [pages, Hkv, {144 * d}], "
                          f"got {tuple(shape)}")
+    return shape[0], shape[1]
+
+
+def _check_cache(pool, page_table, seq_lens, d):
+    """(pages, Hkv, B, max_pages, row stride of the table)."""
+    pages, hkv = _check_pool(pool, d)
     (b, max_pages), (ld, _) = _int32(page_table, "page_table", 2)
     (n,), _ = _int32(seq_lens, "seq_lens", 1)
     if n != b:
         raise ValueError(f"page_table has {b} rows, seq_lens {n}")
-    return shape[0], shape[1], b, max_pages, ld if b > 1 else max_pages
+    return pages, hkv, b, max_pages, ld if b > 1 else max_pages
 
 
 def nvfp4_kv_append(k, v, seq_lens, page_table, pool, cu_tokens=None) -> None:
@@ -752,6 +759,109 @@ def nvfp4_kv_append(k, v, seq_lens, page_table, pool, cu_tokens=None) -> None:
             _ptr(cu_tokens), seq_lens.data_ptr(), page_table.data_ptr(), ld_t, max_pages,
             pool.data_ptr(), pages)
     _overwritten(pool)
+
+
+def nvfp4_kv_append_slots(k, v, slots, pool) -> None:
+    """nvfp4_kv_append with each token's place given: slots int64 [T] (nvfp4_kv_extend's), 128 *
+    page + row; a token of a negative slot is not written."""
+    t, hkv, d, ld_k = _rows_nd(k, "k")
+    tv, hv, dv, ld_v = _rows_nd(v, "v")
+    if (tv, hv, dv) != (t, hkv, d):
+        raise ValueError(f"v must be {(t, hkv, d)}, got {(tv, hv, dv)}")
+    pages, heads = _check_pool(pool, d)
+    if heads != hkv:
+        raise ValueError(f"pool has {heads} heads, k {hkv}")
+    _check(slots, "slots", torch.int64)
+    if slots.dim() != 1 or slots.shape[0] != t or not slots.is_contiguous():
+        raise ValueError(f"slots must be contiguous [{t}]")
+    index = _device_of(k, v, slots, pool)
+    _launch(index, "nvfp4_kv_append_slots", k.data_ptr(), ld_k, v.data_ptr(), ld_v, t, hkv, d,
+            slots.data_ptr(), pool.data_ptr(), pages)
+    _overwritten(pool)
+
+
+class KvStep(typing.NamedTuple):
+    """What nvfp4_kv_extend tells of a step."""
+    seq_lens: torch.Tensor    # int32 [B], after the step
+    free_count: torch.Tensor  # int32 [1], after the step
+    cu_tokens: torch.Tensor   # int32 [B + 1]: offsets of the sequences' new tokens
+    positions: torch.Tensor   # int32 [tokens], for rope_apply; -1 behind the last token
+    slots: torch.Tensor       # int64 [tokens], for nvfp4_kv_append_slots; -1 behind the last
+
+
+def _check_free(page_table, seq_lens, free_pages, free_count):
+    """(B, max_pages, row stride of the table, pages)."""
+    (b, max_pages), (ld, _) = _int32(page_table, "page_table", 2)
+    if _int32(seq_lens, "seq_lens", 1)[0][0] != b:
+        raise ValueError(f"page_table has {b} rows, seq_lens {seq_lens.shape[0]}")
+    (pages,), _ = _int32(free_pages, "free_pages", 1)
+    if not (isinstance(free_count, torch.Tensor) and free_count.dtype is torch.int32 and
+            free_count.numel() == 1):
+        raise ValueError("free_count must be an int32 tensor of one number")
+    return b, max_pages, ld if b > 1 else max_pages, pages
+
+
+def nvfp4_kv_extend(new_tokens, seq_lens, page_table, free_pages, free_count, tokens=None,
+                    start=None, seq_lens_out=None, free_count_out=None, cu_tokens=None,
+                    positions=None, slots=None) -> KvStep:
+    """Pages and places for new tokens, found on the device: new_tokens and seq_lens int32 [B],
+    page_table int32 [B, max_pages] (entries of new pages are written), free_pages int32
+    [pages] of which the first free_count (int32 [1]) are free and the last of those are taken.
+    ``tokens``: rows of positions and slots (default: one per sequence).  ``start`` int32 [B]:
+    added to the positions.  seq_lens_out and free_count_out may be seq_lens and free_count:
+    a captured step then advances them in place.  A call that does not fit (pages, rows, the
+    table's width) changes nothing, gives no tokens and is reported by device_status()."""
+    b, max_pages, ld, pages = _check_free(page_table, seq_lens, free_pages, free_count)
+    if _int32(new_tokens, "new_tokens", 1)[0][0] != b:
+        raise ValueError(f"new_tokens must be [{b}], got {tuple(new_tokens.shape)}")
+    if start is not None and _int32(start, "start", 1)[0][0] != b:
+        raise ValueError(f"start must be [{b}], got {tuple(start.shape)}")
+    t = b if tokens is None else int(tokens)
+    if t < 0:
+        raise ValueError(f"tokens must be >= 0, got {t}")
+    given = (seq_lens_out, free_count_out, cu_tokens, positions, slots)
+    out = KvStep(_check_out(seq_lens_out, "seq_lens_out", (b,), torch.int32, seq_lens),
+                 _check_out(free_count_out, "free_count_out", (1,), torch.int32, seq_lens),
+                 _check_out(cu_tokens, "cu_tokens", (b + 1,), torch.int32, seq_lens),
+                 _check_out(positions, "positions", (t,), torch.int32, seq_lens),
+                 _check_out(slots, "slots", (t,), torch.int64, seq_lens))
+    index = _device_of(seq_lens, new_tokens, page_table, free_pages, free_count, start, *out)
+    if index < 0:
+        _check(seq_lens, "seq_lens", torch.int32)
+    if b == 0:  # no sequences
+        out.free_count.copy_(free_count.view(1))
+        for o, v in ((out.cu_tokens, 0), (out.positions, -1), (out.slots, -1)):
+            o.fill_(v)
+        return out
+    _launch(index, "nvfp4_kv_extend", new_tokens.data_ptr(), seq_lens.data_ptr(), _ptr(start), b,
+            page_table.data_ptr(), ld, max_pages, free_pages.data_ptr(), free_count.data_ptr(),
+            pages, t, *(o.data_ptr() for o in out))
+    _overwritten(page_table, *given)
+    return out
+
+
+def nvfp4_kv_release(done, seq_lens, page_table, free_pages, free_count, seq_lens_out=None,
+                     free_count_out=None):
+    """The pages of the sequences with done[b] (bool [B]) back to the free ones: returns
+    (seq_lens, free_count) after it, the lengths of those sequences 0; free_pages is written
+    behind its first free_count entries.  seq_lens_out and free_count_out may be seq_lens and
+    free_count."""
+    b, max_pages, ld, pages = _check_free(page_table, seq_lens, free_pages, free_count)
+    _check(done, "done", torch.bool)
+    if done.dim() != 1 or done.shape[0] != b or not done.is_contiguous():
+        raise ValueError(f"done must be contiguous [{b}]")
+    given = (seq_lens_out, free_count_out)
+    lens = _check_out(seq_lens_out, "seq_lens_out", (b,), torch.int32, seq_lens)
+    count = _check_out(free_count_out, "free_count_out", (1,), torch.int32, seq_lens)
+    index = _device_of(seq_lens, done, page_table, free_pages, free_count, lens, count)
+    if b == 0:  # no sequences
+        count.copy_(free_count.view(1))
+        return lens, count
+    _launch(index, "nvfp4_kv_release", done.data_ptr(), seq_lens.data_ptr(), b,
+            page_table.data_ptr(), ld, max_pages, free_pages.data_ptr(), free_count.data_ptr(),
+            pages, lens.data_ptr(), count.data_ptr())
+    _overwritten(free_pages, *given)
+    return lens, count
 
 
 def attn_qat_decode_workspace(b, h, hkv, d, max_pages) -> int:
@@ -799,7 +909,7 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
 # Kernel kinds of nvq_timing_read (include/nvfp4attn.h, NVQ_KERNEL_*)
 KERNEL_KINDS = {"quantize": 0, "attn_fwd": 1, "bwd_delta": 2, "bwd_dkdv": 3, "bwd_dq": 4,
                 "global_sf": 5, "vsa": 6, "linear": 7}
-SERVING_KINDS = {"rope": 16, "kv_append": 17, "decode": 18}
+SERVING_KINDS = {"rope": 16, "kv_append": 17, "decode": 18, "kv_tables": 19, "cross": 20}
 
 
 def timing_enable(on: bool = True) -> None:

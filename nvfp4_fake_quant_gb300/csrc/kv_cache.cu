@@ -39,6 +39,7 @@ struct AppendArgs {
   const uint16_t* v;
   int64_t ld_k, ld_v, T;
   int B, Hkv;
+  const int64_t* slots;  // places given (lens, table, cu unused), or nullptr
   const int32_t* cu;  // nullptr: one token per sequence
   const int32_t* lens;
   const int32_t* table;
@@ -52,6 +53,16 @@ struct AppendArgs {
 // Where token t goes: its page's first record and its row there; nullptr if it
 // is not written.
 __device__ __forceinline__ uint8_t* find_row(const AppendArgs& a, int64_t t, int D, int* row) {
+  if (a.slots != nullptr) {
+    const int64_t slot = a.slots[t];
+    if (slot < 0) return nullptr;
+    if (slot / kPage >= a.num_pages) {
+      atomicMax(a.err, kErrTable);
+      return nullptr;
+    }
+    *row = static_cast<int>(slot % kPage);
+    return a.pool + slot / kPage * a.Hkv * record_bytes(D);
+  }
   int b = 0;
   int64_t end = t + 1;
   if (a.cu == nullptr) {
@@ -126,6 +137,37 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
   }
 }
 
+// The checks of k and v that both append calls make (T tokens of Hkv heads; nothing of a call
+// without tokens is looked at).
+nvq_status check_rows(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int Hkv, int D,
+                      int64_t T) {
+  if (D != 64 && D != 128) return NVQ_ERR_UNSUPPORTED;
+  if (Hkv > 65535) return NVQ_ERR_UNSUPPORTED;
+  if (T == 0) return NVQ_OK;
+  const int64_t row = static_cast<int64_t>(Hkv) * D;
+  if (k == nullptr || v == nullptr || (reinterpret_cast<uintptr_t>(k) & 15u) != 0 ||
+      (reinterpret_cast<uintptr_t>(v) & 15u) != 0 || ld_k < row || ld_v < row || ld_k % 8 != 0 ||
+      ld_v % 8 != 0)
+    return NVQ_ERR_INVALID;
+  return NVQ_OK;
+}
+
+nvq_status launch_append(AppendArgs a, int D, cudaStream_t stream) {
+  const int64_t groups = (a.T + kTokens - 1) / kTokens;
+  if (groups > 0x7FFFFFFF) return NVQ_ERR_UNSUPPORTED;
+  if ((a.err = device_error_word()) == nullptr) return NVQ_ERR_CUDA;
+  // a few tokens: spread their heads over the SMs
+  const int rows = kThreads / (D / 16 * kTokens);
+  const int64_t want = std::max<int64_t>(1, (2 * device_sms() + groups - 1) / groups);
+  const int y = static_cast<int>(std::min<int64_t>(want, (2 * a.Hkv + rows - 1) / rows));
+  const cudaError_t e = timed(NVQ_KERNEL_KV_APPEND, stream, [&] {
+    const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(y));
+    return launch_pdl(D == 128 ? kv_append_kernel<128> : kv_append_kernel<64>, grid, dim3(kThreads),
+                      0, stream, 1, a);
+  });
+  return e == cudaSuccess ? NVQ_OK : fail_cuda("kv append", e);
+}
+
 }  // namespace
 
 }  // namespace nvq
@@ -144,33 +186,31 @@ nvq_status nvfp4_kv_append(const void* k, int64_t ld_k, const void* v, int64_t l
   using namespace nvq;
   if (T < 0 || B < 1 || Hkv < 1 || (cu_tokens == nullptr && T != B && T != 0))
     return NVQ_ERR_INVALID;
-  if (D != 64 && D != 128) return NVQ_ERR_UNSUPPORTED;
-  if (Hkv > 65535) return NVQ_ERR_UNSUPPORTED;
-  if (T == 0) return NVQ_OK;
-  const int64_t row = static_cast<int64_t>(Hkv) * D;
-  if (k == nullptr || v == nullptr || (reinterpret_cast<uintptr_t>(k) & 15u) != 0 ||
-      (reinterpret_cast<uintptr_t>(v) & 15u) != 0 || ld_k < row || ld_v < row || ld_k % 8 != 0 ||
-      ld_v % 8 != 0 || (reinterpret_cast<uintptr_t>(cu_tokens) & 3u) != 0)
-    return NVQ_ERR_INVALID;
-  nvq_status st = check_kv(pool, num_pages, page_table, ld_table, max_pages, seq_lens);
+  nvq_status st = check_rows(k, ld_k, v, ld_v, Hkv, D, T);
+  if (st != NVQ_OK || T == 0) return st;
+  if ((reinterpret_cast<uintptr_t>(cu_tokens) & 3u) != 0) return NVQ_ERR_INVALID;
+  st = check_kv(pool, num_pages, page_table, ld_table, max_pages, seq_lens);
   if (st != NVQ_OK) return st;
-  const int64_t groups = (T + kTokens - 1) / kTokens;
-  if (groups > 0x7FFFFFFF) return NVQ_ERR_UNSUPPORTED;
-  int* err = device_error_word();
-  if (err == nullptr) return NVQ_ERR_CUDA;
-  const AppendArgs a{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), ld_k, ld_v,
-                     T, B, Hkv, cu_tokens, seq_lens, page_table, ld_table, max_pages,
-                     static_cast<uint8_t*>(pool), num_pages, err};
-  // a few tokens: spread their heads over the SMs
-  const int rows = kThreads / (D / 16 * kTokens);
-  const int64_t want = std::max<int64_t>(1, (2 * device_sms() + groups - 1) / groups);
-  const int y = static_cast<int>(std::min<int64_t>(want, (2 * Hkv + rows - 1) / rows));
-  const cudaError_t e = timed(NVQ_KERNEL_KV_APPEND, stream, [&] {
-    const dim3 grid(static_cast<unsigned>(groups), static_cast<unsigned>(y));
-    return launch_pdl(D == 128 ? kv_append_kernel<128> : kv_append_kernel<64>, grid, dim3(kThreads),
-                      0, stream, 1, a);
-  });
-  return e == cudaSuccess ? NVQ_OK : fail_cuda("kv append", e);
+  return launch_append({static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), ld_k,
+                        ld_v, T, B, Hkv, nullptr, cu_tokens, seq_lens, page_table, ld_table,
+                        max_pages, static_cast<uint8_t*>(pool), num_pages, nullptr},
+                       D, stream);
+}
+
+nvq_status nvfp4_kv_append_slots(const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                                 int64_t T, int Hkv, int D, const int64_t* slots, void* pool,
+                                 int64_t num_pages, nvq_stream_t stream) {
+  using namespace nvq;
+  if (T < 0 || Hkv < 1) return NVQ_ERR_INVALID;
+  const nvq_status st = check_rows(k, ld_k, v, ld_v, Hkv, D, T);
+  if (st != NVQ_OK || T == 0) return st;
+  if (slots == nullptr || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0 || pool == nullptr ||
+      (reinterpret_cast<uintptr_t>(pool) & 15u) != 0 || num_pages < 1 || num_pages > 0x7FFFFFFF)
+    return NVQ_ERR_INVALID;
+  return launch_append({static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), ld_k,
+                        ld_v, T, 0, Hkv, slots, nullptr, nullptr, nullptr, 0, 0,
+                        static_cast<uint8_t*>(pool), num_pages, nullptr},
+                       D, stream);
 }
 
 }  // extern "C"

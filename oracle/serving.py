@@ -88,3 +88,42 @@ def decode(q, pool, table, lens, scale, window=0, sinks=0, keep=None):
                 lse[i, hh] = torch.logsumexp(s, 0)
                 err_s[i, hh] = scale * (k.abs() @ qq[i, hh].abs()).max()
     return o, lse, mag, err_s
+
+
+def extend(new, lens, table, free, count, tokens, start=None, max_pages=None):
+    """Lists: (lens, count, cu, positions, slots, table) after the new tokens took their pages
+    from the end of free[:count], one sequence and one token after another; None if they do
+    not fit."""
+    table = [list(row) for row in table]
+    max_pages = len(table[0]) if max_pages is None else max_pages
+    left, cu, positions, slots, after = count, [0], [], [], []
+    for b, (t, n) in enumerate(zip(new, lens)):
+        t, n = max(t, 0), max(n, 0)
+        for p in range(n, n + t):
+            if p >= PAGE * max_pages:
+                return None
+            if p % PAGE == 0:
+                left -= 1
+                if left < 0:
+                    return None
+                table[b][p // PAGE] = free[left]
+            positions.append(p + (start[b] if start is not None else 0))
+            slots.append(table[b][p // PAGE] * PAGE + p % PAGE)
+        cu.append(cu[-1] + t)
+        after.append(n + t)
+    rest = tokens - cu[-1]
+    if rest < 0:
+        return None
+    return after, left, cu, positions + [-1] * rest, slots + [-1] * rest, table
+
+
+def release(done, lens, table, free, count):
+    """Lists: (lens, count, free) after the done sequences gave their pages back."""
+    free, after = list(free), list(lens)
+    for b, d in enumerate(done):
+        if d:
+            for i in range(-(-max(lens[b], 0) // PAGE)):
+                free[count] = table[b][i]
+                count += 1
+            after[b] = 0
+    return after, count, free

@@ -597,6 +597,60 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
                            int window, int sinks, void* o, float* lse, void* ws, size_t ws_bytes,
                            nvq_stream_t stream);
 
+/*
+ * Attention of many rows over the cache, without a mask: every token of sequence b
+ * attends to all kv_lens[b] cached keys (cross attention to an encoder's states,
+ * appended once and read by every step).
+ *   q          bf16 [T, H, D], row stride ld_q (elements, % 8 == 0, >= H*D)
+ *   cu_tokens  int32 [B + 1]: sequence b's tokens are rows [cu_tokens[b],
+ *              cu_tokens[b + 1]), not decreasing; NULL: T / B tokens each (T % B == 0).
+ *              Offsets outside [0, T] or that decrease are cut to what is there and
+ *              NVQ_ERR_INVALID is recorded for nvq_device_status()
+ *   page_table int32 [B, max_pages], kv_lens int32 [B]: the keys' pages and numbers,
+ *              checked as in attn_qat_decode
+ *   o          bf16 [T, H, D] contiguous, not overlapping q; lse f32 [T, H] or NULL
+ *              (written)
+ * S, o and lse as in attn_qat_decode (q~ quantized, the probabilities not).  A row
+ * without keys, and a row outside every sequence, gets o = 0 and lse = -inf.
+ * D in {64, 128}; T >= 1, T*H < 2^31 - 256, B, H <= 65535, and
+ * (T*H/Hkv/128 + B) * Hkv * max_pages < 2^37 (else NVQ_ERR_UNSUPPORTED).  Work is split over
+ * rows and keys and joined in a fixed order: results do not vary from run to run.
+ * ws: attn_qat_cross_workspace(T, B, H, Hkv, D, max_pages) bytes, 256-byte aligned;
+ * its size follows from the current device's multiprocessor count.
+ */
+size_t attn_qat_cross_workspace(int64_t T, int B, int H, int Hkv, int D, int max_pages);
+nvq_status attn_qat_cross(const void* q, int64_t ld_q, int64_t T, const void* pool,
+                          int64_t num_pages, const int32_t* page_table, int64_t ld_table,
+                          int max_pages, const int32_t* kv_lens, const int32_t* cu_tokens, int B,
+                          int H, int Hkv, int D, float scale, void* o, float* lse, void* ws,
+                          size_t ws_bytes, nvq_stream_t stream);
+
+/*
+ * attn_qat_decode for a batch whose sequences share cached prefixes, each prefix read
+ * once for all that share it.
+ *   q, page_table, seq_lens  as in attn_qat_decode: the new tokens, and the pages and
+ *                number of every sequence's own keys (0: none yet)
+ *   prefix_table int32 [S, prefix_pages] (row stride ld_prefix), prefix_lens int32 [S]:
+ *                the shared keys of group s, in the same pool (0: none)
+ *   cu_seqs      int32 [S + 1]: sequences [cu_seqs[s], cu_seqs[s + 1]) share prefix s;
+ *                those outside all groups have none; checked as attn_qat_cross's
+ *                cu_tokens.  NULL: B / S consecutive sequences a group (B % S == 0)
+ * o and lse are attn_qat_decode's over the prefix's keys and the sequence's own
+ * together; the two parts meet in fp32.  Positions are the caller's: a sequence's own
+ * tokens follow prefix_lens[s] others.  No window.  Limits of attn_qat_decode, and of
+ * attn_qat_cross for B rows and S sequences.  ws: attn_qat_decode_prefix_workspace(...)
+ * bytes, 256-byte aligned; follows from the multiprocessor count.
+ */
+size_t attn_qat_decode_prefix_workspace(int B, int S, int H, int Hkv, int D, int max_pages,
+                                        int prefix_pages);
+nvq_status attn_qat_decode_prefix(const void* q, int64_t ld_q, const void* pool, int64_t num_pages,
+                                  const int32_t* page_table, int64_t ld_table, int max_pages,
+                                  const int32_t* seq_lens, const int32_t* prefix_table,
+                                  int64_t ld_prefix, int prefix_pages, const int32_t* prefix_lens,
+                                  const int32_t* cu_seqs, int S, int B, int H, int Hkv, int D,
+                                  float scale, void* o, float* lse, void* ws, size_t ws_bytes,
+                                  nvq_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Per-kernel device timing (a profiling aid; no counterpart in the pages)  */
 /* ------------------------------------------------------------------------ */

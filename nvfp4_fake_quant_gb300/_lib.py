@@ -79,6 +79,16 @@ SIGNATURES = {
     "attn_qat_decode": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int,
                                 c_void_p, c_int, c_int, c_int, c_int, c_float, c_int, c_int,
                                 c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "attn_qat_cross_workspace": (c_size_t, [c_int64, c_int, c_int, c_int, c_int, c_int]),
+    "attn_qat_cross": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                               c_int, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_float,
+                               c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "attn_qat_decode_prefix_workspace": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int,
+                                                    c_int]),
+    "attn_qat_decode_prefix": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                       c_int, c_void_p, c_void_p, c_int64, c_int, c_void_p,
+                                       c_void_p, c_int, c_int, c_int, c_int, c_int, c_float,
+                                       c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "vsa_reorder": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                             c_int, c_void_p, c_void_p]),
     "vsa_select_workspace": (c_size_t, [c_int, c_int, c_int, c_int]),

@@ -906,6 +906,106 @@ def attn_qat_decode(q, pool, page_table, seq_lens, scale=None, window=0, sinks=0
     return o, lse
 
 
+def _with_workspace(index, name, args, workspace, size, like):
+    """The entry point with the caller's workspace, or with one of our own where none is given
+    or it is too small (or misaligned)."""
+    if workspace is not None:
+        try:
+            return _launch(index, name, *args, workspace.data_ptr(),
+                           workspace.numel() * workspace.element_size())
+        except _lib.NvqError as e:
+            if e.status != 3:
+                raise
+    ws = _workspace(_on(index, name + "_workspace", *size), like.device, None)
+    _launch(index, name, *args, ws.data_ptr(), ws.numel())
+
+
+def _check_offsets(cu, name, groups, rows):
+    """A device list of offsets, or None for equal groups."""
+    if cu is not None:
+        if _int32(cu, name, 1)[0][0] != groups + 1:
+            raise ValueError(f"{name} must have {groups + 1} entries")
+    elif groups == 0 or rows % groups:
+        raise ValueError(f"without {name} equal groups are expected: {rows} rows, {groups} groups")
+
+
+def attn_qat_cross_workspace(t, b, h, hkv, d, max_pages) -> int:
+    return int(_lib.load().attn_qat_cross_workspace(t, b, h, hkv, d, max_pages))
+
+
+def attn_qat_cross(q, pool, page_table, kv_lens, cu_tokens=None, scale=None, o=None, lse=None,
+                   workspace=None):
+    """Attention of every token of a sequence to all of the sequence's cached keys (an encoder's
+    states): q bf16 [T, H, D] (rows may be strided), page_table int32 [B, max_pages], kv_lens
+    int32 [B]; cu_tokens int32 [B + 1] offsets of the sequences' tokens (None: T / B each).
+    Returns (o bf16 [T, H, D], lse f32 [T, H]); rows without keys or outside all sequences are
+    0 and -inf.  No tokens is a valid call that launches nothing."""
+    t, h, d, ld_q = _rows_nd(q, "q")
+    pages, hkv, b, max_pages, ld_t = _check_cache(pool, page_table, kv_lens, d)
+    if t > 0 or cu_tokens is not None:
+        _check_offsets(cu_tokens, "cu_tokens", b, t)
+    scale = _scale(scale, d)
+    _check_workspace(workspace)
+    given = (o, lse)
+    o = _check_out(o, "o", (t, h, d), BF16, q)
+    lse = _check_out(lse, "lse", (t, h), torch.float32, q)
+    index = _device_of(q, pool, page_table, kv_lens, cu_tokens, o, lse, workspace)
+    if t == 0 and attn_qat_cross_workspace(1, max(b, 1), h, hkv, d, max(max_pages, 1)):
+        return o, lse  # no tokens
+    if b == 0 and attn_qat_cross_workspace(t, 1, h, hkv, d, 1):  # no sequences: rows outside all
+        o.zero_()
+        lse.fill_(-math.inf)
+        return o, lse
+    _with_workspace(index, "attn_qat_cross",
+                    (q.data_ptr(), ld_q, t, pool.data_ptr(), pages, page_table.data_ptr(), ld_t,
+                     max_pages, kv_lens.data_ptr(), _ptr(cu_tokens), b, h, hkv, d, scale,
+                     o.data_ptr(), lse.data_ptr()),
+                    workspace, (t, b, h, hkv, d, max_pages), q)
+    _overwritten(*given)
+    return o, lse
+
+
+def attn_qat_decode_prefix_workspace(b, groups, h, hkv, d, max_pages, prefix_pages) -> int:
+    return int(_lib.load().attn_qat_decode_prefix_workspace(b, groups, h, hkv, d, max_pages,
+                                                            prefix_pages))
+
+
+def attn_qat_decode_prefix(q, pool, page_table, seq_lens, prefix_table, prefix_lens, cu_seqs=None,
+                           scale=None, o=None, lse=None, workspace=None):
+    """attn_qat_decode where groups of sequences share cached prefixes, each read once:
+    page_table and seq_lens tell of the sequences' own keys, prefix_table int32 [S, pages] and
+    prefix_lens int32 [S] of the shared ones, cu_seqs int32 [S + 1] which sequences share them
+    (None: B / S consecutive ones each).  Returns (o bf16 [B, H, D], lse f32 [B, H]) over both
+    together.  No sequences is a valid call that launches nothing."""
+    b, h, d, ld_q = _rows_nd(q, "q")
+    pages, hkv, bt, max_pages, ld_t = _check_cache(pool, page_table, seq_lens, d)
+    if bt != b:
+        raise ValueError(f"q has {b} rows, page_table {bt}")
+    _, _, s, prefix_pages, ld_p = _check_cache(pool, prefix_table, prefix_lens, d)
+    if b > 0 or cu_seqs is not None:
+        _check_offsets(cu_seqs, "cu_seqs", s, b)
+    if s == 0:  # no prefixes (offsets of no groups)
+        return attn_qat_decode(q, pool, page_table, seq_lens, scale, 0, 0, o, lse, workspace)
+    scale = _scale(scale, d)
+    _check_workspace(workspace)
+    given = (o, lse)
+    o = _check_out(o, "o", (b, h, d), BF16, q)
+    lse = _check_out(lse, "lse", (b, h), torch.float32, q)
+    index = _device_of(q, pool, page_table, seq_lens, prefix_table, prefix_lens, cu_seqs, o, lse,
+                       workspace)
+    if b == 0 and attn_qat_decode_prefix_workspace(1, s, h, hkv, d, max(max_pages, 1),
+                                                   max(prefix_pages, 1)):
+        return o, lse  # no sequences
+    _with_workspace(index, "attn_qat_decode_prefix",
+                    (q.data_ptr(), ld_q, pool.data_ptr(), pages, page_table.data_ptr(), ld_t,
+                     max_pages, seq_lens.data_ptr(), prefix_table.data_ptr(), ld_p, prefix_pages,
+                     prefix_lens.data_ptr(), _ptr(cu_seqs), s, b, h, hkv, d, scale, o.data_ptr(),
+                     lse.data_ptr()),
+                    workspace, (b, s, h, hkv, d, max_pages, prefix_pages), q)
+    _overwritten(*given)
+    return o, lse
+
+
 # Kernel kinds of nvq_timing_read (include/nvfp4attn.h, NVQ_KERNEL_*)
 KERNEL_KINDS = {"quantize": 0, "attn_fwd": 1, "bwd_delta": 2, "bwd_dkdv": 3, "bwd_dq": 4,
                 "global_sf": 5, "vsa": 6, "linear": 7}

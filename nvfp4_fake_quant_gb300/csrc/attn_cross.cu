@@ -1,0 +1,946 @@
+// Attention of many query rows over the paged NVFP4 cache, every row of a sequence seeing all
+// of the sequence's cached keys:
+//   S_j = scale q~ . K~_j,  o = sum_j exp(S_j - lse) V~_j,  lse = ln sum exp S_j
+// The rows of a (sequence, KV head) are its tokens times the query heads that share the KV
+// head.  Two callers: cross attention (the keys: an encoder's states), and single tokens
+// behind a shared prefix (a "sequence": the batch entries that share it; the keys: the
+// prefix, read once for all of them).
+//
+// Work split.  Tiles (128 rows x one page of 128 keys) of all (sequence, KV head, row tile)
+// lie one after another on one line, cut into equal runs, one CTA each, whatever the lengths.
+// A segment (one sequence, KV head and row tile) inside a run is written by it; one that
+// crosses runs leaves (m, l, sum p V~) per run in the workspace, joined in run order by a
+// second kernel: results do not vary from run to run.
+//
+// One CTA, sixteen warps:
+//   producer   K codes by tensor-map loads with the swizzle the MMA reads, the record's rest
+//              by bulk copies, into a ring of stages, with a description of each tile
+//   S          scales of K into the scale operand's order; S = Q~ K~^T as block-scaled FP4
+//              tcgen05 MMAs on the codes, into one of two buffers of 128 columns
+//   PV         O += P V~ as f16 MMAs, P from tensor memory (over the S it came from)
+//   4 decode   V's codes times scales, exactly, to f16 rows in shared memory (scales run
+//              along D, so codes cannot be the FP4 operand of a product over keys); q~ of a
+//              segment that begins
+//   2 x 4      softmax, one thread a row: warpgroup w takes every other tile.  Both accumulate
+//              into one O, so p refers to a maximum that goes from tile to tile through shared
+//              memory, published before the exponentials; it is raised only where a score
+//              exceeds it by 8 (log2), when that tile's threads rescale O themselves.
+// p is rounded to f16 (below 2^8), its sum taken before the rounding; all sums are fp32.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "nvq_internal.h"
+#include "nvq_kv.cuh"
+#include "nvq_ptx.cuh"
+#include "nvq_quant.cuh"
+
+namespace nvq {
+
+namespace {
+
+constexpr int kRows = 128;     // query rows of a tile
+constexpr int kThreads = 512;
+constexpr int kDecodeWarp = 8, kProducerWarp = 12, kSWarp = 13, kPvWarp = 14, kSpareWarp = 15;
+constexpr int kDescs = 16;     // descriptions outlive their stages by the tiles in softmax
+constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// tensor memory columns: S of tile j at 128 (j & 1), O, the scales of q~ (two buffers) and of K
+// (four: a copy never overwrites what an MMA in flight may read, see the S warp)
+constexpr uint32_t kO = 256, kSfQ = 384, kSfK = 400;
+
+enum : int { kStart = 1, kSecond = 2, kNextEnd = 4, kEnd = 8, kAbsent = 16 };
+
+struct Tile {
+  int flags, valid;  // keys of the page that hold tokens
+  int rows;          // of the segment's 128
+  int row0;          // its first row among the rows of its (sequence, KV head)
+  int tok0, hk;      // first token of the sequence; KV head
+  int slot;          // where the segment's part goes (-1: it is whole)
+  int seg;           // segments before this one in the run
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr uint32_t kRec = record_bytes(D);
+  static constexpr uint32_t kV = kRows * D * 2;          // a page's V~ in f16
+  static constexpr uint32_t kQ = kRows * D / 2;          // codes of q~
+  static constexpr uint32_t kQSc = D / 64 * 512;         // and scales
+  static constexpr uint32_t kVAt = kStages * kRec;       // [2]
+  static constexpr uint32_t kQAt = kVAt + 2 * kV;        // [2]
+  static constexpr uint32_t kQScAt = kQAt + 2 * kQ;      // [2]
+  static constexpr uint32_t kMAt = kQScAt + 2 * kQSc;    // float [2][128]: maximum by tile parity
+  static constexpr uint32_t kLAt = kMAt + 2 * kRows * 4;  // float2 [2][128]: (m, l) by segment parity
+  static constexpr uint32_t kDescAt = kLAt + 2 * kRows * 8;
+  static constexpr uint32_t kBarAt = kDescAt + kDescs * 32;
+  static constexpr int kBars = 2 * kStages + kDescs + 2 * 7 + 8 + 8 + 3;
+  // heads of 64: padded so that no CTA of the few-rows linear lies beside one
+  static constexpr uint32_t kUsed = kBarAt + kBars * 8 + 1024;
+  static constexpr uint32_t kSmem = kUsed > 152 * 1024 ? kUsed : 152 * 1024;
+  static_assert(kRec % 1024 == 0 && kQ % 1024 == 0, "swizzle atoms");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(apart_from_linear_small(kSmem), "tensor memory");
+};
+
+// A segment that begins in a run and goes on in later ones; last < 0: none.
+struct Split {
+  int run, last, slot, rows, row0, tok0, hk, pad;
+};
+
+struct CrossArgs {
+  const uint16_t* q;
+  int64_t ld_q;
+  int T;
+  const uint8_t* pool;
+  int64_t num_pages;
+  const int32_t* table;
+  int64_t ld_table;
+  int max_pages;
+  const int32_t* lens;
+  const int32_t* cu;
+  int per_seq;  // tokens of each sequence where cu is null
+  int B, H, Hkv, G;
+  float scale_log2;
+  __nv_bfloat16* o;  // or, where null, o32 with the logarithms (base 2) in lse
+  float* o32;
+  float* lse;
+  Split* split;
+  float* parts;  // [2 runs][part_rows] (m, l), then [part_rows][D]
+  int part_rows, runs;
+  int* err;
+};
+
+__host__ __device__ constexpr int64_t part_floats(int rows, int D) {
+  return static_cast<int64_t>(rows) * (D + 2);
+}
+
+struct Extent {
+  int tok0, toks, len, row_tiles, key_tiles;
+};
+
+__device__ __forceinline__ Extent extent(const CrossArgs& a, int s, bool* bad) {
+  Extent e;
+  if (a.cu == nullptr) {
+    e.tok0 = s * a.per_seq;
+    e.toks = a.per_seq;
+    *bad = false;
+  } else {
+    const int lo = a.cu[s], hi = a.cu[s + 1];
+    e.tok0 = min(max(lo, 0), a.T);
+    const int end = min(max(hi, e.tok0), a.T);
+    e.toks = end - e.tok0;
+    *bad = lo != e.tok0 || hi != end;
+  }
+  const int cap = a.max_pages * kPage, n = a.lens[s];
+  *bad |= n > cap;
+  e.len = max(0, min(n, cap));
+  e.row_tiles = (e.toks * a.G + kRows - 1) / kRows;
+  e.key_tiles = e.row_tiles > 0 ? (e.len + kPage - 1) / kPage : 0;
+  return e;
+}
+
+// Place in a ring of `stages`: stage and the parity of its use.
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// q~ of a segment by the 128 decode threads: codes in the swizzled rows of the A operand, scales
+// in the 512-byte blocks of the scale operand.  Rows beyond the segment's: zeros.
+template <int D>
+__device__ __forceinline__ void quantize_q(const CrossArgs& a, const Tile& td, uint8_t* codes,
+                                           uint8_t* scales, int t) {
+  constexpr int kBlocks = D / 16, kStep = 128 / kBlocks, kBatch = 4;
+  const int j = t % kBlocks;
+  for (int i = 0; i < kRows / kStep; i += kBatch) {
+    uint4 lo[kBatch], hi[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int n = (i + u) * kStep + t / kBlocks;
+      lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
+      if (n < td.rows) {
+        const int row = td.row0 + n, tok = row / a.G;
+        const uint16_t* src = a.q + (td.tok0 + tok) * a.ld_q +
+                              static_cast<int64_t>(td.hk * a.G + row - tok * a.G) * D + j * 16;
+        lo[u] = ld16(src);
+        hi[u] = ld16(src + 8);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int n = (i + u) * kStep + t / kBlocks;
+      const uint32_t v[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w, hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+      const Codes16 r = codes16_unit(v);
+      const int swz = D == 128 ? (n >> 1) & 3 : (n >> 2) & 1;  // 64- and 32-byte swizzles
+      *reinterpret_cast<uint2*>(codes + n * (D / 2) + (((j >> 1) ^ swz) << 4) + (j & 1) * 8) =
+          make_uint2(r.codes[0], r.codes[1]);
+      scales[(j >> 2) * 512 + (n & 31) * 16 + (n >> 5) * 4 + (j & 3)] =
+          static_cast<uint8_t>(r.sbyte);
+    }
+  }
+}
+
+// K's scales [128][D/16] to D/64 blocks of 512 bytes, in place: row r of a block holds the words
+// (4 scales) of keys r, r + 32, r + 64, r + 96.
+template <int D>
+__device__ __forceinline__ void arrange_scales(uint8_t* sc, int lane) {
+  uint32_t w[D / 64][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (D == 128) {
+      const uint2 v = *reinterpret_cast<const uint2*>(sc + (lane + 32 * i) * 8);
+      w[0][i] = v.x;
+      w[1][i] = v.y;
+    } else {
+      w[0][i] = *reinterpret_cast<const uint32_t*>(sc + (lane + 32 * i) * 4);
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k)
+    *reinterpret_cast<uint4*>(sc + k * 512 + lane * 16) =
+        make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+}
+
+// V~ of a page as f16 rows of 64 elements (128 bytes, swizzled; elements 64.. in a second block)
+// by four warps, 32 keys each.  A lane takes 32 elements (16 bytes of codes, two scales) of a
+// key; lanes of consecutive pieces read consecutive bytes.  In heads of 128 the lanes of a row's
+// second half take their words in another order, so that no two of eight lanes write the same
+// banks.  Keys behind the last token become zeros: their bytes may be anything.
+template <int D>
+__device__ __forceinline__ void decode_v(const uint8_t* rec, uint8_t* dst, int valid, int warp,
+                                         int lane) {
+  constexpr int kPieces = D / 32, kKeys = 32 / kPieces;
+  const int piece = lane % kPieces, flip = piece >> 1;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int key = 32 * warp + i * kKeys + lane / kPieces;
+    const uint4 c = *reinterpret_cast<const uint4*>(rec + v_codes_at(D) + key * (D / 2) + piece * 16);
+    uint32_t sc = *reinterpret_cast<const uint16_t*>(rec + v_scales_at(D) + key * (D / 16) + piece * 2);
+    if (key >= valid) sc = 0;
+    const uint32_t s2 = e4m3x2_to_f16x2(sc);
+    const uint32_t sa = __byte_perm(s2, 0, 0x1010), sb = __byte_perm(s2, 0, 0x3232);
+    const uint32_t w[4] = {flip ? c.z : c.x, flip ? c.w : c.y, flip ? c.x : c.z, flip ? c.y : c.w};
+    const uint32_t s[2] = {flip ? sb : sa, flip ? sa : sb};
+    uint8_t* row = dst + (piece >> 1) * (kRows * 128) + key * 128;
+    const int chunk = ((piece & 1) * 4 + 2 * flip) ^ (key & 7);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      uint32_t h[4];
+      e2m1x8_to_f16x2(w[x], h);
+      *reinterpret_cast<uint4*>(row + ((chunk ^ x) << 4)) =
+          make_uint4(hmul2(h[0], s[x >> 1]), hmul2(h[1], s[x >> 1]), hmul2(h[2], s[x >> 1]),
+                     hmul2(h[3], s[x >> 1]));
+    }
+  }
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  uint32_t a[16], b[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    a[i] = r[i];
+    b[i] = r[16 + i];
+  }
+  tmem_st16(taddr, a);
+  tmem_st16(taddr + 16, b);
+}
+
+// What is written as a row's lse: the natural logarithm, or base 2 beside an output in fp32.
+__device__ __forceinline__ float row_lse(const CrossArgs& a, float m, float l) {
+  if (!(l > 0.f)) return -INFINITY;
+  const float v = m + log2f(l);
+  return a.o != nullptr ? v * kLn2 : v;
+}
+
+// A token without visible keys: o = 0 (in fp32 left as it is), lse = -inf.
+template <int D>
+__device__ __forceinline__ void empty_token(const CrossArgs& a, int tok, int lane) {
+  const int64_t row0 = static_cast<int64_t>(tok) * a.H;
+  if (a.o != nullptr)
+    for (int x = lane; x < a.H * (D / 8); x += 32)
+      reinterpret_cast<uint4*>(a.o + row0 * D)[x] = make_uint4(0, 0, 0, 0);
+  if (a.lse != nullptr)
+    for (int x = lane; x < a.H; x += 32) a.lse[row0 + x] = -INFINITY;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_kernel(const __grid_constant__ CUtensorMap tk, const CrossArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int64_t warp_sum[kThreads / 32];
+  __shared__ int64_t start_before;
+  __shared__ int start_s;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) &
+                                             ~static_cast<uintptr_t>(1023u));
+  float* m_of = reinterpret_cast<float*>(smem + C::kMAt);     // [2][128]
+  float2* ml_of = reinterpret_cast<float2*>(smem + C::kLAt);  // [2][128]
+  Tile* desc = reinterpret_cast<Tile*>(smem + C::kDescAt);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarAt);
+  uint64_t* empty = full + C::kStages;        // S done with the stage, four decode warps
+  uint64_t* described = empty + C::kStages;   // [kDescs]
+  uint64_t* v_full = described + kDescs;      // [2], four decode warps
+  uint64_t* v_empty = v_full + 2;             // [2]
+  uint64_t* q_full = v_empty + 2;             // [2], four decode warps
+  uint64_t* q_empty = q_full + 2;             // [2]
+  uint64_t* s_full = q_empty + 2;             // [2]
+  uint64_t* p_full = s_full + 2;              // [2], four softmax warps
+  uint64_t* pv_done = p_full + 2;             // [2]
+  uint64_t* m_ready = pv_done + 2;            // [2][4]: maximum of tile parity, by quarter
+  uint64_t* l_ready = m_ready + 8;            // [2][4]: the other warpgroup's (m, l), by segment
+  uint64_t* o_read = l_ready + 8;             // four softmax warps
+  uint64_t* drain = o_read + 1;
+  volatile int* abort = &abort_word;
+  pdl_trigger();
+
+  if (threadIdx.x == 0) {
+    *abort = 0;
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 5);
+    }
+    for (int i = 0; i < kDescs; ++i) mbar_init(&described[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&v_full[i], 4);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&q_full[i], 4);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&m_ready[i], 1);
+      mbar_init(&l_ready[i], 1);
+    }
+    mbar_init(o_read, 4);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
+    fence_mbar_init();
+  }
+  if (warp == kSpareWarp) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+    tma_prefetch_desc(&tk);
+  }
+  pdl_wait();  // before this nothing that another kernel may have written is read
+  // ---- the run of this CTA: a scan over the sequences
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int s_lo = min(a.B, static_cast<int>(threadIdx.x) * per), s_hi = min(a.B, s_lo + per);
+  int64_t mine = 0;
+  for (int s = s_lo; s < s_hi; ++s) {
+    bool bad;
+    const Extent e = extent(a, s, &bad);
+    mine += static_cast<int64_t>(e.row_tiles) * e.key_tiles * a.Hkv;
+    if (bad && blockIdx.x == 0) atomicMax(a.err, kErrTable);
+  }
+  int64_t scan = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, off);
+    if (lane >= off) scan += v;
+  }
+  if (lane == 31) warp_sum[warp] = scan;
+  __syncthreads();
+  int64_t all = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) scan += warp_sum[w];
+    all += warp_sum[w];
+  }
+  const int64_t before = scan - mine;  // tiles before this thread's sequences
+  const int run = blockIdx.x;
+  // all < 2^37 (check_cross), runs < 2^10: no overflow
+  const int64_t n_runs = all < a.runs ? all : a.runs;
+  const int64_t u0 = run < n_runs ? all * run / n_runs : all;
+  const int64_t u1 = run < n_runs ? all * (run + 1) / n_runs : all;
+  if (mine > 0 && before <= u0 && u0 < before + mine) {
+    int64_t at = before;
+    int s = s_lo;
+    for (;; ++s) {
+      bool bad;
+      const Extent e = extent(a, s, &bad);
+      const int64_t n = static_cast<int64_t>(e.row_tiles) * e.key_tiles * a.Hkv;
+      if (u0 < at + n) break;
+      at += n;
+    }
+    start_s = s;
+    start_before = at;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int n_tiles = static_cast<int>(u1 - u0);
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) a.split[run].last = -1;
+    if (n_tiles > 0) {
+      int s = start_s;
+      bool bad, ok = true;
+      Extent e = extent(a, s, &bad);
+      int64_t seg0 = start_before;  // line position of the sequence's first tile
+      const int64_t nth = (u0 - seg0) / e.key_tiles;  // segment of the sequence
+      int hk = static_cast<int>(nth / e.row_tiles);
+      int rt = static_cast<int>(nth - static_cast<int64_t>(hk) * e.row_tiles);
+      int i = static_cast<int>(u0 - seg0 - nth * e.key_tiles);
+      int n = 0;
+      Tile td;
+      td.seg = 0;
+      Ring ring;
+      while (n < n_tiles && ok) {
+        // ---- one segment (the part of it that lies in the run: tiles i .. i_end - 1)
+        const int64_t first = seg0 + (static_cast<int64_t>(hk) * e.row_tiles + rt) * e.key_tiles;
+        const int i0 = i, i_end = min(e.key_tiles, i + n_tiles - n);
+        const bool whole = first >= u0 && first + e.key_tiles <= u1;
+        td.row0 = rt * kRows;
+        td.rows = min(kRows, e.toks * a.G - td.row0);
+        td.tok0 = e.tok0;
+        td.hk = hk;
+        // a part that begins with the run goes to the run's slot 0, one inside it to slot 1
+        td.slot = whole ? -1 : 2 * run + (first > u0 ? 1 : 0);
+        const int32_t* table = a.table + s * a.ld_table;
+        int pages = 0;  // this lane's page number: of tile i0 + 32 k + lane
+        for (; i < i_end; ++i, ++n, ring.next(C::kStages)) {
+          if (((i - i0) & 31) == 0) {
+            const int x = i + lane;
+            pages = x < e.key_tiles ? table[x] : -1;
+          }
+          const int page = __shfl_sync(0xFFFFFFFFu, pages, (i - i0) & 31);
+          const bool there = page >= 0 && page < a.num_pages;
+          td.flags = (i == i0 ? kStart : 0) | (i == i0 + 1 ? kSecond : 0) |
+                     (i == i_end - 2 ? kNextEnd : 0) | (i == i_end - 1 ? kEnd : 0) |
+                     (there ? 0 : kAbsent);
+          td.valid = there ? min(kPage, e.len - i * kPage) : 0;
+          if (!there && lane == 0) atomicMax(a.err, kErrTable);
+          const int st = ring.s;
+          if (!(ok = mbar_wait_warp(&empty[st], ring.phase ^ 1, abort))) break;
+          if (lane == 0) {
+            desc[n % kDescs] = td;
+            mbar_arrive(&described[n % kDescs]);
+          }
+          __syncwarp();
+          uint8_t* dst = smem + st * C::kRec;
+          if (there) {
+            const int rec = page * a.Hkv + hk;
+            mbar_arrive_expect_tx_w(&full[st], C::kRec);
+            tma_load_4d_w(dst, &tk, 0, 0, rec, 0, &full[st]);
+            bulk_load_w(dst + v_codes_at(D),
+                        a.pool + static_cast<int64_t>(rec) * record_bytes(D) + v_codes_at(D),
+                        C::kRec - v_codes_at(D), &full[st]);
+          } else {
+            mbar_arrive_expect_tx_w(&full[st], 0);
+          }
+        }
+        if (lane == 0 && first >= u0 && first + e.key_tiles > u1) {
+          // the run that holds tile u: the last c with all c / n_runs <= u
+          const int64_t u = first + e.key_tiles - 1;
+          a.split[run] = {run, static_cast<int>(((u + 1) * n_runs + all - 1) / all - 1), td.slot,
+                          td.rows, td.row0, td.tok0, td.hk, 0};
+        }
+        if (n == n_tiles || !ok) break;
+        ++td.seg;
+        i = 0;
+        if (++rt == e.row_tiles) {
+          rt = 0;
+          if (++hk == a.Hkv) {
+            hk = 0;
+            seg0 += static_cast<int64_t>(e.row_tiles) * e.key_tiles * a.Hkv;
+            do {
+              e = extent(a, ++s, &bad);
+            } while (e.key_tiles == 0);
+          }
+        }
+      }
+      if (!ok) {  // let the copies already issued land before the block leaves
+        for (int m = max(0, n - C::kStages); m < n; ++m)
+          mbar_wait_warp(&full[m % C::kStages], (m / C::kStages) & 1, nullptr, 10000000ull);
+      }
+    }
+  } else if (warp == kSWarp) {
+    // ------------------------------------------------------------ S = Q~ K~^T
+    constexpr uint32_t idesc = idesc_mxf4nvf4(kRows, kPage);
+    constexpr uint32_t lay = D == 128 ? 4u : 6u, sbo = 4 * D;  // swizzle, bytes of 8 rows
+    bool ok = true;
+    Ring ring;
+    for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
+      const int st = ring.s;
+      if (!(ok = mbar_wait_warp(&described[n % kDescs], (n / kDescs) & 1, abort))) break;
+      const struct { int flags, seg; } td {desc[n % kDescs].flags, desc[n % kDescs].seg};
+      if (!(ok = mbar_wait_warp(&full[st], ring.phase, abort))) break;
+      const int qb = td.seg & 1;
+      if ((td.flags & kStart) &&
+          !(ok = mbar_wait_warp(&q_full[qb], (td.seg >> 1) & 1, abort)))
+        break;
+      tc_fence_after();
+      const uint32_t sfq = tmem + kSfQ + 8 * qb, sfk = tmem + kSfK + 8 * (n & 3);
+      uint8_t* stage = smem + st * C::kRec;
+      // The copies below go to columns whose last readers have completed: of K's scales the
+      // MMAs of tile n - 4, as those of tile n - 2 went out behind the PV of tile n - 4; of
+      // q's the MMAs of segment seg - 2, which the decode warps waited for.
+      if (td.flags & kStart) {
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+          tmem_cp_32x128_x4_w(sfq + 4 * k, smem_u32(smem + C::kQScAt + qb * C::kQSc) + 512 * k);
+      }
+      if (!(td.flags & kAbsent)) {
+        arrange_scales<D>(stage + k_scales_at(D), lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+          tmem_cp_32x128_x4_w(sfk + 4 * k, smem_u32(stage + k_scales_at(D)) + 512 * k);
+      }
+      // S's buffer is free when the PV of tile n - 2 has read the P that lies over it
+      if (n >= 2) {
+        if (!(ok = mbar_wait_warp(&pv_done[n & 1], ((n - 2) >> 1) & 1, abort))) break;
+        tc_fence_after();
+      }
+      if (!(td.flags & kAbsent)) {
+        const uint32_t qa = smem_u32(smem + C::kQAt + qb * C::kQ), ka = smem_u32(stage);
+        const uint64_t qd[2] = {sdesc(qa, 16, sbo, lay), sdesc(qa, 16, sbo, lay) + 2};
+        const uint64_t kd[2] = {sdesc(ka, 16, sbo, lay), sdesc(ka, 16, sbo, lay) + 2};
+        umma_fp4_group_w<D / 64>(tmem + 128 * (n & 1), qd, kd, idesc, sfq, sfk,
+                                 bar_u32(&s_full[n & 1]), bar_u32(&empty[st]));
+      } else {
+        umma_commit_w(&s_full[n & 1]);
+        umma_commit_w(&empty[st]);
+      }
+      if (td.flags & kEnd) umma_commit_w(&q_empty[qb]);
+    }
+    umma_commit_w(&drain[0]);  // the MMAs in flight end before the block
+    mbar_wait_warp(&drain[0], 0, nullptr, 10000000ull);
+  } else if (warp == kPvWarp) {
+    // ------------------------------------------------------------ O += P V~
+    constexpr uint32_t idesc = idesc_f16(kRows, D, 0, 0, 1);
+    const uint64_t v_d0 = sdesc_sw128(smem_u32(smem + C::kVAt), kRows * 128, 1024);
+    for (int n = 0; n < n_tiles; ++n) {
+      const int b = n & 1;
+      const uint32_t phase = (n >> 1) & 1;
+      if (!mbar_wait_warp(&described[n % kDescs], (n / kDescs) & 1, abort)) break;
+      const struct { int flags, seg; } td {desc[n % kDescs].flags, desc[n % kDescs].seg};
+      // O of the segment before has been read
+      if ((td.flags & kStart) && td.seg > 0 &&
+          !mbar_wait_warp(o_read, (td.seg - 1) & 1, abort))
+        break;
+      if (!mbar_wait_warp(&v_full[b], phase, abort)) break;
+      if (!mbar_wait_warp(&p_full[b], phase, abort)) break;
+      tc_fence_after();
+      uint32_t p[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) p[k] = tmem + 128 * b + 8 * k;
+      umma_f16_ts8_w(tmem + kO, p, v_d0 + static_cast<uint64_t>(b) * (C::kV >> 4), idesc,
+                     td.flags & kStart ? 0u : 1u, bar_u32(&pv_done[b]), bar_u32(&v_empty[b]));
+    }
+    umma_commit_w(&drain[1]);
+    mbar_wait_warp(&drain[1], 0, nullptr, 10000000ull);
+  } else if (warp >= kDecodeWarp && warp < kDecodeWarp + 4) {
+    // ------------------------------------------------------------ V~, q~
+    const int t = threadIdx.x - 32 * kDecodeWarp;
+    Ring ring;
+    for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
+      const int st = ring.s, b = n & 1;
+      if (!mbar_wait_warp(&described[n % kDescs], (n / kDescs) & 1, abort)) break;
+      const Tile td = desc[n % kDescs];
+      if (td.flags & kStart) {
+        const int qb = td.seg & 1;
+        if (!mbar_wait_warp(&q_empty[qb], ((td.seg >> 1) & 1) ^ 1, abort)) break;
+        quantize_q<D>(a, td, smem + C::kQAt + qb * C::kQ, smem + C::kQScAt + qb * C::kQSc, t);
+        fence_proxy_async_smem();
+        mbar_arrive_warp(&q_full[qb]);
+      }
+      if (!mbar_wait_warp(&full[st], ring.phase, abort)) break;
+      if (!mbar_wait_warp(&v_empty[b], ((n >> 1) & 1) ^ 1, abort)) break;
+      decode_v<D>(smem + st * C::kRec, smem + C::kVAt + b * C::kV, td.valid, warp - kDecodeWarp,
+                  lane);
+      fence_proxy_async_smem();
+      mbar_arrive_warp(&v_full[b]);
+      mbar_arrive_warp(&empty[st]);
+    }
+  } else if (warp < kDecodeWarp) {
+    // ------------------------------------------------------------ softmax
+    const int wg = warp >> 2, quarter = warp & 3;
+    const int r = threadIdx.x & 127;  // row of the tile == lane of tensor memory
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint64_t scale2 = pk2(a.scale_log2, a.scale_log2);
+    float m = -INFINITY;  // reference maximum (log2 units) of this warpgroup's last tile
+    uint64_t l2 = pk2(0.f, 0.f);
+    for (int n = wg; n < n_tiles; n += 2) {
+      const int b = n & 1;
+      if (!mbar_wait_warp(&described[n % kDescs], (n / kDescs) & 1, abort)) break;
+      const Tile td = desc[n % kDescs];
+      const bool live = quarter * 32 < td.rows;  // else: rows that nobody reads
+      if (!mbar_wait_warp(&s_full[b], (n >> 1) & 1, abort)) break;
+      tc_fence_after();
+      const uint32_t s_at = lanes + 128 * b;
+      if (td.flags & (kStart | kSecond)) {
+        m = -INFINITY;
+        l2 = pk2(0.f, 0.f);
+      }
+      float mx = -INFINITY;
+      if (live) {
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          uint32_t x[32], y[32];
+          tmem_ld32(s_at + 32 * c, x);
+          tmem_ld32(s_at + 32 * c + 32, y);
+          tmem_wait_ld();
+          if (td.valid < kPage) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (32 * c + i >= td.valid) x[i] = 0xFF800000u;
+              if (32 * c + 32 + i >= td.valid) y[i] = 0xFF800000u;
+            }
+          }
+          float v[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            v[0] = max3f(v[0], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            v[1] = max3f(v[1], __uint_as_float(x[16 + i]), __uint_as_float(x[17 + i]));
+            v[2] = max3f(v[2], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+            v[3] = max3f(v[3], __uint_as_float(y[16 + i]), __uint_as_float(y[17 + i]));
+          }
+          mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+        }
+        mx *= a.scale_log2;
+      }
+      // ---- the maximum so far, from the tile before; also where a segment begins, for the order
+      if (n > 0 &&
+          !mbar_wait_warp(&m_ready[4 * (b ^ 1) + quarter], ((n - 1) >> 1) & 1, abort))
+        break;
+      float old = td.flags & kStart ? -INFINITY : m_of[kRows * (b ^ 1) + r];
+      const bool grows = mx > old + kSlack || (old == -INFINITY && mx > -INFINITY);
+      const float now = grows ? mx : old;
+      m_of[kRows * b + r] = now;
+      mbar_arrive_warp(&m_ready[4 * b + quarter]);
+      if (!(td.flags & kStart) && __any_sync(0xFFFFFFFFu, grows)) {
+        // raised behind the segment's first tile: O so far, which the PV before has finished
+        if (!mbar_wait_warp(&pv_done[b ^ 1], ((n - 1) >> 1) & 1, abort)) break;
+        tc_fence_after();
+        const float c = grows ? ex2_f32(old - now) : 1.f;
+#pragma unroll
+        for (int x = 0; x < D; x += 32) {
+          uint32_t v[32];
+          tmem_ld32(lanes + kO + x, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * c);
+          tmem_st32(lanes + kO + x, v);
+        }
+        tmem_wait_st();
+      }
+      if (m != now) {  // raised since this warpgroup's last tile, by either
+        const float c = ex2_f32(m - now);  // 0 where the segment begins
+        l2 = mul2(l2, pk2(c, c));
+        m = now;
+      }
+      // ---- p = 2^(S log2e - m), over S
+      if (live) {
+        const float ref = -fmaxf(now, -3.4e38f);
+        const uint64_t neg_m = pk2(ref, ref);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t x[32], p[16];
+          tmem_ld32(s_at + 32 * c, x);
+          tmem_wait_ld();
+          if (td.valid < kPage) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= td.valid) x[i] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float p0, p1;
+            up2(fma2(pk2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale2, neg_m),
+                p0, p1);
+            p0 = ex2_f32(p0);
+            p1 = ex2_f32(p1);
+            l2 = add2(l2, pk2(p0, p1));
+            p[i] = pack_f16x2_rn(p0, p1);
+          }
+          tmem_st16(s_at + 16 * c, p);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      mbar_arrive_warp(&p_full[b]);
+      if (td.flags & kNextEnd) {  // the other warpgroup writes the segment
+        float l0, l1;
+        up2(l2, l0, l1);
+        ml_of[kRows * (td.seg & 1) + r] = make_float2(m, l0 + l1);
+        mbar_arrive_warp(&l_ready[4 * (td.seg & 1) + quarter]);
+      }
+      if (!(td.flags & kEnd)) continue;
+      // ---- the segment's end
+      float l0, l1;
+      up2(l2, l0, l1);
+      float l = l0 + l1;
+      // (m, l) of the other warpgroup; of a segment of one tile nobody else has one
+      if (td.flags & kStart) mbar_arrive_warp(&l_ready[4 * (td.seg & 1) + quarter]);
+      if (!mbar_wait_warp(&l_ready[4 * (td.seg & 1) + quarter], (td.seg >> 1) & 1, abort)) break;
+      if (!(td.flags & kStart)) {
+        const float2 v = ml_of[kRows * (td.seg & 1) + r];
+        if (v.x > -INFINITY) l = fmaf(v.y, ex2_f32(v.x - m), l);
+      }
+      if (!mbar_wait_warp(&pv_done[b], (n >> 1) & 1, abort)) break;
+      tc_fence_after();
+      const bool mine = r < td.rows;
+      const int row = td.row0 + r, tok = row / a.G;
+      const int64_t at = static_cast<int64_t>(td.tok0 + tok) * a.H + td.hk * a.G + row - tok * a.G;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      float* part = a.parts + max(td.slot, 0) * part_floats(a.part_rows, D);
+      if (live) {
+#pragma unroll
+        for (int x = 0; x < D; x += 32) {
+          uint32_t v[32];
+          __syncwarp();
+          tmem_ld32(lanes + kO + x, v);
+          tmem_wait_ld();
+          if (!mine) {
+          } else if (td.slot < 0 && a.o != nullptr) {
+            uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(
+                    __uint_as_float(v[8 * i + 2 * u]) * inv, __uint_as_float(v[8 * i + 2 * u + 1]) * inv);
+                w[u] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            const float f = td.slot < 0 ? inv : 1.f;
+            float4* dst = reinterpret_cast<float4*>(
+                td.slot < 0 ? a.o32 + at * D + x : part + 2 * a.part_rows + r * D + x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(__uint_as_float(v[4 * i]) * f, __uint_as_float(v[4 * i + 1]) * f,
+                                   __uint_as_float(v[4 * i + 2]) * f,
+                                   __uint_as_float(v[4 * i + 3]) * f);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive_warp(o_read);
+      if (mine) {
+        if (td.slot >= 0)
+          *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
+        else if (a.lse != nullptr)
+          a.lse[at] = row_lse(a, m, l);
+      }
+    }
+  } else if (warp == kSpareWarp) {
+    // ------------------------------------- rows without keys, rows outside of all sequences
+    const int ctas = static_cast<int>(gridDim.x);
+    for (int s0 = 0; s0 < a.B; s0 += 32) {
+      bool bad;
+      Extent e{0, 0, 0, 0, 1};
+      if (s0 + lane < a.B) e = extent(a, s0 + lane, &bad);
+      uint32_t none = __ballot_sync(0xFFFFFFFFu, e.toks > 0 && e.key_tiles == 0);
+      for (; none != 0; none &= none - 1) {
+        const int i = __ffs(none) - 1;
+        const int tok0 = __shfl_sync(0xFFFFFFFFu, e.tok0, i), toks = __shfl_sync(0xFFFFFFFFu, e.toks, i);
+        for (int t = run; t < toks; t += ctas) empty_token<D>(a, tok0 + t, lane);
+      }
+    }
+    if (a.cu != nullptr) {
+      const int lo = min(max(a.cu[0], 0), a.T), hi = min(max(a.cu[a.B], 0), a.T);
+      for (int t = run; t < lo; t += ctas) empty_token<D>(a, t, lane);
+      for (int64_t t = static_cast<int64_t>(hi) + run; t < a.T; t += ctas)
+        empty_token<D>(a, static_cast<int>(t), lane);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  report_abort(abort, a.err);
+  if (warp == kSpareWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the segments that cross runs, in run order.  Block (c, y): the segment that
+// begins in run c, if any; a thread takes four elements of a row.
+template <int D>
+__global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a) {
+  constexpr int kLanes = D / 4, kBatch = 4;
+  pdl_trigger();
+  pdl_wait();
+  const Split s = a.split[blockIdx.x];
+  // last < 0: nothing to join; what else is out of range was never written, by a kernel that gave
+  // up a wait and has reported it
+  if (s.run != static_cast<int>(blockIdx.x) || s.last < s.run || s.last >= a.runs || s.slot < 0 ||
+      s.slot >= 2 * a.runs || s.rows > a.part_rows)
+    return;
+  const int r = (blockIdx.y * 256 + threadIdx.x) / kLanes, x = threadIdx.x % kLanes;
+  if (r >= s.rows) return;
+  const int64_t stride = part_floats(a.part_rows, D);
+  float mx = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  // loads of a few parts in flight: one after another they cost a memory latency each
+  for (int c0 = s.run; c0 <= s.last; c0 += kBatch) {
+    float2 ml[kBatch];
+    float4 po[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int c = min(c0 + i, s.last);
+      const float* part = a.parts + (c == s.run ? s.slot : 2 * c) * stride;
+      ml[i] = *reinterpret_cast<const float2*>(part + 2 * r);
+      po[i] = *reinterpret_cast<const float4*>(part + 2 * a.part_rows + r * D + 4 * x);
+      if (c0 + i > s.last) ml[i] = make_float2(-INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float mn = fmaxf(mx, ml[i].x), ref = fmaxf(mn, -3.4e38f);
+      const float co = ex2_f32(mx - ref), cn = ex2_f32(ml[i].x - ref);
+      mx = mn;
+      l = l * co + ml[i].y * cn;
+      o = make_float4(o.x * co + po[i].x * cn, o.y * co + po[i].y * cn, o.z * co + po[i].z * cn,
+                      o.w * co + po[i].w * cn);
+    }
+  }
+  const int row = s.row0 + r, tok = row / a.G;
+  const int64_t at = static_cast<int64_t>(s.tok0 + tok) * a.H + s.hk * a.G + row - tok * a.G;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (a.o != nullptr) {
+    const __nv_bfloat162 h[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv),
+                                 __floats2bfloat162_rn(o.z * inv, o.w * inv)};
+    *reinterpret_cast<uint2*>(a.o + at * D + 4 * x) = *reinterpret_cast<const uint2*>(h);
+  } else {
+    *reinterpret_cast<float4*>(a.o32 + at * D + 4 * x) =
+        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  }
+  if (x == 0 && a.lse != nullptr) a.lse[at] = row_lse(a, mx, l);
+}
+
+template <int D>
+cudaError_t launch_cross_d(const CUtensorMap& tk, const CrossArgs& a, cudaStream_t stream) {
+  using C = Cfg<D>;
+  const cudaError_t e = cudaFuncSetAttribute(
+      cross_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(a.runs));
+  const cudaError_t k =
+      launch_pdl(cross_kernel<D>, grid, dim3(kThreads), C::kSmem, stream, 1, tk, a);
+  if (k != cudaSuccess) return k;
+  return launch_pdl(cross_join_kernel<D>,
+                    dim3(grid.x, static_cast<unsigned>(a.part_rows * (D / 4) / 256)), dim3(256), 0,
+                    stream, 1, a);
+}
+
+struct Plan {
+  int runs, part_rows;
+  size_t parts, total;
+};
+
+Plan plan(int64_t T, int B, int H, int Hkv, int D, int max_pages) {
+  const int64_t rows = T * (H / Hkv);
+  const int64_t tiles = (rows / kRows + B) * Hkv * max_pages;  // at most
+  Plan p;
+  p.runs = static_cast<int>(std::min<int64_t>(std::max<int64_t>(tiles, 1), device_sms()));
+  p.part_rows = static_cast<int>(std::min<int64_t>(kRows, (rows + 31) / 32 * 32));
+  p.parts = (p.runs * sizeof(Split) + 255) / 256 * 256;
+  p.total = p.parts + 2 * p.runs * part_floats(p.part_rows, D) * sizeof(float);
+  return p;
+}
+
+}  // namespace
+
+nvq_status check_cross(int64_t T, int B, int H, int Hkv, int D, int max_pages) {
+  if (T < 1 || B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || max_pages < 1 ||
+      max_pages > 0x7FFFFFFF / kPage)
+    return NVQ_ERR_INVALID;
+  if (D != 64 && D != 128) return NVQ_ERR_UNSUPPORTED;
+  if (B > 65535 || H > 65535 || T > 0x7FFFFF00 / H) return NVQ_ERR_UNSUPPORTED;
+  // (rows / 128 + B) Hkv < 2^24 + 2^33: no overflow; a run counts its tiles in 31 bits
+  const int64_t heads = (T * (H / Hkv) / kRows + B) * Hkv;
+  return heads * max_pages / 64 >= 0x7FFFFFFF ? NVQ_ERR_UNSUPPORTED : NVQ_OK;
+}
+
+size_t cross_workspace(int64_t T, int B, int H, int Hkv, int D, int max_pages) {
+  return plan(T, B, H, Hkv, D, max_pages).total;
+}
+
+nvq_status launch_cross(const CrossCall& c, uint8_t* ws, cudaStream_t stream) {
+  const Plan p = plan(c.T, c.B, c.H, c.Hkv, c.D, c.max_pages);
+  if (c.num_pages > 0x7FFFFFFF / c.Hkv) return NVQ_ERR_UNSUPPORTED;  // tensor-map coordinates
+  int* err = device_error_word();
+  if (err == nullptr) return NVQ_ERR_CUDA;
+  CUtensorMap tk;
+  if (const int r = make_kv_codes_map(&tk, c.pool, c.num_pages * c.Hkv, c.D, kPage); r != 0)
+    return fail_driver("cuTensorMapEncodeTiled", r);
+  const CrossArgs a{static_cast<const uint16_t*>(c.q), c.ld_q, static_cast<int>(c.T),
+                    static_cast<const uint8_t*>(c.pool), c.num_pages, c.page_table, c.ld_table,
+                    c.max_pages, c.kv_lens, c.cu_tokens, static_cast<int>(c.T / c.B), c.B, c.H,
+                    c.Hkv, c.H / c.Hkv, c.scale * kLog2e, static_cast<__nv_bfloat16*>(c.o), c.o32,
+                    c.lse, reinterpret_cast<Split*>(ws), reinterpret_cast<float*>(ws + p.parts),
+                    p.part_rows, p.runs, err};
+  const cudaError_t e = timed(NVQ_KERNEL_CROSS, stream, [&] {
+    return c.D == 128 ? launch_cross_d<128>(tk, a, stream) : launch_cross_d<64>(tk, a, stream);
+  });
+  return e == cudaSuccess ? NVQ_OK : fail_cuda("attn cross", e);
+}
+
+}  // namespace nvq
+
+extern "C" {
+
+size_t attn_qat_cross_workspace(int64_t T, int B, int H, int Hkv, int D, int max_pages) {
+  if (nvq::check_cross(T, B, H, Hkv, D, max_pages) != NVQ_OK) return 0;
+  const size_t n = nvq::cross_workspace(T, B, H, Hkv, D, max_pages);
+  return T == B ? std::max(n, attn_qat_decode_workspace(B, H, Hkv, D, max_pages)) : n;
+}
+
+nvq_status attn_qat_cross(const void* q, int64_t ld_q, int64_t T, const void* pool,
+                          int64_t num_pages, const int32_t* page_table, int64_t ld_table,
+                          int max_pages, const int32_t* kv_lens, const int32_t* cu_tokens, int B,
+                          int H, int Hkv, int D, float scale, void* o, float* lse, void* ws,
+                          size_t ws_bytes, nvq_stream_t stream) {
+  using namespace nvq;
+  nvq_status st = check_cross(T, B, H, Hkv, D, max_pages);
+  if (st != NVQ_OK) return st;
+  const int64_t row = static_cast<int64_t>(H) * D;
+  if (!(std::isfinite(scale) && scale > 0.f) || (cu_tokens == nullptr && T % B != 0) ||
+      (reinterpret_cast<uintptr_t>(cu_tokens) & 3u) != 0)
+    return NVQ_ERR_INVALID;
+  if (q == nullptr || o == nullptr || (reinterpret_cast<uintptr_t>(q) & 15u) != 0 ||
+      (reinterpret_cast<uintptr_t>(o) & 15u) != 0 || ld_q < row || ld_q % 8 != 0 ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return NVQ_ERR_INVALID;
+  st = check_kv(pool, num_pages, page_table, ld_table, max_pages, kv_lens);
+  if (st != NVQ_OK) return st;
+  if (ws == nullptr || ws_bytes < attn_qat_cross_workspace(T, B, H, Hkv, D, max_pages) ||
+      (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return NVQ_ERR_WORKSPACE;
+  // a row of q is read by one run after another, at whatever time: o elsewhere
+  if (ranges_meet(q, 2 * static_cast<uint64_t>((T - 1) * ld_q + row), o,
+                  2 * static_cast<uint64_t>(row * T)))
+    return NVQ_ERR_INVALID;
+  // one token a sequence: a row tile would be all but empty
+  if (cu_tokens == nullptr && T == B)
+    return attn_qat_decode(q, ld_q, pool, num_pages, page_table, ld_table, max_pages, kv_lens, B,
+                           H, Hkv, D, scale, 0, 0, o, lse, ws, ws_bytes, stream);
+  return launch_cross({q, ld_q, T, pool, num_pages, page_table, ld_table, max_pages, kv_lens,
+                       cu_tokens, B, H, Hkv, D, scale, o, nullptr, lse},
+                      static_cast<uint8_t*>(ws), stream);
+}
+
+}  // extern "C"

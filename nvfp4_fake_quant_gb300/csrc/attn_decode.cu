@@ -115,6 +115,8 @@ struct DecodeArgs {
   int window, sinks;
   __nv_bfloat16* o;
   float* lse;
+  const float* prior_o;   // [B, H, D]: o over other keys (a shared prefix), or null
+  const float* prior_l2;  // [B, H]: its logarithm of the sum of exponentials, base 2
   struct RunInfo* split;  // what crosses runs, by run or by segment (workspace)
   int by_segment;         // 1: entries by segment (there are fewer than runs)
   float* parts;           // [2 runs] parts (workspace)
@@ -157,6 +159,21 @@ struct Runs {
   }
 };
 
+// What a row has over its own keys (maximum m and sum l, log2 units) together with `prior`, the
+// logarithm over other keys: m and l of both, and the factors of the two sums of p V~ (the other
+// one is normalised).  Without other keys nothing changes.
+struct Fold {
+  float own, other;
+};
+__device__ __forceinline__ Fold fold_prior(float prior, float& m, float& l) {
+  if (!(prior > -INFINITY)) return {1.f, 0.f};
+  const float mn = fmaxf(m, prior);
+  const Fold f{ex2_f32(m - mn), ex2_f32(prior - mn)};
+  m = mn;
+  l = fmaf(l, f.own, f.other);
+  return f;
+}
+
 // The tiles of a sequence: pages [0, sink_pages) and [first, pages).
 struct Extent {
   int len, sink_pages, first, tiles, wstart;
@@ -183,6 +200,10 @@ __device__ __forceinline__ int kv_head(const DecodeArgs& a, int hg) {
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return __byte_perm(a, b, sel);
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
   uint32_t r;
@@ -680,10 +701,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
         if (extent(a, b, &over).tiles > 0) continue;
         for (int x = lane; a.by_segment && x < hgs; x += 32) a.split[b * hgs + x].last = -1;
         const int64_t row0 = static_cast<int64_t>(b) * a.H;
-        for (int x = lane; x < a.H * (D / 8); x += 32)
-          reinterpret_cast<uint4*>(a.o + row0 * D)[x] = make_uint4(0, 0, 0, 0);
+        for (int x = lane; x < a.H * (D / 8); x += 32) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (a.prior_o != nullptr && a.prior_l2[row0 + x / (D / 8)] > -INFINITY) {
+            const float4* p = reinterpret_cast<const float4*>(a.prior_o + row0 * D) + 2 * x;
+            const float4 lo = p[0], hi = p[1];
+            v = make_uint4(pack_bf16x2(lo.x, lo.y), pack_bf16x2(lo.z, lo.w),
+                           pack_bf16x2(hi.x, hi.y), pack_bf16x2(hi.z, hi.w));
+          }
+          reinterpret_cast<uint4*>(a.o + row0 * D)[x] = v;
+        }
         if (a.lse != nullptr)
-          for (int x = lane; x < a.H; x += 32) a.lse[row0 + x] = -INFINITY;
+          for (int x = lane; x < a.H; x += 32)
+            a.lse[row0 + x] = a.prior_o != nullptr ? a.prior_l2[row0 + x] * kLn2 : -INFINITY;
       }
     }
     Ring ring;
@@ -794,6 +824,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
           l = fmaf(v.y, c[w], l);
         }
         const int64_t row = static_cast<int64_t>(td.b) * a.H + hk * a.G + g0 + head;
+        Fold f{1.f, 0.f};
+        const bool folds = a.prior_o != nullptr && td.slot < 0;
+        if (folds) f = fold_prior(a.prior_l2[row], mx, l);
         const float inv = l > 0.f ? 1.f / l : 0.f;
         float* part = a.parts + static_cast<int64_t>(max(td.slot, 0)) * part_floats(D, C::kHeads);
 #pragma unroll
@@ -806,6 +839,14 @@ __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
                 join + (w * C::kHeads + head) * C::kRow + pos);
             o0 = fmaf(ov.x, c[w], o0);
             o1 = fmaf(ov.y, c[w], o1);
+          }
+          if (folds && f.other > 0.f) {
+            const float2 p = *reinterpret_cast<const float2*>(a.prior_o + row * D + element_of<D>(pos));
+            o0 = fmaf(o0, f.own, p.x * f.other);
+            o1 = fmaf(o1, f.own, p.y * f.other);
+          } else if (folds) {
+            o0 *= f.own;
+            o1 *= f.own;
           }
           if (td.slot < 0)
             *reinterpret_cast<__nv_bfloat162*>(a.o + row * D + element_of<D>(pos)) =
@@ -902,6 +943,17 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const DecodeArgs a) {
     }
     if (sub == 0 && g0 + head < a.G) {
       const int64_t row = static_cast<int64_t>(r.b) * a.H + r.hg / a.chunks * a.G + g0 + head;
+      if (a.prior_o != nullptr) {
+        const Fold f = fold_prior(a.prior_l2[row], mx, l);
+        float2 p = make_float2(0.f, 0.f), q = p;
+        if (f.other > 0.f) {
+          const float* src = a.prior_o + row * D;
+          p = *reinterpret_cast<const float2*>(src + element_of<D>(4 * x));
+          q = *reinterpret_cast<const float2*>(src + element_of<D>(4 * x + 2));
+        }
+        o = make_float4(fmaf(o.x, f.own, p.x * f.other), fmaf(o.y, f.own, p.y * f.other),
+                        fmaf(o.z, f.own, q.x * f.other), fmaf(o.w, f.own, q.y * f.other));
+      }
       const float inv = l > 0.f ? 1.f / l : 0.f;
       __nv_bfloat16* dst = a.o + row * D;
       *reinterpret_cast<__nv_bfloat162*>(dst + element_of<D>(4 * x)) =
@@ -983,6 +1035,89 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tk32, const 
 
 }  // namespace nvq
 
+namespace nvq {
+
+namespace {
+
+// The call behind the entry points: arguments as in attn_qat_decode; prior_o, prior_l2 as in
+// DecodeArgs.
+nvq_status run_decode(const void* q, int64_t ld_q, const void* pool, int64_t num_pages,
+                      const int32_t* page_table, int64_t ld_table, int max_pages,
+                      const int32_t* seq_lens, int B, int H, int Hkv, int D, float scale, int window,
+                      int sinks, void* o, float* lse, const float* prior_o, const float* prior_l2,
+                      void* ws, const Plan& p, cudaStream_t stream) {
+  int* err = device_error_word();
+  if (err == nullptr) return NVQ_ERR_CUDA;
+  CUtensorMap tk, tk32;
+  int r;
+  if ((r = make_kv_codes_map(&tk, pool, num_pages * Hkv, D, kPage)) != 0 ||
+      (r = make_kv_codes_map(&tk32, pool, num_pages * Hkv, D, 32)) != 0)
+    return fail_driver("cuTensorMapEncodeTiled", r);
+  uint8_t* wb = static_cast<uint8_t*>(ws);
+  const DecodeArgs a{static_cast<const uint16_t*>(q), ld_q, static_cast<const uint8_t*>(pool),
+                     num_pages, page_table, ld_table, max_pages, seq_lens, B, H, Hkv, H / Hkv,
+                     p.chunks, scale * kLog2e, window, sinks, static_cast<__nv_bfloat16*>(o), lse,
+                     prior_o, prior_l2, reinterpret_cast<RunInfo*>(wb), p.by_segment,
+                     reinterpret_cast<float*>(wb + p.parts), p.runs,
+                     ~uint64_t{0} / p.runs + 1, err};
+  const cudaError_t e = timed(NVQ_KERNEL_DECODE, stream, [&] {
+    if (D == 128)
+      return p.nt == 1 ? launch_decode<128, 1, 3>(tk, tk32, a, p, stream)
+                       : launch_decode<128, 2, 2>(tk, tk32, a, p, stream);
+    if (p.nt == 2) return launch_decode<64, 2, 2>(tk, tk32, a, p, stream);
+    return p.per_cta == 4 ? launch_decode<64, 1, 4>(tk, tk32, a, p, stream)
+                          : launch_decode<64, 1, 3>(tk, tk32, a, p, stream);
+  });
+  return e == cudaSuccess ? NVQ_OK : fail_cuda("attn decode", e);
+}
+
+// What attn_qat_decode and attn_qat_decode_prefix refuse alike, behind check_decode.
+nvq_status check_decode_call(const void* q, int64_t ld_q, const void* pool, int64_t num_pages,
+                             const int32_t* page_table, int64_t ld_table, int max_pages,
+                             const int32_t* seq_lens, int H, int Hkv, int D, float scale,
+                             const void* o, const float* lse) {
+  if (!(std::isfinite(scale) && scale > 0.f)) return NVQ_ERR_INVALID;
+  if (q == nullptr || o == nullptr || (reinterpret_cast<uintptr_t>(q) & 15u) != 0 ||
+      (reinterpret_cast<uintptr_t>(o) & 15u) != 0 || ld_q < static_cast<int64_t>(H) * D ||
+      ld_q % 8 != 0 || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return NVQ_ERR_INVALID;
+  const nvq_status st = check_kv(pool, num_pages, page_table, ld_table, max_pages, seq_lens);
+  if (st != NVQ_OK) return st;
+  return num_pages > 0x7FFFFFFF / Hkv ? NVQ_ERR_UNSUPPORTED : NVQ_OK;  // tensor-map coordinates
+}
+
+// Whether a run's tiles, counted in 31 bits, may be too many.
+bool too_many_tiles(int B, int Hkv, int max_pages, const Plan& p) {
+  return static_cast<int64_t>(B) * Hkv * p.chunks * max_pages / p.runs >= 0x7FFFFFFF;
+}
+
+// q is read by every run of its sequence, at whatever time: o elsewhere.
+bool over_queries(const void* q, int64_t ld_q, const void* o, int B, int H, int D) {
+  const int64_t row = static_cast<int64_t>(H) * D;
+  return ranges_meet(q, 2 * static_cast<uint64_t>((B - 1) * ld_q + row), o,
+                     2 * static_cast<uint64_t>(row * B));
+}
+
+// Workspace of the call behind a prefix: the decode's, the prefix's attention's, its o and
+// logarithms.
+struct PrefixWs {
+  size_t cross, o, l2, total;
+};
+
+PrefixWs prefix_ws(int B, int S, int H, int Hkv, int D, int prefix_pages, const Plan& p) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  PrefixWs w;
+  w.cross = up(p.total);
+  w.o = w.cross + up(cross_workspace(B, S, H, Hkv, D, prefix_pages));
+  w.l2 = w.o + up(static_cast<size_t>(B) * H * D * 4);
+  w.total = w.l2 + static_cast<size_t>(B) * H * 4;
+  return w;
+}
+
+}  // namespace
+
+}  // namespace nvq
+
 extern "C" {
 
 size_t attn_qat_decode_workspace(int B, int H, int Hkv, int D, int max_pages) {
@@ -998,48 +1133,61 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
   using namespace nvq;
   nvq_status st = check_decode(B, H, Hkv, D, max_pages);
   if (st != NVQ_OK) return st;
-  if (!(std::isfinite(scale) && scale > 0.f) || window < 0 || sinks < 0) return NVQ_ERR_INVALID;
-  if (q == nullptr || o == nullptr || (reinterpret_cast<uintptr_t>(q) & 15u) != 0 ||
-      (reinterpret_cast<uintptr_t>(o) & 15u) != 0 || ld_q < static_cast<int64_t>(H) * D ||
-      ld_q % 8 != 0 || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
-    return NVQ_ERR_INVALID;
-  st = check_kv(pool, num_pages, page_table, ld_table, max_pages, seq_lens);
+  if (window < 0 || sinks < 0) return NVQ_ERR_INVALID;
+  st = check_decode_call(q, ld_q, pool, num_pages, page_table, ld_table, max_pages, seq_lens, H,
+                         Hkv, D, scale, o, lse);
   if (st != NVQ_OK) return st;
   const Plan p = plan(B, H, Hkv, D, max_pages, window, sinks);
-  if (num_pages > 0x7FFFFFFF / Hkv) return NVQ_ERR_UNSUPPORTED;  // tensor-map coordinates
-  // a run counts its tiles in 31 bits
-  if (static_cast<int64_t>(B) * Hkv * p.chunks * max_pages / p.runs >= 0x7FFFFFFF)
-    return NVQ_ERR_UNSUPPORTED;
+  if (too_many_tiles(B, Hkv, max_pages, p)) return NVQ_ERR_UNSUPPORTED;
   if (ws == nullptr || ws_bytes < p.total || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return NVQ_ERR_WORKSPACE;
-  // q is read by every run of its sequence, at whatever time: o elsewhere
-  const int64_t row = static_cast<int64_t>(H) * D;
-  if (ranges_meet(q, 2 * static_cast<uint64_t>((B - 1) * ld_q + row), o,
-                  2 * static_cast<uint64_t>(row * B)))
+  if (over_queries(q, ld_q, o, B, H, D)) return NVQ_ERR_INVALID;
+  return run_decode(q, ld_q, pool, num_pages, page_table, ld_table, max_pages, seq_lens, B, H, Hkv,
+                    D, scale, window, sinks, o, lse, nullptr, nullptr, ws, p, stream);
+}
+
+size_t attn_qat_decode_prefix_workspace(int B, int S, int H, int Hkv, int D, int max_pages,
+                                        int prefix_pages) {
+  using namespace nvq;
+  if (check_decode(B, H, Hkv, D, max_pages) != NVQ_OK ||
+      check_cross(B, S, H, Hkv, D, prefix_pages) != NVQ_OK)
+    return 0;
+  return prefix_ws(B, S, H, Hkv, D, prefix_pages, plan(B, H, Hkv, D, max_pages, 0, 0)).total;
+}
+
+nvq_status attn_qat_decode_prefix(const void* q, int64_t ld_q, const void* pool, int64_t num_pages,
+                                  const int32_t* page_table, int64_t ld_table, int max_pages,
+                                  const int32_t* seq_lens, const int32_t* prefix_table,
+                                  int64_t ld_prefix, int prefix_pages, const int32_t* prefix_lens,
+                                  const int32_t* cu_seqs, int S, int B, int H, int Hkv, int D,
+                                  float scale, void* o, float* lse, void* ws, size_t ws_bytes,
+                                  nvq_stream_t stream) {
+  using namespace nvq;
+  nvq_status st = check_decode(B, H, Hkv, D, max_pages);
+  if (st == NVQ_OK) st = check_cross(B, S, H, Hkv, D, prefix_pages);
+  if (st != NVQ_OK) return st;
+  if ((cu_seqs == nullptr && B % S != 0) || (reinterpret_cast<uintptr_t>(cu_seqs) & 3u) != 0)
     return NVQ_ERR_INVALID;
-  int* err = device_error_word();
-  if (err == nullptr) return NVQ_ERR_CUDA;
-  CUtensorMap tk, tk32;
-  int r;
-  if ((r = make_kv_codes_map(&tk, pool, num_pages * Hkv, D, kPage)) != 0 ||
-      (r = make_kv_codes_map(&tk32, pool, num_pages * Hkv, D, 32)) != 0)
-    return fail_driver("cuTensorMapEncodeTiled", r);
+  st = check_decode_call(q, ld_q, pool, num_pages, page_table, ld_table, max_pages, seq_lens, H,
+                         Hkv, D, scale, o, lse);
+  if (st == NVQ_OK)
+    st = check_kv(pool, num_pages, prefix_table, ld_prefix, prefix_pages, prefix_lens);
+  if (st != NVQ_OK) return st;
+  const Plan p = plan(B, H, Hkv, D, max_pages, 0, 0);
+  if (too_many_tiles(B, Hkv, max_pages, p)) return NVQ_ERR_UNSUPPORTED;
+  const PrefixWs w = prefix_ws(B, S, H, Hkv, D, prefix_pages, p);
+  if (ws == nullptr || ws_bytes < w.total || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return NVQ_ERR_WORKSPACE;
+  if (over_queries(q, ld_q, o, B, H, D)) return NVQ_ERR_INVALID;
   uint8_t* wb = static_cast<uint8_t*>(ws);
-  const DecodeArgs a{static_cast<const uint16_t*>(q), ld_q, static_cast<const uint8_t*>(pool),
-                     num_pages, page_table, ld_table, max_pages, seq_lens, B, H, Hkv, H / Hkv,
-                     p.chunks, scale * kLog2e, window, sinks, static_cast<__nv_bfloat16*>(o), lse,
-                     reinterpret_cast<RunInfo*>(wb), p.by_segment,
-                     reinterpret_cast<float*>(wb + p.parts), p.runs,
-                     ~uint64_t{0} / p.runs + 1, err};
-  const cudaError_t e = timed(NVQ_KERNEL_DECODE, stream, [&] {
-    if (D == 128)
-      return p.nt == 1 ? launch_decode<128, 1, 3>(tk, tk32, a, p, stream)
-                       : launch_decode<128, 2, 2>(tk, tk32, a, p, stream);
-    if (p.nt == 2) return launch_decode<64, 2, 2>(tk, tk32, a, p, stream);
-    return p.per_cta == 4 ? launch_decode<64, 1, 4>(tk, tk32, a, p, stream)
-                          : launch_decode<64, 1, 3>(tk, tk32, a, p, stream);
-  });
-  return e == cudaSuccess ? NVQ_OK : fail_cuda("attn decode", e);
+  float* prior_o = reinterpret_cast<float*>(wb + w.o);
+  float* prior_l2 = reinterpret_cast<float*>(wb + w.l2);
+  st = launch_cross({q, ld_q, B, pool, num_pages, prefix_table, ld_prefix, prefix_pages,
+                     prefix_lens, cu_seqs, S, H, Hkv, D, scale, nullptr, prior_o, prior_l2},
+                    wb + w.cross, stream);
+  if (st != NVQ_OK) return st;
+  return run_decode(q, ld_q, pool, num_pages, page_table, ld_table, max_pages, seq_lens, B, H, Hkv,
+                    D, scale, 0, 0, o, lse, prior_o, prior_l2, ws, p, stream);
 }
 
 }  // extern "C"

@@ -272,6 +272,29 @@ cudaError_t launch_linear_small(const void* x, int64_t ld_x, const float* gx,
                                 const float* gw, const void* bias, int64_t M, int64_t N, int64_t K,
                                 void* out, uint8_t* ws, int* err, cudaStream_t stream);
 
+// Many rows over the paged cache (attn_cross.cu): the call, its checks of sizes, the workspace.
+// Exactly one of o (bf16, lse natural) and o32 (fp32, lse to base 2, rows without keys in lse
+// alone) is not null.
+struct CrossCall {
+  const void* q;
+  int64_t ld_q, T;
+  const void* pool;
+  int64_t num_pages;
+  const int32_t* page_table;
+  int64_t ld_table;
+  int max_pages;
+  const int32_t* kv_lens;
+  const int32_t* cu_tokens;  // or nullptr: T / B tokens a sequence
+  int B, H, Hkv, D;
+  float scale;
+  void* o;
+  float* o32;
+  float* lse;
+};
+nvq_status check_cross(int64_t T, int B, int H, int Hkv, int D, int max_pages);
+size_t cross_workspace(int64_t T, int B, int H, int Hkv, int D, int max_pages);
+nvq_status launch_cross(const CrossCall& c, uint8_t* ws, cudaStream_t stream);
+
 // Maps a [rows, cols] 16-bit row-major matrix with a box of {64, box_rows}.
 int make_2d_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows);
 // Maps a [rows, row_bytes] byte matrix (row stride ld bytes) with a box of

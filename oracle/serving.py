@@ -127,3 +127,31 @@ def release(done, lens, table, free, count):
                 count += 1
             after[b] = 0
     return after, count, free
+
+
+def attend(q, pool, spans, scale, keep=None):
+    """Rows q [R, H, D] over the keys of ``spans``, a list of (row of a page table, length), one
+    after another: (o, lse, mag, err_s) as ``decode``.  keep(span, j): False leaves a key out."""
+    r, h, d = q.shape
+    hkv = pool.shape[1]
+    kc, vc, ks, vs = record_parts(pool, d)
+    qq = fq(q).view(r, hkv, h // hkv, d)
+    o, mag = torch.zeros(r, h, d, dtype=F64), torch.zeros(r, h, d, dtype=F64)
+    lse, err_s = torch.full((r, h), -float("inf"), dtype=F64), torch.zeros(r, h, dtype=F64)
+    page, row = [], []
+    for i, (table, n) in enumerate(spans):
+        j = torch.tensor([j for j in range(n) if keep is None or keep(i, j)], dtype=torch.long)
+        page.append(table.cpu()[j // PAGE].long())
+        row.append(j % PAGE)
+    page, row = torch.cat(page), torch.cat(row)
+    if len(page) == 0 or r == 0:
+        return o, lse, mag, err_s
+    for hk in range(hkv):
+        k = unpack(kc[page, hk, row], ks[page, hk, row])
+        v = unpack(vc[page, hk, row], vs[page, hk, row])
+        s = scale * (qq[:, hk] @ k.T)
+        p = torch.softmax(s, -1)
+        at = slice(hk * (h // hkv), (hk + 1) * (h // hkv))
+        o[:, at], mag[:, at], lse[:, at] = p @ v, p @ v.abs(), torch.logsumexp(s, -1)
+        err_s[:, at] = scale * (qq[:, hk].abs() @ k.abs().T).amax(-1)
+    return o, lse, mag, err_s

@@ -12,15 +12,15 @@
 // crosses runs leaves (m, l, sum p V~) per run in the workspace, joined in run order by a
 // second kernel: results do not vary from run to run.
 //
-// One CTA, sixteen warps:
+// One CTA, nineteen warps:
 //   producer   K codes by tensor-map loads with the swizzle the MMA reads, the record's rest
 //              by bulk copies, into a ring of stages, with a description of each tile
 //   S          scales of K into the scale operand's order; S = Q~ K~^T as block-scaled FP4
 //              tcgen05 MMAs on the codes, into one of two buffers of 128 columns
 //   PV         O += P V~ as f16 MMAs, P from tensor memory (over the S it came from)
 //   4 decode   V's codes times scales, exactly, to f16 rows in shared memory (scales run
-//              along D, so codes cannot be the FP4 operand of a product over keys); q~ of a
-//              segment that begins
+//              along D, so codes cannot be the FP4 operand of a product over keys)
+//   4 query    q~ of the segments, up to two ahead; rows without keys
 //   2 x 4      softmax, one thread a row: warpgroup w takes every other tile.  Both accumulate
 //              into one O, so p refers to a maximum that goes from tile to tile through shared
 //              memory, published before the exponentials; it is raised only where a score
@@ -43,8 +43,8 @@ namespace nvq {
 namespace {
 
 constexpr int kRows = 128;     // query rows of a tile
-constexpr int kThreads = 512;
-constexpr int kDecodeWarp = 8, kProducerWarp = 12, kSWarp = 13, kPvWarp = 14, kSpareWarp = 15;
+constexpr int kThreads = 608;
+constexpr int kDecodeWarp = 8, kQWarp = 12, kProducerWarp = 16, kSWarp = 17, kPvWarp = 18;
 constexpr int kDescs = 16;     // descriptions outlive their stages by the tiles in softmax
 constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -73,7 +73,8 @@ struct Cfg {
   static constexpr uint32_t kVAt = kStages * kRec;       // [2]
   static constexpr uint32_t kQAt = kVAt + 2 * kV;        // [2]
   static constexpr uint32_t kQScAt = kQAt + 2 * kQ;      // [2]
-  static constexpr uint32_t kMAt = kQScAt + 2 * kQSc;    // float [2][128]: maximum by tile parity
+  static constexpr uint32_t kRawAt = kQScAt + 2 * kQSc;  // bf16 rows of the next segment
+  static constexpr uint32_t kMAt = kRawAt + kRows * D * 2;  // float [2][128]: maximum by tile parity
   static constexpr uint32_t kLAt = kMAt + 2 * kRows * 4;  // float2 [2][128]: (m, l) by segment parity
   static constexpr uint32_t kDescAt = kLAt + 2 * kRows * 8;
   static constexpr uint32_t kBarAt = kDescAt + kDescs * 32;
@@ -143,6 +144,84 @@ __device__ __forceinline__ Extent extent(const CrossArgs& a, int s, bool* bad) {
   return e;
 }
 
+// The segments of a run, one after another: sequence s (its first tile at seg0 of the line),
+// KV head hk, row tile rt, of it the tiles i .. i_end - 1.
+struct Walk {
+  Extent e;
+  int64_t seg0, first;
+  int s, hk, rt, i, i_end, left;  // left: tiles of the run from this segment on
+  __device__ __forceinline__ Walk(const CrossArgs& a, int s_, int64_t seg0_, int64_t u0, int n)
+      : seg0(seg0_), s(s_), left(n) {
+    bool bad;
+    e = extent(a, s, &bad);
+    const int64_t nth = (u0 - seg0) / e.key_tiles;  // segment of the sequence
+    hk = static_cast<int>(nth / e.row_tiles);
+    rt = static_cast<int>(nth - static_cast<int64_t>(hk) * e.row_tiles);
+    i = static_cast<int>(u0 - seg0 - nth * e.key_tiles);
+    cut();
+  }
+  __device__ __forceinline__ void cut() {
+    first = seg0 + (static_cast<int64_t>(hk) * e.row_tiles + rt) * e.key_tiles;
+    i_end = min(e.key_tiles, i + left);
+  }
+  __device__ __forceinline__ bool next(const CrossArgs& a) {
+    left -= i_end - i;
+    if (left == 0) return false;
+    i = 0;
+    if (++rt == e.row_tiles) {
+      rt = 0;
+      if (++hk == a.Hkv) {
+        hk = 0;
+        seg0 += static_cast<int64_t>(e.row_tiles) * e.key_tiles * a.Hkv;
+        bool bad;
+#pragma unroll 1
+        do {
+          e = extent(a, ++s, &bad);
+        } while (e.key_tiles == 0);
+      }
+    }
+    cut();
+    return true;
+  }
+  __device__ __forceinline__ int row0() const { return rt * kRows; }
+  __device__ __forceinline__ int rows(const CrossArgs& a) const {
+    return min(kRows, e.toks * a.G - row0());
+  }
+};
+
+// The value of lane 0, which the compiler then keeps where tcgen05 instructions take it from.
+template <class T>
+__device__ __forceinline__ T uniform(T v) {
+  return __shfl_sync(0xFFFFFFFFu, v, 0);
+}
+
+// mbar_wait_warp in few instructions.  Nineteen warps of six roles run their own code at once, and
+// what does not fit the instruction caches costs more than all arithmetic (with the waits of
+// nvq_ptx.cuh inline, loops unrolled and masks in the softmax's chunks the kernel was 113 KB, three
+// warps of eleven waited for instructions and a tile took 3350 cycles).  A wait gives up after
+// 2^21 tries of up to a microsecond, or when another thread has.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t abort) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 n, v;\n\t"
+      "mov.u32 n, 0;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+      "@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\t"
+      "setp.gt.u32 q, n, 0x200000;\n\t"
+      "@q st.volatile.shared.u32 [%3], 1;\n\t"
+      "ld.volatile.shared.u32 v, [%3];\n\t"
+      "setp.eq.u32 q, v, 0;\n\t"
+      "@q bra AGAIN;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(abort)
+      : "memory");
+  return __all_sync(0xFFFFFFFFu, ok != 0);
+}
+
 // Place in a ring of `stages`: stage and the parity of its use.
 struct Ring {
   int s = 0;
@@ -155,31 +234,52 @@ struct Ring {
   }
 };
 
-// q~ of a segment by the 128 decode threads: codes in the swizzled rows of the A operand, scales
-// in the 512-byte blocks of the scale operand.  Rows beyond the segment's: zeros.
+// q~ of a segment by 128 threads, thread t taking block t % (D/16) of every kStep-th row: its
+// bf16 rows by asynchronous copies (each thread reads back what it has copied itself), codes into
+// the swizzled rows of the A operand, scales into the 512-byte blocks of the scale operand.
+// Rows beyond the segment's: zeros.
 template <int D>
-__device__ __forceinline__ void quantize_q(const CrossArgs& a, const Tile& td, uint8_t* codes,
-                                           uint8_t* scales, int t) {
-  constexpr int kBlocks = D / 16, kStep = 128 / kBlocks, kBatch = 4;
-  const int j = t % kBlocks;
-  for (int i = 0; i < kRows / kStep; i += kBatch) {
-    uint4 lo[kBatch], hi[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int n = (i + u) * kStep + t / kBlocks;
-      lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
-      if (n < td.rows) {
-        const int row = td.row0 + n, tok = row / a.G;
-        const uint16_t* src = a.q + (td.tok0 + tok) * a.ld_q +
-                              static_cast<int64_t>(td.hk * a.G + row - tok * a.G) * D + j * 16;
-        lo[u] = ld16(src);
-        hi[u] = ld16(src + 8);
+struct QueryTile {
+  static constexpr int kBlocks = D / 16, kStep = 128 / kBlocks;
+
+  static __device__ __forceinline__ void fetch(const CrossArgs& a, const Walk& w, uint8_t* raw,
+                                               int t) {
+    const int j = t % kBlocks, rows = w.rows(a);
+    const int row = w.row0() + t / kBlocks;
+    int tok = row / a.G, g = row - tok * a.G;
+    const int step_t = kStep / a.G, step_g = kStep - step_t * a.G;
+    tok += w.e.tok0;
+#pragma unroll 1
+    for (int n = t / kBlocks; n < kRows; n += kStep) {
+      const uint16_t* src = a.q;
+      uint32_t bytes = 0;  // 0: filled with zeros, nothing is read
+      if (n < rows) {
+        src += tok * a.ld_q + static_cast<int64_t>(w.hk * a.G + g) * D + j * 16;
+        bytes = 16;
+      }
+      const uint32_t dst = smem_u32(raw) + n * (D * 2) + ((j ^ (n & (kBlocks - 1))) << 5);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                   : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16), "l"(src + 8),
+                   "r"(bytes)
+                   : "memory");
+      tok += step_t;
+      if ((g += step_g) >= a.G) {
+        g -= a.G;
+        ++tok;
       }
     }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int n = (i + u) * kStep + t / kBlocks;
-      const uint32_t v[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w, hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+  }
+  static __device__ __forceinline__ void quantize(const uint8_t* raw, uint8_t* codes,
+                                                  uint8_t* scales, int t) {
+    const int j = t % kBlocks;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+    for (int n = t / kBlocks; n < kRows; n += kStep) {
+      const uint4* src =
+          reinterpret_cast<const uint4*>(raw + n * (D * 2) + ((j ^ (n & (kBlocks - 1))) << 5));
+      const uint4 lo = src[0], hi = src[1];
+      const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
       const Codes16 r = codes16_unit(v);
       const int swz = D == 128 ? (n >> 1) & 3 : (n >> 2) & 1;  // 64- and 32-byte swizzles
       *reinterpret_cast<uint2*>(codes + n * (D / 2) + (((j >> 1) ^ swz) << 4) + (j & 1) * 8) =
@@ -188,7 +288,7 @@ __device__ __forceinline__ void quantize_q(const CrossArgs& a, const Tile& td, u
           static_cast<uint8_t>(r.sbyte);
     }
   }
-}
+};
 
 // K's scales [128][D/16] to D/64 blocks of 512 bytes, in place: row r of a block holds the words
 // (4 scales) of keys r, r + 32, r + 64, r + 96.
@@ -222,7 +322,7 @@ __device__ __forceinline__ void decode_v(const uint8_t* rec, uint8_t* dst, int v
                                          int lane) {
   constexpr int kPieces = D / 32, kKeys = 32 / kPieces;
   const int piece = lane % kPieces, flip = piece >> 1;
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kPieces; ++i) {
     const int key = 32 * warp + i * kKeys + lane / kPieces;
     const uint4 c = *reinterpret_cast<const uint4*>(rec + v_codes_at(D) + key * (D / 2) + piece * 16);
@@ -245,17 +345,6 @@ __device__ __forceinline__ void decode_v(const uint8_t* rec, uint8_t* dst, int v
   }
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  uint32_t a[16], b[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    a[i] = r[i];
-    b[i] = r[16 + i];
-  }
-  tmem_st16(taddr, a);
-  tmem_st16(taddr + 16, b);
-}
-
 // What is written as a row's lse: the natural logarithm, or base 2 beside an output in fp32.
 __device__ __forceinline__ float row_lse(const CrossArgs& a, float m, float l) {
   if (!(l > 0.f)) return -INFINITY;
@@ -263,14 +352,35 @@ __device__ __forceinline__ float row_lse(const CrossArgs& a, float m, float l) {
   return a.o != nullptr ? v * kLn2 : v;
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(const uint32_t* v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[0]), __uint_as_float(v[1]));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// p = 2^(s scale - m) of 32 scores, their sums added to l, p as f16 pairs.
+__device__ __forceinline__ void exponentials(const uint32_t (&s)[32], uint64_t scale2,
+                                             uint64_t neg_m, uint64_t& l2, uint32_t (&p)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float p0, p1;
+    up2(fma2(pk2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale2, neg_m), p0, p1);
+    p0 = ex2_f32(p0);
+    p1 = ex2_f32(p1);
+    l2 = add2(l2, pk2(p0, p1));
+    p[i] = pack_f16x2_rn(p0, p1);
+  }
+}
+
 // A token without visible keys: o = 0 (in fp32 left as it is), lse = -inf.
 template <int D>
 __device__ __forceinline__ void empty_token(const CrossArgs& a, int tok, int lane) {
   const int64_t row0 = static_cast<int64_t>(tok) * a.H;
   if (a.o != nullptr)
+#pragma unroll 1
     for (int x = lane; x < a.H * (D / 8); x += 32)
       reinterpret_cast<uint4*>(a.o + row0 * D)[x] = make_uint4(0, 0, 0, 0);
   if (a.lse != nullptr)
+#pragma unroll 1
     for (int x = lane; x < a.H; x += 32) a.lse[row0 + x] = -INFINITY;
 }
 
@@ -284,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int start_s;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) &
                                              ~static_cast<uintptr_t>(1023u));
   float* m_of = reinterpret_cast<float*>(smem + C::kMAt);     // [2][128]
@@ -304,11 +414,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* l_ready = m_ready + 8;            // [2][4]: the other warpgroup's (m, l), by segment
   uint64_t* o_read = l_ready + 8;             // four softmax warps
   uint64_t* drain = o_read + 1;
-  volatile int* abort = &abort_word;
+  const uint32_t abort = smem_u32(&abort_word);
   pdl_trigger();
 
   if (threadIdx.x == 0) {
-    *abort = 0;
+    abort_word = 0;
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 5);
@@ -332,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&drain[1], 1);
     fence_mbar_init();
   }
-  if (warp == kSpareWarp) {
+  if (warp == kSWarp) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
     tma_prefetch_desc(&tk);
@@ -342,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = (a.B + kThreads - 1) / kThreads;
   const int s_lo = min(a.B, static_cast<int>(threadIdx.x) * per), s_hi = min(a.B, s_lo + per);
   int64_t mine = 0;
+#pragma unroll 1
   for (int s = s_lo; s < s_hi; ++s) {
     bool bad;
     const Extent e = extent(a, s, &bad);
@@ -370,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (mine > 0 && before <= u0 && u0 < before + mine) {
     int64_t at = before;
     int s = s_lo;
+#pragma unroll 1
     for (;; ++s) {
       bool bad;
       const Extent e = extent(a, s, &bad);
@@ -383,52 +495,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
-  const int n_tiles = static_cast<int>(u1 - u0);
+  const uint32_t tmem = uniform(tmem_slot);
+  const int n_tiles = uniform(static_cast<int>(u1 - u0));
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     if (lane == 0) a.split[run].last = -1;
     if (n_tiles > 0) {
-      int s = start_s;
-      bool bad, ok = true;
-      Extent e = extent(a, s, &bad);
-      int64_t seg0 = start_before;  // line position of the sequence's first tile
-      const int64_t nth = (u0 - seg0) / e.key_tiles;  // segment of the sequence
-      int hk = static_cast<int>(nth / e.row_tiles);
-      int rt = static_cast<int>(nth - static_cast<int64_t>(hk) * e.row_tiles);
-      int i = static_cast<int>(u0 - seg0 - nth * e.key_tiles);
+      bool ok = true;
       int n = 0;
       Tile td;
       td.seg = 0;
       Ring ring;
-      while (n < n_tiles && ok) {
-        // ---- one segment (the part of it that lies in the run: tiles i .. i_end - 1)
-        const int64_t first = seg0 + (static_cast<int64_t>(hk) * e.row_tiles + rt) * e.key_tiles;
-        const int i0 = i, i_end = min(e.key_tiles, i + n_tiles - n);
-        const bool whole = first >= u0 && first + e.key_tiles <= u1;
-        td.row0 = rt * kRows;
-        td.rows = min(kRows, e.toks * a.G - td.row0);
-        td.tok0 = e.tok0;
-        td.hk = hk;
+      Walk w(a, start_s, start_before, u0, n_tiles);
+      do {
+        const bool whole = w.first >= u0 && w.first + w.e.key_tiles <= u1;
+        td.row0 = w.row0();
+        td.rows = w.rows(a);
+        td.tok0 = w.e.tok0;
+        td.hk = w.hk;
         // a part that begins with the run goes to the run's slot 0, one inside it to slot 1
-        td.slot = whole ? -1 : 2 * run + (first > u0 ? 1 : 0);
-        const int32_t* table = a.table + s * a.ld_table;
+        td.slot = whole ? -1 : 2 * run + (w.first > u0 ? 1 : 0);
+        const int32_t* table = a.table + w.s * a.ld_table;
         int pages = 0;  // this lane's page number: of tile i0 + 32 k + lane
-        for (; i < i_end; ++i, ++n, ring.next(C::kStages)) {
-          if (((i - i0) & 31) == 0) {
+#pragma unroll 1
+        for (int i = w.i; i < w.i_end; ++i, ++n, ring.next(C::kStages)) {
+          if (((i - w.i) & 31) == 0) {
             const int x = i + lane;
-            pages = x < e.key_tiles ? table[x] : -1;
+            pages = x < w.e.key_tiles ? table[x] : -1;
           }
-          const int page = __shfl_sync(0xFFFFFFFFu, pages, (i - i0) & 31);
+          const int page = __shfl_sync(0xFFFFFFFFu, pages, (i - w.i) & 31);
           const bool there = page >= 0 && page < a.num_pages;
-          td.flags = (i == i0 ? kStart : 0) | (i == i0 + 1 ? kSecond : 0) |
-                     (i == i_end - 2 ? kNextEnd : 0) | (i == i_end - 1 ? kEnd : 0) |
+          td.flags = (i == w.i ? kStart : 0) | (i == w.i + 1 ? kSecond : 0) |
+                     (i == w.i_end - 2 ? kNextEnd : 0) | (i == w.i_end - 1 ? kEnd : 0) |
                      (there ? 0 : kAbsent);
-          td.valid = there ? min(kPage, e.len - i * kPage) : 0;
+          td.valid = there ? min(kPage, w.e.len - i * kPage) : 0;
           if (!there && lane == 0) atomicMax(a.err, kErrTable);
           const int st = ring.s;
-          if (!(ok = mbar_wait_warp(&empty[st], ring.phase ^ 1, abort))) break;
+          if (!(ok = wait(&empty[st], ring.phase ^ 1, abort))) break;
           if (lane == 0) {
             desc[n % kDescs] = td;
             mbar_arrive(&described[n % kDescs]);
@@ -436,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           uint8_t* dst = smem + st * C::kRec;
           if (there) {
-            const int rec = page * a.Hkv + hk;
+            const int rec = page * a.Hkv + w.hk;
             mbar_arrive_expect_tx_w(&full[st], C::kRec);
             tma_load_4d_w(dst, &tk, 0, 0, rec, 0, &full[st]);
             bulk_load_w(dst + v_codes_at(D),
@@ -446,27 +550,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx_w(&full[st], 0);
           }
         }
-        if (lane == 0 && first >= u0 && first + e.key_tiles > u1) {
+        if (lane == 0 && w.first >= u0 && w.first + w.e.key_tiles > u1) {
           // the run that holds tile u: the last c with all c / n_runs <= u
-          const int64_t u = first + e.key_tiles - 1;
+          const int64_t u = w.first + w.e.key_tiles - 1;
           a.split[run] = {run, static_cast<int>(((u + 1) * n_runs + all - 1) / all - 1), td.slot,
                           td.rows, td.row0, td.tok0, td.hk, 0};
         }
-        if (n == n_tiles || !ok) break;
         ++td.seg;
-        i = 0;
-        if (++rt == e.row_tiles) {
-          rt = 0;
-          if (++hk == a.Hkv) {
-            hk = 0;
-            seg0 += static_cast<int64_t>(e.row_tiles) * e.key_tiles * a.Hkv;
-            do {
-              e = extent(a, ++s, &bad);
-            } while (e.key_tiles == 0);
-          }
-        }
-      }
+      } while (ok && w.next(a));
       if (!ok) {  // let the copies already issued land before the block leaves
+#pragma unroll 1
         for (int m = max(0, n - C::kStages); m < n; ++m)
           mbar_wait_warp(&full[m % C::kStages], (m / C::kStages) & 1, nullptr, 10000000ull);
       }
@@ -477,14 +570,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t lay = D == 128 ? 4u : 6u, sbo = 4 * D;  // swizzle, bytes of 8 rows
     bool ok = true;
     Ring ring;
+#pragma unroll 1
     for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
       const int st = ring.s;
-      if (!(ok = mbar_wait_warp(&described[n % kDescs], (n / kDescs) & 1, abort))) break;
-      const struct { int flags, seg; } td {desc[n % kDescs].flags, desc[n % kDescs].seg};
-      if (!(ok = mbar_wait_warp(&full[st], ring.phase, abort))) break;
+      if (!(ok = wait(&described[n % kDescs], (n / kDescs) & 1, abort))) break;
+      const struct { int flags, seg; } td{uniform(desc[n % kDescs].flags),
+                                          uniform(desc[n % kDescs].seg)};
+      if (!(ok = wait(&full[st], ring.phase, abort))) break;
       const int qb = td.seg & 1;
       if ((td.flags & kStart) &&
-          !(ok = mbar_wait_warp(&q_full[qb], (td.seg >> 1) & 1, abort)))
+          !(ok = wait(&q_full[qb], (td.seg >> 1) & 1, abort)))
         break;
       tc_fence_after();
       const uint32_t sfq = tmem + kSfQ + 8 * qb, sfk = tmem + kSfK + 8 * (n & 3);
@@ -507,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // S's buffer is free when the PV of tile n - 2 has read the P that lies over it
       if (n >= 2) {
-        if (!(ok = mbar_wait_warp(&pv_done[n & 1], ((n - 2) >> 1) & 1, abort))) break;
+        if (!(ok = wait(&pv_done[n & 1], ((n - 2) >> 1) & 1, abort))) break;
         tc_fence_after();
       }
       if (!(td.flags & kAbsent)) {
@@ -528,17 +623,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ O += P V~
     constexpr uint32_t idesc = idesc_f16(kRows, D, 0, 0, 1);
     const uint64_t v_d0 = sdesc_sw128(smem_u32(smem + C::kVAt), kRows * 128, 1024);
+#pragma unroll 1
     for (int n = 0; n < n_tiles; ++n) {
       const int b = n & 1;
       const uint32_t phase = (n >> 1) & 1;
-      if (!mbar_wait_warp(&described[n % kDescs], (n / kDescs) & 1, abort)) break;
-      const struct { int flags, seg; } td {desc[n % kDescs].flags, desc[n % kDescs].seg};
+      if (!wait(&described[n % kDescs], (n / kDescs) & 1, abort)) break;
+      const struct { int flags, seg; } td{uniform(desc[n % kDescs].flags),
+                                          uniform(desc[n % kDescs].seg)};
       // O of the segment before has been read
       if ((td.flags & kStart) && td.seg > 0 &&
-          !mbar_wait_warp(o_read, (td.seg - 1) & 1, abort))
+          !wait(o_read, (td.seg - 1) & 1, abort))
         break;
-      if (!mbar_wait_warp(&v_full[b], phase, abort)) break;
-      if (!mbar_wait_warp(&p_full[b], phase, abort)) break;
+      if (!wait(&v_full[b], phase, abort)) break;
+      if (!wait(&p_full[b], phase, abort)) break;
       tc_fence_after();
       uint32_t p[8];
 #pragma unroll
@@ -548,28 +645,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     umma_commit_w(&drain[1]);
     mbar_wait_warp(&drain[1], 0, nullptr, 10000000ull);
-  } else if (warp >= kDecodeWarp && warp < kDecodeWarp + 4) {
-    // ------------------------------------------------------------ V~, q~
-    const int t = threadIdx.x - 32 * kDecodeWarp;
+  } else if (warp >= kDecodeWarp && warp < kQWarp) {
+    // ------------------------------------------------------------ V~
     Ring ring;
+#pragma unroll 1
     for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
       const int st = ring.s, b = n & 1;
-      if (!mbar_wait_warp(&described[n % kDescs], (n / kDescs) & 1, abort)) break;
-      const Tile td = desc[n % kDescs];
-      if (td.flags & kStart) {
-        const int qb = td.seg & 1;
-        if (!mbar_wait_warp(&q_empty[qb], ((td.seg >> 1) & 1) ^ 1, abort)) break;
-        quantize_q<D>(a, td, smem + C::kQAt + qb * C::kQ, smem + C::kQScAt + qb * C::kQSc, t);
-        fence_proxy_async_smem();
-        mbar_arrive_warp(&q_full[qb]);
-      }
-      if (!mbar_wait_warp(&full[st], ring.phase, abort)) break;
-      if (!mbar_wait_warp(&v_empty[b], ((n >> 1) & 1) ^ 1, abort)) break;
-      decode_v<D>(smem + st * C::kRec, smem + C::kVAt + b * C::kV, td.valid, warp - kDecodeWarp,
-                  lane);
+      if (!wait(&described[n % kDescs], (n / kDescs) & 1, abort)) break;
+      const int valid = desc[n % kDescs].valid;
+      if (!wait(&full[st], ring.phase, abort)) break;
+      if (!wait(&v_empty[b], ((n >> 1) & 1) ^ 1, abort)) break;
+      decode_v<D>(smem + st * C::kRec, smem + C::kVAt + b * C::kV, valid, warp - kDecodeWarp, lane);
       fence_proxy_async_smem();
       mbar_arrive_warp(&v_full[b]);
       mbar_arrive_warp(&empty[st]);
+    }
+  } else if (warp >= kQWarp && warp < kProducerWarp) {
+    // ------------------------------------------------------------ q~
+    if (n_tiles > 0) {
+      const int t = threadIdx.x - 32 * kQWarp;
+      Walk w(a, start_s, start_before, u0, n_tiles);
+      int seg = 0;
+      do {
+        QueryTile<D>::fetch(a, w, smem + C::kRawAt, t);
+        const int qb = seg & 1;
+        if (!wait(&q_empty[qb], ((seg >> 1) & 1) ^ 1, abort)) break;
+        QueryTile<D>::quantize(smem + C::kRawAt, smem + C::kQAt + qb * C::kQ,
+                               smem + C::kQScAt + qb * C::kQSc, t);
+        fence_proxy_async_smem();
+        mbar_arrive_warp(&q_full[qb]);
+        ++seg;
+      } while (w.next(a));
+    }
+    // ---- rows without keys, rows outside of all sequences
+    const int first = 4 * run + warp - kQWarp, step = 4 * static_cast<int>(gridDim.x);
+#pragma unroll 1
+    for (int s0 = 0; s0 < a.B; s0 += 32) {
+      bool bad;
+      Extent e{0, 0, 0, 0, 1};
+      if (s0 + lane < a.B) e = extent(a, s0 + lane, &bad);
+      uint32_t none = __ballot_sync(0xFFFFFFFFu, e.toks > 0 && e.key_tiles == 0);
+      for (; none != 0; none &= none - 1) {
+        const int i = __ffs(none) - 1;
+        const int tok0 = __shfl_sync(0xFFFFFFFFu, e.tok0, i), toks = __shfl_sync(0xFFFFFFFFu, e.toks, i);
+#pragma unroll 1
+        for (int t = first; t < toks; t += step) empty_token<D>(a, tok0 + t, lane);
+      }
+    }
+    if (a.cu != nullptr) {
+      const int lo = min(max(a.cu[0], 0), a.T), hi = min(max(a.cu[a.B], 0), a.T);
+#pragma unroll 1
+      for (int t = first; t < lo; t += step) empty_token<D>(a, t, lane);
+#pragma unroll 1
+      for (int64_t t = static_cast<int64_t>(hi) + first; t < a.T; t += step)
+        empty_token<D>(a, static_cast<int>(t), lane);
     }
   } else if (warp < kDecodeWarp) {
     // ------------------------------------------------------------ softmax
@@ -579,33 +708,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t scale2 = pk2(a.scale_log2, a.scale_log2);
     float m = -INFINITY;  // reference maximum (log2 units) of this warpgroup's last tile
     uint64_t l2 = pk2(0.f, 0.f);
+#pragma unroll 1
     for (int n = wg; n < n_tiles; n += 2) {
       const int b = n & 1;
-      if (!mbar_wait_warp(&described[n % kDescs], (n / kDescs) & 1, abort)) break;
+      if (!wait(&described[n % kDescs], (n / kDescs) & 1, abort)) break;
       const Tile td = desc[n % kDescs];
       const bool live = quarter * 32 < td.rows;  // else: rows that nobody reads
-      if (!mbar_wait_warp(&s_full[b], (n >> 1) & 1, abort)) break;
+      if (!wait(&s_full[b], (n >> 1) & 1, abort)) break;
       tc_fence_after();
       const uint32_t s_at = lanes + 128 * b;
       if (td.flags & (kStart | kSecond)) {
         m = -INFINITY;
         l2 = pk2(0.f, 0.f);
       }
+      if (live && td.valid < kPage) {  // keys behind the last: -inf, before S is read
+#pragma unroll 1
+        for (int c = td.valid & ~15; c < kPage; c += 16) {
+          uint32_t x[16];
+          tmem_ld16(s_at + c, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c + i >= td.valid) x[i] = 0xFF800000u;
+          tmem_st16(s_at + c, x);
+        }
+        tmem_wait_st();
+      }
       float mx = -INFINITY;
       if (live) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; c += 2) {
           uint32_t x[32], y[32];
           tmem_ld32(s_at + 32 * c, x);
           tmem_ld32(s_at + 32 * c + 32, y);
           tmem_wait_ld();
-          if (td.valid < kPage) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (32 * c + i >= td.valid) x[i] = 0xFF800000u;
-              if (32 * c + 32 + i >= td.valid) y[i] = 0xFF800000u;
-            }
-          }
           float v[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
@@ -620,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- the maximum so far, from the tile before; also where a segment begins, for the order
       if (n > 0 &&
-          !mbar_wait_warp(&m_ready[4 * (b ^ 1) + quarter], ((n - 1) >> 1) & 1, abort))
+          !wait(&m_ready[4 * (b ^ 1) + quarter], ((n - 1) >> 1) & 1, abort))
         break;
       float old = td.flags & kStart ? -INFINITY : m_of[kRows * (b ^ 1) + r];
       const bool grows = mx > old + kSlack || (old == -INFINITY && mx > -INFINITY);
@@ -629,17 +765,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive_warp(&m_ready[4 * b + quarter]);
       if (!(td.flags & kStart) && __any_sync(0xFFFFFFFFu, grows)) {
         // raised behind the segment's first tile: O so far, which the PV before has finished
-        if (!mbar_wait_warp(&pv_done[b ^ 1], ((n - 1) >> 1) & 1, abort)) break;
+        if (!wait(&pv_done[b ^ 1], ((n - 1) >> 1) & 1, abort)) break;
         tc_fence_after();
         const float c = grows ? ex2_f32(old - now) : 1.f;
-#pragma unroll
-        for (int x = 0; x < D; x += 32) {
-          uint32_t v[32];
-          tmem_ld32(lanes + kO + x, v);
+#pragma unroll 1
+        for (int x = 0; x < D; x += 16) {
+          uint32_t v[16];
+          tmem_ld16(lanes + kO + x, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * c);
-          tmem_st32(lanes + kO + x, v);
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * c);
+          tmem_st16(lanes + kO + x, v);
         }
         tmem_wait_st();
       }
@@ -652,27 +788,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (live) {
         const float ref = -fmaxf(now, -3.4e38f);
         const uint64_t neg_m = pk2(ref, ref);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x[32], p[16];
-          tmem_ld32(s_at + 32 * c, x);
+        // columns c .. c + 31 are read a step ahead of those before them
+        uint32_t x[32], y[32];
+        tmem_ld32(s_at, x);
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 64) {
+          uint32_t p[16];
           tmem_wait_ld();
-          if (td.valid < kPage) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= td.valid) x[i] = 0xFF800000u;
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float p0, p1;
-            up2(fma2(pk2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale2, neg_m),
-                p0, p1);
-            p0 = ex2_f32(p0);
-            p1 = ex2_f32(p1);
-            l2 = add2(l2, pk2(p0, p1));
-            p[i] = pack_f16x2_rn(p0, p1);
-          }
-          tmem_st16(s_at + 16 * c, p);
+          tmem_ld32(s_at + c + 32, y);
+          exponentials(x, scale2, neg_m, l2, p);
+          tmem_wait_ld();
+          tmem_st16(s_at + c / 2, p);
+          if (c == 0) tmem_ld32(s_at + 64, x);
+          exponentials(y, scale2, neg_m, l2, p);
+          tmem_st16(s_at + c / 2 + 16, p);
         }
         tmem_wait_st();
       }
@@ -691,48 +820,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l = l0 + l1;
       // (m, l) of the other warpgroup; of a segment of one tile nobody else has one
       if (td.flags & kStart) mbar_arrive_warp(&l_ready[4 * (td.seg & 1) + quarter]);
-      if (!mbar_wait_warp(&l_ready[4 * (td.seg & 1) + quarter], (td.seg >> 1) & 1, abort)) break;
+      if (!wait(&l_ready[4 * (td.seg & 1) + quarter], (td.seg >> 1) & 1, abort)) break;
       if (!(td.flags & kStart)) {
         const float2 v = ml_of[kRows * (td.seg & 1) + r];
         if (v.x > -INFINITY) l = fmaf(v.y, ex2_f32(v.x - m), l);
       }
-      if (!mbar_wait_warp(&pv_done[b], (n >> 1) & 1, abort)) break;
+      if (!wait(&pv_done[b], (n >> 1) & 1, abort)) break;
       tc_fence_after();
       const bool mine = r < td.rows;
       const int row = td.row0 + r, tok = row / a.G;
       const int64_t at = static_cast<int64_t>(td.tok0 + tok) * a.H + td.hk * a.G + row - tok * a.G;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float f = td.slot >= 0 ? 1.f : l > 0.f ? __fdividef(1.f, l) : 0.f;
       float* part = a.parts + max(td.slot, 0) * part_floats(a.part_rows, D);
+      __nv_bfloat16* out16 = td.slot < 0 && a.o != nullptr ? a.o + at * D : nullptr;
+      float* out32 = td.slot < 0 ? a.o32 + at * D : part + 2 * a.part_rows + r * D;
       if (live) {
-#pragma unroll
-        for (int x = 0; x < D; x += 32) {
-          uint32_t v[32];
+#pragma unroll 1
+        for (int x = 0; x < D; x += 16) {
+          uint32_t v[16];
           __syncwarp();
-          tmem_ld32(lanes + kO + x, v);
+          tmem_ld16(lanes + kO + x, v);
           tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
           if (!mine) {
-          } else if (td.slot < 0 && a.o != nullptr) {
-            uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + x);
+          } else if (out16 != nullptr) {
+            uint4* dst = reinterpret_cast<uint4*>(out16 + x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(
-                    __uint_as_float(v[8 * i + 2 * u]) * inv, __uint_as_float(v[8 * i + 2 * u + 1]) * inv);
-                w[u] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int i = 0; i < 2; ++i)
+              dst[i] = make_uint4(pack_bf16(v + 8 * i), pack_bf16(v + 8 * i + 2),
+                                  pack_bf16(v + 8 * i + 4), pack_bf16(v + 8 * i + 6));
           } else {
-            const float f = td.slot < 0 ? inv : 1.f;
-            float4* dst = reinterpret_cast<float4*>(
-                td.slot < 0 ? a.o32 + at * D + x : part + 2 * a.part_rows + r * D + x);
+            uint4* dst = reinterpret_cast<uint4*>(out32 + x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(__uint_as_float(v[4 * i]) * f, __uint_as_float(v[4 * i + 1]) * f,
-                                   __uint_as_float(v[4 * i + 2]) * f,
-                                   __uint_as_float(v[4 * i + 3]) * f);
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
       }
@@ -745,32 +867,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.lse[at] = row_lse(a, m, l);
       }
     }
-  } else if (warp == kSpareWarp) {
-    // ------------------------------------- rows without keys, rows outside of all sequences
-    const int ctas = static_cast<int>(gridDim.x);
-    for (int s0 = 0; s0 < a.B; s0 += 32) {
-      bool bad;
-      Extent e{0, 0, 0, 0, 1};
-      if (s0 + lane < a.B) e = extent(a, s0 + lane, &bad);
-      uint32_t none = __ballot_sync(0xFFFFFFFFu, e.toks > 0 && e.key_tiles == 0);
-      for (; none != 0; none &= none - 1) {
-        const int i = __ffs(none) - 1;
-        const int tok0 = __shfl_sync(0xFFFFFFFFu, e.tok0, i), toks = __shfl_sync(0xFFFFFFFFu, e.toks, i);
-        for (int t = run; t < toks; t += ctas) empty_token<D>(a, tok0 + t, lane);
-      }
-    }
-    if (a.cu != nullptr) {
-      const int lo = min(max(a.cu[0], 0), a.T), hi = min(max(a.cu[a.B], 0), a.T);
-      for (int t = run; t < lo; t += ctas) empty_token<D>(a, t, lane);
-      for (int64_t t = static_cast<int64_t>(hi) + run; t < a.T; t += ctas)
-        empty_token<D>(a, static_cast<int>(t), lane);
-    }
   }
 
   tc_fence_before();
   __syncthreads();
-  report_abort(abort, a.err);
-  if (warp == kSpareWarp) {
+  report_abort(&abort_word, a.err);
+  if (warp == kSWarp) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);

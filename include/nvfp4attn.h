@@ -613,7 +613,7 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
  * S, o and lse as in attn_qat_decode (q~ quantized, the probabilities not).  A row
  * without keys, and a row outside every sequence, gets o = 0 and lse = -inf.
  * D in {64, 128}; T >= 1, T*H < 2^31 - 256, B, H <= 65535, and
- * (T*H/Hkv/128 + B) * Hkv * max_pages < 2^37 (else NVQ_ERR_UNSUPPORTED).  Work is split over
+ * (T*H/Hkv/128 + B) * Hkv * max_pages < 2^34 (else NVQ_ERR_UNSUPPORTED).  Work is split over
  * rows and keys and joined in a fixed order: results do not vary from run to run.
  * ws: attn_qat_cross_workspace(T, B, H, Hkv, D, max_pages) bytes, 256-byte aligned;
  * its size follows from the current device's multiprocessor count.

@@ -6,7 +6,7 @@
 // behind a shared prefix (a "sequence": the batch entries that share it; the keys: the
 // prefix, read once for all of them).
 //
-// Work split.  Tiles (128 rows x one page of 128 keys) of all (sequence, KV head, row tile)
+// Work split.  Tiles (256 rows x one page of 128 keys) of all (sequence, KV head, row tile)
 // lie one after another on one line, cut into equal runs, one CTA each, whatever the lengths.
 // A segment (one sequence, KV head and row tile) inside a run is written by it; one that
 // crosses runs leaves (m, l, sum p V~) per run in the workspace, joined in run order by a
@@ -16,15 +16,17 @@
 //   producer   K codes by tensor-map loads with the swizzle the MMA reads, the record's rest
 //              by bulk copies, into a ring of stages, with a description of each tile
 //   S          scales of K into the scale operand's order; S = Q~ K~^T as block-scaled FP4
-//              tcgen05 MMAs on the codes, into one of two buffers of 128 columns
+//              tcgen05 MMAs on the codes.  A unit is 128 rows x 64 keys; the units of a tile
+//              (rows' halves A and B in turn) go through three buffers of 64 columns, so that
+//              S of the next unit is there when a half's softmax has ended
 //   PV         O += P V~ as f16 MMAs, P from tensor memory (over the S it came from)
 //   4 decode   V's codes times scales, exactly, to f16 rows in shared memory (scales run
-//              along D, so codes cannot be the FP4 operand of a product over keys)
+//              along D, so codes cannot be the FP4 operand of a product over keys), once for
+//              both halves
+//   2 x 4      softmax, one thread a row, a warpgroup for each half of the rows.  The maximum
+//              that p refers to is raised only where a score exceeds it by 8 (log2); the
+//              row's thread then rescales O itself
 //   4 query    q~ of the segments, up to two ahead; rows without keys
-//   2 x 4      softmax, one thread a row: warpgroup w takes every other tile.  Both accumulate
-//              into one O, so p refers to a maximum that goes from tile to tile through shared
-//              memory, published before the exponentials; it is raised only where a score
-//              exceeds it by 8 (log2), when that tile's threads rescale O themselves.
 // p is rounded to f16 (below 2^8), its sum taken before the rounding; all sums are fp32.
 #include <algorithm>
 #include <cmath>
@@ -42,21 +44,23 @@ namespace nvq {
 
 namespace {
 
-constexpr int kRows = 128;     // query rows of a tile
+constexpr int kRows = 128;     // query rows of a unit
+constexpr int kPair = 256;     // and of a tile
+constexpr int kKeys = 64;      // keys of a unit
 constexpr int kThreads = 608;
 constexpr int kDecodeWarp = 8, kQWarp = 12, kProducerWarp = 16, kSWarp = 17, kPvWarp = 18;
-constexpr int kDescs = 16;     // descriptions outlive their stages by the tiles in softmax
 constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// tensor memory columns: S of tile j at 128 (j & 1), O, the scales of q~ (two buffers) and of K
-// (four: a copy never overwrites what an MMA in flight may read, see the S warp)
-constexpr uint32_t kO = 256, kSfQ = 384, kSfK = 400;
+// tensor memory columns: S of unit u at 64 (u % 3), O of the two halves, the scales of q~ (two
+// buffers of both halves) and of K (four: a copy never overwrites what an MMA in flight may
+// read, see the S warp)
+constexpr uint32_t kO = 192, kSfQ = 448, kSfK = 480;
 
-enum : int { kStart = 1, kSecond = 2, kNextEnd = 4, kEnd = 8, kAbsent = 16 };
+enum : int { kStart = 1, kEnd = 2, kAbsent = 4, kBoth = 8 };
 
 struct Tile {
-  int flags, valid;  // keys of the page that hold tokens
-  int rows;          // of the segment's 128
+  int flags, valid;  // kBoth: over 128 rows; keys of the page that hold tokens
+  int rows;          // of the segment's 256
   int row0;          // its first row among the rows of its (sequence, KV head)
   int tok0, hk;      // first token of the sequence; KV head
   int slot;          // where the segment's part goes (-1: it is whole)
@@ -71,14 +75,12 @@ struct Cfg {
   static constexpr uint32_t kQ = kRows * D / 2;          // codes of q~
   static constexpr uint32_t kQSc = D / 64 * 512;         // and scales
   static constexpr uint32_t kVAt = kStages * kRec;       // [2]
-  static constexpr uint32_t kQAt = kVAt + 2 * kV;        // [2]
-  static constexpr uint32_t kQScAt = kQAt + 2 * kQ;      // [2]
-  static constexpr uint32_t kRawAt = kQScAt + 2 * kQSc;  // bf16 rows of the next segment
-  static constexpr uint32_t kMAt = kRawAt + kRows * D * 2;  // float [2][128]: maximum by tile parity
-  static constexpr uint32_t kLAt = kMAt + 2 * kRows * 4;  // float2 [2][128]: (m, l) by segment parity
-  static constexpr uint32_t kDescAt = kLAt + 2 * kRows * 8;
-  static constexpr uint32_t kBarAt = kDescAt + kDescs * 32;
-  static constexpr int kBars = 2 * kStages + kDescs + 2 * 7 + 8 + 8 + 3;
+  static constexpr uint32_t kQAt = kVAt + 2 * kV;        // [2][2 halves]
+  static constexpr uint32_t kQScAt = kQAt + 4 * kQ;      // [2][2]
+  static constexpr uint32_t kRawAt = kQScAt + 4 * kQSc;  // bf16 rows of the next half
+  static constexpr uint32_t kDescAt = kRawAt + kRows * D * 2;
+  static constexpr uint32_t kBarAt = kDescAt + kStages * 32;
+  static constexpr int kBars = 2 * kStages + 4 * 2 + 4 * 3 + 3 * 2;
   // heads of 64: padded so that no CTA of the few-rows linear lies beside one
   static constexpr uint32_t kUsed = kBarAt + kBars * 8 + 1024;
   static constexpr uint32_t kSmem = kUsed > 152 * 1024 ? kUsed : 152 * 1024;
@@ -139,7 +141,7 @@ __device__ __forceinline__ Extent extent(const CrossArgs& a, int s, bool* bad) {
   const int cap = a.max_pages * kPage, n = a.lens[s];
   *bad |= n > cap;
   e.len = max(0, min(n, cap));
-  e.row_tiles = (e.toks * a.G + kRows - 1) / kRows;
+  e.row_tiles = (e.toks * a.G + kPair - 1) / kPair;
   e.key_tiles = e.row_tiles > 0 ? (e.len + kPage - 1) / kPage : 0;
   return e;
 }
@@ -183,9 +185,9 @@ struct Walk {
     cut();
     return true;
   }
-  __device__ __forceinline__ int row0() const { return rt * kRows; }
+  __device__ __forceinline__ int row0() const { return rt * kPair; }
   __device__ __forceinline__ int rows(const CrossArgs& a) const {
-    return min(kRows, e.toks * a.G - row0());
+    return min(kPair, e.toks * a.G - row0());
   }
 };
 
@@ -198,18 +200,22 @@ __device__ __forceinline__ T uniform(T v) {
 // mbar_wait_warp in few instructions.  Nineteen warps of six roles run their own code at once, and
 // what does not fit the instruction caches costs more than all arithmetic (with the waits of
 // nvq_ptx.cuh inline, loops unrolled and masks in the softmax's chunks the kernel was 113 KB, three
-// warps of eleven waited for instructions and a tile took 3350 cycles).  A wait gives up after
-// 2^21 tries of up to a microsecond, or when another thread has.
+// warps of eleven waited for instructions and a tile took 3350 cycles).  A wait gives up after two
+// seconds, or when another thread has.  (With a suspend-time hint of a microsecond on the
+// try_wait a warp now and then slept all of it: 32 x 64 heads behind 131072 keys 166 us, HINTLESS.)
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t abort) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b32 n, v;\n\t"
-      "mov.u32 n, 0;\n\t"
-      "AGAIN:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 t0, t, v;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "@p bra DONE;\n\t"
-      "add.u32 n, n, 1;\n\t"
-      "setp.gt.u32 q, n, 0x200000;\n\t"
+      "mov.u32 t0, %%globaltimer_lo;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u32 t, %%globaltimer_lo;\n\t"
+      "sub.u32 t, t, t0;\n\t"
+      "setp.gt.u32 q, t, 2000000000;\n\t"
       "@q st.volatile.shared.u32 [%3], 1;\n\t"
       "ld.volatile.shared.u32 v, [%3];\n\t"
       "setp.eq.u32 q, v, 0;\n\t"
@@ -234,7 +240,7 @@ struct Ring {
   }
 };
 
-// q~ of a segment by 128 threads, thread t taking block t % (D/16) of every kStep-th row: its
+// q~ of half a segment (128 rows from row0 on, `rows` of them there) by 128 threads, thread t taking block t % (D/16) of every kStep-th row: its
 // bf16 rows by asynchronous copies (each thread reads back what it has copied itself), codes into
 // the swizzled rows of the A operand, scales into the 512-byte blocks of the scale operand.
 // Rows beyond the segment's: zeros.
@@ -242,10 +248,9 @@ template <int D>
 struct QueryTile {
   static constexpr int kBlocks = D / 16, kStep = 128 / kBlocks;
 
-  static __device__ __forceinline__ void fetch(const CrossArgs& a, const Walk& w, uint8_t* raw,
-                                               int t) {
-    const int j = t % kBlocks, rows = w.rows(a);
-    const int row = w.row0() + t / kBlocks;
+  static __device__ __forceinline__ void fetch(const CrossArgs& a, const Walk& w, int row0,
+                                               int rows, uint8_t* raw, int t) {
+    const int j = t % kBlocks, row = row0 + t / kBlocks;
     int tok = row / a.G, g = row - tok * a.G;
     const int step_t = kStep / a.G, step_g = kStep - step_t * a.G;
     tok += w.e.tok0;
@@ -274,7 +279,7 @@ struct QueryTile {
                                                   uint8_t* scales, int t) {
     const int j = t % kBlocks;
     asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 1
+#pragma unroll 2
     for (int n = t / kBlocks; n < kRows; n += kStep) {
       const uint4* src =
           reinterpret_cast<const uint4*>(raw + n * (D * 2) + ((j ^ (n & (kBlocks - 1))) << 5));
@@ -345,11 +350,51 @@ __device__ __forceinline__ void decode_v(const uint8_t* rec, uint8_t* dst, int v
   }
 }
 
+// Four kind::f16 UMMAs (K = 16 each) into the accumulator d: A in tensor memory at a + 8 k, B
+// through b0 advanced by 2048 k bytes; commits to c0 and, unless it is 0, to c1.
+__device__ __forceinline__ void umma_f16_ts4_w(uint32_t d, uint32_t a, uint64_t b0, uint32_t idesc,
+                                               uint32_t acc, uint32_t c0, uint32_t c1) {
+  asm volatile(
+      "{\n\t.reg .pred p, e, t, q;\n\t.reg .b32 lo, hi, a1, a2, a3;\n\t"
+      ".reg .b64 b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "setp.eq.u32 t, 0, 0;\n\t"
+      "mov.b64 {lo, hi}, %4;\n\t"
+      "add.u32 lo, lo, 128;\n\tmov.b64 b1, {lo, hi};\n\t"
+      "add.u32 lo, lo, 128;\n\tmov.b64 b2, {lo, hi};\n\t"
+      "add.u32 lo, lo, 128;\n\tmov.b64 b3, {lo, hi};\n\t"
+      "add.u32 a1, %3, 8;\n\tadd.u32 a2, %3, 16;\n\tadd.u32 a3, %3, 24;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.and.u32 q, %6, 0, e;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %4, %1, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %1, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %1, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %1, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t}"
+      ::"r"(d), "r"(idesc), "r"(acc), "r"(a), "l"(b0), "r"(c0), "r"(c1)
+      : "memory");
+}
+
 // What is written as a row's lse: the natural logarithm, or base 2 beside an output in fp32.
 __device__ __forceinline__ float row_lse(const CrossArgs& a, float m, float l) {
   if (!(l > 0.f)) return -INFINITY;
   const float v = m + log2f(l);
   return a.o != nullptr ? v * kLn2 : v;
+}
+
+// 32 lanes x 8 columns (32x32b shape).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                   taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(const uint32_t* v) {
@@ -397,23 +442,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) &
                                              ~static_cast<uintptr_t>(1023u));
-  float* m_of = reinterpret_cast<float*>(smem + C::kMAt);     // [2][128]
-  float2* ml_of = reinterpret_cast<float2*>(smem + C::kLAt);  // [2][128]
   Tile* desc = reinterpret_cast<Tile*>(smem + C::kDescAt);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarAt);
-  uint64_t* empty = full + C::kStages;        // S done with the stage, four decode warps
-  uint64_t* described = empty + C::kStages;   // [kDescs]
-  uint64_t* v_full = described + kDescs;      // [2], four decode warps
-  uint64_t* v_empty = v_full + 2;             // [2]
-  uint64_t* q_full = v_empty + 2;             // [2], four decode warps
-  uint64_t* q_empty = q_full + 2;             // [2]
-  uint64_t* s_full = q_empty + 2;             // [2]
-  uint64_t* p_full = s_full + 2;              // [2], four softmax warps
-  uint64_t* pv_done = p_full + 2;             // [2]
-  uint64_t* m_ready = pv_done + 2;            // [2][4]: maximum of tile parity, by quarter
-  uint64_t* l_ready = m_ready + 8;            // [2][4]: the other warpgroup's (m, l), by segment
-  uint64_t* o_read = l_ready + 8;             // four softmax warps
-  uint64_t* drain = o_read + 1;
+  uint64_t* empty = full + C::kStages;   // S and the PV, decode and softmax warps done with it
+  uint64_t* v_full = empty + C::kStages;  // [2], four decode warps
+  uint64_t* v_empty = v_full + 2;         // [2]
+  uint64_t* q_full = v_empty + 2;         // [2], four query warps
+  uint64_t* q_empty = q_full + 2;         // [2]
+  uint64_t* s_full = q_empty + 2;         // [2 halves][3], by the units of the half
+  uint64_t* p_full = s_full + 6;          // [3] by the unit's buffer, four softmax warps
+  uint64_t* pv_done = p_full + 3;         // [3]
+  uint64_t* o_full = pv_done + 3;         // [2 halves]: a segment's last PV is done
+  uint64_t* o_read = o_full + 2;          // [2 halves], four softmax warps
+  uint64_t* drain = o_read + 2;           // [2]
   const uint32_t abort = smem_u32(&abort_word);
   pdl_trigger();
 
@@ -421,25 +462,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_word = 0;
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 5);
+      mbar_init(&empty[s], 1 + 1 + 4 + 8);
     }
-    for (int i = 0; i < kDescs; ++i) mbar_init(&described[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&v_full[i], 4);
       mbar_init(&v_empty[i], 1);
       mbar_init(&q_full[i], 4);
       mbar_init(&q_empty[i], 1);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_read[i], 4);
+      mbar_init(&drain[i], 1);
+    }
+    for (int i = 0; i < 3; ++i) {
       mbar_init(&s_full[i], 1);
+      mbar_init(&s_full[3 + i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
-    for (int i = 0; i < 8; ++i) {
-      mbar_init(&m_ready[i], 1);
-      mbar_init(&l_ready[i], 1);
-    }
-    mbar_init(o_read, 4);
-    mbar_init(&drain[0], 1);
-    mbar_init(&drain[1], 1);
     fence_mbar_init();
   }
   if (warp == kSWarp) {
@@ -474,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int64_t before = scan - mine;  // tiles before this thread's sequences
   const int run = blockIdx.x;
-  // all < 2^37 (check_cross), runs < 2^10: no overflow
+  // all < 2^35 (check_cross), runs < 2^10: no overflow
   const int64_t n_runs = all < a.runs ? all : a.runs;
   const int64_t u0 = run < n_runs ? all * run / n_runs : all;
   const int64_t u1 = run < n_runs ? all * (run + 1) / n_runs : all;
@@ -526,17 +565,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int page = __shfl_sync(0xFFFFFFFFu, pages, (i - w.i) & 31);
           const bool there = page >= 0 && page < a.num_pages;
-          td.flags = (i == w.i ? kStart : 0) | (i == w.i + 1 ? kSecond : 0) |
-                     (i == w.i_end - 2 ? kNextEnd : 0) | (i == w.i_end - 1 ? kEnd : 0) |
-                     (there ? 0 : kAbsent);
+          td.flags = (i == w.i ? kStart : 0) | (i == w.i_end - 1 ? kEnd : 0) |
+                     (there ? 0 : kAbsent) | (td.rows > kRows ? kBoth : 0);
           td.valid = there ? min(kPage, w.e.len - i * kPage) : 0;
           if (!there && lane == 0) atomicMax(a.err, kErrTable);
           const int st = ring.s;
           if (!(ok = wait(&empty[st], ring.phase ^ 1, abort))) break;
-          if (lane == 0) {
-            desc[n % kDescs] = td;
-            mbar_arrive(&described[n % kDescs]);
-          }
+          if (lane == 0) desc[st] = td;
           __syncwarp();
           uint8_t* dst = smem + st * C::kRec;
           if (there) {
@@ -566,33 +601,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kSWarp) {
     // ------------------------------------------------------------ S = Q~ K~^T
-    constexpr uint32_t idesc = idesc_mxf4nvf4(kRows, kPage);
+    constexpr uint32_t idesc = idesc_mxf4nvf4(kRows, kKeys);
     constexpr uint32_t lay = D == 128 ? 4u : 6u, sbo = 4 * D;  // swizzle, bytes of 8 rows
+    Ring ring, unit;
+    int done[2] = {0, 0};  // units of the halves so far, modulo 3
     bool ok = true;
-    Ring ring;
 #pragma unroll 1
-    for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
+    for (int n = 0; n < n_tiles && ok; ++n, ring.next(C::kStages)) {
       const int st = ring.s;
-      if (!(ok = wait(&described[n % kDescs], (n / kDescs) & 1, abort))) break;
-      const struct { int flags, seg; } td{uniform(desc[n % kDescs].flags),
-                                          uniform(desc[n % kDescs].seg)};
-      if (!(ok = wait(&full[st], ring.phase, abort))) break;
-      const int qb = td.seg & 1;
-      if ((td.flags & kStart) &&
-          !(ok = wait(&q_full[qb], (td.seg >> 1) & 1, abort)))
-        break;
+      if (!wait(&full[st], ring.phase, abort)) break;
+      const int flags = uniform(desc[st].flags), seg = uniform(desc[st].seg);
+      const int qb = seg & 1, halves = flags & kBoth ? 2 : 1;
+      if ((flags & kStart) && !wait(&q_full[qb], (seg >> 1) & 1, abort)) break;
       tc_fence_after();
-      const uint32_t sfq = tmem + kSfQ + 8 * qb, sfk = tmem + kSfK + 8 * (n & 3);
+      const uint32_t sfq = tmem + kSfQ + 16 * qb, sfk = tmem + kSfK + 8 * (n & 3);
       uint8_t* stage = smem + st * C::kRec;
       // The copies below go to columns whose last readers have completed: of K's scales the
-      // MMAs of tile n - 4, as those of tile n - 2 went out behind the PV of tile n - 4; of
-      // q's the MMAs of segment seg - 2, which the decode warps waited for.
-      if (td.flags & kStart) {
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k)
-          tmem_cp_32x128_x4_w(sfq + 4 * k, smem_u32(smem + C::kQScAt + qb * C::kQSc) + 512 * k);
+      // MMAs of tile n - 4, as the last unit of tile n - 1 went out behind the PV of a unit three
+      // before it; of q's the MMAs of segment seg - 2, which the query warps waited for.
+      if (flags & kStart) {
+#pragma unroll 1
+        for (int k = 0; k < halves * (D / 64); ++k)  // a half's blocks at 8 columns
+          tmem_cp_32x128_x4_w(sfq + (D == 128 ? 4 * k : 8 * k),
+                              smem_u32(smem + C::kQScAt + 2 * qb * C::kQSc) + 512 * k);
       }
-      if (!(td.flags & kAbsent)) {
+      if (!(flags & kAbsent)) {
         arrange_scales<D>(stage + k_scales_at(D), lane);
         fence_proxy_async_smem();
         __syncwarp();
@@ -600,22 +633,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < D / 64; ++k)
           tmem_cp_32x128_x4_w(sfk + 4 * k, smem_u32(stage + k_scales_at(D)) + 512 * k);
       }
-      // S's buffer is free when the PV of tile n - 2 has read the P that lies over it
-      if (n >= 2) {
-        if (!(ok = wait(&pv_done[n & 1], ((n - 2) >> 1) & 1, abort))) break;
-        tc_fence_after();
-      }
-      if (!(td.flags & kAbsent)) {
-        const uint32_t qa = smem_u32(smem + C::kQAt + qb * C::kQ), ka = smem_u32(stage);
+#pragma unroll 1
+      for (int u = 0; u < 2 * halves; ++u, unit.next(3)) {
+        const int key = halves == 2 ? u >> 1 : u, half = halves == 2 ? u & 1 : 0;
+        const bool last = u == 2 * halves - 1;
+        const uint32_t qa = smem_u32(smem + C::kQAt + (2 * qb + half) * C::kQ);
+        const uint32_t ka = smem_u32(stage) + key * (kKeys * D / 2);
         const uint64_t qd[2] = {sdesc(qa, 16, sbo, lay), sdesc(qa, 16, sbo, lay) + 2};
         const uint64_t kd[2] = {sdesc(ka, 16, sbo, lay), sdesc(ka, 16, sbo, lay) + 2};
-        umma_fp4_group_w<D / 64>(tmem + 128 * (n & 1), qd, kd, idesc, sfq, sfk,
-                                 bar_u32(&s_full[n & 1]), bar_u32(&empty[st]));
-      } else {
-        umma_commit_w(&s_full[n & 1]);
-        umma_commit_w(&empty[st]);
+        // the buffer is free when the PV of the unit three before has read the P over it
+        if (!(ok = wait(&pv_done[unit.s], unit.phase ^ 1, abort))) break;
+        tc_fence_after();
+        uint64_t* const ready = &s_full[half == 0 ? done[0] : 3 + done[1]];
+        if (half == 0) done[0] = done[0] == 2 ? 0 : done[0] + 1;
+        else done[1] = done[1] == 2 ? 0 : done[1] + 1;
+        if (!(flags & kAbsent)) {
+          umma_fp4_group_w<D / 64>(tmem + 64 * unit.s, qd, kd, idesc, sfq + 8 * half, sfk + 2 * key,
+                                   bar_u32(ready), last ? bar_u32(&empty[st]) : 0u);
+        } else {
+          umma_commit_w(ready);
+          if (last) umma_commit_w(&empty[st]);
+        }
       }
-      if (td.flags & kEnd) umma_commit_w(&q_empty[qb]);
+      if (flags & kEnd) umma_commit_w(&q_empty[qb]);
     }
     umma_commit_w(&drain[0]);  // the MMAs in flight end before the block
     mbar_wait_warp(&drain[0], 0, nullptr, 10000000ull);
@@ -623,25 +663,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ O += P V~
     constexpr uint32_t idesc = idesc_f16(kRows, D, 0, 0, 1);
     const uint64_t v_d0 = sdesc_sw128(smem_u32(smem + C::kVAt), kRows * 128, 1024);
+    Ring ring, unit;
+    int seg_b = 0;  // segments of both halves so far
+    bool ok = true;
 #pragma unroll 1
-    for (int n = 0; n < n_tiles; ++n) {
+    for (int n = 0; n < n_tiles && ok; ++n, ring.next(C::kStages)) {
       const int b = n & 1;
-      const uint32_t phase = (n >> 1) & 1;
-      if (!wait(&described[n % kDescs], (n / kDescs) & 1, abort)) break;
-      const struct { int flags, seg; } td{uniform(desc[n % kDescs].flags),
-                                          uniform(desc[n % kDescs].seg)};
-      // O of the segment before has been read
-      if ((td.flags & kStart) && td.seg > 0 &&
-          !wait(o_read, (td.seg - 1) & 1, abort))
-        break;
-      if (!wait(&v_full[b], phase, abort)) break;
-      if (!wait(&p_full[b], phase, abort)) break;
-      tc_fence_after();
-      uint32_t p[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) p[k] = tmem + 128 * b + 8 * k;
-      umma_f16_ts8_w(tmem + kO, p, v_d0 + static_cast<uint64_t>(b) * (C::kV >> 4), idesc,
-                     td.flags & kStart ? 0u : 1u, bar_u32(&pv_done[b]), bar_u32(&v_empty[b]));
+      if (!wait(&full[ring.s], ring.phase, abort)) break;
+      const int flags = uniform(desc[ring.s].flags), seg = uniform(desc[ring.s].seg);
+      mbar_arrive_warp(&empty[ring.s]);
+      const int halves = flags & kBoth ? 2 : 1;
+      if (!wait(&v_full[b], (n >> 1) & 1, abort)) break;
+#pragma unroll 1
+      for (int u = 0; u < 2 * halves; ++u, unit.next(3)) {
+        const int key = halves == 2 ? u >> 1 : u, half = halves == 2 ? u & 1 : 0;
+        const bool first = (flags & kStart) && key == 0;
+        // O of the half's segment before has been read
+        if (first) {
+          const int before = half == 0 ? seg : seg_b++;
+          if (before > 0 && !(ok = wait(&o_read[half], (before - 1) & 1, abort))) break;
+        }
+        if (!(ok = wait(&p_full[unit.s], unit.phase, abort))) break;
+        tc_fence_after();
+        umma_f16_ts4_w(tmem + kO + D * half, tmem + 64 * unit.s,
+                       v_d0 + static_cast<uint64_t>(b) * (C::kV >> 4) + 512 * key, idesc,
+                       first ? 0u : 1u, bar_u32(&pv_done[unit.s]),
+                       u == 2 * halves - 1 ? bar_u32(&v_empty[b]) : 0u);
+        if ((flags & kEnd) && key == 1) umma_commit_w(&o_full[half]);
+      }
     }
     umma_commit_w(&drain[1]);
     mbar_wait_warp(&drain[1], 0, nullptr, 10000000ull);
@@ -651,14 +700,170 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
     for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
       const int st = ring.s, b = n & 1;
-      if (!wait(&described[n % kDescs], (n / kDescs) & 1, abort)) break;
-      const int valid = desc[n % kDescs].valid;
       if (!wait(&full[st], ring.phase, abort)) break;
       if (!wait(&v_empty[b], ((n >> 1) & 1) ^ 1, abort)) break;
-      decode_v<D>(smem + st * C::kRec, smem + C::kVAt + b * C::kV, valid, warp - kDecodeWarp, lane);
+      decode_v<D>(smem + st * C::kRec, smem + C::kVAt + b * C::kV, desc[st].valid,
+                  warp - kDecodeWarp, lane);
       fence_proxy_async_smem();
       mbar_arrive_warp(&v_full[b]);
       mbar_arrive_warp(&empty[st]);
+    }
+  } else if (warp < kDecodeWarp) {
+    // ------------------------------------------------------------ softmax
+    const int half = warp >> 2, quarter = warp & 3;
+    const int r = threadIdx.x;  // row of the segment; r % 128: lane of tensor memory
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t o_at = lanes + kO + D * half;
+    const uint64_t scale2 = pk2(a.scale_log2, a.scale_log2);
+    float m = -INFINITY;  // reference maximum (log2 units)
+    uint64_t l2 = pk2(0.f, 0.f);
+    uint32_t unit0 = 0;   // units before this tile
+    uint32_t ends = 0;    // segments of this half before this one
+    bool ok = true;
+    // s_full is the half's own: a half that has nothing to do for a while would miss phases of a
+    // barrier that both share, and take an older one's end for the one it waits for
+    Ring ring, mine_full;
+#pragma unroll 1
+    for (int n = 0; n < n_tiles && ok; ++n, ring.next(C::kStages)) {
+      if (!wait(&full[ring.s], ring.phase, abort)) break;
+      // the description is read again where the segment ends: its fields held over the softmax
+      // would be spilled, to a cache that shared memory leaves next to nothing of
+      const Tile* const td = &desc[ring.s];
+      const int flags = td->flags;
+      const uint32_t halves = flags & kBoth ? 2 : 1;
+      uint32_t u = unit0 + half;
+      unit0 += 2 * halves;
+      if (half == 1 && halves == 1) {
+        mbar_arrive_warp(&empty[ring.s]);
+        continue;
+      }
+      const int all_valid = td->valid;
+      const bool live = 32 * warp < td->rows;  // else: rows that nobody reads
+      if (flags & kStart) {
+        m = -INFINITY;
+        l2 = pk2(0.f, 0.f);
+      }
+#pragma unroll 1
+      for (int key = 0; key < 2; ++key, u += halves, mine_full.next(3)) {
+        const uint32_t buf = u % 3;
+        const int valid = all_valid - kKeys * key;
+        if (!(ok = wait(&s_full[3 * half + mine_full.s], mine_full.phase, abort))) break;
+        tc_fence_after();
+        const uint32_t s_at = lanes + 64 * buf;
+        if (live) {
+          if (valid < kKeys) {  // keys behind the last: -inf, before S is read
+#pragma unroll 1
+            for (int c = max(valid, 0) & ~15; c < kKeys; c += 16) {
+              uint32_t x[16];
+              tmem_ld16(s_at + c, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (c + i >= valid) x[i] = 0xFF800000u;
+              tmem_st16(s_at + c, x);
+            }
+            tmem_wait_st();
+          }
+          uint32_t x[32], y[32];
+          tmem_ld32(s_at, x);
+          tmem_ld32(s_at + 32, y);
+          tmem_wait_ld();
+          float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            v[0] = max3f(v[0], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            v[1] = max3f(v[1], __uint_as_float(x[16 + i]), __uint_as_float(x[17 + i]));
+            v[2] = max3f(v[2], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+            v[3] = max3f(v[3], __uint_as_float(y[16 + i]), __uint_as_float(y[17 + i]));
+          }
+          const float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * a.scale_log2;
+          const bool grows = mx > m + kSlack;  // -inf: always, where there is a key
+          if (__any_sync(0xFFFFFFFFu, grows)) {
+            const float c = grows ? ex2_f32(m - mx) : 1.f;
+            if (grows) m = mx;
+            l2 = mul2(l2, pk2(c, c));
+            // raised behind the segment's first unit: O so far, which the half's PV before has
+            // finished
+            if (!(flags & kStart) || key > 0) {
+              const uint32_t w = u - halves;
+              if (!(ok = wait(&pv_done[w % 3], (w / 3) & 1, abort))) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int z = 0; z < D; z += 8) {
+                uint32_t t[8];
+                tmem_ld8(o_at + z, t);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) t[i] = __float_as_uint(__uint_as_float(t[i]) * c);
+                tmem_st8(o_at + z, t);
+              }
+            }
+          }
+          // ---- p = 2^(S log2e - m), over S
+          const float ref = -fmaxf(m, -3.4e38f);
+          const uint64_t neg_m = pk2(ref, ref);
+          uint32_t p[16];
+          exponentials(x, scale2, neg_m, l2, p);
+          tmem_st16(s_at, p);
+          exponentials(y, scale2, neg_m, l2, p);
+          tmem_st16(s_at + 16, p);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive_warp(&p_full[buf]);
+      }
+      if (!ok) break;
+      if (!(flags & kEnd)) {
+        mbar_arrive_warp(&empty[ring.s]);
+        continue;
+      }
+      // ---- the segment's end
+      if (!wait(&o_full[half], ends++ & 1, abort)) break;
+      tc_fence_after();
+      float l0, l1;
+      up2(l2, l0, l1);
+      const float l = l0 + l1;
+      const bool mine = r < td->rows;
+      const int slot = td->slot, row = td->row0 + r, tok = row / a.G;
+      const int64_t at =
+          static_cast<int64_t>(td->tok0 + tok) * a.H + td->hk * a.G + row - tok * a.G;
+      mbar_arrive_warp(&empty[ring.s]);
+      const float f = slot >= 0 ? 1.f : l > 0.f ? __fdividef(1.f, l) : 0.f;
+      float* part = a.parts + max(slot, 0) * part_floats(a.part_rows, D);
+      __nv_bfloat16* out16 = slot < 0 && a.o != nullptr ? a.o + at * D : nullptr;
+      float* out32 = slot < 0 ? a.o32 + at * D : part + 2 * a.part_rows + r * D;
+      if (live) {
+#pragma unroll 1
+        for (int x = 0; x < D; x += 16) {
+          uint32_t v[16];
+          __syncwarp();
+          tmem_ld16(o_at + x, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+          if (!mine) {
+          } else if (out16 != nullptr) {
+            uint4* dst = reinterpret_cast<uint4*>(out16 + x);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              dst[i] = make_uint4(pack_bf16(v + 8 * i), pack_bf16(v + 8 * i + 2),
+                                  pack_bf16(v + 8 * i + 4), pack_bf16(v + 8 * i + 6));
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(out32 + x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive_warp(&o_read[half]);
+      if (mine) {
+        if (slot >= 0)
+          *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
+        else if (a.lse != nullptr)
+          a.lse[at] = row_lse(a, m, l);
+      }
     }
   } else if (warp >= kQWarp && warp < kProducerWarp) {
     // ------------------------------------------------------------ q~
@@ -666,16 +871,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = threadIdx.x - 32 * kQWarp;
       Walk w(a, start_s, start_before, u0, n_tiles);
       int seg = 0;
+      bool ok = true;
       do {
-        QueryTile<D>::fetch(a, w, smem + C::kRawAt, t);
-        const int qb = seg & 1;
-        if (!wait(&q_empty[qb], ((seg >> 1) & 1) ^ 1, abort)) break;
-        QueryTile<D>::quantize(smem + C::kRawAt, smem + C::kQAt + qb * C::kQ,
-                               smem + C::kQScAt + qb * C::kQSc, t);
+        const int qb = seg & 1, rows = w.rows(a);
+#pragma unroll 1
+        for (int half = 0; half < (rows > kRows ? 2 : 1) && ok; ++half) {
+          QueryTile<D>::fetch(a, w, w.row0() + half * kRows, rows - half * kRows, smem + C::kRawAt,
+                              t);
+          if (half == 0) ok = wait(&q_empty[qb], ((seg >> 1) & 1) ^ 1, abort);
+          if (ok)
+            QueryTile<D>::quantize(smem + C::kRawAt, smem + C::kQAt + (2 * qb + half) * C::kQ,
+                                   smem + C::kQScAt + (2 * qb + half) * C::kQSc, t);
+        }
         fence_proxy_async_smem();
         mbar_arrive_warp(&q_full[qb]);
         ++seg;
-      } while (w.next(a));
+      } while (ok && w.next(a));
     }
     // ---- rows without keys, rows outside of all sequences
     const int first = 4 * run + warp - kQWarp, step = 4 * static_cast<int>(gridDim.x);
@@ -699,173 +910,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int64_t t = static_cast<int64_t>(hi) + first; t < a.T; t += step)
         empty_token<D>(a, static_cast<int>(t), lane);
-    }
-  } else if (warp < kDecodeWarp) {
-    // ------------------------------------------------------------ softmax
-    const int wg = warp >> 2, quarter = warp & 3;
-    const int r = threadIdx.x & 127;  // row of the tile == lane of tensor memory
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint64_t scale2 = pk2(a.scale_log2, a.scale_log2);
-    float m = -INFINITY;  // reference maximum (log2 units) of this warpgroup's last tile
-    uint64_t l2 = pk2(0.f, 0.f);
-#pragma unroll 1
-    for (int n = wg; n < n_tiles; n += 2) {
-      const int b = n & 1;
-      if (!wait(&described[n % kDescs], (n / kDescs) & 1, abort)) break;
-      const Tile td = desc[n % kDescs];
-      const bool live = quarter * 32 < td.rows;  // else: rows that nobody reads
-      if (!wait(&s_full[b], (n >> 1) & 1, abort)) break;
-      tc_fence_after();
-      const uint32_t s_at = lanes + 128 * b;
-      if (td.flags & (kStart | kSecond)) {
-        m = -INFINITY;
-        l2 = pk2(0.f, 0.f);
-      }
-      if (live && td.valid < kPage) {  // keys behind the last: -inf, before S is read
-#pragma unroll 1
-        for (int c = td.valid & ~15; c < kPage; c += 16) {
-          uint32_t x[16];
-          tmem_ld16(s_at + c, x);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c + i >= td.valid) x[i] = 0xFF800000u;
-          tmem_st16(s_at + c, x);
-        }
-        tmem_wait_st();
-      }
-      float mx = -INFINITY;
-      if (live) {
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          uint32_t x[32], y[32];
-          tmem_ld32(s_at + 32 * c, x);
-          tmem_ld32(s_at + 32 * c + 32, y);
-          tmem_wait_ld();
-          float v[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            v[0] = max3f(v[0], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-            v[1] = max3f(v[1], __uint_as_float(x[16 + i]), __uint_as_float(x[17 + i]));
-            v[2] = max3f(v[2], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-            v[3] = max3f(v[3], __uint_as_float(y[16 + i]), __uint_as_float(y[17 + i]));
-          }
-          mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-        }
-        mx *= a.scale_log2;
-      }
-      // ---- the maximum so far, from the tile before; also where a segment begins, for the order
-      if (n > 0 &&
-          !wait(&m_ready[4 * (b ^ 1) + quarter], ((n - 1) >> 1) & 1, abort))
-        break;
-      float old = td.flags & kStart ? -INFINITY : m_of[kRows * (b ^ 1) + r];
-      const bool grows = mx > old + kSlack || (old == -INFINITY && mx > -INFINITY);
-      const float now = grows ? mx : old;
-      m_of[kRows * b + r] = now;
-      mbar_arrive_warp(&m_ready[4 * b + quarter]);
-      if (!(td.flags & kStart) && __any_sync(0xFFFFFFFFu, grows)) {
-        // raised behind the segment's first tile: O so far, which the PV before has finished
-        if (!wait(&pv_done[b ^ 1], ((n - 1) >> 1) & 1, abort)) break;
-        tc_fence_after();
-        const float c = grows ? ex2_f32(old - now) : 1.f;
-#pragma unroll 1
-        for (int x = 0; x < D; x += 16) {
-          uint32_t v[16];
-          tmem_ld16(lanes + kO + x, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * c);
-          tmem_st16(lanes + kO + x, v);
-        }
-        tmem_wait_st();
-      }
-      if (m != now) {  // raised since this warpgroup's last tile, by either
-        const float c = ex2_f32(m - now);  // 0 where the segment begins
-        l2 = mul2(l2, pk2(c, c));
-        m = now;
-      }
-      // ---- p = 2^(S log2e - m), over S
-      if (live) {
-        const float ref = -fmaxf(now, -3.4e38f);
-        const uint64_t neg_m = pk2(ref, ref);
-        // columns c .. c + 31 are read a step ahead of those before them
-        uint32_t x[32], y[32];
-        tmem_ld32(s_at, x);
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 64) {
-          uint32_t p[16];
-          tmem_wait_ld();
-          tmem_ld32(s_at + c + 32, y);
-          exponentials(x, scale2, neg_m, l2, p);
-          tmem_wait_ld();
-          tmem_st16(s_at + c / 2, p);
-          if (c == 0) tmem_ld32(s_at + 64, x);
-          exponentials(y, scale2, neg_m, l2, p);
-          tmem_st16(s_at + c / 2 + 16, p);
-        }
-        tmem_wait_st();
-      }
-      tc_fence_before();
-      mbar_arrive_warp(&p_full[b]);
-      if (td.flags & kNextEnd) {  // the other warpgroup writes the segment
-        float l0, l1;
-        up2(l2, l0, l1);
-        ml_of[kRows * (td.seg & 1) + r] = make_float2(m, l0 + l1);
-        mbar_arrive_warp(&l_ready[4 * (td.seg & 1) + quarter]);
-      }
-      if (!(td.flags & kEnd)) continue;
-      // ---- the segment's end
-      float l0, l1;
-      up2(l2, l0, l1);
-      float l = l0 + l1;
-      // (m, l) of the other warpgroup; of a segment of one tile nobody else has one
-      if (td.flags & kStart) mbar_arrive_warp(&l_ready[4 * (td.seg & 1) + quarter]);
-      if (!wait(&l_ready[4 * (td.seg & 1) + quarter], (td.seg >> 1) & 1, abort)) break;
-      if (!(td.flags & kStart)) {
-        const float2 v = ml_of[kRows * (td.seg & 1) + r];
-        if (v.x > -INFINITY) l = fmaf(v.y, ex2_f32(v.x - m), l);
-      }
-      if (!wait(&pv_done[b], (n >> 1) & 1, abort)) break;
-      tc_fence_after();
-      const bool mine = r < td.rows;
-      const int row = td.row0 + r, tok = row / a.G;
-      const int64_t at = static_cast<int64_t>(td.tok0 + tok) * a.H + td.hk * a.G + row - tok * a.G;
-      const float f = td.slot >= 0 ? 1.f : l > 0.f ? __fdividef(1.f, l) : 0.f;
-      float* part = a.parts + max(td.slot, 0) * part_floats(a.part_rows, D);
-      __nv_bfloat16* out16 = td.slot < 0 && a.o != nullptr ? a.o + at * D : nullptr;
-      float* out32 = td.slot < 0 ? a.o32 + at * D : part + 2 * a.part_rows + r * D;
-      if (live) {
-#pragma unroll 1
-        for (int x = 0; x < D; x += 16) {
-          uint32_t v[16];
-          __syncwarp();
-          tmem_ld16(lanes + kO + x, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-          if (!mine) {
-          } else if (out16 != nullptr) {
-            uint4* dst = reinterpret_cast<uint4*>(out16 + x);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              dst[i] = make_uint4(pack_bf16(v + 8 * i), pack_bf16(v + 8 * i + 2),
-                                  pack_bf16(v + 8 * i + 4), pack_bf16(v + 8 * i + 6));
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(out32 + x);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-        }
-      }
-      tc_fence_before();
-      mbar_arrive_warp(o_read);
-      if (mine) {
-        if (td.slot >= 0)
-          *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
-        else if (a.lse != nullptr)
-          a.lse[at] = row_lse(a, m, l);
-      }
     }
   }
 
@@ -955,10 +999,10 @@ struct Plan {
 
 Plan plan(int64_t T, int B, int H, int Hkv, int D, int max_pages) {
   const int64_t rows = T * (H / Hkv);
-  const int64_t tiles = (rows / kRows + B) * Hkv * max_pages;  // at most
+  const int64_t tiles = (rows / kPair + B) * Hkv * max_pages;  // at most
   Plan p;
   p.runs = static_cast<int>(std::min<int64_t>(std::max<int64_t>(tiles, 1), device_sms()));
-  p.part_rows = static_cast<int>(std::min<int64_t>(kRows, (rows + 31) / 32 * 32));
+  p.part_rows = static_cast<int>(std::min<int64_t>(kPair, (rows + 31) / 32 * 32));
   p.parts = (p.runs * sizeof(Split) + 255) / 256 * 256;
   p.total = p.parts + 2 * p.runs * part_floats(p.part_rows, D) * sizeof(float);
   return p;
@@ -972,9 +1016,10 @@ nvq_status check_cross(int64_t T, int B, int H, int Hkv, int D, int max_pages) {
     return NVQ_ERR_INVALID;
   if (D != 64 && D != 128) return NVQ_ERR_UNSUPPORTED;
   if (B > 65535 || H > 65535 || T > 0x7FFFFF00 / H) return NVQ_ERR_UNSUPPORTED;
-  // (rows / 128 + B) Hkv < 2^24 + 2^33: no overflow; a run counts its tiles in 31 bits
+  // (rows / 128 + B) Hkv < 2^24 + 2^33: no overflow; a run counts its tiles in
+  // 29 bits (four units each)
   const int64_t heads = (T * (H / Hkv) / kRows + B) * Hkv;
-  return heads * max_pages / 64 >= 0x7FFFFFFF ? NVQ_ERR_UNSUPPORTED : NVQ_OK;
+  return heads * max_pages / 64 >= 0x1FFFFFFF ? NVQ_ERR_UNSUPPORTED : NVQ_OK;
 }
 
 size_t cross_workspace(int64_t T, int B, int H, int Hkv, int D, int max_pages) {

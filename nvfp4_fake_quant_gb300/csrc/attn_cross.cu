@@ -12,18 +12,19 @@
 // crosses runs leaves (m, l, sum p V~) per run in the workspace, joined in run order by a
 // second kernel: results do not vary from run to run.
 //
-// One CTA, nineteen warps:
+// One CTA, twenty warps:
 //   producer   K codes by tensor-map loads with the swizzle the MMA reads, the record's rest
 //              by bulk copies, into a ring of stages, with a description of each tile
-//   S          scales of K into the scale operand's order; S = Q~ K~^T as block-scaled FP4
-//              tcgen05 MMAs on the codes.  A unit is 128 rows x 64 keys; the units of a tile
-//              (rows' halves A and B in turn) go through three buffers of 64 columns, so that
-//              S of the next unit is there when a half's softmax has ended
+//   scales     K's scales into the scale operand's order
+//   S          S = Q~ K~^T as block-scaled FP4 tcgen05 MMAs on the codes.  A unit is 128 rows x 64 keys; the units of two
+//              streams (two halves of the rows; of 128 rows or fewer two halves of the keys,
+//              joined where the segment ends) go in turn through three buffers of 64 columns,
+//              so that S of the next unit is there when a stream's softmax has ended
 //   PV         O += P V~ as f16 MMAs, P from tensor memory (over the S it came from)
 //   4 decode   V's codes times scales, exactly, to f16 rows in shared memory (scales run
 //              along D, so codes cannot be the FP4 operand of a product over keys), once for
-//              both halves
-//   2 x 4      softmax, one thread a row, a warpgroup for each half of the rows.  The maximum
+//              both streams
+//   2 x 4      softmax, one thread a row, a warpgroup for each stream.  The maximum
 //              that p refers to is raised only where a score exceeds it by 8 (log2); the
 //              row's thread then rescales O itself
 //   4 query    q~ of the segments, up to two ahead; rows without keys
@@ -47,8 +48,11 @@ namespace {
 constexpr int kRows = 128;     // query rows of a unit
 constexpr int kPair = 256;     // and of a tile
 constexpr int kKeys = 64;      // keys of a unit
-constexpr int kThreads = 608;
-constexpr int kDecodeWarp = 8, kQWarp = 12, kProducerWarp = 16, kSWarp = 17, kPvWarp = 18;
+constexpr int kThreads = 640;
+constexpr int kDecodeWarp = 8, kQWarp = 12, kProducerWarp = 16, kSWarp = 17, kPvWarp = 18,
+              kScaleWarp = 19;
+constexpr int kSegs = 8;       // descriptions of segments: the query warps are two ahead of S, the
+                               // softmax of an end may be one behind it
 constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // tensor memory columns: S of unit u at 64 (u % 3), O of the two halves, the scales of q~ (two
@@ -60,16 +64,12 @@ enum : int { kStart = 1, kEnd = 2, kAbsent = 4, kBoth = 8 };
 
 struct Tile {
   int flags, valid;  // kBoth: over 128 rows; keys of the page that hold tokens
-  int rows;          // of the segment's 256
-  int row0;          // its first row among the rows of its (sequence, KV head)
-  int tok0, hk;      // first token of the sequence; KV head
-  int slot;          // where the segment's part goes (-1: it is whole)
-  int seg;           // segments before this one in the run
+  int rows, seg;     // of the segment; segments before it in the run
 };
 
 template <int D>
 struct Cfg {
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kStages = D == 128 ? 3 : 8;
   static constexpr uint32_t kRec = record_bytes(D);
   static constexpr uint32_t kV = kRows * D * 2;          // a page's V~ in f16
   static constexpr uint32_t kQ = kRows * D / 2;          // codes of q~
@@ -77,10 +77,13 @@ struct Cfg {
   static constexpr uint32_t kVAt = kStages * kRec;       // [2]
   static constexpr uint32_t kQAt = kVAt + 2 * kV;        // [2][2 halves]
   static constexpr uint32_t kQScAt = kQAt + 4 * kQ;      // [2][2]
-  static constexpr uint32_t kRawAt = kQScAt + 4 * kQSc;  // bf16 rows of the next half
-  static constexpr uint32_t kDescAt = kRawAt + kRows * D * 2;
-  static constexpr uint32_t kBarAt = kDescAt + kStages * 32;
-  static constexpr int kBars = 2 * kStages + 4 * 2 + 4 * 3 + 3 * 2;
+  static constexpr uint32_t kOutAt = kQScAt + 4 * kQSc;  // bf16 rows of o on their way out,
+  static constexpr uint32_t kOutRow = D * 2 + 16;        // apart by an odd number of 16 bytes
+  static constexpr uint32_t kMlAt = kOutAt + kPair * kOutRow;  // float2 [128]: the other keys' (m, l)
+  static constexpr uint32_t kDescAt = kMlAt + kRows * 8;
+  static constexpr uint32_t kSegAt = kDescAt + kStages * 16;   // Segment [kSegs]
+  static constexpr uint32_t kBarAt = kSegAt + kSegs * 48;
+  static constexpr int kBars = 3 * kStages + 4 * 2 + 4 * 3 + 3 * 2 + 4 + kSegs;
   // heads of 64: padded so that no CTA of the few-rows linear lies beside one
   static constexpr uint32_t kUsed = kBarAt + kBars * 8 + 1024;
   static constexpr uint32_t kSmem = kUsed > 152 * 1024 ? kUsed : 152 * 1024;
@@ -89,9 +92,20 @@ struct Cfg {
   static_assert(apart_from_linear_small(kSmem), "tensor memory");
 };
 
-// A segment that begins in a run and goes on in later ones; last < 0: none.
+// A segment that begins in a run and goes on in later ones: the line's last tile of it (below 0:
+// there is none) and the number of tiles of the line.
 struct Split {
-  int run, last, slot, rows, row0, tok0, hk, pad;
+  int64_t end, all;
+  int slot, rows, row0, tok0, hk, pad;
+};
+
+// A segment as the query warps hand it to the others.
+struct Segment {
+  int row0, rows;  // its first row among the rows of its (sequence, KV head), and their number
+  int tok0, hk;    // first token of the sequence; KV head
+  int slot;        // where the segment's part goes (-1: it is whole)
+  int s, i, i_end, len;  // its pages in the run, of a sequence of len keys
+  int pad[3];
 };
 
 struct CrossArgs {
@@ -111,9 +125,10 @@ struct CrossArgs {
   __nv_bfloat16* o;  // or, where null, o32 with the logarithms (base 2) in lse
   float* o32;
   float* lse;
-  Split* split;
+  Split* split;  // [runs]
   float* parts;  // [2 runs][part_rows] (m, l), then [part_rows][D]
   int part_rows, runs;
+  uint64_t runs_magic;  // 2^64 / runs, rounded up
   int* err;
 };
 
@@ -123,6 +138,41 @@ __host__ __device__ constexpr int64_t part_floats(int rows, int D) {
 
 struct Extent {
   int tok0, toks, len, row_tiles, key_tiles;
+};
+
+// The line of `all` tiles is cut into n = min(all, runs) runs: run c is [all c / n,
+// all (c + 1) / n), never empty; of the grid's runs those from n on have nothing.
+// all c / n = (all / n) c + (all % n) c / n.  n is the grid's or all itself, so there is
+// nothing to divide: the host gives 2^64 / runs, rounded up (all <= 2^53 and runs < 2^10
+// keep the product's error below 1 / runs).
+struct Runs {
+  int64_t all, per;
+  int n, rest;
+  uint32_t magic;
+  __device__ __forceinline__ Runs(int64_t all_, int runs, uint64_t magic_) : all(all_) {
+    if (all < runs) {
+      n = static_cast<int>(all);
+      per = 1;
+      rest = 0;
+    } else {
+      n = runs;
+      // (the reciprocal of 1 has no place in 64 bits)
+      per = runs == 1 ? all : static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(all), magic_));
+      rest = static_cast<int>(all - per * runs);
+    }
+    magic = static_cast<uint32_t>(magic_ >> 32) + 1;  // rest c < 2^24: exact as well
+  }
+  __device__ __forceinline__ int64_t begin(int c) const {
+    return c < n ? per * c + __umulhi(static_cast<uint32_t>(rest * c), magic) : all;
+  }
+};
+
+// Where a run begins: tile i of (sequence s, KV head hk, row tile rt), the sequence's first tile
+// at seg0 of the line.
+struct Start {
+  int64_t seg0;
+  Extent e;
+  int s, hk, rt, i;
 };
 
 __device__ __forceinline__ Extent extent(const CrossArgs& a, int s, bool* bad) {
@@ -152,14 +202,8 @@ struct Walk {
   Extent e;
   int64_t seg0, first;
   int s, hk, rt, i, i_end, left;  // left: tiles of the run from this segment on
-  __device__ __forceinline__ Walk(const CrossArgs& a, int s_, int64_t seg0_, int64_t u0, int n)
-      : seg0(seg0_), s(s_), left(n) {
-    bool bad;
-    e = extent(a, s, &bad);
-    const int64_t nth = (u0 - seg0) / e.key_tiles;  // segment of the sequence
-    hk = static_cast<int>(nth / e.row_tiles);
-    rt = static_cast<int>(nth - static_cast<int64_t>(hk) * e.row_tiles);
-    i = static_cast<int>(u0 - seg0 - nth * e.key_tiles);
+  __device__ __forceinline__ Walk(const Start& st, int n_tiles)
+      : e(st.e), seg0(st.seg0), s(st.s), hk(st.hk), rt(st.rt), i(st.i), left(n_tiles) {
     cut();
   }
   __device__ __forceinline__ void cut() {
@@ -197,7 +241,7 @@ __device__ __forceinline__ T uniform(T v) {
   return __shfl_sync(0xFFFFFFFFu, v, 0);
 }
 
-// mbar_wait_warp in few instructions.  Nineteen warps of six roles run their own code at once, and
+// mbar_wait_warp in few instructions.  Twenty warps of six roles run their own code at once, and
 // what does not fit the instruction caches costs more than all arithmetic (with the waits of
 // nvq_ptx.cuh inline, loops unrolled and masks in the softmax's chunks the kernel was 113 KB, three
 // warps of eleven waited for instructions and a tile took 3350 cycles).  A wait gives up after two
@@ -240,57 +284,61 @@ struct Ring {
   }
 };
 
-// q~ of half a segment (128 rows from row0 on, `rows` of them there) by 128 threads, thread t taking block t % (D/16) of every kStep-th row: its
-// bf16 rows by asynchronous copies (each thread reads back what it has copied itself), codes into
-// the swizzled rows of the A operand, scales into the 512-byte blocks of the scale operand.
-// Rows beyond the segment's: zeros.
+// q~ of a segment by 128 threads, thread t taking block t % (D/16) of every kStep-th row, four
+// rows' values on their way: codes into the swizzled rows of the A operand, scales into the
+// 512-byte blocks of the scale operand, of the two halves one after another.  Rows beyond the
+// segment's: zeros.
 template <int D>
 struct QueryTile {
   static constexpr int kBlocks = D / 16, kStep = 128 / kBlocks;
+  static constexpr int kAhead = 4;
+  uint4 lo[kAhead], hi[kAhead];
+  int tok, g, rows, step_t, step_g;  // the next row's token and query head; a step's
 
-  static __device__ __forceinline__ void fetch(const CrossArgs& a, const Walk& w, int row0,
-                                               int rows, uint8_t* raw, int t) {
-    const int j = t % kBlocks, row = row0 + t / kBlocks;
-    int tok = row / a.G, g = row - tok * a.G;
-    const int step_t = kStep / a.G, step_g = kStep - step_t * a.G;
-    tok += w.e.tok0;
-#pragma unroll 1
-    for (int n = t / kBlocks; n < kRows; n += kStep) {
-      const uint16_t* src = a.q;
-      uint32_t bytes = 0;  // 0: filled with zeros, nothing is read
-      if (n < rows) {
-        src += tok * a.ld_q + static_cast<int64_t>(w.hk * a.G + g) * D + j * 16;
-        bytes = 16;
-      }
-      const uint32_t dst = smem_u32(raw) + n * (D * 2) + ((j ^ (n & (kBlocks - 1))) << 5);
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                   : "memory");
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 16), "l"(src + 8),
-                   "r"(bytes)
-                   : "memory");
-      tok += step_t;
-      if ((g += step_g) >= a.G) {
-        g -= a.G;
-        ++tok;
-      }
+  __device__ __forceinline__ void begin(const CrossArgs& a, const Walk& w, int t) {
+    rows = w.rows(a);
+    const int row = w.row0() + t / kBlocks;
+    tok = row / a.G;
+    g = row - tok * a.G;
+    step_t = kStep / a.G;
+    step_g = kStep - step_t * a.G;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) load(a, w, t, t / kBlocks + u * kStep, lo[u], hi[u]);
+  }
+  __device__ __forceinline__ void load(const CrossArgs& a, const Walk& w, int t, int n, uint4& lo,
+                                       uint4& hi) {
+    lo = hi = make_uint4(0, 0, 0, 0);
+    if (n < rows) {
+      const uint16_t* src = a.q + (w.e.tok0 + tok) * a.ld_q +
+                            static_cast<int64_t>(w.hk * a.G + g) * D + t % kBlocks * 16;
+      lo = ld16(src);
+      hi = ld16(src + 8);
+    }
+    tok += step_t;
+    if ((g += step_g) >= a.G) {
+      g -= a.G;
+      ++tok;
     }
   }
-  static __device__ __forceinline__ void quantize(const uint8_t* raw, uint8_t* codes,
-                                                  uint8_t* scales, int t) {
-    const int j = t % kBlocks;
-    asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 2
-    for (int n = t / kBlocks; n < kRows; n += kStep) {
-      const uint4* src =
-          reinterpret_cast<const uint4*>(raw + n * (D * 2) + ((j ^ (n & (kBlocks - 1))) << 5));
-      const uint4 lo = src[0], hi = src[1];
-      const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-      const Codes16 r = codes16_unit(v);
-      const int swz = D == 128 ? (n >> 1) & 3 : (n >> 2) & 1;  // 64- and 32-byte swizzles
-      *reinterpret_cast<uint2*>(codes + n * (D / 2) + (((j >> 1) ^ swz) << 4) + (j & 1) * 8) =
-          make_uint2(r.codes[0], r.codes[1]);
-      scales[(j >> 2) * 512 + (n & 31) * 16 + (n >> 5) * 4 + (j & 3)] =
-          static_cast<uint8_t>(r.sbyte);
+  __device__ __forceinline__ void quantize(const CrossArgs& a, const Walk& w, uint8_t* codes,
+                                           uint8_t* scales, int t) {
+    const int j = t % kBlocks, end = rows > kRows ? kPair : kRows;
+#pragma unroll 1
+    for (int n0 = t / kBlocks; n0 < end; n0 += kAhead * kStep) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int n = n0 + u * kStep;
+        const uint32_t v[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w,
+                               hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+        load(a, w, t, n + kAhead * kStep, lo[u], hi[u]);
+        const Codes16 r = codes16_unit(v);
+        const int swz = D == 128 ? (n >> 1) & 3 : (n >> 2) & 1;  // 64- and 32-byte swizzles
+        // the halves' codes and scales lie one behind the other
+        *reinterpret_cast<uint2*>(codes + n * (D / 2) + (((j >> 1) ^ swz) << 4) + (j & 1) * 8) =
+            make_uint2(r.codes[0], r.codes[1]);
+        scales[(n >> 7) * (D / 64 * 512) + (j >> 2) * 512 + (n & 31) * 16 + (n >> 5 & 3) * 4 +
+               (j & 3)] = static_cast<uint8_t>(r.sbyte);
+      }
     }
   }
 };
@@ -376,6 +424,15 @@ __device__ __forceinline__ void umma_f16_ts4_w(uint32_t d, uint32_t a, uint64_t 
       : "memory");
 }
 
+// Contiguous copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) from shared to
+// global memory, in this thread's bulk group.
+__device__ __forceinline__ void bulk_store(void* dst, const void* smem_src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                   reinterpret_cast<uint64_t>(dst)),
+               "r"(smem_u32(smem_src)), "r"(bytes)
+               : "memory");
+}
+
 // What is written as a row's lse: the natural logarithm, or base 2 beside an output in fp32.
 __device__ __forceinline__ float row_lse(const CrossArgs& a, float m, float l) {
   if (!(l > 0.f)) return -INFINITY;
@@ -435,8 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int64_t warp_sum[kThreads / 32];
-  __shared__ int64_t start_before;
-  __shared__ int start_s;
+  __shared__ Start start;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -445,16 +501,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   Tile* desc = reinterpret_cast<Tile*>(smem + C::kDescAt);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarAt);
   uint64_t* empty = full + C::kStages;   // S and the PV, decode and softmax warps done with it
-  uint64_t* v_full = empty + C::kStages;  // [2], four decode warps
+  uint64_t* k_ready = empty + C::kStages;  // K's scales in order
+  uint64_t* v_full = k_ready + C::kStages;  // [2], four decode warps
   uint64_t* v_empty = v_full + 2;         // [2]
   uint64_t* q_full = v_empty + 2;         // [2], four query warps
   uint64_t* q_empty = q_full + 2;         // [2]
-  uint64_t* s_full = q_empty + 2;         // [2 halves][3], by the units of the half
+  uint64_t* s_full = q_empty + 2;         // [2 streams][3], by the units of the stream
   uint64_t* p_full = s_full + 6;          // [3] by the unit's buffer, four softmax warps
   uint64_t* pv_done = p_full + 3;         // [3]
-  uint64_t* o_full = pv_done + 3;         // [2 halves]: a segment's last PV is done
-  uint64_t* o_read = o_full + 2;          // [2 halves], four softmax warps
+  uint64_t* o_full = pv_done + 3;         // [2 streams]: a segment's last PV is done
+  uint64_t* o_read = o_full + 2;          // [2 streams], four softmax warps (of either stream)
   uint64_t* drain = o_read + 2;           // [2]
+  uint64_t* merge = drain + 2;            // [4]: by 32 rows, the other keys' sums are done
+  uint64_t* described = merge + 4;        // [kSegs]
+  Segment* segs = reinterpret_cast<Segment*>(smem + C::kSegAt);
+  float2* ml = reinterpret_cast<float2*>(smem + C::kMlAt);
   const uint32_t abort = smem_u32(&abort_word);
   pdl_trigger();
 
@@ -463,6 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1 + 1 + 4 + 8);
+      mbar_init(&k_ready[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&v_full[i], 4);
@@ -479,9 +541,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&merge[i], 1);
+    for (int i = 0; i < kSegs; ++i) mbar_init(&described[i], 1);
     fence_mbar_init();
   }
-  if (warp == kSWarp) {
+  if (warp == kScaleWarp) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
     tma_prefetch_desc(&tk);
@@ -491,10 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = (a.B + kThreads - 1) / kThreads;
   const int s_lo = min(a.B, static_cast<int>(threadIdx.x) * per), s_hi = min(a.B, s_lo + per);
   int64_t mine = 0;
+  Extent e{};
 #pragma unroll 1
   for (int s = s_lo; s < s_hi; ++s) {
     bool bad;
-    const Extent e = extent(a, s, &bad);
+    e = extent(a, s, &bad);
     mine += static_cast<int64_t>(e.row_tiles) * e.key_tiles * a.Hkv;
     if (bad && blockIdx.x == 0) atomicMax(a.err, kErrTable);
   }
@@ -507,29 +572,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (lane == 31) warp_sum[warp] = scan;
   __syncthreads();
   int64_t all = 0;
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) scan += warp_sum[w];
     all += warp_sum[w];
   }
   const int64_t before = scan - mine;  // tiles before this thread's sequences
   const int run = blockIdx.x;
-  // all < 2^35 (check_cross), runs < 2^10: no overflow
-  const int64_t n_runs = all < a.runs ? all : a.runs;
-  const int64_t u0 = run < n_runs ? all * run / n_runs : all;
-  const int64_t u1 = run < n_runs ? all * (run + 1) / n_runs : all;
+  const Runs line(all, a.runs, a.runs_magic);
+  const int64_t u0 = line.begin(run), u1 = line.begin(run + 1);
   if (mine > 0 && before <= u0 && u0 < before + mine) {
     int64_t at = before;
     int s = s_lo;
+    if (per > 1) {
 #pragma unroll 1
-    for (;; ++s) {
-      bool bad;
-      const Extent e = extent(a, s, &bad);
-      const int64_t n = static_cast<int64_t>(e.row_tiles) * e.key_tiles * a.Hkv;
-      if (u0 < at + n) break;
-      at += n;
+      for (;; ++s) {
+        bool bad;
+        e = extent(a, s, &bad);
+        const int64_t n = static_cast<int64_t>(e.row_tiles) * e.key_tiles * a.Hkv;
+        if (u0 < at + n) break;
+        at += n;
+      }
     }
-    start_s = s;
-    start_before = at;
+    int64_t nth;  // segment of the sequence
+    int i;
+    if (u0 - at < (int64_t{1} << 31)) {
+      nth = static_cast<uint32_t>(u0 - at) / static_cast<uint32_t>(e.key_tiles);
+    } else {
+      nth = (u0 - at) / e.key_tiles;
+    }
+    i = static_cast<int>(u0 - at - nth * e.key_tiles);
+    const int hk = static_cast<int>(nth / e.row_tiles);
+    start = {at, e, s, hk, static_cast<int>(nth - static_cast<int64_t>(hk) * e.row_tiles), i};
   }
   tc_fence_before();
   __syncthreads();
@@ -539,79 +613,61 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) a.split[run].last = -1;
-    if (n_tiles > 0) {
-      bool ok = true;
-      int n = 0;
-      Tile td;
-      td.seg = 0;
-      Ring ring;
-      Walk w(a, start_s, start_before, u0, n_tiles);
-      do {
-        const bool whole = w.first >= u0 && w.first + w.e.key_tiles <= u1;
-        td.row0 = w.row0();
-        td.rows = w.rows(a);
-        td.tok0 = w.e.tok0;
-        td.hk = w.hk;
-        // a part that begins with the run goes to the run's slot 0, one inside it to slot 1
-        td.slot = whole ? -1 : 2 * run + (w.first > u0 ? 1 : 0);
-        const int32_t* table = a.table + w.s * a.ld_table;
-        int pages = 0;  // this lane's page number: of tile i0 + 32 k + lane
+    bool ok = true;
+    int n = 0;
+    Ring ring;
 #pragma unroll 1
-        for (int i = w.i; i < w.i_end; ++i, ++n, ring.next(C::kStages)) {
-          if (((i - w.i) & 31) == 0) {
-            const int x = i + lane;
-            pages = x < w.e.key_tiles ? table[x] : -1;
-          }
-          const int page = __shfl_sync(0xFFFFFFFFu, pages, (i - w.i) & 31);
-          const bool there = page >= 0 && page < a.num_pages;
-          td.flags = (i == w.i ? kStart : 0) | (i == w.i_end - 1 ? kEnd : 0) |
-                     (there ? 0 : kAbsent) | (td.rows > kRows ? kBoth : 0);
-          td.valid = there ? min(kPage, w.e.len - i * kPage) : 0;
-          if (!there && lane == 0) atomicMax(a.err, kErrTable);
-          const int st = ring.s;
-          if (!(ok = wait(&empty[st], ring.phase ^ 1, abort))) break;
-          if (lane == 0) desc[st] = td;
-          __syncwarp();
-          uint8_t* dst = smem + st * C::kRec;
-          if (there) {
-            const int rec = page * a.Hkv + w.hk;
-            mbar_arrive_expect_tx_w(&full[st], C::kRec);
-            tma_load_4d_w(dst, &tk, 0, 0, rec, 0, &full[st]);
-            bulk_load_w(dst + v_codes_at(D),
-                        a.pool + static_cast<int64_t>(rec) * record_bytes(D) + v_codes_at(D),
-                        C::kRec - v_codes_at(D), &full[st]);
-          } else {
-            mbar_arrive_expect_tx_w(&full[st], 0);
-          }
-        }
-        if (lane == 0 && w.first >= u0 && w.first + w.e.key_tiles > u1) {
-          // the run that holds tile u: the last c with all c / n_runs <= u
-          const int64_t u = w.first + w.e.key_tiles - 1;
-          a.split[run] = {run, static_cast<int>(((u + 1) * n_runs + all - 1) / all - 1), td.slot,
-                          td.rows, td.row0, td.tok0, td.hk, 0};
-        }
-        ++td.seg;
-      } while (ok && w.next(a));
-      if (!ok) {  // let the copies already issued land before the block leaves
+    for (int seg = 0; n < n_tiles && ok; ++seg) {
+      if (!(ok = wait(&described[seg % kSegs], (seg / kSegs) & 1, abort))) break;
+      const Segment& sg = segs[seg % kSegs];
+      const int hk = sg.hk, len = sg.len, i0 = sg.i, i_end = sg.i_end;
+      const int32_t* table = a.table + sg.s * a.ld_table;
+      Tile td{0, 0, sg.rows, seg};
+      int pages = 0;  // this lane's page number: of tile i0 + 32 k + lane
 #pragma unroll 1
-        for (int m = max(0, n - C::kStages); m < n; ++m)
-          mbar_wait_warp(&full[m % C::kStages], (m / C::kStages) & 1, nullptr, 10000000ull);
+      for (int i = i0; i < i_end; ++i, ++n, ring.next(C::kStages)) {
+        if (((i - i0) & 31) == 0) pages = i + lane < i_end ? table[i + lane] : -1;
+        const int page = __shfl_sync(0xFFFFFFFFu, pages, (i - i0) & 31);
+        const bool there = page >= 0 && page < a.num_pages;
+        td.flags = (i == i0 ? kStart : 0) | (i == i_end - 1 ? kEnd : 0) | (there ? 0 : kAbsent) |
+                   (td.rows > kRows ? kBoth : 0);
+        td.valid = there ? min(kPage, len - i * kPage) : 0;
+        if (!there && lane == 0) atomicMax(a.err, kErrTable);
+        const int st = ring.s;
+        if (!(ok = wait(&empty[st], ring.phase ^ 1, abort))) break;
+        if (lane == 0) desc[st] = td;
+        __syncwarp();
+        uint8_t* dst = smem + st * C::kRec;
+        if (there) {
+          const int rec = page * a.Hkv + hk;
+          mbar_arrive_expect_tx_w(&full[st], C::kRec);
+          tma_load_4d_w(dst, &tk, 0, 0, rec, 0, &full[st]);
+          bulk_load_w(dst + v_codes_at(D),
+                      a.pool + static_cast<int64_t>(rec) * record_bytes(D) + v_codes_at(D),
+                      C::kRec - v_codes_at(D), &full[st]);
+        } else {
+          mbar_arrive_expect_tx_w(&full[st], 0);
+        }
       }
+    }
+    if (!ok) {  // let the copies already issued land before the block leaves
+#pragma unroll 1
+      for (int m = max(0, n - C::kStages); m < n; ++m)
+        mbar_wait_warp(&full[m % C::kStages], (m / C::kStages) & 1, nullptr, 10000000ull);
     }
   } else if (warp == kSWarp) {
     // ------------------------------------------------------------ S = Q~ K~^T
     constexpr uint32_t idesc = idesc_mxf4nvf4(kRows, kKeys);
     constexpr uint32_t lay = D == 128 ? 4u : 6u, sbo = 4 * D;  // swizzle, bytes of 8 rows
     Ring ring, unit;
-    int done[2] = {0, 0};  // units of the halves so far, modulo 3
+    int done = 0;  // units of a stream so far, modulo 3
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; n < n_tiles && ok; ++n, ring.next(C::kStages)) {
       const int st = ring.s;
-      if (!wait(&full[st], ring.phase, abort)) break;
+      if (!wait(&k_ready[st], ring.phase, abort)) break;
       const int flags = uniform(desc[st].flags), seg = uniform(desc[st].seg);
-      const int qb = seg & 1, halves = flags & kBoth ? 2 : 1;
+      const int qb = seg & 1, halves = flags & kBoth ? 2 : 1;  // of the rows
       if ((flags & kStart) && !wait(&q_full[qb], (seg >> 1) & 1, abort)) break;
       tc_fence_after();
       const uint32_t sfq = tmem + kSfQ + 16 * qb, sfk = tmem + kSfK + 8 * (n & 3);
@@ -626,16 +682,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                               smem_u32(smem + C::kQScAt + 2 * qb * C::kQSc) + 512 * k);
       }
       if (!(flags & kAbsent)) {
-        arrange_scales<D>(stage + k_scales_at(D), lane);
-        fence_proxy_async_smem();
-        __syncwarp();
 #pragma unroll
         for (int k = 0; k < D / 64; ++k)
           tmem_cp_32x128_x4_w(sfk + 4 * k, smem_u32(stage + k_scales_at(D)) + 512 * k);
       }
 #pragma unroll 1
       for (int u = 0; u < 2 * halves; ++u, unit.next(3)) {
-        const int key = halves == 2 ? u >> 1 : u, half = halves == 2 ? u & 1 : 0;
+        const int stream = u & 1, key = halves == 2 ? u >> 1 : u, half = halves == 2 ? stream : 0;
         const bool last = u == 2 * halves - 1;
         const uint32_t qa = smem_u32(smem + C::kQAt + (2 * qb + half) * C::kQ);
         const uint32_t ka = smem_u32(stage) + key * (kKeys * D / 2);
@@ -644,9 +697,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the buffer is free when the PV of the unit three before has read the P over it
         if (!(ok = wait(&pv_done[unit.s], unit.phase ^ 1, abort))) break;
         tc_fence_after();
-        uint64_t* const ready = &s_full[half == 0 ? done[0] : 3 + done[1]];
-        if (half == 0) done[0] = done[0] == 2 ? 0 : done[0] + 1;
-        else done[1] = done[1] == 2 ? 0 : done[1] + 1;
+        uint64_t* const ready = &s_full[3 * stream + done];
+        if (stream == 1) done = done == 2 ? 0 : done + 1;
         if (!(flags & kAbsent)) {
           umma_fp4_group_w<D / 64>(tmem + 64 * unit.s, qd, kd, idesc, sfq + 8 * half, sfk + 2 * key,
                                    bar_u32(ready), last ? bar_u32(&empty[st]) : 0u);
@@ -659,12 +711,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     umma_commit_w(&drain[0]);  // the MMAs in flight end before the block
     mbar_wait_warp(&drain[0], 0, nullptr, 10000000ull);
+  } else if (warp == kScaleWarp) {
+    // ------------------------------------------------------------ scales of K
+    Ring ring;
+#pragma unroll 1
+    for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
+      if (!wait(&full[ring.s], ring.phase, abort)) break;
+      if (!(desc[ring.s].flags & kAbsent)) {
+        arrange_scales<D>(smem + ring.s * C::kRec + k_scales_at(D), lane);
+        fence_proxy_async_smem();
+      }
+      mbar_arrive_warp(&k_ready[ring.s]);
+    }
   } else if (warp == kPvWarp) {
     // ------------------------------------------------------------ O += P V~
     constexpr uint32_t idesc = idesc_f16(kRows, D, 0, 0, 1);
     const uint64_t v_d0 = sdesc_sw128(smem_u32(smem + C::kVAt), kRows * 128, 1024);
     Ring ring, unit;
-    int seg_b = 0;  // segments of both halves so far
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; n < n_tiles && ok; ++n, ring.next(C::kStages)) {
@@ -676,20 +739,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&v_full[b], (n >> 1) & 1, abort)) break;
 #pragma unroll 1
       for (int u = 0; u < 2 * halves; ++u, unit.next(3)) {
-        const int key = halves == 2 ? u >> 1 : u, half = halves == 2 ? u & 1 : 0;
-        const bool first = (flags & kStart) && key == 0;
-        // O of the half's segment before has been read
-        if (first) {
-          const int before = half == 0 ? seg : seg_b++;
-          if (before > 0 && !(ok = wait(&o_read[half], (before - 1) & 1, abort))) break;
-        }
+        const int stream = u & 1, key = halves == 2 ? u >> 1 : u;
+        const bool first = (flags & kStart) && u < 2;
+        // O of the stream's segment before has been read
+        if (first && seg > 0 && !(ok = wait(&o_read[stream], (seg - 1) & 1, abort))) break;
         if (!(ok = wait(&p_full[unit.s], unit.phase, abort))) break;
         tc_fence_after();
-        umma_f16_ts4_w(tmem + kO + D * half, tmem + 64 * unit.s,
+        umma_f16_ts4_w(tmem + kO + D * stream, tmem + 64 * unit.s,
                        v_d0 + static_cast<uint64_t>(b) * (C::kV >> 4) + 512 * key, idesc,
                        first ? 0u : 1u, bar_u32(&pv_done[unit.s]),
                        u == 2 * halves - 1 ? bar_u32(&v_empty[b]) : 0u);
-        if ((flags & kEnd) && key == 1) umma_commit_w(&o_full[half]);
+        if ((flags & kEnd) && u >= 2 * halves - 2) umma_commit_w(&o_full[stream]);
       }
     }
     umma_commit_w(&drain[1]);
@@ -710,18 +770,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kDecodeWarp) {
     // ------------------------------------------------------------ softmax
-    const int half = warp >> 2, quarter = warp & 3;
-    const int r = threadIdx.x;  // row of the segment; r % 128: lane of tensor memory
+    const int stream = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t o_at = lanes + kO + D * half;
+    const uint32_t o_at = lanes + kO + D * stream;
     const uint64_t scale2 = pk2(a.scale_log2, a.scale_log2);
     float m = -INFINITY;  // reference maximum (log2 units)
     uint64_t l2 = pk2(0.f, 0.f);
-    uint32_t unit0 = 0;   // units before this tile
-    uint32_t ends = 0;    // segments of this half before this one
+    uint32_t u = stream;  // its units are every other one
+    uint32_t ends = 0, joins = 0;  // segments, and those whose keys were shared, so far
     bool ok = true;
-    // s_full is the half's own: a half that has nothing to do for a while would miss phases of a
-    // barrier that both share, and take an older one's end for the one it waits for
+    // s_full is the stream's own: a barrier of both would be phases ahead or behind of one of them,
+    // whose parity would tell it of an older phase's end
     Ring ring, mine_full;
 #pragma unroll 1
     for (int n = 0; n < n_tiles && ok; ++n, ring.next(C::kStages)) {
@@ -730,24 +789,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // would be spilled, to a cache that shared memory leaves next to nothing of
       const Tile* const td = &desc[ring.s];
       const int flags = td->flags;
-      const uint32_t halves = flags & kBoth ? 2 : 1;
-      uint32_t u = unit0 + half;
-      unit0 += 2 * halves;
-      if (half == 1 && halves == 1) {
-        mbar_arrive_warp(&empty[ring.s]);
-        continue;
-      }
-      const int all_valid = td->valid;
-      const bool live = 32 * warp < td->rows;  // else: rows that nobody reads
-      if (flags & kStart) {
+      const bool both = flags & kBoth;
+      int valid = td->valid - (both ? 0 : kKeys * stream);
+      const bool live = 32 * (both ? warp : quarter) < td->rows;  // else: rows that nobody reads
+      bool first = flags & kStart;
+      if (first) {
         m = -INFINITY;
         l2 = pk2(0.f, 0.f);
       }
 #pragma unroll 1
-      for (int key = 0; key < 2; ++key, u += halves, mine_full.next(3)) {
+      for (int left = both ? 2 : 1; left > 0;
+           --left, u += 2, valid -= kKeys, first = false, mine_full.next(3)) {
         const uint32_t buf = u % 3;
-        const int valid = all_valid - kKeys * key;
-        if (!(ok = wait(&s_full[3 * half + mine_full.s], mine_full.phase, abort))) break;
+        if (!(ok = wait(&s_full[3 * stream + mine_full.s], mine_full.phase, abort))) break;
         tc_fence_after();
         const uint32_t s_at = lanes + 64 * buf;
         if (live) {
@@ -782,10 +836,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float c = grows ? ex2_f32(m - mx) : 1.f;
             if (grows) m = mx;
             l2 = mul2(l2, pk2(c, c));
-            // raised behind the segment's first unit: O so far, which the half's PV before has
+            // raised behind the segment's first unit: O so far, which the stream's PV before has
             // finished
-            if (!(flags & kStart) || key > 0) {
-              const uint32_t w = u - halves;
+            if (!first) {
+              const uint32_t w = u - 2;
               if (!(ok = wait(&pv_done[w % 3], (w / 3) & 1, abort))) break;
               tc_fence_after();
 #pragma unroll 1
@@ -818,20 +872,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       // ---- the segment's end
-      if (!wait(&o_full[half], ends++ & 1, abort)) break;
+      if (!wait(&o_full[stream], ends++ & 1, abort)) break;
       tc_fence_after();
       float l0, l1;
       up2(l2, l0, l1);
-      const float l = l0 + l1;
-      const bool mine = r < td->rows;
-      const int slot = td->slot, row = td->row0 + r, tok = row / a.G;
-      const int64_t at =
-          static_cast<int64_t>(td->tok0 + tok) * a.H + td->hk * a.G + row - tok * a.G;
+      float l = l0 + l1, own = 1.f, other = 0.f;
+      const int r = both ? threadIdx.x : threadIdx.x & (kRows - 1);  // row of the segment
+      const Segment& sg = segs[td->seg % kSegs];
+      const bool mine = r < sg.rows;
+      const int slot = sg.slot, row = sg.row0 + r, tok = row / a.G;
+      const int64_t at = static_cast<int64_t>(sg.tok0 + tok) * a.H + sg.hk * a.G + row - tok * a.G;
       mbar_arrive_warp(&empty[ring.s]);
-      const float f = slot >= 0 ? 1.f : l > 0.f ? __fdividef(1.f, l) : 0.f;
+      if (!both && stream == 1) {  // the warp that has the other keys of these rows takes both
+        if (live) ml[r] = make_float2(m, l);
+        mbar_arrive_warp(&merge[quarter]);
+        continue;
+      }
+      if (!both) {
+        if (!wait(&merge[quarter], joins++ & 1, abort)) break;
+        tc_fence_after();
+        const float2 v = ml[r];
+        const float top = fmaxf(m, v.x), ref = fmaxf(top, -3.4e38f);
+        own = ex2_f32(m - ref);
+        other = ex2_f32(v.x - ref);
+        l = fmaf(l, own, v.y * other);
+        m = top;
+      }
+      if (slot < 0) {
+        const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
+        own *= inv;
+        other *= inv;
+      }
       float* part = a.parts + max(slot, 0) * part_floats(a.part_rows, D);
       __nv_bfloat16* out16 = slot < 0 && a.o != nullptr ? a.o + at * D : nullptr;
       float* out32 = slot < 0 ? a.o32 + at * D : part + 2 * a.part_rows + r * D;
+      // rows go out by bulk copies, a thread's own each (stores of 16 bytes a row kept the warps
+      // for 9000 cycles a segment, more than two tiles' softmax): all of a bf16 row, or one half
+      // after the other of one in fp32
+      uint8_t* const staged = smem + C::kOutAt + threadIdx.x * C::kOutRow;
+      bulk_wait_group_read<0>();
       if (live) {
 #pragma unroll 1
         for (int x = 0; x < D; x += 16) {
@@ -840,24 +919,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld16(o_at + x, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-          if (!mine) {
-          } else if (out16 != nullptr) {
-            uint4* dst = reinterpret_cast<uint4*>(out16 + x);
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * own);
+          if (!both) {
+            uint32_t z[16];
+            tmem_ld16(o_at + D + x, z);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              v[i] = __float_as_uint(
+                  fmaf(__uint_as_float(z[i]), other, __uint_as_float(v[i])));
+          }
+          if (out16 != nullptr) {
+            uint4* dst = reinterpret_cast<uint4*>(staged + 2 * x);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
               dst[i] = make_uint4(pack_bf16(v + 8 * i), pack_bf16(v + 8 * i + 2),
                                   pack_bf16(v + 8 * i + 4), pack_bf16(v + 8 * i + 6));
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(out32 + x);
+            uint4* dst = reinterpret_cast<uint4*>(staged + 4 * (x % (D / 2)));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            if (x == D / 2 - 16) {
+              fence_proxy_async_smem();
+              if (mine) bulk_store(out32, staged, 2 * D);
+              bulk_commit_group();
+              bulk_wait_group_read<0>();
+            }
           }
         }
       }
       tc_fence_before();
-      mbar_arrive_warp(&o_read[half]);
+      mbar_arrive_warp(&o_read[stream]);
+      if (!both) mbar_arrive_warp(&o_read[1]);
+      fence_proxy_async_smem();
+      if (mine) {
+        if (out16 != nullptr) bulk_store(out16, staged, 2 * D);
+        else bulk_store(out32 + D / 2, staged, 2 * D);
+      }
+      bulk_commit_group();
       if (mine) {
         if (slot >= 0)
           *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
@@ -865,58 +965,68 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.lse[at] = row_lse(a, m, l);
       }
     }
+    bulk_wait_group<0>();
   } else if (warp >= kQWarp && warp < kProducerWarp) {
     // ------------------------------------------------------------ q~
+    const int t = threadIdx.x - 32 * kQWarp;
+    if (t == 0) a.split[run].end = -1;
     if (n_tiles > 0) {
-      const int t = threadIdx.x - 32 * kQWarp;
-      Walk w(a, start_s, start_before, u0, n_tiles);
-      int seg = 0;
+      Walk w(start, n_tiles);
       bool ok = true;
-      do {
-        const int qb = seg & 1, rows = w.rows(a);
+      int seg = 0;
 #pragma unroll 1
-        for (int half = 0; half < (rows > kRows ? 2 : 1) && ok; ++half) {
-          QueryTile<D>::fetch(a, w, w.row0() + half * kRows, rows - half * kRows, smem + C::kRawAt,
-                              t);
-          if (half == 0) ok = wait(&q_empty[qb], ((seg >> 1) & 1) ^ 1, abort);
-          if (ok)
-            QueryTile<D>::quantize(smem + C::kRawAt, smem + C::kQAt + (2 * qb + half) * C::kQ,
-                                   smem + C::kQScAt + (2 * qb + half) * C::kQSc, t);
+      do {
+        if (t == 0) {
+          const bool begins = w.first >= u0, ends = w.first + w.e.key_tiles <= u1;
+          // a part that begins with the run goes to the run's slot 0, one inside it to slot 1
+          const int slot = begins && ends ? -1 : 2 * run + (w.first > u0 ? 1 : 0);
+          segs[seg % kSegs] = {w.row0(), w.rows(a), w.e.tok0, w.hk, slot,
+                               w.s, w.i, w.i_end, w.e.len, {0, 0, 0}};
+          mbar_arrive(&described[seg % kSegs]);
+          if (begins && !ends)
+            a.split[run] = {w.first + w.e.key_tiles - 1, all, slot, w.rows(a), w.row0(), w.e.tok0,
+                            w.hk, 0};
         }
+        __syncwarp();
+        QueryTile<D> q;
+        q.begin(a, w, t);
+        const int qb = seg & 1;
+        if (!(ok = wait(&q_empty[qb], ((seg >> 1) & 1) ^ 1, abort))) break;
+        q.quantize(a, w, smem + C::kQAt + 2 * qb * C::kQ, smem + C::kQScAt + 2 * qb * C::kQSc, t);
         fence_proxy_async_smem();
         mbar_arrive_warp(&q_full[qb]);
         ++seg;
-      } while (ok && w.next(a));
+      } while (w.next(a));
     }
     // ---- rows without keys, rows outside of all sequences
     const int first = 4 * run + warp - kQWarp, step = 4 * static_cast<int>(gridDim.x);
 #pragma unroll 1
     for (int s0 = 0; s0 < a.B; s0 += 32) {
       bool bad;
-      Extent e{0, 0, 0, 0, 1};
-      if (s0 + lane < a.B) e = extent(a, s0 + lane, &bad);
-      uint32_t none = __ballot_sync(0xFFFFFFFFu, e.toks > 0 && e.key_tiles == 0);
+      Extent x{0, 0, 0, 0, 1};
+      if (s0 + lane < a.B) x = extent(a, s0 + lane, &bad);
+      uint32_t none = __ballot_sync(0xFFFFFFFFu, x.toks > 0 && x.key_tiles == 0);
+#pragma unroll 1
       for (; none != 0; none &= none - 1) {
         const int i = __ffs(none) - 1;
-        const int tok0 = __shfl_sync(0xFFFFFFFFu, e.tok0, i), toks = __shfl_sync(0xFFFFFFFFu, e.toks, i);
+        const int tok0 = __shfl_sync(0xFFFFFFFFu, x.tok0, i), toks = __shfl_sync(0xFFFFFFFFu, x.toks, i);
 #pragma unroll 1
-        for (int t = first; t < toks; t += step) empty_token<D>(a, tok0 + t, lane);
+        for (int64_t z = first; z < toks; z += step) empty_token<D>(a, tok0 + static_cast<int>(z), lane);
       }
     }
     if (a.cu != nullptr) {
       const int lo = min(max(a.cu[0], 0), a.T), hi = min(max(a.cu[a.B], 0), a.T);
+      // rows [0, lo) and [hi, T), as one run of rows
 #pragma unroll 1
-      for (int t = first; t < lo; t += step) empty_token<D>(a, t, lane);
-#pragma unroll 1
-      for (int64_t t = static_cast<int64_t>(hi) + first; t < a.T; t += step)
-        empty_token<D>(a, static_cast<int>(t), lane);
+      for (int64_t z = first; z < static_cast<int64_t>(lo) + a.T - hi; z += step)
+        empty_token<D>(a, static_cast<int>(z < lo ? z : z - lo + hi), lane);
     }
   }
 
   tc_fence_before();
   __syncthreads();
   report_abort(&abort_word, a.err);
-  if (warp == kSWarp) {
+  if (warp == kScaleWarp) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -931,27 +1041,30 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a) {
   pdl_trigger();
   pdl_wait();
   const Split s = a.split[blockIdx.x];
-  // last < 0: nothing to join; what else is out of range was never written, by a kernel that gave
+  const int run = blockIdx.x;
+  // end < 0: nothing to join; what else is out of range was never written, by a kernel that gave
   // up a wait and has reported it
-  if (s.run != static_cast<int>(blockIdx.x) || s.last < s.run || s.last >= a.runs || s.slot < 0 ||
-      s.slot >= 2 * a.runs || s.rows > a.part_rows)
+  if (s.end < 0 || s.all <= s.end || s.slot < 0 || s.slot >= 2 * a.runs || s.rows > a.part_rows)
     return;
+  // the run that holds tile u: the last c with all c / n <= u
+  const int64_t n_runs = s.all < a.runs ? s.all : a.runs;
+  const int last = static_cast<int>(((s.end + 1) * n_runs + s.all - 1) / s.all - 1);
   const int r = (blockIdx.y * 256 + threadIdx.x) / kLanes, x = threadIdx.x % kLanes;
   if (r >= s.rows) return;
   const int64_t stride = part_floats(a.part_rows, D);
   float mx = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   // loads of a few parts in flight: one after another they cost a memory latency each
-  for (int c0 = s.run; c0 <= s.last; c0 += kBatch) {
+  for (int c0 = run; c0 <= last; c0 += kBatch) {
     float2 ml[kBatch];
     float4 po[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int c = min(c0 + i, s.last);
-      const float* part = a.parts + (c == s.run ? s.slot : 2 * c) * stride;
+      const int c = min(c0 + i, last);
+      const float* part = a.parts + (c == run ? s.slot : 2 * c) * stride;
       ml[i] = *reinterpret_cast<const float2*>(part + 2 * r);
       po[i] = *reinterpret_cast<const float4*>(part + 2 * a.part_rows + r * D + 4 * x);
-      if (c0 + i > s.last) ml[i] = make_float2(-INFINITY, 0.f);
+      if (c0 + i > last) ml[i] = make_float2(-INFINITY, 0.f);
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -1038,8 +1151,9 @@ nvq_status launch_cross(const CrossCall& c, uint8_t* ws, cudaStream_t stream) {
                     static_cast<const uint8_t*>(c.pool), c.num_pages, c.page_table, c.ld_table,
                     c.max_pages, c.kv_lens, c.cu_tokens, static_cast<int>(c.T / c.B), c.B, c.H,
                     c.Hkv, c.H / c.Hkv, c.scale * kLog2e, static_cast<__nv_bfloat16*>(c.o), c.o32,
-                    c.lse, reinterpret_cast<Split*>(ws), reinterpret_cast<float*>(ws + p.parts),
-                    p.part_rows, p.runs, err};
+                    c.lse, reinterpret_cast<Split*>(ws),
+                    reinterpret_cast<float*>(ws + p.parts),
+                    p.part_rows, p.runs, ~uint64_t{0} / p.runs + 1, err};
   const cudaError_t e = timed(NVQ_KERNEL_CROSS, stream, [&] {
     return c.D == 128 ? launch_cross_d<128>(tk, a, stream) : launch_cross_d<64>(tk, a, stream);
   });

@@ -61,6 +61,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kO = 192, kSfQ = 448, kSfK = 480;
 
 enum : int { kStart = 1, kEnd = 2, kAbsent = 4, kBoth = 8 };
+enum : int { kValid = 127, kUnitStart = 128, kUnitEnd = 256, kUnitLast = 512 };
 
 struct Tile {
   int flags, valid;  // kBoth: over 128 rows; keys of the page that hold tokens
@@ -82,7 +83,8 @@ struct Cfg {
   static constexpr uint32_t kMlAt = kOutAt + kPair * kOutRow;  // float2 [128]: the other keys' (m, l)
   static constexpr uint32_t kDescAt = kMlAt + kRows * 8;
   static constexpr uint32_t kSegAt = kDescAt + kStages * 16;   // Segment [kSegs]
-  static constexpr uint32_t kBarAt = kSegAt + kSegs * 48;
+  static constexpr uint32_t kUnitAt = kSegAt + kSegs * 48;       // int [2 streams][3 (4)]
+  static constexpr uint32_t kBarAt = kUnitAt + 32;
   static constexpr int kBars = 3 * kStages + 4 * 2 + 4 * 3 + 3 * 2 + 4 + kSegs;
   // heads of 64: padded so that no CTA of the few-rows linear lies beside one
   static constexpr uint32_t kUsed = kBarAt + kBars * 8 + 1024;
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~static_cast<uintptr_t>(1023u));
   Tile* desc = reinterpret_cast<Tile*>(smem + C::kDescAt);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarAt);
-  uint64_t* empty = full + C::kStages;   // S and the PV, decode and softmax warps done with it
+  uint64_t* empty = full + C::kStages;   // S and the PV and decode warps done with it
   uint64_t* k_ready = empty + C::kStages;  // K's scales in order
   uint64_t* v_full = k_ready + C::kStages;  // [2], four decode warps
   uint64_t* v_empty = v_full + 2;         // [2]
@@ -515,6 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* merge = drain + 2;            // [4]: by 32 rows, the other keys' sums are done
   uint64_t* described = merge + 4;        // [kSegs]
   Segment* segs = reinterpret_cast<Segment*>(smem + C::kSegAt);
+  int* units = reinterpret_cast<int*>(smem + C::kUnitAt);  // as s_full: keys that hold tokens, flags
   float2* ml = reinterpret_cast<float2*>(smem + C::kMlAt);
   const uint32_t abort = smem_u32(&abort_word);
   pdl_trigger();
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_word = 0;
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1 + 1 + 4 + 8);
+      mbar_init(&empty[s], 1 + 1 + 4);
       mbar_init(&k_ready[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -536,8 +539,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&drain[i], 1);
     }
     for (int i = 0; i < 3; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_full[3 + i], 1);
+      mbar_init(&s_full[i], 2);  // the MMAs, and what the S warp tells of the unit
+      mbar_init(&s_full[3 + i], 2);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
     }
@@ -667,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int st = ring.s;
       if (!wait(&k_ready[st], ring.phase, abort)) break;
       const int flags = uniform(desc[st].flags), seg = uniform(desc[st].seg);
+      const int valid = desc[st].valid;
       const int qb = seg & 1, halves = flags & kBoth ? 2 : 1;  // of the rows
       if ((flags & kStart) && !wait(&q_full[qb], (seg >> 1) & 1, abort)) break;
       tc_fence_after();
@@ -694,11 +698,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ka = smem_u32(stage) + key * (kKeys * D / 2);
         const uint64_t qd[2] = {sdesc(qa, 16, sbo, lay), sdesc(qa, 16, sbo, lay) + 2};
         const uint64_t kd[2] = {sdesc(ka, 16, sbo, lay), sdesc(ka, 16, sbo, lay) + 2};
+        uint64_t* const ready = &s_full[3 * stream + done];
+        if (lane == 0)  // (the PV of the stream's unit three before is done: the word is free)
+          units[4 * stream + done] =
+              max(0, min(kKeys, valid - kKeys * key)) | ((flags & kStart) && u < 2 ? kUnitStart : 0) |
+              (u >= 2 * halves - 2 ? ((flags & kEnd) ? kUnitEnd : 0) | (n == n_tiles - 1 ? kUnitLast : 0)
+                                   : 0);
+        if (stream == 1) done = done == 2 ? 0 : done + 1;
         // the buffer is free when the PV of the unit three before has read the P over it
         if (!(ok = wait(&pv_done[unit.s], unit.phase ^ 1, abort))) break;
         tc_fence_after();
-        uint64_t* const ready = &s_full[3 * stream + done];
-        if (stream == 1) done = done == 2 ? 0 : done + 1;
         if (!(flags & kAbsent)) {
           umma_fp4_group_w<D / 64>(tmem + 64 * unit.s, qd, kd, idesc, sfq + 8 * half, sfk + 2 * key,
                                    bar_u32(ready), last ? bar_u32(&empty[st]) : 0u);
@@ -706,6 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit_w(ready);
           if (last) umma_commit_w(&empty[st]);
         }
+        mbar_arrive_warp(ready);
       }
       if (flags & kEnd) umma_commit_w(&q_empty[qb]);
     }
@@ -776,33 +786,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t scale2 = pk2(a.scale_log2, a.scale_log2);
     float m = -INFINITY;  // reference maximum (log2 units)
     uint64_t l2 = pk2(0.f, 0.f);
-    uint32_t u = stream;  // its units are every other one
+    uint32_t u = stream;           // its units are every other one
     uint32_t ends = 0, joins = 0;  // segments, and those whose keys were shared, so far
-    bool ok = true;
+    int rows = 0;                  // of the segment
+    int what = n_tiles > 0 ? 0 : kUnitLast;  // the S warp's word
     // s_full is the stream's own: a barrier of both would be phases ahead or behind of one of them,
     // whose parity would tell it of an older phase's end
-    Ring ring, mine_full;
+    Ring mine_full;
 #pragma unroll 1
-    for (int n = 0; n < n_tiles && ok; ++n, ring.next(C::kStages)) {
-      if (!wait(&full[ring.s], ring.phase, abort)) break;
-      // the description is read again where the segment ends: its fields held over the softmax
-      // would be spilled, to a cache that shared memory leaves next to nothing of
-      const Tile* const td = &desc[ring.s];
-      const int flags = td->flags;
-      const bool both = flags & kBoth;
-      int valid = td->valid - (both ? 0 : kKeys * stream);
-      const bool live = 32 * (both ? warp : quarter) < td->rows;  // else: rows that nobody reads
-      bool first = flags & kStart;
-      if (first) {
-        m = -INFINITY;
-        l2 = pk2(0.f, 0.f);
-      }
-#pragma unroll 1
-      for (int left = both ? 2 : 1; left > 0;
-           --left, u += 2, valid -= kKeys, first = false, mine_full.next(3)) {
+    for (; !(what & kUnitLast); u += 2, mine_full.next(3)) {
         const uint32_t buf = u % 3;
-        if (!(ok = wait(&s_full[3 * stream + mine_full.s], mine_full.phase, abort))) break;
+        if (!wait(&s_full[3 * stream + mine_full.s], mine_full.phase, abort)) break;
         tc_fence_after();
+        what = units[4 * stream + mine_full.s];
+        if (what & kUnitStart) {
+          m = -INFINITY;
+          l2 = pk2(0.f, 0.f);
+          rows = segs[ends % kSegs].rows;
+        }
+        const int valid = what & kValid;
+        const bool both = rows > kRows;
+        const bool live = 32 * (both ? warp : quarter) < rows;  // else: rows that nobody reads
         const uint32_t s_at = lanes + 64 * buf;
         if (live) {
           if (valid < kKeys) {  // keys behind the last: -inf, before S is read
@@ -838,9 +842,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             l2 = mul2(l2, pk2(c, c));
             // raised behind the segment's first unit: O so far, which the stream's PV before has
             // finished
-            if (!first) {
+            if (!(what & kUnitStart)) {
               const uint32_t w = u - 2;
-              if (!(ok = wait(&pv_done[w % 3], (w / 3) & 1, abort))) break;
+              if (!wait(&pv_done[w % 3], (w / 3) & 1, abort)) break;
               tc_fence_after();
 #pragma unroll 1
               for (int z = 0; z < D; z += 8) {
@@ -865,24 +869,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         mbar_arrive_warp(&p_full[buf]);
-      }
-      if (!ok) break;
-      if (!(flags & kEnd)) {
-        mbar_arrive_warp(&empty[ring.s]);
-        continue;
-      }
+      if (!(what & kUnitEnd)) continue;
       // ---- the segment's end
+      const Segment& sg = segs[ends % kSegs];
       if (!wait(&o_full[stream], ends++ & 1, abort)) break;
       tc_fence_after();
       float l0, l1;
       up2(l2, l0, l1);
       float l = l0 + l1, own = 1.f, other = 0.f;
       const int r = both ? threadIdx.x : threadIdx.x & (kRows - 1);  // row of the segment
-      const Segment& sg = segs[td->seg % kSegs];
-      const bool mine = r < sg.rows;
+      const bool mine = r < rows;
       const int slot = sg.slot, row = sg.row0 + r, tok = row / a.G;
       const int64_t at = static_cast<int64_t>(sg.tok0 + tok) * a.H + sg.hk * a.G + row - tok * a.G;
-      mbar_arrive_warp(&empty[ring.s]);
       if (!both && stream == 1) {  // the warp that has the other keys of these rows takes both
         if (live) ml[r] = make_float2(m, l);
         mbar_arrive_warp(&merge[quarter]);

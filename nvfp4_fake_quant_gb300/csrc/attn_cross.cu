@@ -15,19 +15,19 @@
 // One CTA, twenty warps:
 //   producer   K codes by tensor-map loads with the swizzle the MMA reads, the record's rest
 //              by bulk copies, into a ring of stages, with a description of each tile
-//   scales     K's scales into the scale operand's order
-//   S          S = Q~ K~^T as block-scaled FP4 tcgen05 MMAs on the codes.  A unit is 128 rows x 64 keys; the units of two
-//              streams (two halves of the rows; of 128 rows or fewer two halves of the keys,
-//              joined where the segment ends) go in turn through three buffers of 64 columns,
-//              so that S of the next unit is there when a stream's softmax has ended
-//   PV         O += P V~ as f16 MMAs, P from tensor memory (over the S it came from)
 //   4 decode   V's codes times scales, exactly, to f16 rows in shared memory (scales run
 //              along D, so codes cannot be the FP4 operand of a product over keys), once for
-//              both streams
-//   2 x 4      softmax, one thread a row, a warpgroup for each stream.  The maximum
-//              that p refers to is raised only where a score exceeds it by 8 (log2); the
-//              row's thread then rescales O itself
+//              both streams; the first of them brings K's scales into the scale operand's order
 //   4 query    q~ of the segments, up to two ahead; rows without keys
+//   2 x S      S = Q~ K~^T as block-scaled FP4 tcgen05 MMAs on the codes.  A unit is 128 rows x
+//              64 keys; the units of two streams (two halves of the rows; of 128 rows or fewer
+//              two halves of the keys, joined where the segment ends) go in turn through three
+//              buffers of 64 columns, so that S of the next unit is there when a stream's
+//              softmax has ended
+//   PV         O += P V~ as f16 MMAs, P from tensor memory (over the S it came from)
+//   2 x 4      softmax, one thread a row, a warpgroup for each stream.  The maximum that p
+//              refers to is raised only where a score exceeds it by 8 (log2); the row's thread
+//              then rescales O itself
 // p is rounded to f16 (below 2^8), its sum taken before the rounding; all sums are fp32.
 #include <algorithm>
 #include <cmath>
@@ -49,8 +49,7 @@ constexpr int kRows = 128;     // query rows of a unit
 constexpr int kPair = 256;     // and of a tile
 constexpr int kKeys = 64;      // keys of a unit
 constexpr int kThreads = 640;
-constexpr int kDecodeWarp = 8, kQWarp = 12, kProducerWarp = 16, kSWarp = 17, kPvWarp = 18,
-              kScaleWarp = 19;
+constexpr int kDecodeWarp = 8, kQWarp = 12, kProducerWarp = 16, kSWarp = 17, kPvWarp = 19;
 constexpr int kSegs = 8;       // descriptions of segments: the query warps are two ahead of S, the
                                // softmax of an end may be one behind it
 constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
@@ -85,7 +84,7 @@ struct Cfg {
   static constexpr uint32_t kSegAt = kDescAt + kStages * 16;   // Segment [kSegs]
   static constexpr uint32_t kUnitAt = kSegAt + kSegs * 48;       // int [2 streams][3 (4)]
   static constexpr uint32_t kBarAt = kUnitAt + 32;
-  static constexpr int kBars = 3 * kStages + 4 * 2 + 4 * 3 + 3 * 2 + 4 + kSegs;
+  static constexpr int kBars = 3 * kStages + 4 * 2 + 4 * 3 + 2 * 2 + 3 + 4 + kSegs;
   // heads of 64: padded so that no CTA of the few-rows linear lies beside one
   static constexpr uint32_t kUsed = kBarAt + kBars * 8 + 1024;
   static constexpr uint32_t kSmem = kUsed > 152 * 1024 ? kUsed : 152 * 1024;
@@ -513,8 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* pv_done = p_full + 3;         // [3]
   uint64_t* o_full = pv_done + 3;         // [2 streams]: a segment's last PV is done
   uint64_t* o_read = o_full + 2;          // [2 streams], four softmax warps (of either stream)
-  uint64_t* drain = o_read + 2;           // [2]
-  uint64_t* merge = drain + 2;            // [4]: by 32 rows, the other keys' sums are done
+  uint64_t* drain = o_read + 2;           // [3]
+  uint64_t* merge = drain + 3;            // [4]: by 32 rows, the other keys' sums are done
   uint64_t* described = merge + 4;        // [kSegs]
   Segment* segs = reinterpret_cast<Segment*>(smem + C::kSegAt);
   int* units = reinterpret_cast<int*>(smem + C::kUnitAt);  // as s_full: keys that hold tokens, flags
@@ -526,29 +525,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_word = 0;
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1 + 1 + 4);
+      mbar_init(&empty[s], 2 + 1 + 4);
       mbar_init(&k_ready[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&v_full[i], 4);
       mbar_init(&v_empty[i], 1);
       mbar_init(&q_full[i], 4);
-      mbar_init(&q_empty[i], 1);
+      mbar_init(&q_empty[i], 2);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_read[i], 4);
-      mbar_init(&drain[i], 1);
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(&s_full[i], 2);  // the MMAs, and what the S warp tells of the unit
       mbar_init(&s_full[3 + i], 2);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
+      mbar_init(&drain[i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&merge[i], 1);
     for (int i = 0; i < kSegs; ++i) mbar_init(&described[i], 1);
     fence_mbar_init();
   }
-  if (warp == kScaleWarp) {
+  if (warp == kPvWarp) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
     tma_prefetch_desc(&tk);
@@ -658,12 +657,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int m = max(0, n - C::kStages); m < n; ++m)
         mbar_wait_warp(&full[m % C::kStages], (m / C::kStages) & 1, nullptr, 10000000ull);
     }
-  } else if (warp == kSWarp) {
-    // ------------------------------------------------------------ S = Q~ K~^T
+  } else if (warp == kSWarp || warp == kSWarp + 1) {
+    // ------------------------------------------------------------ S = Q~ K~^T of a stream's units
     constexpr uint32_t idesc = idesc_mxf4nvf4(kRows, kKeys);
     constexpr uint32_t lay = D == 128 ? 4u : 6u, sbo = 4 * D;  // swizzle, bytes of 8 rows
-    Ring ring, unit;
-    int done = 0;  // units of a stream so far, modulo 3
+    const int stream = warp - kSWarp;
+    const uint64_t q_d0 = sdesc(smem_u32(smem + C::kQAt), 16, sbo, lay);
+    const uint64_t k_d0 = sdesc(smem_u32(smem), 16, sbo, lay);
+    Ring ring, unit;  // the buffer of the stream's next unit, every other one
+    if (stream == 1) unit.next(3);
+    int word = 0;     // units of the stream so far, modulo 3
     bool ok = true;
 #pragma unroll 1
     for (int n = 0; n < n_tiles && ok; ++n, ring.next(C::kStages)) {
@@ -671,68 +674,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&k_ready[st], ring.phase, abort)) break;
       const int flags = uniform(desc[st].flags), seg = uniform(desc[st].seg);
       const int valid = desc[st].valid;
-      const int qb = seg & 1, halves = flags & kBoth ? 2 : 1;  // of the rows
+      const int qb = seg & 1, both = flags & kBoth ? 1 : 0;
+      const int half = both ? stream : 0;  // of the rows
       if ((flags & kStart) && !wait(&q_full[qb], (seg >> 1) & 1, abort)) break;
-      tc_fence_after();
-      const uint32_t sfq = tmem + kSfQ + 16 * qb, sfk = tmem + kSfK + 8 * (n & 3);
-      uint8_t* stage = smem + st * C::kRec;
-      // The copies below go to columns whose last readers have completed: of K's scales the
-      // MMAs of tile n - 4, as the last unit of tile n - 1 went out behind the PV of a unit three
-      // before it; of q's the MMAs of segment seg - 2, which the query warps waited for.
-      if (flags & kStart) {
+      const uint32_t sfq = tmem + kSfQ + 16 * qb + 8 * stream;
+      const uint32_t sfk = tmem + kSfK + 16 * stream + 8 * (n & 1);
+      const uint64_t qd = q_d0 + static_cast<uint64_t>((2 * qb + half) * (C::kQ >> 4));
+      const uint64_t qds[2] = {qd, qd + 2};
 #pragma unroll 1
-        for (int k = 0; k < halves * (D / 64); ++k)  // a half's blocks at 8 columns
-          tmem_cp_32x128_x4_w(sfq + (D == 128 ? 4 * k : 8 * k),
-                              smem_u32(smem + C::kQScAt + 2 * qb * C::kQSc) + 512 * k);
-      }
-      if (!(flags & kAbsent)) {
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k)
-          tmem_cp_32x128_x4_w(sfk + 4 * k, smem_u32(stage + k_scales_at(D)) + 512 * k);
-      }
-#pragma unroll 1
-      for (int u = 0; u < 2 * halves; ++u, unit.next(3)) {
-        const int stream = u & 1, key = halves == 2 ? u >> 1 : u, half = halves == 2 ? stream : 0;
-        const bool last = u == 2 * halves - 1;
-        const uint32_t qa = smem_u32(smem + C::kQAt + (2 * qb + half) * C::kQ);
-        const uint32_t ka = smem_u32(stage) + key * (kKeys * D / 2);
-        const uint64_t qd[2] = {sdesc(qa, 16, sbo, lay), sdesc(qa, 16, sbo, lay) + 2};
-        const uint64_t kd[2] = {sdesc(ka, 16, sbo, lay), sdesc(ka, 16, sbo, lay) + 2};
-        uint64_t* const ready = &s_full[3 * stream + done];
+      for (int j = 0; j <= both; ++j) {
+        const int key = both ? j : stream;
+        const bool last = j == both;
+        const uint64_t kd =
+            k_d0 + static_cast<uint64_t>(st * (C::kRec >> 4) + key * (kKeys * D / 2 >> 4));
+        const uint64_t kds[2] = {kd, kd + 2};
+        uint64_t* const ready = &s_full[3 * stream + word];
         if (lane == 0)  // (the PV of the stream's unit three before is done: the word is free)
-          units[4 * stream + done] =
-              max(0, min(kKeys, valid - kKeys * key)) | ((flags & kStart) && u < 2 ? kUnitStart : 0) |
-              (u >= 2 * halves - 2 ? ((flags & kEnd) ? kUnitEnd : 0) | (n == n_tiles - 1 ? kUnitLast : 0)
-                                   : 0);
-        if (stream == 1) done = done == 2 ? 0 : done + 1;
+          units[4 * stream + word] =
+              max(0, min(kKeys, valid - kKeys * key)) |
+              ((flags & kStart) && j == 0 ? kUnitStart : 0) |
+              (last ? ((flags & kEnd) ? kUnitEnd : 0) | (n == n_tiles - 1 ? kUnitLast : 0) : 0);
+        word = word == 2 ? 0 : word + 1;
         // the buffer is free when the PV of the unit three before has read the P over it
         if (!(ok = wait(&pv_done[unit.s], unit.phase ^ 1, abort))) break;
         tc_fence_after();
+        if (j == 0) {
+          // The copies go to columns whose last readers have completed: the stream's MMAs of tile
+          // n - 2 (the PVs waited for lie behind them), and of q's of segment seg - 2, which the
+          // query warps waited for.
+          if (flags & kStart) {
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k)
+              tmem_cp_32x128_x4_w(sfq + 4 * k,
+                                  smem_u32(smem + C::kQScAt + (2 * qb + half) * C::kQSc) + 512 * k);
+          }
+          if (!(flags & kAbsent)) {
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k)
+              tmem_cp_32x128_x4_w(sfk + 4 * k,
+                                  smem_u32(smem + st * C::kRec + k_scales_at(D)) + 512 * k);
+          }
+        }
         if (!(flags & kAbsent)) {
-          umma_fp4_group_w<D / 64>(tmem + 64 * unit.s, qd, kd, idesc, sfq + 8 * half, sfk + 2 * key,
+          umma_fp4_group_w<D / 64>(tmem + 64 * unit.s, qds, kds, idesc, sfq, sfk + 2 * key,
                                    bar_u32(ready), last ? bar_u32(&empty[st]) : 0u);
         } else {
           umma_commit_w(ready);
           if (last) umma_commit_w(&empty[st]);
         }
         mbar_arrive_warp(ready);
+        unit.next(3);
+        unit.next(3);
       }
       if (flags & kEnd) umma_commit_w(&q_empty[qb]);
     }
-    umma_commit_w(&drain[0]);  // the MMAs in flight end before the block
-    mbar_wait_warp(&drain[0], 0, nullptr, 10000000ull);
-  } else if (warp == kScaleWarp) {
-    // ------------------------------------------------------------ scales of K
-    Ring ring;
-#pragma unroll 1
-    for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
-      if (!wait(&full[ring.s], ring.phase, abort)) break;
-      if (!(desc[ring.s].flags & kAbsent)) {
-        arrange_scales<D>(smem + ring.s * C::kRec + k_scales_at(D), lane);
-        fence_proxy_async_smem();
-      }
-      mbar_arrive_warp(&k_ready[ring.s]);
-    }
+    umma_commit_w(&drain[stream]);  // the MMAs in flight end before the block
+    mbar_wait_warp(&drain[stream], 0, nullptr, 10000000ull);
   } else if (warp == kPvWarp) {
     // ------------------------------------------------------------ O += P V~
     constexpr uint32_t idesc = idesc_f16(kRows, D, 0, 0, 1);
@@ -762,8 +759,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((flags & kEnd) && u >= 2 * halves - 2) umma_commit_w(&o_full[stream]);
       }
     }
-    umma_commit_w(&drain[1]);
-    mbar_wait_warp(&drain[1], 0, nullptr, 10000000ull);
+    umma_commit_w(&drain[2]);
+    mbar_wait_warp(&drain[2], 0, nullptr, 10000000ull);
   } else if (warp >= kDecodeWarp && warp < kQWarp) {
     // ------------------------------------------------------------ V~
     Ring ring;
@@ -771,6 +768,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; n < n_tiles; ++n, ring.next(C::kStages)) {
       const int st = ring.s, b = n & 1;
       if (!wait(&full[st], ring.phase, abort)) break;
+      if (warp == kDecodeWarp) {
+        if (!(desc[st].flags & kAbsent)) {
+          arrange_scales<D>(smem + st * C::kRec + k_scales_at(D), lane);
+          fence_proxy_async_smem();
+        }
+        mbar_arrive_warp(&k_ready[st]);
+      }
       if (!wait(&v_empty[b], ((n >> 1) & 1) ^ 1, abort)) break;
       decode_v<D>(smem + st * C::kRec, smem + C::kVAt + b * C::kV, desc[st].valid,
                   warp - kDecodeWarp, lane);
@@ -1024,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   report_abort(&abort_word, a.err);
-  if (warp == kScaleWarp) {
+  if (warp == kPvWarp) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);

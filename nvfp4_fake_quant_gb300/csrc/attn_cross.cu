@@ -425,19 +425,10 @@ __device__ __forceinline__ void umma_f16_ts4_w(uint32_t d, uint32_t a, uint64_t 
       : "memory");
 }
 
-// Contiguous copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) from shared to
-// global memory, in this thread's bulk group.
-__device__ __forceinline__ void bulk_store(void* dst, const void* smem_src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                   reinterpret_cast<uint64_t>(dst)),
-               "r"(smem_u32(smem_src)), "r"(bytes)
-               : "memory");
-}
-
 // What is written as a row's lse: the natural logarithm, or base 2 beside an output in fp32.
 __device__ __forceinline__ float row_lse(const CrossArgs& a, float m, float l) {
   if (!(l > 0.f)) return -INFINITY;
-  const float v = m + log2f(l);
+  const float v = m + __log2f(l);
   return a.o != nullptr ? v * kLn2 : v;
 }
 
@@ -906,68 +897,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         other *= inv;
       }
       float* part = a.parts + max(slot, 0) * part_floats(a.part_rows, D);
-      __nv_bfloat16* out16 = slot < 0 && a.o != nullptr ? a.o + at * D : nullptr;
-      float* out32 = slot < 0 ? a.o32 + at * D : part + 2 * a.part_rows + r * D;
-      // rows go out by bulk copies, a thread's own each (stores of 16 bytes a row kept the warps
-      // for 9000 cycles a segment, more than two tiles' softmax): all of a bf16 row, or one half
-      // after the other of one in fp32
-      uint8_t* const staged = smem + C::kOutAt + threadIdx.x * C::kOutRow;
-      bulk_wait_group_read<0>();
-      if (live) {
-#pragma unroll 1
-        for (int x = 0; x < D; x += 16) {
-          uint32_t v[16];
-          __syncwarp();
-          tmem_ld16(o_at + x, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * own);
-          if (!both) {
-            uint32_t z[16];
-            tmem_ld16(o_at + D + x, z);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              v[i] = __float_as_uint(
-                  fmaf(__uint_as_float(z[i]), other, __uint_as_float(v[i])));
-          }
-          if (out16 != nullptr) {
-            uint4* dst = reinterpret_cast<uint4*>(staged + 2 * x);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              dst[i] = make_uint4(pack_bf16(v + 8 * i), pack_bf16(v + 8 * i + 2),
-                                  pack_bf16(v + 8 * i + 4), pack_bf16(v + 8 * i + 6));
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(staged + 4 * (x % (D / 2)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            if (x == D / 2 - 16) {
-              fence_proxy_async_smem();
-              if (mine) bulk_store(out32, staged, 2 * D);
-              bulk_commit_group();
-              bulk_wait_group_read<0>();
-            }
-          }
-        }
-      }
-      tc_fence_before();
-      mbar_arrive_warp(&o_read[stream]);
-      if (!both) mbar_arrive_warp(&o_read[1]);
-      fence_proxy_async_smem();
-      if (mine) {
-        if (out16 != nullptr) bulk_store(out16, staged, 2 * D);
-        else bulk_store(out32 + D / 2, staged, 2 * D);
-      }
-      bulk_commit_group();
       if (mine) {
         if (slot >= 0)
           *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
         else if (a.lse != nullptr)
           a.lse[at] = row_lse(a, m, l);
       }
+      // The warp's rows go through shared memory, so that it stores whole rows, 512 bytes at a time
+      // (16 bytes of 32 rows at a time kept it for 9000 cycles a segment, more than two tiles'
+      // softmax; a bulk copy for each row for 2500): bf16 rows at once, halves of fp32 ones.
+      const bool narrow = slot < 0 && a.o != nullptr;
+      uint8_t* const out = narrow       ? reinterpret_cast<uint8_t*>(a.o + at * D)
+                           : slot < 0 ? reinterpret_cast<uint8_t*>(a.o32 + at * D)
+                                      : reinterpret_cast<uint8_t*>(part + 2 * a.part_rows + r * D);
+      uint8_t* const area = smem + C::kOutAt + 32 * warp * C::kOutRow;
+      const int there = rows - (r - lane);  // rows of the warp's 32
+      const int cols = narrow ? D : D / 2;
+#pragma unroll 1
+      for (int x0 = 0; x0 < D; x0 += cols) {
+        if (live) {
+#pragma unroll 1
+          for (int x = x0; x < x0 + cols; x += 32) {
+            uint32_t v[32];
+            tmem_ld32(o_at + x, v);
+            tmem_wait_ld();
+            const uint64_t own2 = pk2(own, own);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float z0, z1;
+              up2(mul2(pk2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), own2), z0, z1);
+              v[i] = __float_as_uint(z0);
+              v[i + 1] = __float_as_uint(z1);
+            }
+            if (!both) {
+              uint32_t z[32];
+              tmem_ld32(o_at + D + x, z);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                v[i] = __float_as_uint(fmaf(__uint_as_float(z[i]), other, __uint_as_float(v[i])));
+            }
+            if (narrow) {
+              uint4* dst = reinterpret_cast<uint4*>(area + lane * C::kOutRow + 2 * x);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_uint4(pack_bf16(v + 8 * i), pack_bf16(v + 8 * i + 2),
+                                    pack_bf16(v + 8 * i + 4), pack_bf16(v + 8 * i + 6));
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(area + lane * C::kOutRow + 4 * (x - x0));
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+          }
+        }
+        if (x0 + cols == D) {
+          tc_fence_before();
+          mbar_arrive_warp(&o_read[stream]);
+          if (!both) mbar_arrive_warp(&o_read[1]);
+        }
+        __syncwarp();
+        constexpr int kAtOnce = 32 * 16 / (2 * D);  // rows of 2 D bytes in a store of the warp
+        const int sub = lane / (32 / kAtOnce);
+#pragma unroll 4
+        for (int i = 0; i < 32; i += kAtOnce) {
+          const unsigned long long to =
+              __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(out), i + sub);
+          if (i + sub < there) {
+            const int at16 = lane % (32 / kAtOnce) * 16;
+            const uint4 w = *reinterpret_cast<const uint4*>(area + (i + sub) * C::kOutRow + at16);
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(to) + 4 * x0 + at16) = w;
+          }
+        }
+        __syncwarp();
+      }
     }
-    bulk_wait_group<0>();
   } else if (warp >= kQWarp && warp < kProducerWarp) {
     // ------------------------------------------------------------ q~
     const int t = threadIdx.x - 32 * kQWarp;

@@ -54,9 +54,9 @@ constexpr int kSegs = 8;       // descriptions of segments: the query warps are 
                                // softmax of an end may be one behind it
 constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// tensor memory columns: S of unit u at 64 (u % 3), O of the two halves, the scales of q~ (two
-// buffers of both halves) and of K (four: a copy never overwrites what an MMA in flight may
-// read, see the S warp)
+// tensor memory columns: S of unit u at 64 (u % 3), O of the two streams, the scales of q~ (two
+// buffers of both streams) and of K (of each stream two: a copy never overwrites what an MMA in
+// flight may read, see the S warps)
 constexpr uint32_t kO = 192, kSfQ = 448, kSfK = 480;
 
 enum : int { kStart = 1, kEnd = 2, kAbsent = 4, kBoth = 8 };
@@ -79,7 +79,7 @@ struct Cfg {
   static constexpr uint32_t kQScAt = kQAt + 4 * kQ;      // [2][2]
   static constexpr uint32_t kOutAt = kQScAt + 4 * kQSc;  // bf16 rows of o on their way out,
   static constexpr uint32_t kOutRow = D * 2 + 16;        // apart by an odd number of 16 bytes
-  static constexpr uint32_t kMlAt = kOutAt + kPair * kOutRow;  // float2 [128]: the other keys' (m, l)
+  static constexpr uint32_t kMlAt = kOutAt + kPair * kOutRow;  // float2 [128]: (m, l), other keys
   static constexpr uint32_t kDescAt = kMlAt + kRows * 8;
   static constexpr uint32_t kSegAt = kDescAt + kStages * 16;   // Segment [kSegs]
   static constexpr uint32_t kUnitAt = kSegAt + kSegs * 48;       // int [2 streams][3 (4)]
@@ -246,8 +246,8 @@ __device__ __forceinline__ T uniform(T v) {
 // what does not fit the instruction caches costs more than all arithmetic (with the waits of
 // nvq_ptx.cuh inline, loops unrolled and masks in the softmax's chunks the kernel was 113 KB, three
 // warps of eleven waited for instructions and a tile took 3350 cycles).  A wait gives up after two
-// seconds, or when another thread has.  (With a suspend-time hint of a microsecond on the
-// try_wait a warp now and then slept all of it: 32 x 64 heads behind 131072 keys 166 us, HINTLESS.)
+// seconds, or when another thread has.  (With a suspend-time hint of a
+// microsecond on the try_wait a warp now and then slept all of it: not faster.)
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t abort) {
   uint32_t ok;
   asm volatile(
@@ -379,8 +379,10 @@ __device__ __forceinline__ void decode_v(const uint8_t* rec, uint8_t* dst, int v
 #pragma unroll 1
   for (int i = 0; i < kPieces; ++i) {
     const int key = 32 * warp + i * kKeys + lane / kPieces;
-    const uint4 c = *reinterpret_cast<const uint4*>(rec + v_codes_at(D) + key * (D / 2) + piece * 16);
-    uint32_t sc = *reinterpret_cast<const uint16_t*>(rec + v_scales_at(D) + key * (D / 16) + piece * 2);
+    const uint4 c =
+        *reinterpret_cast<const uint4*>(rec + v_codes_at(D) + key * (D / 2) + piece * 16);
+    uint32_t sc =
+        *reinterpret_cast<const uint16_t*>(rec + v_scales_at(D) + key * (D / 16) + piece * 2);
     if (key >= valid) sc = 0;
     const uint32_t s2 = e4m3x2_to_f16x2(sc);
     const uint32_t sa = __byte_perm(s2, 0, 0x1010), sb = __byte_perm(s2, 0, 0x3232);
@@ -425,11 +427,13 @@ __device__ __forceinline__ void umma_f16_ts4_w(uint32_t d, uint32_t a, uint64_t 
       : "memory");
 }
 
-// What is written as a row's lse: the natural logarithm, or base 2 beside an output in fp32.
+// What is written as a row's lse: the natural logarithm (-inf of a row with a NaN, as for single
+// tokens), or base 2 beside an output in fp32 (there NaN, so that who folds it in sees it).
 __device__ __forceinline__ float row_lse(const CrossArgs& a, float m, float l) {
-  if (!(l > 0.f)) return -INFINITY;
+  if (l == 0.f) return -INFINITY;
   const float v = m + __log2f(l);
-  return a.o != nullptr ? v * kLn2 : v;
+  if (a.o == nullptr) return v;
+  return l > 0.f ? v * kLn2 : -INFINITY;
 }
 
 // 32 lanes x 8 columns (32x32b shape).
@@ -440,9 +444,9 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
-                   taddr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+               "r"(r[6]), "r"(r[7])
                : "memory");
 }
 
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* merge = drain + 3;            // [4]: by 32 rows, the other keys' sums are done
   uint64_t* described = merge + 4;        // [kSegs]
   Segment* segs = reinterpret_cast<Segment*>(smem + C::kSegAt);
-  int* units = reinterpret_cast<int*>(smem + C::kUnitAt);  // as s_full: keys that hold tokens, flags
+  int* units = reinterpret_cast<int*>(smem + C::kUnitAt);  // by s_full: keys with tokens, flags
   float2* ml = reinterpret_cast<float2*>(smem + C::kMlAt);
   const uint32_t abort = smem_u32(&abort_word);
   pdl_trigger();
@@ -790,80 +794,80 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring mine_full;
 #pragma unroll 1
     for (; !(what & kUnitLast); u += 2, mine_full.next(3)) {
-        const uint32_t buf = u % 3;
-        if (!wait(&s_full[3 * stream + mine_full.s], mine_full.phase, abort)) break;
-        tc_fence_after();
-        what = units[4 * stream + mine_full.s];
-        if (what & kUnitStart) {
-          m = -INFINITY;
-          l2 = pk2(0.f, 0.f);
-          rows = segs[ends % kSegs].rows;
-        }
-        const int valid = what & kValid;
-        const bool both = rows > kRows;
-        const bool live = 32 * (both ? warp : quarter) < rows;  // else: rows that nobody reads
-        const uint32_t s_at = lanes + 64 * buf;
-        if (live) {
-          if (valid < kKeys) {  // keys behind the last: -inf, before S is read
+      const uint32_t buf = u % 3;
+      if (!wait(&s_full[3 * stream + mine_full.s], mine_full.phase, abort)) break;
+      tc_fence_after();
+      what = units[4 * stream + mine_full.s];
+      if (what & kUnitStart) {
+        m = -INFINITY;
+        l2 = pk2(0.f, 0.f);
+        rows = segs[ends % kSegs].rows;
+      }
+      const int valid = what & kValid;
+      const bool both = rows > kRows;
+      const bool live = 32 * (both ? warp : quarter) < rows;  // else: rows that nobody reads
+      const uint32_t s_at = lanes + 64 * buf;
+      if (live) {
+        if (valid < kKeys) {  // keys behind the last: -inf, before S is read
 #pragma unroll 1
-            for (int c = max(valid, 0) & ~15; c < kKeys; c += 16) {
-              uint32_t x[16];
-              tmem_ld16(s_at + c, x);
-              tmem_wait_ld();
+          for (int c = valid & ~15; c < kKeys; c += 16) {
+            uint32_t x[16];
+            tmem_ld16(s_at + c, x);
+            tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (c + i >= valid) x[i] = 0xFF800000u;
-              tmem_st16(s_at + c, x);
-            }
-            tmem_wait_st();
+            for (int i = 0; i < 16; ++i)
+              if (c + i >= valid) x[i] = 0xFF800000u;
+            tmem_st16(s_at + c, x);
           }
-          uint32_t x[32], y[32];
-          tmem_ld32(s_at, x);
-          tmem_ld32(s_at + 32, y);
-          tmem_wait_ld();
-          float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            v[0] = max3f(v[0], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-            v[1] = max3f(v[1], __uint_as_float(x[16 + i]), __uint_as_float(x[17 + i]));
-            v[2] = max3f(v[2], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-            v[3] = max3f(v[3], __uint_as_float(y[16 + i]), __uint_as_float(y[17 + i]));
-          }
-          const float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * a.scale_log2;
-          const bool grows = mx > m + kSlack;  // -inf: always, where there is a key
-          if (__any_sync(0xFFFFFFFFu, grows)) {
-            const float c = grows ? ex2_f32(m - mx) : 1.f;
-            if (grows) m = mx;
-            l2 = mul2(l2, pk2(c, c));
-            // raised behind the segment's first unit: O so far, which the stream's PV before has
-            // finished
-            if (!(what & kUnitStart)) {
-              const uint32_t w = u - 2;
-              if (!wait(&pv_done[w % 3], (w / 3) & 1, abort)) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int z = 0; z < D; z += 8) {
-                uint32_t t[8];
-                tmem_ld8(o_at + z, t);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) t[i] = __float_as_uint(__uint_as_float(t[i]) * c);
-                tmem_st8(o_at + z, t);
-              }
-            }
-          }
-          // ---- p = 2^(S log2e - m), over S
-          const float ref = -fmaxf(m, -3.4e38f);
-          const uint64_t neg_m = pk2(ref, ref);
-          uint32_t p[16];
-          exponentials(x, scale2, neg_m, l2, p);
-          tmem_st16(s_at, p);
-          exponentials(y, scale2, neg_m, l2, p);
-          tmem_st16(s_at + 16, p);
           tmem_wait_st();
         }
-        tc_fence_before();
-        mbar_arrive_warp(&p_full[buf]);
+        uint32_t x[32], y[32];
+        tmem_ld32(s_at, x);
+        tmem_ld32(s_at + 32, y);
+        tmem_wait_ld();
+        float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          v[0] = max3f(v[0], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          v[1] = max3f(v[1], __uint_as_float(x[16 + i]), __uint_as_float(x[17 + i]));
+          v[2] = max3f(v[2], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+          v[3] = max3f(v[3], __uint_as_float(y[16 + i]), __uint_as_float(y[17 + i]));
+        }
+        const float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * a.scale_log2;
+        const bool grows = mx > m + kSlack;  // -inf: always, where there is a key
+        if (__any_sync(0xFFFFFFFFu, grows)) {
+          const float c = grows ? ex2_f32(m - mx) : 1.f;
+          if (grows) m = mx;
+          l2 = mul2(l2, pk2(c, c));
+          // raised behind the segment's first unit: O so far, which the stream's PV before has
+          // finished
+          if (!(what & kUnitStart)) {
+            const uint32_t w = u - 2;
+            if (!wait(&pv_done[w % 3], (w / 3) & 1, abort)) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int z = 0; z < D; z += 8) {
+              uint32_t t[8];
+              tmem_ld8(o_at + z, t);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) t[i] = __float_as_uint(__uint_as_float(t[i]) * c);
+              tmem_st8(o_at + z, t);
+            }
+          }
+        }
+        // ---- p = 2^(S log2e - m), over S
+        const float ref = -fmaxf(m, -3.4e38f);
+        const uint64_t neg_m = pk2(ref, ref);
+        uint32_t p[16];
+        exponentials(x, scale2, neg_m, l2, p);
+        tmem_st16(s_at, p);
+        exponentials(y, scale2, neg_m, l2, p);
+        tmem_st16(s_at + 16, p);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      mbar_arrive_warp(&p_full[buf]);
       if (!(what & kUnitEnd)) continue;
       // ---- the segment's end
       const Segment& sg = segs[ends % kSegs];
@@ -1015,9 +1019,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (; none != 0; none &= none - 1) {
         const int i = __ffs(none) - 1;
-        const int tok0 = __shfl_sync(0xFFFFFFFFu, x.tok0, i), toks = __shfl_sync(0xFFFFFFFFu, x.toks, i);
+        const int tok0 = __shfl_sync(0xFFFFFFFFu, x.tok0, i);
+        const int toks = __shfl_sync(0xFFFFFFFFu, x.toks, i);
 #pragma unroll 1
-        for (int64_t z = first; z < toks; z += step) empty_token<D>(a, tok0 + static_cast<int>(z), lane);
+        for (int64_t z = first; z < toks; z += step)
+          empty_token<D>(a, tok0 + static_cast<int>(z), lane);
       }
     }
     if (a.cu != nullptr) {

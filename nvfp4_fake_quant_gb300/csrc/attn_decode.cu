@@ -161,12 +161,12 @@ struct Runs {
 
 // What a row has over its own keys (maximum m and sum l, log2 units) together with `prior`, the
 // logarithm over other keys: m and l of both, and the factors of the two sums of p V~ (the other
-// one is normalised).  Without other keys nothing changes.
+// one is normalised).  Without other keys nothing changes; a NaN among them makes both NaN.
 struct Fold {
   float own, other;
 };
 __device__ __forceinline__ Fold fold_prior(float prior, float& m, float& l) {
-  if (!(prior > -INFINITY)) return {1.f, 0.f};
+  if (prior == -INFINITY) return {1.f, 0.f};
   const float mn = fmaxf(m, prior);
   const Fold f{ex2_f32(m - mn), ex2_f32(prior - mn)};
   m = mn;
@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
         const int64_t row0 = static_cast<int64_t>(b) * a.H;
         for (int x = lane; x < a.H * (D / 8); x += 32) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (a.prior_o != nullptr && a.prior_l2[row0 + x / (D / 8)] > -INFINITY) {
+          if (a.prior_o != nullptr && a.prior_l2[row0 + x / (D / 8)] != -INFINITY) {
             const float4* p = reinterpret_cast<const float4*>(a.prior_o + row0 * D) + 2 * x;
             const float4 lo = p[0], hi = p[1];
             v = make_uint4(pack_bf16x2(lo.x, lo.y), pack_bf16x2(lo.z, lo.w),
@@ -840,7 +840,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
             o0 = fmaf(ov.x, c[w], o0);
             o1 = fmaf(ov.y, c[w], o1);
           }
-          if (folds && f.other > 0.f) {
+          if (folds && f.other != 0.f) {
             const float2 p = *reinterpret_cast<const float2*>(a.prior_o + row * D + element_of<D>(pos));
             o0 = fmaf(o0, f.own, p.x * f.other);
             o1 = fmaf(o1, f.own, p.y * f.other);
@@ -946,7 +946,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const DecodeArgs a) {
       if (a.prior_o != nullptr) {
         const Fold f = fold_prior(a.prior_l2[row], mx, l);
         float2 p = make_float2(0.f, 0.f), q = p;
-        if (f.other > 0.f) {
+        if (f.other != 0.f) {
           const float* src = a.prior_o + row * D;
           p = *reinterpret_cast<const float2*>(src + element_of<D>(4 * x));
           q = *reinterpret_cast<const float2*>(src + element_of<D>(4 * x + 2));

@@ -303,6 +303,27 @@ def test_prefix_of_many_sequences_is_the_decode_over_both():
     assert bool(((lse - lse2)[fin].abs() <= 2.0 ** -11).all()) and api.device_status() == 0
 
 
+@pytest.mark.parametrize("own", [0, 5, 300])
+def test_a_nan_in_a_cached_key_is_seen(own):
+    """A NaN scale byte among the keys: rows that see it are NaN, others as they were; also where
+    the prefix holds it and the sequence's own keys are none, few, or cut into parts."""
+    h, hkv, d = 4, 2, 128
+    g = torch.Generator().manual_seed(own)
+    pool = make_pool(8, hkv, d, g)
+    pool[1, 1, 128 * d + 7 * d // 16] = 0x7F  # K's scales, page 1, head 1, key 7
+    q = torch.randn(4, h, d, generator=g).to(BF16).cuda()
+    prefix, shared = ints([[0, 1], [2, 3]]), ints([200, 200])
+    table, lens = ints([[4, 5, 6]] * 4), ints([own] * 4)
+    pool = pool.cuda()
+    o, _ = api.attn_qat_decode_prefix(q, pool, table, lens, prefix, shared)
+    sees = torch.zeros(4, h, dtype=torch.bool)
+    sees[:2, 2:] = True
+    assert torch.equal(o.isnan().all(-1).cpu(), sees) and torch.equal(o.isnan().any(-1).cpu(), sees)
+    o, lse = api.attn_qat_cross(q, pool, prefix, shared)
+    assert torch.equal(o.isnan().all(-1).cpu(), sees) and torch.equal(o.isnan().any(-1).cpu(), sees)
+    assert bool(torch.isfinite(lse.cpu()[~sees]).all()) and api.device_status() == 0
+
+
 def test_offsets_past_32_bits():
     """A pool of over 4 GiB: pages at its end, read where they are."""
     hkv, d = 8, 128

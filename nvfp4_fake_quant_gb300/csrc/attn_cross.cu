@@ -18,7 +18,8 @@
 //   4 decode   V's codes times scales, exactly, to f16 rows in shared memory (scales run
 //              along D, so codes cannot be the FP4 operand of a product over keys), once for
 //              both streams; the first of them brings K's scales into the scale operand's order
-//   4 query    q~ of the segments, up to two ahead; rows without keys
+//   4 query    q~ of the segments, up to two ahead (of the first with the help of the softmax and
+//              decode warps); rows without keys
 //   2 x S      S = Q~ K~^T as block-scaled FP4 tcgen05 MMAs on the codes.  A unit is 128 rows x
 //              64 keys; the units of two streams (two halves of the rows; of 128 rows or fewer
 //              two halves of the keys, joined where the segment ends) go in turn through three
@@ -84,7 +85,7 @@ struct Cfg {
   static constexpr uint32_t kSegAt = kDescAt + kStages * 16;   // Segment [kSegs]
   static constexpr uint32_t kUnitAt = kSegAt + kSegs * 48;       // int [2 streams][3 (4)]
   static constexpr uint32_t kBarAt = kUnitAt + 32;
-  static constexpr int kBars = 3 * kStages + 4 * 2 + 4 * 3 + 2 * 2 + 3 + 4 + kSegs;
+  static constexpr int kBars = 3 * kStages + 4 * 2 + 4 * 3 + 2 * 2 + 3 + 4 + kSegs + 1;
   // heads of 64: padded so that no CTA of the few-rows linear lies beside one
   static constexpr uint32_t kUsed = kBarAt + kBars * 8 + 1024;
   static constexpr uint32_t kSmem = kUsed > 152 * 1024 ? kUsed : 152 * 1024;
@@ -285,33 +286,34 @@ struct Ring {
   }
 };
 
-// q~ of a segment by 128 threads, thread t taking block t % (D/16) of every kStep-th row, four
-// rows' values on their way: codes into the swizzled rows of the A operand, scales into the
+// q~ of a segment by N threads, thread t taking block t % (D/16) of every kStep-th row, kAhead
+// rows' values on their way (four spill beside the rest: 32760 rows x 12 heads 133 us, with two
+// 123 us, with one 144 us; with rows brought to L2 before 120 us): codes into the swizzled rows of the A operand, scales into the
 // 512-byte blocks of the scale operand, of the two halves one after another.  Rows beyond the
 // segment's: zeros.
-template <int D>
+template <int D, int N>
 struct QueryTile {
-  static constexpr int kBlocks = D / 16, kStep = 128 / kBlocks;
-  static constexpr int kAhead = 4;
+  static constexpr int kBlocks = D / 16, kStep = N / kBlocks;
+  static constexpr int kAhead = N == 128 ? 2 : 4;
   uint4 lo[kAhead], hi[kAhead];
+  const uint16_t* base;              // block t % kBlocks of the segment's first query head
   int tok, g, rows, step_t, step_g;  // the next row's token and query head; a step's
 
-  __device__ __forceinline__ void begin(const CrossArgs& a, const Walk& w, int t) {
-    rows = w.rows(a);
-    const int row = w.row0() + t / kBlocks;
+  __device__ __forceinline__ void begin(const CrossArgs& a, const Segment& sg, int t) {
+    rows = sg.rows;
+    base = a.q + sg.tok0 * a.ld_q + static_cast<int64_t>(sg.hk * a.G) * D + t % kBlocks * 16;
+    const int row = sg.row0 + t / kBlocks;
     tok = row / a.G;
     g = row - tok * a.G;
     step_t = kStep / a.G;
     step_g = kStep - step_t * a.G;
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) load(a, w, t, t / kBlocks + u * kStep, lo[u], hi[u]);
+    for (int u = 0; u < kAhead; ++u) load(a, t / kBlocks + u * kStep, lo[u], hi[u]);
   }
-  __device__ __forceinline__ void load(const CrossArgs& a, const Walk& w, int t, int n, uint4& lo,
-                                       uint4& hi) {
+  __device__ __forceinline__ void load(const CrossArgs& a, int n, uint4& lo, uint4& hi) {
     lo = hi = make_uint4(0, 0, 0, 0);
     if (n < rows) {
-      const uint16_t* src = a.q + (w.e.tok0 + tok) * a.ld_q +
-                            static_cast<int64_t>(w.hk * a.G + g) * D + t % kBlocks * 16;
+      const uint16_t* src = base + tok * a.ld_q + g * D;
       lo = ld16(src);
       hi = ld16(src + 8);
     }
@@ -321,26 +323,43 @@ struct QueryTile {
       ++tok;
     }
   }
-  __device__ __forceinline__ void quantize(const CrossArgs& a, const Walk& w, uint8_t* codes,
-                                           uint8_t* scales, int t) {
-    const int j = t % kBlocks, end = rows > kRows ? kPair : kRows;
+  __device__ __forceinline__ void quantize(const CrossArgs& a, uint8_t* codes, uint8_t* scales,
+                                           int t) {
+    const int end = rows > kRows ? kPair : kRows;
+    if constexpr (kAhead * kStep >= kPair) {  // all loads are on their way
 #pragma unroll 1
-    for (int n0 = t / kBlocks; n0 < end; n0 += kAhead * kStep) {
+      for (int n = t / kBlocks; n < end; n += kStep) {
+        row(lo[0], hi[0], codes, scales, n, t % kBlocks);
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int n = n0 + u * kStep;
-        const uint32_t v[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w,
-                               hi[u].x, hi[u].y, hi[u].z, hi[u].w};
-        load(a, w, t, n + kAhead * kStep, lo[u], hi[u]);
-        const Codes16 r = codes16_unit(v);
-        const int swz = D == 128 ? (n >> 1) & 3 : (n >> 2) & 1;  // 64- and 32-byte swizzles
-        // the halves' codes and scales lie one behind the other
-        *reinterpret_cast<uint2*>(codes + n * (D / 2) + (((j >> 1) ^ swz) << 4) + (j & 1) * 8) =
-            make_uint2(r.codes[0], r.codes[1]);
-        scales[(n >> 7) * (D / 64 * 512) + (j >> 2) * 512 + (n & 31) * 16 + (n >> 5 & 3) * 4 +
-               (j & 3)] = static_cast<uint8_t>(r.sbyte);
+        for (int u = 0; u + 1 < kAhead; ++u) {
+          lo[u] = lo[u + 1];
+          hi[u] = hi[u + 1];
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int n0 = t / kBlocks; n0 < end; n0 += kAhead * kStep) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int n = n0 + u * kStep;
+          const uint4 x = lo[u], y = hi[u];
+          load(a, n + kAhead * kStep, lo[u], hi[u]);
+          row(x, y, codes, scales, n, t % kBlocks);
+        }
       }
     }
+  }
+  // block j of row n
+  static __device__ __forceinline__ void row(const uint4& x, const uint4& y, uint8_t* codes,
+                                             uint8_t* scales, int n, int j) {
+    const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    const Codes16 r = codes16_unit(v);
+    const int swz = D == 128 ? (n >> 1) & 3 : (n >> 2) & 1;  // 64- and 32-byte swizzles
+    // the halves' codes and scales lie one behind the other
+    *reinterpret_cast<uint2*>(codes + n * (D / 2) + (((j >> 1) ^ swz) << 4) + (j & 1) * 8) =
+        make_uint2(r.codes[0], r.codes[1]);
+    scales[(n >> 7) * (D / 64 * 512) + (j >> 2) * 512 + (n & 31) * 16 + (n >> 5 & 3) * 4 + (j & 3)] =
+        static_cast<uint8_t>(r.sbyte);
   }
 };
 
@@ -482,6 +501,19 @@ __device__ __forceinline__ void empty_token(const CrossArgs& a, int tok, int lan
     for (int x = lane; x < a.H; x += 32) a.lse[row0 + x] = -INFINITY;
 }
 
+// Tells the other warps of a segment of the run [u0, u1), and the join of one that begins in it
+// and goes on behind it.
+__device__ __forceinline__ void describe(const CrossArgs& a, const Walk& w, int run, int64_t u0,
+                                         int64_t u1, int64_t all, Segment& to, uint64_t* described) {
+  const bool begins = w.first >= u0, ends = w.first + w.e.key_tiles <= u1;
+  // a part that begins with the run goes to the run's slot 0, one inside it to slot 1
+  const int slot = begins && ends ? -1 : 2 * run + (w.first > u0 ? 1 : 0);
+  to = {w.row0(), w.rows(a), w.e.tok0, w.hk, slot, w.s, w.i, w.i_end, w.e.len, {0, 0, 0}};
+  mbar_arrive(described);
+  if (begins && !ends)
+    a.split[run] = {w.first + w.e.key_tiles - 1, all, slot, w.rows(a), w.row0(), w.e.tok0, w.hk, 0};
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_kernel(const __grid_constant__ CUtensorMap tk, const CrossArgs a) {
@@ -489,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ int64_t warp_sum[kThreads / 32];
   __shared__ Start start;
+  __shared__ alignas(8) unsigned char walk_bytes[sizeof(Walk)];  // of the query warps' first thread
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -510,10 +543,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = o_read + 2;           // [3]
   uint64_t* merge = drain + 3;            // [4]: by 32 rows, the other keys' sums are done
   uint64_t* described = merge + 4;        // [kSegs]
+  uint64_t* q_first = described + kSegs;  // the other warps that quantize the run's first segment
   Segment* segs = reinterpret_cast<Segment*>(smem + C::kSegAt);
   int* units = reinterpret_cast<int*>(smem + C::kUnitAt);  // by s_full: keys with tokens, flags
   float2* ml = reinterpret_cast<float2*>(smem + C::kMlAt);
   const uint32_t abort = smem_u32(&abort_word);
+  const auto walk = [&]() -> Walk& { return *reinterpret_cast<Walk*>(walk_bytes); };
   pdl_trigger();
 
   if (threadIdx.x == 0) {
@@ -540,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 4; ++i) mbar_init(&merge[i], 1);
     for (int i = 0; i < kSegs; ++i) mbar_init(&described[i], 1);
+    mbar_init(q_first, kQWarp);
     fence_mbar_init();
   }
   if (warp == kPvWarp) {
@@ -608,6 +644,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = uniform(tmem_slot);
   const int n_tiles = uniform(static_cast<int>(u1 - u0));
 
+  // ---- the run's first segment: nothing can begin before its q~, which the query warps alone took
+  // 9000 cycles for, so all that will wait for it help
+  if (threadIdx.x == 32 * kQWarp) {
+    a.split[run].end = -1;
+    if (n_tiles > 0) {
+      const Walk w(start, n_tiles);
+      walk() = w;
+      describe(a, w, run, u0, u1, all, segs[0], &described[0]);
+    }
+  }
+  if (warp < kProducerWarp && n_tiles > 0 && wait(&described[0], 0, abort)) {
+    QueryTile<D, 32 * kProducerWarp> q;
+    q.begin(a, segs[0], threadIdx.x);
+    q.quantize(a, smem + C::kQAt, smem + C::kQScAt, threadIdx.x);
+    fence_proxy_async_smem();
+    mbar_arrive_warp(warp < kQWarp ? q_first : &q_full[0]);
+  }
+
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
     bool ok = true;
@@ -672,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qb = seg & 1, both = flags & kBoth ? 1 : 0;
       const int half = both ? stream : 0;  // of the rows
       if ((flags & kStart) && !wait(&q_full[qb], (seg >> 1) & 1, abort)) break;
+      if (n == 0 && !wait(q_first, 0, abort)) break;
       const uint32_t sfq = tmem + kSfQ + 16 * qb + 8 * stream;
       const uint32_t sfk = tmem + kSfK + 16 * stream + 8 * (n & 1);
       const uint64_t qd = q_d0 + static_cast<uint64_t>((2 * qb + half) * (C::kQ >> 4));
@@ -979,34 +1034,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kQWarp && warp < kProducerWarp) {
     // ------------------------------------------------------------ q~
     const int t = threadIdx.x - 32 * kQWarp;
-    if (t == 0) a.split[run].end = -1;
-    if (n_tiles > 0) {
-      Walk w(start, n_tiles);
-      bool ok = true;
-      int seg = 0;
+    int left = n_tiles > 0 ? n_tiles - (segs[0].i_end - segs[0].i) : 0;  // tiles behind the segment
 #pragma unroll 1
-      do {
-        if (t == 0) {
-          const bool begins = w.first >= u0, ends = w.first + w.e.key_tiles <= u1;
-          // a part that begins with the run goes to the run's slot 0, one inside it to slot 1
-          const int slot = begins && ends ? -1 : 2 * run + (w.first > u0 ? 1 : 0);
-          segs[seg % kSegs] = {w.row0(), w.rows(a), w.e.tok0, w.hk, slot,
-                               w.s, w.i, w.i_end, w.e.len, {0, 0, 0}};
-          mbar_arrive(&described[seg % kSegs]);
-          if (begins && !ends)
-            a.split[run] = {w.first + w.e.key_tiles - 1, all, slot, w.rows(a), w.row0(), w.e.tok0,
-                            w.hk, 0};
-        }
-        __syncwarp();
-        QueryTile<D> q;
-        q.begin(a, w, t);
-        const int qb = seg & 1;
-        if (!(ok = wait(&q_empty[qb], ((seg >> 1) & 1) ^ 1, abort))) break;
-        q.quantize(a, w, smem + C::kQAt + 2 * qb * C::kQ, smem + C::kQScAt + 2 * qb * C::kQSc, t);
-        fence_proxy_async_smem();
-        mbar_arrive_warp(&q_full[qb]);
-        ++seg;
-      } while (w.next(a));
+    for (int seg = 1; left > 0; ++seg) {
+      const Segment& sg = segs[seg % kSegs];
+      if (t == 0) {  // (between the segments the walk lies in shared memory, not in registers)
+        Walk w = walk();
+        w.next(a);
+        walk() = w;
+        describe(a, w, run, u0, u1, all, segs[seg % kSegs], &described[seg % kSegs]);
+      }
+      if (!wait(&described[seg % kSegs], (seg / kSegs) & 1, abort)) break;
+      left -= sg.i_end - sg.i;
+      // all rows on their way to L2 at once: registers hold those of two loads a thread only
+#pragma unroll 1
+      for (int r = t; r < sg.rows; r += 128) {
+        const int row = sg.row0 + r, tok = row / a.G;
+        const uint16_t* src = a.q + (sg.tok0 + tok) * a.ld_q +
+                              static_cast<int64_t>(sg.hk * a.G + row - tok * a.G) * D;
+#pragma unroll
+        for (int x = 0; x < D; x += 64)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src + x));
+      }
+      QueryTile<D, 128> q;
+      q.begin(a, sg, t);
+      const int qb = seg & 1;
+      if (!wait(&q_empty[qb], ((seg >> 1) & 1) ^ 1, abort)) break;
+      q.quantize(a, smem + C::kQAt + 2 * qb * C::kQ, smem + C::kQScAt + 2 * qb * C::kQSc, t);
+      fence_proxy_async_smem();
+      mbar_arrive_warp(&q_full[qb]);
     }
     // ---- rows without keys, rows outside of all sequences
     const int first = 4 * run + warp - kQWarp, step = 4 * static_cast<int>(gridDim.x);

@@ -286,11 +286,11 @@ struct Ring {
   }
 };
 
-// q~ of a segment by N threads, thread t taking block t % (D/16) of every kStep-th row, kAhead
-// rows' values on their way (four spill beside the rest: 32760 rows x 12 heads 133 us, with two
-// 123 us, with one 144 us; with rows brought to L2 before 120 us): codes into the swizzled rows of the A operand, scales into the
-// 512-byte blocks of the scale operand, of the two halves one after another.  Rows beyond the
-// segment's: zeros.
+// q~ of a segment by N threads, thread t taking block t % (D/16) of every kStep-th row: codes into
+// the swizzled rows of the A operand, scales into the 512-byte blocks of the scale operand, of the
+// two halves one after another.  Rows beyond the segment's: zeros.  kAhead rows' values are on
+// their way (four spill beside the rest: 32760 rows x 12 heads 133 us; two 123 us, one 144 us; two
+// with the rows brought to L2 before, 120 us).
 template <int D, int N>
 struct QueryTile {
   static constexpr int kBlocks = D / 16, kStep = N / kBlocks;
@@ -358,8 +358,8 @@ struct QueryTile {
     // the halves' codes and scales lie one behind the other
     *reinterpret_cast<uint2*>(codes + n * (D / 2) + (((j >> 1) ^ swz) << 4) + (j & 1) * 8) =
         make_uint2(r.codes[0], r.codes[1]);
-    scales[(n >> 7) * (D / 64 * 512) + (j >> 2) * 512 + (n & 31) * 16 + (n >> 5 & 3) * 4 + (j & 3)] =
-        static_cast<uint8_t>(r.sbyte);
+    scales[(n >> 7) * (D / 64 * 512) + (j >> 2) * 512 + (n & 31) * 16 + (n >> 5 & 3) * 4 +
+           (j & 3)] = static_cast<uint8_t>(r.sbyte);
   }
 };
 
@@ -504,7 +504,8 @@ __device__ __forceinline__ void empty_token(const CrossArgs& a, int tok, int lan
 // Tells the other warps of a segment of the run [u0, u1), and the join of one that begins in it
 // and goes on behind it.
 __device__ __forceinline__ void describe(const CrossArgs& a, const Walk& w, int run, int64_t u0,
-                                         int64_t u1, int64_t all, Segment& to, uint64_t* described) {
+                                         int64_t u1, int64_t all, Segment& to,
+                                         uint64_t* described) {
   const bool begins = w.first >= u0, ends = w.first + w.e.key_tiles <= u1;
   // a part that begins with the run goes to the run's slot 0, one inside it to slot 1
   const int slot = begins && ends ? -1 : 2 * run + (w.first > u0 ? 1 : 0);
@@ -644,8 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = uniform(tmem_slot);
   const int n_tiles = uniform(static_cast<int>(u1 - u0));
 
-  // ---- the run's first segment: nothing can begin before its q~, which the query warps alone took
-  // 9000 cycles for, so all that will wait for it help
+  // ---- the run's first segment: nothing can begin before its q~, which took the query warps alone
+  // 9000 cycles, so all that would wait for it help (64 tokens behind a shared prefix 55 -> 53 us)
   if (threadIdx.x == 32 * kQWarp) {
     a.split[run].end = -1;
     if (n_tiles > 0) {

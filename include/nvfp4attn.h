@@ -534,7 +534,8 @@ nvq_status nvfp4_kv_append_slots(const void* k, int64_t ld_k, const void* v, int
  *   start            int32 [B] or NULL (0): added to the positions (the length of a
  *                    prefix that is cached apart)
  *   seq_lens_out, free_count_out  lengths and count after the call; may be seq_lens
- *                    and free_count
+ *                    and free_count (what else is written may not lie over any other
+ *                    argument: NVQ_ERR_INVALID)
  *   cu_tokens        int32 [B + 1] (written): offsets of the sequences' new tokens
  *   positions, slots int32 [T], int64 [T] (written): of new token i of sequence b, in
  *                    row cu_tokens[b] + i, p = seq_lens[b] + i: position start[b] + p

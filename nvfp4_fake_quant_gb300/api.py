@@ -763,7 +763,7 @@ def nvfp4_kv_append(k, v, seq_lens, page_table, pool, cu_tokens=None) -> None:
 
 def nvfp4_kv_append_slots(k, v, slots, pool) -> None:
     """nvfp4_kv_append with each token's place given: slots int64 [T] (nvfp4_kv_extend's), 128 *
-    page + row; a token of a negative slot is not written."""
+    page + row, each once; a token of a negative slot is not written."""
     t, hkv, d, ld_k = _rows_nd(k, "k")
     tv, hv, dv, ld_v = _rows_nd(v, "v")
     if (tv, hv, dv) != (t, hkv, d):
@@ -808,8 +808,8 @@ def nvfp4_kv_extend(new_tokens, seq_lens, page_table, free_pages, free_count, to
     page_table int32 [B, max_pages] (entries of new pages are written), free_pages int32
     [pages] of which the first free_count (int32 [1]) are free and the last of those are taken.
     ``tokens``: rows of positions and slots (default: one per sequence).  ``start`` int32 [B]:
-    added to the positions.  seq_lens_out and free_count_out may be seq_lens and free_count:
-    a captured step then advances them in place.  A call that does not fit (pages, rows, the
+    added to the positions.  seq_lens_out and free_count_out may be seq_lens and free_count (no
+    other output may lie over an argument): a captured step then advances them in place.  A call that does not fit (pages, rows, the
     table's width) changes nothing, gives no tokens and is reported by device_status()."""
     b, max_pages, ld, pages = _check_free(page_table, seq_lens, free_pages, free_count)
     if _int32(new_tokens, "new_tokens", 1)[0][0] != b:

@@ -16,6 +16,7 @@
 // Bound by latency: a launch, two dependent loads, the scan's barriers.
 #include <algorithm>
 #include <cstdint>
+#include <initializer_list>
 
 #include <cuda_runtime.h>
 
@@ -48,7 +49,8 @@ __device__ __forceinline__ Total block_scan(int64_t t, int64_t p, Total* warps, 
   int64_t st = t, sp = p;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int64_t a = __shfl_up_sync(0xFFFFFFFFu, st, off), b = __shfl_up_sync(0xFFFFFFFFu, sp, off);
+    const int64_t a = __shfl_up_sync(0xFFFFFFFFu, st, off),
+                  b = __shfl_up_sync(0xFFFFFFFFu, sp, off);
     if (lane >= off) {
       st += a;
       sp += b;
@@ -199,7 +201,8 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const ExtendArgs a) {
         }
         const int tok = g.y + (row - at), held = pages_of(g.y);
         const int i = tok / kPage;
-        const int page = i < held ? a.table[b * a.ld_table + i] : a.free_pages[count - 1 - (k + i - held)];
+        const int page = i < held ? a.table[b * a.ld_table + i]
+                                  : a.free_pages[count - 1 - (k + i - held)];
         pos = tok + (a.start == nullptr ? 0 : a.start[b]);
         if (page >= 0 && page < a.num_pages)
           slot = static_cast<int64_t>(page) * kPage + tok % kPage;
@@ -315,6 +318,30 @@ nvq_status check_tables(int B, const int32_t* seq_lens, const int32_t* page_tabl
   return B > 65535 ? NVQ_ERR_UNSUPPORTED : NVQ_OK;
 }
 
+struct Range {
+  const void* p;
+  uint64_t n;  // bytes
+};
+
+// What is written lies apart from everything else: threads read their inputs at any time until the
+// block's last barrier, and of many tokens in a second kernel.
+bool apart(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+  const auto meet = [](const Range& a, const Range& b) {
+    return a.n > 0 && b.n > 0 && ranges_meet(a.p, a.n, b.p, b.n);
+  };
+  for (const Range* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Range* x = o + 1; x != outs.end(); ++x)
+      if (meet(*o, *x)) return false;
+    for (const Range& x : ins)
+      if (meet(*o, x)) return false;
+  }
+  return true;
+}
+
+uint64_t table_bytes(int B, int64_t ld, int max_pages) {
+  return 4 * static_cast<uint64_t>((B - 1) * ld + max_pages);
+}
+
 }  // namespace
 
 }  // namespace nvq
@@ -336,6 +363,16 @@ nvq_status nvfp4_kv_extend(const int32_t* new_tokens, const int32_t* seq_lens,
       (T > 0 && (!aligned(positions, 4) || !aligned(slots, 8))))
     return NVQ_ERR_INVALID;
   if (T > 0x7FFFFFFF) return NVQ_ERR_UNSUPPORTED;
+  const uint64_t seqs = 4 * static_cast<uint64_t>(B), none = 0;
+  const uint64_t rows = static_cast<uint64_t>(T);
+  if (!apart({{seq_lens_out, seqs}, {free_count_out, 4}, {cu_tokens, seqs + 4},
+              {positions, 4 * rows}, {slots, 8 * rows},
+              {page_table, table_bytes(B, ld_table, max_pages)}},
+             {{new_tokens, seqs}, {start, start != nullptr ? seqs : none},
+              {seq_lens, seq_lens != seq_lens_out ? seqs : none},
+              {free_count, free_count != free_count_out ? 4 : none},
+              {free_pages, 4 * static_cast<uint64_t>(num_pages)}}))
+    return NVQ_ERR_INVALID;
   int* err = device_error_word();
   if (err == nullptr) return NVQ_ERR_CUDA;
   const ExtendArgs a{new_tokens, seq_lens, start, B, page_table, ld_table, max_pages, free_pages,
@@ -363,6 +400,13 @@ nvq_status nvfp4_kv_release(const uint8_t* done, const int32_t* seq_lens, int B,
                                num_pages, seq_lens_out, free_count_out);
   if (st != NVQ_OK) return st;
   if (done == nullptr) return NVQ_ERR_INVALID;
+  const uint64_t seqs = 4 * static_cast<uint64_t>(B), none = 0;
+  if (!apart({{seq_lens_out, seqs}, {free_count_out, 4},
+              {free_pages, 4 * static_cast<uint64_t>(num_pages)}},
+             {{done, static_cast<uint64_t>(B)}, {seq_lens, seq_lens != seq_lens_out ? seqs : none},
+              {free_count, free_count != free_count_out ? 4 : none},
+              {page_table, table_bytes(B, ld_table, max_pages)}}))
+    return NVQ_ERR_INVALID;
   int* err = device_error_word();
   if (err == nullptr) return NVQ_ERR_CUDA;
   const ReleaseArgs a{done, seq_lens, B, page_table, ld_table, max_pages, free_pages, free_count,

@@ -43,6 +43,39 @@ def test_release_refusals(lib):
     assert rel(b=65536) == UNSUPPORTED
 
 
+def test_outputs_over_other_arguments_are_refused(lib):
+    """Every other argument on a range of its own, then one output at a time over another (the
+    starts as the lengths that the call writes: a second kernel would read them too late)."""
+    names = "new lens start table free count lens_out count_out cu pos slots".split()
+    at = {n: A + 0x10000 * i for i, n in enumerate(names)}
+
+    def ext(b=3, t=5, ld=6, **over):
+        g = at | over
+        return lib.nvfp4_kv_extend(g["new"], g["lens"], g["start"], b, g["table"], ld, 4, g["free"],
+                                   g["count"], 8, t, g["lens_out"], g["count_out"], g["cu"],
+                                   g["pos"], g["slots"], None)
+    size = dict(new=12, lens=12, start=12, table=64, free=32, count=4, lens_out=12, count_out=4,
+                cu=16, pos=20, slots=40)
+    for out in ("lens_out", "count_out", "cu", "pos", "slots", "table"):
+        for other in names:
+            step = 8 if out == "slots" else 4
+            last = at[other] + (size[other] - 1) // step * step  # its last word
+            if other != out and not (out, other) == ("count_out", "count"):
+                assert ext(**{out: last}) == INVALID, (out, other)
+    assert ext(lens_out=at["lens"] + 4) == INVALID
+    assert ext(start=at["lens_out"], lens=at["lens_out"]) == INVALID
+    assert ext(t=0, pos=at["table"] + 8, slots=at["table"] + 16, lens_out=at["cu"]) == INVALID
+
+    def rel(b=3, **over):
+        g = at | over
+        return lib.nvfp4_kv_release(g["new"], g["lens"], b, g["table"], 6, 4, g["free"], g["count"],
+                                    8, g["lens_out"], g["count_out"], None)
+    for over in (dict(lens_out=at["table"] + 60), dict(lens_out=at["free"]), dict(lens_out=at["new"]),
+                 dict(count_out=at["free"] + 28), dict(free=at["table"] + 32), dict(free=at["lens"]),
+                 dict(count_out=at["lens_out"] + 8), dict(free=at["count"] - 28)):
+        assert rel(**over) == INVALID, over
+
+
 def test_append_slots_refusals(lib):
     def app(k=A, ld_k=256, v=A, ld_v=256, t=3, hkv=2, d=128, slots=A, pool=A, pages=8):
         return lib.nvfp4_kv_append_slots(k, ld_k, v, ld_v, t, hkv, d, slots, pool, pages, None)

@@ -30,6 +30,16 @@
 //              refers to is raised only where a score exceeds it by 8 (log2); the row's thread
 //              then rescales O itself
 // p is rounded to f16 (below 2^8), its sum taken before the rounding; all sums are fp32.
+//
+// Measured, in a replayed graph: 32760 tokens x 12 heads over 512 keys 120 us (0.86 PFLOP/s, 43% of
+// the bf16 rate; plain 9158 us), four latents of up to 6272 tokens 102 us, nine short pieces 24.5
+// us; 32 sequences x 64 heads behind 131072 shared keys 130 us with the join and the sequences' own
+// keys (1.0 PFLOP/s; one read of the prefix takes 22 us).  A tile takes 3800 cycles, of which its
+// MMAs need 1280 and its exponentials 1024: the bound is the chain of waits between the roles
+// (150 to 300 cycles each beside four other warps of the scheduler), and in short segments q~ and
+// the rows on their way out.  Slower were: P beside S with S a unit ahead for each stream (146 us
+// where this is 130), with two warps for P V~ at 80 registers a thread (147), one warp for S and two
+// for P V~ (140), 128-key units, sixteen softmax warps.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

@@ -115,7 +115,7 @@ struct DecodeArgs {
   int window, sinks;
   __nv_bfloat16* o;
   float* lse;
-  const float* prior_o;   // [B, H, D]: o over other keys (a shared prefix), or null
+  const float* prior_o;   // [B, H, D]: o over other keys (a shared prefix); read if kFold
   const float* prior_l2;  // [B, H]: its logarithm of the sum of exponentials, base 2
   struct RunInfo* split;  // what crosses runs, by run or by segment (workspace)
   int by_segment;         // 1: entries by segment (there are fewer than runs)
@@ -477,7 +477,9 @@ struct Ring {
   }
 };
 
-template <int D, int NT, int kRunsPerCta>
+// kFold: what is over other keys (a.prior_o, a.prior_l2) goes into each row.  An instance of its
+// own: with the choice at run time heads of 64 behind a window took 15.9 us instead of 15.2.
+template <int D, int NT, int kRunsPerCta, bool kFold>
 __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tk32, const DecodeArgs a) {
@@ -703,7 +705,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
         const int64_t row0 = static_cast<int64_t>(b) * a.H;
         for (int x = lane; x < a.H * (D / 8); x += 32) {
           uint4 v = make_uint4(0, 0, 0, 0);
-          if (a.prior_o != nullptr && a.prior_l2[row0 + x / (D / 8)] != -INFINITY) {
+          if (kFold && a.prior_l2[row0 + x / (D / 8)] != -INFINITY) {
             const float4* p = reinterpret_cast<const float4*>(a.prior_o + row0 * D) + 2 * x;
             const float4 lo = p[0], hi = p[1];
             v = make_uint4(pack_bf16x2(lo.x, lo.y), pack_bf16x2(lo.z, lo.w),
@@ -713,7 +715,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
         }
         if (a.lse != nullptr)
           for (int x = lane; x < a.H; x += 32)
-            a.lse[row0 + x] = a.prior_o != nullptr ? a.prior_l2[row0 + x] * kLn2 : -INFINITY;
+            a.lse[row0 + x] = kFold ? a.prior_l2[row0 + x] * kLn2 : -INFINITY;
       }
     }
     Ring ring;
@@ -825,7 +827,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
         }
         const int64_t row = static_cast<int64_t>(td.b) * a.H + hk * a.G + g0 + head;
         Fold f{1.f, 0.f};
-        const bool folds = a.prior_o != nullptr && td.slot < 0;
+        const bool folds = kFold && td.slot < 0;
         if (folds) f = fold_prior(a.prior_l2[row], mx, l);
         const float inv = l > 0.f ? 1.f / l : 0.f;
         float* part = a.parts + static_cast<int64_t>(max(td.slot, 0)) * part_floats(D, C::kHeads);
@@ -878,7 +880,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
 // of what crosses runs, heads [y, y + 1) kHeads / gridDim.y.  Sixteen or 32 lanes of
 // four stored positions take one head; where fewer heads than lane groups are left,
 // the groups share the parts and meet in shared memory.
-template <int D, int NT, int kThreads>
+template <int D, int NT, int kThreads, bool kFold>
 __global__ void __launch_bounds__(kThreads) join_kernel(const DecodeArgs a) {
   constexpr int kHeads = 8 * NT, kLanes = D / 4, kGroups = kThreads / kLanes;
   constexpr int kFloats = part_floats(D, kHeads);
@@ -943,7 +945,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const DecodeArgs a) {
     }
     if (sub == 0 && g0 + head < a.G) {
       const int64_t row = static_cast<int64_t>(r.b) * a.H + r.hg / a.chunks * a.G + g0 + head;
-      if (a.prior_o != nullptr) {
+      if constexpr (kFold) {
         const Fold f = fold_prior(a.prior_l2[row], mx, l);
         float2 p = make_float2(0.f, 0.f), q = p;
         if (f.other != 0.f) {
@@ -1014,11 +1016,11 @@ Plan plan(int B, int H, int Hkv, int D, int max_pages, int window, int sinks) {
   return p;
 }
 
-template <int D, int NT, int kRunsPerCta>
+template <int D, int NT, int kRunsPerCta, bool kFold>
 cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tk32, const DecodeArgs& a,
                           const Plan& p, cudaStream_t stream) {
   using C = Cfg<D, NT, kRunsPerCta>;
-  const auto kernel = decode_kernel<D, NT, kRunsPerCta>;
+  const auto kernel = decode_kernel<D, NT, kRunsPerCta, kFold>;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
@@ -1027,8 +1029,8 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tk32, const 
     return e;
   const dim3 grid(p.join_x, p.join_y);
   if (p.join_threads == 1024)
-    return launch_pdl(join_kernel<D, NT, 1024>, grid, dim3(1024), 0, stream, 1, a);
-  return launch_pdl(join_kernel<D, NT, 256>, grid, dim3(256), 0, stream, 1, a);
+    return launch_pdl(join_kernel<D, NT, 1024, kFold>, grid, dim3(1024), 0, stream, 1, a);
+  return launch_pdl(join_kernel<D, NT, 256, kFold>, grid, dim3(256), 0, stream, 1, a);
 }
 
 }  // namespace
@@ -1038,6 +1040,17 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tk32, const 
 namespace nvq {
 
 namespace {
+
+template <bool kFold>
+cudaError_t launch_decode_form(int D, const CUtensorMap& tk, const CUtensorMap& tk32,
+                               const DecodeArgs& a, const Plan& p, cudaStream_t stream) {
+  if (D == 128)
+    return p.nt == 1 ? launch_decode<128, 1, 3, kFold>(tk, tk32, a, p, stream)
+                     : launch_decode<128, 2, 2, kFold>(tk, tk32, a, p, stream);
+  if (p.nt == 2) return launch_decode<64, 2, 2, kFold>(tk, tk32, a, p, stream);
+  return p.per_cta == 4 ? launch_decode<64, 1, 4, kFold>(tk, tk32, a, p, stream)
+                        : launch_decode<64, 1, 3, kFold>(tk, tk32, a, p, stream);
+}
 
 // The call behind the entry points: arguments as in attn_qat_decode; prior_o, prior_l2 as in
 // DecodeArgs.
@@ -1061,12 +1074,8 @@ nvq_status run_decode(const void* q, int64_t ld_q, const void* pool, int64_t num
                      reinterpret_cast<float*>(wb + p.parts), p.runs,
                      ~uint64_t{0} / p.runs + 1, err};
   const cudaError_t e = timed(NVQ_KERNEL_DECODE, stream, [&] {
-    if (D == 128)
-      return p.nt == 1 ? launch_decode<128, 1, 3>(tk, tk32, a, p, stream)
-                       : launch_decode<128, 2, 2>(tk, tk32, a, p, stream);
-    if (p.nt == 2) return launch_decode<64, 2, 2>(tk, tk32, a, p, stream);
-    return p.per_cta == 4 ? launch_decode<64, 1, 4>(tk, tk32, a, p, stream)
-                          : launch_decode<64, 1, 3>(tk, tk32, a, p, stream);
+    return prior_o != nullptr ? launch_decode_form<true>(D, tk, tk32, a, p, stream)
+                              : launch_decode_form<false>(D, tk, tk32, a, p, stream);
   });
   return e == cudaSuccess ? NVQ_OK : fail_cuda("attn decode", e);
 }

@@ -198,6 +198,23 @@ int make_kv_codes_map(CUtensorMap* map, const void* pool, int64_t records, int D
   return static_cast<int>(r);
 }
 
+int make_rows_map(CUtensorMap* map, const void* base, int64_t T, int H, int D, int heads,
+                  int tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return CUDA_ERROR_NOT_FOUND;
+  const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
+                              static_cast<cuuint64_t>(T), 1};
+  const cuuint64_t strides[3] = {row, row * H, row * H * static_cast<cuuint64_t>(T)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return static_cast<int>(r);
+}
+
 int* device_error_word() { return error_word(); }
 
 int make_codes_map(CUtensorMap* map, const void* base, int64_t rows, int64_t row_bytes,

@@ -88,9 +88,9 @@ struct Cfg {
   static constexpr uint32_t kVAt = kStages * kRec;       // [2]
   static constexpr uint32_t kQAt = kVAt + 2 * kV;        // [2][2 halves]
   static constexpr uint32_t kQScAt = kQAt + 4 * kQ;      // [2][2]
-  static constexpr uint32_t kOutAt = kQScAt + 4 * kQSc;  // bf16 rows of o on their way out,
-  static constexpr uint32_t kOutRow = D * 2 + 16;        // apart by an odd number of 16 bytes
-  static constexpr uint32_t kMlAt = kOutAt + kPair * kOutRow;  // float2 [128]: (m, l), other keys
+  static constexpr uint32_t kOutAt = kQScAt + 4 * kQSc;  // rows of o on their way out: of each
+  static constexpr uint32_t kOut = 32 * D * 2;           // warp 32 of 2 D bytes
+  static constexpr uint32_t kMlAt = kOutAt + kPair / 32 * kOut;  // float2 [128]: (m, l), other keys
   static constexpr uint32_t kDescAt = kMlAt + kRows * 8;
   static constexpr uint32_t kSegAt = kDescAt + kStages * 16;   // Segment [kSegs]
   static constexpr uint32_t kUnitAt = kSegAt + kSegs * 48;       // int [2 streams][3 (4)]
@@ -99,7 +99,7 @@ struct Cfg {
   // heads of 64: padded so that no CTA of the few-rows linear lies beside one
   static constexpr uint32_t kUsed = kBarAt + kBars * 8 + 1024;
   static constexpr uint32_t kSmem = kUsed > 152 * 1024 ? kUsed : 152 * 1024;
-  static_assert(kRec % 1024 == 0 && kQ % 1024 == 0, "swizzle atoms");
+  static_assert(kRec % 1024 == 0 && kQ % 1024 == 0 && kOutAt % 1024 == 0, "swizzle atoms");
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(apart_from_linear_small(kSmem), "tensor memory");
 };
@@ -133,6 +133,7 @@ struct CrossArgs {
   const int32_t* cu;
   int per_seq;  // tokens of each sequence where cu is null
   int B, H, Hkv, G;
+  int tiles;  // whole warps' rows of o go by the tensor map: G divides 32
   float scale_log2;
   __nv_bfloat16* o;  // or, where null, o32 with the logarithms (base 2) in lse
   float* o32;
@@ -527,7 +528,8 @@ __device__ __forceinline__ void describe(const CrossArgs& a, const Walk& w, int 
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    cross_kernel(const __grid_constant__ CUtensorMap tk, const CrossArgs a) {
+    cross_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap to,
+                 const CrossArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int64_t warp_sum[kThreads / 32];
@@ -616,8 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (lane == 31) warp_sum[warp] = scan;
   __syncthreads();
   int64_t all = 0;
+  const int busy = ((a.B + per - 1) / per + 31) / 32;  // warps that have sequences
 #pragma unroll 1
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < busy; ++w) {
     if (w < warp) scan += warp_sum[w];
     all += warp_sum[w];
   }
@@ -638,16 +641,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         at += n;
       }
     }
-    int64_t nth;  // segment of the sequence
-    int i;
-    if (u0 - at < (int64_t{1} << 31)) {
-      nth = static_cast<uint32_t>(u0 - at) / static_cast<uint32_t>(e.key_tiles);
+    // the run's first segment of the sequence, and the first of its tiles
+    int hk, rt, i;
+    const int64_t x = u0 - at;
+    if (x < (int64_t{1} << 31)) {
+      const uint32_t y = static_cast<uint32_t>(x), nth = y / static_cast<uint32_t>(e.key_tiles);
+      i = static_cast<int>(y - nth * e.key_tiles);
+      hk = static_cast<int>(nth / static_cast<uint32_t>(e.row_tiles));
+      rt = static_cast<int>(nth - hk * e.row_tiles);
     } else {
-      nth = (u0 - at) / e.key_tiles;
+      const int64_t nth = x / e.key_tiles;
+      i = static_cast<int>(x - nth * e.key_tiles);
+      hk = static_cast<int>(nth / e.row_tiles);
+      rt = static_cast<int>(nth - static_cast<int64_t>(hk) * e.row_tiles);
     }
-    i = static_cast<int>(u0 - at - nth * e.key_tiles);
-    const int hk = static_cast<int>(nth / e.row_tiles);
-    start = {at, e, s, hk, static_cast<int>(nth - static_cast<int64_t>(hk) * e.row_tiles), i};
+    start = {at, e, s, hk, rt, i};
   }
   tc_fence_before();
   __syncthreads();
@@ -935,10 +943,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive_warp(&p_full[buf]);
       if (!(what & kUnitEnd)) continue;
-      // ---- the segment's end
+      // ---- the segment's end: what does not need O, while its last PV is on its way
       const Segment& sg = segs[ends % kSegs];
-      if (!wait(&o_full[stream], ends++ & 1, abort)) break;
-      tc_fence_after();
+      const uint32_t o_phase = ends++ & 1;
       float l0, l1;
       up2(l2, l0, l1);
       float l = l0 + l1, own = 1.f, other = 0.f;
@@ -948,6 +955,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t at = static_cast<int64_t>(sg.tok0 + tok) * a.H + sg.hk * a.G + row - tok * a.G;
       if (!both && stream == 1) {  // the warp that has the other keys of these rows takes both
         if (live) ml[r] = make_float2(m, l);
+        if (!wait(&o_full[1], o_phase, abort)) break;
+        tc_fence_before();
         mbar_arrive_warp(&merge[quarter]);
         continue;
       }
@@ -973,16 +982,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (a.lse != nullptr)
           a.lse[at] = row_lse(a, m, l);
       }
-      // The warp's rows go through shared memory, so that it stores whole rows, 512 bytes at a time
-      // (16 bytes of 32 rows at a time kept it for 9000 cycles a segment, more than two tiles'
-      // softmax; a bulk copy for each row for 2500): bf16 rows at once, halves of fp32 ones.
+      // The warp's rows go through shared memory (16-byte pieces in the 128-byte swizzle): 32 whole
+      // rows of o as tiles that one lane hands over, others a row at a time, 512 bytes a store;
+      // bf16 rows at once, fp32 ones in two halves.  (Stores of 16 bytes of 32 rows kept the warp
+      // for 9000 cycles a segment, more than two tiles' softmax, a bulk copy for each row for 2500,
+      // the rows' stores for 2700, the tiles for 500.)
       const bool narrow = slot < 0 && a.o != nullptr;
-      uint8_t* const out = narrow       ? reinterpret_cast<uint8_t*>(a.o + at * D)
-                           : slot < 0 ? reinterpret_cast<uint8_t*>(a.o32 + at * D)
-                                      : reinterpret_cast<uint8_t*>(part + 2 * a.part_rows + r * D);
-      uint8_t* const area = smem + C::kOutAt + 32 * warp * C::kOutRow;
       const int there = rows - (r - lane);  // rows of the warp's 32
+      const bool tiles = narrow && a.tiles && there >= 32;
+      uint8_t* const area = smem + C::kOutAt + (4 * stream + quarter) * C::kOut;
+      const auto piece = [&](int n, int c) {
+        return reinterpret_cast<uint4*>(area + (c >> 3) * 4096 + n * 128 + (((c ^ n) & 7) << 4));
+      };
       const int cols = narrow ? D : D / 2;
+      if (lane == 0) bulk_wait_group_read<0>();  // of the segment before
+      if (!wait(&o_full[stream], o_phase, abort)) break;
+      tc_fence_after();
 #pragma unroll 1
       for (int x0 = 0; x0 < D; x0 += cols) {
         if (live) {
@@ -1000,24 +1015,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[i + 1] = __float_as_uint(z1);
             }
             if (!both) {
-              uint32_t z[32];
-              tmem_ld32(o_at + D + x, z);
-              tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                v[i] = __float_as_uint(fmaf(__uint_as_float(z[i]), other, __uint_as_float(v[i])));
+              for (int h = 0; h < 32; h += 16) {
+                uint32_t z[16];
+                tmem_ld16(o_at + D + x + h, z);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  v[h + i] = __float_as_uint(
+                      fmaf(__uint_as_float(z[i]), other, __uint_as_float(v[h + i])));
+              }
             }
             if (narrow) {
-              uint4* dst = reinterpret_cast<uint4*>(area + lane * C::kOutRow + 2 * x);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                dst[i] = make_uint4(pack_bf16(v + 8 * i), pack_bf16(v + 8 * i + 2),
-                                    pack_bf16(v + 8 * i + 4), pack_bf16(v + 8 * i + 6));
+                *piece(lane, x / 8 + i) =
+                    make_uint4(pack_bf16(v + 8 * i), pack_bf16(v + 8 * i + 2),
+                               pack_bf16(v + 8 * i + 4), pack_bf16(v + 8 * i + 6));
             } else {
-              uint4* dst = reinterpret_cast<uint4*>(area + lane * C::kOutRow + 4 * (x - x0));
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                *piece(lane, (x - x0) / 4 + i) =
+                    make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
           }
         }
@@ -1026,22 +1045,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_warp(&o_read[stream]);
           if (!both) mbar_arrive_warp(&o_read[1]);
         }
+        if (tiles) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+#pragma unroll
+            for (int x = 0; x < D; x += 64)
+              tma_store_4d(&to, area + x * 64, x, sg.hk * a.G, sg.tok0 + tok, 0);
+            bulk_commit_group();
+          }
+          break;
+        }
         __syncwarp();
+        uint8_t* const out = narrow       ? reinterpret_cast<uint8_t*>(a.o + at * D)
+                             : slot < 0 ? reinterpret_cast<uint8_t*>(a.o32 + at * D)
+                                        : reinterpret_cast<uint8_t*>(part + 2 * a.part_rows + r * D);
         constexpr int kAtOnce = 32 * 16 / (2 * D);  // rows of 2 D bytes in a store of the warp
-        const int sub = lane / (32 / kAtOnce);
+        const int sub = lane / (32 / kAtOnce), c = lane % (32 / kAtOnce);
 #pragma unroll 4
         for (int i = 0; i < 32; i += kAtOnce) {
-          const unsigned long long to =
+          const unsigned long long dst =
               __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(out), i + sub);
-          if (i + sub < there) {
-            const int at16 = lane % (32 / kAtOnce) * 16;
-            const uint4 w = *reinterpret_cast<const uint4*>(area + (i + sub) * C::kOutRow + at16);
-            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(to) + 4 * x0 + at16) = w;
-          }
+          if (i + sub < there)
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(dst) + 4 * x0 + 16 * c) =
+                *piece(i + sub, c);
         }
         __syncwarp();
       }
     }
+    if (lane == 0) bulk_wait_group<0>();
   } else if (warp >= kQWarp && warp < kProducerWarp) {
     // ------------------------------------------------------------ q~
     const int t = threadIdx.x - 32 * kQWarp;
@@ -1170,14 +1202,15 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a) {
 }
 
 template <int D>
-cudaError_t launch_cross_d(const CUtensorMap& tk, const CrossArgs& a, cudaStream_t stream) {
+cudaError_t launch_cross_d(const CUtensorMap& tk, const CUtensorMap& to, const CrossArgs& a,
+                           cudaStream_t stream) {
   using C = Cfg<D>;
   const cudaError_t e = cudaFuncSetAttribute(
       cross_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(a.runs));
   const cudaError_t k =
-      launch_pdl(cross_kernel<D>, grid, dim3(kThreads), C::kSmem, stream, 1, tk, a);
+      launch_pdl(cross_kernel<D>, grid, dim3(kThreads), C::kSmem, stream, 1, tk, to, a);
   if (k != cudaSuccess) return k;
   return launch_pdl(cross_join_kernel<D>,
                     dim3(grid.x, static_cast<unsigned>(a.part_rows * (D / 4) / 256)), dim3(256), 0,
@@ -1226,15 +1259,21 @@ nvq_status launch_cross(const CrossCall& c, uint8_t* ws, cudaStream_t stream) {
   CUtensorMap tk;
   if (const int r = make_kv_codes_map(&tk, c.pool, c.num_pages * c.Hkv, c.D, kPage); r != 0)
     return fail_driver("cuTensorMapEncodeTiled", r);
+  const int G = c.H / c.Hkv;
+  CUtensorMap to = tk;
+  if (c.o != nullptr && 32 % G == 0)
+    if (const int r = make_rows_map(&to, c.o, c.T, c.H, c.D, G, 32 / G); r != 0)
+      return fail_driver("cuTensorMapEncodeTiled", r);
   const CrossArgs a{static_cast<const uint16_t*>(c.q), c.ld_q, static_cast<int>(c.T),
                     static_cast<const uint8_t*>(c.pool), c.num_pages, c.page_table, c.ld_table,
                     c.max_pages, c.kv_lens, c.cu_tokens, static_cast<int>(c.T / c.B), c.B, c.H,
-                    c.Hkv, c.H / c.Hkv, c.scale * kLog2e, static_cast<__nv_bfloat16*>(c.o), c.o32,
+                    c.Hkv, G, c.o != nullptr && 32 % G == 0, c.scale * kLog2e, static_cast<__nv_bfloat16*>(c.o), c.o32,
                     c.lse, reinterpret_cast<Split*>(ws),
                     reinterpret_cast<float*>(ws + p.parts),
                     p.part_rows, p.runs, ~uint64_t{0} / p.runs + 1, err};
   const cudaError_t e = timed(NVQ_KERNEL_CROSS, stream, [&] {
-    return c.D == 128 ? launch_cross_d<128>(tk, a, stream) : launch_cross_d<64>(tk, a, stream);
+    return c.D == 128 ? launch_cross_d<128>(tk, to, a, stream)
+                      : launch_cross_d<64>(tk, to, a, stream);
   });
   return e == cudaSuccess ? NVQ_OK : fail_cuda("attn cross", e);
 }

@@ -31,15 +31,15 @@
 //              then rescales O itself
 // p is rounded to f16 (below 2^8), its sum taken before the rounding; all sums are fp32.
 //
-// Measured, in a replayed graph: 32760 tokens x 12 heads over 512 keys 120 us (0.86 PFLOP/s, 43% of
-// the bf16 rate; plain 9158 us), four latents of up to 6272 tokens 102 us, nine short pieces 24.5
+// Measured, in a replayed graph: 32760 tokens x 12 heads over 512 keys 113 us (0.91 PFLOP/s, 46% of
+// the bf16 rate; plain 9158 us), four latents of up to 6272 tokens 100 us, nine short pieces 23.7
 // us; 32 sequences x 64 heads behind 131072 shared keys 130 us with the join and the sequences' own
-// keys (1.0 PFLOP/s; one read of the prefix takes 22 us).  A tile takes 3800 cycles, of which its
-// MMAs need 1280 and its exponentials 1024: the bound is the chain of waits between the roles
-// (150 to 300 cycles each beside four other warps of the scheduler), and in short segments q~ and
-// the rows on their way out.  Slower were: P beside S with S a unit ahead for each stream (146 us
-// where this is 130), with two warps for P V~ at 80 registers a thread (147), one warp for S and two
-// for P V~ (140), 128-key units, sixteen softmax warps.
+// keys (1.06 PFLOP/s; one read of the prefix takes 22 us).  A tile takes 3400 to 3800 cycles, of
+// which its MMAs need 1280 and its exponentials 1024: the bound is the chain of waits between the
+// roles (150 to 300 cycles each beside four other warps of the scheduler), and in short segments q~
+// and the rows on their way out (4000 cycles a segment).  Slower were: P beside S with S a unit
+// ahead for each stream (146 us where this is 130), with two warps for P V~ at 80 registers a thread
+// (147), one warp for S and two for P V~ (140), 128-key units, sixteen softmax warps.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -90,12 +90,12 @@ struct Cfg {
   static constexpr uint32_t kQScAt = kQAt + 4 * kQ;      // [2][2]
   static constexpr uint32_t kOutAt = kQScAt + 4 * kQSc;  // rows of o on their way out: of each
   static constexpr uint32_t kOut = 32 * D * 2;           // warp 32 of 2 D bytes
-  static constexpr uint32_t kMlAt = kOutAt + kPair / 32 * kOut;  // float2 [128]: (m, l), other keys
-  static constexpr uint32_t kDescAt = kMlAt + kRows * 8;
+  static constexpr uint32_t kMlAt = kOutAt + kPair / 32 * kOut;  // float2 [2][128]: streams' (m, l)
+  static constexpr uint32_t kDescAt = kMlAt + 2 * kRows * 8;
   static constexpr uint32_t kSegAt = kDescAt + kStages * 16;   // Segment [kSegs]
   static constexpr uint32_t kUnitAt = kSegAt + kSegs * 48;       // int [2 streams][3 (4)]
   static constexpr uint32_t kBarAt = kUnitAt + 32;
-  static constexpr int kBars = 3 * kStages + 4 * 2 + 4 * 3 + 2 * 2 + 3 + 4 + kSegs + 1;
+  static constexpr int kBars = 3 * kStages + 4 * 2 + 4 * 3 + 2 * 2 + 3 + 8 + kSegs + 1;
   // heads of 64: padded so that no CTA of the few-rows linear lies beside one
   static constexpr uint32_t kUsed = kBarAt + kBars * 8 + 1024;
   static constexpr uint32_t kSmem = kUsed > 152 * 1024 ? kUsed : 152 * 1024;
@@ -533,7 +533,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int64_t warp_sum[kThreads / 32];
-  __shared__ Start start;
   __shared__ alignas(8) unsigned char walk_bytes[sizeof(Walk)];  // of the query warps' first thread
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -552,10 +551,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = s_full + 6;          // [3] by the unit's buffer, four softmax warps
   uint64_t* pv_done = p_full + 3;         // [3]
   uint64_t* o_full = pv_done + 3;         // [2 streams]: a segment's last PV is done
-  uint64_t* o_read = o_full + 2;          // [2 streams], four softmax warps (of either stream)
+  uint64_t* o_read = o_full + 2;          // [2 streams], eight: two by each of its softmax warps,
+                                          // or one by each of both streams'
   uint64_t* drain = o_read + 2;           // [3]
-  uint64_t* merge = drain + 3;            // [4]: by 32 rows, the other keys' sums are done
-  uint64_t* described = merge + 4;        // [kSegs]
+  uint64_t* merge = drain + 3;            // [2 streams][4]: by 32 rows, the stream's keys are done
+  uint64_t* described = merge + 8;        // [kSegs]
   uint64_t* q_first = described + kSegs;  // the other warps that quantize the run's first segment
   Segment* segs = reinterpret_cast<Segment*>(smem + C::kSegAt);
   int* units = reinterpret_cast<int*>(smem + C::kUnitAt);  // by s_full: keys with tokens, flags
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto walk = [&]() -> Walk& { return *reinterpret_cast<Walk*>(walk_bytes); };
   pdl_trigger();
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32 * kProducerWarp) {  // (the first warps look at sequences meanwhile)
     abort_word = 0;
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[i], 4);
       mbar_init(&q_empty[i], 2);
       mbar_init(&o_full[i], 1);
-      mbar_init(&o_read[i], 4);
+      mbar_init(&o_read[i], 8);
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(&s_full[i], 2);  // the MMAs, and what the S warp tells of the unit
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&pv_done[i], 1);
       mbar_init(&drain[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&merge[i], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&merge[i], 1);
     for (int i = 0; i < kSegs; ++i) mbar_init(&described[i], 1);
     mbar_init(q_first, kQWarp);
     fence_mbar_init();
@@ -655,8 +655,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       hk = static_cast<int>(nth / e.row_tiles);
       rt = static_cast<int>(nth - static_cast<int64_t>(hk) * e.row_tiles);
     }
-    start = {at, e, s, hk, rt, i};
+    // the run's first segment, described before anyone looks
+    const Start st{at, e, s, hk, rt, i};
+    const Walk w(st, static_cast<int>(u1 - u0));
+    walk() = w;
+    a.split[run].end = -1;
+    describe(a, w, run, u0, u1, all, segs[0], &described[0]);
   }
+  if (u0 == u1 && threadIdx.x == 0) a.split[run].end = -1;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -665,15 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- the run's first segment: nothing can begin before its q~, which took the query warps alone
   // 9000 cycles, so all that would wait for it help (64 tokens behind a shared prefix 55 -> 53 us)
-  if (threadIdx.x == 32 * kQWarp) {
-    a.split[run].end = -1;
-    if (n_tiles > 0) {
-      const Walk w(start, n_tiles);
-      walk() = w;
-      describe(a, w, run, u0, u1, all, segs[0], &described[0]);
-    }
-  }
-  if (warp < kProducerWarp && n_tiles > 0 && wait(&described[0], 0, abort)) {
+  if (warp < kProducerWarp && n_tiles > 0) {
     QueryTile<D, 32 * kProducerWarp> q;
     q.begin(a, segs[0], threadIdx.x);
     q.quantize(a, smem + C::kQAt, smem + C::kQScAt, threadIdx.x);
@@ -945,25 +943,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(what & kUnitEnd)) continue;
       // ---- the segment's end: what does not need O, while its last PV is on its way
       const Segment& sg = segs[ends % kSegs];
-      const uint32_t o_phase = ends++ & 1;
       float l0, l1;
       up2(l2, l0, l1);
       float l = l0 + l1, own = 1.f, other = 0.f;
       const int r = both ? threadIdx.x : threadIdx.x & (kRows - 1);  // row of the segment
-      const bool mine = r < rows;
       const int slot = sg.slot, row = sg.row0 + r, tok = row / a.G;
       const int64_t at = static_cast<int64_t>(sg.tok0 + tok) * a.H + sg.hk * a.G + row - tok * a.G;
-      if (!both && stream == 1) {  // the warp that has the other keys of these rows takes both
-        if (live) ml[r] = make_float2(m, l);
-        if (!wait(&o_full[1], o_phase, abort)) break;
+      if (lane == 0) bulk_wait_group_read<0>();  // of the segment before
+      if (!wait(&o_full[stream], ends++ & 1, abort)) break;
+      tc_fence_after();
+      if (!both) {  // the streams have halves of the keys: each takes half of the columns of both
+        if (live) ml[kRows * stream + r] = make_float2(m, l);
         tc_fence_before();
-        mbar_arrive_warp(&merge[quarter]);
-        continue;
-      }
-      if (!both) {
-        if (!wait(&merge[quarter], joins++ & 1, abort)) break;
+        mbar_arrive_warp(&merge[4 * stream + quarter]);
+        if (!wait(&merge[4 * (stream ^ 1) + quarter], joins++ & 1, abort)) break;
         tc_fence_after();
-        const float2 v = ml[r];
+        const float2 v = ml[kRows * (stream ^ 1) + r];
         const float top = fmaxf(m, v.x), ref = fmaxf(top, -3.4e38f);
         own = ex2_f32(m - ref);
         other = ex2_f32(v.x - ref);
@@ -976,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         other *= inv;
       }
       float* part = a.parts + max(slot, 0) * part_floats(a.part_rows, D);
-      if (mine) {
+      if (r < rows && (both || stream == 0)) {
         if (slot >= 0)
           *reinterpret_cast<float2*>(part + 2 * r) = make_float2(m, l);
         else if (a.lse != nullptr)
@@ -989,22 +984,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the rows' stores for 2700, the tiles for 500.)
       const bool narrow = slot < 0 && a.o != nullptr;
       const int there = rows - (r - lane);  // rows of the warp's 32
-      const bool tiles = narrow && a.tiles && there >= 32;
+      const int wide = both ? D : D / 2, x_end = both ? D : D / 2 + D / 2 * stream;
+      const int cols = narrow ? wide : D / 2;  // at a time
+      const bool tiles = narrow && a.tiles && there >= 32 && wide % 64 == 0;
+      const uint32_t o_other = stream == 0 ? o_at + D : o_at - D;
       uint8_t* const area = smem + C::kOutAt + (4 * stream + quarter) * C::kOut;
       const auto piece = [&](int n, int c) {
         return reinterpret_cast<uint4*>(area + (c >> 3) * 4096 + n * 128 + (((c ^ n) & 7) << 4));
       };
-      const int cols = narrow ? D : D / 2;
-      if (lane == 0) bulk_wait_group_read<0>();  // of the segment before
-      if (!wait(&o_full[stream], o_phase, abort)) break;
-      tc_fence_after();
 #pragma unroll 1
-      for (int x0 = 0; x0 < D; x0 += cols) {
+      for (int x0 = x_end - wide; x0 < x_end; x0 += cols) {
         if (live) {
 #pragma unroll 1
-          for (int x = x0; x < x0 + cols; x += 32) {
+          for (int x = 0; x < cols; x += 32) {
             uint32_t v[32];
-            tmem_ld32(o_at + x, v);
+            tmem_ld32(o_at + x0 + x, v);
             tmem_wait_ld();
             const uint64_t own2 = pk2(own, own);
 #pragma unroll
@@ -1018,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int h = 0; h < 32; h += 16) {
                 uint32_t z[16];
-                tmem_ld16(o_at + D + x + h, z);
+                tmem_ld16(o_other + x0 + x + h, z);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -1035,40 +1029,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                *piece(lane, (x - x0) / 4 + i) =
+                *piece(lane, x / 4 + i) =
                     make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
             }
           }
         }
-        if (x0 + cols == D) {
+        if (x0 + cols == x_end) {
           tc_fence_before();
           mbar_arrive_warp(&o_read[stream]);
-          if (!both) mbar_arrive_warp(&o_read[1]);
+          mbar_arrive_warp(&o_read[both ? stream : stream ^ 1]);
         }
         if (tiles) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-#pragma unroll
-            for (int x = 0; x < D; x += 64)
-              tma_store_4d(&to, area + x * 64, x, sg.hk * a.G, sg.tok0 + tok, 0);
+#pragma unroll 1
+            for (int x = 0; x < cols; x += 64)
+              tma_store_4d(&to, area + x * 64, x0 + x, sg.hk * a.G, sg.tok0 + tok, 0);
             bulk_commit_group();
           }
           break;
         }
         __syncwarp();
-        uint8_t* const out = narrow       ? reinterpret_cast<uint8_t*>(a.o + at * D)
-                             : slot < 0 ? reinterpret_cast<uint8_t*>(a.o32 + at * D)
-                                        : reinterpret_cast<uint8_t*>(part + 2 * a.part_rows + r * D);
-        constexpr int kAtOnce = 32 * 16 / (2 * D);  // rows of 2 D bytes in a store of the warp
-        const int sub = lane / (32 / kAtOnce), c = lane % (32 / kAtOnce);
+        float* const wide_row = slot < 0 ? a.o32 + at * D : part + 2 * a.part_rows + r * D;
+        uint8_t* const out = narrow ? reinterpret_cast<uint8_t*>(a.o + at * D + x0)
+                                    : reinterpret_cast<uint8_t*>(wide_row + x0);
+        // a row's pieces: 16 or 8 of heads of 128, 8 or 4 of heads of 64
+        constexpr int kLog = D == 128 ? 4 : 3;
+        const int log = narrow && !both ? kLog - 1 : kLog;
+        const int sub = lane >> log, c = lane & ((1 << log) - 1);
 #pragma unroll 4
-        for (int i = 0; i < 32; i += kAtOnce) {
+        for (int i = 0; i < 32; i += 32 >> log) {
           const unsigned long long dst =
               __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(out), i + sub);
           if (i + sub < there)
-            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(dst) + 4 * x0 + 16 * c) =
-                *piece(i + sub, c);
+            reinterpret_cast<uint4*>(dst)[c] = *piece(i + sub, c);
         }
         __syncwarp();
       }
@@ -1267,7 +1262,8 @@ nvq_status launch_cross(const CrossCall& c, uint8_t* ws, cudaStream_t stream) {
   const CrossArgs a{static_cast<const uint16_t*>(c.q), c.ld_q, static_cast<int>(c.T),
                     static_cast<const uint8_t*>(c.pool), c.num_pages, c.page_table, c.ld_table,
                     c.max_pages, c.kv_lens, c.cu_tokens, static_cast<int>(c.T / c.B), c.B, c.H,
-                    c.Hkv, G, c.o != nullptr && 32 % G == 0, c.scale * kLog2e, static_cast<__nv_bfloat16*>(c.o), c.o32,
+                    c.Hkv, G, c.o != nullptr && 32 % G == 0, c.scale * kLog2e,
+                    static_cast<__nv_bfloat16*>(c.o), c.o32,
                     c.lse, reinterpret_cast<Split*>(ws),
                     reinterpret_cast<float*>(ws + p.parts),
                     p.part_rows, p.runs, ~uint64_t{0} / p.runs + 1, err};

@@ -38,8 +38,8 @@
 // which its MMAs need 1280 and its exponentials 1024: the bound is the chain of waits between the
 // roles (150 to 300 cycles each beside four other warps of the scheduler), and in short segments q~
 // and the rows on their way out (4000 cycles a segment).  Slower were: P beside S with S a unit
-// ahead for each stream (146 us where this is 130), with two warps for P V~ at 80 registers a thread
-// (147), one warp for S and two for P V~ (140), 128-key units, sixteen softmax warps.
+// ahead for each stream (146 us where this is 130), the same with two warps for P V~ at 80
+// registers (147), one warp for S and two for P V~ (140), 128-key units, sixteen softmax warps.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

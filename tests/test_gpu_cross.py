@@ -56,6 +56,8 @@ CASES = [  # h, hkv, d, tokens, lengths
     (12, 12, 128, [130], [512]), (16, 1, 64, [17, 8, 9], [700, 17, 256]),
     (24, 2, 64, [11, 11], [383, 385]), (40, 1, 128, [7], [130]), (2, 1, 128, [700], [64]),
     (3, 3, 64, [129, 255, 1], [128, 256, 2000]), (1, 1, 128, [9], [5000]), (1, 1, 64, [400], [4100]),
+    (32, 1, 128, [9, 40], [300, 100]), (64, 2, 64, [3, 70], [130, 128]), (8, 8, 128, [100, 33], [128, 1]),
+    (96, 2, 64, [5, 11], [100, 260]),
 ]
 
 

@@ -135,3 +135,20 @@ def test_a_step_that_does_not_fit_writes_nothing_and_is_reported():
         assert torch.equal(t, v)
     assert step.slots.tolist() == [-1] * 512 and step.cu_tokens.tolist() == offsets([0] * 4)
     assert not bool(o.any()) and bool((lse == -float("inf")).all())
+
+
+def test_the_timing_files_each_call_under_its_kind():
+    server = Server(4, 2, 64)
+    x, ones = server.rows(4), ints([1] * 4)
+    server.step(x, ones, True)
+    api.timing_enable(True)
+    try:
+        server.step(x, ones, True)
+        api.nvfp4_kv_release(torch.zeros(4, dtype=torch.bool, device="cuda"), server.lens,
+                             server.table, server.free, server.count)
+        got = {k: n for k, (n, _) in api.timing_read().items() if n}
+    finally:
+        api.timing_enable(False)
+    # the prefix part is timed as cross attention, the fold as a decode
+    assert got == {"kv_tables": 2, "rope": 1, "kv_append": 1, "cross": 2, "decode": 1}
+    assert api.device_status() == 0

@@ -29,7 +29,10 @@
 //   2 x 4      softmax, one thread a row, a warpgroup for each stream.  The maximum that p
 //              refers to is raised only where a score exceeds it by 8 (log2); the row's thread
 //              then rescales O itself
-// p is rounded to f16 (below 2^8), its sum taken before the rounding; all sums are fp32.
+// p is rounded to f16, its sum taken before the rounding; all sums are fp32.  p is 2^7 where the
+// score is the reference maximum, so at most 2^15: f16 has no more room above, and 2^32 below the
+// best key a p is still seen (from 1 on, keys 2^25 below a dominant one vanished from O, not from
+// the sum).
 //
 // Measured, in a replayed graph: 32760 tokens x 12 heads over 512 keys 113 us (0.91 PFLOP/s, 46% of
 // the bf16 rate; plain 9158 us), four latents of up to 6272 tokens 100 us, nine short pieces 23.7
@@ -64,6 +67,7 @@ constexpr int kDecodeWarp = 8, kQWarp = 12, kProducerWarp = 16, kSWarp = 17, kPv
 constexpr int kSegs = 8;       // descriptions of segments: the query warps are two ahead of S, the
                                // softmax of an end may be one behind it
 constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
+constexpr float kUp = 7.f;     // p is 2^kUp at the reference maximum
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // tensor memory columns: S of unit u at 64 (u % 3), O of the two streams, the scales of q~ (two
 // buffers of both streams) and of K (of each stream two: a copy never overwrites what an MMA in
@@ -485,7 +489,7 @@ __device__ __forceinline__ uint32_t pack_bf16(const uint32_t* v) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// p = 2^(s scale - m) of 32 scores, their sums added to l, p as f16 pairs.
+// p = 2^(s scale + neg_m) of 32 scores, their sums added to l, p as f16 pairs.
 __device__ __forceinline__ void exponentials(const uint32_t (&s)[32], uint64_t scale2,
                                              uint64_t neg_m, uint64_t& l2, uint32_t (&p)[16]) {
 #pragma unroll
@@ -928,8 +932,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // ---- p = 2^(S log2e - m), over S
-        const float ref = -fmaxf(m, -3.4e38f);
+        // ---- p = 2^(S log2e - m + kUp), over S
+        const float ref = kUp - fmaxf(m, -3.4e38f);
         const uint64_t neg_m = pk2(ref, ref);
         uint32_t p[16];
         exponentials(x, scale2, neg_m, l2, p);
@@ -946,6 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l0, l1;
       up2(l2, l0, l1);
       float l = l0 + l1, own = 1.f, other = 0.f;
+      m -= kUp;  // what l and O refer to
       const int r = both ? threadIdx.x : threadIdx.x & (kRows - 1);  // row of the segment
       const int slot = sg.slot, row = sg.row0 + r, tok = row / a.G;
       const int64_t at = static_cast<int64_t>(sg.tok0 + tok) * a.H + sg.hk * a.G + row - tok * a.G;

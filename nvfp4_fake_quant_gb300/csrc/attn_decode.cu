@@ -36,8 +36,10 @@
 // lanes.  Codes become f16 by the hardware conversion times their scale, exactly;
 // p is rounded to f16 (as in the training forward), its sum is taken before the
 // rounding; all sums are fp32.  The maximum that p refers to is raised only when
-// a score exceeds it by 8 (log2): p then stays below 2^8, far inside f16, and the
-// cross-lane maximum and the rescaling of O leave the common path.
+// a score exceeds it by 8 (log2), so the cross-lane maximum and the rescaling of O
+// leave the common path.  p stays below 2^8, and is rounded times 2^7: f16 then has
+// no more room above, and a p is still seen 2^32 below the reference.  (Without the
+// factor keys 2^25 below a dominant one vanished from O, not from the sum.)
 //
 // Measured (calls in a CUDA graph): 8 x up to 131072 tokens, 64 heads on 8 of 128:
 // 117 us, 87% of the copy rate in bytes of the cache; 64 sequences of up to 8192, 32
@@ -64,6 +66,7 @@ constexpr int kWarps = 4;  // consumer warps of a run, 32 keys of a tile each
 constexpr int kProducer = kWarps, kMma = kWarps + 1;
 constexpr int kRunWarps = kWarps + 2;
 constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
+constexpr float kUp = 128.f;   // p in f16 and O are times this
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Per shape: query heads per run (8 NT), runs per CTA, ring stages; shared memory and
@@ -363,6 +366,7 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
       }
   }
   uint32_t pb[2][NT][2];
+  const uint64_t up = pk2(kUp, kUp);
   const uint32_t swap = odd ? 0x1032u : 0x3210u;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -379,6 +383,8 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
       p2 = ex2_f32(p2);
       p3 = ex2_f32(p3);
       l2 = add2(l2, add2(pk2(p0, p1), pk2(p2, p3)));
+      up2(mul2(pk2(p0, p1), up), p0, p1);
+      up2(mul2(pk2(p2, p3), up), p2, p3);
       pb[i][nt][0] = movmatrix_trans(pack_f16x2_rn(p0, p1));
       pb[i][nt][1] = movmatrix_trans(pack_f16x2_rn(p2, p3));
       pb[i][nt][0] = prmt(pb[i][nt][0], 0u, swap);
@@ -824,6 +830,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
           const float2 v = ml[w * C::kHeads + head];
           c[w] = ex2_f32(v.x - ref);
           l = fmaf(v.y, c[w], l);
+          c[w] *= 1.f / kUp;  // O's own factor
         }
         const int64_t row = static_cast<int64_t>(td.b) * a.H + hk * a.G + g0 + head;
         Fold f{1.f, 0.f};

@@ -13,19 +13,19 @@ import torch
 
 from nvfp4_fake_quant_gb300 import api
 from oracle import serving as os_
-from test_gpu_cross import ints, queries, vmax_of
+from test_gpu_cross import ints, vmax_of
 from test_gpu_kv_cache import BF16, PAGE
 
 pytestmark = pytest.mark.gpu
 PAGES = 24
 
 
-def sink_pool(hkv, d, g):
+def sink_pool(hkv, d, g, spread=1.0):
     """PAGES pages: key 0 of page 0 scores about 16 (nats) above the rest for rows of ones and
-    scale d^-0.5; its V is 0, the others' V are above 0."""
+    scale d^-0.5; its V is 0, the others' V are above 0, of mean 1 where their spread is less."""
     pool = torch.empty(PAGES, hkv, 144 * d, dtype=torch.uint8)
     k = torch.randn(PAGES, hkv, PAGE, d, generator=g) * 0.2
-    v = torch.randn(PAGES, hkv, PAGE, d, generator=g).abs() + 0.1
+    v = torch.randn(PAGES, hkv, PAGE, d, generator=g).abs() * spread + max(0.1, 1 - spread)
     k[0, :, 0], v[0, :, 0] = 16.2 * d ** -0.5, 0.0
     for x, at_c, at_s in ((k, 0, 128 * d), (v, 64 * d, 136 * d)):
         c, s = os_.pack(x.to(BF16))
@@ -83,4 +83,24 @@ def test_behind_a_prefix_that_begins_with_it(h, hkv, d, own):
     o, lse = api.attn_qat_decode_prefix(q.cuda(), pool.cuda(), mine.expand(b, 2).contiguous().cuda(),
                                         ints([own] * b), prefix.cuda(), ints([n]))
     check(o, lse, ref, n + own, vmax_of(pool, d))
+    assert api.device_status() == 0
+
+
+@pytest.mark.parametrize("h,hkv,d", [(8, 8, 64), (16, 8, 128), (36, 3, 64)])
+def test_single_tokens(h, hkv, d):
+    """40 sequences of the same keys: runs hold most of a segment."""
+    g = torch.Generator().manual_seed(h + d)
+    b, n = 40, PAGES * PAGE - 5
+    pool, q = sink_pool(hkv, d, g, spread=0.1), rows(b, h, d)
+    table = torch.arange(PAGES, dtype=torch.int32)[None]
+    ref = os_.attend(q, pool, [(table[0], n)], d ** -0.5)
+    args = (q.cuda(), pool.cuda(), table.expand(b, -1).contiguous().cuda(), ints([n] * b))
+    for call in (api.attn_qat_decode, api.attn_qat_cross):
+        o, lse = call(*args)
+        check(o, lse, ref, n, vmax_of(pool, d))
+    # the same as own keys behind a prefix of some of the others
+    prefix = torch.tensor([[3, 7, 8]], dtype=torch.int32)
+    ref = os_.attend(q, pool, [(prefix[0], 300), (table[0], n)], d ** -0.5)
+    o, lse = api.attn_qat_decode_prefix(*args, prefix.cuda(), ints([300]))
+    check(o, lse, ref, n + 300, vmax_of(pool, d))
     assert api.device_status() == 0

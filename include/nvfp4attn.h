@@ -605,8 +605,9 @@ nvq_status attn_qat_decode(const void* q, int64_t ld_q, const void* pool, int64_
  *   q          bf16 [T, H, D], row stride ld_q (elements, % 8 == 0, >= H*D)
  *   cu_tokens  int32 [B + 1]: sequence b's tokens are rows [cu_tokens[b],
  *              cu_tokens[b + 1]), not decreasing; NULL: T / B tokens each (T % B == 0).
- *              Offsets outside [0, T] or that decrease are cut to what is there and
- *              NVQ_ERR_INVALID is recorded for nvq_device_status()
+ *              Offsets outside [0, T] are cut to what is there; where one is then
+ *              below the one before it, no sequence has rows.  NVQ_ERR_INVALID is
+ *              recorded for nvq_device_status()
  *   page_table int32 [B, max_pages], kv_lens int32 [B]: the keys' pages and numbers,
  *              checked as in attn_qat_decode
  *   o          bf16 [T, H, D] contiguous, not overlapping q; lse f32 [T, H] or NULL

@@ -192,21 +192,25 @@ struct Start {
   int s, hk, rt, i;
 };
 
-__device__ __forceinline__ Extent extent(const CrossArgs& a, int s, bool* bad) {
+// What is wrong with a sequence: something to report; offsets that decrease, so that sequences
+// would have rows in common.
+enum : int { kReport = 1, kFalls = 2 };
+
+__device__ __forceinline__ Extent extent(const CrossArgs& a, int s, int* wrong) {
   Extent e;
   if (a.cu == nullptr) {
     e.tok0 = s * a.per_seq;
     e.toks = a.per_seq;
-    *bad = false;
+    *wrong = 0;
   } else {
     const int lo = a.cu[s], hi = a.cu[s + 1];
     e.tok0 = min(max(lo, 0), a.T);
-    const int end = min(max(hi, e.tok0), a.T);
-    e.toks = end - e.tok0;
-    *bad = lo != e.tok0 || hi != end;
+    const int end = min(max(hi, 0), a.T);
+    e.toks = max(end - e.tok0, 0);
+    *wrong = (lo != e.tok0 || hi != end ? kReport : 0) | (end < e.tok0 ? kReport | kFalls : 0);
   }
   const int cap = a.max_pages * kPage, n = a.lens[s];
-  *bad |= n > cap;
+  if (n > cap) *wrong |= kReport;
   e.len = max(0, min(n, cap));
   e.row_tiles = (e.toks * a.G + kPair - 1) / kPair;
   e.key_tiles = e.row_tiles > 0 ? (e.len + kPage - 1) / kPage : 0;
@@ -236,10 +240,10 @@ struct Walk {
       if (++hk == a.Hkv) {
         hk = 0;
         seg0 += static_cast<int64_t>(e.row_tiles) * e.key_tiles * a.Hkv;
-        bool bad;
+        int wrong;
 #pragma unroll 1
         do {
-          e = extent(a, ++s, &bad);
+          e = extent(a, ++s, &wrong);
         } while (e.key_tiles == 0);
       }
     }
@@ -605,14 +609,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = (a.B + kThreads - 1) / kThreads;
   const int s_lo = min(a.B, static_cast<int>(threadIdx.x) * per), s_hi = min(a.B, s_lo + per);
   int64_t mine = 0;
+  int any = 0;
   Extent e{};
 #pragma unroll 1
   for (int s = s_lo; s < s_hi; ++s) {
-    bool bad;
-    e = extent(a, s, &bad);
+    int wrong;
+    e = extent(a, s, &wrong);
+    any |= wrong;
     mine += static_cast<int64_t>(e.row_tiles) * e.key_tiles * a.Hkv;
-    if (bad && blockIdx.x == 0) atomicMax(a.err, kErrTable);
   }
+  if (any != 0 && blockIdx.x == 0) atomicMax(a.err, kErrTable);
   int64_t scan = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -620,7 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane >= off) scan += v;
   }
   if (lane == 31) warp_sum[warp] = scan;
-  __syncthreads();
+  // sequences with rows in common would write them in any order: then nobody has rows
+  const bool falls = __syncthreads_or(any & kFalls);
   int64_t all = 0;
   const int busy = ((a.B + per - 1) / per + 31) / 32;  // warps that have sequences
 #pragma unroll 1
@@ -629,6 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     all += warp_sum[w];
   }
   const int64_t before = scan - mine;  // tiles before this thread's sequences
+  if (falls) all = mine = 0;
   const int run = blockIdx.x;
   const Runs line(all, a.runs, a.runs_magic);
   const int64_t u0 = line.begin(run), u1 = line.begin(run + 1);
@@ -638,8 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (per > 1) {
 #pragma unroll 1
       for (;; ++s) {
-        bool bad;
-        e = extent(a, s, &bad);
+        int wrong;
+        e = extent(a, s, &wrong);
         const int64_t n = static_cast<int64_t>(e.row_tiles) * e.key_tiles * a.Hkv;
         if (u0 < at + n) break;
         at += n;
@@ -1110,10 +1118,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- rows without keys, rows outside of all sequences
     const int first = 4 * run + warp - kQWarp, step = 4 * static_cast<int>(gridDim.x);
 #pragma unroll 1
-    for (int s0 = 0; s0 < a.B; s0 += 32) {
-      bool bad;
+    for (int s0 = 0; s0 < a.B && !falls; s0 += 32) {
+      int wrong;
       Extent x{0, 0, 0, 0, 1};
-      if (s0 + lane < a.B) x = extent(a, s0 + lane, &bad);
+      if (s0 + lane < a.B) x = extent(a, s0 + lane, &wrong);
       uint32_t none = __ballot_sync(0xFFFFFFFFu, x.toks > 0 && x.key_tiles == 0);
 #pragma unroll 1
       for (; none != 0; none &= none - 1) {
@@ -1126,7 +1134,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (a.cu != nullptr) {
-      const int lo = min(max(a.cu[0], 0), a.T), hi = min(max(a.cu[a.B], 0), a.T);
+      const int lo = falls ? 0 : min(max(a.cu[0], 0), a.T);
+      const int hi = falls ? 0 : min(max(a.cu[a.B], 0), a.T);
       // rows [0, lo) and [hi, T), as one run of rows
 #pragma unroll 1
       for (int64_t z = first; z < static_cast<int64_t>(lo) + a.T - hi; z += step)

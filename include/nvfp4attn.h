@@ -583,10 +583,10 @@ nvq_status nvfp4_kv_release(const uint8_t* done, const int32_t* seq_lens, int B,
  * Visible keys: all j < seq_lens[b] when window == 0; with window > 0 the last
  * `window` of them and the first `sinks`.  The new token's own K and V are in
  * the cache (append first).  A sequence without visible keys gets o = 0 and
- * lse = -inf.  D in {64, 128}; window, sinks >= 0; 1 <= B, H <= 65535, B*H < 2^31,
- * B*H*max_pages <= 2^53, and a call takes less than 2^31 records for each of its
- * runs, of which there are 304 to 608 on 152 multiprocessors (else
- * NVQ_ERR_UNSUPPORTED).  Long sequences are split
+ * lse = -inf, a row that sees a NaN o = NaN and lse = -inf.  D in {64, 128};
+ * window, sinks >= 0; 1 <= B, H <= 65535, B*H < 2^31, B*H*max_pages <= 2^53, and a
+ * call takes less than 2^31 records for each of its runs, of which there are 304 to
+ * 608 on 152 multiprocessors (else NVQ_ERR_UNSUPPORTED).  Long sequences are split
  * over the GPU and joined in a fixed order: results do not vary from run to run.
  * ws: attn_qat_decode_workspace(B, H, Hkv, D, max_pages) bytes, 256-byte
  * aligned; its size follows from the current device's multiprocessor count.

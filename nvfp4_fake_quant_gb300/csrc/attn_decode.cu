@@ -720,8 +720,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
           reinterpret_cast<uint4*>(a.o + row0 * D)[x] = v;
         }
         if (a.lse != nullptr)
-          for (int x = lane; x < a.H; x += 32)
-            a.lse[row0 + x] = kFold ? a.prior_l2[row0 + x] * kLn2 : -INFINITY;
+          for (int x = lane; x < a.H; x += 32) {
+            const float v = kFold ? a.prior_l2[row0 + x] * kLn2 : -INFINITY;
+            a.lse[row0 + x] = v == v ? v : -INFINITY;  // a NaN: as a row's own gives it
+          }
       }
     }
     Ring ring;

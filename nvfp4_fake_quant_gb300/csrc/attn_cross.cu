@@ -1249,11 +1249,14 @@ nvq_status check_cross(int64_t T, int B, int H, int Hkv, int D, int max_pages) {
       max_pages > 0x7FFFFFFF / kPage)
     return NVQ_ERR_INVALID;
   if (D != 64 && D != 128) return NVQ_ERR_UNSUPPORTED;
-  if (B > 65535 || H > 65535 || T > 0x7FFFFF00 / H) return NVQ_ERR_UNSUPPORTED;
-  // (rows / 128 + B) Hkv < 2^24 + 2^33: no overflow; a run counts its tiles in
-  // 29 bits (four units each)
-  const int64_t heads = (T * (H / Hkv) / kRows + B) * Hkv;
-  return heads * max_pages / 64 >= 0x1FFFFFFF ? NVQ_ERR_UNSUPPORTED : NVQ_OK;
+  if (B > 65535 || H > 65535 || T > (0x7FFFFF00 - 1) / H) return NVQ_ERR_UNSUPPORTED;
+  // The line has at most (rows / 256 + B) Hkv max_pages tiles ((rows / 128 + B) Hkv < 2^24 + 2^32:
+  // no overflow), of which a run counts its own in 29 bits (four units each).  The second holds
+  // for 32 runs and more by the first.
+  const int64_t tiles = (T * (H / Hkv) / kRows + B) * Hkv * max_pages;
+  if (tiles >= int64_t{1} << 34) return NVQ_ERR_UNSUPPORTED;
+  if (tiles >= 1 << 29 && tiles / device_sms() >= (1 << 29) - 1) return NVQ_ERR_UNSUPPORTED;
+  return NVQ_OK;
 }
 
 size_t cross_workspace(int64_t T, int B, int H, int Hkv, int D, int max_pages) {

@@ -293,6 +293,27 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t ab
   return __all_sync(0xFFFFFFFFu, ok != 0);
 }
 
+// The same for a wait that lasts as long as a segment, which may have any number of tiles: it gives
+// up only where no tile has begun (`begun` has not changed) for two seconds.
+__device__ __forceinline__ bool wait_segment(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                             const volatile int* begun) {
+  int seen = *begun;
+  uint64_t t0 = globaltimer_ns();
+  bool ok;
+#pragma unroll 1
+  while (!(ok = mbar_try_wait(bar, parity)) && *abort == 0) {
+    const int now = *begun;
+    const uint64_t t = globaltimer_ns();
+    if (now != seen) {
+      seen = now;
+      t0 = t;
+    } else if (t - t0 > NVQ_WAIT_LIMIT_NS) {
+      *abort = 1;
+    }
+  }
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
 // Place in a ring of `stages`: stage and the parity of its use.
 struct Ring {
   int s = 0;
@@ -543,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int64_t warp_sum[kThreads / 32];
   __shared__ alignas(8) unsigned char walk_bytes[sizeof(Walk)];  // of the query warps' first thread
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_word;
+  __shared__ int abort_word, begun;  // begun: the tile that the producer is at
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023u) &
                                              ~static_cast<uintptr_t>(1023u));
@@ -573,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
 
   if (threadIdx.x == 32 * kProducerWarp) {  // (the first warps look at sequences meanwhile)
-    abort_word = 0;
+    abort_word = begun = 0;
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 2 + 1 + 4);
@@ -715,7 +736,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!there && lane == 0) atomicMax(a.err, kErrTable);
         const int st = ring.s;
         if (!(ok = wait(&empty[st], ring.phase ^ 1, abort))) break;
-        if (lane == 0) desc[st] = td;
+        if (lane == 0) {
+          desc[st] = td;
+          begun = n;
+        }
         __syncwarp();
         uint8_t* dst = smem + st * C::kRec;
         if (there) {
@@ -1110,7 +1134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       QueryTile<D, 128> q;
       q.begin(a, sg, t);
       const int qb = seg & 1;
-      if (!wait(&q_empty[qb], ((seg >> 1) & 1) ^ 1, abort)) break;
+      if (!wait_segment(&q_empty[qb], ((seg >> 1) & 1) ^ 1, &abort_word, &begun)) break;
       q.quantize(a, smem + C::kQAt + 2 * qb * C::kQ, smem + C::kQScAt + 2 * qb * C::kQSc, t);
       fence_proxy_async_smem();
       mbar_arrive_warp(&q_full[qb]);

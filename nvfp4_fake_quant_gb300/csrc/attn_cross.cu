@@ -1350,8 +1350,13 @@ nvq_status attn_qat_cross(const void* q, int64_t ld_q, int64_t T, const void* po
   if (ranges_meet(q, 2 * static_cast<uint64_t>((T - 1) * ld_q + row), o,
                   2 * static_cast<uint64_t>(row * T)))
     return NVQ_ERR_INVALID;
-  // one token a sequence: a row tile would be all but empty
-  if (cu_tokens == nullptr && T == B)
+  // One token a sequence goes to the single-token kernel, up to the 16 query heads of a KV head
+  // that one of its runs takes: it reads every key again for each 16 more, and here 256 rows cost
+  // little more than one.  64 sequences of 8192 keys, 8 KV heads of 128, there and here: 1 head a
+  // KV head 102 and 220 us, 16 heads 149 and 263, 32 heads 279 and 279, 64 heads 537 and 290, 128
+  // heads 1055 and 301; 8 sequences of 512 keys, one KV head of 64: 8.6 and 8.7, 9.4 and 8.6, 9.9
+  // and 8.7, 11.3 and 8.7, 13.6 and 9.4.
+  if (cu_tokens == nullptr && T == B && H / Hkv <= 16)
     return attn_qat_decode(q, ld_q, pool, num_pages, page_table, ld_table, max_pages, kv_lens, B,
                            H, Hkv, D, scale, 0, 0, o, lse, ws, ws_bytes, stream);
   return launch_cross({q, ld_q, T, pool, num_pages, page_table, ld_table, max_pages, kv_lens,

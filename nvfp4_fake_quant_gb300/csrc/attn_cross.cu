@@ -66,9 +66,7 @@ constexpr int kThreads = 640;
 constexpr int kDecodeWarp = 8, kQWarp = 12, kProducerWarp = 16, kSWarp = 17, kPvWarp = 19;
 constexpr int kSegs = 8;       // descriptions of segments: the query warps are two ahead of S, the
                                // softmax of an end may be one behind it
-constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
 constexpr float kUp = 7.f;     // p is 2^kUp at the reference maximum
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // tensor memory columns: S of unit u at 64 (u % 3), O of the two streams, the scales of q~ (two
 // buffers of both streams) and of K (of each stream two: a copy never overwrites what an MMA in
 // flight may read, see the S warps)
@@ -155,33 +153,6 @@ __host__ __device__ constexpr int64_t part_floats(int rows, int D) {
 
 struct Extent {
   int tok0, toks, len, row_tiles, key_tiles;
-};
-
-// The line of `all` tiles is cut into n = min(all, runs) runs: run c is [all c / n,
-// all (c + 1) / n), never empty; of the grid's runs those from n on have nothing.
-// all c / n = (all / n) c + (all % n) c / n.  n is the grid's or all itself, so there is
-// nothing to divide: the host gives 2^64 / runs, rounded up (all <= 2^53 and runs < 2^10
-// keep the product's error below 1 / runs).
-struct Runs {
-  int64_t all, per;
-  int n, rest;
-  uint32_t magic;
-  __device__ __forceinline__ Runs(int64_t all_, int runs, uint64_t magic_) : all(all_) {
-    if (all < runs) {
-      n = static_cast<int>(all);
-      per = 1;
-      rest = 0;
-    } else {
-      n = runs;
-      // (the reciprocal of 1 has no place in 64 bits)
-      per = runs == 1 ? all : static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(all), magic_));
-      rest = static_cast<int>(all - per * runs);
-    }
-    magic = static_cast<uint32_t>(magic_ >> 32) + 1;  // rest c < 2^24: exact as well
-  }
-  __device__ __forceinline__ int64_t begin(int c) const {
-    return c < n ? per * c + __umulhi(static_cast<uint32_t>(rest * c), magic) : all;
-  }
 };
 
 // Where a run begins: tile i of (sequence s, KV head hk, row tile rt), the sequence's first tile
@@ -314,18 +285,6 @@ __device__ __forceinline__ bool wait_segment(uint64_t* bar, uint32_t parity, vol
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
-// Place in a ring of `stages`: stage and the parity of its use.
-struct Ring {
-  int s = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next(int stages) {
-    if (++s == stages) {
-      s = 0;
-      phase ^= 1;
-    }
-  }
-};
-
 // q~ of a segment by N threads, thread t taking block t % (D/16) of every kStep-th row: codes into
 // the swizzled rows of the A operand, scales into the 512-byte blocks of the scale operand, of the
 // two halves one after another.  Rows beyond the segment's: zeros.  kAhead rows' values are on
@@ -402,28 +361,6 @@ struct QueryTile {
            (j & 3)] = static_cast<uint8_t>(r.sbyte);
   }
 };
-
-// K's scales [128][D/16] to D/64 blocks of 512 bytes, in place: row r of a block holds the words
-// (4 scales) of keys r, r + 32, r + 64, r + 96.
-template <int D>
-__device__ __forceinline__ void arrange_scales(uint8_t* sc, int lane) {
-  uint32_t w[D / 64][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (D == 128) {
-      const uint2 v = *reinterpret_cast<const uint2*>(sc + (lane + 32 * i) * 8);
-      w[0][i] = v.x;
-      w[1][i] = v.y;
-    } else {
-      w[0][i] = *reinterpret_cast<const uint32_t*>(sc + (lane + 32 * i) * 4);
-    }
-  }
-  __syncwarp();
-#pragma unroll
-  for (int k = 0; k < D / 64; ++k)
-    *reinterpret_cast<uint4*>(sc + k * 512 + lane * 16) =
-        make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
-}
 
 // V~ of a page as f16 rows of 64 elements (128 bytes, swizzled; elements 64.. in a second block)
 // by four warps, 32 keys each.  A lane takes 32 elements (16 bytes of codes, two scales) of a

@@ -65,9 +65,7 @@ namespace {
 constexpr int kWarps = 4;  // consumer warps of a run, 32 keys of a tile each
 constexpr int kProducer = kWarps, kMma = kWarps + 1;
 constexpr int kRunWarps = kWarps + 2;
-constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
 constexpr float kUp = 128.f;   // p in f16 and O are times this
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Per shape: query heads per run (8 NT), runs per CTA, ring stages; shared memory and
 // tensor memory of a run.
@@ -135,32 +133,6 @@ struct RunInfo {
 
 // Floats of one part: m (log2 units) and l per head, then the sums [heads][D].
 __host__ __device__ constexpr int part_floats(int D, int heads) { return heads * (D + 2); }
-
-// The line of `all` tiles is cut into n = min(all, runs) runs: run c is [all c / n,
-// all (c + 1) / n), never empty; of the grid's runs those from n on have nothing.
-// all c / n = (all / n) c + (all % n) c / n.  n is the grid's or all itself, so there is
-// nothing to divide: the host gives 2^64 / runs, rounded up (all <= 2^53 and runs < 2^10
-// keep the product's error below 1 / runs).
-struct Runs {
-  int64_t all, per;
-  int n, rest;
-  uint32_t magic;
-  __device__ __forceinline__ Runs(int64_t all_, int runs, uint64_t magic_) : all(all_) {
-    if (all < runs) {
-      n = static_cast<int>(all);
-      per = 1;
-      rest = 0;
-    } else {
-      n = runs;
-      per = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(all), magic_));
-      rest = static_cast<int>(all - per * runs);
-    }
-    magic = static_cast<uint32_t>(magic_ >> 32) + 1;  // rest c < 2^24: exact as well
-  }
-  __device__ __forceinline__ int64_t begin(int c) const {
-    return c < n ? per * c + __umulhi(static_cast<uint32_t>(rest * c), magic) : all;
-  }
-};
 
 // What a row has over its own keys (maximum m and sum l, log2 units) together with `prior`, the
 // logarithm over other keys: m and l of both, and the factors of the two sums of p V~ (the other
@@ -442,46 +414,12 @@ __device__ __forceinline__ void quantize_q(const uint8_t* qraw, int heads, uint8
   }
 }
 
-// K's scales [128][D/16] to D/64 blocks of 512 bytes, in place: row r of a block holds
-// the words (4 scales) of keys r, r + 32, r + 64, r + 96.
-template <int D>
-__device__ __forceinline__ void arrange_scales(uint8_t* sc, int lane) {
-  uint32_t w[D / 64][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (D == 128) {
-      const uint2 v = *reinterpret_cast<const uint2*>(sc + (lane + 32 * i) * 8);
-      w[0][i] = v.x;
-      w[1][i] = v.y;
-    } else {
-      w[0][i] = *reinterpret_cast<const uint32_t*>(sc + (lane + 32 * i) * 4);
-    }
-  }
-  __syncwarp();
-#pragma unroll
-  for (int k = 0; k < D / 64; ++k)
-    *reinterpret_cast<uint4*>(sc + k * 512 + lane * 16) =
-        make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
-}
-
 // Element of O at position `pos` of a stored row: the rows keep the order in which
 // the lanes hold them, pos = 16 i + 2 g + e for d = D/8 g + 2 i + e.
 template <int D>
 __device__ __forceinline__ int element_of(int pos) {
   return (pos >> 1 & 7) * (D / 8) + (pos >> 4) * 2 + (pos & 1);
 }
-
-// Place in a ring of `stages`: stage and the parity of its use.
-struct Ring {
-  int s = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next(int stages) {
-    if (++s == stages) {
-      s = 0;
-      phase ^= 1;
-    }
-  }
-};
 
 // kFold: what is over other keys (a.prior_o, a.prior_l2) goes into each row.  An instance of its
 // own: with the choice at run time heads of 64 behind a window took 15.9 us instead of 15.2.
@@ -1041,14 +979,6 @@ cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tk32, const 
     return launch_pdl(join_kernel<D, NT, 1024, kFold>, grid, dim3(1024), 0, stream, 1, a);
   return launch_pdl(join_kernel<D, NT, 256, kFold>, grid, dim3(256), 0, stream, 1, a);
 }
-
-}  // namespace
-
-}  // namespace nvq
-
-namespace nvq {
-
-namespace {
 
 template <bool kFold>
 cudaError_t launch_decode_form(int D, const CUtensorMap& tk, const CUtensorMap& tk32,

@@ -15,7 +15,7 @@ import torch
 from nvfp4_fake_quant_gb300 import api
 from oracle import serving as os_
 from test_gpu_cross import ints, offsets, vmax_of
-from test_gpu_kv_cache import BF16, PAGE, make_pool
+from test_gpu_kv_cache import BF16, PAGE, check_decode, make_pool
 
 pytestmark = pytest.mark.gpu
 PAGES, WIDE = 16, 12
@@ -94,3 +94,16 @@ def test_random_shapes(seed, d, hkv):
         want = api.attn_qat_decode(q[:r], pool, both.int(), own + shared[seq[:r]])
         close((o, lse), want, e[:r], (WIDE + 4) * PAGE, vmax)
         assert api.device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [0, 1, 100, 128])
+def test_one_run(d, n):
+    """A table of one page and one KV head: a grid of one run."""
+    gen = torch.Generator().manual_seed(n)
+    pool, table, q = make_pool(2, 1, d, gen), ints([[1]]), torch.randn(5, 3, d, generator=gen).to(BF16)
+    ref = os_.attend(q, pool, [(table[0], n)], d ** -0.5)
+    for more in ((), (ints([0, 5]),)):
+        o, lse = api.attn_qat_cross(q.cuda(), pool.cuda(), table, ints([n]), *more)
+        check_decode(o, lse, ref, n, vmax_of(pool, d))
+    assert api.device_status() == 0

@@ -136,7 +136,7 @@ struct CrossArgs {
   int per_seq;  // tokens of each sequence where cu is null
   int B, H, Hkv, G;
   int tiles;  // whole warps' rows of o go by the tensor map: G divides 32
-  float scale_log2;
+  Scales scale;
   __nv_bfloat16* o;  // or, where null, o32 with the logarithms (base 2) in lse
   float* o32;
   float* lse;
@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int stream = warp >> 2, quarter = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t o_at = lanes + kO + D * stream;
-    const uint64_t scale2 = pk2(a.scale_log2, a.scale_log2);
+    const uint64_t scale2 = pk2(a.scale.fused, a.scale.fused);
     float m = -INFINITY;  // reference maximum (log2 units)
     uint64_t l2 = pk2(0.f, 0.f);
     uint32_t u = stream;           // its units are every other one
@@ -855,15 +855,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = 32 * (both ? warp : quarter) < rows;  // else: rows that nobody reads
       const uint32_t s_at = lanes + 64 * buf;
       if (live) {
-        if (valid < kKeys) {  // keys behind the last: -inf, before S is read
+        // before S is read: keys behind the last, -inf; large scales
+        const bool scaled = a.scale.before != 1.f;
+        if (valid < kKeys || scaled) {
 #pragma unroll 1
-          for (int c = valid & ~15; c < kKeys; c += 16) {
+          for (int c = scaled ? 0 : valid & ~15; c < kKeys; c += 16) {
             uint32_t x[16];
             tmem_ld16(s_at + c, x);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
+            for (int i = 0; i < 16; ++i) {
+              x[i] = __float_as_uint(__uint_as_float(x[i]) * a.scale.before);
               if (c + i >= valid) x[i] = 0xFF800000u;
+            }
             tmem_st16(s_at + c, x);
           }
           tmem_wait_st();
@@ -880,8 +884,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           v[2] = max3f(v[2], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
           v[3] = max3f(v[3], __uint_as_float(y[16 + i]), __uint_as_float(y[17 + i]));
         }
-        const float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * a.scale_log2;
-        const bool grows = mx > m + kSlack;  // -inf: always, where there is a key
+        // (a product of its own: fused with a difference from m it would be another number)
+        const float mx = __fmul_rn(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), a.scale.fused);
+        const bool grows = mx > fmaxf(m, limit_of(m));  // -inf: always, where there is a key
         if (__any_sync(0xFFFFFFFFu, grows)) {
           const float c = grows ? ex2_f32(m - mx) : 1.f;
           if (grows) m = mx;
@@ -1245,7 +1250,7 @@ nvq_status launch_cross(const CrossCall& c, uint8_t* ws, cudaStream_t stream) {
   const CrossArgs a{static_cast<const uint16_t*>(c.q), c.ld_q, static_cast<int>(c.T),
                     static_cast<const uint8_t*>(c.pool), c.num_pages, c.page_table, c.ld_table,
                     c.max_pages, c.kv_lens, c.cu_tokens, static_cast<int>(c.T / c.B), c.B, c.H,
-                    c.Hkv, G, c.o != nullptr && 32 % G == 0, c.scale * kLog2e,
+                    c.Hkv, G, c.o != nullptr && 32 % G == 0, scales_of(c.scale * kLog2e, c.D),
                     static_cast<__nv_bfloat16*>(c.o), c.o32,
                     c.lse, reinterpret_cast<Split*>(ws),
                     reinterpret_cast<float*>(ws + p.parts),

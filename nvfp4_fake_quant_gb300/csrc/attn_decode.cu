@@ -112,7 +112,7 @@ struct DecodeArgs {
   int max_pages;
   const int32_t* lens;
   int B, H, Hkv, G, chunks;  // G query heads per KV head in `chunks` groups
-  float scale_log2;
+  Scales scale;
   int window, sinks;
   __nv_bfloat16* o;
   float* lse;
@@ -297,6 +297,14 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
   tc_fence_before();
   mbar_arrive_warp(release);
   // ---- p = 2^(S log2e - m)
+  if (a.scale.before != 1.f) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][nt][e] *= a.scale.before;
+  }
   float mx[NT][2];
   bool grows = false;
 #pragma unroll
@@ -312,8 +320,8 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       mx[nt][h] = max3f(s[0][nt][h], s[0][nt][2 + h], fmaxf(s[1][nt][h], s[1][nt][2 + h]));
-      mx[nt][h] *= a.scale_log2;
-      grows |= mx[nt][h] > st.m[nt][h] + kSlack;
+      mx[nt][h] *= a.scale.fused;
+      grows |= mx[nt][h] > limit_of(st.m[nt][h]);
     }
   }
   if (__any_sync(0xFFFFFFFFu, grows)) {
@@ -343,7 +351,7 @@ __device__ __forceinline__ void tile_keys(const DecodeArgs& a, const uint8_t* re
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const uint64_t neg_m = pk2(-fmaxf(st.m[nt][0], -3.4e38f), -fmaxf(st.m[nt][1], -3.4e38f));
-    const uint64_t scale2 = pk2(a.scale_log2, a.scale_log2);
+    const uint64_t scale2 = pk2(a.scale.fused, a.scale.fused);
     uint64_t l2 = pk2(st.l[nt][0], st.l[nt][1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -1008,8 +1016,8 @@ nvq_status run_decode(const void* q, int64_t ld_q, const void* pool, int64_t num
   uint8_t* wb = static_cast<uint8_t*>(ws);
   const DecodeArgs a{static_cast<const uint16_t*>(q), ld_q, static_cast<const uint8_t*>(pool),
                      num_pages, page_table, ld_table, max_pages, seq_lens, B, H, Hkv, H / Hkv,
-                     p.chunks, scale * kLog2e, window, sinks, static_cast<__nv_bfloat16*>(o), lse,
-                     prior_o, prior_l2, reinterpret_cast<RunInfo*>(wb), p.by_segment,
+                     p.chunks, scales_of(scale * kLog2e, D), window, sinks,
+                     static_cast<__nv_bfloat16*>(o), lse, prior_o, prior_l2, reinterpret_cast<RunInfo*>(wb), p.by_segment,
                      reinterpret_cast<float*>(wb + p.parts), p.runs,
                      ~uint64_t{0} / p.runs + 1, err};
   const cudaError_t e = timed(NVQ_KERNEL_DECODE, stream, [&] {

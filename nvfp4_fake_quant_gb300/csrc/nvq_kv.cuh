@@ -15,6 +15,19 @@ __host__ __device__ constexpr int v_codes_at(int D) { return kPage * D / 2; }
 __host__ __device__ constexpr int k_scales_at(int D) { return kPage * D; }
 __host__ __device__ constexpr int v_scales_at(int D) { return kPage * D + kPage * D / 16; }
 
+// How the kernels multiply the scores S by scale (in log2 units).  p = 2^(S scale - m) is one fused
+// product and difference, while the reference m is a score times scale, rounded: up to half a step
+// of m may come on top of kSlack, for |m| < 2^28 at most 8.  |S| <= 2688^2 D (codes of 6, scales of
+// 448), so any scale up to 25.7 / D, more than twice D^-0.5, keeps S scale below 2^28.  For a larger
+// one S is first replaced by S scale, rounded as m is; the difference is then exact.
+struct Scales {
+  float before, fused;  // S before (1: not at all); in the fused product
+};
+inline Scales scales_of(float scale_log2, int D) {
+  if (scale_log2 * (2688.f * 2688.f * static_cast<float>(D)) < 0x1p28f) return {1.f, scale_log2};
+  return {scale_log2, 1.f};
+}
+
 inline nvq_status check_kv(const void* pool, int64_t num_pages, const int32_t* page_table,
                            int64_t ld_table, int max_pages, const int32_t* seq_lens) {
   if (pool == nullptr || (reinterpret_cast<uintptr_t>(pool) & 15u) != 0 || num_pages < 1 ||
@@ -27,6 +40,11 @@ inline nvq_status check_kv(const void* pool, int64_t num_pages, const int32_t* p
 }
 
 constexpr float kSlack = 8.f;  // scores may exceed the reference maximum by this (log2)
+// The largest score for which m stays the reference.  m's rounding adds to kSlack: from steps of
+// 1/8 (2^20) on less is left, from 2^24 on nothing (the result is then m or below it).
+__device__ __forceinline__ float limit_of(float m) {
+  return fmaf(fabsf(m), -0x1p-21f, m + kSlack);
+}
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // The line of `all` tiles is cut into n = min(all, runs) runs: run c is [all c / n,

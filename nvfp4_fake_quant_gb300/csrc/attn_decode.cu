@@ -1017,7 +1017,8 @@ nvq_status run_decode(const void* q, int64_t ld_q, const void* pool, int64_t num
   const DecodeArgs a{static_cast<const uint16_t*>(q), ld_q, static_cast<const uint8_t*>(pool),
                      num_pages, page_table, ld_table, max_pages, seq_lens, B, H, Hkv, H / Hkv,
                      p.chunks, scales_of(scale * kLog2e, D), window, sinks,
-                     static_cast<__nv_bfloat16*>(o), lse, prior_o, prior_l2, reinterpret_cast<RunInfo*>(wb), p.by_segment,
+                     static_cast<__nv_bfloat16*>(o), lse, prior_o, prior_l2,
+                     reinterpret_cast<RunInfo*>(wb), p.by_segment,
                      reinterpret_cast<float*>(wb + p.parts), p.runs,
                      ~uint64_t{0} / p.runs + 1, err};
   const cudaError_t e = timed(NVQ_KERNEL_DECODE, stream, [&] {

@@ -164,8 +164,8 @@ struct Start {
 };
 
 // What is wrong with a sequence: something to report; offsets that decrease, so that sequences
-// would have rows in common.
-enum : int { kReport = 1, kFalls = 2 };
+// would have rows in common; rows without keys (of the scan alone).
+enum : int { kReport = 1, kFalls = 2, kEmpty = 4 };
 
 __device__ __forceinline__ Extent extent(const CrossArgs& a, int s, int* wrong) {
   Extent e;
@@ -575,10 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int s = s_lo; s < s_hi; ++s) {
     int wrong;
     e = extent(a, s, &wrong);
-    any |= wrong;
+    any |= wrong | (e.toks > 0 && e.key_tiles == 0 ? kEmpty : 0);
     mine += static_cast<int64_t>(e.row_tiles) * e.key_tiles * a.Hkv;
   }
-  if (any != 0 && blockIdx.x == 0) atomicMax(a.err, kErrTable);
+  if ((any & kReport) && blockIdx.x == 0) atomicMax(a.err, kErrTable);
   int64_t scan = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (u0 == u1 && threadIdx.x == 0) a.split[run].end = -1;
   tc_fence_before();
-  __syncthreads();
+  const bool empties = __syncthreads_or(any & kEmpty) && !falls;
   tc_fence_after();
   const uint32_t tmem = uniform(tmem_slot);
   const int n_tiles = uniform(static_cast<int>(u1 - u0));
@@ -1086,21 +1086,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive_warp(&q_full[qb]);
     }
-    // ---- rows without keys, rows outside of all sequences
+    // ---- rows without keys, rows outside of all sequences: by their numbers over all these warps
+    // (counted from each sequence's first one warp had all sequences of a row: 256 of them took
+    // 52 us)
     const int first = 4 * run + warp - kQWarp, step = 4 * static_cast<int>(gridDim.x);
 #pragma unroll 1
-    for (int s0 = 0; s0 < a.B && !falls; s0 += 32) {
+    for (int s0 = 0; s0 < a.B && empties; s0 += 32) {
       int wrong;
       Extent x{0, 0, 0, 0, 1};
       if (s0 + lane < a.B) x = extent(a, s0 + lane, &wrong);
       uint32_t none = __ballot_sync(0xFFFFFFFFu, x.toks > 0 && x.key_tiles == 0);
+      if (none == 0) continue;
+      int z0 = first - x.tok0 % step;  // the warp's first row of the sequence
+      if (z0 < 0) z0 += step;
+      none &= __ballot_sync(0xFFFFFFFFu, x.toks > z0);
 #pragma unroll 1
       for (; none != 0; none &= none - 1) {
         const int i = __ffs(none) - 1;
         const int tok0 = __shfl_sync(0xFFFFFFFFu, x.tok0, i);
         const int toks = __shfl_sync(0xFFFFFFFFu, x.toks, i);
 #pragma unroll 1
-        for (int64_t z = first; z < toks; z += step)
+        for (int64_t z = __shfl_sync(0xFFFFFFFFu, z0, i); z < toks; z += step)
           empty_token<D>(a, tok0 + static_cast<int>(z), lane);
       }
     }

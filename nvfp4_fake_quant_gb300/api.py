@@ -809,8 +809,9 @@ def nvfp4_kv_extend(new_tokens, seq_lens, page_table, free_pages, free_count, to
     [pages] of which the first free_count (int32 [1]) are free and the last of those are taken.
     ``tokens``: rows of positions and slots (default: one per sequence).  ``start`` int32 [B]:
     added to the positions.  seq_lens_out and free_count_out may be seq_lens and free_count (no
-    other output may lie over an argument): a captured step then advances them in place.  A call that does not fit (pages, rows, the
-    table's width) changes nothing, gives no tokens and is reported by device_status()."""
+    other output may lie over an argument): a captured step then advances them in place.  A call
+    that does not fit (pages, rows, the table's width) changes nothing, gives no tokens and is
+    reported by device_status()."""
     b, max_pages, ld, pages = _check_free(page_table, seq_lens, free_pages, free_count)
     if _int32(new_tokens, "new_tokens", 1)[0][0] != b:
         raise ValueError(f"new_tokens must be [{b}], got {tuple(new_tokens.shape)}")

@@ -34,10 +34,10 @@
 // best key a p is still seen (from 1 on, keys 2^25 below a dominant one vanished from O, not from
 // the sum).
 //
-// Measured, in a replayed graph: 32760 tokens x 12 heads over 512 keys 113 us (0.91 PFLOP/s, 46% of
-// the bf16 rate; plain 9158 us), four latents of up to 6272 tokens 100 us, nine short pieces 23.7
-// us; 32 sequences x 64 heads behind 131072 shared keys 130 us with the join and the sequences' own
-// keys (1.06 PFLOP/s; one read of the prefix takes 22 us).  A tile takes 3400 to 3800 cycles, of
+// Measured, in a replayed graph: 32760 tokens x 12 heads over 512 keys 113.5 us (0.91 PFLOP/s, 46%
+// of the bf16 rate; plain 9203 us), four latents of up to 6272 tokens 101.5 us, nine short pieces
+// 23.6 us; 32 sequences x 64 heads behind 131072 shared keys 131 us with the join and the sequences' own
+// keys (1.05 PFLOP/s; one read of the prefix takes 22 us).  A tile takes 3400 to 3800 cycles, of
 // which its MMAs need 1280 and its exponentials 1024: the bound is the chain of waits between the
 // roles (150 to 300 cycles each beside four other warps of the scheduler), and in short segments q~
 // and the rows on their way out (4000 cycles a segment).  Slower were: P beside S with S a unit
@@ -69,7 +69,7 @@ constexpr int kSegs = 8;       // descriptions of segments: the query warps are 
 constexpr float kUp = 7.f;     // p is 2^kUp at the reference maximum
 // tensor memory columns: S of unit u at 64 (u % 3), O of the two streams, the scales of q~ (two
 // buffers of both streams) and of K (of each stream two: a copy never overwrites what an MMA in
-// flight may read, see the S warps)
+// flight may read, see the S warps).  Heads of 64 leave columns 320 to 447 unused.
 constexpr uint32_t kO = 192, kSfQ = 448, kSfK = 480;
 
 enum : int { kStart = 1, kEnd = 2, kAbsent = 4, kBoth = 8 };

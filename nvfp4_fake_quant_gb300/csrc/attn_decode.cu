@@ -798,7 +798,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, kRunsPerCta>::kThreads, 1)
             o1 = fmaf(ov.y, c[w], o1);
           }
           if (folds && f.other != 0.f) {
-            const float2 p = *reinterpret_cast<const float2*>(a.prior_o + row * D + element_of<D>(pos));
+            const float2 p =
+                *reinterpret_cast<const float2*>(a.prior_o + row * D + element_of<D>(pos));
             o0 = fmaf(o0, f.own, p.x * f.other);
             o1 = fmaf(o1, f.own, p.y * f.other);
           } else if (folds) {
@@ -1003,8 +1004,8 @@ cudaError_t launch_decode_form(int D, const CUtensorMap& tk, const CUtensorMap& 
 // DecodeArgs.
 nvq_status run_decode(const void* q, int64_t ld_q, const void* pool, int64_t num_pages,
                       const int32_t* page_table, int64_t ld_table, int max_pages,
-                      const int32_t* seq_lens, int B, int H, int Hkv, int D, float scale, int window,
-                      int sinks, void* o, float* lse, const float* prior_o, const float* prior_l2,
+                      const int32_t* seq_lens, int B, int H, int Hkv, int D, float scale,
+                      int window, int sinks, void* o, float* lse, const float* prior_o, const float* prior_l2,
                       void* ws, const Plan& p, cudaStream_t stream) {
   int* err = device_error_word();
   if (err == nullptr) return NVQ_ERR_CUDA;

@@ -18,8 +18,8 @@ __host__ __device__ constexpr int v_scales_at(int D) { return kPage * D + kPage 
 // How the kernels multiply the scores S by scale (in log2 units).  p = 2^(S scale - m) is one fused
 // product and difference, while the reference m is a score times scale, rounded: up to half a step
 // of m may come on top of kSlack, for |m| < 2^28 at most 8.  |S| <= 2688^2 D (codes of 6, scales of
-// 448), so any scale up to 25.7 / D, more than twice D^-0.5, keeps S scale below 2^28.  For a larger
-// one S is first replaced by S scale, rounded as m is; the difference is then exact.
+// 448), so any scale up to 25.7 / D, more than twice D^-0.5, keeps S scale below 2^28.  For a
+// larger one S is first replaced by S scale, rounded as m is; the difference is then exact.
 struct Scales {
   float before, fused;  // S before (1: not at all); in the fused product
 };
